@@ -659,7 +659,8 @@ grs_status grs_check_device_errors(const grs_plan* p, void* stream) {
     static const char* const kSite[grs::SITE_COUNT] = {
         "?", "reduce_kernel", "norm_pass1_kernel", "update_kernel", "accumulate_kernel", "gather_kernel",
         "state_logical_kernel", "norm_pass1_masked_kernel", "update_masked_kernel",
-        "check_already_reduced_kernel", "small_update_kernel", "update_kernel (per-tensor parameters)"};
+        "check_already_reduced_kernel", "small_update_kernel", "update_kernel (per-tensor parameters)",
+        "list_norm_kernel", "list_step_kernel"};
     const int site = h[grs::FLAG_BOUNDS] > 0 && h[grs::FLAG_BOUNDS] < grs::SITE_COUNT ? h[grs::FLAG_BOUNDS] : 0;
     return fail(GRS_ERR_BOUNDS, std::string("checked build: an index left its buffer in ") + kSite[site]);
   }

@@ -233,7 +233,9 @@ enum : int {
   SITE_AR_CHECK = 9,
   SITE_SMALL = 10,
   SITE_UPDATE_TENSORS = 11,
-  SITE_COUNT = 12
+  SITE_LIST_NORM = 12,
+  SITE_LIST_STEP = 13,
+  SITE_COUNT = 14
 };
 
 // Programmatic dependent launch between the path's kernels: measured on

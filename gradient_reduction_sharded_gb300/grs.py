@@ -35,6 +35,8 @@ GRS_MAX_WORLD = 128
 GRS_NOALLOC_SCRATCH_BYTES = 4 << 20
 GRS_SMALL_MAX_TILES = 128
 GRS_SMALL_MAX_BUFFERS = 256
+GRS_DTYPE_BF16, GRS_DTYPE_FP32 = 0, 1
+GRS_STATE_BLOCK = 256
 
 STATUS_NAMES = {0: "OK", 1: "INVALID_ARG", 2: "UNSUPPORTED_COMPOSITION", 3: "SHAPE",
                 4: "ALIGNMENT", 5: "CUDA", 6: "TIMEOUT", 7: "NONFINITE", 8: "NO_DEVICE",
@@ -87,6 +89,11 @@ class grs_adamw(ctypes.Structure):
                 ("n_micro", ctypes.c_int32)]
 
 
+class grs_tensors_info(ctypes.Structure):
+    _fields_ = [("n_tensors", ctypes.c_int32), ("device", ctypes.c_int32), ("n_elements", ctypes.c_int64),
+                ("n_state", ctypes.c_int64), ("n_blocks", ctypes.c_int64), ("workspace_bytes", ctypes.c_int64)]
+
+
 if not os.path.exists(LIB_PATH):
     raise ImportError(f"{LIB_PATH} is missing: build it with __graft_entry__.build() "
                       "(there is no CPU fallback)")
@@ -131,6 +138,17 @@ _sig = {
     "grs_step_from_host": ([_vp, _P(grs_adamw), _P(_vp), _P(_vp), _vp, _vp, _vp, _vp, _vp, _vp, _vp,
                             _vp, _vp, _vp], ctypes.c_int),
     "grs_update_small": ([_vp, _P(grs_adamw), _P(_vp), _vp, _vp, _vp, _vp, _vp, _vp, _vp], ctypes.c_int),
+    "grs_tensors_create": ([_P(ctypes.c_int64), ctypes.c_int32, ctypes.c_uint32, _P(_vp)], ctypes.c_int),
+    "grs_tensors_destroy": ([_vp], None),
+    "grs_tensors_query": ([_vp, _P(grs_tensors_info)], ctypes.c_int),
+    "grs_tensors_offset": ([_vp, ctypes.c_int32, _P(ctypes.c_int64)], ctypes.c_int),
+    "grs_tensors_norm_sq": ([_vp, _vp, ctypes.c_int32, ctypes.c_int32, _vp, _vp, _vp], ctypes.c_int),
+    "grs_tensors_adamw_step": ([_vp, _P(grs_adamw), _vp, _vp, ctypes.c_int32, _vp, _vp, _vp, _vp, _vp], ctypes.c_int),
+    "grs_tensors_adamw8_step": ([_vp, _P(grs_adamw), ctypes.c_uint64, _vp, _vp, ctypes.c_int32, _vp, _vp, _vp, _vp,
+                                 _vp, _vp, _vp], ctypes.c_int),
+    "grs_tensors_pack8": ([_vp] * 8, ctypes.c_int),
+    "grs_tensors_unpack8": ([_vp] * 8, ctypes.c_int),
+    "grs_tensors_check_device_errors": ([_vp, _vp], ctypes.c_int),
     "grs_last_error": ([], ctypes.c_char_p),
     "grs_build_features": ([], ctypes.c_uint32),
 }
@@ -356,4 +374,67 @@ def grs_check_device_errors(plan: int, stream: int) -> int:
     st = _lib.grs_check_device_errors(plan, stream)
     if st == GRS_ERR_CUDA:
         _check(st, "grs_check_device_errors")
+    return st
+
+
+def grs_tensors_create(numels: Sequence[int], flags: int = 0) -> int:
+    n = len(numels)
+    ne = (ctypes.c_int64 * max(1, n))(*numels)
+    out = _vp()
+    _check(_lib.grs_tensors_create(ne, n, flags, ctypes.byref(out)), "grs_tensors_create")
+    return out.value
+
+
+def grs_tensors_destroy(tensors: int) -> None:
+    _lib.grs_tensors_destroy(tensors)
+
+
+def grs_tensors_query(tensors: int) -> Dict[str, int]:
+    o = grs_tensors_info()
+    _check(_lib.grs_tensors_query(tensors, ctypes.byref(o)), "grs_tensors_query")
+    return _as_dict(o)
+
+
+def grs_tensors_offset(tensors: int, tensor: int) -> int:
+    o = ctypes.c_int64()
+    _check(_lib.grs_tensors_offset(tensors, tensor, ctypes.byref(o)), "grs_tensors_offset")
+    return o.value
+
+
+def grs_tensors_norm_sq(tensors: int, d_grads: int, grad_dtype: int, n_micro: int, workspace: int, d_norm_sq: int,
+                        stream: int) -> None:
+    """d_grads (here and below): device address of an int64 array of
+    per-tensor device pointers (0 = no gradient)."""
+    _check(_lib.grs_tensors_norm_sq(tensors, d_grads, grad_dtype, n_micro, workspace, d_norm_sq, stream),
+           "grs_tensors_norm_sq")
+
+
+def grs_tensors_adamw_step(tensors: int, hp: grs_adamw, d_norm_sq: Optional[int], d_grads: int, grad_dtype: int,
+                           master: int, m: int, v: int, d_params_bf16: Optional[int], stream: int) -> None:
+    _check(_lib.grs_tensors_adamw_step(tensors, ctypes.byref(hp), d_norm_sq, d_grads, grad_dtype, master, m, v,
+                                       d_params_bf16, stream), "grs_tensors_adamw_step")
+
+
+def grs_tensors_adamw8_step(tensors: int, hp: grs_adamw, seed: int, d_norm_sq: Optional[int], d_grads: int,
+                            grad_dtype: int, master: int, m8: int, m_scale: int, s8: int, s_scale: int,
+                            d_params_bf16: Optional[int], stream: int) -> None:
+    _check(_lib.grs_tensors_adamw8_step(tensors, ctypes.byref(hp), seed, d_norm_sq, d_grads, grad_dtype, master, m8,
+                                        m_scale, s8, s_scale, d_params_bf16, stream), "grs_tensors_adamw8_step")
+
+
+def grs_tensors_pack8(tensors: int, m: int, v: int, m8: int, m_scale: int, s8: int, s_scale: int,
+                      stream: int) -> None:
+    _check(_lib.grs_tensors_pack8(tensors, m, v, m8, m_scale, s8, s_scale, stream), "grs_tensors_pack8")
+
+
+def grs_tensors_unpack8(tensors: int, m8: int, m_scale: int, s8: int, s_scale: int, m: int, v: int,
+                        stream: int) -> None:
+    _check(_lib.grs_tensors_unpack8(tensors, m8, m_scale, s8, s_scale, m, v, stream), "grs_tensors_unpack8")
+
+
+def grs_tensors_check_device_errors(tensors: int, stream: int) -> int:
+    """Returns the status (raises only for CUDA errors)."""
+    st = _lib.grs_tensors_check_device_errors(tensors, stream)
+    if st == GRS_ERR_CUDA:
+        _check(st, "grs_tensors_check_device_errors")
     return st

@@ -4,9 +4,9 @@
  * C ABI of libgrs.so.  Plain pointers and sizes only: host pointers are
  * marked "host", device pointers "device".  Every entry point returns a
  * grs_status; on failure a thread-local message is available from
- * grs_last_error().  Nothing here synchronises with the host except
- * grs_check_device_errors(), and nothing allocates device memory except
- * grs_plan_create() (its small tables and error flags).
+ * grs_last_error().  Nothing here synchronises with the host except the
+ * *_check_device_errors() calls, and nothing allocates device memory except
+ * the calls that create a handle (its small tables and error flags).
  *
  * The operation follows these web pages (cited by title and section):
  *   [ISSUE]  "refactor(distributed): establish shared native TP replica
@@ -589,6 +589,120 @@ grs_status grs_state_from_logical(const grs_plan* plan, const float* logical, fl
  * NaN/Inf since the last check, INVALID_ARG if grs_check_already_reduced
  * found copies that differ, else OK (or CUDA). */
 grs_status grs_check_device_errors(const grs_plan* plan, void* stream);
+
+/* ------------------------------------------- a list of separate tensors */
+
+/* Element type of a buffer that comes in more than one. */
+typedef enum grs_dtype {
+  GRS_DTYPE_BF16 = 0,
+  GRS_DTYPE_FP32 = 1
+} grs_dtype;
+
+#define GRS_STATE_BLOCK 256 /* elements of one scale of the 8-bit states; each tensor's state starts at a multiple */
+
+/* AdamW over a list of tensors that keep their own storage, for parameters
+ * outside a reduction plan, and with its states in 32 or in 8 bits for any
+ * parameters: a plan's arrays (acc, master, params_bf16, each
+ * [n_state_pad]), or a shard view's, are a list of one tensor.
+ *
+ * The list's layout is fixed at creation: tensor i's state begins at element
+ * grs_tensors_offset(i) of the state arrays, which have n_state elements
+ * (every tensor rounded up to GRS_STATE_BLOCK).  State padding is ignored on
+ * input and written as zeros for every tensor that is updated.  Gradients
+ * and bf16 parameters stay where they are: a call takes DEVICE arrays
+ * [n_tensors] of device pointers (8-byte aligned; entry i points at tensor
+ * i's contiguous elements, aligned to the element).  The library cannot check
+ * the entries; the caller guarantees their extent.  A tensor whose gradient entry is NULL has no
+ * gradient this step: it is left out of the norm and keeps its state and
+ * parameter (torch.optim.AdamW skips such parameters); every tensor takes
+ * hp->step as its step count. */
+typedef struct grs_tensors grs_tensors; /* opaque; owned by the caller via create/destroy */
+
+typedef struct grs_tensors_info {
+  int32_t n_tensors;
+  int32_t device;          /* CUDA device of the tables, -1 when host-only */
+  int64_t n_elements;      /* sum of the tensors' elements */
+  int64_t n_state;         /* elements of each state array */
+  int64_t n_blocks;        /* n_state / GRS_STATE_BLOCK: scales of each 8-bit state */
+  int64_t workspace_bytes; /* device workspace of grs_tensors_norm_sq; zero it once */
+} grs_tensors_info;
+
+/* numels: host array [n_tensors], >= 0.  flags: 0 or GRS_PLAN_HOST_ONLY.
+ * The device tables go to the current device.  Errors: INVALID_ARG (NULL,
+ * n_tensors <= 0, flags), SHAPE (a negative or too large numel), CUDA. */
+grs_status grs_tensors_create(const int64_t* numels, int32_t n_tensors, uint32_t flags, grs_tensors** out);
+/* NULL is a no-op.  No launch using the list may still be in flight. */
+void grs_tensors_destroy(grs_tensors* list);
+grs_status grs_tensors_query(const grs_tensors* list, grs_tensors_info* out);
+/* State offset of tensor i: the sum over the tensors before it of their
+ * elements rounded up to GRS_STATE_BLOCK. */
+grs_status grs_tensors_offset(const grs_tensors* list, int32_t tensor, int64_t* out);
+
+/* S = sum over every tensor with a gradient of (g / n_micro)^2 to *d_norm_sq
+ * (device double), deterministic: fixed tiles of 2048 elements, each summed
+ * as an unevaluated pair of floats (48 bits), then fp64 in a fixed order.  A non-finite S raises the flag that
+ * grs_tensors_check_device_errors reports.  workspace: device, 16-byte
+ * aligned, workspace_bytes, zeroed once before its first use; calls that
+ * share one must not overlap.  Errors: INVALID_ARG, ALIGNMENT, NO_DEVICE,
+ * CUDA. */
+grs_status grs_tensors_norm_sq(const grs_tensors* list, const void* const* d_grads, int32_t grad_dtype,
+                               int32_t n_micro, void* workspace, double* d_norm_sq, void* stream);
+
+/* Clip + AdamW + bf16 cast over the list, states in 32 bits: per element the
+ * arithmetic of grs_clip_adamw_step with acc = the tensor's gradient (the
+ * sum of hp->n_micro microbatches).
+ *   d_norm_sq  : device double; may be NULL when hp->max_norm <= 0.
+ *   master, m, v : device fp32 [n_state], 16-byte aligned, updated in place.
+ *   d_params_bf16 : device array of pointers to the bf16 parameters, written;
+ *                NULL (or NULL entries): none.
+ * Errors: INVALID_ARG, ALIGNMENT, NO_DEVICE, CUDA. */
+grs_status grs_tensors_adamw_step(const grs_tensors* list, const grs_adamw* hp, const double* d_norm_sq,
+                                  const void* const* d_grads, int32_t grad_dtype, float* master, float* m,
+                                  float* v, uint16_t* const* d_params_bf16, void* stream);
+
+/* The same update with both moments held in 8 bits, 2 bytes and two 1/256
+ * scales an element instead of 8 bytes.
+ * Format: a block is GRS_STATE_BLOCK elements of the state arrays.  m8 holds
+ * m, s8 holds sqrt(v), as 8-bit floating-point numbers (sign, 4 exponent
+ * bits of bias 7, 3 mantissa bits: "E4M3") in units of the block's scale, a
+ * power of two that brings the block's largest magnitude x to 128 < x/scale
+ * <= 256 (scale >= 2^-126), so that nothing saturates and the scaling is
+ * exact.  All-zero codes and scales stand for zero: the states before the
+ * first step.
+ * Step: the moments are read as fp32, stepped and used in fp32 as in the
+ * 32-bit form (products and sums rounded one by one, so that the codes are
+ * reproducible by any IEEE arithmetic), and only then rounded to 8 bits.
+ * Rounding is stochastic: up with the probability of the fraction cut off,
+ * from 16 random bits an element that are a hash of `seed` and the element's
+ * index in the state arrays (same seed, same result; give each step another).  With
+ * beta2 near 1 a step moves sqrt(v) by far less than the distance between
+ * two codes: rounding to nearest would keep it where it is, stochastic
+ * rounding moves it right on average.  A positive sqrt(v) never becomes
+ * zero.  A block that holds a NaN or an infinity gets the scale NaN and code
+ * 0: all of its moments are NaN from then on.
+ *   m8, s8        : device uint8 [n_state], 16-byte aligned.
+ *   m_scale, s_scale : device fp32 [n_blocks], 4-byte aligned.
+ * Other arguments and errors as grs_tensors_adamw_step. */
+grs_status grs_tensors_adamw8_step(const grs_tensors* list, const grs_adamw* hp, uint64_t seed,
+                                   const double* d_norm_sq, const void* const* d_grads, int32_t grad_dtype,
+                                   float* master, uint8_t* m8, float* m_scale, uint8_t* s8, float* s_scale,
+                                   uint16_t* const* d_params_bf16, void* stream);
+
+/* 32-bit moments to the 8-bit format (rounded to nearest even; sqrt(v) of a
+ * negative v is NaN) and back (v = (code * scale)^2), every tensor of the
+ * list: for a change of format in mid-run and for checkpoints.  Packing
+ * what was unpacked stands for the same values, as long as no sqrt(v) in use
+ * is below 2^-63 (v itself would leave fp32's normal range).  State padding is read
+ * as zeros and written as zeros.  fp32 arrays [n_state] and codes 16-byte
+ * aligned.  Errors as grs_tensors_norm_sq. */
+grs_status grs_tensors_pack8(const grs_tensors* list, const float* m, const float* v, uint8_t* m8, float* m_scale,
+                             uint8_t* s8, float* s_scale, void* stream);
+grs_status grs_tensors_unpack8(const grs_tensors* list, const uint8_t* m8, const float* m_scale, const uint8_t* s8,
+                               const float* s_scale, float* m, float* v, void* stream);
+
+/* Synchronise `stream`, read and clear the list's flags: BOUNDS, NONFINITE,
+ * OK or CUDA, as grs_check_device_errors. */
+grs_status grs_tensors_check_device_errors(const grs_tensors* list, void* stream);
 
 /* Build features of the loaded library.  GRS_FEATURE_CHECKED: compiled with
  * GRS_CHECKED=1 — every kernel checks each index it derives against the

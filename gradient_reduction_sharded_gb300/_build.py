@@ -19,7 +19,8 @@ CHECKED_LIB = os.path.join(PKG, "checked", "libgrs.so")
 CHECKED_FLAGS = ("-DGRS_CHECKED=1",)
 
 SOURCES = ["plan.cpp", "api.cu", "kernels_reduce.cu", "kernels_update.cu", "kernels_gather.cu",
-           "noalloc.cu", "host_step.cu", "kernels_masked.cu", "kernels_small.cu", "kernels_list.cu"]
+           "noalloc.cu", "host_step.cu", "kernels_masked.cu", "kernels_small.cu", "kernels_list.cu",
+           "kernels_layernorm.cu", "kernels_moe.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -37,6 +37,7 @@ GRS_SMALL_MAX_TILES = 128
 GRS_SMALL_MAX_BUFFERS = 256
 GRS_DTYPE_BF16, GRS_DTYPE_FP32 = 0, 1
 GRS_STATE_BLOCK = 256
+GRS_MOE_MAX_EXPERTS = 1024
 
 STATUS_NAMES = {0: "OK", 1: "INVALID_ARG", 2: "UNSUPPORTED_COMPOSITION", 3: "SHAPE",
                 4: "ALIGNMENT", 5: "CUDA", 6: "TIMEOUT", 7: "NONFINITE", 8: "NO_DEVICE",
@@ -94,6 +95,19 @@ class grs_tensors_info(ctypes.Structure):
                 ("n_state", ctypes.c_int64), ("n_blocks", ctypes.c_int64), ("workspace_bytes", ctypes.c_int64)]
 
 
+class grs_norm(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("ld_x", ctypes.c_int64), ("ld_y", ctypes.c_int64),
+                ("ld_dy", ctypes.c_int64), ("ld_dx", ctypes.c_int64), ("cols", ctypes.c_int32),
+                ("eps", ctypes.c_float), ("dtype", ctypes.c_int32), ("param_dtype", ctypes.c_int32),
+                ("grad_dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class grs_moe(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int64), ("top_k", ctypes.c_int32), ("expert_begin", ctypes.c_int32),
+                ("expert_end", ctypes.c_int32), ("hidden", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
+
+
 if not os.path.exists(LIB_PATH):
     raise ImportError(f"{LIB_PATH} is missing: build it with __graft_entry__.build() "
                       "(there is no CPU fallback)")
@@ -149,6 +163,15 @@ _sig = {
     "grs_tensors_pack8": ([_vp] * 8, ctypes.c_int),
     "grs_tensors_unpack8": ([_vp] * 8, ctypes.c_int),
     "grs_tensors_check_device_errors": ([_vp, _vp], ctypes.c_int),
+    "grs_layernorm_forward": ([_P(grs_norm)] + [_vp] * 7, ctypes.c_int),
+    "grs_layernorm_backward": ([_P(grs_norm)] + [_vp] * 10, ctypes.c_int),
+    "grs_layernorm_workspace_bytes": ([_P(grs_norm)], ctypes.c_int64),
+    "grs_moe_sort": ([_P(grs_moe)] + [_vp] * 6, ctypes.c_int),
+    "grs_moe_workspace_bytes": ([_P(grs_moe)], ctypes.c_int64),
+    "grs_moe_dispatch": ([_P(grs_moe)] + [_vp] * 4, ctypes.c_int),
+    "grs_moe_dispatch_backward": ([_P(grs_moe)] + [_vp] * 4, ctypes.c_int),
+    "grs_moe_combine": ([_P(grs_moe)] + [_vp] * 5, ctypes.c_int),
+    "grs_moe_combine_backward": ([_P(grs_moe)] + [_vp] * 7, ctypes.c_int),
     "grs_last_error": ([], ctypes.c_char_p),
     "grs_build_features": ([], ctypes.c_uint32),
 }
@@ -438,3 +461,67 @@ def grs_tensors_check_device_errors(tensors: int, stream: int) -> int:
     if st == GRS_ERR_CUDA:
         _check(st, "grs_tensors_check_device_errors")
     return st
+
+
+def make_norm(rows: int, cols: int, eps: float, dtype: int, param_dtype: int, grad_dtype: int, ld_x: int = 0,
+              ld_y: int = 0, ld_dy: int = 0, ld_dx: int = 0) -> grs_norm:
+    return grs_norm(rows, ld_x, ld_y, ld_dy, ld_dx, cols, eps, dtype, param_dtype, grad_dtype, 0)
+
+
+def grs_layernorm_forward(shape: grs_norm, x: int, w: Optional[int], b: Optional[int], y: int, mean: Optional[int],
+                          rstd: Optional[int], stream: int) -> None:
+    _check(_lib.grs_layernorm_forward(ctypes.byref(shape), x, w, b, y, mean, rstd, stream), "grs_layernorm_forward")
+
+
+def grs_layernorm_backward(shape: grs_norm, dy: int, x: int, w: Optional[int], mean: int, rstd: int,
+                           dx: Optional[int], dw: Optional[int], db: Optional[int], workspace: Optional[int],
+                           stream: int) -> None:
+    _check(_lib.grs_layernorm_backward(ctypes.byref(shape), dy, x, w, mean, rstd, dx, dw, db, workspace, stream),
+           "grs_layernorm_backward")
+
+
+def _bytes(n: int, func: str) -> int:
+    if n < 0:
+        raise GrsError(GRS_ERR_INVALID_ARG, func, grs_last_error())
+    return n
+
+
+def grs_layernorm_workspace_bytes(shape: grs_norm) -> int:
+    return _bytes(int(_lib.grs_layernorm_workspace_bytes(ctypes.byref(shape))), "grs_layernorm_workspace_bytes")
+
+
+def make_moe(tokens: int, top_k: int, n_experts: int, expert_begin: int, expert_end: int, hidden: int,
+             dtype: int) -> grs_moe:
+    """n_experts is what the router chooses from; the call's experts are
+    [expert_begin, expert_end) of them."""
+    if not 0 <= expert_begin < expert_end <= n_experts:
+        raise GrsError(GRS_ERR_INVALID_ARG, "make_moe", "the expert range must lie in [0, n_experts)")
+    return grs_moe(tokens, top_k, expert_begin, expert_end, hidden, dtype, 0)
+
+
+def grs_moe_workspace_bytes(shape: grs_moe) -> int:
+    return _bytes(int(_lib.grs_moe_workspace_bytes(ctypes.byref(shape))), "grs_moe_workspace_bytes")
+
+
+def grs_moe_sort(shape: grs_moe, expert_ids: int, expert_offsets: int, row_slot: int, slot_row: int, workspace: int,
+                 stream: int) -> None:
+    _check(_lib.grs_moe_sort(ctypes.byref(shape), expert_ids, expert_offsets, row_slot, slot_row, workspace, stream),
+           "grs_moe_sort")
+
+
+def grs_moe_dispatch(shape: grs_moe, x: int, slot_row: int, xs: int, stream: int) -> None:
+    _check(_lib.grs_moe_dispatch(ctypes.byref(shape), x, slot_row, xs, stream), "grs_moe_dispatch")
+
+
+def grs_moe_dispatch_backward(shape: grs_moe, dxs: int, slot_row: int, dx: int, stream: int) -> None:
+    _check(_lib.grs_moe_dispatch_backward(ctypes.byref(shape), dxs, slot_row, dx, stream), "grs_moe_dispatch_backward")
+
+
+def grs_moe_combine(shape: grs_moe, ys: int, slot_row: int, weights: int, y: int, stream: int) -> None:
+    _check(_lib.grs_moe_combine(ctypes.byref(shape), ys, slot_row, weights, y, stream), "grs_moe_combine")
+
+
+def grs_moe_combine_backward(shape: grs_moe, dy: int, ys: int, slot_row: int, weights: int, dys: int, dweights: int,
+                             stream: int) -> None:
+    _check(_lib.grs_moe_combine_backward(ctypes.byref(shape), dy, ys, slot_row, weights, dys, dweights, stream),
+           "grs_moe_combine_backward")

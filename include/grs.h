@@ -704,6 +704,105 @@ grs_status grs_tensors_unpack8(const grs_tensors* list, const uint8_t* m8, const
  * OK or CUDA, as grs_check_device_errors. */
 grs_status grs_tensors_check_device_errors(const grs_tensors* list, void* stream);
 
+/* ------------------------------------------------------------ layer norm */
+
+/* Layer norm over the rows of a matrix, forward and backward.  The weight's
+ * gradient of a norm over a sequence- or head-sharded activation is the
+ * PARTIAL_SUM parameter of [ISSUE] "Why this needs separate work"; it is
+ * written in grad_dtype, so that it can go straight into a rank's gradient
+ * buffer at the tensor's place. */
+typedef struct grs_norm {
+  int64_t rows;          /* >= 0 */
+  int64_t ld_x;          /* elements from one row to the next, 0 = cols (also below) */
+  int64_t ld_y;
+  int64_t ld_dy;
+  int64_t ld_dx;
+  int32_t cols;          /* C >= 1 */
+  float eps;             /* >= 0 */
+  int32_t dtype;         /* grs_dtype of x, y, dy, dx */
+  int32_t param_dtype;   /* of w and b */
+  int32_t grad_dtype;    /* of dw and db */
+  int32_t reserved;
+} grs_norm;
+
+/* mean = sum x / C; rstd = 1 / sqrt(sum (x - mean)^2 / C + eps);
+ * y = (x - mean) * rstd * w + b, in fp32, rounded once.
+ *   x [rows, cols], y: device, aligned to the element, rows ld_x and ld_y
+ *   elements apart; rows that start at multiples of 16 bytes are fastest.
+ *   w, b    : device [cols], or NULL (1 and 0).
+ *   mean, rstd : device fp32 [rows], kept for the backward pass, or NULL.
+ * Runs on the current device.  Errors: INVALID_ARG, SHAPE, ALIGNMENT, CUDA. */
+grs_status grs_layernorm_forward(const grs_norm* shape, const void* x, const void* w, const void* b, void* y,
+                                 float* mean, float* rstd, void* stream);
+
+/* With h = (x - mean) * rstd and dh = dy * w:
+ *   dx = rstd * (dh - mean_C(dh) - h * mean_C(dh * h)),
+ *   dw = sum over rows of dy * h,  db = sum over rows of dy (overwritten;
+ *   zeros when rows is 0), each of the three NULL if not wanted.
+ * Sums in fp32 in an order that the shape alone fixes: the same call gives the
+ * same bits.  workspace: device, 16-byte aligned, grs_layernorm_workspace_bytes
+ * (not initialised), needed for dw or db.  No output may overlap an input. */
+grs_status grs_layernorm_backward(const grs_norm* shape, const void* dy, const void* x, const void* w,
+                                  const float* mean, const float* rstd, void* dx, void* dw, void* db,
+                                  void* workspace, void* stream);
+/* Bytes, or -1 for a shape that the calls refuse. */
+int64_t grs_layernorm_workspace_bytes(const grs_norm* shape);
+
+/* --------------------------------------------- tokens sorted by expert */
+
+#define GRS_MOE_MAX_EXPERTS 1024 /* experts of one call's range */
+
+/* Tokens to their experts and back.  A slot is one choice of one token (index
+ * token * top_k + choice).  The call's experts are those of [expert_begin,
+ * expert_end): all of them, or the ones that an expert-owned LOCAL_SHARD
+ * rank holds; a slot with any other id (negative ones too) has no row here. */
+typedef struct grs_moe {
+  int64_t tokens;        /* >= 0; tokens * top_k < 2^31 */
+  int32_t top_k;         /* >= 1 */
+  int32_t expert_begin;
+  int32_t expert_end;
+  int32_t hidden;        /* elements of a token's vector, >= 1 */
+  int32_t dtype;         /* grs_dtype of the vectors */
+  int32_t reserved;
+} grs_moe;
+
+/* Stable counting sort of the slots by expert.
+ *   expert_ids     : device int32 [tokens * top_k].
+ *   expert_offsets : device int32 [expert_end - expert_begin + 1], written: expert e's rows
+ *                    are [offsets[e - begin], offsets[e - begin + 1]).
+ *   row_slot       : device int32 [tokens * top_k], written: the slot of each
+ *                    row; -1 from the last expert's end on.
+ *   slot_row       : device int32 [tokens * top_k], written: the row of each
+ *                    slot, -1 for a slot without one.
+ *   workspace      : device, 16-byte aligned, grs_moe_workspace_bytes (not initialised).
+ * Runs on the current device.  Errors (here and below): INVALID_ARG, SHAPE, ALIGNMENT, CUDA. */
+grs_status grs_moe_sort(const grs_moe* shape, const int32_t* expert_ids, int32_t* expert_offsets,
+                        int32_t* row_slot, int32_t* slot_row, void* workspace, void* stream);
+/* Bytes, or -1 for a shape that the calls refuse. */
+int64_t grs_moe_workspace_bytes(const grs_moe* shape);
+
+/* The calls below take vectors as contiguous rows of `hidden` elements,
+ * aligned to the element (16 bytes and hidden * size a multiple of 16 are
+ * fastest).  An entry of slot_row outside [0, tokens * top_k) stands for no
+ * row; the entries that do not must differ from each other.
+ *
+ * dispatch: xs[slot_row[s]] = x[s / top_k]; rows without a slot are not written.
+ * dispatch_backward: dx[t] = sum of dxs over the token's rows, in fp32 in the
+ *   order of its choices (zeros for a token without a row). */
+grs_status grs_moe_dispatch(const grs_moe* shape, const void* x, const int32_t* slot_row, void* xs, void* stream);
+grs_status grs_moe_dispatch_backward(const grs_moe* shape, const void* dxs, const int32_t* slot_row, void* dx,
+                                     void* stream);
+/* combine: y[t] = sum over the token's rows of weights[s] * ys[slot_row[s]],
+ *   in fp32 in the order of its choices (zeros without a row).
+ * combine_backward: dys[slot_row[s]] = weights[s] * dy[t]; dweights[s] =
+ *   <ys[slot_row[s]], dy[t]> in fp32 (0 for a slot without a row).
+ *   weights, dweights : device fp32 [tokens * top_k]; weights of slots
+ *   without a row are not used. */
+grs_status grs_moe_combine(const grs_moe* shape, const void* ys, const int32_t* slot_row, const float* weights,
+                           void* y, void* stream);
+grs_status grs_moe_combine_backward(const grs_moe* shape, const void* dy, const void* ys, const int32_t* slot_row,
+                                    const float* weights, void* dys, float* dweights, void* stream);
+
 /* Build features of the loaded library.  GRS_FEATURE_CHECKED: compiled with
  * GRS_CHECKED=1 — every kernel checks each index it derives against the
  * extent of the buffer it addresses (the sizes this header documents for

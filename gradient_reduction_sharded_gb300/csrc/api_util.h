@@ -3,6 +3,7 @@
 
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 #include <string>
 
@@ -45,6 +46,21 @@ class ApiDevice {
   int prev_ = 0;
   bool ok_ = false, switched_ = false;
 };
+
+// Lets `Kernel` use up to `bytes` of dynamic shared memory on the current
+// device; asked once a device, so that a call does not pay for it again.
+template <auto* Kernel>
+cudaError_t allow_smem(int bytes) {
+  static std::atomic<uint64_t> done{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (dev < 64 && (done.load(std::memory_order_acquire) & bit) != 0) return cudaSuccess;
+  e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess && dev < 64) done.fetch_or(bit, std::memory_order_release);
+  return e;
+}
 
 inline bool dtype_ok(int32_t t) { return t == GRS_DTYPE_BF16 || t == GRS_DTYPE_FP32; }
 inline int dtype_size(int32_t t) { return t == GRS_DTYPE_FP32 ? 4 : 2; }

@@ -15,12 +15,16 @@
 #include "device.cuh"
 #include "internal.h"
 #include "launch.cuh"
+#include "packed.cuh"
 
 namespace grs {
 namespace {
 
 constexpr int LN_THREADS = 256;
-constexpr int LN_PARTS = 304;  // partial rows of dw and db at most
+constexpr int LN_RING_THREADS = 256; // a block of the forward ring at most; two blocks an SM
+constexpr int LN_RED_BYTES = 256;    // two float2 a warp of a block, twice
+constexpr int LN_BWD_THREADS = 512;  // a block of the backward pass at most
+constexpr int LN_PARTS = 304;        // partial rows of dw and db at most: two blocks an SM
 
 __device__ __forceinline__ float ln_load(const uint16_t* p) { return __uint_as_float(uint32_t(*p) << 16); }
 __device__ __forceinline__ float ln_load(const float* p) { return *p; }
@@ -36,6 +40,512 @@ __device__ __forceinline__ float ln_block_sum(float x, float* red) {
   float s = red[0];
   for (int k = 1; k < LN_THREADS / 32; ++k) s = __fadd_rn(s, red[k]);
   return s;
+}
+
+// --------------------------------------------- rows held in registers
+// A group of `tpr` threads (a power of two up to a warp, or whole warps) has
+// a row: thread t holds the chunks t, t + tpr, ... of VEC elements, E
+// elements in all, read once.  VEC is 16 bytes where every row starts at a
+// multiple of 16 bytes and has whole chunks, else a pair of elements, of
+// which the row's last may be half (a "loose" row).
+template <typename T, int VEC, int E>
+struct Row {
+  static constexpr int NV = E / VEC;
+  static constexpr int WORDS = VEC * static_cast<int>(sizeof(T)) / 4;  // 32-bit words of a chunk
+  uint32_t r[NV * WORDS];
+
+  // Elements 2 i and 2 i + 1 of the thread's E.
+  __device__ __forceinline__ float2 pair(int i) const {
+    if constexpr (sizeof(T) == 4) return make_float2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
+    return bf16_pair(r[i]);
+  }
+  // Straight from memory; zeros beyond the row.
+  __device__ __forceinline__ void load(const T* p, int t, int tpr, int cols, bool on) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int c = (t + j * tpr) * VEC;
+      if constexpr (VEC == 2) {
+        const float lo = on && c < cols ? ln_load(p + c) : 0.0f, hi = on && c + 1 < cols ? ln_load(p + c + 1) : 0.0f;
+        if constexpr (sizeof(T) == 4) {
+          r[2 * j] = __float_as_uint(lo);
+          r[2 * j + 1] = __float_as_uint(hi);
+        } else {
+          r[j] = __float_as_uint(lo) >> 16 | __float_as_uint(hi);
+        }
+      } else {
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (on && c < cols) v = *reinterpret_cast<const uint4*>(p + c);
+        r[4 * j] = v.x;
+        r[4 * j + 1] = v.y;
+        r[4 * j + 2] = v.z;
+        r[4 * j + 3] = v.w;
+      }
+    }
+  }
+};
+
+// The rows to come, in flight in shared memory (cp.async, 16 bytes each), so
+// that the bytes in flight do not cost registers.  A slot is refilled one row
+// after it was read.  `slot` is the slot's first byte.
+//
+// Whole rows: a thread copies the chunks that it will read itself, so nobody
+// waits for anybody; a thread's chunks lie blockDim.x chunks apart.
+// Loose rows: the group copies the aligned 16-byte pieces that cover the row,
+// which keeps its place modulo 16 bytes, and waits for one another before
+// reading pairs.  A piece that reaches outside the matrix is copied by its
+// elements.
+struct Matrix {
+  const uint8_t *first, *last;  // the first byte and the one after the last
+};
+
+template <typename T, int VEC, int E>
+struct Ring {
+  static constexpr int NV = E / VEC;
+  static constexpr int BYTES = E * static_cast<int>(sizeof(T));  // a thread and row
+  static constexpr int EXTRA = VEC == 2 ? 32 : 0;                // a group's row may start and end inside a piece
+
+  static __device__ __forceinline__ void copy16(void* dst, const void* src, int bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(dst)), "l"(src), "r"(bytes) : "memory");
+  }
+
+  static __device__ __forceinline__ void issue(uint8_t* slot, const T* p, const Matrix& m, int g, int t, int tpr, int cols,
+                                               bool on) {
+    if constexpr (VEC > 2) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const int c = (t + j * tpr) * VEC;
+        const bool in = on && c < cols;
+        copy16(slot + (j * blockDim.x + threadIdx.x) * 16, in ? p + c : p, in ? 16 : 0);
+      }
+    } else if (on) {
+      uint8_t* row = slot + g * (tpr * BYTES + EXTRA);
+      const uint8_t* end = reinterpret_cast<const uint8_t*>(p + cols);
+      const uint8_t* src = reinterpret_cast<const uint8_t*>(reinterpret_cast<uintptr_t>(p) & ~uintptr_t(15)) + t * 16;
+      for (int at = t * 16; src < end; at += tpr * 16, src += tpr * 16) {
+        if (src >= m.first && src + 16 <= m.last) {
+          copy16(row + at, src, 16);
+        } else {
+          for (int k = 0; k < 16; k += sizeof(T))
+            if (src + k >= reinterpret_cast<const uint8_t*>(p) && src + k < end)
+              *reinterpret_cast<T*>(row + at + k) = *reinterpret_cast<const T*>(src + k);
+        }
+      }
+    }
+  }
+
+  // p: the row that was copied to the slot.
+  static __device__ __forceinline__ void read(const uint8_t* slot, const T* p, int g, int t, int tpr, int cols, bool on,
+                                              Row<T, VEC, E>& x) {
+    if constexpr (VEC > 2) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const uint4 v = *reinterpret_cast<const uint4*>(slot + (j * blockDim.x + threadIdx.x) * 16);
+        x.r[4 * j] = v.x;
+        x.r[4 * j + 1] = v.y;
+        x.r[4 * j + 2] = v.z;
+        x.r[4 * j + 3] = v.w;
+      }
+    } else {
+      const uint8_t* row = slot + g * (tpr * BYTES + EXTRA) + (reinterpret_cast<uintptr_t>(p) & 15);
+      const bool odd = sizeof(T) == 2 && (reinterpret_cast<uintptr_t>(p) & 2) != 0;
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const int c = 2 * (t + j * tpr);
+        const bool lo = on && c < cols, hi = on && c + 1 < cols;
+        if constexpr (sizeof(T) == 4) {
+          const float* f = reinterpret_cast<const float*>(row) + c;
+          x.r[2 * j] = lo ? __float_as_uint(f[0]) : 0u;
+          x.r[2 * j + 1] = hi ? __float_as_uint(f[1]) : 0u;
+        } else {
+          // the pair is one word, or the high half of one and the low half of the next
+          const uint32_t* w = reinterpret_cast<const uint32_t*>(row + 2 * c - (odd ? 2 : 0));
+          uint32_t v = lo ? w[0] : 0u;
+          if (odd) v = __funnelshift_r(v, lo ? w[1] : 0u, 16);
+          x.r[j] = hi ? v : lo ? v & 0xffffu : 0u;
+        }
+      }
+    }
+  }
+};
+
+__device__ __forceinline__ void ring_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void ring_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Slots of a ring whose rows take `bytes` a thread: two blocks of 256 threads an SM.
+__host__ __device__ constexpr int ring_slots(int bytes) { return bytes <= 16 ? 8 : bytes <= 32 ? 6 : bytes <= 64 ? 5 : 3; }
+
+// The thread's E elements to a row, rounded to T.
+template <typename T, int VEC, int E>
+__device__ __forceinline__ void store_row(T* p, int t, int tpr, int cols, const float2 (&o)[E / 2]) {
+  if constexpr (VEC == 2) {
+    const bool whole = (reinterpret_cast<uintptr_t>(p) & (2 * sizeof(T) - 1)) == 0;
+#pragma unroll
+    for (int j = 0; j < E / 2; ++j) {
+      const int c = 2 * (t + j * tpr);
+      if (whole && c + 1 < cols) {
+        if constexpr (sizeof(T) == 4)
+          *reinterpret_cast<float2*>(p + c) = o[j];
+        else
+          *reinterpret_cast<uint32_t*>(p + c) = to_bf16_pair(o[j]);
+      } else {
+        if (c < cols) ln_store(p + c, o[j].x);
+        if (c + 1 < cols) ln_store(p + c + 1, o[j].y);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < E / VEC; ++j) {
+      const int c = (t + j * tpr) * VEC;
+      if (c >= cols) continue;
+      if constexpr (sizeof(T) == 4)
+        *reinterpret_cast<float4*>(p + c) = make_float4(o[2 * j].x, o[2 * j].y, o[2 * j + 1].x, o[2 * j + 1].y);
+      else
+        *reinterpret_cast<uint4*>(p + c) = make_uint4(to_bf16_pair(o[4 * j]), to_bf16_pair(o[4 * j + 1]),
+                                                      to_bf16_pair(o[4 * j + 2]), to_bf16_pair(o[4 * j + 3]));
+    }
+  }
+}
+
+// A thread's place: its group of tpr threads in the block, and where the
+// group's warps leave their sums ([2 phases][warps] float2 in shared memory).
+struct Place {
+  int tpr, t, g, warps, bar;
+  float2 *red, *mine;
+};
+
+__device__ __forceinline__ Place ln_place(int tpr, float2* red) {
+  Place p;
+  p.tpr = tpr;
+  p.g = threadIdx.x / tpr;
+  p.t = threadIdx.x - p.g * tpr;
+  p.warps = tpr >> 5;
+  p.bar = 1 + p.g;  // barrier 0 is the block's
+  p.red = red + p.g * 2 * p.warps;
+  p.mine = p.red + (p.t >> 5);
+  return p;
+}
+
+// Sums over the group, the same bits for each of its threads.  Successive
+// calls alternate `phase`, so one barrier a call is enough: who writes a
+// phase again has passed the barrier of the other, after all of its reads.
+__device__ __forceinline__ void group_sum2(float& a, float& b, const Place& p, int phase) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const float x = __shfl_xor_sync(0xffffffffu, a, o), y = __shfl_xor_sync(0xffffffffu, b, o);
+    if (o < p.tpr) {
+      a = __fadd_rn(a, x);
+      b = __fadd_rn(b, y);
+    }
+  }
+  if (p.tpr <= 32) return;
+  const int at = phase ? p.warps : 0;
+  if ((threadIdx.x & 31) == 0) p.mine[at] = make_float2(a, b);
+  asm volatile("bar.sync %0, %1;" ::"r"(p.bar), "r"(p.tpr) : "memory");
+  a = b = 0.0f;
+#pragma unroll 4
+  for (int k = 0; k < p.warps; ++k) {
+    const float2 v = p.red[at + k];
+    a = __fadd_rn(a, v.x);
+    b = __fadd_rn(b, v.y);
+  }
+}
+
+__device__ __forceinline__ float group_sum(float a, const Place& p, int phase) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const float x = __shfl_xor_sync(0xffffffffu, a, o);
+    if (o < p.tpr) a = __fadd_rn(a, x);
+  }
+  if (p.tpr <= 32) return a;
+  const int at = phase ? p.warps : 0;
+  if ((threadIdx.x & 31) == 0) p.mine[at].x = a;
+  asm volatile("bar.sync %0, %1;" ::"r"(p.bar), "r"(p.tpr) : "memory");
+  a = 0.0f;
+#pragma unroll 4
+  for (int k = 0; k < p.warps; ++k) a = __fadd_rn(a, p.red[at + k].x);
+  return a;
+}
+
+// The thread's E parameters of p, `none` without any and beyond the row.
+template <typename W, int VEC, int E>
+__device__ __forceinline__ void row_params(const W* p, float none, int t, int tpr, int cols, float2 (&o)[E / 2]) {
+#pragma unroll
+  for (int i = 0; i < E / 2; ++i) o[i] = both(none);
+  if (p == nullptr) return;
+#pragma unroll
+  for (int j = 0; j < E / VEC; ++j) {
+    const int c = (t + j * tpr) * VEC;
+    if (c >= cols) continue;
+    float2* v = o + j * VEC / 2;
+    if constexpr (VEC == 2) {
+      v[0].x = ln_load(p + c);
+      if (c + 1 < cols) v[0].y = ln_load(p + c + 1);
+    } else if constexpr (sizeof(W) == 4) {
+#pragma unroll
+      for (int i = 0; i < VEC / 4; ++i) {
+        const float4 f = __ldg(reinterpret_cast<const float4*>(p + c) + i);
+        v[2 * i] = make_float2(f.x, f.y);
+        v[2 * i + 1] = make_float2(f.z, f.w);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < VEC / 4; ++i) {
+        const uint2 u = __ldg(reinterpret_cast<const uint2*>(p + c) + i);
+        v[2 * i] = bf16_pair(u.x);
+        v[2 * i + 1] = bf16_pair(u.y);
+      }
+    }
+  }
+}
+
+template <typename T, typename W>
+struct LnFwd {
+  const T* x;
+  const W *w, *b;
+  T* y;
+  float *mean, *rstd;
+  int64_t ld_x, ld_y, rows;
+  int32_t cols, tpr;
+  float eps;
+};
+
+// The row in d (this thread's E elements, zeros beyond the row) to y.
+template <typename T, typename W, int VEC, int E>
+__device__ __forceinline__ void ln_fwd_row(const LnFwd<T, W>& a, float2 (&d)[E / 2], const float2 (&w)[E / 2],
+                                           const float2 (&b)[E / 2], int64_t row, T* y, const Place& p, float inv_c) {
+  float2 s = both(0.0f);
+#pragma unroll
+  for (int i = 0; i < E / 2; ++i) s = add2(s, d[i]);
+  const float mean = group_sum(s.x + s.y, p, 0) * inv_c;
+  s = both(0.0f);
+#pragma unroll
+  for (int i = 0; i < E / 2; ++i) {
+    d[i] = add2(d[i], both(-mean));
+    const int c = (p.t + (2 * i / VEC) * p.tpr) * VEC;
+    if constexpr (VEC == 2) {
+      if (c < a.cols) s.x = fmaf(d[i].x, d[i].x, s.x);
+      if (c + 1 < a.cols) s.y = fmaf(d[i].y, d[i].y, s.y);
+    } else if (c < a.cols) {
+      s = fma2(d[i], d[i], s);
+    }
+  }
+  const float rstd = 1.0f / sqrtf(group_sum(s.x + s.y, p, 1) * inv_c + a.eps);
+  if (row >= a.rows) return;
+#pragma unroll
+  for (int i = 0; i < E / 2; ++i) d[i] = fma2(mul2(d[i], both(rstd)), w[i], b[i]);
+  store_row<T, VEC, E>(y, p.t, p.tpr, a.cols, d);
+  if (p.t == 0) {
+    if (a.mean != nullptr) a.mean[row] = mean;
+    if (a.rstd != nullptr) a.rstd[row] = rstd;
+  }
+}
+
+// Few rows: a group a row, as many threads as its loads can use.
+template <typename T, typename W, int VEC, int E>
+__global__ void __launch_bounds__(1024) ln_fwd_kernel(const __grid_constant__ LnFwd<T, W> a) {
+  __shared__ float2 red[2 * 32];
+  pdl_wait();
+  pdl_trigger();
+  const Place p = ln_place(a.tpr, red);
+  const int64_t row = int64_t(blockIdx.x) * (blockDim.x / a.tpr) + p.g;
+  const bool on = row < a.rows;
+  float2 d[E / 2], w[E / 2], b[E / 2];
+  Row<T, VEC, E> x;
+  x.load(a.x + (on ? row : 0) * a.ld_x, p.t, p.tpr, a.cols, on);
+  row_params<W, VEC, E>(a.w, 1.0f, p.t, p.tpr, a.cols, w);
+  row_params<W, VEC, E>(a.b, 0.0f, p.t, p.tpr, a.cols, b);
+#pragma unroll
+  for (int i = 0; i < E / 2; ++i) d[i] = x.pair(i);
+  ln_fwd_row<T, W, VEC, E>(a, d, w, b, row, a.y + row * a.ld_y, p, 1.0f / static_cast<float>(a.cols));
+}
+
+// The group's threads have each other's copies (loose rows only).
+template <int VEC>
+__device__ __forceinline__ void group_meet(const Place& p) {
+  if constexpr (VEC == 2) {
+    if (p.tpr <= 32)
+      __syncwarp();
+    else
+      asm volatile("bar.sync %0, %1;" ::"r"(p.bar), "r"(p.tpr) : "memory");
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ Matrix matrix_of(const T* p, int64_t ld, int64_t rows, int32_t cols) {
+  return {reinterpret_cast<const uint8_t*>(p), reinterpret_cast<const uint8_t*>(p + (rows - 1) * ld + cols)};
+}
+
+// Many rows: blocks that stay, each group walking the rows with the stride
+// of the whole grid, the parameters in registers and the rows to come in
+// flight in shared memory.
+template <typename T, typename W, int VEC, int E>
+__global__ void __launch_bounds__(LN_RING_THREADS, 2) ln_fwd_ring_kernel(const __grid_constant__ LnFwd<T, W> a) {
+  extern __shared__ __align__(16) uint8_t ring[];
+  __shared__ float2 red[2 * (LN_RING_THREADS / 32)];
+  pdl_wait();
+  pdl_trigger();
+  using R = Ring<T, VEC, E>;
+  constexpr int SLOTS = ring_slots(R::BYTES);
+  const Place p = ln_place(a.tpr, red);
+  const int groups = blockDim.x / a.tpr, slot_bytes = R::BYTES * blockDim.x + R::EXTRA * groups;
+  const Matrix m = matrix_of(a.x, a.ld_x, a.rows, a.cols);
+  const int64_t step = int64_t(gridDim.x) * groups, x_step = step * a.ld_x, y_step = step * a.ld_y;
+  int64_t row = int64_t(blockIdx.x) * groups + p.g, ahead = row;
+  const T *x_ahead = a.x + ahead * a.ld_x, *x_now = x_ahead;
+  T* y = a.y + row * a.ld_y;
+  const auto issue = [&](int slot) {  // the next row to come
+    const bool on = ahead < a.rows;
+    R::issue(ring + slot * slot_bytes, on ? x_ahead : a.x, m, p.g, p.t, p.tpr, a.cols, on);
+    ring_commit();
+    ahead += step;
+    x_ahead += x_step;
+  };
+#pragma unroll 1
+  for (int s = 0; s < SLOTS - 1; ++s) issue(s);
+  float2 w[E / 2], b[E / 2];
+  row_params<W, VEC, E>(a.w, 1.0f, p.t, p.tpr, a.cols, w);
+  row_params<W, VEC, E>(a.b, 0.0f, p.t, p.tpr, a.cols, b);
+  const float inv_c = 1.0f / static_cast<float>(a.cols);
+  int slot = 0;
+  for (int64_t base = row - p.g; base < a.rows; base += step, row += step, y += y_step, x_now += x_step) {
+    ring_wait<SLOTS - 2>();
+    group_meet<VEC>(p);
+    float2 d[E / 2];
+    {
+      Row<T, VEC, E> x;
+      R::read(ring + slot * slot_bytes, x_now, p.g, p.t, p.tpr, a.cols, row < a.rows, x);
+#pragma unroll
+      for (int i = 0; i < E / 2; ++i) d[i] = x.pair(i);
+    }
+    issue(slot == 0 ? SLOTS - 1 : slot - 1);
+    slot = slot == SLOTS - 1 ? 0 : slot + 1;
+    ln_fwd_row<T, W, VEC, E>(a, d, w, b, row, y, p, inv_c);
+  }
+  ring_wait<0>();  // no copy outlives the slots
+}
+
+template <typename T, typename W>
+struct LnBwd {
+  const T *dy, *x;
+  const W* w;
+  const float *mean, *rstd;
+  T* dx;         // may be null
+  float* parts;  // [gridDim.x][2][cols], or null
+  int64_t ld_dy, ld_x, ld_dx, rows;
+  int32_t cols, tpr;
+};
+
+// A block's groups walk the rows with the stride of the whole grid; each
+// thread keeps its columns' dw and db in registers over all its rows, and the
+// block adds its groups' sums in shared memory into one part.  The next row
+// is in flight while a row is worked on.
+template <typename T, typename W, int VEC, int E>
+__global__ void __launch_bounds__(LN_BWD_THREADS) ln_bwd_kernel(const __grid_constant__ LnBwd<T, W> a) {
+  extern __shared__ __align__(16) float sums[];  // [threads][E] at a time; the groups' warp sums before that
+  pdl_wait();
+  pdl_trigger();
+  const Place p = ln_place(a.tpr, reinterpret_cast<float2*>(sums));
+  const int tpr = a.tpr, t = p.t, g = p.g, groups = blockDim.x / tpr;
+  const float inv_c = 1.0f / static_cast<float>(a.cols);
+  const int64_t step = int64_t(gridDim.x) * groups;
+  int64_t row = int64_t(blockIdx.x) * groups + g, ahead = row;
+  const int64_t x_step = step * a.ld_x, dy_step = step * a.ld_dy, dx_step = step * a.ld_dx;
+  const T *x_ahead = a.x + row * a.ld_x, *dy_ahead = a.dy + row * a.ld_dy, *x_now = x_ahead, *dy_now = dy_ahead;
+  T* dx = a.dx != nullptr ? a.dx + row * a.ld_dx : nullptr;
+  const Matrix mx = matrix_of(a.x, a.ld_x, a.rows, a.cols), my = matrix_of(a.dy, a.ld_dy, a.rows, a.cols);
+  Row<T, VEC, E> x, dy;
+  // Statistics two rows ahead (their loads are as far away as the rows').
+  float mean, rstd, mean_1, rstd_1, mean_2, rstd_2;
+  const auto stats = [&](int64_t r, float& m, float& s) {
+    m = r < a.rows ? __ldg(a.mean + r) : 0.0f;
+    s = r < a.rows ? __ldg(a.rstd + r) : 0.0f;
+  };
+  using R = Ring<T, VEC, E>;
+  constexpr int SLOTS = ring_slots(2 * R::BYTES);
+  uint8_t* ring = reinterpret_cast<uint8_t*>(sums) + LN_RED_BYTES;
+  const int half_slot = R::BYTES * blockDim.x + R::EXTRA * groups;
+  const auto fetch = [&](int slot) {  // the next rows to come
+    const bool on = ahead < a.rows;
+    uint8_t* at = ring + slot * (2 * half_slot);
+    R::issue(at, on ? x_ahead : a.x, mx, g, t, tpr, a.cols, on);
+    R::issue(at + half_slot, on ? dy_ahead : a.dy, my, g, t, tpr, a.cols, on);
+    ring_commit();
+    ahead += step;
+    x_ahead += x_step;
+    dy_ahead += dy_step;
+  };
+  int slot = 0, phase = 0;
+  if (a.rows > 0) {
+#pragma unroll 1
+    for (int s = 0; s < SLOTS - 1; ++s) fetch(s);
+  }
+  stats(row, mean, rstd);
+  stats(row + step, mean_1, rstd_1);
+  float2 w[E / 2], dw[E / 2], db[E / 2];
+  row_params<W, VEC, E>(a.w, 1.0f, t, tpr, a.cols, w);
+#pragma unroll
+  for (int i = 0; i < E / 2; ++i) dw[i] = db[i] = both(0.0f);
+  for (int64_t base = row - g; base < a.rows; base += step) {
+    stats(row + 2 * step, mean_2, rstd_2);
+    ring_wait<SLOTS - 2>();
+    group_meet<VEC>(p);
+    const uint8_t* at = ring + slot * (2 * half_slot);
+    R::read(at, x_now, g, t, tpr, a.cols, row < a.rows, x);
+    R::read(at + half_slot, dy_now, g, t, tpr, a.cols, row < a.rows, dy);
+    fetch(slot == 0 ? SLOTS - 1 : slot - 1);
+    slot = slot == SLOTS - 1 ? 0 : slot + 1;
+    x_now += x_step;
+    dy_now += dy_step;
+    float2 h[E / 2], dh[E / 2], s1 = both(0.0f), s2 = both(0.0f);
+#pragma unroll
+    for (int i = 0; i < E / 2; ++i) {
+      const float2 d = dy.pair(i);
+      h[i] = mul2(add2(x.pair(i), both(-mean)), both(rstd));
+      dh[i] = mul2(d, w[i]);
+      s1 = add2(s1, dh[i]);
+      s2 = fma2(dh[i], h[i], s2);
+      dw[i] = fma2(d, h[i], dw[i]);
+      db[i] = add2(db[i], d);
+    }
+    if (dx != nullptr) {
+      float c1 = s1.x + s1.y, c2 = s2.x + s2.y;
+      group_sum2(c1, c2, p, phase);
+      phase ^= 1;
+      // dx = r dh - r c1 - h r c2
+      c1 *= -inv_c * rstd;
+      c2 *= -inv_c * rstd;
+#pragma unroll
+      for (int i = 0; i < E / 2; ++i) dh[i] = fma2(h[i], both(c2), fma2(dh[i], both(rstd), both(c1)));
+      if (row < a.rows) store_row<T, VEC, E>(dx, t, tpr, a.cols, dh);
+      dx += dx_step;
+    }
+    row += step;
+    mean = mean_1;
+    rstd = rstd_1;
+    mean_1 = mean_2;
+    rstd_1 = rstd_2;
+  }
+  ring_wait<0>();  // no copy outlives the slots
+  if (a.parts == nullptr) return;
+  float* part = a.parts + int64_t(blockIdx.x) * 2 * a.cols;
+#pragma unroll
+  for (int pass = 0; pass < 2; ++pass) {
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+      const float2 v = pass == 0 ? dw[i / 2] : db[i / 2];
+      sums[(i / VEC * tpr + t) * VEC + i % VEC + g * tpr * E] = i & 1 ? v.y : v.x;
+    }
+    __syncthreads();
+    for (int c = threadIdx.x; c < a.cols; c += blockDim.x) {
+      float s = sums[c];
+      for (int k = 1; k < groups; ++k) s += sums[c + k * tpr * E];
+      part[pass * a.cols + c] = s;
+    }
+  }
 }
 
 // ------------------------------------------------ any width, any alignment
@@ -125,25 +635,32 @@ __global__ void __launch_bounds__(LN_THREADS) ln_dparam_any_kernel(const T* __re
   p[cols + c] = db;
 }
 
-// dw and db from the parts, in the parts' order.  A block takes 32 of the
-// 2 C sums, warp k of it the parts k, k + 8, ...
+// dw and db from the parts, in a fixed order.  A block takes 32 of the 2 C
+// sums, warp k of it the parts k, k + 32, ...
 template <typename D>
-__global__ void __launch_bounds__(LN_THREADS) ln_dparam_sum_kernel(const float* __restrict__ parts, int32_t n_parts,
-                                                                   int32_t cols, D* __restrict__ dw, D* __restrict__ db) {
-  __shared__ float red[LN_THREADS / 32][32];
+__global__ void __launch_bounds__(1024) ln_dparam_sum_kernel(const float* __restrict__ parts, int32_t n_parts, int32_t cols,
+                                                             D* __restrict__ dw, D* __restrict__ db) {
+  __shared__ float red[32][33];
   pdl_wait();
   pdl_trigger();
   const int lane = threadIdx.x & 31, k = threadIdx.x >> 5;
   const int64_t c = int64_t(blockIdx.x) * 32 + lane, width = 2 * int64_t(cols);
   float s = 0.0f;
-  if (c < width)
-    for (int p = k; p < n_parts; p += LN_THREADS / 32) s += parts[p * width + c];
+  if (c < width) {
+    float x[(LN_PARTS + 31) / 32];  // all in flight at once
+#pragma unroll
+    for (int i = 0; i < (LN_PARTS + 31) / 32; ++i) x[i] = k + 32 * i < n_parts ? parts[(k + 32 * i) * width + c] : 0.0f;
+#pragma unroll
+    for (int i = 0; i < (LN_PARTS + 31) / 32; ++i) s += x[i];
+  }
   red[k][lane] = s;
   __syncthreads();
-  if (k != 0 || c >= width) return;
-  for (int j = 1; j < LN_THREADS / 32; ++j) s += red[j][lane];
-  D* out = c < cols ? dw : db;
-  if (out != nullptr) ln_store(out + (c < cols ? c : c - cols), s);
+  // warp k adds up the sum of column k
+  s = warp_sum(red[lane][k]);
+  const int64_t col = int64_t(blockIdx.x) * 32 + k;
+  if (lane != 0 || col >= width) return;
+  D* out = col < cols ? dw : db;
+  if (out != nullptr) ln_store(out + (col < cols ? col : col - cols), s);
 }
 
 int32_t ln_parts(int64_t rows) { return static_cast<int32_t>(rows < LN_PARTS ? (rows > 0 ? rows : 1) : LN_PARTS); }
@@ -165,37 +682,134 @@ grs_status check_norm(const grs_norm* s, const char* who, LnLd* ld) {
   return GRS_OK;
 }
 
+// Whether every row of a matrix starts at a multiple of 16 bytes.
+bool rows16(const void* p, int64_t ld, int esize) { return api_aligned(p, 16) && ld * esize % 16 == 0; }
+
+// Threads of a row of `cols` elements with e elements a thread: a power of two up to a warp, then whole warps.
+int32_t ln_tpr(int32_t cols, int e) {
+  const int64_t need = (int64_t(cols) + e - 1) / e;
+  if (need > 32) return static_cast<int32_t>((need + 31) / 32 * 32);
+  int32_t t = 1;
+  while (t < need) t *= 2;
+  return t;
+}
+
+template <typename T, typename W, int VEC, int E, bool kRing>
+cudaError_t ln_forward_e(const LnFwd<T, W>& args, void* stream) {
+  LnFwd<T, W> a = args;
+  a.tpr = ln_tpr(a.cols, E);
+  if constexpr (kRing) {
+    const int groups = LN_RING_THREADS / a.tpr, threads = groups * a.tpr;
+    int64_t grid = (a.rows + groups - 1) / groups;
+    // Two blocks an SM; one for an fp32 matrix beyond L2: 65536 x 1024 takes 82 us
+    // with one and 94 with two (8192 x 1024 the other way round, 14.1 and 13.0).
+    const int64_t most = sizeof(T) == 4 && a.rows * a.cols * 4 > (int64_t(128) << 20) ? 152 : 304;
+    if (grid > most) grid = most;
+    using R = Ring<T, VEC, E>;
+    constexpr int SLOTS = ring_slots(R::BYTES);
+    const cudaError_t e = allow_smem<ln_fwd_ring_kernel<T, W, VEC, E>>(SLOTS * LN_RING_THREADS * (R::BYTES + R::EXTRA));
+    if (e != cudaSuccess) return e;
+    return launch_pdl(ln_fwd_ring_kernel<T, W, VEC, E>, dim3(static_cast<unsigned>(grid)), dim3(threads),
+                    size_t(SLOTS) * (threads * R::BYTES + groups * R::EXTRA), stream, a);
+  } else {
+    const int threads = a.tpr > 128 ? a.tpr : 128 / a.tpr * a.tpr;
+    const int64_t per = threads / a.tpr;
+    return launch_pdl(ln_fwd_kernel<T, W, VEC, E>, dim3(static_cast<unsigned>((a.rows + per - 1) / per)), dim3(threads), 0, stream, a);
+  }
+}
+
+// Measured on bf16 rows of 2048: 32 elements a thread (64 threads a row)
+// take 43.6 us for 32768 rows against 50.6 with 16 and 94 with 8, whose sums
+// meet across more warps; up to 4096 rows 16 fill the SMs better, and a few
+// rows are done soonest with 8 (one row: 2.2 us).
+template <typename T, typename W, int VEC>
+cudaError_t ln_forward_vec(const LnFwd<T, W>& a, void* stream, bool* done) {
+  const int t8 = ln_tpr(a.cols, 8), t16 = ln_tpr(a.cols, 16);
+  *done = a.rows <= INT32_MAX && t16 <= 1024;
+  if (!*done) return cudaSuccess;
+  if constexpr (VEC == 8)
+    if (a.rows >= 4096 && ln_tpr(a.cols, 32) <= LN_RING_THREADS) return ln_forward_e<T, W, VEC, 32, true>(a, stream);
+  if (a.rows > 1216 && t16 <= LN_RING_THREADS) return ln_forward_e<T, W, VEC, 16, true>(a, stream);
+  if (t8 <= 1024) return ln_forward_e<T, W, VEC, 8, false>(a, stream);
+  return ln_forward_e<T, W, VEC, 16, false>(a, stream);
+}
+
 template <typename T, typename W>
 cudaError_t ln_forward(const grs_norm* s, const LnLd& ld, const void* x, const void* w, const void* b, void* y, float* mean,
                        float* rstd, void* stream) {
+  const LnFwd<T, W> a{static_cast<const T*>(x), static_cast<const W*>(w), static_cast<const W*>(b), static_cast<T*>(y), mean,
+                      rstd, ld.x, ld.y, s->rows, s->cols, 0, s->eps};
+  constexpr int VEC = 16 / sizeof(T);
+  bool done = false;
+  const bool vec = s->cols % VEC == 0 && rows16(x, ld.x, sizeof(T)) && rows16(y, ld.y, sizeof(T)) && api_aligned(w, 16) && api_aligned(b, 16);
+  const cudaError_t e = vec ? ln_forward_vec<T, W, VEC>(a, stream, &done) : ln_forward_vec<T, W, 2>(a, stream, &done);
+  if (done || e != cudaSuccess) return e;
   const unsigned grid = static_cast<unsigned>(s->rows < 1 << 20 ? s->rows : 1 << 20);
-  return launch_k(ln_fwd_any_kernel<T, W>, dim3(grid), dim3(LN_THREADS), 0, stream, static_cast<const T*>(x), ld.x,
-                  static_cast<const W*>(w), static_cast<const W*>(b), static_cast<T*>(y), ld.y, mean, rstd, s->rows, s->cols,
-                  s->eps);
+  return launch_pdl(ln_fwd_any_kernel<T, W>, dim3(grid), dim3(LN_THREADS), 0, stream, a.x, ld.x, a.w, a.b, a.y, ld.y, mean, rstd,
+                  s->rows, s->cols, s->eps);
+}
+
+template <typename T, typename W, int VEC, int E>
+cudaError_t ln_backward_e(const LnBwd<T, W>& args, int32_t* parts, void* stream) {
+  LnBwd<T, W> a = args;
+  a.tpr = ln_tpr(a.cols, E);
+  const int groups = a.tpr > 256 ? 1 : 256 / a.tpr, threads = groups * a.tpr;
+  int64_t grid = (a.rows + groups - 1) / groups;
+  if (grid > LN_PARTS) grid = LN_PARTS;
+  if (grid < 1) grid = 1;
+  *parts = static_cast<int32_t>(grid);
+  using R = Ring<T, VEC, E>;
+  constexpr int SLOTS = ring_slots(2 * R::BYTES);
+  const size_t sums = size_t(threads) * E * 4;  // the groups' sums at the end, in the ring's place
+  const size_t ring = LN_RED_BYTES + size_t(SLOTS) * 2 * (threads * R::BYTES + groups * R::EXTRA);
+  constexpr int most = LN_RED_BYTES + SLOTS * 2 * LN_BWD_THREADS * (R::BYTES + R::EXTRA / 4);
+  static_assert(most <= 227 * 1024, "shared memory of a block");
+  const cudaError_t e = allow_smem<ln_bwd_kernel<T, W, VEC, E>>(most);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(ln_bwd_kernel<T, W, VEC, E>, dim3(static_cast<unsigned>(grid)), dim3(threads), ring > sums ? ring : sums, stream, a);
+}
+
+template <typename T, typename W, int VEC>
+cudaError_t ln_backward_vec(const LnBwd<T, W>& a, int32_t* parts, void* stream) {
+  const int t8 = ln_tpr(a.cols, 8), t16 = ln_tpr(a.cols, 16);
+  // Fewer elements a thread where registers are short (fp32) or rows few.
+  if ((a.rows <= LN_PARTS || sizeof(T) == 4) && t8 <= LN_BWD_THREADS) return ln_backward_e<T, W, VEC, 8>(a, parts, stream);
+  if (t16 <= LN_BWD_THREADS) return ln_backward_e<T, W, VEC, 16>(a, parts, stream);
+  return cudaSuccess;
 }
 
 template <typename T, typename W>
 cudaError_t ln_backward(const grs_norm* s, const LnLd& ld, const void* dy, const void* x, const void* w, const float* mean,
                         const float* rstd, void* dx, void* dw, void* db, float* ws, void* stream) {
-  cudaError_t e = cudaSuccess;
-  if (dx != nullptr && s->rows > 0) {
-    const unsigned grid = static_cast<unsigned>(s->rows < 1 << 20 ? s->rows : 1 << 20);
-    e = launch_k(ln_dx_any_kernel<T, W>, dim3(grid), dim3(LN_THREADS), 0, stream, static_cast<const T*>(dy), ld.dy,
-                 static_cast<const T*>(x), ld.x, static_cast<const W*>(w), mean, rstd, static_cast<T*>(dx), ld.dx, s->rows,
-                 s->cols);
-  }
-  if (e != cudaSuccess || (dw == nullptr && db == nullptr)) return e;
-  const int32_t parts = ln_parts(s->rows);
-  e = launch_k(ln_dparam_any_kernel<T>, dim3((unsigned(s->cols) + LN_THREADS - 1) / LN_THREADS, unsigned(parts)),
-               dim3(LN_THREADS), 0, stream, static_cast<const T*>(dy), ld.dy, static_cast<const T*>(x), ld.x, mean, rstd, ws,
-               s->rows, s->cols);
+  const bool params = dw != nullptr || db != nullptr;
+  const LnBwd<T, W> a{static_cast<const T*>(dy), static_cast<const T*>(x), static_cast<const W*>(w), mean, rstd,
+                      static_cast<T*>(dx), params ? ws : nullptr, ld.dy, ld.x, ld.dx, s->rows, s->cols, 0};
+  if (dx == nullptr && !params) return cudaSuccess;
+  constexpr int VEC = 16 / sizeof(T);
+  const bool vec = s->cols % VEC == 0 && rows16(x, ld.x, sizeof(T)) && rows16(dy, ld.dy, sizeof(T)) &&
+                   (dx == nullptr || rows16(dx, ld.dx, sizeof(T))) && api_aligned(w, 16);
+  int32_t parts = 0;
+  cudaError_t e = vec ? ln_backward_vec<T, W, VEC>(a, &parts, stream) : ln_backward_vec<T, W, 2>(a, &parts, stream);
   if (e != cudaSuccess) return e;
+  if (parts == 0) {  // rows wider than the registers of a block
+    if (dx != nullptr && s->rows > 0) {
+      const unsigned grid = static_cast<unsigned>(s->rows < 1 << 20 ? s->rows : 1 << 20);
+      e = launch_pdl(ln_dx_any_kernel<T, W>, dim3(grid), dim3(LN_THREADS), 0, stream, a.dy, ld.dy, a.x, ld.x, a.w, mean, rstd, a.dx,
+                   ld.dx, s->rows, s->cols);
+    }
+    if (e != cudaSuccess || !params) return e;
+    parts = ln_parts(s->rows);
+    e = launch_pdl(ln_dparam_any_kernel<T>, dim3((unsigned(s->cols) + LN_THREADS - 1) / LN_THREADS, unsigned(parts)),
+                 dim3(LN_THREADS), 0, stream, a.dy, ld.dy, a.x, ld.x, mean, rstd, ws, s->rows, s->cols);
+    if (e != cudaSuccess) return e;
+  }
+  if (!params) return cudaSuccess;
   const dim3 grid(static_cast<unsigned>((2 * int64_t(s->cols) + 31) / 32));
   const float* parts_in = ws;
   return s->grad_dtype == GRS_DTYPE_FP32
-             ? launch_k(ln_dparam_sum_kernel<float>, grid, dim3(LN_THREADS), 0, stream, parts_in, parts, s->cols,
+             ? launch_pdl(ln_dparam_sum_kernel<float>, grid, dim3(1024), 0, stream, parts_in, parts, s->cols,
                         static_cast<float*>(dw), static_cast<float*>(db))
-             : launch_k(ln_dparam_sum_kernel<uint16_t>, grid, dim3(LN_THREADS), 0, stream, parts_in, parts, s->cols,
+             : launch_pdl(ln_dparam_sum_kernel<uint16_t>, grid, dim3(1024), 0, stream, parts_in, parts, s->cols,
                         static_cast<uint16_t*>(dw), static_cast<uint16_t*>(db));
 }
 

@@ -535,8 +535,8 @@ grs_status launch_list_step(const grs_tensors* l, const ListArgs& a, int32_t gra
   ApiDevice dev(l->device);
   if (!dev.ok()) return api_fail(GRS_ERR_CUDA, who, "cannot select the list's device");
   const dim3 grid(static_cast<unsigned>(l->n_tiles)), block(LIST_THREADS);
-  const cudaError_t e = grad_dtype == GRS_DTYPE_FP32 ? launch_k(list_step_kernel<float, k8>, grid, block, 0, stream, a)
-                                                     : launch_k(list_step_kernel<uint16_t, k8>, grid, block, 0, stream, a);
+  const cudaError_t e = grad_dtype == GRS_DTYPE_FP32 ? launch_pdl(list_step_kernel<float, k8>, grid, block, 0, stream, a)
+                                                     : launch_pdl(list_step_kernel<uint16_t, k8>, grid, block, 0, stream, a);
   return e == cudaSuccess ? GRS_OK : api_cuda_fail(e, who);
 }
 
@@ -660,14 +660,14 @@ grs_status grs_tensors_norm_sq(const grs_tensors* l, const void* const* d_grads,
     const dim3 grid(static_cast<unsigned>(l->n_tiles)), block(LIST_THREADS);
     const ListTile* tiles = l->d_tiles;
     e = grad_dtype == GRS_DTYPE_FP32
-            ? launch_k(list_norm_kernel<float>, grid, block, 0, stream, tiles, l->n_tiles,
+            ? launch_pdl(list_norm_kernel<float>, grid, block, 0, stream, tiles, l->n_tiles,
                        reinterpret_cast<const float* const*>(d_grads), nt, partials, l->d_flags)
-            : launch_k(list_norm_kernel<uint16_t>, grid, block, 0, stream, tiles, l->n_tiles,
+            : launch_pdl(list_norm_kernel<uint16_t>, grid, block, 0, stream, tiles, l->n_tiles,
                        reinterpret_cast<const uint16_t* const*>(d_grads), nt, partials, l->d_flags);
   }
   if (e != cudaSuccess) return api_cuda_fail(e, who);
   const double inv_m = 1.0 / static_cast<double>(n_micro);
-  e = launch_k(list_norm_finish_kernel, dim3(NORM_L2_BLOCKS), dim3(LIST_THREADS), 0, stream, partials, l->n_tiles, level2,
+  e = launch_pdl(list_norm_finish_kernel, dim3(NORM_L2_BLOCKS), dim3(LIST_THREADS), 0, stream, partials, l->n_tiles, level2,
                ticket, inv_m * inv_m, d_norm_sq, l->d_flags);
   return e == cudaSuccess ? GRS_OK : api_cuda_fail(e, who);
 }
@@ -719,7 +719,7 @@ static grs_status convert(const grs_tensors* l, float* m, float* v, uint8_t* m8,
   ApiDevice dev(l->device);
   if (!dev.ok()) return api_fail(GRS_ERR_CUDA, who, "cannot select the list's device");
   const ConvertArgs a{l->d_tiles, m, v, m8, s8, m_scale, s_scale, l->d_flags, l->n_tiles, l->n_state};
-  const cudaError_t e = launch_k(pack ? list_pack8_kernel : list_unpack8_kernel, dim3(static_cast<unsigned>(l->n_tiles)),
+  const cudaError_t e = launch_pdl(pack ? list_pack8_kernel : list_unpack8_kernel, dim3(static_cast<unsigned>(l->n_tiles)),
                                  dim3(LIST_THREADS), 0, stream, a);
   return e == cudaSuccess ? GRS_OK : api_cuda_fail(e, who);
 }

@@ -258,17 +258,17 @@ grs_status grs_moe_sort(const grs_moe* s, const int32_t* expert_ids, int32_t* ex
     e = cudaMemsetAsync(expert_offsets, 0, (size_t(count) + 1) * 4, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? GRS_OK : api_cuda_fail(e, who);
   }
-  e = launch_k(moe_count_kernel, dim3(chunks), dim3(MOE_SORT_THREADS), count * 4, stream, expert_ids, n, s->expert_begin, count,
+  e = launch_pdl(moe_count_kernel, dim3(chunks), dim3(MOE_SORT_THREADS), count * 4, stream, expert_ids, n, s->expert_begin, count,
                counts);
   if (e == cudaSuccess)
-    e = launch_k(moe_scan_kernel, dim3(1), dim3(MOE_SORT_THREADS), 0, stream, counts, chunks, count, expert_offsets);
+    e = launch_pdl(moe_scan_kernel, dim3(1), dim3(MOE_SORT_THREADS), 0, stream, counts, chunks, count, expert_offsets);
   if (e == cudaSuccess) {
     const size_t smem = size_t(MOE_WARPS) * count * 4;
     if (smem > 48 * 1024)
       e = cudaFuncSetAttribute(moe_rows_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     const int32_t *starts = counts, *offsets = expert_offsets;
     if (e == cudaSuccess)
-      e = launch_k(moe_rows_kernel, dim3(chunks), dim3(MOE_SORT_THREADS), smem, stream, expert_ids, n, s->expert_begin, count,
+      e = launch_pdl(moe_rows_kernel, dim3(chunks), dim3(MOE_SORT_THREADS), smem, stream, expert_ids, n, s->expert_begin, count,
                    starts, offsets, row_slot, slot_row);
   }
   return e == cudaSuccess ? GRS_OK : api_cuda_fail(e, who);
@@ -285,9 +285,9 @@ grs_status grs_moe_dispatch(const grs_moe* s, const void* x, const int32_t* slot
     return api_fail(GRS_ERR_ALIGNMENT, who, "a pointer is not aligned to its element");
   const dim3 grid(moe_grid(s->tokens)), block(MOE_THREADS);
   const cudaError_t e = s->dtype == GRS_DTYPE_FP32
-                            ? launch_k(moe_dispatch_kernel<float>, grid, block, 0, stream, static_cast<const float*>(x), slot_row,
+                            ? launch_pdl(moe_dispatch_kernel<float>, grid, block, 0, stream, static_cast<const float*>(x), slot_row,
                                        static_cast<float*>(xs), s->tokens, s->top_k, s->hidden)
-                            : launch_k(moe_dispatch_kernel<uint16_t>, grid, block, 0, stream, static_cast<const uint16_t*>(x),
+                            : launch_pdl(moe_dispatch_kernel<uint16_t>, grid, block, 0, stream, static_cast<const uint16_t*>(x),
                                        slot_row, static_cast<uint16_t*>(xs), s->tokens, s->top_k, s->hidden);
   return e == cudaSuccess ? GRS_OK : api_cuda_fail(e, who);
 }
@@ -305,9 +305,9 @@ static grs_status combine(const grs_moe* s, const void* ys, const int32_t* slot_
   const dim3 grid(moe_grid(s->tokens)), block(MOE_THREADS);
   const cudaError_t e =
       s->dtype == GRS_DTYPE_FP32
-          ? launch_k(moe_combine_kernel<float>, grid, block, 0, stream, static_cast<const float*>(ys), slot_row, weights,
+          ? launch_pdl(moe_combine_kernel<float>, grid, block, 0, stream, static_cast<const float*>(ys), slot_row, weights,
                      static_cast<float*>(y), s->tokens, s->top_k, s->hidden)
-          : launch_k(moe_combine_kernel<uint16_t>, grid, block, 0, stream, static_cast<const uint16_t*>(ys), slot_row, weights,
+          : launch_pdl(moe_combine_kernel<uint16_t>, grid, block, 0, stream, static_cast<const uint16_t*>(ys), slot_row, weights,
                      static_cast<uint16_t*>(y), s->tokens, s->top_k, s->hidden);
   return e == cudaSuccess ? GRS_OK : api_cuda_fail(e, who);
 }
@@ -335,9 +335,9 @@ grs_status grs_moe_combine_backward(const grs_moe* s, const void* dy, const void
   const dim3 grid(moe_grid(s->tokens * s->top_k)), block(MOE_THREADS);
   const cudaError_t e =
       s->dtype == GRS_DTYPE_FP32
-          ? launch_k(moe_combine_bwd_kernel<float>, grid, block, 0, stream, static_cast<const float*>(dy),
+          ? launch_pdl(moe_combine_bwd_kernel<float>, grid, block, 0, stream, static_cast<const float*>(dy),
                      static_cast<const float*>(ys), slot_row, weights, static_cast<float*>(dys), dweights, s->tokens, s->top_k, s->hidden)
-          : launch_k(moe_combine_bwd_kernel<uint16_t>, grid, block, 0, stream, static_cast<const uint16_t*>(dy),
+          : launch_pdl(moe_combine_bwd_kernel<uint16_t>, grid, block, 0, stream, static_cast<const uint16_t*>(dy),
                      static_cast<const uint16_t*>(ys), slot_row, weights, static_cast<uint16_t*>(dys), dweights, s->tokens, s->top_k,
                      s->hidden);
   return e == cudaSuccess ? GRS_OK : api_cuda_fail(e, who);

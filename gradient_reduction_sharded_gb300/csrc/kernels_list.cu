@@ -19,6 +19,7 @@
 #include "device.cuh"
 #include "internal.h"
 #include "launch.cuh"
+#include "packed.cuh"
 
 namespace grs {
 namespace {
@@ -33,7 +34,7 @@ struct alignas(16) ListTile {
   int64_t e0;      // first element in the tensor
   int32_t tensor;
   int32_t n;       // elements of the tensor in the tile
-  int64_t pad_;
+  int64_t rest;    // elements of the tensor from e0 on
 };
 static_assert(sizeof(ListTile) == 32, "two 16-byte loads");
 
@@ -59,66 +60,183 @@ __device__ __forceinline__ ListTile load_tile(const ListTile* p) {
   t.e0 = (int64_t(a.w) << 32) | uint32_t(a.z);
   t.tensor = b.x;
   t.n = b.y;
-  t.pad_ = 0;
+  t.rest = (int64_t(b.w) << 32) | uint32_t(b.z);
   return t;
 }
 
-__device__ __forceinline__ float as_float(uint16_t bits) { return __uint_as_float(uint32_t(bits) << 16); }
-__device__ __forceinline__ float as_float(float x) { return x; }
+// A warp's 256 consecutive elements of a tensor that starts at any multiple
+// of its element: 8 to a lane.
+//
+// Aligned runs go as 16-byte chunks.  For the others every lane moves the
+// aligned chunk (or two, in fp32) that holds its first element, and the
+// elements that lie in the next lane's chunk cross by a shuffle: K words and
+// perhaps half a word.  Only the run's two ends go by element, or all of a
+// run that the tensor's own ends cut short (`inner` false): a chunk that
+// reaches outside the tensor is not touched.
+struct Run {
+  int mis;     // bytes that the run starts after a 16-byte boundary
+  bool inner;  // 8 elements of the tensor before the run and 8 after it
+};
 
-// Elements [0, n) of the 8 at p (zeros beyond), one by one.
 template <typename G>
-__device__ __forceinline__ void load8_slow(const G* p, int n, float (&o)[8]) {
+__device__ __forceinline__ Run run_of(const G* p, int64_t before, int64_t rest) {
+  return {static_cast<int>(reinterpret_cast<uintptr_t>(p) & 15), before >= 8 && rest >= 264};
+}
+
+// The N words that start BYTES (even, below 16) after the first of (own, next).
+template <int BYTES, int N>
+__device__ __forceinline__ void shift_words(const uint32_t (&own)[N], const uint32_t (&next)[4], uint32_t (&o)[N]) {
+  constexpr int K = BYTES / 4;
+  uint32_t w[N + 4];
 #pragma unroll
-  for (int q = 0; q < 8; ++q) o[q] = q < n ? as_float(p[q]) : 0.0f;
+  for (int i = 0; i < N; ++i) w[i] = own[i];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w[N + i] = next[i];
+#pragma unroll
+  for (int i = 0; i < N; ++i) o[i] = (BYTES & 2) != 0 ? __funnelshift_r(w[i + K], w[i + K + 1], 16) : w[i + K];
 }
 
-__device__ __forceinline__ void load8(const uint16_t* p, int n, float (&o)[8]) {
-  if (n >= 8 && (reinterpret_cast<uintptr_t>(p) & 15u) == 0) {
-    const uint4 w = __ldcs(reinterpret_cast<const uint4*>(p));
-    set_bf16x8(o, w);
-  } else {
-    load8_slow(p, n, o);
+// The lane's N words from p, MIS bytes after a 16-byte boundary; whole warp.
+template <int MIS, int N>
+__device__ __forceinline__ void load_shifted(const uint8_t* p, uint32_t (&o)[N]) {
+  const uint4* c = reinterpret_cast<const uint4*>(p - MIS);
+  uint32_t own[N];
+#pragma unroll
+  for (int i = 0; i < N / 4; ++i) {
+    const uint4 v = __ldcs(c + i);
+    own[4 * i] = v.x;
+    own[4 * i + 1] = v.y;
+    own[4 * i + 2] = v.z;
+    own[4 * i + 3] = v.w;
+  }
+  const bool end = (threadIdx.x & 31) == 31;
+  uint4 last;
+  if (end) last = __ldcs(c + N / 4);
+  uint32_t next[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) next[i] = __shfl_down_sync(0xffffffffu, own[i], 1);
+  if (end) {
+    next[0] = last.x;
+    next[1] = last.y;
+    next[2] = last.z;
+    next[3] = last.w;
+  }
+  shift_words<MIS>(own, next, o);
+}
+
+// The lane's 4 words to p, MIS bytes after a 16-byte boundary; whole warp.
+// The aligned chunk that starts in a lane's words ends in the next lane's.
+template <int MIS>
+__device__ __forceinline__ void store_shifted(uint8_t* p, const uint32_t (&w)[4]) {
+  constexpr int SKIP = 16 - MIS, HALF = MIS & 2;
+  const int lane = threadIdx.x & 31;
+  uint32_t next[4], c[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) next[i] = __shfl_down_sync(0xffffffffu, w[i], 1);
+  shift_words<SKIP>(w, next, c);
+  if (lane < 31) __stcs(reinterpret_cast<uint4*>(p + SKIP), make_uint4(c[0], c[1], c[2], c[3]));
+  if (lane == 0) {  // the run's first SKIP bytes
+    if (HALF) *reinterpret_cast<uint16_t*>(p) = static_cast<uint16_t>(w[0]);
+#pragma unroll
+    for (int j = 0; j < SKIP / 4; ++j)
+      *reinterpret_cast<uint32_t*>(p + HALF + 4 * j) = HALF ? __funnelshift_r(w[j], w[j + 1 < 4 ? j + 1 : 3], 16) : w[j];
+  }
+  if (lane == 31) {  // and its last MIS bytes
+#pragma unroll
+    for (int j = 0; j < MIS / 4; ++j) *reinterpret_cast<uint32_t*>(p + SKIP + 4 * j) = c[j];
+    if (HALF) *reinterpret_cast<uint16_t*>(p + 14) = static_cast<uint16_t>(w[3] >> 16);
   }
 }
 
-__device__ __forceinline__ void load8(const float* p, int n, float (&o)[8]) {
-  if (n >= 8 && (reinterpret_cast<uintptr_t>(p) & 15u) == 0) {
-    const float4 a = __ldcs(reinterpret_cast<const float4*>(p));
-    const float4 b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
-    o[0] = a.x; o[1] = a.y; o[2] = a.z; o[3] = a.w;
-    o[4] = b.x; o[5] = b.y; o[6] = b.z; o[7] = b.w;
+// Elements [0, n) of the lane's 8 at p, zeros beyond; whole warp.
+__device__ __forceinline__ void load8(const uint16_t* p, Run r, int n, float2 (&o)[4]) {
+  uint32_t w[4];
+  if (r.mis == 0 && n >= 8) {
+    const uint4 v = __ldcs(reinterpret_cast<const uint4*>(p));
+    w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
+  } else if (r.inner) {
+    const uint8_t* b = reinterpret_cast<const uint8_t*>(p);
+    switch (r.mis) {
+      case 2: load_shifted<2>(b, w); break;
+      case 4: load_shifted<4>(b, w); break;
+      case 6: load_shifted<6>(b, w); break;
+      case 8: load_shifted<8>(b, w); break;
+      case 10: load_shifted<10>(b, w); break;
+      case 12: load_shifted<12>(b, w); break;
+      default: load_shifted<14>(b, w); break;
+    }
   } else {
-    load8_slow(p, n, o);
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      w[q] = (2 * q < n ? uint32_t(p[2 * q]) : 0u) | (2 * q + 1 < n ? uint32_t(p[2 * q + 1]) << 16 : 0u);
   }
+#pragma unroll
+  for (int q = 0; q < 4; ++q) o[q] = bf16_pair(w[q]);
 }
 
-__device__ __forceinline__ void load_state8(const float* p, int n, float (&o)[8]) {
+__device__ __forceinline__ void load8(const float* p, Run r, int n, float2 (&o)[4]) {
+  uint32_t w[8];
+  if (r.mis == 0 && n >= 8) {
+    const uint4 a = __ldcs(reinterpret_cast<const uint4*>(p)), b = __ldcs(reinterpret_cast<const uint4*>(p) + 1);
+    w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
+    w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
+  } else if (r.inner) {
+    const uint8_t* b = reinterpret_cast<const uint8_t*>(p);
+    switch (r.mis) {
+      case 4: load_shifted<4>(b, w); break;
+      case 8: load_shifted<8>(b, w); break;
+      default: load_shifted<12>(b, w); break;
+    }
+  } else {
+#pragma unroll
+    for (int q = 0; q < 8; ++q) w[q] = q < n ? __float_as_uint(p[q]) : 0u;
+  }
+#pragma unroll
+  for (int q = 0; q < 4; ++q) o[q] = make_float2(__uint_as_float(w[2 * q]), __uint_as_float(w[2 * q + 1]));
+}
+
+__device__ __forceinline__ void load_state8(const float* p, float2 (&o)[4]) {
   const float4 a = __ldcs(reinterpret_cast<const float4*>(p));
   const float4 b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
-  o[0] = a.x; o[1] = a.y; o[2] = a.z; o[3] = a.w;
-  o[4] = b.x; o[5] = b.y; o[6] = b.z; o[7] = b.w;
-  if (n < 8) {
-#pragma unroll
-    for (int q = 0; q < 8; ++q)
-      if (q >= n) o[q] = 0.0f;  // state padding may hold anything
-  }
+  o[0] = make_float2(a.x, a.y);
+  o[1] = make_float2(a.z, a.w);
+  o[2] = make_float2(b.x, b.y);
+  o[3] = make_float2(b.z, b.w);
 }
 
-__device__ __forceinline__ void store_state8(float* p, const float (&o)[8]) {
-  __stcs(reinterpret_cast<float4*>(p), make_float4(o[0], o[1], o[2], o[3]));
-  __stcs(reinterpret_cast<float4*>(p) + 1, make_float4(o[4], o[5], o[6], o[7]));
-}
-
-__device__ __forceinline__ void store_bf16x8(uint16_t* p, int n, const float (&o)[8]) {
-  uint32_t w[4];
+// Zeros in the place of elements n, n + 1, ...: state padding may hold anything.
+__device__ __forceinline__ void clear_beyond(int n, float2 (&o)[4]) {
+  if (n >= 8) return;
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(o[2 * q], o[2 * q + 1]);
-    w[q] = *reinterpret_cast<const uint32_t*>(&h);
+    if (2 * q >= n) o[q].x = 0.0f;
+    if (2 * q + 1 >= n) o[q].y = 0.0f;
   }
-  if (n >= 8 && (reinterpret_cast<uintptr_t>(p) & 15u) == 0) {
+}
+
+__device__ __forceinline__ void store_state8(float* p, const float2 (&o)[4]) {
+  __stcs(reinterpret_cast<float4*>(p), make_float4(o[0].x, o[0].y, o[1].x, o[1].y));
+  __stcs(reinterpret_cast<float4*>(p) + 1, make_float4(o[2].x, o[2].y, o[3].x, o[3].y));
+}
+
+// The lane's elements [0, n) to p as bf16; whole warp.
+__device__ __forceinline__ void store_bf16x8(uint16_t* p, Run r, int n, const float2 (&o)[4]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) w[q] = to_bf16_pair(o[q]);
+  if (r.mis == 0 && n >= 8) {
     __stcs(reinterpret_cast<uint4*>(p), make_uint4(w[0], w[1], w[2], w[3]));
+  } else if (r.inner) {
+    uint8_t* b = reinterpret_cast<uint8_t*>(p);
+    switch (r.mis) {
+      case 2: store_shifted<2>(b, w); break;
+      case 4: store_shifted<4>(b, w); break;
+      case 6: store_shifted<6>(b, w); break;
+      case 8: store_shifted<8>(b, w); break;
+      case 10: store_shifted<10>(b, w); break;
+      case 12: store_shifted<12>(b, w); break;
+      default: store_shifted<14>(b, w); break;
+    }
   } else {
 #pragma unroll
     for (int q = 0; q < 8; ++q)
@@ -127,73 +245,39 @@ __device__ __forceinline__ void store_bf16x8(uint16_t* p, int n, const float (&o
 }
 
 // ------------------------------------------------------------------- norm
-// A sum held as the unevaluated pair hi + lo of floats (Knuth's TwoSum keeps
-// each addition's rounding error), about 48 bits: S is then as exact as a sum
-// in fp64, whose additions would take several times the time of the loads.
-struct Pair {
-  float hi, lo;
+// Sums held as unevaluated pairs hi + lo of floats (Knuth's TwoSum keeps each
+// addition's rounding error), about 48 bits, two elements at a time: S is
+// then as exact as a sum in fp64, whose additions would take several times
+// the time of the loads.
+struct Sums {
+  float2 hi, lo;
 };
 
-__device__ __forceinline__ void pair_add(Pair& a, float x, float x_lo) {
-  const float t = __fadd_rn(a.hi, x);
-  const float z = __fsub_rn(t, a.hi);
-  const float err = __fadd_rn(__fsub_rn(a.hi, __fsub_rn(t, z)), __fsub_rn(x, z));
-  a.lo = __fadd_rn(__fadd_rn(a.lo, x_lo), err);
+__device__ __forceinline__ float2 sub2(float2 a, float2 b) { return fma2(b, both(-1.0f), a); }
+
+__device__ __forceinline__ void two_sum(Sums& a, float2 x) {
+  const float2 t = add2(a.hi, x), z = sub2(t, a.hi);
+  a.lo = add2(a.lo, add2(sub2(a.hi, sub2(t, z)), sub2(x, z)));
   a.hi = t;
 }
 
-// Sum over 2 * `from` neighbouring lanes; both sides of each exchange compute the same pair.
-__device__ __forceinline__ void pair_reduce(Pair& a, int from) {
-  for (int o = from; o > 0; o >>= 1) {
-    const float h = __shfl_xor_sync(0xffffffffu, a.hi, o), l = __shfl_xor_sync(0xffffffffu, a.lo, o);
-    pair_add(a, h, l);
-  }
+// x * x: exact for bf16 numbers; for fp32 ones its rounding error goes to lo.
+__device__ __forceinline__ void add_square(Sums& a, float2 x, float minus_zero, uint16_t) { two_sum(a, mul2_rounded(x, x, minus_zero)); }
+__device__ __forceinline__ void add_square(Sums& a, float2 x, float minus_zero, float) {
+  const float2 sq = mul2_rounded(x, x, minus_zero);
+  two_sum(a, sq);
+  a.lo = add2(a.lo, fma2(x, x, make_float2(-sq.x, -sq.y)));
 }
 
-// The square's own rounding error; a bf16 number's square is exact.
-__device__ __forceinline__ float square_err(float x, float sq, float) { return __fmaf_rn(x, x, -sq); }
-__device__ __forceinline__ float square_err(float, float, uint16_t) { return 0.0f; }
-
-// partials[tile] = sum of squares of the tile, in a fixed order.
-template <typename G>
-__global__ void __launch_bounds__(LIST_THREADS) list_norm_kernel(const ListTile* __restrict__ tiles, int64_t n_tiles,
-                                                                 const G* const* __restrict__ grads, int32_t n_tensors,
-                                                                 double* __restrict__ partials, int* __restrict__ flags) {
-  __shared__ Pair red[LIST_THREADS / 32];
-  const int64_t tile = blockIdx.x;
-  const ListTile t = load_tile(tiles + tile);
-  pdl_wait();
-  pdl_trigger();
-  const bool ok = GRS_CHECK(tile < n_tiles && t.tensor >= 0 && t.tensor < n_tensors && t.n >= 0 && t.n <= LIST_T,
-                            flags, SITE_LIST_NORM);
-  const G* g = ok ? grads[t.tensor] : nullptr;
-  const int at = threadIdx.x * 8;
-  Pair s = {0.0f, 0.0f};
-  if (g != nullptr && at < t.n) {
-    float x[8];
-    load8(g + t.e0 + at, t.n - at, x);
-#pragma unroll
-    for (int q = 0; q < 8; ++q) {
-      const float sq = __fmul_rn(x[q], x[q]);
-      pair_add(s, sq, square_err(x[q], sq, G()));
-    }
-  }
-  pair_reduce(s, 16);
-  const int lane = threadIdx.x & 31;
-  if (lane == 0) red[threadIdx.x >> 5] = s;
-  __syncthreads();
-  if (threadIdx.x >= 32) return;
-  s = red[lane & (LIST_THREADS / 32 - 1)];
-  pair_reduce(s, LIST_THREADS / 64);
-  // An infinite or NaN sum has no error term (inf - inf is NaN).
-  if (lane == 0) partials[tile] = isfinite(s.hi) ? static_cast<double>(s.hi) + static_cast<double>(s.lo) : static_cast<double>(s.hi);
+// An infinite or NaN sum has no error term (inf - inf is NaN).
+__device__ __forceinline__ double sum_value(float hi, float lo) {
+  return isfinite(hi) ? static_cast<double>(hi) + static_cast<double>(lo) : static_cast<double>(hi);
 }
 
-// *out = inv_m2 * the sum of the partials in fp64: block b of NORM_L2_BLOCKS
-// sums a contiguous range, the block that is last (the ticket) the blocks'
-// sums, every addition in a fixed order.
+// Every sum over the block's warps in a fixed order, in fp64.
 __device__ __forceinline__ double block_sum(double x, double* red) {
   x = warp_sum(x);
+  __syncthreads();  // red may still be read from the sum before
   if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = x;
   __syncthreads();
   double s = red[0];
@@ -201,40 +285,123 @@ __device__ __forceinline__ double block_sum(double x, double* red) {
   return s;
 }
 
-__global__ void __launch_bounds__(LIST_THREADS) list_norm_finish_kernel(const double* __restrict__ partials, int64_t n,
-                                                                        double* __restrict__ level2,
-                                                                        unsigned int* __restrict__ ticket, double inv_m2,
-                                                                        double* __restrict__ out, int* __restrict__ flags) {
+// A warp takes the tiles w, w + (all warps), ..., each as the 16-byte chunks
+// that it starts in (a tensor that starts off a 16-byte boundary has its
+// tiles' ends moved back to one; the order of a sum is free), half a tile's
+// loads in flight at once and the next tile's record already there.  A lane
+// keeps its sums in fp32 pairs over a tile and in fp64 over its tiles.  Each
+// block leaves one fp64 sum, and the block that is last (the ticket) adds
+// those up.  The grid is the same everywhere (or goes by the number of
+// tiles), so every addition has its fixed place.
+constexpr int LIST_NORM_BLOCKS = 608;  // four blocks an SM
+
+// The chunk of 16 bytes at p: all of it, or its elements [lo, hi).
+__device__ __forceinline__ uint4 load_chunk(const uint16_t* p, int lo, int hi) {
+  if (lo <= 0 && hi >= 8) return __ldcs(reinterpret_cast<const uint4*>(p));
+  uint32_t w[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q)
+    w[q] = (2 * q >= lo && 2 * q < hi ? uint32_t(p[2 * q]) : 0u) | (2 * q + 1 >= lo && 2 * q + 1 < hi ? uint32_t(p[2 * q + 1]) << 16 : 0u);
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ uint4 load_chunk(const float* p, int lo, int hi) {
+  if (lo <= 0 && hi >= 4) return __ldcs(reinterpret_cast<const uint4*>(p));
+  uint32_t w[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) w[q] = q >= lo && q < hi ? __float_as_uint(p[q]) : 0u;
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+__device__ __forceinline__ void add_chunk(Sums& s, uint4 v, float minus_zero, uint16_t tag) {
+  add_square(s, bf16_pair(v.x), minus_zero, tag);
+  add_square(s, bf16_pair(v.y), minus_zero, tag);
+  add_square(s, bf16_pair(v.z), minus_zero, tag);
+  add_square(s, bf16_pair(v.w), minus_zero, tag);
+}
+__device__ __forceinline__ void add_chunk(Sums& s, uint4 v, float minus_zero, float tag) {
+  add_square(s, make_float2(__uint_as_float(v.x), __uint_as_float(v.y)), minus_zero, tag);
+  add_square(s, make_float2(__uint_as_float(v.z), __uint_as_float(v.w)), minus_zero, tag);
+}
+
+template <typename G>
+__global__ void __launch_bounds__(LIST_THREADS, 4) list_norm_kernel(const ListTile* __restrict__ tiles, int64_t n_tiles,
+                                                                    const G* const* __restrict__ grads, int32_t n_tensors,
+                                                                    double* __restrict__ partials,
+                                                                    unsigned int* __restrict__ ticket, double inv_m2,
+                                                                    float minus_zero, double* __restrict__ out,
+                                                                    int* __restrict__ flags) {
   __shared__ double red[LIST_THREADS / 32];
   __shared__ bool last;
-  pdl_wait();
+  constexpr int EL = 16 / sizeof(G), CHUNKS = static_cast<int>(LIST_T) / EL / 32, BATCH = 8;
+  const int lane = threadIdx.x & 31;
+  const int64_t warps = int64_t(gridDim.x) * (LIST_THREADS / 32);
+  double total = 0.0;
+  int64_t tile = int64_t(blockIdx.x) * (LIST_THREADS / 32) + (threadIdx.x >> 5);
+  ListTile t{};
+  if (tile < n_tiles) t = load_tile(tiles + tile);
+  pdl_wait();  // the table above is the list's own and does not change
   pdl_trigger();
-  const int64_t chunk = (n + NORM_L2_BLOCKS - 1) / NORM_L2_BLOCKS;
-  const int64_t lo = blockIdx.x * chunk, hi = lo + chunk < n ? lo + chunk : n;
-  double s = 0.0;
-  for (int64_t i = lo + threadIdx.x; i < hi; i += LIST_THREADS) s = __dadd_rn(s, partials[i]);
-  s = block_sum(s, red);
+  const auto gradient = [&](int64_t at) -> const G* {
+    if (at >= n_tiles || !GRS_CHECK(t.tensor >= 0 && t.tensor < n_tensors && t.n > 0 && t.n <= LIST_T, flags, SITE_LIST_NORM))
+      return nullptr;
+    return grads[t.tensor];
+  };
+  const G* g = gradient(tile);
+  while (tile < n_tiles) {
+    const ListTile now = t;
+    const G* p = g;
+    tile += warps;
+    if (tile < n_tiles) t = load_tile(tiles + tile);
+    g = gradient(tile);
+    if (p == nullptr) continue;
+    p += now.e0;
+    const int mis = static_cast<int>(reinterpret_cast<uintptr_t>(p) & 15) / static_cast<int>(sizeof(G));
+    // Elements of the tensor from the tile's first chunk on, as far as one
+    // tile and chunk reach; its own first is `head`, 0 inside the tensor.
+    const int head = now.e0 > 0 ? 0 : mis;
+    const int64_t rest = now.rest + mis;
+    const int end = rest < 2 * LIST_T ? static_cast<int>(rest) : static_cast<int>(2 * LIST_T);
+    p -= mis;
+    Sums s = {both(0.0f), both(0.0f)};
+#pragma unroll
+    for (int half = 0; half < CHUNKS; half += BATCH) {
+      if (half * 32 * EL >= end) break;
+      uint4 x[BATCH];
+#pragma unroll
+      for (int r = 0; r < BATCH; ++r) {
+        const int c = ((half + r) * 32 + lane) * EL;
+        x[r] = c < end ? load_chunk(p + c, head - c, end - c) : make_uint4(0, 0, 0, 0);
+      }
+#pragma unroll
+      for (int r = 0; r < BATCH; ++r) add_chunk(s, x[r], minus_zero, G());
+    }
+    // A last tile may have a few elements left after its last whole chunk.
+    if (lane == 0 && now.rest <= LIST_T && end > LIST_T) add_chunk(s, load_chunk(p + LIST_T, 0, end - static_cast<int>(LIST_T)), minus_zero, G());
+    total = __dadd_rn(total, __dadd_rn(sum_value(s.hi.x, s.lo.x), sum_value(s.hi.y, s.lo.y)));
+  }
+  total = block_sum(total, red);
   if (threadIdx.x == 0) {
-    level2[blockIdx.x] = s;
+    partials[blockIdx.x] = total;
     __threadfence();
-    last = atomicAdd(ticket, 1u) == NORM_L2_BLOCKS - 1;
+    last = atomicAdd(ticket, 1u) == gridDim.x - 1;
   }
   __syncthreads();
   if (!last) return;
   __threadfence();
-  s = block_sum(threadIdx.x < NORM_L2_BLOCKS ? __ldcg(level2 + threadIdx.x) : 0.0, red);
+  total = 0.0;
+  for (int i = threadIdx.x; i < static_cast<int>(gridDim.x); i += LIST_THREADS) total = __dadd_rn(total, __ldcg(partials + i));
+  total = block_sum(total, red);
   if (threadIdx.x == 0) {
-    s = __dmul_rn(s, inv_m2);
-    *out = s;
-    if (!isfinite(s)) atomicOr(flags + FLAG_NONFINITE, 1);
+    total = __dmul_rn(total, inv_m2);
+    *out = total;
+    if (!isfinite(total)) atomicOr(flags + FLAG_NONFINITE, 1);
     *ticket = 0u;
   }
 }
 
-// Workspace of the norm: [n_tiles doubles][NORM_L2_BLOCKS doubles][ticket].
-int64_t list_ws_level2(int64_t n_tiles) { return (n_tiles * 8 + 255) / 256 * 256; }
-int64_t list_ws_ticket(int64_t n_tiles) { return list_ws_level2(n_tiles) + NORM_L2_BLOCKS * 8; }
-int64_t list_ws_bytes(int64_t n_tiles) { return list_ws_ticket(n_tiles) + 256; }
+// Workspace of the norm: [LIST_NORM_BLOCKS doubles][ticket].
+constexpr int64_t LIST_WS_TICKET = LIST_NORM_BLOCKS * 8;
+constexpr int64_t LIST_WS_BYTES = LIST_WS_TICKET + 256;
 
 // ---------------------------------------------------------- 8-bit format
 // Counter-based random bits: an integer hash of the element's index under
@@ -275,48 +442,98 @@ __device__ __forceinline__ uint32_t random_bits(uint32_t lo, uint32_t k0, uint32
 // that a largest magnitude that was rounded up to a power of two keeps its
 // scale when it is packed again.
 struct Scale {
-  float scale, inv;
-  bool bad;
+  float scale;
+  float to_code;  // 1 / scale * 2^-120, if that is a normal number
+  float inv;      // 1 / scale
+  bool bad;       // not finite
+  bool plain;     // to_code holds
 };
 __device__ __forceinline__ Scale block_scale(uint32_t top) {
   Scale s;
   s.bad = top >= 0x7f800000u;
   int e = static_cast<int>((top + 0x7fffffu) >> 23) - 8;
   e = e < 1 ? 1 : e;
-  s.inv = __uint_as_float(static_cast<uint32_t>(254 - e) << 23);
+  s.plain = e <= 133;
   s.scale = s.bad ? __uint_as_float(0x7fc00000u) : __uint_as_float(static_cast<uint32_t>(e) << 23);
-  if (s.bad) s.inv = 0.0f;
+  s.inv = __uint_as_float(static_cast<uint32_t>(254 - e) << 23);
+  s.to_code = __uint_as_float(static_cast<uint32_t>(134 - e) << 23);
   return s;
+}
+
+// Largest of three, NaN if one is NaN (fmaxf would drop it).
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
 }
 
 // Largest magnitude of the warp's 256 values, as bits (ordered like the
 // values, NaN above infinity).
-__device__ __forceinline__ uint32_t warp_absmax(const float (&x)[8]) {
-  uint32_t top = 0;
+__device__ __forceinline__ uint32_t warp_absmax(const float2 (&x)[4]) {
+  float top = 0.0f;
 #pragma unroll
-  for (int q = 0; q < 8; ++q) top = max(top, __float_as_uint(x[q]) & 0x7fffffffu);
-  return __reduce_max_sync(0xffffffffu, top);
+  for (int q = 0; q < 4; ++q) top = max_nan(max_nan(top, fabsf(x[q].x)), fabsf(x[q].y));
+  return __reduce_max_sync(0xffffffffu, __float_as_uint(top));
 }
 
-// E4M3 code of x / scale.  Times 2^-120 an E4M3 number (bias 7) has its own
-// exponent and subnormals as binary32 (bias 127), so the code is the top of
-// the binary32 pattern, and adding to the 20 bits below it before they are
-// cut off rounds: a random number below 2^20 stochastically, the usual
-// half-minus-one plus the last bit kept to nearest even.
-__device__ __forceinline__ uint32_t code_bits(float x, float inv) {
-  return __float_as_uint(__fmul_rn(__fmul_rn(fabsf(x), inv), 0x1p-120f));
-}
-__device__ __forceinline__ uint32_t sign_bit(float x) { return (__float_as_uint(x) >> 24) & 0x80u; }
-
-// The value of a code (in the low byte of `code`) in units of 1.
-__device__ __forceinline__ float code_value(uint32_t code) {
-  const float y = __uint_as_float((code & 0x7fu) << 20) * 0x1p120f;
-  return __uint_as_float(__float_as_uint(y) | (code & 0x80u) << 24);
-}
-
-__device__ __forceinline__ void decode8(uint2 w, float scale, float (&o)[8]) {
+// Times 2^-120 an E4M3 number (bias 7) has its own exponent and subnormals
+// as binary32 (bias 127), so the code of x / scale is the top of that
+// binary32 pattern, and adding to the 20 bits below it before they are cut
+// off rounds: a random number below 2^20 stochastically, the usual
+// half-minus-one plus the last bit kept to nearest even.  The pattern is below
+// 2^27 (no code is above 0x78), the sign stays in bit 31.
+__device__ __forceinline__ void code_patterns(const float2 (&x)[4], const Scale& s, uint32_t (&t)[8]) {
 #pragma unroll
-  for (int q = 0; q < 8; ++q) o[q] = __fmul_rn(code_value((q < 4 ? w.x : w.y) >> (8 * (q & 3))), scale);
+  for (int q = 0; q < 4; ++q) {
+    // The scale is a power of two: one product gives the same number where
+    // its factor is normal (magnitudes up to 2^14).
+    const float2 y = s.plain ? mul2(x[q], both(s.to_code)) : mul2(mul2(x[q], both(s.inv)), both(0x1p-120f));
+    t[2 * q] = __float_as_uint(y.x);
+    t[2 * q + 1] = __float_as_uint(y.y);
+  }
+}
+
+// Bytes of sign and code from the rounded patterns; zeros for a bad block.
+__device__ __forceinline__ uint2 code_bytes(const uint32_t (&t)[8], bool bad) {
+  uint32_t w[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint32_t u[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) u[q] = (t[4 * h + q] << 4) | (t[4 * h + q] & 0x80000000u);  // the code in the top byte
+    w[h] = bad ? 0u : __byte_perm(__byte_perm(u[0], u[1], 0x0073), __byte_perm(u[2], u[3], 0x0073), 0x5410);
+  }
+  return make_uint2(w[0], w[1]);
+}
+
+// A positive sqrt(v) never becomes zero.  (sqrt of a positive fp32 number is
+// normal, so its bits are above 2^20.)
+__device__ __forceinline__ void keep_positive(const float2 (&s)[4], uint32_t (&t)[8]) {
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    t[2 * q] = max(t[2 * q], min(__float_as_uint(s[q].x), 1u << 20));
+    t[2 * q + 1] = max(t[2 * q + 1], min(__float_as_uint(s[q].y), 1u << 20));
+  }
+}
+
+__device__ __forceinline__ void to_nearest(uint32_t (&t)[8]) {
+#pragma unroll
+  for (int q = 0; q < 8; ++q) t[q] += 0x7ffffu + (t[q] >> 20 & 1u);
+}
+
+// The numbers of 8 codes times the block's scale.
+__device__ __forceinline__ void decode8(uint2 w, float scale, float2 (&o)[4]) {
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const uint32_t two = (q & 2 ? w.y : w.x) >> (q & 1 ? 16 : 0);
+    uint32_t h;
+    asm("{\n\t.reg .b16 c;\n\tcvt.u16.u32 c, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, c;\n\t}" : "=r"(h) : "r"(two));
+    float lo, hi;
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}"
+        : "=f"(lo), "=f"(hi)
+        : "r"(h));
+    o[q] = mul2(make_float2(lo, hi), both(scale));
+  }
 }
 
 // ------------------------------------------------------------------- step
@@ -334,23 +551,28 @@ struct ListArgs {
   int32_t n_tensors;
   AdamwK k;
   float step_size, inv_bc2_sqrt, max_norm, inv_m;
+  float minus_zero;  // -0, unknown to the compiler (mul2_rounded)
   Keys keys;
 };
 
-// AdamW on one element with every product and sum rounded by itself;
-// returns sqrt(v).
-__device__ __forceinline__ float adamw_elem_sep(float g, float step_size, float inv_bc2_sqrt, const AdamwK& k,
-                                                float& P, float& M, float V) {
-  M = __fadd_rn(__fmul_rn(M, k.b1), __fmul_rn(g, k.omb1));
-  V = __fadd_rn(__fmul_rn(V, k.b2), __fmul_rn(__fmul_rn(g, k.omb2), g));
-  const float s = __fsqrt_rn(V);
-  const float upd = __fdiv_rn(M, __fadd_rn(__fmul_rn(s, inv_bc2_sqrt), k.eps));
-  P = __fsub_rn(__fmul_rn(P, k.decay), __fmul_rn(upd, step_size));
-  return s;
+// AdamW on two elements.  What the next state comes from (m, v, sqrt(v)) is
+// rounded product by product and sum by sum; the parameter's own step, which
+// no state depends on, takes fused products and the fast quotient (2 units in
+// the last place of the step, about 2^-22 of lr).  V comes in as v and leaves
+// as sqrt(v).
+__device__ __forceinline__ void adamw_pair_sep(float2 g, const ListArgs& a, float2& P, float2& M, float2& V) {
+  const AdamwK& k = a.k;
+  const float z = a.minus_zero;
+  M = add2(mul2_rounded(M, both(k.b1), z), mul2_rounded(g, both(k.omb1), z));
+  V = add2(mul2_rounded(V, both(k.b2), z), mul2_rounded(mul2(g, both(k.omb2)), g, z));
+  V = make_float2(__fsqrt_rn(V.x), __fsqrt_rn(V.y));
+  const float2 d = fma2(V, both(a.inv_bc2_sqrt), both(k.eps));
+  const float2 u = make_float2(__fdividef(M.x, d.x), __fdividef(M.y, d.y));
+  P = fma2(u, both(-a.step_size), mul2(P, both(k.decay)));
 }
 
 template <typename G, bool k8>
-__global__ void __launch_bounds__(LIST_THREADS) list_step_kernel(const __grid_constant__ ListArgs a) {
+__global__ void __launch_bounds__(LIST_THREADS, 5) list_step_kernel(const __grid_constant__ ListArgs a) {
   const int64_t tile = blockIdx.x;
   const ListTile t = load_tile(a.tiles + tile);
   pdl_wait();
@@ -359,61 +581,76 @@ __global__ void __launch_bounds__(LIST_THREADS) list_step_kernel(const __grid_co
                      t.state0 >= 0 && t.state0 + (t.n + 255) / 256 * 256 <= a.n_state,
                  a.flags, SITE_LIST_STEP))
     return;
+  const int at = threadIdx.x * 8, first = at & ~255;  // the warp's first element
+  if (first >= t.n) return;                           // whole warps beyond the tensor's last block
+  const int n = t.n - at;                             // elements of this thread's 8 (may be <= 0 or > 8)
   const G* g = static_cast<const G*>(a.grads[t.tensor]);
-  if (g == nullptr) return;
-  const int at = threadIdx.x * 8;
-  if ((at & ~255) >= t.n) return;  // whole warps beyond the tensor's last block
-  const int n = t.n - at;          // elements of this thread's 8 (may be <= 0 or > 8)
   uint16_t* p16 = a.params != nullptr ? a.params[t.tensor] : nullptr;
-  const float gscale = a.max_norm > 0.0f ? clip_gscale(*a.norm_sq, a.max_norm, a.inv_m) : a.inv_m;
   const int64_t i = t.state0 + at;
-  float G8[8], P[8], M[8], V[8];
-  load8(g + t.e0 + at, n, G8);
-  load_state8(a.master + i, n, P);
-  if (k8) {
-    const uint2 mw = __ldcs(reinterpret_cast<const uint2*>(a.m8 + i));
-    const uint2 sw = __ldcs(reinterpret_cast<const uint2*>(a.s8 + i));
-    decode8(mw, a.m_scale[i >> 8], M);
-    decode8(sw, a.s_scale[i >> 8], V);
+  // The state's loads do not wait for the gradient's pointer.
+  float2 P[4], M[4], V[4];
+  uint2 mw, sw;
+  float m_scale, s_scale;
+  load_state8(a.master + i, P);
+  if constexpr (k8) {
+    mw = __ldcs(reinterpret_cast<const uint2*>(a.m8 + i));
+    sw = __ldcs(reinterpret_cast<const uint2*>(a.s8 + i));
+    m_scale = a.m_scale[i >> 8];
+    s_scale = a.s_scale[i >> 8];
+  } else {
+    load_state8(a.m + i, M);
+    load_state8(a.v + i, V);
+  }
+  if (g == nullptr) return;
+  float2 G2[4];
+  g += t.e0 + at;
+  load8(g, run_of(g, t.e0 + first, t.rest - first), n, G2);
+  const float gscale = a.max_norm > 0.0f ? clip_gscale(*a.norm_sq, a.max_norm, a.inv_m) : a.inv_m;
+  if constexpr (k8) {
+    decode8(mw, m_scale, M);
+    decode8(sw, s_scale, V);
 #pragma unroll
-    for (int q = 0; q < 8; ++q) {
-      V[q] = __fmul_rn(V[q], V[q]);
-      V[q] = adamw_elem_sep(__fmul_rn(G8[q], gscale), a.step_size, a.inv_bc2_sqrt, a.k, P[q], M[q], V[q]);
-      if (q >= n) P[q] = M[q] = V[q] = 0.0f;
+    for (int q = 0; q < 4; ++q) {
+      V[q] = mul2(V[q], V[q]);
+      adamw_pair_sep(mul2(G2[q], both(gscale)), a, P[q], M[q], V[q]);
     }
+    clear_beyond(n, M);
+    clear_beyond(n, V);
     const Scale ms = block_scale(warp_absmax(M)), ss = block_scale(warp_absmax(V));
     const uint32_t k0 = a.keys.k0 ^ static_cast<uint32_t>(i >> 32) * MIX_B;
-    uint32_t mo[2] = {0, 0}, so[2] = {0, 0};
+    uint32_t mt[8], st[8];
+    code_patterns(M, ms, mt);
+    code_patterns(V, ss, st);
 #pragma unroll
     for (int q = 0; q < 8; ++q) {
       const uint32_t r = random_bits(static_cast<uint32_t>(i) + q, k0, a.keys.k1);
-      uint32_t mc = (code_bits(M[q], ms.inv) + ((r & 0xffffu) << 4 | 8u)) >> 20 | sign_bit(M[q]);
-      uint32_t sc = (code_bits(V[q], ss.inv) + ((r >> 16) << 4 | 8u)) >> 20;
-      if (V[q] > 0.0f && sc == 0) sc = 1;
-      if (ms.bad) mc = 0;
-      if (ss.bad) sc = 0;
-      mo[q >> 2] |= mc << (8 * (q & 3));
-      so[q >> 2] |= sc << (8 * (q & 3));
+      mt[q] += (r << 4 & 0xffff0u) | 8u;
+      st[q] += (r >> 12 & 0xffff0u) | 8u;
     }
-    __stcs(reinterpret_cast<uint2*>(a.m8 + i), make_uint2(mo[0], mo[1]));
-    __stcs(reinterpret_cast<uint2*>(a.s8 + i), make_uint2(so[0], so[1]));
+    keep_positive(V, st);
+    __stcs(reinterpret_cast<uint2*>(a.m8 + i), code_bytes(mt, ms.bad));
+    __stcs(reinterpret_cast<uint2*>(a.s8 + i), code_bytes(st, ss.bad));
     if ((threadIdx.x & 31) == 0) {
       a.m_scale[i >> 8] = ms.scale;
       a.s_scale[i >> 8] = ss.scale;
     }
   } else {
-    load_state8(a.m + i, n, M);
-    load_state8(a.v + i, n, V);
 #pragma unroll
-    for (int q = 0; q < 8; ++q) {
-      adamw_elem(G8[q], gscale, a.step_size, a.inv_bc2_sqrt, a.k, P[q], M[q], V[q]);
-      if (q >= n) P[q] = M[q] = V[q] = 0.0f;
+    for (int q = 0; q < 4; ++q) {
+      adamw_elem(G2[q].x, gscale, a.step_size, a.inv_bc2_sqrt, a.k, P[q].x, M[q].x, V[q].x);
+      adamw_elem(G2[q].y, gscale, a.step_size, a.inv_bc2_sqrt, a.k, P[q].y, M[q].y, V[q].y);
     }
+    clear_beyond(n, M);
+    clear_beyond(n, V);
     store_state8(a.m + i, M);
     store_state8(a.v + i, V);
   }
+  clear_beyond(n, P);
   store_state8(a.master + i, P);
-  if (p16 != nullptr && n > 0) store_bf16x8(p16 + t.e0 + at, n, P);
+  if (p16 != nullptr) {
+    p16 += t.e0 + at;
+    store_bf16x8(p16, run_of(p16, t.e0 + first, t.rest - first), n, P);
+  }
 }
 
 // ---------------------------------------------------------- pack / unpack
@@ -447,26 +684,22 @@ __global__ void __launch_bounds__(LIST_THREADS) list_pack8_kernel(const __grid_c
   int n;
   const int64_t i = convert_at(a, &n);
   if (i < 0) return;
-  float M[8], V[8];
-  load_state8(a.m + i, n, M);
-  load_state8(a.v + i, n, V);
+  float2 M[4], V[4];
+  load_state8(a.m + i, M);
+  load_state8(a.v + i, V);
 #pragma unroll
-  for (int q = 0; q < 8; ++q) V[q] = __fsqrt_rn(V[q]);
+  for (int q = 0; q < 4; ++q) V[q] = add2(make_float2(__fsqrt_rn(V[q].x), __fsqrt_rn(V[q].y)), both(0.0f));  // -0 to 0
+  clear_beyond(n, M);
+  clear_beyond(n, V);
   const Scale ms = block_scale(warp_absmax(M)), ss = block_scale(warp_absmax(V));
-  uint32_t mo[2] = {0, 0}, so[2] = {0, 0};
-#pragma unroll
-  for (int q = 0; q < 8; ++q) {
-    const uint32_t mb = code_bits(M[q], ms.inv), sb = code_bits(V[q], ss.inv);
-    uint32_t mc = (mb + 0x7ffffu + (mb >> 20 & 1u)) >> 20 | sign_bit(M[q]);
-    uint32_t sc = (sb + 0x7ffffu + (sb >> 20 & 1u)) >> 20;
-    if (V[q] > 0.0f && sc == 0) sc = 1;
-    if (ms.bad) mc = 0;
-    if (ss.bad) sc = 0;
-    mo[q >> 2] |= mc << (8 * (q & 3));
-    so[q >> 2] |= sc << (8 * (q & 3));
-  }
-  __stcs(reinterpret_cast<uint2*>(a.m8 + i), make_uint2(mo[0], mo[1]));
-  __stcs(reinterpret_cast<uint2*>(a.s8 + i), make_uint2(so[0], so[1]));
+  uint32_t mt[8], st[8];
+  code_patterns(M, ms, mt);
+  code_patterns(V, ss, st);
+  to_nearest(mt);
+  to_nearest(st);
+  keep_positive(V, st);
+  __stcs(reinterpret_cast<uint2*>(a.m8 + i), code_bytes(mt, ms.bad));
+  __stcs(reinterpret_cast<uint2*>(a.s8 + i), code_bytes(st, ss.bad));
   if ((threadIdx.x & 31) == 0) {
     a.m_scale[i >> 8] = ms.scale;
     a.s_scale[i >> 8] = ss.scale;
@@ -479,14 +712,13 @@ __global__ void __launch_bounds__(LIST_THREADS) list_unpack8_kernel(const __grid
   int n;
   const int64_t i = convert_at(a, &n);
   if (i < 0) return;
-  float M[8], V[8];
+  float2 M[4], V[4];
   decode8(__ldcs(reinterpret_cast<const uint2*>(a.m8 + i)), a.m_scale[i >> 8], M);
   decode8(__ldcs(reinterpret_cast<const uint2*>(a.s8 + i)), a.s_scale[i >> 8], V);
 #pragma unroll
-  for (int q = 0; q < 8; ++q) {
-    V[q] = __fmul_rn(V[q], V[q]);
-    if (q >= n) M[q] = V[q] = 0.0f;
-  }
+  for (int q = 0; q < 4; ++q) V[q] = mul2(V[q], V[q]);
+  clear_beyond(n, M);
+  clear_beyond(n, V);
   store_state8(a.m + i, M);
   store_state8(a.v + i, V);
 }
@@ -572,7 +804,7 @@ grs_status grs_tensors_create(const int64_t* numels, int32_t n_tensors, uint32_t
       if ((flags & GRS_PLAN_HOST_ONLY) == 0)
         for (int64_t e0 = 0; e0 < numels[i]; e0 += LIST_T) {
           const int64_t rem = numels[i] - e0;
-          host.push_back(ListTile{l->n_state + e0, e0, i, static_cast<int32_t>(rem < LIST_T ? rem : LIST_T), 0});
+          host.push_back(ListTile{l->n_state + e0, e0, i, static_cast<int32_t>(rem < LIST_T ? rem : LIST_T), rem});
         }
       l->n_elements += numels[i];
       l->n_state += (numels[i] + GRS_STATE_BLOCK - 1) / GRS_STATE_BLOCK * GRS_STATE_BLOCK;
@@ -625,7 +857,7 @@ grs_status grs_tensors_query(const grs_tensors* l, grs_tensors_info* o) {
   o->n_elements = l->n_elements;
   o->n_state = l->n_state;
   o->n_blocks = l->n_state / GRS_STATE_BLOCK;
-  o->workspace_bytes = list_ws_bytes(l->n_tiles);
+  o->workspace_bytes = LIST_WS_BYTES;
   return GRS_OK;
 }
 
@@ -652,23 +884,20 @@ grs_status grs_tensors_norm_sq(const grs_tensors* l, const void* const* d_grads,
   if (!dev.ok()) return api_fail(GRS_ERR_CUDA, who, "cannot select the list's device");
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   double* partials = reinterpret_cast<double*>(ws);
-  double* level2 = reinterpret_cast<double*>(ws + list_ws_level2(l->n_tiles));
-  unsigned int* ticket = reinterpret_cast<unsigned int*>(ws + list_ws_ticket(l->n_tiles));
+  unsigned int* ticket = reinterpret_cast<unsigned int*>(ws + LIST_WS_TICKET);
   const int32_t nt = static_cast<int32_t>(l->numel.size());
-  cudaError_t e = cudaSuccess;
-  if (l->n_tiles > 0) {
-    const dim3 grid(static_cast<unsigned>(l->n_tiles)), block(LIST_THREADS);
-    const ListTile* tiles = l->d_tiles;
-    e = grad_dtype == GRS_DTYPE_FP32
-            ? launch_pdl(list_norm_kernel<float>, grid, block, 0, stream, tiles, l->n_tiles,
-                       reinterpret_cast<const float* const*>(d_grads), nt, partials, l->d_flags)
-            : launch_pdl(list_norm_kernel<uint16_t>, grid, block, 0, stream, tiles, l->n_tiles,
-                       reinterpret_cast<const uint16_t* const*>(d_grads), nt, partials, l->d_flags);
-  }
-  if (e != cudaSuccess) return api_cuda_fail(e, who);
+  const ListTile* tiles = l->d_tiles;
+  const int64_t need = (l->n_tiles + LIST_THREADS / 32 - 1) / (LIST_THREADS / 32);
+  const dim3 grid(static_cast<unsigned>(need < 1 ? 1 : need < LIST_NORM_BLOCKS ? need : LIST_NORM_BLOCKS)), block(LIST_THREADS);
   const double inv_m = 1.0 / static_cast<double>(n_micro);
-  e = launch_pdl(list_norm_finish_kernel, dim3(NORM_L2_BLOCKS), dim3(LIST_THREADS), 0, stream, partials, l->n_tiles, level2,
-               ticket, inv_m * inv_m, d_norm_sq, l->d_flags);
+  const cudaError_t e =
+      grad_dtype == GRS_DTYPE_FP32
+          ? launch_pdl(list_norm_kernel<float>, grid, block, 0, stream, tiles, l->n_tiles,
+                       reinterpret_cast<const float* const*>(d_grads), nt, partials, ticket, inv_m * inv_m, -0.0f, d_norm_sq,
+                       l->d_flags)
+          : launch_pdl(list_norm_kernel<uint16_t>, grid, block, 0, stream, tiles, l->n_tiles,
+                       reinterpret_cast<const uint16_t* const*>(d_grads), nt, partials, ticket, inv_m * inv_m, -0.0f, d_norm_sq,
+                       l->d_flags);
   return e == cudaSuccess ? GRS_OK : api_cuda_fail(e, who);
 }
 
@@ -703,6 +932,7 @@ grs_status grs_tensors_adamw8_step(const grs_tensors* l, const grs_adamw* hp, ui
   a.m_scale = m_scale;
   a.s_scale = s_scale;
   a.keys = make_keys(seed);
+  a.minus_zero = -0.0f;
   return launch_list_step<true>(l, a, grad_dtype, stream, who);
 }
 

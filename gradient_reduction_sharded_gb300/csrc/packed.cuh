@@ -1,6 +1,5 @@
 // Two fp32 numbers in one instruction: sm_103a adds, multiplies and fuses
-// pairs of neighbouring registers (add/mul/fma.rn.f32x2), each half rounded
-// as the scalar instruction rounds it.  The streaming kernels that are bound
+// pairs of neighbouring registers (add/mul/fma.rn.f32x2).  The streaming kernels that are bound
 // by instruction issue, not by memory, work on pairs.
 #pragma once
 
@@ -39,6 +38,13 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
 }
 
 __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+
+// The product rounded by itself, whatever is added to it.  The assembler
+// fuses mul.rn.f32x2 and an addition of its result into one rounding (which
+// it does not do with the scalar mul.rn.f32), also where the product is
+// written as a fused one with a -0 that it knows; with a -0 that comes in at
+// run time the product stays, and has a product's value and sign.
+__device__ __forceinline__ float2 mul2_rounded(float2 a, float2 b, float minus_zero) { return fma2(a, b, both(minus_zero)); }
 
 // bf16 pair in one word <-> two floats.
 __device__ __forceinline__ float2 bf16_pair(uint32_t w) {

@@ -639,8 +639,8 @@ grs_status grs_tensors_query(const grs_tensors* list, grs_tensors_info* out);
 grs_status grs_tensors_offset(const grs_tensors* list, int32_t tensor, int64_t* out);
 
 /* S = sum over every tensor with a gradient of (g / n_micro)^2 to *d_norm_sq
- * (device double), deterministic: fixed tiles of 2048 elements, each summed
- * as an unevaluated pair of floats (48 bits), then fp64 in a fixed order.  A non-finite S raises the flag that
+ * (device double), deterministic: fixed tiles of 2048 elements, summed as
+ * unevaluated pairs of floats (48 bits), then fp64 in a fixed order.  A non-finite S raises the flag that
  * grs_tensors_check_device_errors reports.  workspace: device, 16-byte
  * aligned, workspace_bytes, zeroed once before its first use; calls that
  * share one must not overlap.  Errors: INVALID_ARG, ALIGNMENT, NO_DEVICE,

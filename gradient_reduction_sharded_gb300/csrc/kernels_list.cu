@@ -20,6 +20,7 @@
 #include "internal.h"
 #include "launch.cuh"
 #include "packed.cuh"
+#include "shifted.cuh"
 
 namespace grs {
 namespace {
@@ -64,137 +65,6 @@ __device__ __forceinline__ ListTile load_tile(const ListTile* p) {
   return t;
 }
 
-// A warp's 256 consecutive elements of a tensor that starts at any multiple
-// of its element: 8 to a lane.
-//
-// Aligned runs go as 16-byte chunks.  For the others every lane moves the
-// aligned chunk (or two, in fp32) that holds its first element, and the
-// elements that lie in the next lane's chunk cross by a shuffle: K words and
-// perhaps half a word.  Only the run's two ends go by element, or all of a
-// run that the tensor's own ends cut short (`inner` false): a chunk that
-// reaches outside the tensor is not touched.
-struct Run {
-  int mis;     // bytes that the run starts after a 16-byte boundary
-  bool inner;  // 8 elements of the tensor before the run and 8 after it
-};
-
-template <typename G>
-__device__ __forceinline__ Run run_of(const G* p, int64_t before, int64_t rest) {
-  return {static_cast<int>(reinterpret_cast<uintptr_t>(p) & 15), before >= 8 && rest >= 264};
-}
-
-// The N words that start BYTES (even, below 16) after the first of (own, next).
-template <int BYTES, int N>
-__device__ __forceinline__ void shift_words(const uint32_t (&own)[N], const uint32_t (&next)[4], uint32_t (&o)[N]) {
-  constexpr int K = BYTES / 4;
-  uint32_t w[N + 4];
-#pragma unroll
-  for (int i = 0; i < N; ++i) w[i] = own[i];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) w[N + i] = next[i];
-#pragma unroll
-  for (int i = 0; i < N; ++i) o[i] = (BYTES & 2) != 0 ? __funnelshift_r(w[i + K], w[i + K + 1], 16) : w[i + K];
-}
-
-// The lane's N words from p, MIS bytes after a 16-byte boundary; whole warp.
-template <int MIS, int N>
-__device__ __forceinline__ void load_shifted(const uint8_t* p, uint32_t (&o)[N]) {
-  const uint4* c = reinterpret_cast<const uint4*>(p - MIS);
-  uint32_t own[N];
-#pragma unroll
-  for (int i = 0; i < N / 4; ++i) {
-    const uint4 v = __ldcs(c + i);
-    own[4 * i] = v.x;
-    own[4 * i + 1] = v.y;
-    own[4 * i + 2] = v.z;
-    own[4 * i + 3] = v.w;
-  }
-  const bool end = (threadIdx.x & 31) == 31;
-  uint4 last;
-  if (end) last = __ldcs(c + N / 4);
-  uint32_t next[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) next[i] = __shfl_down_sync(0xffffffffu, own[i], 1);
-  if (end) {
-    next[0] = last.x;
-    next[1] = last.y;
-    next[2] = last.z;
-    next[3] = last.w;
-  }
-  shift_words<MIS>(own, next, o);
-}
-
-// The lane's 4 words to p, MIS bytes after a 16-byte boundary; whole warp.
-// The aligned chunk that starts in a lane's words ends in the next lane's.
-template <int MIS>
-__device__ __forceinline__ void store_shifted(uint8_t* p, const uint32_t (&w)[4]) {
-  constexpr int SKIP = 16 - MIS, HALF = MIS & 2;
-  const int lane = threadIdx.x & 31;
-  uint32_t next[4], c[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) next[i] = __shfl_down_sync(0xffffffffu, w[i], 1);
-  shift_words<SKIP>(w, next, c);
-  if (lane < 31) __stcs(reinterpret_cast<uint4*>(p + SKIP), make_uint4(c[0], c[1], c[2], c[3]));
-  if (lane == 0) {  // the run's first SKIP bytes
-    if (HALF) *reinterpret_cast<uint16_t*>(p) = static_cast<uint16_t>(w[0]);
-#pragma unroll
-    for (int j = 0; j < SKIP / 4; ++j)
-      *reinterpret_cast<uint32_t*>(p + HALF + 4 * j) = HALF ? __funnelshift_r(w[j], w[j + 1 < 4 ? j + 1 : 3], 16) : w[j];
-  }
-  if (lane == 31) {  // and its last MIS bytes
-#pragma unroll
-    for (int j = 0; j < MIS / 4; ++j) *reinterpret_cast<uint32_t*>(p + SKIP + 4 * j) = c[j];
-    if (HALF) *reinterpret_cast<uint16_t*>(p + 14) = static_cast<uint16_t>(w[3] >> 16);
-  }
-}
-
-// Elements [0, n) of the lane's 8 at p, zeros beyond; whole warp.
-__device__ __forceinline__ void load8(const uint16_t* p, Run r, int n, float2 (&o)[4]) {
-  uint32_t w[4];
-  if (r.mis == 0 && n >= 8) {
-    const uint4 v = __ldcs(reinterpret_cast<const uint4*>(p));
-    w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
-  } else if (r.inner) {
-    const uint8_t* b = reinterpret_cast<const uint8_t*>(p);
-    switch (r.mis) {
-      case 2: load_shifted<2>(b, w); break;
-      case 4: load_shifted<4>(b, w); break;
-      case 6: load_shifted<6>(b, w); break;
-      case 8: load_shifted<8>(b, w); break;
-      case 10: load_shifted<10>(b, w); break;
-      case 12: load_shifted<12>(b, w); break;
-      default: load_shifted<14>(b, w); break;
-    }
-  } else {
-#pragma unroll
-    for (int q = 0; q < 4; ++q)
-      w[q] = (2 * q < n ? uint32_t(p[2 * q]) : 0u) | (2 * q + 1 < n ? uint32_t(p[2 * q + 1]) << 16 : 0u);
-  }
-#pragma unroll
-  for (int q = 0; q < 4; ++q) o[q] = bf16_pair(w[q]);
-}
-
-__device__ __forceinline__ void load8(const float* p, Run r, int n, float2 (&o)[4]) {
-  uint32_t w[8];
-  if (r.mis == 0 && n >= 8) {
-    const uint4 a = __ldcs(reinterpret_cast<const uint4*>(p)), b = __ldcs(reinterpret_cast<const uint4*>(p) + 1);
-    w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
-    w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
-  } else if (r.inner) {
-    const uint8_t* b = reinterpret_cast<const uint8_t*>(p);
-    switch (r.mis) {
-      case 4: load_shifted<4>(b, w); break;
-      case 8: load_shifted<8>(b, w); break;
-      default: load_shifted<12>(b, w); break;
-    }
-  } else {
-#pragma unroll
-    for (int q = 0; q < 8; ++q) w[q] = q < n ? __float_as_uint(p[q]) : 0u;
-  }
-#pragma unroll
-  for (int q = 0; q < 4; ++q) o[q] = make_float2(__uint_as_float(w[2 * q]), __uint_as_float(w[2 * q + 1]));
-}
-
 __device__ __forceinline__ void load_state8(const float* p, float2 (&o)[4]) {
   const float4 a = __ldcs(reinterpret_cast<const float4*>(p));
   const float4 b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
@@ -217,31 +87,6 @@ __device__ __forceinline__ void clear_beyond(int n, float2 (&o)[4]) {
 __device__ __forceinline__ void store_state8(float* p, const float2 (&o)[4]) {
   __stcs(reinterpret_cast<float4*>(p), make_float4(o[0].x, o[0].y, o[1].x, o[1].y));
   __stcs(reinterpret_cast<float4*>(p) + 1, make_float4(o[2].x, o[2].y, o[3].x, o[3].y));
-}
-
-// The lane's elements [0, n) to p as bf16; whole warp.
-__device__ __forceinline__ void store_bf16x8(uint16_t* p, Run r, int n, const float2 (&o)[4]) {
-  uint32_t w[4];
-#pragma unroll
-  for (int q = 0; q < 4; ++q) w[q] = to_bf16_pair(o[q]);
-  if (r.mis == 0 && n >= 8) {
-    __stcs(reinterpret_cast<uint4*>(p), make_uint4(w[0], w[1], w[2], w[3]));
-  } else if (r.inner) {
-    uint8_t* b = reinterpret_cast<uint8_t*>(p);
-    switch (r.mis) {
-      case 2: store_shifted<2>(b, w); break;
-      case 4: store_shifted<4>(b, w); break;
-      case 6: store_shifted<6>(b, w); break;
-      case 8: store_shifted<8>(b, w); break;
-      case 10: store_shifted<10>(b, w); break;
-      case 12: store_shifted<12>(b, w); break;
-      default: store_shifted<14>(b, w); break;
-    }
-  } else {
-#pragma unroll
-    for (int q = 0; q < 8; ++q)
-      if (q < n) p[q] = static_cast<uint16_t>(w[q >> 1] >> (16 * (q & 1)));
-  }
 }
 
 // ------------------------------------------------------------------- norm
@@ -429,12 +274,12 @@ Keys make_keys(uint64_t seed) {
   return k;
 }
 
-// `lo`: low word of the element's index; k0 carries the high word's part.
-__device__ __forceinline__ uint32_t random_bits(uint32_t lo, uint32_t k0, uint32_t k1) {
-  uint32_t x = lo ^ k0;
-  x = (x ^ (x >> 16)) * MIX_A ^ k1;
-  x = (x ^ (x >> 15)) * MIX_C;
-  return x ^ (x >> 16);
+// The number of element `index` is x ^ (x >> 16) for
+//   x = lo ^ k0 ^ hi * MIX_B (index = hi : lo), x = (x ^ (x >> 16)) * MIX_A ^ k1, x = (x ^ (x >> 15)) * MIX_C;
+// this is the part after the first fold and without the last.
+__device__ __forceinline__ uint32_t random_rest(uint32_t folded, uint32_t k1) {
+  const uint32_t x = folded * MIX_A ^ k1;
+  return (x ^ (x >> 15)) * MIX_C;
 }
 
 // The scale of a block whose largest magnitude has the bits `top`:
@@ -551,24 +396,26 @@ struct ListArgs {
   int32_t n_tensors;
   AdamwK k;
   float step_size, inv_bc2_sqrt, max_norm, inv_m;
-  float minus_zero;  // -0, unknown to the compiler (mul2_rounded)
   Keys keys;
 };
 
-// AdamW on two elements.  What the next state comes from (m, v, sqrt(v)) is
+__device__ __forceinline__ float reciprocal(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// AdamW on one element.  What the next state comes from (m, v, sqrt(v)) is
 // rounded product by product and sum by sum; the parameter's own step, which
-// no state depends on, takes fused products and the fast quotient (2 units in
-// the last place of the step, about 2^-22 of lr).  V comes in as v and leaves
-// as sqrt(v).
-__device__ __forceinline__ void adamw_pair_sep(float2 g, const ListArgs& a, float2& P, float2& M, float2& V) {
+// no state depends on, takes fused products and the fast reciprocal (1 unit in
+// the last place; the step's error is about 2^-22 of lr).  V comes in as v and leaves
+// as sqrt(v).  Scalar on purpose: a factor from the constant bank costs a
+// scalar product nothing, a paired one two moves.
+__device__ __forceinline__ void adamw_elem_sep(float g, const ListArgs& a, float& P, float& M, float& V) {
   const AdamwK& k = a.k;
-  const float z = a.minus_zero;
-  M = add2(mul2_rounded(M, both(k.b1), z), mul2_rounded(g, both(k.omb1), z));
-  V = add2(mul2_rounded(V, both(k.b2), z), mul2_rounded(mul2(g, both(k.omb2)), g, z));
-  V = make_float2(__fsqrt_rn(V.x), __fsqrt_rn(V.y));
-  const float2 d = fma2(V, both(a.inv_bc2_sqrt), both(k.eps));
-  const float2 u = make_float2(__fdividef(M.x, d.x), __fdividef(M.y, d.y));
-  P = fma2(u, both(-a.step_size), mul2(P, both(k.decay)));
+  M = __fadd_rn(__fmul_rn(M, k.b1), __fmul_rn(g, k.omb1));
+  V = __fsqrt_rn(__fadd_rn(__fmul_rn(V, k.b2), __fmul_rn(__fmul_rn(g, k.omb2), g)));
+  P = fmaf(M * reciprocal(fmaf(V, a.inv_bc2_sqrt, k.eps)), -a.step_size, P * k.decay);
 }
 
 template <typename G, bool k8>
@@ -612,7 +459,8 @@ __global__ void __launch_bounds__(LIST_THREADS, 5) list_step_kernel(const __grid
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       V[q] = mul2(V[q], V[q]);
-      adamw_pair_sep(mul2(G2[q], both(gscale)), a, P[q], M[q], V[q]);
+      adamw_elem_sep(__fmul_rn(G2[q].x, gscale), a, P[q].x, M[q].x, V[q].x);
+      adamw_elem_sep(__fmul_rn(G2[q].y, gscale), a, P[q].y, M[q].y, V[q].y);
     }
     clear_beyond(n, M);
     clear_beyond(n, V);
@@ -621,11 +469,14 @@ __global__ void __launch_bounds__(LIST_THREADS, 5) list_step_kernel(const __grid
     uint32_t mt[8], st[8];
     code_patterns(M, ms, mt);
     code_patterns(V, ss, st);
+    // random_bits() of i ... i + 7, i a multiple of 8: the first fold is the
+    // same for all.  m takes the low half of a number, sqrt(v) the high one.
+    const uint32_t x0 = static_cast<uint32_t>(i) ^ k0, base = x0 ^ (x0 >> 16);
 #pragma unroll
     for (int q = 0; q < 8; ++q) {
-      const uint32_t r = random_bits(static_cast<uint32_t>(i) + q, k0, a.keys.k1);
-      mt[q] += (r << 4 & 0xffff0u) | 8u;
-      st[q] += (r >> 12 & 0xffff0u) | 8u;
+      const uint32_t x = random_rest(base ^ q, a.keys.k1), hi = x >> 12;
+      mt[q] += ((x << 4 ^ hi) & 0xffff0u) + 8u;
+      st[q] += (hi & 0xffff0u) + 8u;
     }
     keep_positive(V, st);
     __stcs(reinterpret_cast<uint2*>(a.m8 + i), code_bytes(mt, ms.bad));
@@ -649,7 +500,7 @@ __global__ void __launch_bounds__(LIST_THREADS, 5) list_step_kernel(const __grid
   store_state8(a.master + i, P);
   if (p16 != nullptr) {
     p16 += t.e0 + at;
-    store_bf16x8(p16, run_of(p16, t.e0 + first, t.rest - first), n, P);
+    store8(p16, run_of(p16, t.e0 + first, t.rest - first), n, P);
   }
 }
 
@@ -932,7 +783,6 @@ grs_status grs_tensors_adamw8_step(const grs_tensors* l, const grs_adamw* hp, ui
   a.m_scale = m_scale;
   a.s_scale = s_scale;
   a.keys = make_keys(seed);
-  a.minus_zero = -0.0f;
   return launch_list_step<true>(l, a, grad_dtype, stream, who);
 }
 

@@ -13,20 +13,15 @@
 #include "device.cuh"
 #include "internal.h"
 #include "launch.cuh"
+#include "packed.cuh"
+#include "shifted.cuh"
 
 namespace grs {
 namespace {
 
 constexpr int MOE_THREADS = 256;
-constexpr int MOE_CHUNK = 4096;        // slots of one sorting block
-constexpr int MOE_SORT_THREADS = 1024; // 32 warps of 128 slots each
+constexpr int MOE_SORT_THREADS = 1024;
 constexpr int MOE_WARPS = MOE_SORT_THREADS / 32;
-static_assert(MOE_CHUNK == MOE_WARPS * 128, "four groups of 32 slots a warp");
-
-__device__ __forceinline__ float moe_load(const uint16_t* p) { return __uint_as_float(uint32_t(*p) << 16); }
-__device__ __forceinline__ float moe_load(const float* p) { return *p; }
-__device__ __forceinline__ void moe_store(uint16_t* p, float x) { *p = __bfloat16_as_ushort(__float2bfloat16_rn(x)); }
-__device__ __forceinline__ void moe_store(float* p, float x) { *p = x; }
 
 // Local expert of a slot, -1 when it goes elsewhere (or is no expert).
 __device__ __forceinline__ int local_expert(const int32_t* ids, int64_t slot, int64_t n, int32_t begin, int32_t count) {
@@ -35,7 +30,9 @@ __device__ __forceinline__ int local_expert(const int32_t* ids, int64_t slot, in
   return e >= 0 && e < count ? static_cast<int>(e) : -1;
 }
 
-// Counts of one chunk's slots per expert: counts[expert * n_chunks + chunk].
+// A sorting block takes a chunk of 1024 J consecutive slots, a warp of it 32 J.
+// Counts of one chunk's slots per expert: counts[chunk * count + expert].
+template <int J>
 __global__ void __launch_bounds__(MOE_SORT_THREADS) moe_count_kernel(const int32_t* __restrict__ ids, int64_t n, int32_t begin,
                                                                      int32_t count, int32_t* __restrict__ counts) {
   extern __shared__ int32_t hist[];
@@ -43,171 +40,347 @@ __global__ void __launch_bounds__(MOE_SORT_THREADS) moe_count_kernel(const int32
   pdl_trigger();
   for (int e = threadIdx.x; e < count; e += MOE_SORT_THREADS) hist[e] = 0;
   __syncthreads();
-  const int64_t s0 = int64_t(blockIdx.x) * MOE_CHUNK;
-  for (int i = threadIdx.x; i < MOE_CHUNK; i += MOE_SORT_THREADS) {
-    const int e = local_expert(ids, s0 + i, n, begin, count);
+  const int64_t s0 = int64_t(blockIdx.x) * (MOE_SORT_THREADS * J);
+#pragma unroll
+  for (int j = 0; j < J; ++j) {
+    const int e = local_expert(ids, s0 + j * MOE_SORT_THREADS + threadIdx.x, n, begin, count);
     if (e >= 0) atomicAdd(&hist[e], 1);  // counts of whole numbers: any order gives the same
   }
   __syncthreads();
-  for (int e = threadIdx.x; e < count; e += MOE_SORT_THREADS) counts[int64_t(e) * gridDim.x + blockIdx.x] = hist[e];
+  for (int e = threadIdx.x; e < count; e += MOE_SORT_THREADS) counts[int64_t(blockIdx.x) * count + e] = hist[e];
 }
 
-// Exclusive prefix over counts[0 .. len) in place, by one block; the
-// experts' offsets are the prefixes at chunk 0.
+// Exclusive prefix of a block's 1024 values; *total = their sum.
+__device__ __forceinline__ int32_t block_prefix(int32_t x, int32_t* warp_total, int32_t* total) {
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  int32_t s = x;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int32_t y = __shfl_up_sync(0xffffffffu, s, o);
+    if (lane >= o) s += y;
+  }
+  if (lane == 31) warp_total[w] = s;
+  __syncthreads();
+  int32_t t = lane < w ? warp_total[lane] : 0, all = warp_total[lane];
+  t = __reduce_add_sync(0xffffffffu, t);
+  *total = __reduce_add_sync(0xffffffffu, all);
+  __syncthreads();
+  return t + s - x;
+}
+
+// For very many chunks: counts to each (chunk, expert)'s first row, a block an
+// expert; then moe_rows_kernel finds its starts with one load (`ready`).
 __global__ void __launch_bounds__(MOE_SORT_THREADS) moe_scan_kernel(int32_t* __restrict__ counts, int32_t n_chunks, int32_t count,
-                                                                    int32_t* __restrict__ offsets) {
+                                                                    int32_t* __restrict__ totals) {
+  __shared__ int32_t warp_total[MOE_WARPS];
+  pdl_wait();
+  pdl_trigger();
+  int32_t carry = 0;
+  for (int64_t c0 = 0; c0 < n_chunks; c0 += MOE_SORT_THREADS) {
+    const int64_t c = c0 + threadIdx.x;
+    const int32_t x = c < n_chunks ? counts[c * count + blockIdx.x] : 0;
+    int32_t all;
+    const int32_t before = block_prefix(x, warp_total, &all);
+    if (c < n_chunks) counts[c * count + blockIdx.x] = carry + before;
+    carry += all;
+  }
+  if (threadIdx.x == 0) totals[blockIdx.x] = carry;
+}
+
+// Rows of one chunk's slots.  A warp ranks its slots, 32 at a time, by a match
+// of equal experts, and counts them per expert in shared memory; a prefix over
+// the warps turns the counts into the warp's starts behind the chunk's.  So
+// the order of slots is kept.  The chunk's starts come from its own counts
+// alone (one chunk), from all chunks' counts (few of them: each block adds up
+// the whole table), or from the scan above (`totals`).
+template <int J>
+__global__ void __launch_bounds__(MOE_SORT_THREADS) moe_rows_kernel(const int32_t* __restrict__ ids, int64_t n, int32_t begin,
+                                                                    int32_t count, int32_t n_chunks,
+                                                                    const int32_t* __restrict__ counts,
+                                                                    const int32_t* __restrict__ totals,
+                                                                    int32_t* __restrict__ offsets,
+                                                                    int32_t* __restrict__ row_slot,
+                                                                    int32_t* __restrict__ slot_row) {
+  extern __shared__ int32_t at[];  // [MOE_WARPS][count], then the experts' totals and what lies before the chunk
   __shared__ int32_t warp_total[MOE_WARPS];
   pdl_wait();
   pdl_trigger();
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  const int64_t len = int64_t(n_chunks) * count;
-  int32_t carry = 0;
-  for (int64_t base = 0; base < len; base += MOE_SORT_THREADS) {
-    const int64_t i = base + threadIdx.x;
-    const int32_t x = i < len ? counts[i] : 0;
-    int32_t s = x;
+  const int64_t s0 = int64_t(blockIdx.x) * (MOE_SORT_THREADS * J) + w * (32 * J);
+  int32_t *mine = at + w * count, *total = at + MOE_WARPS * count, *before = total + count;
+  int e[J], rank[J];
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int32_t y = __shfl_up_sync(0xffffffffu, s, o);
-      if (lane >= o) s += y;
-    }
-    if (lane == 31) warp_total[w] = s;
-    __syncthreads();
-    int32_t before = carry, all = 0;
-    for (int k = 0; k < MOE_WARPS; ++k) {
-      if (k < w) before += warp_total[k];
-      all += warp_total[k];
-    }
-    if (i < len) {
-      counts[i] = before + s - x;
-      if (i % n_chunks == 0) offsets[i / n_chunks] = before + s - x;
-    }
-    carry += all;
-    __syncthreads();
-  }
-  if (threadIdx.x == 0) offsets[count] = carry;
-}
-
-// Rows of one chunk's slots.  A warp owns 128 consecutive slots; its count
-// per expert so far is in shared memory, turned into a start per warp by a
-// prefix over the warps, and slots of one group of 32 are ranked by a match
-// of equal experts: the order of slots is kept.
-__global__ void __launch_bounds__(MOE_SORT_THREADS) moe_rows_kernel(const int32_t* __restrict__ ids, int64_t n, int32_t begin,
-                                                                    int32_t count, const int32_t* __restrict__ starts,
-                                                                    const int32_t* __restrict__ offsets,
-                                                                    int32_t* __restrict__ row_slot,
-                                                                    int32_t* __restrict__ slot_row) {
-  extern __shared__ int32_t at[];  // [MOE_WARPS][count]
-  pdl_wait();
-  pdl_trigger();
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  const int64_t s0 = int64_t(blockIdx.x) * MOE_CHUNK + w * 128;
-  int32_t* mine = at + w * count;
-  for (int i = threadIdx.x; i < MOE_WARPS * count; i += MOE_SORT_THREADS) at[i] = 0;
+  for (int j = 0; j < J; ++j) e[j] = local_expert(ids, s0 + j * 32 + lane, n, begin, count);
+  for (int i = threadIdx.x; i < (MOE_WARPS + 2) * count; i += MOE_SORT_THREADS) at[i] = 0;
   __syncthreads();
-  int e[4];
-  int rank[4];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    e[j] = local_expert(ids, s0 + j * 32 + lane, n, begin, count);
+  for (int j = 0; j < J; ++j) {
     const unsigned same = __match_any_sync(0xffffffffu, e[j]);
-    rank[j] = 0;
-    if (e[j] >= 0) {
-      rank[j] = mine[e[j]] + __popc(same & ((1u << lane) - 1u));
-    }
+    rank[j] = e[j] >= 0 ? mine[e[j]] + __popc(same & ((1u << lane) - 1u)) : 0;
     __syncwarp();
     if (e[j] >= 0 && lane == __ffs(same) - 1) mine[e[j]] += __popc(same);
     __syncwarp();
   }
+  if (n_chunks > 1 && totals == nullptr) {
+    for (int c = w; c < n_chunks; c += MOE_WARPS)
+      for (int x = lane; x < count; x += 32) {
+        const int32_t v = counts[int64_t(c) * count + x];
+        if (v != 0) {
+          atomicAdd(&total[x], v);
+          if (c < static_cast<int>(blockIdx.x)) atomicAdd(&before[x], v);
+        }
+      }
+  }
   __syncthreads();
-  for (int x = threadIdx.x; x < count; x += MOE_SORT_THREADS) {
-    int32_t s = starts[int64_t(x) * gridDim.x + blockIdx.x];
+  // The warps' counts to their offsets in the chunk (at most 1024 experts: a thread each).
+  const int x = threadIdx.x;
+  int32_t sum = 0;
+  if (x < count) {
     for (int k = 0; k < MOE_WARPS; ++k) {
       const int32_t c = at[k * count + x];
-      at[k * count + x] = s;
-      s += c;
+      at[k * count + x] = sum;
+      sum += c;
     }
+    if (n_chunks > 1) sum = totals != nullptr ? totals[x] : total[x];
   }
+  int32_t rows;
+  int32_t start = block_prefix(x < count ? sum : 0, warp_total, &rows);
+  if (x < count) {
+    if (blockIdx.x == 0) offsets[x] = start;
+    start += totals != nullptr ? counts[int64_t(blockIdx.x) * count + x] : before[x];
+    before[x] = start;
+  }
+  if (blockIdx.x == 0 && x == 0) offsets[count] = rows;
   __syncthreads();
-  const int32_t total = offsets[count];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
+  for (int j = 0; j < J; ++j) {
     const int64_t slot = s0 + j * 32 + lane;
     if (slot >= n) continue;
-    const int32_t row = e[j] >= 0 ? mine[e[j]] + rank[j] : -1;
+    const int32_t row = e[j] >= 0 ? before[e[j]] + mine[e[j]] + rank[j] : -1;
     slot_row[slot] = row;
     if (row >= 0) row_slot[row] = static_cast<int32_t>(slot);
-    if (slot >= total) row_slot[slot] = -1;  // rows that no slot has
+    if (slot >= rows) row_slot[slot] = -1;  // rows that no slot has
   }
 }
 
+// ------------------------------------------------------------- vectors
+// Every thread handles 8 consecutive elements of a token and of its rows.
+// With whole vectors (hidden a multiple of 8 elements, 16-byte aligned) a
+// thread stands by itself; otherwise a warp takes a run of 256 elements whose
+// rows all start anywhere (shifted.cuh).
+template <typename T>
+struct MoeArgs {
+  const T *a, *b;              // inputs: tokens' or rows' vectors
+  T *o;                        // output
+  const int32_t* slot_row;
+  const float* weights;        // may be null
+  float* dweights;
+  int64_t tokens, slots;
+  int32_t k, d, units;         // units: 8-element groups of a vector, 256-element runs of a loose one
+  int32_t group;               // threads of a token (combine_backward)
+};
+
 // A row index of the caller's map, -1 unless it is a row.
-__device__ __forceinline__ int64_t checked_row(const int32_t* slot_row, int64_t slot, int64_t n_slots) {
-  const int64_t r = slot_row[slot];
-  return r >= 0 && r < n_slots ? r : -1;
+template <typename T>
+__device__ __forceinline__ int64_t moe_row(const MoeArgs<T>& a, int64_t slot) {
+  const int64_t r = __ldg(a.slot_row + slot);
+  return r >= 0 && r < a.slots ? r : -1;
 }
 
-template <typename T>
-__global__ void __launch_bounds__(MOE_THREADS) moe_dispatch_kernel(const T* __restrict__ x, const int32_t* __restrict__ slot_row,
-                                                                   T* __restrict__ xs, int64_t tokens, int32_t k, int32_t d) {
-  pdl_wait();
-  pdl_trigger();
-  for (int64_t t = blockIdx.x; t < tokens; t += gridDim.x)
-    for (int c = threadIdx.x; c < d; c += MOE_THREADS) {
-      const T v = x[t * d + c];
-      for (int j = 0; j < k; ++j) {
-        const int64_t r = checked_row(slot_row, t * k + j, tokens * k);
-        if (r >= 0) xs[r * d + c] = v;
+// The thread's elements [c, c + 8) of vector v of a matrix of `vectors`, on
+// their way and as pairs; zeros if v < 0 and beyond the vector.
+template <bool kWhole, typename T>
+struct Vec {
+  Moving<T> m;
+  int mis;      // loose vectors: where they start, -1 for no vector
+  bool inner;
+
+  __device__ __forceinline__ void start(const T* base, int64_t v, int64_t vectors, int c, int d) {
+#pragma unroll
+    for (int i = 0; i < Moving<T>::N; ++i) m.own[i] = 0u;
+    mis = -1;
+    inner = false;
+    if (v < 0) return;
+    const T* p = base + v * d + c;
+    if constexpr (kWhole) {
+      m.start(p, Run{0, true}, 8);
+    } else {
+      const int64_t first = v * d + (c & ~255);
+      const Run r = run_of(p, first, vectors * d - first);
+      m.start(p, r, r.inner ? 8 : d - c);
+      mis = r.mis;
+      inner = r.inner;
+    }
+  }
+  __device__ __forceinline__ void finish(int c, int d) {
+    if constexpr (!kWhole) {
+      if (mis < 0) return;
+      m.finish(Run{mis, inner});
+      if (d - c < 8) {  // a run's last elements may have come with the next vector's
+        constexpr int E = 4 / static_cast<int>(sizeof(T));  // elements of a word
+#pragma unroll
+        for (int i = 0; i < Moving<T>::N; ++i) {
+          if (i * E >= d - c) m.own[i] = 0u;
+          if (E == 2 && i * E + 1 >= d - c) m.own[i] &= 0xffffu;
+        }
       }
     }
+  }
+  __device__ __forceinline__ float2 pair(int q) const { return m.pair(q); }
+};
+
+// Where a vector's elements from c on are stored.
+template <bool kWhole, typename T>
+__device__ __forceinline__ Run store_run(const T* p, int c, int d) {
+  if constexpr (kWhole) return Run{0, true};
+  return Run{static_cast<int>(reinterpret_cast<uintptr_t>(p) & 15), d - (c & ~255) >= 256};
 }
+
+template <bool kWhole, typename T>
+__device__ __forceinline__ void vec_store(T* m, int64_t v, int c, int d, const float2 (&o)[4]) {
+  T* p = m + v * d + c;
+  store8(p, store_run<kWhole>(p, c, d), kWhole ? 8 : d - c, o);
+}
+
+// The token and the first element of this thread; false beyond the last.
+template <bool kWhole, typename T>
+__device__ __forceinline__ bool moe_place(const MoeArgs<T>& a, int64_t* t, int* c) {
+  const int64_t i = kWhole ? int64_t(blockIdx.x) * MOE_THREADS + threadIdx.x
+                           : int64_t(blockIdx.x) * (MOE_THREADS / 32) + (threadIdx.x >> 5);
+  *t = i <= UINT32_MAX ? static_cast<uint32_t>(i) / static_cast<uint32_t>(a.units) : i / a.units;
+  const int u = static_cast<int>(i - *t * a.units);
+  *c = kWhole ? u * 8 : u * 256 + (threadIdx.x & 31) * 8;
+  return *t < a.tokens;
+}
+
+// xs[row] = x[t] for each of the token's rows: x is read once.
+template <typename T, bool kWhole>
+__global__ void __launch_bounds__(MOE_THREADS) moe_dispatch_kernel(const __grid_constant__ MoeArgs<T> a) {
+  pdl_wait();
+  pdl_trigger();
+  int64_t t;
+  int c;
+  if (!moe_place<kWhole>(a, &t, &c)) return;
+  Vec<kWhole, T> x;
+  x.start(a.a, t, a.tokens, c, a.d);
+  x.finish(c, a.d);
+  for (int j0 = 0; j0 < a.k; j0 += 8) {
+    int64_t r[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) r[j] = j0 + j < a.k ? moe_row(a, t * a.k + j0 + j) : -1;
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (r[j] >= 0) {
+        T* p = a.o + r[j] * a.d + c;
+        store_words(p, store_run<kWhole>(p, c, a.d), kWhole ? 8 : a.d - c, x.m.own);  // the bits as they are
+      }
+  }
+}
+
+// Rows of a token in flight at once.
+template <bool kWhole>
+constexpr int moe_batch = kWhole ? 8 : 4;
 
 // y[t] = sum over the token's rows of weight * row; without weights, of the row.
-template <typename T>
-__global__ void __launch_bounds__(MOE_THREADS) moe_combine_kernel(const T* __restrict__ ys, const int32_t* __restrict__ slot_row,
-                                                                  const float* __restrict__ weights, T* __restrict__ y,
-                                                                  int64_t tokens, int32_t k, int32_t d) {
+template <typename T, bool kWhole>
+__global__ void __launch_bounds__(MOE_THREADS) moe_combine_kernel(const __grid_constant__ MoeArgs<T> a) {
+  constexpr int B = moe_batch<kWhole>;
   pdl_wait();
   pdl_trigger();
-  for (int64_t t = blockIdx.x; t < tokens; t += gridDim.x)
-    for (int c = threadIdx.x; c < d; c += MOE_THREADS) {
-      float s = 0.0f;
-      for (int j = 0; j < k; ++j) {
-        const int64_t r = checked_row(slot_row, t * k + j, tokens * k);
-        if (r >= 0) s = fmaf(weights != nullptr ? weights[t * k + j] : 1.0f, moe_load(ys + r * d + c), s);
-      }
-      moe_store(y + t * d + c, s);
+  int64_t t;
+  int c;
+  if (!moe_place<kWhole>(a, &t, &c)) return;
+  float2 s[4] = {both(0.0f), both(0.0f), both(0.0f), both(0.0f)};
+  for (int j0 = 0; j0 < a.k; j0 += B) {
+    Vec<kWhole, T> v[B];
+    float w[B];
+#pragma unroll
+    for (int j = 0; j < B; ++j) {
+      const int64_t slot = t * a.k + j0 + j, r = j0 + j < a.k ? moe_row(a, slot) : -1;
+      w[j] = r < 0 ? 0.0f : a.weights != nullptr ? __ldg(a.weights + slot) : 1.0f;
+      v[j].start(a.a, r, a.slots, c, a.d);
     }
+#pragma unroll
+    for (int j = 0; j < B; ++j) {
+      v[j].finish(c, a.d);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) s[q] = fma2(v[j].pair(q), both(w[j]), s[q]);
+    }
+  }
+  vec_store<kWhole>(a.o, t, c, a.d, s);
 }
 
-template <typename T>
-__global__ void __launch_bounds__(MOE_THREADS) moe_combine_bwd_kernel(const T* __restrict__ dy, const T* __restrict__ ys,
-                                                                      const int32_t* __restrict__ slot_row,
-                                                                      const float* __restrict__ weights, T* __restrict__ dys,
-                                                                      float* __restrict__ dweights, int64_t tokens, int32_t k,
-                                                                      int32_t d) {
-  __shared__ float red[MOE_THREADS / 32];
+// dys[row] = weight * dy[t] and dweights[slot] = <ys[row], dy[t]>.  A group of
+// threads a token; its threads' parts of a batch of products meet once.
+template <typename T, bool kWhole>
+__global__ void __launch_bounds__(MOE_THREADS) moe_combine_bwd_kernel(const __grid_constant__ MoeArgs<T> a) {
+  constexpr int B = moe_batch<kWhole>;
+  __shared__ float red[MOE_THREADS / 32][B];
   pdl_wait();
   pdl_trigger();
-  for (int64_t slot = blockIdx.x; slot < tokens * k; slot += gridDim.x) {
-    const int64_t r = checked_row(slot_row, slot, tokens * k), t = slot / k;
-    const float w = weights[slot];
-    float s = 0.0f;
-    if (r >= 0)
-      for (int c = threadIdx.x; c < d; c += MOE_THREADS) {
-        const float g = moe_load(dy + t * d + c);
-        moe_store(dys + r * d + c, w * g);
-        s = fmaf(g, moe_load(ys + r * d + c), s);
-      }
-    s = warp_sum(s);
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = s;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-      s = red[0];
-      for (int j = 1; j < MOE_THREADS / 32; ++j) s += red[j];
-      dweights[slot] = s;
+  const int groups = blockDim.x / a.group, g = threadIdx.x / a.group, i = threadIdx.x - g * a.group;
+  const int64_t t = int64_t(blockIdx.x) * groups + g;
+  const bool on = t < a.tokens;
+  const int per = kWhole ? a.group * 8 : a.group / 32 * 256;
+  const int c0 = kWhole ? i * 8 : (i >> 5) * 256 + (i & 31) * 8;
+  for (int j0 = 0; j0 < a.k; j0 += B) {
+    int64_t r[B];
+    float w[B], dot[B];
+#pragma unroll
+    for (int j = 0; j < B; ++j) {
+      const int64_t slot = t * a.k + j0 + j;
+      r[j] = on && j0 + j < a.k ? moe_row(a, slot) : -1;
+      w[j] = r[j] >= 0 ? __ldg(a.weights + slot) : 0.0f;
+      dot[j] = 0.0f;
     }
-    __syncthreads();
+    if (on)
+#pragma unroll 1
+      for (int c = c0; (kWhole ? c : c & ~255) < a.d; c += per) {
+        Vec<kWhole, T> gv, v[B];
+        gv.start(a.a, t, a.tokens, c, a.d);
+#pragma unroll
+        for (int j = 0; j < B; ++j) v[j].start(a.b, r[j], a.slots, c, a.d);
+        gv.finish(c, a.d);
+        float2 gy[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) gy[q] = gv.pair(q);
+#pragma unroll
+        for (int j = 0; j < B; ++j) {
+          if (r[j] < 0) continue;
+          v[j].finish(c, a.d);
+          float2 s = both(0.0f), o[4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            s = fma2(v[j].pair(q), gy[q], s);
+            o[q] = mul2(gy[q], both(w[j]));
+          }
+          dot[j] += s.x + s.y;
+          vec_store<kWhole>(a.o, r[j], c, a.d, o);
+        }
+      }
+#pragma unroll
+    for (int j = 0; j < B; ++j)
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        const float x = __shfl_xor_sync(0xffffffffu, dot[j], o);
+        if (o < a.group) dot[j] = __fadd_rn(dot[j], x);
+      }
+    if (a.group > 32) {  // one token a block
+      __syncthreads();   // red may still be read
+      if ((threadIdx.x & 31) == 0)
+#pragma unroll
+        for (int j = 0; j < B; ++j) red[threadIdx.x >> 5][j] = dot[j];
+      __syncthreads();
+      if (threadIdx.x < B && j0 + threadIdx.x < a.k) {
+        float s = red[0][threadIdx.x];
+        for (int k = 1; k < static_cast<int>(blockDim.x >> 5); ++k) s = __fadd_rn(s, red[k][threadIdx.x]);
+        if (on) a.dweights[t * a.k + j0 + threadIdx.x] = s;
+      }
+    } else if (on && i == 0) {
+#pragma unroll
+      for (int j = 0; j < B; ++j)
+        if (j0 + j < a.k) a.dweights[t * a.k + j0 + j] = dot[j];
+    }
   }
 }
 
@@ -223,9 +396,92 @@ grs_status check_moe(const grs_moe* s, const char* who) {
   return GRS_OK;
 }
 
-int64_t moe_chunks(const grs_moe* s) { return (s->tokens * s->top_k + MOE_CHUNK - 1) / MOE_CHUNK; }
+// Slots of a sorting block: 1024 while that makes one block an SM, else 4096.
+int moe_chunk_slots(const grs_moe* s) { return s->tokens * s->top_k <= 152 * 1024 ? 1024 : 4096; }
+int64_t moe_chunks(const grs_moe* s) {
+  const int64_t c = moe_chunk_slots(s);
+  return (s->tokens * s->top_k + c - 1) / c;
+}
 
-unsigned moe_grid(int64_t n) { return static_cast<unsigned>(n < 1 << 20 ? n : 1 << 20); }
+template <int J>
+cudaError_t moe_sort(const grs_moe* s, const int32_t* ids, int32_t* offsets, int32_t* row_slot, int32_t* slot_row, int32_t* ws,
+                     void* stream) {
+  const int64_t n = s->tokens * s->top_k;
+  const int32_t count = s->expert_end - s->expert_begin, chunks = static_cast<int32_t>(moe_chunks(s));
+  const dim3 grid(static_cast<unsigned>(chunks)), block(MOE_SORT_THREADS);
+  cudaError_t e = cudaSuccess;
+  if (chunks > 1) e = launch_pdl(moe_count_kernel<J>, grid, block, size_t(count) * 4, stream, ids, n, s->expert_begin, count, ws);
+  // Each block of the last kernel reads the whole table up to 256 Ki counts (1 MB); beyond, the scan is cheaper.
+  const bool scan = int64_t(chunks) * count > 256 * 1024;
+  int32_t* totals = scan ? ws + int64_t(chunks) * count : nullptr;
+  if (e == cudaSuccess && scan)
+    e = launch_pdl(moe_scan_kernel, dim3(static_cast<unsigned>(count)), block, 0, stream, ws, chunks, count, totals);
+  if (e == cudaSuccess) e = allow_smem<moe_rows_kernel<J>>((MOE_WARPS + 2) * GRS_MOE_MAX_EXPERTS * 4);
+  if (e == cudaSuccess)
+    e = launch_pdl(moe_rows_kernel<J>, grid, block, size_t(MOE_WARPS + 2) * count * 4, stream, ids, n, s->expert_begin, count, chunks,
+                   static_cast<const int32_t*>(ws), static_cast<const int32_t*>(totals), offsets, row_slot, slot_row);
+  return e;
+}
+
+template <typename T>
+MoeArgs<T> moe_args(const grs_moe* s, const void* a, const void* b, void* o, const int32_t* slot_row, const float* weights,
+                    float* dweights, bool whole) {
+  const int32_t units = whole ? s->hidden / 8 : (s->hidden - 1) / 256 + 1;
+  return {static_cast<const T*>(a), static_cast<const T*>(b), static_cast<T*>(o), slot_row, weights, dweights, s->tokens,
+          s->tokens * s->top_k, s->top_k, s->hidden, units, 0};
+}
+
+// 16-byte aligned vectors of whole 8-element groups.
+bool moe_whole(const grs_moe* s, const void* a, const void* b, const void* o) {
+  return s->hidden % 8 == 0 && api_aligned(a, 16) && api_aligned(b, 16) && api_aligned(o, 16);
+}
+
+enum class MoeOp { kDispatch, kCombine, kCombineBackward };
+
+template <typename T, bool kWhole>
+cudaError_t moe_launch(MoeOp op, MoeArgs<T> a, void* stream) {
+  if (op == MoeOp::kCombineBackward) {
+    // Threads of a token: its units in whole groups as far as a block goes.
+    int threads = MOE_THREADS;
+    if (kWhole && a.units <= 32) {
+      a.group = 1;
+      while (a.group < a.units) a.group *= 2;
+    } else {
+      int warps = kWhole ? (a.units + 31) / 32 : a.units;
+      // Many tokens of up to 8 KB: a warp each, whose products meet without a
+      // barrier (16384 x 8 of 2048 bf16: 174 us against 194; 4096 x 8 of 4096
+      // fp32 the other way round, 183 and 168).
+      if (a.tokens >= 16 * 152 && a.d * static_cast<int64_t>(sizeof(T)) <= 8192) warps = 1;
+      a.group = 32 * (warps < MOE_THREADS / 32 ? warps : MOE_THREADS / 32);
+      if (a.group > 32) threads = a.group;
+    }
+    const int64_t per = threads / a.group, blocks = (a.tokens + per - 1) / per;
+    return launch_pdl(moe_combine_bwd_kernel<T, kWhole>, dim3(static_cast<unsigned>(blocks)), dim3(threads), 0, stream, a);
+  }
+  const int64_t per = kWhole ? MOE_THREADS : MOE_THREADS / 32, blocks = (a.tokens * a.units + per - 1) / per;
+  if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
+  const dim3 grid(static_cast<unsigned>(blocks)), block(MOE_THREADS);
+  return op == MoeOp::kDispatch ? launch_pdl(moe_dispatch_kernel<T, kWhole>, grid, block, 0, stream, a)
+                                : launch_pdl(moe_combine_kernel<T, kWhole>, grid, block, 0, stream, a);
+}
+
+cudaError_t moe_run(MoeOp op, const grs_moe* s, const void* a, const void* b, void* o, const int32_t* slot_row,
+                    const float* weights, float* dweights, void* stream) {
+  const bool whole = moe_whole(s, a, b, o);
+  if (op == MoeOp::kDispatch && whole && s->dtype == GRS_DTYPE_FP32 && s->hidden <= INT32_MAX / 2) {
+    // A copy of bytes: 16 a thread and row.
+    MoeArgs<uint16_t> x = moe_args<uint16_t>(s, a, b, o, slot_row, weights, dweights, whole);
+    x.d *= 2;
+    x.units *= 2;
+    return moe_launch<uint16_t, true>(op, x, stream);
+  }
+  if (s->dtype == GRS_DTYPE_FP32) {
+    const MoeArgs<float> x = moe_args<float>(s, a, b, o, slot_row, weights, dweights, whole);
+    return whole ? moe_launch<float, true>(op, x, stream) : moe_launch<float, false>(op, x, stream);
+  }
+  const MoeArgs<uint16_t> x = moe_args<uint16_t>(s, a, b, o, slot_row, weights, dweights, whole);
+  return whole ? moe_launch<uint16_t, true>(op, x, stream) : moe_launch<uint16_t, false>(op, x, stream);
+}
 
 }  // namespace
 }  // namespace grs
@@ -236,7 +492,7 @@ extern "C" {
 
 int64_t grs_moe_workspace_bytes(const grs_moe* s) {
   if (check_moe(s, "grs_moe_workspace_bytes") != GRS_OK) return -1;
-  return moe_chunks(s) * (s->expert_end - s->expert_begin) * 4;
+  return (moe_chunks(s) + 1) * (s->expert_end - s->expert_begin) * 4;  // counts of each chunk, totals
 }
 
 grs_status grs_moe_sort(const grs_moe* s, const int32_t* expert_ids, int32_t* expert_offsets, int32_t* row_slot,
@@ -250,27 +506,13 @@ grs_status grs_moe_sort(const grs_moe* s, const int32_t* expert_ids, int32_t* ex
   if (!api_aligned(expert_ids, 4) || !api_aligned(expert_offsets, 4) || !api_aligned(row_slot, 4) || !api_aligned(slot_row, 4) ||
       !api_aligned(workspace, 16))
     return api_fail(GRS_ERR_ALIGNMENT, who, "misaligned pointer");
-  const int32_t count = s->expert_end - s->expert_begin;
-  const int32_t chunks = static_cast<int32_t>(moe_chunks(s));
-  int32_t* counts = static_cast<int32_t*>(workspace);
-  cudaError_t e = cudaSuccess;
-  if (chunks == 0) {
-    e = cudaMemsetAsync(expert_offsets, 0, (size_t(count) + 1) * 4, static_cast<cudaStream_t>(stream));
-    return e == cudaSuccess ? GRS_OK : api_cuda_fail(e, who);
-  }
-  e = launch_pdl(moe_count_kernel, dim3(chunks), dim3(MOE_SORT_THREADS), count * 4, stream, expert_ids, n, s->expert_begin, count,
-               counts);
-  if (e == cudaSuccess)
-    e = launch_pdl(moe_scan_kernel, dim3(1), dim3(MOE_SORT_THREADS), 0, stream, counts, chunks, count, expert_offsets);
-  if (e == cudaSuccess) {
-    const size_t smem = size_t(MOE_WARPS) * count * 4;
-    if (smem > 48 * 1024)
-      e = cudaFuncSetAttribute(moe_rows_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-    const int32_t *starts = counts, *offsets = expert_offsets;
-    if (e == cudaSuccess)
-      e = launch_pdl(moe_rows_kernel, dim3(chunks), dim3(MOE_SORT_THREADS), smem, stream, expert_ids, n, s->expert_begin, count,
-                   starts, offsets, row_slot, slot_row);
-  }
+  int32_t* ws = static_cast<int32_t*>(workspace);
+  cudaError_t e;
+  if (n == 0)
+    e = cudaMemsetAsync(expert_offsets, 0, (size_t(s->expert_end - s->expert_begin) + 1) * 4, static_cast<cudaStream_t>(stream));
+  else
+    e = moe_chunk_slots(s) == 1024 ? moe_sort<1>(s, expert_ids, expert_offsets, row_slot, slot_row, ws, stream)
+                                   : moe_sort<4>(s, expert_ids, expert_offsets, row_slot, slot_row, ws, stream);
   return e == cudaSuccess ? GRS_OK : api_cuda_fail(e, who);
 }
 
@@ -283,12 +525,7 @@ grs_status grs_moe_dispatch(const grs_moe* s, const void* x, const int32_t* slot
   const uintptr_t ea = dtype_size(s->dtype);
   if (!api_aligned(x, ea) || !api_aligned(xs, ea) || !api_aligned(slot_row, 4))
     return api_fail(GRS_ERR_ALIGNMENT, who, "a pointer is not aligned to its element");
-  const dim3 grid(moe_grid(s->tokens)), block(MOE_THREADS);
-  const cudaError_t e = s->dtype == GRS_DTYPE_FP32
-                            ? launch_pdl(moe_dispatch_kernel<float>, grid, block, 0, stream, static_cast<const float*>(x), slot_row,
-                                       static_cast<float*>(xs), s->tokens, s->top_k, s->hidden)
-                            : launch_pdl(moe_dispatch_kernel<uint16_t>, grid, block, 0, stream, static_cast<const uint16_t*>(x),
-                                       slot_row, static_cast<uint16_t*>(xs), s->tokens, s->top_k, s->hidden);
+  const cudaError_t e = moe_run(MoeOp::kDispatch, s, x, nullptr, xs, slot_row, nullptr, nullptr, stream);
   return e == cudaSuccess ? GRS_OK : api_cuda_fail(e, who);
 }
 
@@ -302,13 +539,7 @@ static grs_status combine(const grs_moe* s, const void* ys, const int32_t* slot_
   const uintptr_t ea = dtype_size(s->dtype);
   if (!api_aligned(ys, ea) || !api_aligned(y, ea) || !api_aligned(slot_row, 4) || !api_aligned(weights, 4))
     return api_fail(GRS_ERR_ALIGNMENT, who, "a pointer is not aligned to its element");
-  const dim3 grid(moe_grid(s->tokens)), block(MOE_THREADS);
-  const cudaError_t e =
-      s->dtype == GRS_DTYPE_FP32
-          ? launch_pdl(moe_combine_kernel<float>, grid, block, 0, stream, static_cast<const float*>(ys), slot_row, weights,
-                     static_cast<float*>(y), s->tokens, s->top_k, s->hidden)
-          : launch_pdl(moe_combine_kernel<uint16_t>, grid, block, 0, stream, static_cast<const uint16_t*>(ys), slot_row, weights,
-                     static_cast<uint16_t*>(y), s->tokens, s->top_k, s->hidden);
+  const cudaError_t e = moe_run(MoeOp::kCombine, s, ys, nullptr, y, slot_row, weights, nullptr, stream);
   return e == cudaSuccess ? GRS_OK : api_cuda_fail(e, who);
 }
 
@@ -332,14 +563,7 @@ grs_status grs_moe_combine_backward(const grs_moe* s, const void* dy, const void
   if (!api_aligned(dy, ea) || !api_aligned(ys, ea) || !api_aligned(dys, ea) || !api_aligned(slot_row, 4) ||
       !api_aligned(weights, 4) || !api_aligned(dweights, 4))
     return api_fail(GRS_ERR_ALIGNMENT, who, "a pointer is not aligned to its element");
-  const dim3 grid(moe_grid(s->tokens * s->top_k)), block(MOE_THREADS);
-  const cudaError_t e =
-      s->dtype == GRS_DTYPE_FP32
-          ? launch_pdl(moe_combine_bwd_kernel<float>, grid, block, 0, stream, static_cast<const float*>(dy),
-                     static_cast<const float*>(ys), slot_row, weights, static_cast<float*>(dys), dweights, s->tokens, s->top_k, s->hidden)
-          : launch_pdl(moe_combine_bwd_kernel<uint16_t>, grid, block, 0, stream, static_cast<const uint16_t*>(dy),
-                     static_cast<const uint16_t*>(ys), slot_row, weights, static_cast<uint16_t*>(dys), dweights, s->tokens, s->top_k,
-                     s->hidden);
+  const cudaError_t e = moe_run(MoeOp::kCombineBackward, s, dy, ys, dys, slot_row, weights, dweights, stream);
   return e == cudaSuccess ? GRS_OK : api_cuda_fail(e, who);
 }
 

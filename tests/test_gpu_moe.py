@@ -65,6 +65,16 @@ def test_sort(grs, tokens, k, experts, begin, end, kind):
         assert np.array_equal(a, b)
 
 
+@pytest.mark.parametrize("experts,begin,end", [(1024, 0, 1024), (900, 100, 900), (3, 0, 3)])
+def test_sort_of_many_slots(grs, experts, begin, end):
+    """Tables of counts beyond what one block adds up by itself."""
+    tokens, k = 250007, 8
+    ids = np.random.default_rng(1).integers(0, experts, tokens * k).astype(np.int32)
+    got = sort(grs, grs.make_moe(tokens, k, experts, begin, end, 8, 0), torch.from_numpy(ids).cuda())
+    for a, b in zip(got, sorted64(ids, begin, end)):
+        assert np.array_equal(a, b)
+
+
 class Case:
     def __init__(self, grs, tokens, k, d, act, experts=6, begin=0, end=6, shift=0, seed=0):
         self.grs, self.tokens, self.k, self.d, self.act = grs, tokens, k, d, DT[act]

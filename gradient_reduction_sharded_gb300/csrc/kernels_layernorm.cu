@@ -444,7 +444,7 @@ struct LnBwd {
 // is in flight while a row is worked on.
 template <typename T, typename W, int VEC, int E>
 __global__ void __launch_bounds__(LN_BWD_THREADS) ln_bwd_kernel(const __grid_constant__ LnBwd<T, W> a) {
-  extern __shared__ __align__(16) float sums[];  // [threads][E] at a time; the groups' warp sums before that
+  extern __shared__ __align__(16) float sums[];  // the groups' warp sums and the ring; the parts' sums after it
   pdl_wait();
   pdl_trigger();
   const Place p = ln_place(a.tpr, reinterpret_cast<float2*>(sums));
@@ -530,21 +530,32 @@ __global__ void __launch_bounds__(LN_BWD_THREADS) ln_bwd_kernel(const __grid_con
   }
   ring_wait<0>();  // no copy outlives the slots
   if (a.parts == nullptr) return;
+  // The groups' sums meet in the ring's place: [dw or db][group][tpr * E].
+  const int wide = tpr * E, half = groups * wide;
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    float* mine = sums + k * half + g * wide;
+#pragma unroll
+    for (int i = 0; i < E / 2; i += VEC == 2 ? 1 : 2) {
+      const float2* v = (k == 0 ? dw : db) + i;
+      float* at = mine + (2 * i / VEC * tpr + t) * VEC + 2 * i % VEC;
+      if constexpr (VEC == 2)
+        *reinterpret_cast<float2*>(at) = v[0];
+      else
+        *reinterpret_cast<float4*>(at) = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
+    }
+  }
+  __syncthreads();
   float* part = a.parts + int64_t(blockIdx.x) * 2 * a.cols;
-#pragma unroll
-  for (int pass = 0; pass < 2; ++pass) {
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < E; ++i) {
-      const float2 v = pass == 0 ? dw[i / 2] : db[i / 2];
-      sums[(i / VEC * tpr + t) * VEC + i % VEC + g * tpr * E] = i & 1 ? v.y : v.x;
+  for (int c = threadIdx.x; c < a.cols; c += blockDim.x) {
+    float s = sums[c], u = sums[half + c];
+    for (int k = 1; k < groups; ++k) {
+      s += sums[c + k * wide];
+      u += sums[half + c + k * wide];
     }
-    __syncthreads();
-    for (int c = threadIdx.x; c < a.cols; c += blockDim.x) {
-      float s = sums[c];
-      for (int k = 1; k < groups; ++k) s += sums[c + k * tpr * E];
-      part[pass * a.cols + c] = s;
-    }
+    part[c] = s;
+    part[a.cols + c] = u;
   }
 }
 
@@ -753,14 +764,19 @@ template <typename T, typename W, int VEC, int E>
 cudaError_t ln_backward_e(const LnBwd<T, W>& args, int32_t* parts, void* stream) {
   LnBwd<T, W> a = args;
   a.tpr = ln_tpr(a.cols, E);
-  const int groups = a.tpr > 256 ? 1 : 256 / a.tpr, threads = groups * a.tpr;
+  // Wide rows: one block of 512 threads an SM, half as many parts (8192 x 2048
+  // bf16: 24.6 us, and 25.7 with two of 256); narrow ones the other way round
+  // (65536 x 128: 15.0 and 15.5).
+  const int want = a.tpr >= 64 ? LN_BWD_THREADS : LN_BWD_THREADS / 2;
+  const int groups = want / a.tpr, threads = groups * a.tpr;
+  const int64_t most_parts = a.tpr >= 64 ? LN_PARTS / 2 : LN_PARTS;
   int64_t grid = (a.rows + groups - 1) / groups;
-  if (grid > LN_PARTS) grid = LN_PARTS;
+  if (grid > most_parts) grid = most_parts;
   if (grid < 1) grid = 1;
   *parts = static_cast<int32_t>(grid);
   using R = Ring<T, VEC, E>;
   constexpr int SLOTS = ring_slots(2 * R::BYTES);
-  const size_t sums = size_t(threads) * E * 4;  // the groups' sums at the end, in the ring's place
+  const size_t sums = size_t(threads) * E * 8;  // the groups' sums at the end, in the ring's place
   const size_t ring = LN_RED_BYTES + size_t(SLOTS) * 2 * (threads * R::BYTES + groups * R::EXTRA);
   constexpr int most = LN_RED_BYTES + SLOTS * 2 * LN_BWD_THREADS * (R::BYTES + R::EXTRA / 4);
   static_assert(most <= 227 * 1024, "shared memory of a block");

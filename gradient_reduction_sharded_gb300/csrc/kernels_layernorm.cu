@@ -682,7 +682,8 @@ struct LnLd {
 
 grs_status check_norm(const grs_norm* s, const char* who, LnLd* ld) {
   if (s == nullptr) return api_fail(GRS_ERR_INVALID_ARG, who, "shape is NULL");
-  if (s->rows < 0 || s->cols < 1) return api_fail(GRS_ERR_SHAPE, who, "rows must be >= 0 and cols >= 1");
+  if (s->rows < 0 || s->cols < 1 || s->cols > GRS_MAX_WIDTH)
+    return api_fail(GRS_ERR_SHAPE, who, "rows must be >= 0 and cols in [1, GRS_MAX_WIDTH]");
   if (!dtype_ok(s->dtype) || !dtype_ok(s->param_dtype) || !dtype_ok(s->grad_dtype))
     return api_fail(GRS_ERR_INVALID_ARG, who, "unknown element type");
   if (!(s->eps >= 0.0f) || std::isinf(s->eps)) return api_fail(GRS_ERR_INVALID_ARG, who, "eps must be finite and >= 0");

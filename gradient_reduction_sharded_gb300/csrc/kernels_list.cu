@@ -672,7 +672,7 @@ grs_status grs_tensors_create(const int64_t* numels, int32_t n_tensors, uint32_t
       if (e == cudaSuccess) e = cudaStreamSynchronize(nullptr);  // cleared before any launch on any stream
       if (e == cudaSuccess) l->device = dev;
     }
-  } catch (const std::bad_alloc&) {
+  } catch (...) {  // no memory for the tables
     if (l != nullptr) {
       cudaFree(l->d_tiles);
       cudaFree(l->d_flags);

@@ -386,7 +386,8 @@ __global__ void __launch_bounds__(MOE_THREADS) moe_combine_bwd_kernel(const __gr
 
 grs_status check_moe(const grs_moe* s, const char* who) {
   if (s == nullptr) return api_fail(GRS_ERR_INVALID_ARG, who, "shape is NULL");
-  if (s->tokens < 0 || s->top_k < 1 || s->hidden < 1) return api_fail(GRS_ERR_SHAPE, who, "tokens >= 0, top_k >= 1, hidden >= 1");
+  if (s->tokens < 0 || s->top_k < 1 || s->hidden < 1 || s->hidden > GRS_MAX_WIDTH)
+    return api_fail(GRS_ERR_SHAPE, who, "tokens must be >= 0, top_k >= 1 and hidden in [1, GRS_MAX_WIDTH]");
   if (s->tokens > INT32_MAX / s->top_k) return api_fail(GRS_ERR_SHAPE, who, "tokens * top_k must be below 2^31");
   if (s->expert_begin < 0 || s->expert_end <= s->expert_begin)
     return api_fail(GRS_ERR_INVALID_ARG, who, "the expert range must be 0 <= begin < end");
@@ -468,7 +469,7 @@ cudaError_t moe_launch(MoeOp op, MoeArgs<T> a, void* stream) {
 cudaError_t moe_run(MoeOp op, const grs_moe* s, const void* a, const void* b, void* o, const int32_t* slot_row,
                     const float* weights, float* dweights, void* stream) {
   const bool whole = moe_whole(s, a, b, o);
-  if (op == MoeOp::kDispatch && whole && s->dtype == GRS_DTYPE_FP32 && s->hidden <= INT32_MAX / 2) {
+  if (op == MoeOp::kDispatch && whole && s->dtype == GRS_DTYPE_FP32) {
     // A copy of bytes: 16 a thread and row.
     MoeArgs<uint16_t> x = moe_args<uint16_t>(s, a, b, o, slot_row, weights, dweights, whole);
     x.d *= 2;

@@ -38,6 +38,7 @@ GRS_SMALL_MAX_BUFFERS = 256
 GRS_DTYPE_BF16, GRS_DTYPE_FP32 = 0, 1
 GRS_STATE_BLOCK = 256
 GRS_MOE_MAX_EXPERTS = 1024
+GRS_MAX_WIDTH = 1 << 30
 
 STATUS_NAMES = {0: "OK", 1: "INVALID_ARG", 2: "UNSUPPORTED_COMPOSITION", 3: "SHAPE",
                 4: "ALIGNMENT", 5: "CUDA", 6: "TIMEOUT", 7: "NONFINITE", 8: "NO_DEVICE",

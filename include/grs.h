@@ -706,6 +706,8 @@ grs_status grs_tensors_check_device_errors(const grs_tensors* list, void* stream
 
 /* ------------------------------------------------------------ layer norm */
 
+#define GRS_MAX_WIDTH 1073741824 /* columns of a norm, elements of a token's vector */
+
 /* Layer norm over the rows of a matrix, forward and backward.  The weight's
  * gradient of a norm over a sequence- or head-sharded activation is the
  * PARTIAL_SUM parameter of [ISSUE] "Why this needs separate work"; it is
@@ -717,7 +719,7 @@ typedef struct grs_norm {
   int64_t ld_y;
   int64_t ld_dy;
   int64_t ld_dx;
-  int32_t cols;          /* C >= 1 */
+  int32_t cols;          /* C, 1..GRS_MAX_WIDTH */
   float eps;             /* >= 0 */
   int32_t dtype;         /* grs_dtype of x, y, dy, dx */
   int32_t param_dtype;   /* of w and b */
@@ -761,7 +763,7 @@ typedef struct grs_moe {
   int32_t top_k;         /* >= 1 */
   int32_t expert_begin;
   int32_t expert_end;
-  int32_t hidden;        /* elements of a token's vector, >= 1 */
+  int32_t hidden;        /* elements of a token's vector, 1..GRS_MAX_WIDTH */
   int32_t dtype;         /* grs_dtype of the vectors */
   int32_t reserved;
 } grs_moe;

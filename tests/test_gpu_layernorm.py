@@ -238,7 +238,7 @@ def test_refusals(grs):
     mk = lambda rows=4, cols=32, eps=1e-5, dt=1, pd=1, gd=1, **ld: grs.make_norm(rows, cols, eps, dt, pd, gd, **ld)  # noqa: E731
     fwd = lambda s, x=p, w=p, y=p: grs.grs_layernorm_forward(s, x, w, None, y, None, None, 0)  # noqa: E731
     bwd = lambda s, dy=p, mean=p, dw=p, ws=p, dx=p: grs.grs_layernorm_backward(s, dy, p, p, mean, p, dx, dw, None, ws, 0)  # noqa: E731
-    for call, status in ((lambda: fwd(mk(rows=-1)), sh), (lambda: fwd(mk(cols=0)), sh), (lambda: fwd(mk(ld_x=31)), sh), (lambda: fwd(mk(ld_dx=-1)), sh),
+    for call, status in ((lambda: fwd(mk(rows=-1)), sh), (lambda: fwd(mk(cols=0)), sh), (lambda: fwd(mk(cols=(1 << 30) + 1)), sh), (lambda: fwd(mk(ld_x=31)), sh), (lambda: fwd(mk(ld_dx=-1)), sh),
                          (lambda: fwd(mk(eps=-1.0)), inv), (lambda: fwd(mk(eps=float("nan"))), inv), (lambda: fwd(mk(dt=2)), inv),
                          (lambda: fwd(mk(pd=-1)), inv), (lambda: fwd(mk(gd=9)), inv), (lambda: fwd(mk(), x=None), inv),
                          (lambda: fwd(mk(), y=None), inv), (lambda: fwd(mk(), x=p + 2), ali), (lambda: fwd(mk(), w=p + 1), ali),

@@ -92,6 +92,7 @@ class List:
 
     def close(self):
         torch.cuda.synchronize()
+        assert self.grs.grs_tensors_check_device_errors(self.h, self.stream()) != self.grs.GRS_ERR_BOUNDS
         self.grs.grs_tensors_destroy(self.h)
 
 
@@ -357,6 +358,90 @@ def test_zero_and_tiny_and_nonfinite_blocks(grs):
     assert np.isnan(got[1][2]) and np.isnan(got[3][2]) and (got[0][2 * B:3 * B] == 0).all()
     assert np.isnan(p[2 * B + 3]) and np.isfinite(np.delete(p[2 * B:3 * B], 3)).all()
     assert got[2][3 * B + 9] == 1  # never zero
+    t.close()
+
+
+def test_magnitudes_over_the_whole_range(grs):
+    """Blocks whose moments are huge (beyond one scaling product) and tiny (at the smallest scale): the codes bit for bit."""
+    factors = [1e18, 1e10, 1.0, 1e-10, 1e-18, 3e-36]
+    t = List(grs, [len(factors) * B], seed=14)
+    g = t.g * np.repeat(np.array(factors, np.float32), B)
+    t.store[0][:t.n] = torch.from_numpy(g).cuda()
+    st = [np.zeros(t.n, np.uint8), np.zeros(t.n // B, np.float32), np.zeros(t.n, np.uint8), np.zeros(t.n // B, np.float32)]
+    hp = grs.make_adamw(*HP.values(), 0.0, 1, 1)
+    got = run8(grs, t, st, hp, 77)
+    F = np.float32
+    m = g * F(1 - float(F(0.9)))
+    s = np.sqrt((g * F(1 - float(F(0.999)))) * g)
+    bits = random_bits(t.n, 77)
+    for x, code, scale, r16, pos in ((m, got[0], got[1], bits & 0xFFFF, False), (s, got[2], got[3], bits >> 16, True)):
+        val, sc = to8(x, r16, pos)
+        assert np.array_equal(e4m3(code), val) and np.array_equal(scale, sc)
+    assert np.isfinite(t.master.cpu().numpy()).all()
+    t.close()
+
+
+def test_indexes_beyond_32_bits(grs):
+    """A tensor of more than 2^32 elements: its last blocks' states, whose random numbers take the high word, and its norm."""
+    n = (1 << 32) + 5000
+    h = grs.grs_tensors_create([n])
+    info = grs.grs_tensors_query(h)
+    N = info["n_state"]
+    free = torch.cuda.mem_get_info()[0]
+    if free < 12 * N:
+        pytest.skip("needs about 52 GB of device memory")
+    g = torch.zeros(N, dtype=torch.bfloat16, device="cuda")
+    master = torch.zeros(N, device="cuda")
+    m8, s8 = torch.zeros(N, dtype=torch.uint8, device="cuda"), torch.zeros(N, dtype=torch.uint8, device="cuda")
+    ms, ss = torch.zeros(N // B, device="cuda"), torch.zeros(N // B, device="cuda")
+    lo = N - 4096 - B
+    tail = torch.randn(n - lo, generator=torch.Generator().manual_seed(1)).mul(1e-2).to(torch.bfloat16)
+    g[lo:n] = tail.cuda()
+    table = lambda x: torch.tensor([x.data_ptr()], dtype=torch.int64, device="cuda")  # noqa: E731
+    gp = table(g)
+    ws = torch.zeros(info["workspace_bytes"], dtype=torch.uint8, device="cuda")
+    norm = torch.zeros(1, dtype=torch.float64, device="cuda")
+    st = torch.cuda.current_stream().cuda_stream
+    grs.grs_tensors_norm_sq(h, gp.data_ptr(), grs.GRS_DTYPE_BF16, 1, ws.data_ptr(), norm.data_ptr(), st)
+    hp = grs.make_adamw(*HP.values(), 0.0, 1, 1)
+    grs.grs_tensors_adamw8_step(h, hp, 5, None, gp.data_ptr(), grs.GRS_DTYPE_BF16, master.data_ptr(), m8.data_ptr(), ms.data_ptr(),
+                                s8.data_ptr(), ss.data_ptr(), None, st)
+    torch.cuda.synchronize()
+    x = np.zeros(N - lo, np.float32)
+    x[:n - lo] = tail.float().numpy()
+    want = float(np.sum(x.astype(np.float64) ** 2))
+    assert abs(float(norm.cpu()[0]) - want) <= 22 * 2.0 ** -24 * want
+    idx = np.arange(lo, N, dtype=np.uint64)
+    k0 = mix(5 + 0x9E3779B9 & 0xFFFFFFFF)
+    k1 = mix(k0)
+    y = (idx & np.uint64(0xFFFFFFFF)) ^ np.uint64(k0) ^ ((idx >> np.uint64(32)) * np.uint64(0x6A09E667) & np.uint64(0xFFFFFFFF))
+    y = ((y ^ y >> np.uint64(16)) * np.uint64(0x9E3779B9) & np.uint64(0xFFFFFFFF)) ^ np.uint64(k1)
+    y = (y ^ y >> np.uint64(15)) * np.uint64(0xBB67AE85) & np.uint64(0xFFFFFFFF)
+    bits = (y ^ y >> np.uint64(16)).astype(np.int64)
+    F = np.float32
+    m = x * F(1 - float(F(0.9)))
+    s = np.sqrt((x * F(1 - float(F(0.999)))) * x)
+    for v, code, scale, r16, pos in ((m, m8, ms, bits & 0xFFFF, False), (s, s8, ss, bits >> 16, True)):
+        val, sc = to8(v, r16, pos)
+        assert np.array_equal(e4m3(code[lo:].cpu().numpy()), val)
+        assert np.array_equal(scale[lo // B:].cpu().numpy(), sc)
+    want = step64(x, np.zeros(N - lo), np.zeros(N - lo), np.zeros(N - lo), 1, 1.0, 1)[0]
+    assert np.abs(master[lo:].cpu().numpy() - want).max() <= ATOL + RTOL * np.abs(want).max()
+    assert int(m8[:lo].max()) == 0 and float(master[:1 << 20].abs().max()) == 0
+    grs.grs_tensors_destroy(h)
+    del g, master, m8, s8
+    torch.cuda.empty_cache()
+
+
+def test_only_empty_tensors(grs):
+    t = List(grs, [0, 0])
+    t.norm.fill_(5.0)
+    grs.grs_tensors_norm_sq(t.h, t.gp.data_ptr(), t.dt, 1, t.ws.data_ptr(), t.norm.data_ptr(), t.stream())
+    assert float(t.norm.cpu()[0]) == 0.0
+    hp = grs.make_adamw(*HP.values(), 1.0, 1, 1)
+    x = torch.zeros(16, device="cuda").data_ptr()
+    grs.grs_tensors_adamw_step(t.h, hp, t.norm.data_ptr(), t.gp.data_ptr(), t.dt, x, x, x, t.pp.data_ptr(), t.stream())
+    grs.grs_tensors_adamw8_step(t.h, hp, 1, t.norm.data_ptr(), t.gp.data_ptr(), t.dt, x, x, x, x, x, t.pp.data_ptr(), t.stream())
     t.close()
 
 

@@ -200,6 +200,39 @@ def test_gradients_against_differences(grs):
         assert abs((up - down) / (2 * step) - want) <= 1e3 * 16 * EPS32 / step
 
 
+def test_rows_beyond_32_bits_of_elements(grs):
+    """More than 2^31 elements of rows: the last tokens' rows, there and back."""
+    tokens, k, d = 132000, 8, 2048
+    s = grs.make_moe(tokens, k, 32, 0, 32, d, 0)
+    rows = torch.arange(tokens * k, dtype=torch.int32, device="cuda").view(k, tokens).t().contiguous().view(-1)  # spread over all
+    x = torch.zeros(tokens, d, dtype=torch.bfloat16, device="cuda")
+    x[-50:] = torch.randn(50, d, generator=torch.Generator(device="cuda").manual_seed(1), device="cuda").to(torch.bfloat16)
+    xs = torch.full((tokens * k, d), 3.0, dtype=torch.bfloat16, device="cuda")
+    grs.grs_moe_dispatch(s, x.data_ptr(), rows.data_ptr(), xs.data_ptr(), stream())
+    last = rows.view(tokens, k)[-50:].long()
+    assert torch.equal(xs[last], x[-50:, None, :].expand(50, k, d))
+    assert int((xs[rows.view(tokens, k)[:-50].reshape(-1)[::997].long()] != 0).sum()) == 0
+    y = torch.empty_like(x)
+    grs.grs_moe_dispatch_backward(s, xs.data_ptr(), rows.data_ptr(), y.data_ptr(), stream())
+    assert torch.equal(y[-50:], (x[-50:].float() * k).to(torch.bfloat16))
+    del xs, x, y
+    torch.cuda.empty_cache()
+
+
+def test_a_copy_keeps_every_bit(grs):
+    """dispatch moves NaN payloads and signed zeros as they are, in both types and at any alignment."""
+    for dt, code, word in ((torch.bfloat16, 0, torch.int16), (torch.float32, 1, torch.int32)):
+        for d in (64, 67):
+            g = torch.Generator(device="cuda").manual_seed(d)
+            info = torch.iinfo(word)
+            bits = torch.randint(info.min, info.max, (5, d), generator=g, device="cuda").to(word)
+            s = grs.make_moe(5, 2, 4, 0, 4, d, code)
+            rows = torch.randperm(10, generator=g, device="cuda").to(torch.int32)
+            xs = torch.zeros(10, d, dtype=word, device="cuda")
+            grs.grs_moe_dispatch(s, bits.data_ptr(), rows.data_ptr(), xs.data_ptr(), stream())
+            assert torch.equal(xs[rows.long()], bits.repeat_interleave(2, 0))
+
+
 def test_no_tokens(grs):
     s = grs.make_moe(0, 2, 4, 0, 4, 16, 0)
     off = torch.full((5,), -1, dtype=torch.int32, device="cuda")
@@ -217,7 +250,7 @@ def test_refusals(grs):
     inv, sh, ali = grs.GRS_ERR_INVALID_ARG, grs.GRS_ERR_SHAPE, grs.GRS_ERR_ALIGNMENT
     raw = lambda tokens=4, k=2, b=0, e=4, d=16, dt=1: grs.grs_moe(tokens, k, b, e, d, dt, 0)  # noqa: E731
     disp = lambda s, x=p, r=p, y=p: grs.grs_moe_dispatch(s, x, r, y, 0)  # noqa: E731
-    for call, status in ((lambda: disp(raw(tokens=-1)), sh), (lambda: disp(raw(k=0)), sh), (lambda: disp(raw(d=0)), sh),
+    for call, status in ((lambda: disp(raw(tokens=-1)), sh), (lambda: disp(raw(k=0)), sh), (lambda: disp(raw(d=0)), sh), (lambda: disp(raw(d=(1 << 30) + 8)), sh),
                          (lambda: disp(raw(tokens=1 << 31)), sh), (lambda: disp(raw(tokens=1 << 30, k=2)), sh),
                          (lambda: disp(raw(b=-1)), inv), (lambda: disp(raw(b=4)), inv), (lambda: disp(raw(e=1025)), sh), (lambda: disp(raw(dt=2)), inv),
                          (lambda: disp(raw(), x=None), inv), (lambda: disp(raw(), r=None), inv), (lambda: disp(raw(), y=p + 2), ali),

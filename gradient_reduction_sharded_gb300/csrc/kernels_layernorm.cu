@@ -21,7 +21,7 @@ namespace grs {
 namespace {
 
 constexpr int LN_THREADS = 256;
-constexpr int LN_RING_THREADS = 256; // a block of the forward ring at most; two blocks an SM
+constexpr int LN_RING_THREADS = 512; // a block of the forward ring at most
 constexpr int LN_RED_BYTES = 256;    // two float2 a warp of a block, twice
 constexpr int LN_BWD_THREADS = 512;  // a block of the backward pass at most
 constexpr int LN_PARTS = 304;        // partial rows of dw and db at most: two blocks an SM
@@ -382,7 +382,7 @@ __device__ __forceinline__ Matrix matrix_of(const T* p, int64_t ld, int64_t rows
 // of the whole grid, the parameters in registers and the rows to come in
 // flight in shared memory.
 template <typename T, typename W, int VEC, int E>
-__global__ void __launch_bounds__(LN_RING_THREADS, 2) ln_fwd_ring_kernel(const __grid_constant__ LnFwd<T, W> a) {
+__global__ void __launch_bounds__(LN_RING_THREADS) ln_fwd_ring_kernel(const __grid_constant__ LnFwd<T, W> a) {
   extern __shared__ __align__(16) uint8_t ring[];
   __shared__ float2 red[2 * (LN_RING_THREADS / 32)];
   pdl_wait();
@@ -442,7 +442,8 @@ struct LnBwd {
 // thread keeps its columns' dw and db in registers over all its rows, and the
 // block adds its groups' sums in shared memory into one part.  The next row
 // is in flight while a row is worked on.
-template <typename T, typename W, int VEC, int E>
+// Without kParams the sums over the rows are left out (and E may be larger).
+template <typename T, typename W, int VEC, int E, bool kParams>
 __global__ void __launch_bounds__(LN_BWD_THREADS) ln_bwd_kernel(const __grid_constant__ LnBwd<T, W> a) {
   extern __shared__ __align__(16) float sums[];  // the groups' warp sums and the ring; the parts' sums after it
   pdl_wait();
@@ -507,8 +508,10 @@ __global__ void __launch_bounds__(LN_BWD_THREADS) ln_bwd_kernel(const __grid_con
       dh[i] = mul2(d, w[i]);
       s1 = add2(s1, dh[i]);
       s2 = fma2(dh[i], h[i], s2);
-      dw[i] = fma2(d, h[i], dw[i]);
-      db[i] = add2(db[i], d);
+      if constexpr (kParams) {
+        dw[i] = fma2(d, h[i], dw[i]);
+        db[i] = add2(db[i], d);
+      }
     }
     if (dx != nullptr) {
       float c1 = s1.x + s1.y, c2 = s2.x + s2.y;
@@ -529,7 +532,7 @@ __global__ void __launch_bounds__(LN_BWD_THREADS) ln_bwd_kernel(const __grid_con
     rstd_1 = rstd_2;
   }
   ring_wait<0>();  // no copy outlives the slots
-  if (a.parts == nullptr) return;
+  if constexpr (!kParams) return;
   // The groups' sums meet in the ring's place: [dw or db][group][tpr * E].
   const int wide = tpr * E, half = groups * wide;
   __syncthreads();
@@ -560,6 +563,9 @@ __global__ void __launch_bounds__(LN_BWD_THREADS) ln_bwd_kernel(const __grid_con
 }
 
 // ------------------------------------------------ any width, any alignment
+template <typename T>
+constexpr int ln_dparam_cols = 16 / static_cast<int>(sizeof(T));
+
 // One block a row, the row read again for each pass (it is in L2 by then).
 template <typename T, typename W>
 __global__ void __launch_bounds__(LN_THREADS) ln_fwd_any_kernel(const T* __restrict__ x, int64_t ld_x, const W* __restrict__ w,
@@ -623,27 +629,82 @@ __global__ void __launch_bounds__(LN_THREADS) ln_dx_any_kernel(const T* __restri
   }
 }
 
-// Partial sums of dw and db: part blockIdx.y takes rows blockIdx.y,
-// blockIdx.y + parts, ..., a thread one column.
-template <typename T>
-__global__ void __launch_bounds__(LN_THREADS) ln_dparam_any_kernel(const T* __restrict__ dy, int64_t ld_dy,
-                                                                   const T* __restrict__ x, int64_t ld_x,
-                                                                   const float* __restrict__ mean_in,
-                                                                   const float* __restrict__ rstd_in,
-                                                                   float* __restrict__ parts, int64_t rows, int32_t cols) {
+// Parts of dw and db alone.  A block has a strip of 32 N columns, a lane N of
+// them: N next to each other (kWhole, one 16-byte chunk of each row) or 32
+// apart.  Part blockIdx.y and its warps share the rows, some of a warp's in
+// flight at once; the warps' sums meet in shared memory.
+template <typename T, bool kWhole>
+__global__ void __launch_bounds__(LN_THREADS) ln_dparam_kernel(const T* __restrict__ dy, int64_t ld_dy, const T* __restrict__ x,
+                                                               int64_t ld_x, const float* __restrict__ mean_in,
+                                                               const float* __restrict__ rstd_in, float* __restrict__ parts,
+                                                               int64_t rows, int32_t cols) {
+  constexpr int WARPS = LN_THREADS / 32, N = ln_dparam_cols<T>, ROWS = kWhole ? 4 : 2;
+  __shared__ float red[2][WARPS][32 * N];
   pdl_wait();
   pdl_trigger();
-  const int64_t c = int64_t(blockIdx.x) * LN_THREADS + threadIdx.x;
-  if (c >= cols) return;
-  float dw = 0.0f, db = 0.0f;
-  for (int64_t row = blockIdx.y; row < rows; row += gridDim.y) {
-    const float g = ln_load(dy + row * ld_dy + c);
-    dw = fmaf(g, (ln_load(x + row * ld_x + c) - mean_in[row]) * rstd_in[row], dw);
-    db += g;
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const int c = blockIdx.x * (32 * N) + (kWhole ? lane * N : lane);
+  float dw[N], db[N];
+#pragma unroll
+  for (int q = 0; q < N; ++q) dw[q] = db[q] = 0.0f;
+  const int64_t step = int64_t(gridDim.y) * WARPS;
+  for (int64_t row = int64_t(blockIdx.y) * WARPS + w; row < rows; row += ROWS * step) {
+    float g[ROWS][N], v[ROWS][N], mean[ROWS], rstd[ROWS];
+    uint4 gw[ROWS], vw[ROWS];
+#pragma unroll
+    for (int k = 0; k < ROWS; ++k) {
+      const int64_t r = row + k * step;
+      const bool on = r < rows;
+      mean[k] = on ? __ldg(mean_in + r) : 0.0f;
+      rstd[k] = on ? __ldg(rstd_in + r) : 0.0f;
+      const T *gr = dy + (on ? r : 0) * ld_dy + c, *xr = x + (on ? r : 0) * ld_x + c;
+      if constexpr (kWhole) {
+        gw[k] = vw[k] = make_uint4(0, 0, 0, 0);
+        if (on && c < cols) {
+          gw[k] = *reinterpret_cast<const uint4*>(gr);
+          vw[k] = *reinterpret_cast<const uint4*>(xr);
+        }
+      } else {
+#pragma unroll
+        for (int q = 0; q < N; ++q) {
+          const bool in = on && c + 32 * q < cols;
+          g[k][q] = in ? ln_load(gr + 32 * q) : 0.0f;
+          v[k][q] = in ? ln_load(xr + 32 * q) : 0.0f;
+        }
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < ROWS; ++k) {
+      if constexpr (kWhole) {
+        const uint32_t a[4] = {gw[k].x, gw[k].y, gw[k].z, gw[k].w}, b[4] = {vw[k].x, vw[k].y, vw[k].z, vw[k].w};
+#pragma unroll
+        for (int q = 0; q < N; ++q) {
+          g[k][q] = sizeof(T) == 4 ? __uint_as_float(a[q & 3]) : (q & 1 ? bf16_hi(a[q / 2]) : bf16_lo(a[q / 2]));
+          v[k][q] = sizeof(T) == 4 ? __uint_as_float(b[q & 3]) : (q & 1 ? bf16_hi(b[q / 2]) : bf16_lo(b[q / 2]));
+        }
+      }
+#pragma unroll
+      for (int q = 0; q < N; ++q) {
+        dw[q] = fmaf(g[k][q], (v[k][q] - mean[k]) * rstd[k], dw[q]);
+        db[q] += g[k][q];
+      }
+    }
   }
+#pragma unroll
+  for (int q = 0; q < N; ++q) {
+    red[0][w][lane + 32 * q] = dw[q];
+    red[1][w][lane + 32 * q] = db[q];
+  }
+  __syncthreads();
   float* p = parts + int64_t(blockIdx.y) * 2 * cols;
-  p[c] = dw;
-  p[cols + c] = db;
+  for (int i = threadIdx.x; i < 2 * 32 * N; i += LN_THREADS) {
+    const int k = i / (32 * N), at = i - k * (32 * N);
+    const int64_t col = int64_t(blockIdx.x) * (32 * N) + (kWhole ? (at & 31) * N + at / 32 : at);
+    if (col >= cols) continue;
+    float s = red[k][0][at];
+    for (int j = 1; j < WARPS; ++j) s += red[k][j][at];
+    p[k * int64_t(cols) + col] = s;
+  }
 }
 
 // dw and db from the parts, in a fixed order.  A block takes 32 of the 2 C
@@ -711,7 +772,7 @@ cudaError_t ln_forward_e(const LnFwd<T, W>& args, void* stream) {
   LnFwd<T, W> a = args;
   a.tpr = ln_tpr(a.cols, E);
   if constexpr (kRing) {
-    const int groups = LN_RING_THREADS / a.tpr, threads = groups * a.tpr;
+    const int groups = a.tpr > 256 ? 1 : 256 / a.tpr, threads = groups * a.tpr;
     int64_t grid = (a.rows + groups - 1) / groups;
     // Two blocks an SM; one for an fp32 matrix beyond L2: 65536 x 1024 takes 82 us
     // with one and 94 with two (8192 x 1024 the other way round, 14.1 and 13.0).
@@ -719,7 +780,9 @@ cudaError_t ln_forward_e(const LnFwd<T, W>& args, void* stream) {
     if (grid > most) grid = most;
     using R = Ring<T, VEC, E>;
     constexpr int SLOTS = ring_slots(R::BYTES);
-    const cudaError_t e = allow_smem<ln_fwd_ring_kernel<T, W, VEC, E>>(SLOTS * LN_RING_THREADS * (R::BYTES + R::EXTRA));
+    constexpr int ring_most = SLOTS * LN_RING_THREADS * (R::BYTES + R::EXTRA / 2);  // (at most 256 groups)
+    static_assert(ring_most <= 226 * 1024, "shared memory of a block");
+    const cudaError_t e = allow_smem<ln_fwd_ring_kernel<T, W, VEC, E>>(ring_most);
     if (e != cudaSuccess) return e;
     return launch_pdl(ln_fwd_ring_kernel<T, W, VEC, E>, dim3(static_cast<unsigned>(grid)), dim3(threads),
                     size_t(SLOTS) * (threads * R::BYTES + groups * R::EXTRA), stream, a);
@@ -737,13 +800,17 @@ cudaError_t ln_forward_e(const LnFwd<T, W>& args, void* stream) {
 template <typename T, typename W, int VEC>
 cudaError_t ln_forward_vec(const LnFwd<T, W>& a, void* stream, bool* done) {
   const int t8 = ln_tpr(a.cols, 8), t16 = ln_tpr(a.cols, 16);
-  *done = a.rows <= INT32_MAX && t16 <= 1024;
-  if (!*done) return cudaSuccess;
-  if constexpr (VEC == 8)
-    if (a.rows >= 4096 && ln_tpr(a.cols, 32) <= LN_RING_THREADS) return ln_forward_e<T, W, VEC, 32, true>(a, stream);
-  if (a.rows > 1216 && t16 <= LN_RING_THREADS) return ln_forward_e<T, W, VEC, 16, true>(a, stream);
-  if (t8 <= 1024) return ln_forward_e<T, W, VEC, 8, false>(a, stream);
-  return ln_forward_e<T, W, VEC, 16, false>(a, stream);
+  const int t32 = ln_tpr(a.cols, 32);
+  *done = true;
+  if (a.rows > 1216 || t16 > 1024) {
+    const bool wide = sizeof(T) == 2 ? a.rows >= 4096 || t16 > LN_RING_THREADS : t16 > LN_RING_THREADS;
+    if (!wide) return ln_forward_e<T, W, VEC, 16, true>(a, stream);
+    if (t32 <= LN_RING_THREADS) return ln_forward_e<T, W, VEC, 32, true>(a, stream);
+  }
+  if (a.rows <= INT32_MAX && t8 <= 1024) return ln_forward_e<T, W, VEC, 8, false>(a, stream);
+  if (a.rows <= INT32_MAX && t16 <= 1024) return ln_forward_e<T, W, VEC, 16, false>(a, stream);
+  *done = false;
+  return cudaSuccess;
 }
 
 template <typename T, typename W>
@@ -761,7 +828,7 @@ cudaError_t ln_forward(const grs_norm* s, const LnLd& ld, const void* x, const v
                   s->rows, s->cols, s->eps);
 }
 
-template <typename T, typename W, int VEC, int E>
+template <typename T, typename W, int VEC, int E, bool kParams>
 cudaError_t ln_backward_e(const LnBwd<T, W>& args, int32_t* parts, void* stream) {
   LnBwd<T, W> a = args;
   a.tpr = ln_tpr(a.cols, E);
@@ -781,17 +848,30 @@ cudaError_t ln_backward_e(const LnBwd<T, W>& args, int32_t* parts, void* stream)
   const size_t ring = LN_RED_BYTES + size_t(SLOTS) * 2 * (threads * R::BYTES + groups * R::EXTRA);
   constexpr int most = LN_RED_BYTES + SLOTS * 2 * LN_BWD_THREADS * (R::BYTES + R::EXTRA / 4);
   static_assert(most <= 227 * 1024, "shared memory of a block");
-  const cudaError_t e = allow_smem<ln_bwd_kernel<T, W, VEC, E>>(most);
+  const cudaError_t e = allow_smem<ln_bwd_kernel<T, W, VEC, E, kParams>>(most);
   if (e != cudaSuccess) return e;
-  return launch_pdl(ln_bwd_kernel<T, W, VEC, E>, dim3(static_cast<unsigned>(grid)), dim3(threads), ring > sums ? ring : sums, stream, a);
+  return launch_pdl(ln_bwd_kernel<T, W, VEC, E, kParams>, dim3(static_cast<unsigned>(grid)), dim3(threads), ring > sums ? ring : sums, stream, a);
 }
 
+// dx, and the parts of dw and db (their number in *parts; 0: not done).
 template <typename T, typename W, int VEC>
-cudaError_t ln_backward_vec(const LnBwd<T, W>& a, int32_t* parts, void* stream) {
+cudaError_t ln_backward_vec(const LnBwd<T, W>& a, int32_t* parts, bool* dx_done, void* stream) {
   const int t8 = ln_tpr(a.cols, 8), t16 = ln_tpr(a.cols, 16);
+  *dx_done = true;
   // Fewer elements a thread where registers are short (fp32) or rows few.
-  if ((a.rows <= LN_PARTS || sizeof(T) == 4) && t8 <= LN_BWD_THREADS) return ln_backward_e<T, W, VEC, 8>(a, parts, stream);
-  if (t16 <= LN_BWD_THREADS) return ln_backward_e<T, W, VEC, 16>(a, parts, stream);
+  const bool eight = (a.rows <= LN_PARTS || sizeof(T) == 4) && t8 <= LN_BWD_THREADS;
+  if (a.parts != nullptr) {
+    if (eight) return ln_backward_e<T, W, VEC, 8, true>(a, parts, stream);
+    if (t16 <= LN_BWD_THREADS) return ln_backward_e<T, W, VEC, 16, true>(a, parts, stream);
+  }
+  int32_t unused = 0;
+  if (a.dx != nullptr && a.rows > 0) {
+    if (eight) return ln_backward_e<T, W, VEC, 8, false>(a, &unused, stream);
+    if (t16 <= LN_BWD_THREADS) return ln_backward_e<T, W, VEC, 16, false>(a, &unused, stream);
+    if constexpr (sizeof(T) == 2)  // (the ring of fp32 rows would not fit)
+      if (ln_tpr(a.cols, 32) <= LN_BWD_THREADS) return ln_backward_e<T, W, VEC, 32, false>(a, &unused, stream);
+  }
+  *dx_done = false;
   return cudaSuccess;
 }
 
@@ -806,18 +886,27 @@ cudaError_t ln_backward(const grs_norm* s, const LnLd& ld, const void* dy, const
   const bool vec = s->cols % VEC == 0 && rows16(x, ld.x, sizeof(T)) && rows16(dy, ld.dy, sizeof(T)) &&
                    (dx == nullptr || rows16(dx, ld.dx, sizeof(T))) && api_aligned(w, 16);
   int32_t parts = 0;
-  cudaError_t e = vec ? ln_backward_vec<T, W, VEC>(a, &parts, stream) : ln_backward_vec<T, W, 2>(a, &parts, stream);
+  bool dx_done = false;
+  cudaError_t e = vec ? ln_backward_vec<T, W, VEC>(a, &parts, &dx_done, stream) : ln_backward_vec<T, W, 2>(a, &parts, &dx_done, stream);
   if (e != cudaSuccess) return e;
-  if (parts == 0) {  // rows wider than the registers of a block
-    if (dx != nullptr && s->rows > 0) {
-      const unsigned grid = static_cast<unsigned>(s->rows < 1 << 20 ? s->rows : 1 << 20);
-      e = launch_pdl(ln_dx_any_kernel<T, W>, dim3(grid), dim3(LN_THREADS), 0, stream, a.dy, ld.dy, a.x, ld.x, a.w, mean, rstd, a.dx,
+  if (!dx_done && dx != nullptr && s->rows > 0) {  // rows wider than the registers of a block
+    const unsigned grid = static_cast<unsigned>(s->rows < 1 << 20 ? s->rows : 1 << 20);
+    e = launch_pdl(ln_dx_any_kernel<T, W>, dim3(grid), dim3(LN_THREADS), 0, stream, a.dy, ld.dy, a.x, ld.x, a.w, mean, rstd, a.dx,
                    ld.dx, s->rows, s->cols);
-    }
-    if (e != cudaSuccess || !params) return e;
-    parts = ln_parts(s->rows);
-    e = launch_pdl(ln_dparam_any_kernel<T>, dim3((unsigned(s->cols) + LN_THREADS - 1) / LN_THREADS, unsigned(parts)),
-                 dim3(LN_THREADS), 0, stream, a.dy, ld.dy, a.x, ld.x, mean, rstd, ws, s->rows, s->cols);
+    if (e != cudaSuccess) return e;
+  }
+  if (params && parts == 0) {
+    // A second pass over x and dy: enough strips of columns and parts of rows for eight blocks an SM.
+    constexpr int64_t strip = 32 * ln_dparam_cols<T>;
+    const int64_t strips = (s->cols + strip - 1) / strip;
+    int64_t most = (8 * 152 + strips - 1) / strips, have = (s->rows + LN_THREADS / 32 - 1) / (LN_THREADS / 32);
+    if (most > LN_PARTS) most = LN_PARTS;
+    if (have > most) have = most;
+    const int64_t limit = ln_parts(s->rows);
+    parts = static_cast<int32_t>(have < 1 ? 1 : have > limit ? limit : have);
+    const dim3 grid(static_cast<unsigned>(strips), static_cast<unsigned>(parts));
+    e = vec ? launch_pdl(ln_dparam_kernel<T, true>, grid, dim3(LN_THREADS), 0, stream, a.dy, ld.dy, a.x, ld.x, mean, rstd, ws, s->rows, s->cols)
+            : launch_pdl(ln_dparam_kernel<T, false>, grid, dim3(LN_THREADS), 0, stream, a.dy, ld.dy, a.x, ld.x, mean, rstd, ws, s->rows, s->cols);
     if (e != cudaSuccess) return e;
   }
   if (!params) return cudaSuccess;

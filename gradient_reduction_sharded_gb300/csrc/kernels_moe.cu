@@ -6,6 +6,16 @@
 // each slot, token by token: a token's vector is read (or written) once and
 // its rows are written (or read) once, with no atomics and no order left
 // open.
+//
+// The vectors' kernels are bound by memory.  A thread has 16 bytes (8 bf16 or
+// 8 fp32 elements) of a token and of all its rows, eight rows' loads in flight
+// before the first is used; with the conversion between the loads the compiler
+// waits for each (combine of 16384 tokens x 8 rows of 2048 bf16: 277 us against
+// 88).  At that size dispatch takes 89 us, combine and dispatch_backward 88 and
+// combine_backward 174, 6.6 to 6.9 TB/s of a copy rate of 6.78; 6001 x 6 rows
+// 27, 31 and 56 us.  The sort of those 131072 slots among 32 experts takes 8 us,
+// of 20 slots 2.6 (one launch), bound by latency.  Vectors of any other size
+// go as shifted chunks at 2 to 5 TB/s.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

@@ -342,24 +342,32 @@ __device__ __forceinline__ uint32_t warp_absmax(const float2 (&x)[4]) {
 // half-minus-one plus the last bit kept to nearest even.  The pattern is below
 // 2^27 (no code is above 0x78), the sign stays in bit 31.
 __device__ __forceinline__ void code_patterns(const float2 (&x)[4], const Scale& s, uint32_t (&t)[8]) {
+  float2 y[4];
+  // The scale is a power of two: one product gives the same number where its
+  // factor is normal (magnitudes up to 2^14; the same for the whole warp).
+  if (s.plain) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) y[q] = mul2(x[q], both(s.to_code));
+  } else {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) y[q] = mul2(mul2(x[q], both(s.inv)), both(0x1p-120f));
+  }
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
-    // The scale is a power of two: one product gives the same number where
-    // its factor is normal (magnitudes up to 2^14).
-    const float2 y = s.plain ? mul2(x[q], both(s.to_code)) : mul2(mul2(x[q], both(s.inv)), both(0x1p-120f));
-    t[2 * q] = __float_as_uint(y.x);
-    t[2 * q + 1] = __float_as_uint(y.y);
+    t[2 * q] = __float_as_uint(y[q].x);
+    t[2 * q + 1] = __float_as_uint(y[q].y);
   }
 }
 
-// Bytes of sign and code from the rounded patterns; zeros for a bad block.
+// Bytes of sign (if there is one) and code from the rounded patterns; zeros for a bad block.
+template <bool kSigned>
 __device__ __forceinline__ uint2 code_bytes(const uint32_t (&t)[8], bool bad) {
   uint32_t w[2];
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     uint32_t u[4];
 #pragma unroll
-    for (int q = 0; q < 4; ++q) u[q] = (t[4 * h + q] << 4) | (t[4 * h + q] & 0x80000000u);  // the code in the top byte
+    for (int q = 0; q < 4; ++q) u[q] = t[4 * h + q] << 4 | (kSigned ? t[4 * h + q] & 0x80000000u : 0u);  // the code in the top byte
     w[h] = bad ? 0u : __byte_perm(__byte_perm(u[0], u[1], 0x0073), __byte_perm(u[2], u[3], 0x0073), 0x5410);
   }
   return make_uint2(w[0], w[1]);
@@ -493,8 +501,8 @@ __global__ void __launch_bounds__(LIST_THREADS, 5) list_step_kernel(const __grid
       st[q] += (hi & 0xffff0u) + 8u;
     }
     keep_positive(V, st);
-    __stcs(reinterpret_cast<uint2*>(a.m8 + i), code_bytes(mt, ms.bad));
-    __stcs(reinterpret_cast<uint2*>(a.s8 + i), code_bytes(st, ss.bad));
+    __stcs(reinterpret_cast<uint2*>(a.m8 + i), code_bytes<true>(mt, ms.bad));
+    __stcs(reinterpret_cast<uint2*>(a.s8 + i), code_bytes<false>(st, ss.bad));
     if ((threadIdx.x & 31) == 0) {
       a.m_scale[i >> 8] = ms.scale;
       a.s_scale[i >> 8] = ss.scale;
@@ -563,8 +571,8 @@ __global__ void __launch_bounds__(LIST_THREADS) list_pack8_kernel(const __grid_c
   to_nearest(mt);
   to_nearest(st);
   keep_positive(V, st);
-  __stcs(reinterpret_cast<uint2*>(a.m8 + i), code_bytes(mt, ms.bad));
-  __stcs(reinterpret_cast<uint2*>(a.s8 + i), code_bytes(st, ss.bad));
+  __stcs(reinterpret_cast<uint2*>(a.m8 + i), code_bytes<true>(mt, ms.bad));
+  __stcs(reinterpret_cast<uint2*>(a.s8 + i), code_bytes<false>(st, ss.bad));
   if ((threadIdx.x & 31) == 0) {
     a.m_scale[i >> 8] = ms.scale;
     a.s_scale[i >> 8] = ss.scale;

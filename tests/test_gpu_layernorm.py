@@ -217,6 +217,33 @@ def test_nan_and_infinity_stay_in_their_row(grs, cols):
             assert torch.equal(got[r], clean[r])
 
 
+def test_on_another_stream_and_in_a_graph(grs):
+    """Both passes on a side stream, and replayed from a captured graph on new inputs: the same bits as on the default stream."""
+    c = Case(grs, 700, 2048, "bf16", "bf16", "bf16", seed=9)
+    want = [c.forward().clone(), *(t.clone() for t in c.backward())]
+    y, gx = torch.empty_like(c.x), torch.empty_like(c.x)
+    gw, gb = torch.empty_like(c.w), torch.empty_like(c.w)
+
+    def both(st):
+        grs.grs_layernorm_forward(c.shape, c.x.data_ptr(), c.w.data_ptr(), c.b.data_ptr(), y.data_ptr(), c.mean.data_ptr(), c.rstd.data_ptr(), st)
+        grs.grs_layernorm_backward(c.shape, c.dy.data_ptr(), c.x.data_ptr(), c.w.data_ptr(), c.mean.data_ptr(), c.rstd.data_ptr(), gx.data_ptr(),
+                                   gw.data_ptr(), gb.data_ptr(), c.ws.data_ptr(), st)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    both(side.cuda_stream)
+    side.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip((y, gx, gw, gb), want))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        both(stream())
+    c.x.copy_(c.x.flip(0))
+    c.dy.copy_(c.dy.flip(0))
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(y, want[0].flip(0)) and torch.equal(gx, want[1].flip(0))
+
+
 def test_rows_beyond_32_bits_of_elements(grs):
     """An offset past 2^31 elements: the last rows of a strided view."""
     rows, cols, ld = 5, 64, 1 << 29

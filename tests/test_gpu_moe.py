@@ -233,6 +233,28 @@ def test_a_copy_keeps_every_bit(grs):
             assert torch.equal(xs[rows.long()], bits.repeat_interleave(2, 0))
 
 
+def test_on_another_stream(grs):
+    """Sort, dispatch and combine on a side stream only: what it waits for there is the result."""
+    tokens, k, d = 3000, 4, 512
+    g = torch.Generator(device="cuda").manual_seed(2)
+    s = grs.make_moe(tokens, k, 16, 0, 16, d, 0)
+    ids = torch.randint(0, 16, (tokens * k,), generator=g, device="cuda").to(torch.int32)
+    x = torch.randn(tokens, d, generator=g, device="cuda").to(torch.bfloat16)
+    w = torch.full((tokens * k,), 0.25, device="cuda")
+    off, rs, sr = (torch.zeros(n, dtype=torch.int32, device="cuda") for n in (17, tokens * k, tokens * k))
+    ws = torch.zeros(grs.grs_moe_workspace_bytes(s), dtype=torch.uint8, device="cuda")
+    xs, y = torch.zeros(tokens * k, d, dtype=torch.bfloat16, device="cuda"), torch.zeros_like(x)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    st = side.cuda_stream
+    grs.grs_moe_sort(s, ids.data_ptr(), off.data_ptr(), rs.data_ptr(), sr.data_ptr(), ws.data_ptr(), st)
+    grs.grs_moe_dispatch(s, x.data_ptr(), sr.data_ptr(), xs.data_ptr(), st)
+    grs.grs_moe_combine(s, xs.data_ptr(), sr.data_ptr(), w.data_ptr(), y.data_ptr(), st)
+    side.synchronize()
+    assert torch.equal(y, x)  # four quarters of the token itself
+    assert np.array_equal(sr.cpu().numpy(), sorted64(ids.cpu().numpy(), 0, 16)[2])
+
+
 def test_no_tokens(grs):
     s = grs.make_moe(0, 2, 4, 0, 4, 16, 0)
     off = torch.full((5,), -1, dtype=torch.int32, device="cuda")

@@ -13,7 +13,7 @@
 // waits for each (combine of 16384 tokens x 8 rows of 2048 bf16: 277 us against
 // 88).  At that size dispatch takes 89 us, combine and dispatch_backward 88 and
 // combine_backward 174, 6.6 to 6.9 TB/s of a copy rate of 6.78; 6001 x 6 rows
-// 27, 31 and 56 us.  The sort of those 131072 slots among 32 experts takes 8 us,
+// 27, 31 and 54 us.  The sort of those 131072 slots among 32 experts takes 8 us,
 // of 20 slots 2.6 (one launch), bound by latency.  Vectors of any other size
 // go as shifted chunks at 2 to 5 TB/s.
 #include <cuda_bf16.h>
@@ -287,9 +287,11 @@ __global__ void __launch_bounds__(MOE_THREADS) moe_dispatch_kernel(const __grid_
   }
 }
 
-// Rows of a token in flight at once.
+// Rows of a token in flight at once.  Loose ones two: more rows' shifting is
+// more code than the instruction caches like (combine of 6001 x 6 rows of
+// 2051: bf16 53 us with 2, 68 with 4, 85 with 8; fp32 74, 124, 235).
 template <bool kWhole>
-constexpr int moe_batch = kWhole ? 8 : 4;
+constexpr int moe_batch = kWhole ? 8 : 2;
 
 // y[t] = sum over the token's rows of weight * row; without weights, of the row.
 template <typename T, bool kWhole>
@@ -464,7 +466,7 @@ cudaError_t moe_launch(MoeOp op, MoeArgs<T> a, void* stream) {
       // fp32 the other way round, 183 and 168).
       if (a.tokens >= 16 * 152 && a.d * static_cast<int64_t>(sizeof(T)) <= 8192) warps = 1;
       a.group = 32 * (warps < MOE_THREADS / 32 ? warps : MOE_THREADS / 32);
-      if (a.group > 32) threads = a.group;
+      threads = a.group > 32 ? a.group : 64;  // (two tokens a block: a finer tail than eight, 54.3 and 55.7 us for 6001 x 6)
     }
     const int64_t per = threads / a.group, blocks = (a.tokens + per - 1) / per;
     return launch_pdl(moe_combine_bwd_kernel<T, kWhole>, dim3(static_cast<unsigned>(blocks)), dim3(threads), 0, stream, a);

@@ -8,12 +8,12 @@
 // open.
 //
 // The vectors' kernels are bound by memory.  A thread has 16 bytes (8 bf16 or
-// 8 fp32 elements) of a token and of all its rows, eight rows' loads in flight
-// before the first is used; with the conversion between the loads the compiler
-// waits for each (combine of 16384 tokens x 8 rows of 2048 bf16: 277 us against
-// 88).  At that size dispatch takes 89 us, combine and dispatch_backward 88 and
-// combine_backward 174, 6.6 to 6.9 TB/s of a copy rate of 6.78; 6001 x 6 rows
-// 27, 31 and 54 us.  The sort of those 131072 slots among 32 experts takes 8 us,
+// 8 fp32 elements) of a token and of all its rows, up to eight rows' loads in
+// flight before the first is used; with the conversion between the loads the
+// compiler waits for each (combine of 16384 tokens x 8 rows of 2048 bf16: 277 us
+// against 88).  At that size dispatch takes 91 us, combine and dispatch_backward
+// 88 and combine_backward 171, 6.6 to 6.9 TB/s of a copy rate of 6.78; 6001 x 6
+// rows 27, 29 and 50 us.  The sort of those 131072 slots among 32 experts takes 8 us,
 // of 20 slots 2.6 (one launch), bound by latency.  Vectors of any other size
 // go as shifted chunks at 2 to 5 TB/s.
 #include <cuda_bf16.h>
@@ -252,56 +252,69 @@ __device__ __forceinline__ void vec_store(T* m, int64_t v, int c, int d, const f
   store8(p, store_run<kWhole>(p, c, d), kWhole ? 8 : d - c, o);
 }
 
-// The token and the first element of this thread; false beyond the last.
+// The token and the first element of this thread as one of block `block`;
+// false beyond the last.
 template <bool kWhole, typename T>
-__device__ __forceinline__ bool moe_place(const MoeArgs<T>& a, int64_t* t, int* c) {
-  const int64_t i = kWhole ? int64_t(blockIdx.x) * MOE_THREADS + threadIdx.x
-                           : int64_t(blockIdx.x) * (MOE_THREADS / 32) + (threadIdx.x >> 5);
+__device__ __forceinline__ bool moe_place(const MoeArgs<T>& a, int64_t block, int64_t* t, int* c) {
+  const int64_t i = kWhole ? block * MOE_THREADS + threadIdx.x : block * (MOE_THREADS / 32) + (threadIdx.x >> 5);
   *t = i <= UINT32_MAX ? static_cast<uint32_t>(i) / static_cast<uint32_t>(a.units) : i / a.units;
   const int u = static_cast<int>(i - *t * a.units);
   *c = kWhole ? u * 8 : u * 256 + (threadIdx.x & 31) * 8;
   return *t < a.tokens;
 }
 
-// xs[row] = x[t] for each of the token's rows: x is read once.
-template <typename T, bool kWhole>
+// xs[row] = x[t] for each of the token's rows: x is read once.  A block does
+// the work of U blocks, so that a thread has U loads in flight where few
+// stores follow each (10986 x 1 rows of 4096 bf16: 6.4 TB/s with two, 4.5 with
+// one; x 2: 6.4 and 5.9).
+template <typename T, bool kWhole, int U>
 __global__ void __launch_bounds__(MOE_THREADS) moe_dispatch_kernel(const __grid_constant__ MoeArgs<T> a) {
   pdl_wait();
   pdl_trigger();
-  int64_t t;
-  int c;
-  if (!moe_place<kWhole>(a, &t, &c)) return;
-  Vec<kWhole, T> x;
-  x.start(a.a, t, a.tokens, c, a.d);
-  x.finish(c, a.d);
-  for (int j0 = 0; j0 < a.k; j0 += 8) {
-    int64_t r[8];
+  int64_t t[U];
+  int c[U];
+  bool on[U];
+  Vec<kWhole, T> x[U];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) r[j] = j0 + j < a.k ? moe_row(a, t * a.k + j0 + j) : -1;
+  for (int u = 0; u < U; ++u) {
+    on[u] = moe_place<kWhole>(a, int64_t(blockIdx.x) * U + u, &t[u], &c[u]);
+    if (on[u]) x[u].start(a.a, t[u], a.tokens, c[u], a.d);
+  }
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (r[j] >= 0) {
-        T* p = a.o + r[j] * a.d + c;
-        store_words(p, store_run<kWhole>(p, c, a.d), kWhole ? 8 : a.d - c, x.m.own);  // the bits as they are
-      }
+  for (int u = 0; u < U; ++u) {
+    if (!on[u]) return;
+    x[u].finish(c[u], a.d);
+    constexpr int B = U > 1 ? 2 : 8;
+    for (int j0 = 0; j0 < a.k; j0 += B) {
+      int64_t r[B];
+#pragma unroll
+      for (int j = 0; j < B; ++j) r[j] = j0 + j < a.k ? moe_row(a, t[u] * a.k + j0 + j) : -1;
+#pragma unroll
+      for (int j = 0; j < B; ++j)
+        if (r[j] >= 0) {
+          T* p = a.o + r[j] * a.d + c[u];
+          store_words(p, store_run<kWhole>(p, c[u], a.d), kWhole ? 8 : a.d - c[u], x[u].m.own);  // the bits as they are
+        }
+    }
   }
 }
 
-// Rows of a token in flight at once.  Loose ones two: more rows' shifting is
-// more code than the instruction caches like (combine of 6001 x 6 rows of
-// 2051: bf16 53 us with 2, 68 with 4, 85 with 8; fp32 74, 124, 235).
-template <bool kWhole>
-constexpr int moe_batch = kWhole ? 8 : 2;
+// The next two kernels have B rows of a token in flight at once: as many as
+// tokens have, of 2, 4, 6 and 8: places without a row cost registers, so loads
+// in flight (combine of 4096 x 2 rows of 4096 bf16: 15.0 us, and 29.0 with
+// eight; backward of 6001 x 6 of 2048: 49.7 and 52.6 us).
+// Loose ones two: more rows' shifting is more code than the instruction caches
+// like (combine of 6001 x 6 rows of 2051: bf16 53 us with 2, 68 with 4, 85
+// with 8; fp32 74, 124, 235).
 
 // y[t] = sum over the token's rows of weight * row; without weights, of the row.
-template <typename T, bool kWhole>
+template <typename T, bool kWhole, int B>
 __global__ void __launch_bounds__(MOE_THREADS) moe_combine_kernel(const __grid_constant__ MoeArgs<T> a) {
-  constexpr int B = moe_batch<kWhole>;
   pdl_wait();
   pdl_trigger();
   int64_t t;
   int c;
-  if (!moe_place<kWhole>(a, &t, &c)) return;
+  if (!moe_place<kWhole>(a, blockIdx.x, &t, &c)) return;
   float2 s[4] = {both(0.0f), both(0.0f), both(0.0f), both(0.0f)};
   for (int j0 = 0; j0 < a.k; j0 += B) {
     Vec<kWhole, T> v[B];
@@ -324,9 +337,8 @@ __global__ void __launch_bounds__(MOE_THREADS) moe_combine_kernel(const __grid_c
 
 // dys[row] = weight * dy[t] and dweights[slot] = <ys[row], dy[t]>.  A group of
 // threads a token; its threads' parts of a batch of products meet once.
-template <typename T, bool kWhole>
+template <typename T, bool kWhole, int B>
 __global__ void __launch_bounds__(MOE_THREADS) moe_combine_bwd_kernel(const __grid_constant__ MoeArgs<T> a) {
-  constexpr int B = moe_batch<kWhole>;
   __shared__ float red[MOE_THREADS / 32][B];
   pdl_wait();
   pdl_trigger();
@@ -451,7 +463,7 @@ bool moe_whole(const grs_moe* s, const void* a, const void* b, const void* o) {
 
 enum class MoeOp { kDispatch, kCombine, kCombineBackward };
 
-template <typename T, bool kWhole>
+template <typename T, bool kWhole, int B>
 cudaError_t moe_launch(MoeOp op, MoeArgs<T> a, void* stream) {
   if (op == MoeOp::kCombineBackward) {
     // Threads of a token: its units in whole groups as far as a block goes.
@@ -461,21 +473,35 @@ cudaError_t moe_launch(MoeOp op, MoeArgs<T> a, void* stream) {
       while (a.group < a.units) a.group *= 2;
     } else {
       int warps = kWhole ? (a.units + 31) / 32 : a.units;
-      // Many tokens of up to 8 KB: a warp each, whose products meet without a
-      // barrier (16384 x 8 of 2048 bf16: 174 us against 194; 4096 x 8 of 4096
-      // fp32 the other way round, 183 and 168).
-      if (a.tokens >= 16 * 152 && a.d * static_cast<int64_t>(sizeof(T)) <= 8192) warps = 1;
+      if (a.tokens >= 16 * 152) {
+        // Many tokens: 32 bytes of each row a thread.  With 180 MB of bf16 rows of 2048: 6.4 TB/s, 5.6 with 16
+        // bytes and 256 threads, 5.6 with a warp a token; of 4096: 6.2, 6.1 and 4.9, so up to 128 threads.
+        if (kWhole && sizeof(T) == 2) warps = warps >= 8 ? 4 : (warps + 1) / 2;
+        // A warp for a loose one of up to 8 KB, whose products meet without a barrier.
+        if (!kWhole && a.d * static_cast<int64_t>(sizeof(T)) <= 8192) warps = 1;
+      }
       a.group = 32 * (warps < MOE_THREADS / 32 ? warps : MOE_THREADS / 32);
       threads = a.group > 32 ? a.group : 64;  // (two tokens a block: a finer tail than eight, 54.3 and 55.7 us for 6001 x 6)
     }
     const int64_t per = threads / a.group, blocks = (a.tokens + per - 1) / per;
-    return launch_pdl(moe_combine_bwd_kernel<T, kWhole>, dim3(static_cast<unsigned>(blocks)), dim3(threads), 0, stream, a);
+    return launch_pdl(moe_combine_bwd_kernel<T, kWhole, B>, dim3(static_cast<unsigned>(blocks)), dim3(threads), 0, stream, a);
   }
-  const int64_t per = kWhole ? MOE_THREADS : MOE_THREADS / 32, blocks = (a.tokens * a.units + per - 1) / per;
+  constexpr int U = kWhole && B == 2 ? 2 : 1;
+  const bool dispatch = op == MoeOp::kDispatch;
+  const int64_t per = (kWhole ? MOE_THREADS : MOE_THREADS / 32) * (dispatch ? U : 1), blocks = (a.tokens * a.units + per - 1) / per;
   if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
   const dim3 grid(static_cast<unsigned>(blocks)), block(MOE_THREADS);
-  return op == MoeOp::kDispatch ? launch_pdl(moe_dispatch_kernel<T, kWhole>, grid, block, 0, stream, a)
-                                : launch_pdl(moe_combine_kernel<T, kWhole>, grid, block, 0, stream, a);
+  return dispatch ? launch_pdl(moe_dispatch_kernel<T, kWhole, U>, grid, block, 0, stream, a)
+                  : launch_pdl(moe_combine_kernel<T, kWhole, B>, grid, block, 0, stream, a);
+}
+
+template <typename T>
+cudaError_t moe_launch(MoeOp op, const MoeArgs<T>& a, bool whole, void* stream) {
+  if (!whole) return moe_launch<T, false, 2>(op, a, stream);
+  return a.k <= 2 ? moe_launch<T, true, 2>(op, a, stream)
+         : a.k <= 4 ? moe_launch<T, true, 4>(op, a, stream)
+         : a.k <= 6 ? moe_launch<T, true, 6>(op, a, stream)
+                    : moe_launch<T, true, 8>(op, a, stream);
 }
 
 cudaError_t moe_run(MoeOp op, const grs_moe* s, const void* a, const void* b, void* o, const int32_t* slot_row,
@@ -486,14 +512,14 @@ cudaError_t moe_run(MoeOp op, const grs_moe* s, const void* a, const void* b, vo
     MoeArgs<uint16_t> x = moe_args<uint16_t>(s, a, b, o, slot_row, weights, dweights, whole);
     x.d *= 2;
     x.units *= 2;
-    return moe_launch<uint16_t, true>(op, x, stream);
+    return moe_launch(op, x, true, stream);
   }
   if (s->dtype == GRS_DTYPE_FP32) {
     const MoeArgs<float> x = moe_args<float>(s, a, b, o, slot_row, weights, dweights, whole);
-    return whole ? moe_launch<float, true>(op, x, stream) : moe_launch<float, false>(op, x, stream);
+    return moe_launch(op, x, whole, stream);
   }
   const MoeArgs<uint16_t> x = moe_args<uint16_t>(s, a, b, o, slot_row, weights, dweights, whole);
-  return whole ? moe_launch<uint16_t, true>(op, x, stream) : moe_launch<uint16_t, false>(op, x, stream);
+  return moe_launch(op, x, whole, stream);
 }
 
 }  // namespace

@@ -13,9 +13,9 @@
 // What bounds them, on a GB300 that copies 6.78 TB/s:
 //   step, 32 bits  memory: 28 or 30 bytes an element; 61.8M at 6.9 TB/s
 //                  (248 us with bf16, 265 with fp32 gradients)
-//   step, 8 bits   memory and instruction issue alike: 16 or 18 bytes and 84
+//   step, 8 bits   memory and instruction issue alike: 16 or 18 bytes and 80
 //                  instructions an element; 61.8M fp32 in 172 us (6.5 TB/s),
-//                  1.10B bf16 in 2.93 ms (6.0 TB/s).  Hence the hardware's
+//                  1.10B bf16 in 2.92 ms (6.0 TB/s).  Hence the hardware's
 //                  8-bit decoding, the codes rounded by one product and one
 //                  addition, and the folded hash.
 //   norm           memory for long lists (61.8M fp32: 5.8 TB/s; bf16, whose

@@ -302,7 +302,8 @@ __global__ void __launch_bounds__(MOE_THREADS) moe_dispatch_kernel(const __grid_
 // The next two kernels have B rows of a token in flight at once: as many as
 // tokens have, of 2, 4, 6 and 8: places without a row cost registers, so loads
 // in flight (combine of 4096 x 2 rows of 4096 bf16: 15.0 us, and 29.0 with
-// eight; backward of 6001 x 6 of 2048: 49.7 and 52.6 us).
+// eight; both kernels of the backward pass of 6001 x 6
+// of 2048: 79.3 us, and 85.2).
 // Loose ones two: more rows' shifting is more code than the instruction caches
 // like (combine of 6001 x 6 rows of 2051: bf16 53 us with 2, 68 with 4, 85
 // with 8; fp32 74, 124, 235).

@@ -651,7 +651,7 @@ __global__ void __launch_bounds__(LN_BWD_THREADS) ln_bwd_kernel(const __grid_con
 //   send row i's  ->  dx of row i - 1, its elements read from the ring again.
 // (With a barrier of the cluster in place of the counted sends, its release
 // waits for dx: 2.3 us a row instead of 1.3.)  256 MB in rows of 16384: bf16
-// 156 us (4.9 TB/s), fp32 164; with a pass for dx and another over x and dy
+// 151 us (5.1 TB/s), fp32 161; with a pass for dx and another over x and dy
 // for dw and db 280 and 308.  The ring is read by who filled it, so a slot
 // may be filled again two rows on without a barrier.
 template <typename T, typename W, int E>
@@ -935,32 +935,50 @@ __global__ void __launch_bounds__(LN_THREADS) ln_dparam_kernel(const T* __restri
   }
 }
 
-// dw and db from the parts, in a fixed order.  A block takes 32 of the 2 C
-// sums, warp k of it the parts k, k + 32, ...
+// dw and db from the parts, in a fixed order.  A block of n warps takes 32 of
+// the 2 C sums, warp k of it the parts k, k + n, ..., all in flight at once.
+constexpr int LN_SUM_LOADS = 10;  // a thread's, of LN_PARTS at most
+
 template <typename D>
 __global__ void __launch_bounds__(1024) ln_dparam_sum_kernel(const float* __restrict__ parts, int32_t n_parts, int32_t cols,
                                                              D* __restrict__ dw, D* __restrict__ db) {
   __shared__ float red[32][33];
   pdl_wait();
   pdl_trigger();
-  const int lane = threadIdx.x & 31, k = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31, k = threadIdx.x >> 5, n = blockDim.x >> 5;
   const int64_t c = int64_t(blockIdx.x) * 32 + lane, width = 2 * int64_t(cols);
   float s = 0.0f;
   if (c < width) {
-    float x[(LN_PARTS + 31) / 32];  // all in flight at once
+    float x[LN_SUM_LOADS];
+    const float* p = parts + k * width + c;
 #pragma unroll
-    for (int i = 0; i < (LN_PARTS + 31) / 32; ++i) x[i] = k + 32 * i < n_parts ? parts[(k + 32 * i) * width + c] : 0.0f;
+    for (int i = 0; i < LN_SUM_LOADS; ++i) x[i] = k + n * i < n_parts ? p[n * i * width] : 0.0f;
 #pragma unroll
-    for (int i = 0; i < (LN_PARTS + 31) / 32; ++i) s += x[i];
+    for (int i = 0; i < LN_SUM_LOADS; ++i) s += x[i];
   }
   red[k][lane] = s;
   __syncthreads();
-  // warp k adds up the sum of column k
-  s = warp_sum(red[lane][k]);
-  const int64_t col = int64_t(blockIdx.x) * 32 + k;
-  if (lane != 0 || col >= width) return;
+  int64_t col = c;
+  if (n == 32) {  // warp k adds up column k
+    s = warp_sum(red[lane][k]);
+    col += k - lane;
+    if (lane != 0) return;
+  } else {  // few terms, other blocks beside this one: a lane of warp 0 a column
+    if (k != 0) return;
+#pragma unroll 8
+    for (int i = 1; i < n; ++i) s += red[i][lane];
+  }
+  if (col >= width) return;
   D* out = col < cols ? dw : db;
   if (out != nullptr) ln_store(out + (col < cols ? col : col - cols), s);
+}
+
+// Its threads: 32 warps where a block has an SM to itself; where there are
+// more blocks, as few as have all the parts in flight (2 x 16384 sums of 76
+// parts: 6 us, and 10 with 32 warps).
+dim3 ln_sum_block(int64_t blocks, int32_t parts) {
+  static_assert(32 * LN_SUM_LOADS >= LN_PARTS, "a thread takes its parts at once");
+  return dim3(blocks <= 152 || parts > 16 * LN_SUM_LOADS ? 1024 : parts > 8 * LN_SUM_LOADS ? 512 : 256);
 }
 
 int32_t ln_parts(int64_t rows) { return static_cast<int32_t>(rows < LN_PARTS ? (rows > 0 ? rows : 1) : LN_PARTS); }
@@ -1237,9 +1255,9 @@ cudaError_t ln_backward(const grs_norm* s, const LnLd& ld, const void* dy, const
   const dim3 grid(static_cast<unsigned>((2 * int64_t(s->cols) + 31) / 32));
   const float* parts_in = ws;
   return s->grad_dtype == GRS_DTYPE_FP32
-             ? launch_pdl(ln_dparam_sum_kernel<float>, grid, dim3(1024), 0, stream, parts_in, parts, s->cols,
+             ? launch_pdl(ln_dparam_sum_kernel<float>, grid, ln_sum_block(grid.x, parts), 0, stream, parts_in, parts, s->cols,
                         static_cast<float*>(dw), static_cast<float*>(db))
-             : launch_pdl(ln_dparam_sum_kernel<uint16_t>, grid, dim3(1024), 0, stream, parts_in, parts, s->cols,
+             : launch_pdl(ln_dparam_sum_kernel<uint16_t>, grid, ln_sum_block(grid.x, parts), 0, stream, parts_in, parts, s->cols,
                         static_cast<uint16_t*>(dw), static_cast<uint16_t*>(db));
 }
 

@@ -46,7 +46,12 @@ constexpr int LN_BWD_THREADS = 512;  // a block of the backward pass at most
 constexpr int LN_RED_BYTES = 256;    // two float2 a warp of a block, twice
 constexpr int LN_PEERS = 8;          // blocks of a cluster at most (the portable size)
 constexpr int LN_WIDE_RED = LN_PEERS * LN_RED_BYTES + 16;  // the warps' sums of a cluster, twice, and their barriers
-constexpr int LN_WIDE_SLOTS = 6;
+// Slots of its ring: the row that is finished, the one that is summed, and
+// those in flight.  Few, so that more blocks fit an SM where their registers
+// allow it: fp32 (62 registers) 7812 x 8192 126 us with 3, 150 with 4, 152 with
+// 6; bf16 (122) 7812 x 16384 159, 150 and 151.
+template <typename T>
+constexpr int ln_wide_slots = sizeof(T) == 4 ? 3 : 4;
 constexpr int LN_PARTS = 304;        // partial rows of dw and db at most: two blocks an SM
 
 __device__ __forceinline__ float ln_load(const uint16_t* p) { return __uint_as_float(uint32_t(*p) << 16); }
@@ -651,7 +656,7 @@ __global__ void __launch_bounds__(LN_BWD_THREADS) ln_bwd_kernel(const __grid_con
 //   send row i's  ->  dx of row i - 1, its elements read from the ring again.
 // (With a barrier of the cluster in place of the counted sends, its release
 // waits for dx: 2.3 us a row instead of 1.3.)  256 MB in rows of 16384: bf16
-// 151 us (5.1 TB/s), fp32 161; with a pass for dx and another over x and dy
+// 150 us (5.1 TB/s), fp32 131; with a pass for dx and another over x and dy
 // for dw and db 280 and 308.  The ring is read by who filled it, so a slot
 // may be filled again two rows on without a barrier.
 template <typename T, typename W, int E>
@@ -677,7 +682,7 @@ __global__ void __launch_bounds__(LN_BWD_THREADS) ln_bwd_wide_kernel(const __gri
   const T *x_now = x_ahead, *dy_now = dy_ahead;
   const Matrix mx = matrix_of(a.x, a.ld_x, a.rows, a.cols), my = matrix_of(a.dy, a.ld_dy, a.rows, a.cols);
   using R = Ring<T, VEC, E>;
-  constexpr int SLOTS = LN_WIDE_SLOTS;
+  constexpr int SLOTS = ln_wide_slots<T>;
   uint8_t* ring = reinterpret_cast<uint8_t*>(sums) + LN_WIDE_RED;
   const int half_slot = R::BYTES * tpr;
   int64_t ahead = block;
@@ -1164,8 +1169,8 @@ cudaError_t resident_clusters(int peers, int threads, unsigned smem, int64_t* cl
 }
 
 // Rows over the blocks of a cluster: 2, 4 or 8 of them, as few as hold a row
-// (256 MB of bf16: rows of 20000 233 us in four blocks, 350 in three; rows of
-// 11968 188 us in two blocks of 384 threads and in four of 192).
+// (256 MB of bf16: rows of 20000 225 us in four blocks, half as much again in
+// three; rows of 11968 186 us in two blocks of 384 threads, no less in four).
 template <typename T, typename W, int E>
 cudaError_t ln_backward_wide(const LnBwd<T, W>& args, int32_t* parts, void* stream) {
   LnBwd<T, W> a = args;
@@ -1174,7 +1179,7 @@ cudaError_t ln_backward_wide(const LnBwd<T, W>& args, int32_t* parts, void* stre
   const int32_t eights = (a.cols + 7) / 8;
   a.span = (eights + peers - 1) / peers * 8;
   a.tpr = ln_tpr(a.span, E);
-  constexpr int slots = LN_WIDE_SLOTS * 2 * E * static_cast<int>(sizeof(T));  // a thread's
+  constexpr int slots = ln_wide_slots<T> * 2 * E * static_cast<int>(sizeof(T));  // a thread's
   static_assert(LN_WIDE_RED + slots * LN_BWD_THREADS <= 227 * 1024, "shared memory of a block");
   constexpr auto* kernel = ln_bwd_wide_kernel<T, W, E>;
   cudaError_t e = allow_smem<kernel>(LN_WIDE_RED + slots * LN_BWD_THREADS);
@@ -1199,8 +1204,11 @@ cudaError_t ln_backward_vec(const LnBwd<T, W>& a, int32_t* parts, bool* dx_done,
   const bool eight = (a.rows <= LN_PARTS || sizeof(T) == 4) && t8 <= LN_BWD_THREADS;
   int32_t unused = 0;
   if constexpr (VEC > 2) {
+    // fp32 also from 4096, where there are rows enough to pay for the sums' way (12500 x 5120 127 us, 172 in one
+    // block; 1562 rows 24.5 and 26.7, 390 rows 12.9 and 10.9).
     constexpr int e = sizeof(T) == 4 ? 8 : 16;
-    if (a.rows > 0 && t16 > LN_BWD_THREADS && a.cols <= LN_PEERS * LN_BWD_THREADS * e)
+    const bool wide = t16 > LN_BWD_THREADS || (sizeof(T) == 4 && t8 > LN_BWD_THREADS && a.rows >= 4 * 152);
+    if (a.rows > 0 && wide && a.cols <= LN_PEERS * LN_BWD_THREADS * e)
       return ln_backward_wide<T, W, e>(a, a.parts != nullptr ? parts : &unused, stream);
   }
   if (a.parts != nullptr) {

@@ -38,6 +38,12 @@ def test_wide_rows(grs, rows, cols, act, par, grad, pad, shift):  # noqa: F811
         assert torch.equal(a, b)
 
 
+# fp32 rows that one block could hold, shared where they are many
+@pytest.mark.parametrize("rows,cols", [(607, 4104), (608, 4104), (1500, 8192), (700, 5128), (610, 4097)])
+def test_fp32_rows_of_a_cluster_or_a_block(grs, rows, cols):  # noqa: F811
+    test_wide_rows(grs, rows, cols, "fp32", "fp32", "fp32", 0, 0)
+
+
 @pytest.mark.parametrize("cols", [8200, 16387])
 @pytest.mark.parametrize("act", ["fp32", "bf16"])
 def test_wide_rows_optional_arguments(grs, cols, act):  # noqa: F811

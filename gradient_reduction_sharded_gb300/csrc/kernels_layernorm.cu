@@ -336,14 +336,15 @@ __device__ __forceinline__ void cluster_sum2_send(float a, float b, const Place&
   }
 }
 
-// False if the sums did not come in time.
+// False, for the whole warp, if the sums did not come in time.
 __device__ __forceinline__ bool cluster_sum2_take(float& a, float& b, const Place& p, uint64_t* bar, unsigned peers, int phase,
                                                   uint32_t parity) {
-  if (!mbar_try_wait(bar + phase, parity)) {
+  bool in = mbar_try_wait(bar + phase, parity);
+  if (!in) {
     const uint64_t t0 = global_ns();
-    while (!mbar_try_wait(bar + phase, parity))
-      if (global_ns() - t0 > WAIT_LIMIT_NS) return false;
+    while (!in && global_ns() - t0 <= WAIT_LIMIT_NS) in = mbar_try_wait(bar + phase, parity);
   }
+  if (!__all_sync(0xffffffffu, in)) return false;
   a = b = 0.0f;
   const float2* red = p.red + phase * LN_PEERS * p.warps;
   for (unsigned k = threadIdx.x & 31; k < peers * p.warps; k += 32) {

@@ -743,7 +743,9 @@ grs_status grs_layernorm_forward(const grs_norm* shape, const void* x, const voi
  *   zeros when rows is 0), each of the three NULL if not wanted.
  * Sums in fp32 in an order that the shape alone fixes: the same call gives the
  * same bits.  workspace: device, 16-byte aligned, grs_layernorm_workspace_bytes
- * (not initialised), needed for dw or db.  No output may overlap an input. */
+ * (not initialised), needed for dw or db.  No output may overlap an input.
+ * Blocks that share wide rows wait for one another's sums; a wait that gives
+ * up (after 2 s, which only a defect can cause) leaves NaN in what needed it. */
 grs_status grs_layernorm_backward(const grs_norm* shape, const void* dy, const void* x, const void* w,
                                   const float* mean, const float* rstd, void* dx, void* dw, void* db,
                                   void* workspace, void* stream);

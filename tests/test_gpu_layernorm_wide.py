@@ -71,6 +71,26 @@ def test_wide_rows_nan_and_infinity_stay_in_their_row(grs):  # noqa: F811
     assert bad.tolist() == [i in (2, 6) for i in range(9)]
 
 
+# widths that no other test has: the first call of their launch shape is the captured one
+@pytest.mark.parametrize("act,cols", [("bf16", 10000), ("fp32", 10400)])
+def test_wide_rows_in_a_graph_on_another_stream(grs, act, cols):  # noqa: F811
+    c = Case(grs, 150, cols, act, act, "fp32", seed=3)
+    c.forward()
+    gx, gw, gb = torch.full_like(c.x, float("nan")), torch.zeros(cols, device="cuda"), torch.zeros(cols, device="cuda")
+    shape = grs.make_norm(150, cols, c.eps, *[grs.GRS_DTYPE_BF16 if act == "bf16" else grs.GRS_DTYPE_FP32] * 2, grs.GRS_DTYPE_FP32)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=torch.cuda.Stream()):
+        grs.grs_layernorm_backward(shape, c.dy.data_ptr(), c.x.data_ptr(), c.w.data_ptr(), c.mean.data_ptr(), c.rstd.data_ptr(), gx.data_ptr(),
+                                   gw.data_ptr(), gb.data_ptr(), c.ws.data_ptr(), torch.cuda.current_stream().cuda_stream)
+    for _ in range(3):
+        gx.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        for g, (want, bound), what in zip((gx, gw, gb), gradients64(c), ("dx", "dw", "db")):
+            check(g, want, bound, what)
+
+
 # more than 64 MB of x: the forward pass takes other blocks
 @pytest.mark.parametrize("cols", [1, 7, 16, 33, 768, 2560, 5120])
 @pytest.mark.parametrize("act,pad,shift", [("fp32", 0, 0), ("bf16", 0, 0), ("bf16", 1, 1), ("fp32", 3, 1)])

@@ -20,7 +20,7 @@
 //                  addition, and the folded hash.
 //   norm           memory for long lists (61.8M fp32: 5.8 TB/s; bf16, whose
 //                  sums take as many instructions for half the bytes, 4.0),
-//                  latency for short ones (six tensors: 6 us)
+//                  latency for short ones (12 tensors: 6 us)
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

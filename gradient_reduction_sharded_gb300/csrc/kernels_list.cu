@@ -154,23 +154,6 @@ __device__ __forceinline__ double block_sum(double x, double* red) {
 // tiles), so every addition has its fixed place.
 constexpr int LIST_NORM_BLOCKS = 608;  // four blocks an SM
 
-// The chunk of 16 bytes at p: all of it, or its elements [lo, hi).
-__device__ __forceinline__ uint4 load_chunk(const uint16_t* p, int lo, int hi) {
-  if (lo <= 0 && hi >= 8) return __ldcs(reinterpret_cast<const uint4*>(p));
-  uint32_t w[4];
-#pragma unroll
-  for (int q = 0; q < 4; ++q)
-    w[q] = (2 * q >= lo && 2 * q < hi ? uint32_t(p[2 * q]) : 0u) | (2 * q + 1 >= lo && 2 * q + 1 < hi ? uint32_t(p[2 * q + 1]) << 16 : 0u);
-  return make_uint4(w[0], w[1], w[2], w[3]);
-}
-__device__ __forceinline__ uint4 load_chunk(const float* p, int lo, int hi) {
-  if (lo <= 0 && hi >= 4) return __ldcs(reinterpret_cast<const uint4*>(p));
-  uint32_t w[4];
-#pragma unroll
-  for (int q = 0; q < 4; ++q) w[q] = q >= lo && q < hi ? __float_as_uint(p[q]) : 0u;
-  return make_uint4(w[0], w[1], w[2], w[3]);
-}
-
 __device__ __forceinline__ void add_chunk(Sums& s, uint4 v, float minus_zero, uint16_t tag) {
   add_square(s, bf16_pair(v.x), minus_zero, tag);
   add_square(s, bf16_pair(v.y), minus_zero, tag);

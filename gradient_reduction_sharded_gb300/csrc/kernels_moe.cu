@@ -197,44 +197,30 @@ __device__ __forceinline__ int64_t moe_row(const MoeArgs<T>& a, int64_t slot) {
   return r >= 0 && r < a.slots ? r : -1;
 }
 
-// The thread's elements [c, c + 8) of vector v of a matrix of `vectors`, on
-// their way and as pairs; zeros if v < 0 and beyond the vector.
+// The thread's elements [c, c + 8) of vector v, on their way and as pairs;
+// zeros if v < 0 and beyond the vector.  Nothing behind vector v is read: the
+// caller's matrix may end with it (the vectors before it are there).
 template <bool kWhole, typename T>
 struct Vec {
   Moving<T> m;
-  int mis;      // loose vectors: where they start, -1 for no vector
-  bool inner;
+  int mis;  // loose vectors: bytes that the run starts after a 16-byte boundary
 
-  __device__ __forceinline__ void start(const T* base, int64_t v, int64_t vectors, int c, int d) {
+  __device__ __forceinline__ void start(const T* base, int64_t v, int c, int d) {
 #pragma unroll
     for (int i = 0; i < Moving<T>::N; ++i) m.own[i] = 0u;
-    mis = -1;
-    inner = false;
+    mis = 0;
     if (v < 0) return;
-    const T* p = base + v * d + c;
+    const int64_t before = v * d + c;
+    const T* p = base + before;
     if constexpr (kWhole) {
-      m.start(p, Run{0, true}, 8);
+      m.start(p);
     } else {
-      const int64_t first = v * d + (c & ~255);
-      const Run r = run_of(p, first, vectors * d - first);
-      m.start(p, r, r.inner ? 8 : d - c);
-      mis = r.mis;
-      inner = r.inner;
+      mis = static_cast<int>(reinterpret_cast<uintptr_t>(p) & 15);
+      m.start_within(p, mis, before < 8 ? static_cast<int>(before) : 8, d - c);
     }
   }
-  __device__ __forceinline__ void finish(int c, int d) {
-    if constexpr (!kWhole) {
-      if (mis < 0) return;
-      m.finish(Run{mis, inner});
-      if (d - c < 8) {  // a run's last elements may have come with the next vector's
-        constexpr int E = 4 / static_cast<int>(sizeof(T));  // elements of a word
-#pragma unroll
-        for (int i = 0; i < Moving<T>::N; ++i) {
-          if (i * E >= d - c) m.own[i] = 0u;
-          if (E == 2 && i * E + 1 >= d - c) m.own[i] &= 0xffffu;
-        }
-      }
-    }
+  __device__ __forceinline__ void finish() {
+    if constexpr (!kWhole) m.finish(mis);
   }
   __device__ __forceinline__ float2 pair(int q) const { return m.pair(q); }
 };
@@ -278,12 +264,12 @@ __global__ void __launch_bounds__(MOE_THREADS) moe_dispatch_kernel(const __grid_
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     on[u] = moe_place<kWhole>(a, int64_t(blockIdx.x) * U + u, &t[u], &c[u]);
-    if (on[u]) x[u].start(a.a, t[u], a.tokens, c[u], a.d);
+    if (on[u]) x[u].start(a.a, t[u], c[u], a.d);
   }
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     if (!on[u]) return;
-    x[u].finish(c[u], a.d);
+    x[u].finish();
     constexpr int B = U > 1 ? 2 : 8;
     for (int j0 = 0; j0 < a.k; j0 += B) {
       int64_t r[B];
@@ -324,11 +310,11 @@ __global__ void __launch_bounds__(MOE_THREADS) moe_combine_kernel(const __grid_c
     for (int j = 0; j < B; ++j) {
       const int64_t slot = t * a.k + j0 + j, r = j0 + j < a.k ? moe_row(a, slot) : -1;
       w[j] = r < 0 ? 0.0f : a.weights != nullptr ? __ldg(a.weights + slot) : 1.0f;
-      v[j].start(a.a, r, a.slots, c, a.d);
+      v[j].start(a.a, r, c, a.d);
     }
 #pragma unroll
     for (int j = 0; j < B; ++j) {
-      v[j].finish(c, a.d);
+      v[j].finish();
 #pragma unroll
       for (int q = 0; q < 4; ++q) s[q] = fma2(v[j].pair(q), both(w[j]), s[q]);
     }
@@ -362,17 +348,17 @@ __global__ void __launch_bounds__(MOE_THREADS) moe_combine_bwd_kernel(const __gr
 #pragma unroll 1
       for (int c = c0; (kWhole ? c : c & ~255) < a.d; c += per) {
         Vec<kWhole, T> gv, v[B];
-        gv.start(a.a, t, a.tokens, c, a.d);
+        gv.start(a.a, t, c, a.d);
 #pragma unroll
-        for (int j = 0; j < B; ++j) v[j].start(a.b, r[j], a.slots, c, a.d);
-        gv.finish(c, a.d);
+        for (int j = 0; j < B; ++j) v[j].start(a.b, r[j], c, a.d);
+        gv.finish();
         float2 gy[4];
 #pragma unroll
         for (int q = 0; q < 4; ++q) gy[q] = gv.pair(q);
 #pragma unroll
         for (int j = 0; j < B; ++j) {
           if (r[j] < 0) continue;
-          v[j].finish(c, a.d);
+          v[j].finish();
           float2 s = both(0.0f), o[4];
 #pragma unroll
           for (int q = 0; q < 4; ++q) {

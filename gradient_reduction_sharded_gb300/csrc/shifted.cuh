@@ -40,6 +40,37 @@ __device__ __forceinline__ void shift_words(const uint32_t (&own)[N], const uint
   for (int i = 0; i < N; ++i) o[i] = (BYTES & 2) != 0 ? __funnelshift_r(w[i + K], w[i + K + 1], 16) : w[i + K];
 }
 
+// Of chunk i of a lane whose 8 elements start `off` elements after its first
+// aligned chunk (of el elements) the elements [lo, hi) may be read: elements
+// [-before, n) of the lane.  May reach beyond the chunk.
+struct Span {
+  int lo, hi;
+};
+__host__ __device__ constexpr Span chunk_span(int el, int i, int off, int before, int n) {
+  return {off - before - i * el, off + n - i * el};
+}
+
+// The chunk of 16 bytes at p: all of it, or its elements [lo, hi) and zeros.
+__device__ __forceinline__ uint4 load_chunk(const uint16_t* p, int lo, int hi) {
+  if (lo <= 0 && hi >= 8) return __ldcs(reinterpret_cast<const uint4*>(p));
+  uint32_t w[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q)
+    w[q] = (2 * q >= lo && 2 * q < hi ? uint32_t(p[2 * q]) : 0u) | (2 * q + 1 >= lo && 2 * q + 1 < hi ? uint32_t(p[2 * q + 1]) << 16 : 0u);
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ uint4 load_chunk(const float* p, int lo, int hi) {
+  if (lo <= 0 && hi >= 4) return __ldcs(reinterpret_cast<const uint4*>(p));
+  uint32_t w[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) w[q] = q >= lo && q < hi ? __float_as_uint(p[q]) : 0u;
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+template <typename G>
+__device__ __forceinline__ uint4 load_chunk(const G* p, Span s) {
+  return load_chunk(p, s.lo, s.hi);
+}
+
 // What a lane has of its 8 elements while they are on their way: its own
 // aligned words (the last lane the chunk behind them too), shifted into place
 // by finish().  Several can be in flight: start() only loads.
@@ -49,27 +80,36 @@ struct Moving {
   uint32_t own[N];
   uint4 last;
 
-  // Elements [0, n) of the lane's 8 at p, zeros beyond; whole warp.
-  __device__ __forceinline__ void start(const G* p, Run r, int n) {
-    if ((r.mis == 0 && n >= 8) || r.inner) {
-      const uint4* c = reinterpret_cast<const uint4*>(reinterpret_cast<const uint8_t*>(p) - r.mis);
+  // The lane's 8 elements at p, 16-byte aligned.
+  __device__ __forceinline__ void start(const G* p) {
+    const uint4* c = reinterpret_cast<const uint4*>(p);
 #pragma unroll
-      for (int i = 0; i < N / 4; ++i) {
-        const uint4 v = __ldcs(c + i);
-        own[4 * i] = v.x;
-        own[4 * i + 1] = v.y;
-        own[4 * i + 2] = v.z;
-        own[4 * i + 3] = v.w;
-      }
-      if (r.mis != 0 && (threadIdx.x & 31) == 31) last = __ldcs(c + N / 4);
-    } else if constexpr (sizeof(G) == 2) {
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-        own[q] = (2 * q < n ? uint32_t(p[2 * q]) : 0u) | (2 * q + 1 < n ? uint32_t(p[2 * q + 1]) << 16 : 0u);
-    } else {
-#pragma unroll
-      for (int q = 0; q < 8; ++q) own[q] = q < n ? __float_as_uint(p[q]) : 0u;
+    for (int i = 0; i < N / 4; ++i) {
+      const uint4 v = __ldcs(c + i);
+      own[4 * i] = v.x;
+      own[4 * i + 1] = v.y;
+      own[4 * i + 2] = v.z;
+      own[4 * i + 3] = v.w;
     }
+  }
+
+  // Elements [0, n) of the lane's 8 at p, zeros beyond, where nothing may be
+  // read behind them or more than `before` elements before them.  Aligned
+  // chunks that lie in there come whole, others by their elements.  mis:
+  // bytes that the run starts after a 16-byte boundary; whole warp.
+  __device__ __forceinline__ void start_within(const G* p, int mis, int before, int n) {
+    constexpr int EL = 16 / static_cast<int>(sizeof(G));
+    const int off = mis / static_cast<int>(sizeof(G));
+    const G* c = p - off;
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i) {
+      const uint4 v = load_chunk(c + i * EL, chunk_span(EL, i, off, before, n));
+      own[4 * i] = v.x;
+      own[4 * i + 1] = v.y;
+      own[4 * i + 2] = v.z;
+      own[4 * i + 3] = v.w;
+    }
+    if (mis != 0 && (threadIdx.x & 31) == 31) last = load_chunk(c + N / 4 * EL, chunk_span(EL, N / 4, off, before, n));
   }
 
   template <int MIS>
@@ -90,10 +130,10 @@ struct Moving {
   }
 
   // The same run as start's; whole warp.
-  __device__ __forceinline__ void finish(Run r) {
-    if (r.mis == 0 || !r.inner) return;
+  __device__ __forceinline__ void finish(int mis) {
+    if (mis == 0) return;
     if constexpr (sizeof(G) == 2) {
-      switch (r.mis) {
+      switch (mis) {
         case 2: shift<2>(); break;
         case 4: shift<4>(); break;
         case 6: shift<6>(); break;
@@ -103,7 +143,7 @@ struct Moving {
         default: shift<14>(); break;
       }
     } else {
-      switch (r.mis) {
+      switch (mis) {
         case 4: shift<4>(); break;
         case 8: shift<8>(); break;
         default: shift<12>(); break;

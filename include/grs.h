@@ -788,7 +788,9 @@ int64_t grs_moe_workspace_bytes(const grs_moe* shape);
 /* The calls below take vectors as contiguous rows of `hidden` elements,
  * aligned to the element (16 bytes and hidden * size a multiple of 16 are
  * fastest).  An entry of slot_row outside [0, tokens * top_k) stands for no
- * row; the entries that do not must differ from each other.
+ * row; the entries that do not must differ from each other.  Rows beyond the
+ * largest entry are neither read nor written, so xs, ys, dxs and dys need no
+ * more: with grs_moe_sort's map the rows up to the last of expert_offsets.
  *
  * dispatch: xs[slot_row[s]] = x[s / top_k]; rows without a slot are not written.
  * dispatch_backward: dx[t] = sum of dxs over the token's rows, in fp32 in the

@@ -205,7 +205,9 @@ struct Vec {
   Moving<T> m;
   int mis;  // loose vectors: bytes that the run starts after a 16-byte boundary
 
-  __device__ __forceinline__ void start(const T* base, int64_t v, int c, int d) {
+  // D: the type of a vector's width.
+  template <typename D>
+  __device__ __forceinline__ void start(const T* base, int64_t v, int c, D d) {
 #pragma unroll
     for (int i = 0; i < Moving<T>::N; ++i) m.own[i] = 0u;
     mis = 0;
@@ -216,7 +218,7 @@ struct Vec {
       m.start(p);
     } else {
       mis = static_cast<int>(reinterpret_cast<uintptr_t>(p) & 15);
-      m.start_within(p, mis, before < 8 ? static_cast<int>(before) : 8, d - c);
+      m.start_within(p, mis, before < 8 ? static_cast<int>(before) : 8, static_cast<int>(d - c));
     }
   }
   __device__ __forceinline__ void finish() {
@@ -249,7 +251,9 @@ __device__ __forceinline__ bool moe_place(const MoeArgs<T>& a, int64_t block, in
   return *t < a.tokens;
 }
 
-// xs[row] = x[t] for each of the token's rows: x is read once.  A block does
+// xs[row] = x[t] for each of the token's rows: x is read once.  Whole vectors
+// are bits to copy: fp32 ones go as 16-bit halves, twice as many elements, so
+// their width (up to 2^31) comes from the units in 64 bits.  A block does
 // the work of U blocks, so that a thread has U loads in flight where few
 // stores follow each (10986 x 1 rows of 4096 bf16: 6.4 TB/s with two, 4.5 with
 // one; x 2: 6.4 and 5.9).
@@ -257,6 +261,10 @@ template <typename T, bool kWhole, int U>
 __global__ void __launch_bounds__(MOE_THREADS) moe_dispatch_kernel(const __grid_constant__ MoeArgs<T> a) {
   pdl_wait();
   pdl_trigger();
+  const auto d = [&] {
+    if constexpr (kWhole) return int64_t(a.units) * 8;
+    else return a.d;
+  }();
   int64_t t[U];
   int c[U];
   bool on[U];
@@ -264,7 +272,7 @@ __global__ void __launch_bounds__(MOE_THREADS) moe_dispatch_kernel(const __grid_
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     on[u] = moe_place<kWhole>(a, int64_t(blockIdx.x) * U + u, &t[u], &c[u]);
-    if (on[u]) x[u].start(a.a, t[u], c[u], a.d);
+    if (on[u]) x[u].start(a.a, t[u], c[u], d);
   }
 #pragma unroll
   for (int u = 0; u < U; ++u) {
@@ -278,7 +286,7 @@ __global__ void __launch_bounds__(MOE_THREADS) moe_dispatch_kernel(const __grid_
 #pragma unroll
       for (int j = 0; j < B; ++j)
         if (r[j] >= 0) {
-          T* p = a.o + r[j] * a.d + c[u];
+          T* p = a.o + r[j] * d + c[u];
           store_words(p, store_run<kWhole>(p, c[u], a.d), kWhole ? 8 : a.d - c[u], x[u].m.own);  // the bits as they are
         }
     }
@@ -443,6 +451,13 @@ MoeArgs<T> moe_args(const grs_moe* s, const void* a, const void* b, void* o, con
           s->tokens * s->top_k, s->top_k, s->hidden, units, 0};
 }
 
+// A dispatch of whole fp32 vectors: 16-bit halves, 16 bytes a thread and row.
+MoeArgs<uint16_t> moe_copy_args(const grs_moe* s, const void* x, void* xs, const int32_t* slot_row) {
+  MoeArgs<uint16_t> a = moe_args<uint16_t>(s, x, nullptr, xs, slot_row, nullptr, nullptr, true);
+  a.units *= 2;
+  return a;
+}
+
 // 16-byte aligned vectors of whole 8-element groups.
 bool moe_whole(const grs_moe* s, const void* a, const void* b, const void* o) {
   return s->hidden % 8 == 0 && api_aligned(a, 16) && api_aligned(b, 16) && api_aligned(o, 16);
@@ -478,8 +493,9 @@ cudaError_t moe_launch(MoeOp op, MoeArgs<T> a, void* stream) {
   const int64_t per = (kWhole ? MOE_THREADS : MOE_THREADS / 32) * (dispatch ? U : 1), blocks = (a.tokens * a.units + per - 1) / per;
   if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
   const dim3 grid(static_cast<unsigned>(blocks)), block(MOE_THREADS);
-  return dispatch ? launch_pdl(moe_dispatch_kernel<T, kWhole, U>, grid, block, 0, stream, a)
-                  : launch_pdl(moe_combine_kernel<T, kWhole, B>, grid, block, 0, stream, a);
+  if constexpr (!kWhole || sizeof(T) == 2)  // (whole fp32 vectors are copied as 16-bit halves)
+    if (dispatch) return launch_pdl(moe_dispatch_kernel<T, kWhole, U>, grid, block, 0, stream, a);
+  return launch_pdl(moe_combine_kernel<T, kWhole, B>, grid, block, 0, stream, a);
 }
 
 template <typename T>
@@ -494,13 +510,7 @@ cudaError_t moe_launch(MoeOp op, const MoeArgs<T>& a, bool whole, void* stream) 
 cudaError_t moe_run(MoeOp op, const grs_moe* s, const void* a, const void* b, void* o, const int32_t* slot_row,
                     const float* weights, float* dweights, void* stream) {
   const bool whole = moe_whole(s, a, b, o);
-  if (op == MoeOp::kDispatch && whole && s->dtype == GRS_DTYPE_FP32) {
-    // A copy of bytes: 16 a thread and row.
-    MoeArgs<uint16_t> x = moe_args<uint16_t>(s, a, b, o, slot_row, weights, dweights, whole);
-    x.d *= 2;
-    x.units *= 2;
-    return moe_launch(op, x, true, stream);
-  }
+  if (op == MoeOp::kDispatch && whole && s->dtype == GRS_DTYPE_FP32) return moe_launch(op, moe_copy_args(s, a, o, slot_row), true, stream);
   if (s->dtype == GRS_DTYPE_FP32) {
     const MoeArgs<float> x = moe_args<float>(s, a, b, o, slot_row, weights, dweights, whole);
     return moe_launch(op, x, whole, stream);

@@ -52,6 +52,7 @@ constexpr int LN_WIDE_RED = LN_PEERS * LN_RED_BYTES + 16;  // the warps' sums of
 // 6; bf16 (122) 7812 x 16384 159, 150 and 151.
 template <typename T>
 constexpr int ln_wide_slots = sizeof(T) == 4 ? 3 : 4;
+constexpr uint64_t LN_LINGER_NS = 50000;
 constexpr int LN_PARTS = 304;        // partial rows of dw and db at most: two blocks an SM
 
 __device__ __forceinline__ float ln_load(const uint16_t* p) { return __uint_as_float(uint32_t(*p) << 16); }
@@ -301,7 +302,9 @@ __device__ __forceinline__ float group_sum(float a, const Place& p, int phase) {
 // sends its sums to each block's shared memory, whose barrier of the phase
 // counts their bytes, and every thread adds up the same numbers in the same
 // order.  Who sends to a phase again has taken the sums of the other, so every
-// warp has sent those, after it took what this phase held.
+// warp has sent those, after it took what this phase held.  Hence a warp that
+// gave up a wait sends nothing more: its peers find the next row's sums
+// incomplete and give up in turn, where another row's would complete them.
 __device__ __forceinline__ unsigned cluster_size() {
   unsigned n;
   asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(n));
@@ -338,11 +341,11 @@ __device__ __forceinline__ void cluster_sum2_send(float a, float b, const Place&
 
 // False, for the whole warp, if the sums did not come in time.
 __device__ __forceinline__ bool cluster_sum2_take(float& a, float& b, const Place& p, uint64_t* bar, unsigned peers, int phase,
-                                                  uint32_t parity) {
+                                                  uint32_t parity, uint64_t limit_ns) {
   bool in = mbar_try_wait(bar + phase, parity);
   if (!in) {
     const uint64_t t0 = global_ns();
-    while (!in && global_ns() - t0 <= WAIT_LIMIT_NS) in = mbar_try_wait(bar + phase, parity);
+    while (!in && global_ns() - t0 <= limit_ns) in = mbar_try_wait(bar + phase, parity);
   }
   if (!__all_sync(0xffffffffu, in)) return false;
   a = b = 0.0f;
@@ -515,6 +518,13 @@ __global__ void __launch_bounds__(LN_RING_THREADS) ln_fwd_ring_kernel(const __gr
   ring_wait<0>();  // no copy outlives the slots
 }
 
+// How long a block of a cluster waits for the others' sums.  The self-test
+// has block `quitter` of every cluster give up at its `quit_row`th row.
+struct LnWait {
+  uint64_t limit_ns = WAIT_LIMIT_NS;
+  int32_t quitter = -1, quit_row = 0;
+};
+
 template <typename T, typename W>
 struct LnBwd {
   const T *dy, *x;
@@ -524,6 +534,7 @@ struct LnBwd {
   float* parts;  // [gridDim.x][2][cols], or null
   int64_t ld_dy, ld_x, ld_dx, rows;
   int32_t cols, tpr, span;  // span: columns of a block, where a cluster shares the rows
+  LnWait wait;
 };
 
 // A block's groups walk the rows with the stride of the whole grid; each
@@ -730,9 +741,11 @@ __global__ void __launch_bounds__(LN_BWD_THREADS) ln_bwd_wide_kernel(const __gri
     dx += dx_step;
   };
   cluster_meet();  // every peer has started: its shared memory may be written
-  bool lost = false;  // a wait gave up (never, unless a peer is gone): no number stands for its sums
+  bool lost = false;  // the warp gave up a wait (never, unless a peer is gone): no number stands for sums from there on
   const auto take = [&](float& c1, float& c2, int row_no) {
-    if (!lost) lost = !cluster_sum2_take(c1, c2, p, bar, peers, row_no & 1, (row_no >> 1) & 1);
+    if (!lost)
+      lost = (static_cast<int>(peer) == a.wait.quitter && row_no == a.wait.quit_row) ||
+             !cluster_sum2_take(c1, c2, p, bar, peers, row_no & 1, (row_no >> 1) & 1, a.wait.limit_ns);
     if (lost) c1 = c2 = __int_as_float(0x7fc00000);
   };
   int n = 0;  // this cluster's rows so far
@@ -760,7 +773,7 @@ __global__ void __launch_bounds__(LN_BWD_THREADS) ln_bwd_wide_kernel(const __gri
       const float c1 = warp_sum(s1.x + s1.y), c2 = warp_sum(s2.x + s2.y);
       float l1 = 0.0f, l2 = 0.0f;
       if (n > 0) take(l1, l2, n - 1);
-      cluster_sum2_send(c1, c2, p, bar, peer, peers, n & 1);
+      if (!lost) cluster_sum2_send(c1, c2, p, bar, peer, peers, n & 1);
       if (n > 0) finish(l1, l2);
     }
     ++n;
@@ -780,9 +793,11 @@ __global__ void __launch_bounds__(LN_BWD_THREADS) ln_bwd_wide_kernel(const __gri
     finish(l1, l2);
   }
   ring_wait<0>();  // no copy outlives the slots
-  cluster_meet();  // nor a peer's sums
+  cluster_meet();  // nor a peer's sums, which have been taken
+  if (lost)        // or else were sent before the meeting: far more than their way from a peer (1 us)
+    for (const uint64_t t0 = global_ns(); global_ns() - t0 < LN_LINGER_NS;) {
+    }
   if (a.parts == nullptr) return;
-  if (lost) dw[0] = db[0] = both(__int_as_float(0x7fc00000));
   float* part = a.parts + block * 2 * a.cols + first;
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
@@ -1196,6 +1211,19 @@ cudaError_t ln_backward_wide(const LnBwd<T, W>& args, int32_t* parts, void* stre
                             stream, a);
 }
 
+// Whether whole rows are shared by a cluster: rows wider than a block's
+// registers; fp32 also from 4096, where there are rows enough to pay for the
+// sums' way (12500 x 5120 127 us, 172 in one block; 1562 rows 24.5 and 26.7,
+// 390 rows 12.9 and 10.9).
+template <typename T>
+constexpr int ln_wide_elements = sizeof(T) == 4 ? 8 : 16;  // a thread's
+
+template <typename T>
+bool ln_shares_rows(int64_t rows, int32_t cols) {
+  const bool wide = ln_tpr(cols, 16) > LN_BWD_THREADS || (sizeof(T) == 4 && ln_tpr(cols, 8) > LN_BWD_THREADS && rows >= 4 * 152);
+  return rows > 0 && wide && cols <= LN_PEERS * LN_BWD_THREADS * ln_wide_elements<T>;
+}
+
 // dx, and the parts of dw and db (their number in *parts; 0: not done).
 template <typename T, typename W, int VEC>
 cudaError_t ln_backward_vec(const LnBwd<T, W>& a, int32_t* parts, bool* dx_done, void* stream) {
@@ -1204,14 +1232,9 @@ cudaError_t ln_backward_vec(const LnBwd<T, W>& a, int32_t* parts, bool* dx_done,
   // Fewer elements a thread where registers are short (fp32) or rows few.
   const bool eight = (a.rows <= LN_PARTS || sizeof(T) == 4) && t8 <= LN_BWD_THREADS;
   int32_t unused = 0;
-  if constexpr (VEC > 2) {
-    // fp32 also from 4096, where there are rows enough to pay for the sums' way (12500 x 5120 127 us, 172 in one
-    // block; 1562 rows 24.5 and 26.7, 390 rows 12.9 and 10.9).
-    constexpr int e = sizeof(T) == 4 ? 8 : 16;
-    const bool wide = t16 > LN_BWD_THREADS || (sizeof(T) == 4 && t8 > LN_BWD_THREADS && a.rows >= 4 * 152);
-    if (a.rows > 0 && wide && a.cols <= LN_PEERS * LN_BWD_THREADS * e)
-      return ln_backward_wide<T, W, e>(a, a.parts != nullptr ? parts : &unused, stream);
-  }
+  if constexpr (VEC > 2)
+    if (ln_shares_rows<T>(a.rows, a.cols))
+      return ln_backward_wide<T, W, ln_wide_elements<T>>(a, a.parts != nullptr ? parts : &unused, stream);
   if (a.parts != nullptr) {
     if (eight) return ln_backward_e<T, W, VEC, 8, true>(a, parts, stream);
     if (t16 <= LN_BWD_THREADS) return ln_backward_e<T, W, VEC, 16, true>(a, parts, stream);
@@ -1224,16 +1247,22 @@ cudaError_t ln_backward_vec(const LnBwd<T, W>& a, int32_t* parts, bool* dx_done,
   return cudaSuccess;
 }
 
+// Every row of x, dy and dx and the parameters at multiples of 16 bytes, in whole chunks.
+bool ln_whole_rows(const grs_norm* s, const LnLd& ld, const void* dy, const void* x, const void* w, const void* dx) {
+  const int esize = dtype_size(s->dtype);
+  return s->cols % (16 / esize) == 0 && rows16(x, ld.x, esize) && rows16(dy, ld.dy, esize) && (dx == nullptr || rows16(dx, ld.dx, esize)) &&
+         api_aligned(w, 16);
+}
+
 template <typename T, typename W>
 cudaError_t ln_backward(const grs_norm* s, const LnLd& ld, const void* dy, const void* x, const void* w, const float* mean,
-                        const float* rstd, void* dx, void* dw, void* db, float* ws, void* stream) {
+                        const float* rstd, void* dx, void* dw, void* db, float* ws, const LnWait& wait, void* stream) {
   const bool params = dw != nullptr || db != nullptr;
   const LnBwd<T, W> a{static_cast<const T*>(dy), static_cast<const T*>(x), static_cast<const W*>(w), mean, rstd,
-                      static_cast<T*>(dx), params ? ws : nullptr, ld.dy, ld.x, ld.dx, s->rows, s->cols, 0, s->cols};
+                      static_cast<T*>(dx), params ? ws : nullptr, ld.dy, ld.x, ld.dx, s->rows, s->cols, 0, s->cols, wait};
   if (dx == nullptr && !params) return cudaSuccess;
   constexpr int VEC = 16 / sizeof(T);
-  const bool vec = s->cols % VEC == 0 && rows16(x, ld.x, sizeof(T)) && rows16(dy, ld.dy, sizeof(T)) &&
-                   (dx == nullptr || rows16(dx, ld.dx, sizeof(T))) && api_aligned(w, 16);
+  const bool vec = ln_whole_rows(s, ld, dy, x, w, dx);
   int32_t parts = 0;
   bool dx_done = false;
   cudaError_t e = vec ? ln_backward_vec<T, W, VEC>(a, &parts, &dx_done, stream) : ln_backward_vec<T, W, 2>(a, &parts, &dx_done, stream);
@@ -1303,9 +1332,8 @@ grs_status grs_layernorm_forward(const grs_norm* s, const void* x, const void* w
   return e == cudaSuccess ? GRS_OK : api_cuda_fail(e, who);
 }
 
-grs_status grs_layernorm_backward(const grs_norm* s, const void* dy, const void* x, const void* w, const float* mean,
-                                  const float* rstd, void* dx, void* dw, void* db, void* workspace, void* stream) {
-  static const char who[] = "grs_layernorm_backward";
+static grs_status backward(const grs_norm* s, const void* dy, const void* x, const void* w, const float* mean, const float* rstd,
+                           void* dx, void* dw, void* db, void* workspace, const LnWait& wait, void* stream, const char* who) {
   LnLd ld;
   const grs_status st = check_norm(s, who, &ld);
   if (st != GRS_OK) return st;
@@ -1318,13 +1346,31 @@ grs_status grs_layernorm_backward(const grs_norm* s, const void* dy, const void*
       !api_aligned(db, ga) || !api_aligned(mean, 4) || !api_aligned(rstd, 4))
     return api_fail(GRS_ERR_ALIGNMENT, who, "a pointer is not aligned to its element");
   if (params && !api_aligned(workspace, 16)) return api_fail(GRS_ERR_ALIGNMENT, who, "workspace not 16-byte aligned");
+  if (wait.quitter >= 0 && (dx == nullptr || !ln_whole_rows(s, ld, dy, x, w, dx) ||
+                            !(s->dtype == GRS_DTYPE_FP32 ? ln_shares_rows<float>(s->rows, s->cols) : ln_shares_rows<uint16_t>(s->rows, s->cols))))
+    return api_fail(GRS_ERR_SHAPE, who, "no rows that blocks share");
   const bool f = s->dtype == GRS_DTYPE_FP32, pf = s->param_dtype == GRS_DTYPE_FP32;
   float* ws = static_cast<float*>(workspace);
-  const cudaError_t e = f ? (pf ? ln_backward<float, float>(s, ld, dy, x, w, mean, rstd, dx, dw, db, ws, stream)
-                                : ln_backward<float, uint16_t>(s, ld, dy, x, w, mean, rstd, dx, dw, db, ws, stream))
-                          : (pf ? ln_backward<uint16_t, float>(s, ld, dy, x, w, mean, rstd, dx, dw, db, ws, stream)
-                                : ln_backward<uint16_t, uint16_t>(s, ld, dy, x, w, mean, rstd, dx, dw, db, ws, stream));
+  const cudaError_t e = f ? (pf ? ln_backward<float, float>(s, ld, dy, x, w, mean, rstd, dx, dw, db, ws, wait, stream)
+                                : ln_backward<float, uint16_t>(s, ld, dy, x, w, mean, rstd, dx, dw, db, ws, wait, stream))
+                          : (pf ? ln_backward<uint16_t, float>(s, ld, dy, x, w, mean, rstd, dx, dw, db, ws, wait, stream)
+                                : ln_backward<uint16_t, uint16_t>(s, ld, dy, x, w, mean, rstd, dx, dw, db, ws, wait, stream));
   return e == cudaSuccess ? GRS_OK : api_cuda_fail(e, who);
+}
+
+grs_status grs_layernorm_backward(const grs_norm* s, const void* dy, const void* x, const void* w, const float* mean,
+                                  const float* rstd, void* dx, void* dw, void* db, void* workspace, void* stream) {
+  return backward(s, dy, x, w, mean, rstd, dx, dw, db, workspace, LnWait{}, stream, "grs_layernorm_backward");
+}
+
+grs_status grs_selftest_layernorm_wait(const grs_norm* s, const void* dy, const void* x, const void* w, const float* mean,
+                                       const float* rstd, void* dx, void* dw, void* db, void* workspace, int64_t limit_ns,
+                                       int32_t quitter, int32_t quit_row, void* stream) {
+  static const char who[] = "grs_selftest_layernorm_wait";
+  if (limit_ns < 1000 || limit_ns > 2000000000LL) return api_fail(GRS_ERR_INVALID_ARG, who, "limit_ns must be in [1 us, 2 s]");
+  if (quitter < 0 || quit_row < 0) return api_fail(GRS_ERR_INVALID_ARG, who, "quitter and quit_row must be >= 0");
+  const LnWait wait{static_cast<uint64_t>(limit_ns), quitter, quit_row};
+  return backward(s, dy, x, w, mean, rstd, dx, dw, db, workspace, wait, stream, who);
 }
 
 }  // extern "C"

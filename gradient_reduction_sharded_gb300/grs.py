@@ -167,6 +167,7 @@ _sig = {
     "grs_layernorm_forward": ([_P(grs_norm)] + [_vp] * 7, ctypes.c_int),
     "grs_layernorm_backward": ([_P(grs_norm)] + [_vp] * 10, ctypes.c_int),
     "grs_layernorm_workspace_bytes": ([_P(grs_norm)], ctypes.c_int64),
+    "grs_selftest_layernorm_wait": ([_P(grs_norm)] + [_vp] * 9 + [ctypes.c_int64, ctypes.c_int32, ctypes.c_int32, _vp], ctypes.c_int),
     "grs_moe_sort": ([_P(grs_moe)] + [_vp] * 6, ctypes.c_int),
     "grs_moe_workspace_bytes": ([_P(grs_moe)], ctypes.c_int64),
     "grs_moe_dispatch": ([_P(grs_moe)] + [_vp] * 4, ctypes.c_int),
@@ -489,6 +490,13 @@ def _bytes(n: int, func: str) -> int:
 
 def grs_layernorm_workspace_bytes(shape: grs_norm) -> int:
     return _bytes(int(_lib.grs_layernorm_workspace_bytes(ctypes.byref(shape))), "grs_layernorm_workspace_bytes")
+
+
+def grs_selftest_layernorm_wait(shape: grs_norm, dy: int, x: int, w: Optional[int], mean: int, rstd: int, dx: int,
+                                dw: Optional[int], db: Optional[int], workspace: Optional[int], limit_ns: int,
+                                quitter: int, quit_row: int, stream: int) -> None:
+    _check(_lib.grs_selftest_layernorm_wait(ctypes.byref(shape), dy, x, w, mean, rstd, dx, dw, db, workspace, limit_ns,
+                                            quitter, quit_row, stream), "grs_selftest_layernorm_wait")
 
 
 def make_moe(tokens: int, top_k: int, n_experts: int, expert_begin: int, expert_end: int, hidden: int,

@@ -518,6 +518,9 @@ __global__ void __launch_bounds__(LN_RING_THREADS) ln_fwd_ring_kernel(const __gr
   ring_wait<0>();  // no copy outlives the slots
 }
 
+// Set by a warp that gave up a wait; the calls have no handle to keep it in.
+__device__ int ln_gave_up;
+
 // How long a block of a cluster waits for the others' sums.  The self-test
 // has block `quitter` of every cluster give up at its `quit_row`th row.
 struct LnWait {
@@ -794,9 +797,11 @@ __global__ void __launch_bounds__(LN_BWD_THREADS) ln_bwd_wide_kernel(const __gri
   }
   ring_wait<0>();  // no copy outlives the slots
   cluster_meet();  // nor a peer's sums, which have been taken
-  if (lost)        // or else were sent before the meeting: far more than their way from a peer (1 us)
+  if (lost) {      // or else were sent before the meeting: far more than their way from a peer (1 us)
+    if ((threadIdx.x & 31) == 0) atomicExch(&ln_gave_up, 1);
     for (const uint64_t t0 = global_ns(); global_ns() - t0 < LN_LINGER_NS;) {
     }
+  }
   if (a.parts == nullptr) return;
   float* part = a.parts + block * 2 * a.cols + first;
 #pragma unroll
@@ -1371,6 +1376,20 @@ grs_status grs_selftest_layernorm_wait(const grs_norm* s, const void* dy, const 
   if (quitter < 0 || quit_row < 0) return api_fail(GRS_ERR_INVALID_ARG, who, "quitter and quit_row must be >= 0");
   const LnWait wait{static_cast<uint64_t>(limit_ns), quitter, quit_row};
   return backward(s, dy, x, w, mean, rstd, dx, dw, db, workspace, wait, stream, who);
+}
+
+grs_status grs_layernorm_check_device_errors(void* stream) {
+  static const char who[] = "grs_layernorm_check_device_errors";
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  void* flag = nullptr;
+  int gave_up = 0;
+  cudaError_t e = cudaStreamSynchronize(st);
+  if (e == cudaSuccess) e = cudaGetSymbolAddress(&flag, ln_gave_up);
+  if (e == cudaSuccess) e = cudaMemcpy(&gave_up, flag, sizeof(gave_up), cudaMemcpyDeviceToHost);
+  if (e == cudaSuccess) e = cudaMemsetAsync(flag, 0, sizeof(gave_up), st);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(st);
+  if (e != cudaSuccess) return api_cuda_fail(e, who);
+  return gave_up != 0 ? api_fail(GRS_ERR_TIMEOUT, who, "a bounded device wait timed out") : GRS_OK;
 }
 
 }  // extern "C"

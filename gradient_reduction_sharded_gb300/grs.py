@@ -167,6 +167,7 @@ _sig = {
     "grs_layernorm_forward": ([_P(grs_norm)] + [_vp] * 7, ctypes.c_int),
     "grs_layernorm_backward": ([_P(grs_norm)] + [_vp] * 10, ctypes.c_int),
     "grs_layernorm_workspace_bytes": ([_P(grs_norm)], ctypes.c_int64),
+    "grs_layernorm_check_device_errors": ([_vp], ctypes.c_int),
     "grs_selftest_layernorm_wait": ([_P(grs_norm)] + [_vp] * 9 + [ctypes.c_int64, ctypes.c_int32, ctypes.c_int32, _vp], ctypes.c_int),
     "grs_moe_sort": ([_P(grs_moe)] + [_vp] * 6, ctypes.c_int),
     "grs_moe_workspace_bytes": ([_P(grs_moe)], ctypes.c_int64),
@@ -490,6 +491,14 @@ def _bytes(n: int, func: str) -> int:
 
 def grs_layernorm_workspace_bytes(shape: grs_norm) -> int:
     return _bytes(int(_lib.grs_layernorm_workspace_bytes(ctypes.byref(shape))), "grs_layernorm_workspace_bytes")
+
+
+def grs_layernorm_check_device_errors(stream: int) -> int:
+    """Returns the status (raises only for CUDA errors)."""
+    st = _lib.grs_layernorm_check_device_errors(stream)
+    if st == GRS_ERR_CUDA:
+        _check(st, "grs_layernorm_check_device_errors")
+    return st
 
 
 def grs_selftest_layernorm_wait(shape: grs_norm, dy: int, x: int, w: Optional[int], mean: int, rstd: int, dx: int,

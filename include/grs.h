@@ -747,18 +747,22 @@ grs_status grs_layernorm_forward(const grs_norm* shape, const void* x, const voi
  * Blocks that share wide rows wait for one another's sums.  Where such a wait
  * gives up (after 2 s, which only a defect can cause), dx is NaN in the
  * columns concerned of that row and in all of the rows that the blocks share
- * after it; dw and db do not depend on these sums. */
+ * after it, and grs_layernorm_check_device_errors reports it; dw and db do not
+ * depend on these sums. */
 grs_status grs_layernorm_backward(const grs_norm* shape, const void* dy, const void* x, const void* w,
                                   const float* mean, const float* rstd, void* dx, void* dw, void* db,
                                   void* workspace, void* stream);
 /* Bytes, or -1 for a shape that the calls refuse. */
 int64_t grs_layernorm_workspace_bytes(const grs_norm* shape);
+/* Synchronise `stream`, read and clear the current device's flag, which the
+ * calls of all its streams share: TIMEOUT if a wait gave up, else OK (or CUDA). */
+grs_status grs_layernorm_check_device_errors(void* stream);
 /* Failure-detection self-test: grs_layernorm_backward of rows that blocks
  * share (whole rows of more than 8192 elements, fp32 from 608 rows of more
  * than 4096; others are refused with SHAPE, as is a NULL dx), in which block
  * `quitter` of those that share a row gives up its wait in its quit_row-th row
  * (from 0) and the others wait limit_ns at most (1 us .. 2 s).  The call ends,
- * leaves NaN as above and the CUDA context usable. */
+ * leaves NaN and the flag as above and the CUDA context usable. */
 grs_status grs_selftest_layernorm_wait(const grs_norm* shape, const void* dy, const void* x, const void* w,
                                        const float* mean, const float* rstd, void* dx, void* dw, void* db,
                                        void* workspace, int64_t limit_ns, int32_t quitter, int32_t quit_row,

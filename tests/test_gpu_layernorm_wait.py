@@ -34,6 +34,8 @@ def test_a_lost_wait_leaves_nan_and_nothing_wrong(grs, act, cols, rows, quitter,
         check(got, w64, bound, what)
     full = c.backward()[0]
     lost = torch.isnan(gx)
+    status = grs.grs_layernorm_check_device_errors(torch.cuda.current_stream().cuda_stream)
+    assert status == (grs.GRS_ERR_TIMEOUT if lost.any() else grs.GRS_OK)
     assert torch.equal(gx[~lost], full[~lost])  # right wherever it is a number
     # A cluster has every n-th row.  Its rows before the lost one are whole, of that one the block's columns are lost, then all.
     share = lost.float().mean(1)
@@ -47,6 +49,26 @@ def test_a_lost_wait_leaves_nan_and_nothing_wrong(grs, act, cols, rows, quitter,
         assert (share[:first] == 0).all() and (share[first + len(part):] == 1).all()
     assert torch.equal(c.backward()[0], full)
     check(full, *want[0], "dx")
+
+
+def test_a_lost_wait_is_reported(grs):  # noqa: F811
+    """Once, to the first check after it, also where it was on another stream; the calls that go well report nothing."""
+    c = Case(grs, 100, 16384, "bf16", "bf16", "fp32", seed=5)
+    c.forward()
+    st = torch.cuda.current_stream().cuda_stream
+    c.backward()
+    assert grs.grs_layernorm_check_device_errors(st) == grs.GRS_OK
+    quit_at(c, "bf16", "bf16", 2_000_000, 1, 0)
+    assert grs.grs_layernorm_check_device_errors(st) == grs.GRS_ERR_TIMEOUT
+    assert "timed out" in grs.grs_last_error()
+    assert grs.grs_layernorm_check_device_errors(st) == grs.GRS_OK
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        quit_at(c, "bf16", "bf16", 2_000_000, 0, 0)
+    assert grs.grs_layernorm_check_device_errors(side.cuda_stream) == grs.GRS_ERR_TIMEOUT
+    c.backward()
+    assert grs.grs_layernorm_check_device_errors(st) == grs.GRS_OK
 
 
 def test_refusals(grs):  # noqa: F811

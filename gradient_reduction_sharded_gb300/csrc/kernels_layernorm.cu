@@ -27,7 +27,6 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
-#include <atomic>
 #include <cmath>
 
 #include "api_util.h"
@@ -1162,31 +1161,17 @@ cudaError_t ln_backward_e(const LnBwd<T, W>& args, int32_t* parts, void* stream)
   return launch_pdl(ln_bwd_kernel<T, W, VEC, E, kParams>, dim3(static_cast<unsigned>(grid)), dim3(threads), ring > sums ? ring : sums, stream, a);
 }
 
-// Clusters of `peers` blocks that the device holds at once: fewer than the SMs
-// would hold, where a GPC's are no multiple of it.  Asked once a shape.
-template <auto* Kernel>
-cudaError_t resident_clusters(int peers, int threads, unsigned smem, int64_t* clusters) {
-  static std::atomic<int> known[LN_PEERS + 1][LN_BWD_THREADS / 32 + 1];
-  std::atomic<int>& at = known[peers][threads / 32];
-  int n = at.load(std::memory_order_relaxed);
-  if (n == 0) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(peers));
-    cfg.blockDim = dim3(static_cast<unsigned>(threads));
-    cfg.dynamicSmemBytes = smem;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = static_cast<unsigned>(peers);
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    const cudaError_t e = cudaOccupancyMaxActiveClusters(&n, Kernel, &cfg);
-    if (e != cudaSuccess) return e;
-    if (n < 1) n = 1;
-    at.store(n, std::memory_order_relaxed);
-  }
-  *clusters = n;
-  return cudaSuccess;
+// Clusters of `peers` blocks: as many as a GB300 holds at once, 152 SMs in GPCs
+// that are no multiple of 4 or 8.  Fixed numbers, not what a device says of
+// itself: each cluster leaves one part of dw and db, so their order of
+// addition would go with the device.  One that holds fewer takes them in turn.
+// Blocks an SM by registers: bf16 one (128 a thread), fp32 three of up to 320
+// threads, else two (64).
+template <typename T>
+int32_t ln_wide_clusters(int peers, int threads) {
+  const int blocks = sizeof(T) == 2 ? 1 : threads <= 320 ? 3 : 2;
+  constexpr int32_t held[3][3] = {{76, 152, 228}, {36, 74, 110}, {15, 36, 51}};
+  return held[peers == 2 ? 0 : peers == 4 ? 1 : 2][blocks - 1];
 }
 
 // Rows over the blocks of a cluster: 2, 4 or 8 of them, as few as hold a row
@@ -1203,13 +1188,10 @@ cudaError_t ln_backward_wide(const LnBwd<T, W>& args, int32_t* parts, void* stre
   constexpr int slots = ln_wide_slots<T> * 2 * E * static_cast<int>(sizeof(T));  // a thread's
   static_assert(LN_WIDE_RED + slots * LN_BWD_THREADS <= 227 * 1024, "shared memory of a block");
   constexpr auto* kernel = ln_bwd_wide_kernel<T, W, E>;
-  cudaError_t e = allow_smem<kernel>(LN_WIDE_RED + slots * LN_BWD_THREADS);
+  const cudaError_t e = allow_smem<kernel>(LN_WIDE_RED + slots * LN_BWD_THREADS);
   if (e != cudaSuccess) return e;
   const unsigned smem = LN_WIDE_RED + slots * a.tpr;
-  int64_t clusters = 0;
-  e = resident_clusters<kernel>(peers, a.tpr, smem, &clusters);
-  if (e != cudaSuccess) return e;
-  if (clusters > LN_PARTS) clusters = LN_PARTS;
+  int64_t clusters = ln_wide_clusters<T>(peers, a.tpr);
   if (clusters > a.rows) clusters = a.rows;
   *parts = static_cast<int32_t>(clusters);
   return launch_pdl_cluster(kernel, static_cast<unsigned>(peers), dim3(static_cast<unsigned>(clusters * peers)), dim3(a.tpr), smem,

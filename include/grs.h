@@ -741,8 +741,10 @@ grs_status grs_layernorm_forward(const grs_norm* shape, const void* x, const voi
  *   dx = rstd * (dh - mean_C(dh) - h * mean_C(dh * h)),
  *   dw = sum over rows of dy * h,  db = sum over rows of dy (overwritten;
  *   zeros when rows is 0), each of the three NULL if not wanted.
- * Sums in fp32 in an order that the shape alone fixes: the same call gives the
- * same bits.  workspace: device, 16-byte aligned, grs_layernorm_workspace_bytes
+ * Sums in fp32 in an order that the shape, the types and two facts about the
+ * addresses fix, whether all rows of x, dy and dx are whole 16-byte chunks at
+ * 16-byte boundaries and whether w starts at one: such calls give the same
+ * bits on every device.  workspace: device, 16-byte aligned, grs_layernorm_workspace_bytes
  * (not initialised), needed for dw or db.  No output may overlap an input.
  * Blocks that share wide rows wait for one another's sums.  Where such a wait
  * gives up (after 2 s, which only a defect can cause), dx is NaN in the

@@ -413,8 +413,9 @@ __device__ __forceinline__ float reciprocal(float x) {
 // AdamW on one element.  What the next state comes from (m, v, sqrt(v)) is
 // rounded product by product and sum by sum; the parameter's own step, which
 // no state depends on, takes fused products and the fast reciprocal (1 unit in
-// the last place; the step's error is about 2^-22 of lr).  V comes in as v and leaves
-// as sqrt(v).  Scalar on purpose: a factor from the constant bank costs a
+// the last place; the step's error is about 2^-22 of itself), which takes a
+// denominator below the normal numbers for zero: lift_denominator() keeps it
+// above them.  V comes in as v and leaves as sqrt(v).  Scalar on purpose: a factor from the constant bank costs a
 // scalar product nothing, a paired one two moves.
 __device__ __forceinline__ void adamw_elem_sep(float g, const ListArgs& a, float& P, float& M, float& V) {
   const AdamwK& k = a.k;
@@ -617,6 +618,16 @@ ListArgs list_args(const grs_tensors* l, const grs_adamw* hp, const double* d_no
   return a;
 }
 
+// Where eps is so small that it may leave the normal numbers, the denominator
+// and the step are both 2^30 as large: powers of two, so the quotient is the
+// same.  (The smallest eps is 2^-149, the smallest positive sqrt(v) 2^-75.)
+void lift_denominator(ListArgs* a) {
+  if (a->k.eps >= 0x1p-100f) return;
+  a->k.eps *= 0x1p30f;
+  a->inv_bc2_sqrt *= 0x1p30f;
+  a->step_size *= 0x1p30f;
+}
+
 template <bool k8>
 grs_status launch_list_step(const grs_tensors* l, const ListArgs& a, int32_t grad_dtype, void* stream, const char* who) {
   if (l->n_tiles == 0) return GRS_OK;
@@ -788,6 +799,7 @@ grs_status grs_tensors_adamw8_step(const grs_tensors* l, const grs_adamw* hp, ui
   a.m_scale = m_scale;
   a.s_scale = s_scale;
   a.keys = make_keys(seed);
+  lift_denominator(&a);
   return launch_list_step<true>(l, a, grad_dtype, stream, who);
 }
 

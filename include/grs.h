@@ -669,9 +669,11 @@ grs_status grs_tensors_adamw_step(const grs_tensors* list, const grs_adamw* hp, 
  * <= 256 (scale >= 2^-126), so that nothing saturates and the scaling is
  * exact.  All-zero codes and scales stand for zero: the states before the
  * first step.
- * Step: the moments are read as fp32, stepped and used in fp32 as in the
- * 32-bit form (products and sums rounded one by one, so that the codes are
- * reproducible by any IEEE arithmetic), and only then rounded to 8 bits.
+ * Step: the moments are read as fp32, stepped and used in fp32, and only then
+ * rounded to 8 bits.  The moments' products and sums are rounded one by one as
+ * in the 32-bit form, so that the codes are reproducible by any IEEE
+ * arithmetic; the parameter takes fused products and a reciprocal of 1 unit in
+ * the last place, so its step is the 32-bit form's to 2^-21 of itself.
  * Rounding is stochastic: up with the probability of the fraction cut off,
  * from 16 random bits an element that are a hash of `seed` and the element's
  * index in the state arrays (same seed, same result; give each step another).  With

@@ -639,8 +639,12 @@ grs_status grs_tensors_query(const grs_tensors* list, grs_tensors_info* out);
 grs_status grs_tensors_offset(const grs_tensors* list, int32_t tensor, int64_t* out);
 
 /* S = sum over every tensor with a gradient of (g / n_micro)^2 to *d_norm_sq
- * (device double), deterministic: fixed tiles of 2048 elements, summed as
- * unevaluated pairs of floats (48 bits), then fp64 in a fixed order.  A non-finite S raises the flag that
+ * (device double), deterministic: fixed tiles of 2048 elements, whose ends
+ * move back to the tensor's 16-byte boundaries (so the last bits go with the
+ * addresses modulo 16), summed as unevaluated pairs of floats, then fp64 in a
+ * fixed order.  S is exact to 2^-36 of itself and 2^-149 an element for
+ * gradients of magnitudes up to 2^61; beyond, squares leave fp32's range and S
+ * may be infinite.  A non-finite S raises the flag that
  * grs_tensors_check_device_errors reports.  workspace: device, 16-byte
  * aligned, workspace_bytes, zeroed once before its first use; calls that
  * share one must not overlap.  Errors: INVALID_ARG, ALIGNMENT, NO_DEVICE,

@@ -834,11 +834,14 @@ grs_status grs_moe_combine_backward(const grs_moe* shape, const void* dy, const 
                                     const float* weights, void* dys, float* dweights, void* stream);
 
 /* Build features of the loaded library.  GRS_FEATURE_CHECKED: compiled with
- * GRS_CHECKED=1 — every kernel checks each index it derives against the
- * extent of the buffer it addresses (the sizes this header documents for
- * that call) before the access; a failed check skips the access and raises
- * a device flag that grs_check_device_errors reports as BOUNDS (the message
- * names the kernel).  Slower; for tests and debugging. */
+ * GRS_CHECKED=1 — every kernel that works on a plan checks each index it
+ * derives against the extent of the buffer it addresses (the sizes this header
+ * documents for that call) before the access, every kernel that works on a
+ * list of tensors its tile's record; a failed check skips the access and
+ * raises a device flag that grs_check_device_errors, for a list
+ * grs_tensors_check_device_errors, reports as BOUNDS (the message of the
+ * former names the kernel).  The kernels of grs_layernorm_* and grs_moe_* have
+ * no such checks.  Slower; for tests and debugging. */
 #define GRS_FEATURE_CHECKED 1u
 uint32_t grs_build_features(void);
 

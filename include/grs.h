@@ -602,8 +602,10 @@ typedef enum grs_dtype {
 
 /* AdamW over a list of tensors that keep their own storage, for parameters
  * outside a reduction plan, and with its states in 32 or in 8 bits for any
- * parameters: a plan's arrays (acc, master, params_bf16, each
- * [n_state_pad]), or a shard view's, are a list of one tensor.
+ * parameters: a plan's arrays, or a shard view's, are a list of one tensor of
+ * n_state_pad elements, acc its gradient and params_bf16 its parameter.  Its
+ * state arrays, master among them, have the list's n_state elements, up to 255
+ * more than the plan's: allocate the plan's master that long.
  *
  * The list's layout is fixed at creation: tensor i's state begins at element
  * grs_tensors_offset(i) of the state arrays, which have n_state elements

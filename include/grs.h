@@ -812,8 +812,8 @@ grs_status grs_moe_sort(const grs_moe* shape, const int32_t* expert_ids, int32_t
 int64_t grs_moe_workspace_bytes(const grs_moe* shape);
 
 /* The calls below take vectors as contiguous rows of `hidden` elements,
- * aligned to the element (16 bytes and hidden * size a multiple of 16 are
- * fastest).  An entry of slot_row outside [0, tokens * top_k) stands for no
+ * aligned to the element (16 bytes, with hidden a multiple of 8, is fastest
+ * in either type).  An entry of slot_row outside [0, tokens * top_k) stands for no
  * row; the entries that do not must differ from each other.  Rows beyond the
  * largest entry are neither read nor written, so xs, ys, dxs and dys need no
  * more: with grs_moe_sort's map the rows up to the last of expert_offsets.

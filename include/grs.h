@@ -685,7 +685,8 @@ grs_status grs_tensors_adamw_step(const grs_tensors* list, const grs_adamw* hp, 
  * index in the state arrays (same seed, same result; give each step another).  With
  * beta2 near 1 a step moves sqrt(v) by far less than the distance between
  * two codes: rounding to nearest would keep it where it is, stochastic
- * rounding moves it right on average.  A positive sqrt(v) never becomes
+ * rounding moves it right on average.  Unbiased in sqrt(v), it adds its
+ * variance to v: with beta2 = 0.999 about 5 % once v has settled.  A positive sqrt(v) never becomes
  * zero.  A block that holds a NaN or an infinity gets the scale NaN and code
  * 0: all of its moments are NaN from then on.
  *   m8, s8        : device uint8 [n_state], 16-byte aligned.
@@ -741,7 +742,7 @@ typedef struct grs_norm {
  *   elements apart; rows that start at multiples of 16 bytes are fastest.
  *   w, b    : device [cols], or NULL (1 and 0).
  *   mean, rstd : device fp32 [rows], kept for the backward pass, or NULL.
- * Runs on the current device.  Errors: INVALID_ARG, SHAPE, ALIGNMENT, CUDA. */
+ * No output may overlap an input.  Runs on the current device.  Errors: INVALID_ARG, SHAPE, ALIGNMENT, CUDA. */
 grs_status grs_layernorm_forward(const grs_norm* shape, const void* x, const void* w, const void* b, void* y,
                                  float* mean, float* rstd, void* stream);
 

@@ -670,7 +670,7 @@ __global__ void __launch_bounds__(LN_BWD_THREADS) ln_bwd_kernel(const __grid_con
 //   send row i's  ->  dx of row i - 1, its elements read from the ring again.
 // (With a barrier of the cluster in place of the counted sends, its release
 // waits for dx: 2.3 us a row instead of 1.3.)  256 MB in rows of 16384: bf16
-// 150 us (5.1 TB/s), fp32 131; with a pass for dx and another over x and dy
+// 150 us (5.1 TB/s), fp32 131 to 151; with a pass for dx and another over x and dy
 // for dw and db 280 and 308.  The ring is read by who filled it, so a slot
 // may be filled again two rows on without a barrier.
 template <typename T, typename W, int E>

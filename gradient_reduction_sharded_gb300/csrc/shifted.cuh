@@ -213,8 +213,9 @@ __device__ __forceinline__ void load_shifted(const uint8_t* p, uint32_t (&o)[N])
   shift_words<MIS>(own, next, o);
 }
 
-// Elements [0, n) of the lane's 8 at p, zeros beyond, at once (with fewer registers than
-// a Moving takes); whole warp.
+// Elements [0, n) of the lane's 8 at p, zeros beyond, at once; whole warp.
+// Beside Moving for its registers: of the list step's 48 it spills 0 to 32
+// bytes, a Moving 24 to 112.
 __device__ __forceinline__ void load8(const uint16_t* p, Run r, int n, float2 (&o)[4]) {
   uint32_t w[4];
   if (r.mis == 0 && n >= 8) {

@@ -39,6 +39,7 @@ GRS_DTYPE_BF16, GRS_DTYPE_FP32 = 0, 1
 GRS_STATE_BLOCK = 256
 GRS_MOE_MAX_EXPERTS = 1024
 GRS_MAX_WIDTH = 1 << 30
+GRS_QK_MAX_DIM = 1024
 
 STATUS_NAMES = {0: "OK", 1: "INVALID_ARG", 2: "UNSUPPORTED_COMPOSITION", 3: "SHAPE",
                 4: "ALIGNMENT", 5: "CUDA", 6: "TIMEOUT", 7: "NONFINITE", 8: "NO_DEVICE",
@@ -109,6 +110,24 @@ class grs_moe(ctypes.Structure):
                 ("reserved", ctypes.c_int32)]
 
 
+class grs_experts(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("ld_x", ctypes.c_int64), ("ld_y", ctypes.c_int64), ("experts", ctypes.c_int32),
+                ("in_features", ctypes.c_int32), ("out_features", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("grad_dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class grs_embedding(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int64), ("row_begin", ctypes.c_int32), ("row_end", ctypes.c_int32), ("hidden", ctypes.c_int32),
+                ("scale", ctypes.c_float), ("dtype", ctypes.c_int32), ("grad_dtype", ctypes.c_int32), ("reserved", ctypes.c_int32 * 2)]
+
+
+class grs_qk_norm(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int64), ("ld_q", ctypes.c_int64), ("ld_k", ctypes.c_int64), ("ld_qo", ctypes.c_int64),
+                ("ld_ko", ctypes.c_int64), ("q_heads", ctypes.c_int32), ("k_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("rotary_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("eps", ctypes.c_float), ("dtype", ctypes.c_int32),
+                ("param_dtype", ctypes.c_int32), ("grad_dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
 if not os.path.exists(LIB_PATH):
     raise ImportError(f"{LIB_PATH} is missing: build it with __graft_entry__.build() "
                       "(there is no CPU fallback)")
@@ -175,6 +194,17 @@ _sig = {
     "grs_moe_dispatch_backward": ([_P(grs_moe)] + [_vp] * 4, ctypes.c_int),
     "grs_moe_combine": ([_P(grs_moe)] + [_vp] * 5, ctypes.c_int),
     "grs_moe_combine_backward": ([_P(grs_moe)] + [_vp] * 7, ctypes.c_int),
+    "grs_operators_check_device_errors": ([_vp], ctypes.c_int),
+    "grs_experts_forward": ([_P(grs_experts)] + [_vp] * 6, ctypes.c_int),
+    "grs_experts_backward": ([_P(grs_experts)] + [_vp] * 8, ctypes.c_int),
+    "grs_experts_workspace_bytes": ([_P(grs_experts)], ctypes.c_int64),
+    "grs_embedding_forward": ([_P(grs_embedding)] + [_vp] * 4, ctypes.c_int),
+    "grs_embedding_backward": ([_P(grs_embedding)] + [_vp] * 5, ctypes.c_int),
+    "grs_embedding_workspace_bytes": ([_P(grs_embedding)], ctypes.c_int64),
+    "grs_rope_turns": ([_P(ctypes.c_double), ctypes.c_int32, _P(ctypes.c_uint64)], ctypes.c_int),
+    "grs_qk_norm_forward": ([_P(grs_qk_norm)] + [_vp] * 9, ctypes.c_int),
+    "grs_qk_norm_backward": ([_P(grs_qk_norm)] + [_vp] * 14, ctypes.c_int),
+    "grs_qk_norm_workspace_bytes": ([_P(grs_qk_norm)], ctypes.c_int64),
     "grs_last_error": ([], ctypes.c_char_p),
     "grs_build_features": ([], ctypes.c_uint32),
 }
@@ -543,3 +573,78 @@ def grs_moe_combine_backward(shape: grs_moe, dy: int, ys: int, slot_row: int, we
                              stream: int) -> None:
     _check(_lib.grs_moe_combine_backward(ctypes.byref(shape), dy, ys, slot_row, weights, dys, dweights, stream),
            "grs_moe_combine_backward")
+
+
+def grs_operators_check_device_errors(stream: int) -> int:
+    """Returns the status (raises only for CUDA errors)."""
+    st = _lib.grs_operators_check_device_errors(stream)
+    if st == GRS_ERR_CUDA:
+        _check(st, "grs_operators_check_device_errors")
+    return st
+
+
+def make_experts(rows: int, experts: int, in_features: int, out_features: int, dtype: int, grad_dtype: int, ld_x: int = 0,
+                 ld_y: int = 0) -> grs_experts:
+    return grs_experts(rows, ld_x, ld_y, experts, in_features, out_features, dtype, grad_dtype, 0)
+
+
+def grs_experts_workspace_bytes(shape: grs_experts) -> int:
+    return _bytes(int(_lib.grs_experts_workspace_bytes(ctypes.byref(shape))), "grs_experts_workspace_bytes")
+
+
+def grs_experts_forward(shape: grs_experts, xs: int, w: int, offsets: int, ys: int, workspace: Optional[int], stream: int) -> None:
+    _check(_lib.grs_experts_forward(ctypes.byref(shape), xs, w, offsets, ys, workspace, stream), "grs_experts_forward")
+
+
+def grs_experts_backward(shape: grs_experts, dys: int, xs: Optional[int], w: Optional[int], offsets: int, dxs: Optional[int],
+                         dw: Optional[int], workspace: Optional[int], stream: int) -> None:
+    _check(_lib.grs_experts_backward(ctypes.byref(shape), dys, xs, w, offsets, dxs, dw, workspace, stream),
+           "grs_experts_backward")
+
+
+def make_embedding(tokens: int, row_begin: int, row_end: int, hidden: int, scale: float, dtype: int,
+                   grad_dtype: int) -> grs_embedding:
+    return grs_embedding(tokens, row_begin, row_end, hidden, scale, dtype, grad_dtype)
+
+
+def grs_embedding_workspace_bytes(shape: grs_embedding) -> int:
+    return _bytes(int(_lib.grs_embedding_workspace_bytes(ctypes.byref(shape))), "grs_embedding_workspace_bytes")
+
+
+def grs_embedding_forward(shape: grs_embedding, ids: int, table: int, y: int, stream: int) -> None:
+    _check(_lib.grs_embedding_forward(ctypes.byref(shape), ids, table, y, stream), "grs_embedding_forward")
+
+
+def grs_embedding_backward(shape: grs_embedding, ids: int, dy: int, dtable: int, workspace: Optional[int], stream: int) -> None:
+    _check(_lib.grs_embedding_backward(ctypes.byref(shape), ids, dy, dtable, workspace, stream), "grs_embedding_backward")
+
+
+def make_qk_norm(tokens: int, q_heads: int, k_heads: int, head_dim: int, rotary_dim: int, eps: float, dtype: int, param_dtype: int,
+                 grad_dtype: int, interleaved: bool = False, ld_q: int = 0, ld_k: int = 0, ld_qo: int = 0,
+                 ld_ko: int = 0) -> grs_qk_norm:
+    return grs_qk_norm(tokens, ld_q, ld_k, ld_qo, ld_ko, q_heads, k_heads, head_dim, rotary_dim, int(interleaved), eps, dtype,
+                       param_dtype, grad_dtype, 0)
+
+
+def grs_rope_turns(inv_freq: Sequence[float]) -> list:
+    """The frequencies as fractions of 2^64 of a turn, for a device uint64 tensor."""
+    n = len(inv_freq)
+    out = (ctypes.c_uint64 * max(1, n))()
+    _check(_lib.grs_rope_turns((ctypes.c_double * max(1, n))(*inv_freq), n, out), "grs_rope_turns")
+    return list(out)[:n]
+
+
+def grs_qk_norm_workspace_bytes(shape: grs_qk_norm) -> int:
+    return _bytes(int(_lib.grs_qk_norm_workspace_bytes(ctypes.byref(shape))), "grs_qk_norm_workspace_bytes")
+
+
+def grs_qk_norm_forward(shape: grs_qk_norm, q: Optional[int], k: Optional[int], wq: Optional[int], wk: Optional[int],
+                        positions: Optional[int], turns: Optional[int], qo: Optional[int], ko: Optional[int], stream: int) -> None:
+    _check(_lib.grs_qk_norm_forward(ctypes.byref(shape), q, k, wq, wk, positions, turns, qo, ko, stream), "grs_qk_norm_forward")
+
+
+def grs_qk_norm_backward(shape: grs_qk_norm, dqo: Optional[int], dko: Optional[int], q: Optional[int], k: Optional[int],
+                         wq: Optional[int], wk: Optional[int], positions: Optional[int], turns: Optional[int], dq: Optional[int],
+                         dk: Optional[int], dwq: Optional[int], dwk: Optional[int], workspace: Optional[int], stream: int) -> None:
+    _check(_lib.grs_qk_norm_backward(ctypes.byref(shape), dqo, dko, q, k, wq, wk, positions, turns, dq, dk, dwq, dwk, workspace,
+                                     stream), "grs_qk_norm_backward")

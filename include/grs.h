@@ -836,6 +836,157 @@ grs_status grs_moe_combine(const grs_moe* shape, const void* ys, const int32_t* 
 grs_status grs_moe_combine_backward(const grs_moe* shape, const void* dy, const void* ys, const int32_t* slot_row,
                                     const float* weights, void* dys, float* dweights, void* stream);
 
+/* -------------------- operators of a decoder's other parameters */
+
+/* Synchronise `stream`, read and clear the current device's flags of
+ * grs_experts_*, grs_embedding_* and grs_qk_norm_*, which the calls of all its
+ * streams share: BOUNDS if a checked build found an index out of place, TIMEOUT
+ * if a bounded device wait gave up (only a defect can cause it; the outputs of
+ * that call are not to be used), else OK (or CUDA). */
+grs_status grs_operators_check_device_errors(void* stream);
+
+/* ------------------------------------------- products of the experts */
+
+/* One linear map for each expert on rows sorted by expert, as grs_moe_sort and
+ * grs_moe_dispatch lay them out: expert e's rows are [offsets[e], offsets[e +
+ * 1]) of xs and ys.  The weights are the expert-owned LOCAL_SHARD parameters of
+ * [ISSUE] "Why this needs separate work"; their gradient is written in
+ * grad_dtype, so that it can go straight into a rank's gradient buffer. */
+typedef struct grs_experts {
+  int64_t rows;          /* rows that xs and ys have, 0..2^31 - 1 */
+  int64_t ld_x;          /* elements from one row of xs and dxs to the next, 0 = in_features */
+  int64_t ld_y;          /* of ys and dys, 0 = out_features */
+  int32_t experts;       /* 1..GRS_MOE_MAX_EXPERTS */
+  int32_t in_features;   /* 1..GRS_MAX_WIDTH, here and below */
+  int32_t out_features;
+  int32_t dtype;         /* grs_dtype of xs, w, ys, dys and dxs */
+  int32_t grad_dtype;    /* of dw */
+  int32_t reserved;
+} grs_experts;
+
+/* ys[r] = w[e] xs[r] for every row r of every expert e, summed in fp32, rounded once.
+ *   xs [rows, in_features], ys [rows, out_features] : device.
+ *   w       : device [experts, out_features, in_features], contiguous.
+ *   offsets : device int32 [experts + 1], not descending, 0 <= offsets <= rows
+ *             (values outside are taken as the nearest of them).
+ *   workspace : device, 16-byte aligned, grs_experts_workspace_bytes (not
+ *             initialised); NULL where that is 0.  Calls that share one must not overlap.
+ * Rows outside [offsets[0], offsets[experts]) are neither read for a result nor
+ * written; NaN in them changes nothing.  xs, w and dys start at multiples of 16
+ * bytes, outputs at multiples of their element.  In bf16, widths and row
+ * distances that are multiples of 8 are fastest; operands of others are laid
+ * out anew in the workspace first.  No output may overlap an input.  Runs on
+ * the current device.  Errors: INVALID_ARG, SHAPE, ALIGNMENT, CUDA. */
+grs_status grs_experts_forward(const grs_experts* shape, const void* xs, const void* w, const int32_t* offsets, void* ys,
+                               void* workspace, void* stream);
+/* dxs[r] = w[e]^T dys[r]; dw[e] = sum over the expert's rows of dys[r] xs[r]^T
+ * (overwritten, zeros for an expert without rows), in fp32, rounded once; each
+ * of the two NULL if not wanted (w is needed for dxs, xs for dw).  Sums have an
+ * order that the shape and the offsets fix: no float atomics. */
+grs_status grs_experts_backward(const grs_experts* shape, const void* dys, const void* xs, const void* w,
+                                const int32_t* offsets, void* dxs, void* dw, void* workspace, void* stream);
+/* Bytes (of either call), or -1 for a shape that the calls refuse. */
+int64_t grs_experts_workspace_bytes(const grs_experts* shape);
+
+/* ------------------------------------------------------------- embedding */
+
+/* Vectors of a table by token id, forward and backward.  The table is the rows
+ * [row_begin, row_end) of the vocabulary: all of it, or the part that a
+ * vocabulary-sharded (LOCAL_SHARD) rank holds.  Any other id (negative ones
+ * too: padding) has no row here: its vector is zeros, so that the ranks'
+ * results add up, and its gradient goes nowhere. */
+typedef struct grs_embedding {
+  int64_t tokens;        /* 0..2^31 - 1 */
+  int32_t row_begin;     /* >= 0 */
+  int32_t row_end;       /* > row_begin */
+  int32_t hidden;        /* elements of a vector, 1..GRS_MAX_WIDTH */
+  float scale;           /* of every vector, e.g. sqrt(hidden) or 1 */
+  int32_t dtype;         /* grs_dtype of table, y and dy */
+  int32_t grad_dtype;    /* of dtable */
+  int32_t reserved[2];
+} grs_embedding;
+
+/* y[t] = scale * table[ids[t] - row_begin], rounded once.
+ *   ids     : device int32 [tokens].
+ *   table   : device [row_end - row_begin, hidden]; y: device [tokens, hidden];
+ *             aligned to the element; 16 bytes with hidden a multiple of 8 is fastest.
+ * No output may overlap an input.  Runs on the current device.  Errors: INVALID_ARG, SHAPE, ALIGNMENT, CUDA. */
+grs_status grs_embedding_forward(const grs_embedding* shape, const int32_t* ids, const void* table, void* y,
+                                 void* stream);
+/* dtable[v] = scale * sum of dy[t] over the tokens t with ids[t] = row_begin + v
+ * (overwritten, zeros for a row without tokens), in fp32, rounded once.  Tokens
+ * are sorted by id first and added up in an order that the shape and the ids
+ * fix: no float atomics.  dtable: device [row_end - row_begin, hidden], aligned
+ * to the element.  workspace: device, 16-byte aligned,
+ * grs_embedding_workspace_bytes (not initialised); calls that share one must not overlap. */
+grs_status grs_embedding_backward(const grs_embedding* shape, const int32_t* ids, const void* dy, void* dtable,
+                                  void* workspace, void* stream);
+/* Bytes, or -1 for a shape that the calls refuse. */
+int64_t grs_embedding_workspace_bytes(const grs_embedding* shape);
+
+/* ------------------------- norms of queries and keys with the rotation */
+
+#define GRS_QK_MAX_DIM 1024 /* elements of a head */
+
+/* Root-mean-square norm of every query and key head and, in the same pass, the
+ * rotation by position.  The two weights, shared by all heads, are PARTIAL_SUM
+ * parameters under head-sharded attention ([ISSUE] "Why this needs separate
+ * work"); their gradients are written in grad_dtype, so that they can go
+ * straight into a rank's gradient buffer. */
+typedef struct grs_qk_norm {
+  int64_t tokens;        /* >= 0 */
+  int64_t ld_q;          /* elements from a token's queries to the next token's, 0 = q_heads * head_dim;
+                            q and dq: they may lie in the rows of a joint projection */
+  int64_t ld_k;          /* the same of k and dk */
+  int64_t ld_qo;         /* of qo and dqo */
+  int64_t ld_ko;         /* of ko and dko */
+  int32_t q_heads;       /* >= 0; heads * head_dim at most GRS_MAX_WIDTH */
+  int32_t k_heads;
+  int32_t head_dim;      /* D, 1..GRS_QK_MAX_DIM */
+  int32_t rotary_dim;    /* the first elements of a head, even, 0 (no rotation)..D */
+  int32_t interleaved;   /* pairs of the rotation: 0: (i, i + rotary_dim / 2), 1: (2 i, 2 i + 1) */
+  float eps;             /* >= 0 */
+  int32_t dtype;         /* grs_dtype of q, k, their outputs and gradients */
+  int32_t param_dtype;   /* of wq and wk */
+  int32_t grad_dtype;    /* of dwq and dwk */
+  int32_t reserved;
+} grs_qk_norm;
+
+/* Frequencies of the rotation for the calls below: turns[i] = inv_freq[i] / (2
+ * pi) as a fraction of 2^64 (host arrays; copy `turns` to the device).  A
+ * position's angle is position * turns[i] modulo 2^64, exact to |position| *
+ * 2^-53 of a turn.  Any finite inv_freq
+ * (base^(-2 i / rotary_dim), or one stretched for longer contexts).  Errors: INVALID_ARG. */
+grs_status grs_rope_turns(const double* inv_freq, int32_t n, uint64_t* turns);
+
+/* For each head x of D elements: u = x / sqrt(sum x^2 / D + eps) * w; then pair
+ * i of the first rotary_dim elements, (a, b), becomes (a cos - b sin, a sin + b
+ * cos) of positions[t] * inv_freq[i].  In fp32, rounded once.
+ *   q, k, qo, ko : device, aligned to the element; 16-byte aligned heads (row
+ *             distances and head_dim multiples of 8 elements) are fastest.
+ *   wq, wk  : device [D], or NULL (1).
+ *   positions : device int32 [tokens], any values; turns: device uint64
+ *             [rotary_dim / 2]; both may be NULL when rotary_dim is 0.
+ * q and qo (k and ko) are not used when q_heads (k_heads) is 0.  qo may be q
+ * itself where ld_qo = ld_q, ko k likewise; otherwise no output may overlap an
+ * input.  Runs on the current device.  Errors: INVALID_ARG, SHAPE, ALIGNMENT, CUDA. */
+grs_status grs_qk_norm_forward(const grs_qk_norm* shape, const void* q, const void* k, const void* wq, const void* wk,
+                               const int32_t* positions, const uint64_t* turns, void* qo, void* ko, void* stream);
+/* With du the gradient of the outputs turned back, h = x * r, r = 1 / sqrt(sum
+ * x^2 / D + eps) and dh = du * w:
+ *   dx = r * (dh - h * sum(dh * h) / D),  dw = sum over tokens and heads of du * h
+ * (overwritten; zeros without tokens or heads), each of the four NULL if not wanted.
+ * Sums in fp32 in an order that the shape, the types and whether heads are
+ * whole 16-byte chunks fix.  workspace: device, 16-byte aligned,
+ * grs_qk_norm_workspace_bytes (not initialised), needed for dwq or dwk; calls
+ * that share one must not overlap.  dq may be dqo itself where ld_q = ld_qo, dk
+ * dko likewise; otherwise no output may overlap an input. */
+grs_status grs_qk_norm_backward(const grs_qk_norm* shape, const void* dqo, const void* dko, const void* q, const void* k,
+                                const void* wq, const void* wk, const int32_t* positions, const uint64_t* turns,
+                                void* dq, void* dk, void* dwq, void* dwk, void* workspace, void* stream);
+/* Bytes, or -1 for a shape that the calls refuse. */
+int64_t grs_qk_norm_workspace_bytes(const grs_qk_norm* shape);
+
 /* Build features of the loaded library.  GRS_FEATURE_CHECKED: compiled with
  * GRS_CHECKED=1 — every kernel that works on a plan checks each index it
  * derives against the extent of the buffer it addresses (the sizes this header
@@ -843,8 +994,10 @@ grs_status grs_moe_combine_backward(const grs_moe* shape, const void* dy, const 
  * list of tensors its tile's record; a failed check skips the access and
  * raises a device flag that grs_check_device_errors, for a list
  * grs_tensors_check_device_errors, reports as BOUNDS (the message of the
- * former names the kernel).  The kernels of grs_layernorm_* and grs_moe_* have
- * no such checks.  Slower; for tests and debugging. */
+ * former names the kernel).  The kernels of grs_layernorm_* and grs_moe_*
+ * have no such checks; those of grs_experts_*, grs_embedding_* and grs_qk_norm_*
+ * check the rows, tokens and places that they derive, reported by
+ * grs_operators_check_device_errors.  Slower; for tests and debugging. */
 #define GRS_FEATURE_CHECKED 1u
 uint32_t grs_build_features(void);
 

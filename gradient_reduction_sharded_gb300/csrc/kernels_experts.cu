@@ -1,17 +1,15 @@
 // Products of the experts: one linear map for each expert on rows sorted by
 // expert, with the gradients of the rows and of the weights.
 //
-// Every product is O[c][f] = sum over k of A[f][k] B[c][k] for each expert:
-//   forward   f an output feature of w,  c a row, k an input feature
-//   rows      f an input feature of w,   c a row, k an output feature
-//   weights   f an input feature of xs,  c an output feature of dys, k a row
-// so that f is what lies next to one another in the result and the expert's
-// rows, of which only the device knows how many, are c or k.
+// bf16 goes to the tensor cores (kernels_experts_mma.cu); operands whose row
+// distance is not a multiple of 16 bytes, which TMA wants, are laid out anew
+// in the workspace first.  fp32 goes to the kernel here.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include "api_util.h"
 #include "device.cuh"
+#include "experts.h"
 #include "internal.h"
 #include "launch.cuh"
 #include "operators.cuh"
@@ -23,8 +21,6 @@ constexpr int EXP_THREADS = 256;
 enum : int { SITE_EXP_ROW = 1 };
 
 __device__ int exp_flags[FLAG_COUNT];
-
-enum class Product { kForward, kRows, kWeights };
 
 // An expert's rows, as the caller's offsets say within [0, rows].
 struct Span2 {
@@ -138,10 +134,6 @@ __global__ void __launch_bounds__(EXP_THREADS) exp_general_kernel(const __grid_c
 }
 
 // ------------------------------------------------------------------- host
-struct ExpLd {
-  int64_t x, y;
-};
-
 grs_status check_experts(const grs_experts* s, const char* who, ExpLd* ld) {
   if (s == nullptr) return api_fail(GRS_ERR_INVALID_ARG, who, "shape is NULL");
   if (s->rows < 0 || s->rows > INT32_MAX) return api_fail(GRS_ERR_SHAPE, who, "rows must be in [0, 2^31)");
@@ -153,6 +145,7 @@ grs_status check_experts(const grs_experts* s, const char* who, ExpLd* ld) {
   ld->y = s->ld_y == 0 ? s->out_features : s->ld_y;
   if (ld->x < s->in_features || ld->y < s->out_features || ld->x > GRS_MAX_WIDTH || ld->y > GRS_MAX_WIDTH)
     return api_fail(GRS_ERR_SHAPE, who, "a distance of rows below their width or above GRS_MAX_WIDTH");
+  ld->w = s->in_features;
   return GRS_OK;
 }
 
@@ -177,10 +170,42 @@ cudaError_t exp_general(const grs_experts* s, const ExpLd& ld, const void* a, co
 }
 
 template <Product kP>
-cudaError_t exp_run(const grs_experts* s, const ExpLd& ld, const void* a, const void* b, const int32_t* offsets, void* o, void* stream) {
-  const bool f = s->dtype == GRS_DTYPE_FP32, g = kP == Product::kWeights ? s->grad_dtype == GRS_DTYPE_FP32 : f;
-  if (f) return g ? exp_general<kP, float, float>(s, ld, a, b, offsets, o, stream) : exp_general<kP, float, uint16_t>(s, ld, a, b, offsets, o, stream);
-  return g ? exp_general<kP, uint16_t, float>(s, ld, a, b, offsets, o, stream) : exp_general<kP, uint16_t, uint16_t>(s, ld, a, b, offsets, o, stream);
+cudaError_t exp_general(const grs_experts* s, const ExpLd& ld, const void* a, const void* b, const int32_t* offsets, void* o, void* stream) {
+  if (kP == Product::kWeights && s->grad_dtype == GRS_DTYPE_BF16) return exp_general<kP, float, uint16_t>(s, ld, a, b, offsets, o, stream);
+  return exp_general<kP, float, float>(s, ld, a, b, offsets, o, stream);
+}
+
+// --------------------------------------------------- bf16, rows laid out anew
+__global__ void __launch_bounds__(EXP_THREADS) exp_pad_kernel(const uint16_t* __restrict__ from, int64_t ld, uint16_t* __restrict__ to,
+                                                              int64_t ld_to, int64_t rows, int32_t width) {
+  pdl_wait();
+  pdl_trigger();
+  for (int64_t r = blockIdx.x; r < rows; r += gridDim.x)
+    for (int32_t i = threadIdx.x; i < width; i += EXP_THREADS) to[r * ld_to + i] = from[r * ld + i];
+}
+
+int64_t round8(int64_t n) { return (n + 7) & ~int64_t(7); }
+
+// Bytes of an operand's copy: none where its rows are whole 16-byte chunks apart.
+int64_t pad_bytes(int64_t rows, int64_t ld, int64_t width) { return ld % 8 == 0 ? 0 : rows * round8(width) * 2; }
+
+// `p` itself, or its copy at *ws; *ld becomes the copy's.
+const void* pad_rows(const void* p, int64_t rows, int64_t* ld, int64_t width, uint8_t** ws, void* stream, cudaError_t* e) {
+  const int64_t bytes = pad_bytes(rows, *ld, width);
+  if (bytes == 0 || *e != cudaSuccess) return p;
+  uint16_t* to = reinterpret_cast<uint16_t*>(*ws);
+  *e = launch_pdl(exp_pad_kernel, dim3(static_cast<unsigned>(rows < 152 * 8 ? rows : 152 * 8)), dim3(EXP_THREADS), 0, stream,
+                  static_cast<const uint16_t*>(p), *ld, to, round8(width), rows, static_cast<int32_t>(width));
+  *ws += (bytes + 15) & ~int64_t(15);
+  *ld = round8(width);
+  return to;
+}
+
+int64_t exp_workspace(const grs_experts* s, const ExpLd& ld) {
+  if (s->dtype == GRS_DTYPE_FP32) return 0;
+  auto up = [](int64_t b) { return (b + 15) & ~int64_t(15); };
+  return up(pad_bytes(s->rows, ld.x, s->in_features)) + up(pad_bytes(s->rows, ld.y, s->out_features)) +
+         up(pad_bytes(int64_t(s->experts) * s->out_features, ld.w, s->in_features));
 }
 
 }  // namespace
@@ -199,6 +224,7 @@ grs_status grs_operators_check_device_errors(void* stream) {
   int flags[FLAG_COUNT] = {};
   cudaError_t e = cudaStreamSynchronize(st);
   if (e == cudaSuccess) e = take_experts_flags(flags, st);
+  if (e == cudaSuccess) e = take_experts_mma_flags(flags, st);
   if (e == cudaSuccess) e = take_embedding_flags(flags, st);
   if (e == cudaSuccess) e = take_qk_norm_flags(flags, st);
   if (e != cudaSuccess) return api_cuda_fail(e, who);
@@ -209,7 +235,7 @@ grs_status grs_operators_check_device_errors(void* stream) {
 int64_t grs_experts_workspace_bytes(const grs_experts* s) {
   ExpLd ld;
   if (check_experts(s, "grs_experts_workspace_bytes", &ld) != GRS_OK) return -1;
-  return 0;
+  return exp_workspace(s, ld);
 }
 
 grs_status grs_experts_forward(const grs_experts* s, const void* xs, const void* w, const int32_t* offsets, void* ys, void* workspace,
@@ -223,7 +249,17 @@ grs_status grs_experts_forward(const grs_experts* s, const void* xs, const void*
   if (!api_aligned(xs, 16) || !api_aligned(w, 16) || !api_aligned(offsets, 4) || !api_aligned(ys, dtype_size(s->dtype)) ||
       !api_aligned(workspace, 16))
     return api_fail(GRS_ERR_ALIGNMENT, who, "a misaligned pointer");
-  const cudaError_t e = exp_run<Product::kForward>(s, ld, w, xs, offsets, ys, stream);
+  if (workspace == nullptr && exp_workspace(s, ld) > 0) return api_fail(GRS_ERR_INVALID_ARG, who, "these row distances need a workspace");
+  cudaError_t e = cudaSuccess;
+  if (s->dtype == GRS_DTYPE_FP32) {
+    e = exp_general<Product::kForward>(s, ld, w, xs, offsets, ys, stream);
+  } else {
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    const int64_t ld_y = ld.y;
+    xs = pad_rows(xs, s->rows, &ld.x, s->in_features, &ws, stream, &e);
+    w = pad_rows(w, int64_t(s->experts) * s->out_features, &ld.w, s->in_features, &ws, stream, &e);
+    if (e == cudaSuccess) e = experts_mma(Product::kForward, s, ld, xs, w, nullptr, offsets, ys, ld_y, stream);
+  }
   return e == cudaSuccess ? GRS_OK : api_cuda_fail(e, who);
 }
 
@@ -245,9 +281,24 @@ grs_status grs_experts_backward(const grs_experts* s, const void* dys, const voi
   if (offsets == nullptr || (dys == nullptr && (dxs != nullptr || dw != nullptr)) || (w == nullptr && dxs != nullptr) ||
       (xs == nullptr && dw != nullptr))
     return api_fail(GRS_ERR_INVALID_ARG, who, "NULL argument");
+  if (workspace == nullptr && exp_workspace(s, ld) > 0) return api_fail(GRS_ERR_INVALID_ARG, who, "these row distances need a workspace");
   cudaError_t e = cudaSuccess;
-  if (dxs != nullptr) e = exp_run<Product::kRows>(s, ld, w, dys, offsets, dxs, stream);
-  if (e == cudaSuccess && dw != nullptr) e = exp_run<Product::kWeights>(s, ld, xs, dys, offsets, dw, stream);
+  if (s->dtype == GRS_DTYPE_FP32) {
+    if (dxs != nullptr) e = exp_general<Product::kRows>(s, ld, w, dys, offsets, dxs, stream);
+    if (e == cudaSuccess && dw != nullptr) e = exp_general<Product::kWeights>(s, ld, xs, dys, offsets, dw, stream);
+  } else if (dxs != nullptr || dw != nullptr) {
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    const int64_t ld_x = ld.x;
+    dys = pad_rows(dys, s->rows, &ld.y, s->out_features, &ws, stream, &e);
+    if (dxs != nullptr) {
+      w = pad_rows(w, int64_t(s->experts) * s->out_features, &ld.w, s->in_features, &ws, stream, &e);
+      if (e == cudaSuccess) e = experts_mma(Product::kRows, s, ld, nullptr, w, dys, offsets, dxs, ld_x, stream);
+    }
+    if (dw != nullptr) {
+      xs = pad_rows(xs, s->rows, &ld.x, s->in_features, &ws, stream, &e);
+      if (e == cudaSuccess) e = experts_mma(Product::kWeights, s, ld, xs, nullptr, dys, offsets, dw, s->in_features, stream);
+    }
+  }
   return e == cudaSuccess ? GRS_OK : api_cuda_fail(e, who);
 }
 

@@ -1,0 +1,468 @@
+// The experts' products in bf16 on the tensor cores.
+//
+// A tile is 128 features f (256 of a cluster of two blocks) times up to TC of
+// c, in tensor memory with a lane a feature and a column a c: features lie next
+// to one another in the result, so a warp stores 32 neighbours of a row at
+// once, straight from registers, and an expert's last rows cost only as many
+// columns as there are (in 16s).
+//
+// Blocks stay and take tiles in turn.  One warp loads (TMA, 64 of k a stage),
+// one thread issues the matrix instructions, four warps store; two
+// accumulators, so that a tile is stored while the next is multiplied.
+// Operands lie along k or along the other index, as they are in memory: both
+// are layouts that the instruction takes, nothing is transposed.
+//
+// Ragged ends: rows of forward and rows' gradients are columns of their own, so
+// what is loaded of another expert's rows is not stored, and k is cut off by the
+// tensor map, which fills with zeros.  In the weights' gradient k runs over the
+// expert's rows: there the loading warp sets to zero what the last 16 rows hold
+// beyond the expert's end, in both operands (NaN times zero is NaN).
+//
+// fp32 gradients: the tensor cores add with rounding towards zero (a library
+// product of 4096 rows is 4e-6 off, with a bias), so sections of 512 rows are
+// added up by ordinary fp32 additions, in tensor memory.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "api_util.h"
+#include "device.cuh"
+#include "experts.h"
+#include "internal.h"
+#include "launch.cuh"
+#include "operators.cuh"
+#include "tcgen05.cuh"
+
+namespace grs {
+namespace {
+
+constexpr int MMA_THREADS = 256;
+constexpr int MMA_K = 64;            // of k a stage: a swizzled row of bf16
+constexpr int MMA_F = 128;           // features of a block
+constexpr int MMA_SECTION = 8;       // stages that fp32 gradients add up in the tensor cores
+constexpr int MMA_SMEM = 227 * 1024;
+enum : int { SITE_MMA_ROW = 2 };
+
+__device__ int mma_flags[FLAG_COUNT];
+
+template <int TC, int kCtas>
+struct Shape {
+  static constexpr int A = MMA_F * MMA_K * 2, B = TC / kCtas * MMA_K * 2, STAGE = A + B;
+  static constexpr int FIXED = 1024 + (GRS_MOE_MAX_EXPERTS + 1) * 4 + 512;  // alignment, tiles before each expert, barriers
+  static constexpr int FIT = (MMA_SMEM - FIXED) / STAGE;
+  static constexpr int STAGES = FIT < 10 ? FIT : 10;
+  static constexpr int BYTES = STAGES * STAGE + FIXED;
+};
+
+template <typename O>
+struct MmaArgs {
+  const int32_t* offsets;
+  O* o;
+  int64_t o_c, o_e;        // elements from one c, one expert to the next
+  int64_t f, c, k;         // extents; an expert's rows in the place of c or k
+  int32_t rows, experts;
+};
+
+struct Tile {
+  int e;
+  int64_t f0, c0, c1, k0, k1;
+};
+
+template <Product kP, int TC, int kCtas>
+struct Tiles {
+  const int32_t* offsets;
+  const int32_t* first;  // c tiles before each expert's (not kWeights)
+  int64_t f, c, k, ft, ct, total;
+  int32_t rows;
+  int e = 0;
+
+  template <typename O>
+  __device__ __forceinline__ Tiles(const MmaArgs<O>& a, const int32_t* first_)
+      : offsets(a.offsets), first(first_), f(a.f), c(a.c), k(a.k), rows(a.rows) {
+    ft = (f + MMA_F * kCtas - 1) / (MMA_F * kCtas);
+    ct = (c + TC - 1) / TC;
+    total = kP == Product::kWeights ? ft * ct * a.experts : ft * first[a.experts];
+  }
+
+  __device__ __forceinline__ Tile at(int64_t t) {
+    Tile x;
+    int64_t ci = t / ft;
+    x.f0 = (t - ci * ft) * (MMA_F * kCtas);
+    int32_t from, to;
+    if constexpr (kP == Product::kWeights) {
+      e = static_cast<int>(ci / ct);
+      ci -= e * ct;
+      x.c0 = ci * TC;
+      x.c1 = c < x.c0 + TC ? c : x.c0 + TC;
+    } else {
+      while (first[e + 1] <= ci) ++e;
+    }
+    from = __ldg(offsets + e);
+    to = __ldg(offsets + e + 1);
+    from = from < 0 ? 0 : from > rows ? rows : from;
+    to = to < from ? from : to > rows ? rows : to;
+    if constexpr (kP == Product::kWeights) {
+      x.k0 = from;
+      x.k1 = to;
+    } else {
+      x.c0 = from + (ci - first[e]) * TC;
+      x.c1 = to < x.c0 + TC ? to : x.c0 + TC;
+      x.k0 = 0;
+      x.k1 = k;
+    }
+    x.e = e;
+    return x;
+  }
+};
+
+// Tiles of c before each expert's, by a block of 256.
+template <int TC>
+__device__ __forceinline__ void tile_prefix(const int32_t* offsets, int32_t experts, int32_t rows, int32_t* first) {
+  __shared__ int32_t sums[MMA_THREADS / 32];
+  constexpr int EACH = GRS_MOE_MAX_EXPERTS / MMA_THREADS;
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  int32_t n[EACH], all = 0;
+#pragma unroll
+  for (int i = 0; i < EACH; ++i) {
+    const int e = threadIdx.x * EACH + i;
+    n[i] = 0;
+    if (e < experts) {
+      int32_t a = __ldg(offsets + e), b = __ldg(offsets + e + 1);
+      a = a < 0 ? 0 : a > rows ? rows : a;
+      b = b < a ? a : b > rows ? rows : b;
+      n[i] = (b - a) / TC + ((b - a) % TC != 0);
+    }
+    all += n[i];
+  }
+  int32_t s = all;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int32_t y = __shfl_up_sync(0xffffffffu, s, o);
+    if (lane >= o) s += y;
+  }
+  if (lane == 31) sums[w] = s;
+  __syncthreads();
+  for (int i = 0; i < w; ++i) s += sums[i];
+  s -= all;
+#pragma unroll
+  for (int i = 0; i < EACH; ++i) {
+    const int e = threadIdx.x * EACH + i;
+    if (e < experts) first[e] = s;
+    s += n[i];
+    if (e == experts - 1) first[experts] = s;
+  }
+}
+
+template <int kCtas>
+__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  if constexpr (kCtas == 1) return mbar_wait_bounded(bar, parity, mma_flags, abort);
+  return mbar_wait_cluster(bar, parity, mma_flags, abort);
+}
+
+template <Product kP, int TC, int kCtas, typename O>
+__global__ void __launch_bounds__(MMA_THREADS, 1)
+    exp_mma_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b, const __grid_constant__ MmaArgs<O> a) {
+  using S = Shape<TC, kCtas>;
+  constexpr bool kWeights = kP == Product::kWeights, kASK = kP == Product::kForward, kBSK = !kWeights;  // operands along k
+  constexpr bool kSections = kWeights && sizeof(O) == 4;
+  constexpr uint32_t COLUMNS = kSections ? 3 * TC : 2 * TC;  // accumulators, the sections' sum
+  constexpr uint32_t TMEM = COLUMNS <= 32 ? 32 : COLUMNS <= 64 ? 64 : COLUMNS <= 128 ? 128 : COLUMNS <= 256 ? 256 : 512;
+  static_assert(COLUMNS <= 512, "tensor memory has 512 columns");
+  static_assert(!kWeights || TC / kCtas % 64 == 0, "operands across k come in 64s");
+  extern __shared__ uint8_t smem[];
+  uint8_t* stages = smem + (1024 - (smem_addr(smem) & 1023)) % 1024;
+  int32_t* first = reinterpret_cast<int32_t*>(stages + S::STAGES * S::STAGE);
+  uint64_t* full = reinterpret_cast<uint64_t*>(first + ((GRS_MOE_MAX_EXPERTS + 1 + 1) & ~1));
+  uint64_t *empty = full + S::STAGES, *done = empty + S::STAGES, *taken = done + 2, *tail = taken + 2;
+  uint32_t* tmem_at = reinterpret_cast<uint32_t*>(tail + 1);
+  volatile int* abort = reinterpret_cast<int*>(tmem_at + 1);
+
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const uint32_t rank = kCtas == 1 ? 0 : cluster_rank();
+  if (threadIdx.x == 0) {
+    prefetch_map(&map_a);
+    prefetch_map(&map_b);
+    for (int s = 0; s < S::STAGES; ++s) {
+      mbar_init(full + s, kCtas);
+      mbar_init(empty + s, 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(done + i, 1);
+      mbar_init(taken + i, 4 * kCtas);
+    }
+    mbar_init(tail, 1);
+    *abort = 0;
+    fence_mbar_init();
+  }
+  if (w == 1) tmem_alloc<kCtas>(tmem_at, TMEM);
+  pdl_wait();
+  pdl_trigger();
+  if constexpr (!kWeights) tile_prefix<TC>(a.offsets, a.experts, a.rows, first);
+  tmem_before_sync();
+  if constexpr (kCtas == 2) cluster_sync();
+  else __syncthreads();
+  tmem_after_sync();
+  const uint32_t tmem = *tmem_at;
+
+  Tiles<kP, TC, kCtas> tiles(a, first);
+  const int64_t t0 = blockIdx.x / kCtas, dt = gridDim.x / kCtas;
+
+  if (w == 0) {
+    // ------------------------------------------------------------- loads
+    uint32_t s = 0, parity = 1, tail_parity = 0;
+    bool ok = true;
+    for (int64_t t = t0; t < tiles.total && ok; t += dt) {
+      const Tile x = tiles.at(t);
+      const int64_t blocks = (x.k1 - x.k0 + MMA_K - 1) / MMA_K;
+      const int32_t f0 = static_cast<int32_t>(x.f0) + static_cast<int32_t>(rank) * MMA_F;
+      // Columns of this block: half of the instruction's.
+      const int32_t half = kWeights ? TC / kCtas : (static_cast<int32_t>(x.c1 - x.c0) + 15) / 16 * 16 / kCtas;
+      const int32_t c0 = static_cast<int32_t>(x.c0) + static_cast<int32_t>(rank) * half;
+      for (int64_t kb = 0; kb < blocks && ok; ++kb) {
+        const int32_t k = static_cast<int32_t>(x.k0 + kb * MMA_K);
+        const int32_t valid = x.k1 - k < MMA_K ? static_cast<int32_t>(x.k1 - k) : MMA_K;
+        const bool last = kWeights && valid % 16 != 0;
+        ok = __all_sync(0xffffffffu, wait_for<kCtas>(empty + s, parity, abort));
+        if (!ok) break;
+        uint8_t* stage = stages + s * S::STAGE;
+        const uint32_t to = smem_addr(stage);
+        const uint32_t here = smem_addr(full + s), bar = kCtas == 1 || rank == 0 ? here : peer_addr(here, 0);
+        if (lane == 0) {
+          const uint32_t on = last ? smem_addr(tail) : bar;
+          if (last) mbar_arrive_expect_tx(tail, S::STAGE);
+          else if (kCtas == 1) mbar_arrive_expect_tx(full + s, S::STAGE);
+          else remote_arrive_expect_tx(bar, S::STAGE);
+          if constexpr (kP == Product::kForward) {
+            tma_load<kCtas>(to, &map_a, k, f0, x.e, on);
+          } else if constexpr (kP == Product::kRows) {
+            tma_load<kCtas>(to, &map_a, f0, k, x.e, on);
+            tma_load<kCtas>(to + 8192, &map_a, f0 + 64, k, x.e, on);
+          } else {
+            tma_load<kCtas>(to, &map_a, f0, k, on);
+            tma_load<kCtas>(to + 8192, &map_a, f0 + 64, k, on);
+          }
+          if constexpr (!kWeights) {
+            tma_load<kCtas>(to + S::A, &map_b, k, c0, on);
+          } else {
+#pragma unroll
+            for (int i = 0; i < TC / kCtas / 64; ++i) tma_load<kCtas>(to + S::A + i * 8192, &map_b, c0 + i * 64, k, on);
+          }
+        }
+        if (last) {
+          ok = __all_sync(0xffffffffu, wait_for<kCtas>(tail, tail_parity, abort));
+          if (!ok) break;
+          tail_parity ^= 1;
+          const int32_t bad = (16 - valid % 16) * 8;  // 16-byte chunks of the rows to clear, in each 64 of f or c
+          for (int32_t i = lane; i < bad * (S::STAGE / 8192); i += 32)
+            *reinterpret_cast<uint4*>(stage + i / bad * 8192 + valid * 128 + i % bad * 16) = make_uint4(0, 0, 0, 0);
+          fence_async_shared();
+          __syncwarp();
+          if (lane == 0) {
+            if (kCtas == 1) mbar_arrive(full + s);
+            else remote_arrive(bar);
+          }
+        }
+        if (++s == S::STAGES) {
+          s = 0;
+          parity ^= 1;
+        }
+      }
+    }
+  } else if (w == 1) {
+    // ---------------------------------------------------------- products
+    if (lane == 0 && rank == 0) {
+      uint32_t s = 0, parity = 0, acc = 0, acc_parity = 1;
+      bool ok = true;
+      for (int64_t t = t0; t < tiles.total && ok; t += dt) {
+        const Tile x = tiles.at(t);
+        const int64_t blocks = (x.k1 - x.k0 + MMA_K - 1) / MMA_K;
+        const uint32_t n = kWeights ? TC : (static_cast<uint32_t>(x.c1 - x.c0) + 15) / 16 * 16;
+        const uint32_t desc = product_desc(kASK, kBSK, MMA_F * kCtas, n);
+        int64_t kb = 0;
+        while (kb < blocks && ok) {
+          const int64_t end = kSections && blocks - kb > MMA_SECTION ? kb + MMA_SECTION : blocks;
+          ok = wait_for<kCtas>(taken + acc, acc_parity, abort);
+          tmem_after_sync();
+          const uint32_t d = tmem + acc * TC;
+          bool add = false;
+          for (; kb < end && ok; ++kb) {
+            ok = wait_for<kCtas>(full + s, parity, abort);
+            if (!ok) break;
+            tmem_after_sync();
+            const uint32_t from = smem_addr(stages + s * S::STAGE);
+            const uint64_t da = operand<kASK>(from, 8192), db = operand<kBSK>(from + S::A, 8192);
+            const int64_t rest = x.k1 - x.k0 - kb * MMA_K;
+            const int steps = rest >= MMA_K ? MMA_K / 16 : static_cast<int>(rest + 15) / 16;
+            for (int i = 0; i < steps; ++i) {
+              mma<kCtas>(d, da + i * operand_step<kASK>, db + i * operand_step<kBSK>, desc, add);
+              add = true;
+            }
+            mma_commit<kCtas>(empty + s);
+            if (++s == S::STAGES) {
+              s = 0;
+              parity ^= 1;
+            }
+          }
+          if (!ok) break;
+          mma_commit<kCtas>(done + acc);
+          acc ^= 1;
+          if (acc == 0) acc_parity ^= 1;
+        }
+      }
+    }
+  } else if (w >= 4) {
+    // ------------------------------------------------------------ results
+    uint32_t acc = 0, parity = 0;
+    bool ok = true;
+    const uint32_t lanes = uint32_t(w - 4) << 21;  // (32 (w - 4)) << 16: this warp's lanes
+    for (int64_t t = t0; t < tiles.total && ok; t += dt) {
+      const Tile x = tiles.at(t);
+      const int64_t blocks = (x.k1 - x.k0 + MMA_K - 1) / MMA_K;
+      const int64_t f = x.f0 + int64_t(rank) * MMA_F + (w - 4) * 32 + lane;
+      const int n = static_cast<int>(x.c1 - x.c0);
+      O* o = a.o + x.e * a.o_e + x.c0 * a.o_c + f;
+      const bool on = f < a.f && GRS_CHECK(kWeights || (x.c0 >= 0 && x.c1 <= a.rows), mma_flags, SITE_MMA_ROW);
+      if (blocks == 0) {  // a weights' gradient without rows
+        if (on)
+          for (int j = 0; j < n; ++j) o[j * a.o_c] = from_float<O>(0.0f);
+        continue;
+      }
+      const int64_t sections = kSections ? (blocks + MMA_SECTION - 1) / MMA_SECTION : 1;
+      for (int64_t i = 0; i < sections && ok; ++i) {
+        ok = __all_sync(0xffffffffu, wait_for<kCtas>(done + acc, parity, abort));
+        if (!ok) break;
+        tmem_after_sync();
+        for (int j0 = 0; j0 < n; j0 += 32) {
+          uint32_t v[32];
+          tmem_load32(tmem + lanes + acc * TC + j0, v);
+          if (kSections && i > 0) {
+            uint32_t sum[32];
+            tmem_load32(tmem + lanes + 2 * TC + j0, sum);
+            tmem_wait_load();
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(__fadd_rn(__uint_as_float(v[j]), __uint_as_float(sum[j])));
+          } else {
+            tmem_wait_load();
+          }
+          if (kSections && i < sections - 1) {
+            tmem_store32(tmem + lanes + 2 * TC + j0, v);
+            tmem_wait_store();
+          } else if (on) {
+            O* p = o + j0 * a.o_c;
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+              if (j0 + j < n) *p = from_float<O>(__uint_as_float(v[j]));
+              p += a.o_c;
+            }
+          }
+          __syncwarp();
+        }
+        tmem_before_sync();
+        __syncwarp();
+        if (lane == 0) {
+          if (kCtas == 1) mbar_arrive(taken + acc);
+          else remote_arrive(rank == 0 ? smem_addr(taken + acc) : peer_addr(smem_addr(taken + acc), 0));
+        }
+        acc ^= 1;
+        if (acc == 0) parity ^= 1;
+      }
+    }
+  }
+  // A wait that gave up leaves copies and products under way: they end by themselves.
+  if (*abort) {
+    const uint64_t since = global_ns();
+    while (global_ns() - since < 200000) {
+    }
+  }
+  __syncwarp();
+  tmem_before_sync();
+  if constexpr (kCtas == 2) cluster_sync();
+  else __syncthreads();
+  tmem_after_sync();
+  if (w == 1) tmem_free<kCtas>(tmem, TMEM);
+}
+
+// ------------------------------------------------------------------- host
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                                 const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion,
+                                 CUtensorMapFloatOOBfill);
+
+EncodeTiled encode_tiled() {
+  static const EncodeTiled f = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult found;
+    const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &found);
+    return e == cudaSuccess && found == cudaDriverEntryPointSuccess ? reinterpret_cast<EncodeTiled>(p) : nullptr;
+  }();
+  return f;
+}
+
+// A bf16 tensor of `n` dimensions, its boxes 64 wide with the 128-byte swizzle.
+bool make_map(CUtensorMap* m, const void* p, int n, const int64_t (&dims)[3], const int64_t (&ld)[2], int box_rows) {
+  const EncodeTiled f = encode_tiled();
+  if (f == nullptr) return false;
+  cuuint64_t d[3], stride[2];
+  cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_rows), 1}, one[3] = {1, 1, 1};
+  for (int i = 0; i < 3; ++i) d[i] = static_cast<cuuint64_t>(dims[i]);
+  for (int i = 0; i < 2; ++i) stride[i] = static_cast<cuuint64_t>(ld[i]) * 2;
+  return f(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, static_cast<cuuint32_t>(n), const_cast<void*>(p), d, stride, box, one,
+           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <Product kP, int TC, int kCtas, typename O>
+cudaError_t mma_launch(const grs_experts* s, const ExpLd& ld, const void* xs, const void* w, const void* dys, const int32_t* offsets,
+                       void* o, int64_t o_ld, void* stream) {
+  using S = Shape<TC, kCtas>;
+  const int64_t in = s->in_features, out = s->out_features;
+  CUtensorMap ma, mb;
+  MmaArgs<O> a{};
+  a.offsets = offsets;
+  a.o = static_cast<O*>(o);
+  a.o_c = o_ld;
+  a.rows = static_cast<int32_t>(s->rows);
+  a.experts = s->experts;
+  bool fine;
+  int64_t tiles;  // at most
+  if constexpr (kP == Product::kWeights) {
+    fine = make_map(&ma, xs, 2, {in, s->rows, 1}, {ld.x, 0}, 64) && make_map(&mb, dys, 2, {out, s->rows, 1}, {ld.y, 0}, 64);
+    a.f = in, a.c = out, a.o_e = out * o_ld;
+    tiles = s->experts * ((out + TC - 1) / TC);
+  } else {
+    constexpr bool fwd = kP == Product::kForward;
+    fine = make_map(&ma, w, 3, {in, out, s->experts}, {ld.w, out * ld.w}, fwd ? MMA_F : 64) &&
+           make_map(&mb, fwd ? xs : dys, 2, {fwd ? in : out, s->rows, 1}, {fwd ? ld.x : ld.y, 0}, TC / kCtas);
+    a.f = fwd ? out : in, a.k = fwd ? in : out;
+    tiles = s->rows / TC + (s->rows < s->experts ? s->rows : s->experts);
+  }
+  if (!fine) return cudaErrorInvalidValue;
+  tiles *= (a.f + MMA_F * kCtas - 1) / (MMA_F * kCtas);
+  const int64_t at_once = 152 / kCtas;
+  const unsigned grid = static_cast<unsigned>((tiles < at_once ? tiles : at_once) * kCtas);
+  const cudaError_t e = allow_smem<exp_mma_kernel<kP, TC, kCtas, O>>(S::BYTES);
+  if (e != cudaSuccess) return e;
+  return launch_pdl_cluster(exp_mma_kernel<kP, TC, kCtas, O>, kCtas, dim3(grid), dim3(MMA_THREADS), S::BYTES, stream, ma, mb, a);
+}
+
+template <Product kP>
+cudaError_t mma_rows(const grs_experts* s, const ExpLd& ld, const void* xs, const void* w, const void* dys, const int32_t* offsets, void* o,
+                     int64_t o_ld, void* stream) {
+  const int64_t mean = s->rows / s->experts;
+  if (mean >= 128) return mma_launch<kP, 256, 2, uint16_t>(s, ld, xs, w, dys, offsets, o, o_ld, stream);
+  if (mean >= 32) return mma_launch<kP, 128, 1, uint16_t>(s, ld, xs, w, dys, offsets, o, o_ld, stream);
+  return mma_launch<kP, 32, 1, uint16_t>(s, ld, xs, w, dys, offsets, o, o_ld, stream);
+}
+
+}  // namespace
+
+cudaError_t take_experts_mma_flags(int (&total)[FLAG_COUNT], cudaStream_t st) { return take_flags(mma_flags, total, st); }
+
+cudaError_t experts_mma(Product p, const grs_experts* s, const ExpLd& ld, const void* xs, const void* w, const void* dys,
+                        const int32_t* offsets, void* o, int64_t o_ld, void* stream) {
+  if (p == Product::kForward) return mma_rows<Product::kForward>(s, ld, xs, w, dys, offsets, o, o_ld, stream);
+  if (p == Product::kRows) return mma_rows<Product::kRows>(s, ld, xs, w, dys, offsets, o, o_ld, stream);
+  if (s->grad_dtype == GRS_DTYPE_FP32) return mma_launch<Product::kWeights, 128, 2, float>(s, ld, xs, w, dys, offsets, o, o_ld, stream);
+  return mma_launch<Product::kWeights, 256, 2, uint16_t>(s, ld, xs, w, dys, offsets, o, o_ld, stream);
+}
+
+}  // namespace grs

@@ -64,6 +64,7 @@ cudaError_t take_flags(const Flags& symbol, int (&total)[FLAG_COUNT], cudaStream
 }
 
 cudaError_t take_experts_flags(int (&total)[FLAG_COUNT], cudaStream_t st);
+cudaError_t take_experts_mma_flags(int (&total)[FLAG_COUNT], cudaStream_t st);
 cudaError_t take_embedding_flags(int (&total)[FLAG_COUNT], cudaStream_t st);
 cudaError_t take_qk_norm_flags(int (&total)[FLAG_COUNT], cudaStream_t st);
 

@@ -153,10 +153,8 @@ __device__ __forceinline__ void tile_prefix(const int32_t* offsets, int32_t expe
   }
 }
 
-template <int kCtas>
 __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, volatile int* abort) {
-  if constexpr (kCtas == 1) return mbar_wait_bounded(bar, parity, mma_flags, abort);
-  return mbar_wait_cluster(bar, parity, mma_flags, abort);
+  return mbar_wait_bounded(bar, parity, mma_flags, abort);
 }
 
 template <Product kP, int TC, int kCtas, typename O>
@@ -222,7 +220,7 @@ __global__ void __launch_bounds__(MMA_THREADS, 1)
         const int32_t k = static_cast<int32_t>(x.k0 + kb * MMA_K);
         const int32_t valid = x.k1 - k < MMA_K ? static_cast<int32_t>(x.k1 - k) : MMA_K;
         const bool last = kWeights && valid % 16 != 0;
-        ok = __all_sync(0xffffffffu, wait_for<kCtas>(empty + s, parity, abort));
+        ok = __all_sync(0xffffffffu, wait_for(empty + s, parity, abort));
         if (!ok) break;
         uint8_t* stage = stages + s * S::STAGE;
         const uint32_t to = smem_addr(stage);
@@ -249,7 +247,7 @@ __global__ void __launch_bounds__(MMA_THREADS, 1)
           }
         }
         if (last) {
-          ok = __all_sync(0xffffffffu, wait_for<kCtas>(tail, tail_parity, abort));
+          ok = __all_sync(0xffffffffu, wait_for(tail, tail_parity, abort));
           if (!ok) break;
           tail_parity ^= 1;
           const int32_t bad = (16 - valid % 16) * 8;  // 16-byte chunks of the rows to clear, in each 64 of f or c
@@ -259,7 +257,7 @@ __global__ void __launch_bounds__(MMA_THREADS, 1)
           __syncwarp();
           if (lane == 0) {
             if (kCtas == 1) mbar_arrive(full + s);
-            else remote_arrive(bar);
+            else remote_release(bar);
           }
         }
         if (++s == S::STAGES) {
@@ -281,12 +279,12 @@ __global__ void __launch_bounds__(MMA_THREADS, 1)
         int64_t kb = 0;
         while (kb < blocks && ok) {
           const int64_t end = kSections && blocks - kb > MMA_SECTION ? kb + MMA_SECTION : blocks;
-          ok = wait_for<kCtas>(taken + acc, acc_parity, abort);
+          ok = wait_for(taken + acc, acc_parity, abort);
           tmem_after_sync();
           const uint32_t d = tmem + acc * TC;
           bool add = false;
           for (; kb < end && ok; ++kb) {
-            ok = wait_for<kCtas>(full + s, parity, abort);
+            ok = wait_for(full + s, parity, abort);
             if (!ok) break;
             tmem_after_sync();
             const uint32_t from = smem_addr(stages + s * S::STAGE);
@@ -329,7 +327,7 @@ __global__ void __launch_bounds__(MMA_THREADS, 1)
       }
       const int64_t sections = kSections ? (blocks + MMA_SECTION - 1) / MMA_SECTION : 1;
       for (int64_t i = 0; i < sections && ok; ++i) {
-        ok = __all_sync(0xffffffffu, wait_for<kCtas>(done + acc, parity, abort));
+        ok = __all_sync(0xffffffffu, wait_for(done + acc, parity, abort));
         if (!ok) break;
         tmem_after_sync();
         for (int j0 = 0; j0 < n; j0 += 32) {

@@ -179,18 +179,312 @@ __global__ void __launch_bounds__(QK_THREADS) qk_backward_kernel(const __grid_co
   }
 }
 
-// dwq and dwk: a warp an element, the blocks' parts in a fixed order.
-template <typename G>
-__global__ void __launch_bounds__(QK_THREADS) qk_weights_kernel(const float* __restrict__ parts, int n, int d, G* dwq, G* dwk) {
+// ------------------------------------------------- heads of whole 16-byte chunks
+// A head is shared by LANES lanes, 16 of its elements each: with the pairs (i,
+// i + rot / 2) eight from either half, so that a lane has both of a pair, with
+// neighbouring pairs 16 in a row.  A block takes the heads of a few tokens: it
+// puts the tokens' sines and cosines into shared memory, each computed once
+// for all heads, and its lane groups take the heads in turn, the next head's
+// loads on their way while one is computed.
+constexpr int QK_MAX_UNITS = 32;       // 16-element units of a head
+constexpr int QK_TABLE = 32 * 1024;    // bytes of sines and cosines at most
+
+struct QkShape {
+  int units, turned, lanes;  // units of a head, of them with a rotated part; lanes that share a head (a power of 2)
+  int tokens;                // of a block
+};
+
+template <typename T>
+struct Raw {
+  static constexpr int N = sizeof(T) == 2 ? 1 : 2;  // 16-byte loads of 8 elements
+  uint4 c[2][N];
+  __device__ __forceinline__ void load(const T* p, int i0, int i1) {
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      c[0][k] = i0 >= 0 ? __ldcs(reinterpret_cast<const uint4*>(p + i0) + k) : make_uint4(0, 0, 0, 0);
+      c[1][k] = i1 >= 0 ? __ldcs(reinterpret_cast<const uint4*>(p + i1) + k) : make_uint4(0, 0, 0, 0);
+    }
+  }
+  __device__ __forceinline__ void floats(float (&o)[16]) const {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      if constexpr (sizeof(T) == 2) {
+        float v[8];
+        set_bf16x8(v, c[h][0]);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) o[8 * h + q] = v[q];
+      } else {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          o[8 * h + 4 * k] = __uint_as_float(c[h][k].x);
+          o[8 * h + 4 * k + 1] = __uint_as_float(c[h][k].y);
+          o[8 * h + 4 * k + 2] = __uint_as_float(c[h][k].z);
+          o[8 * h + 4 * k + 3] = __uint_as_float(c[h][k].w);
+        }
+      }
+    }
+  }
+};
+
+// The lane's 16 elements: eight from i0, eight from i1 (-1: none), and whether these are turned.
+template <bool kPairs>
+struct Unit {
+  int i0, i1;
+  bool r0, r1;
+  __device__ __forceinline__ Unit(int u, int units, int d, int rot) {
+    if (u >= units) {
+      i0 = i1 = -1;
+      r0 = r1 = false;
+    } else if (kPairs || u >= rot / 16) {
+      i0 = kPairs ? 16 * u : rot + 16 * (u - rot / 16);
+      i1 = i0 + 8 < d ? i0 + 8 : -1;
+      r0 = kPairs && i0 < rot;
+      r1 = kPairs && i1 >= 0 && i1 < rot;
+    } else {
+      i0 = 8 * u;
+      i1 = 8 * u + rot / 2;
+      r0 = r1 = true;
+    }
+  }
+  // v turned by the unit's eight angles (back: by their negatives).
+  __device__ __forceinline__ void turn(float (&v)[16], const float4* table, int turned, bool back) const {
+    if (!r0) return;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      if (kPairs && q >= 2 && !r1) break;
+      const float4 t = table[q * turned];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int j = 2 * q + k, a = kPairs ? 2 * j : j, b = kPairs ? 2 * j + 1 : j + 8;
+        const float c = k == 0 ? t.x : t.z, s = back ? -(k == 0 ? t.y : t.w) : (k == 0 ? t.y : t.w), x = v[a], y = v[b];
+        v[a] = __fmaf_rn(x, c, -(y * s));
+        v[b] = __fmaf_rn(x, s, y * c);
+      }
+    }
+  }
+};
+
+template <typename T>
+__device__ __forceinline__ void store_unit(T* p, int i0, int i1, const float (&v)[16]) {
+  float a[8], b[8];
+#pragma unroll
+  for (int q = 0; q < 8; ++q) {
+    a[q] = v[q];
+    b[q] = v[8 + q];
+  }
+  if (i0 >= 0) store_floats<8>(p + i0, a);
+  if (i1 >= 0) store_floats<8>(p + i1, b);
+}
+
+__device__ __forceinline__ float lanes_sum(float x, int lanes) {
+  for (int o = lanes / 2; o > 0; o >>= 1) x = __fadd_rn(x, __shfl_xor_sync(0xffffffffu, x, o));
+  return x;
+}
+
+// Shared memory of a block: the angles of its tokens, [token][4][turned] of
+// two (cos, sin), and the weights, [2][4][units] of four.
+template <typename T, typename P, bool kPairs>
+__device__ __forceinline__ void qk_weights_to_smem(const QkArgs<T, P>& a, const QkShape& s, float* w) {
+  for (int i = threadIdx.x; i < 2 * 16 * s.units; i += QK_THREADS) {
+    const int which = i / (16 * s.units), u = i % (16 * s.units) / 16, j = i % 16;
+    const Unit<kPairs> x(u, s.units, a.d, a.rot);
+    const int at = j < 8 ? x.i0 + j : x.i1 + j - 8;
+    const bool on = (j < 8 || x.i1 >= 0) && a.heads[which] > 0;
+    w[((which * 4 + j / 4) * s.units + u) * 4 + j % 4] = on ? weight(a, which, at) : 0.0f;
+  }
+}
+template <typename T, typename P>
+__device__ __forceinline__ void qk_angles_to_smem(const QkArgs<T, P>& a, const QkShape& s, int64_t t0, int tokens, float2* table) {
+  const int half = a.rot / 2, all = s.turned * 8;
+  for (int i = threadIdx.x; i < tokens * all; i += QK_THREADS) {
+    const int t = i / all, p = i - t * all, u = p / 8, j = p % 8;
+    if (p < half) table[((t * 4 + j / 2) * s.turned + u) * 2 + j % 2] = turn_of(__ldg(a.positions + t0 + t), __ldg(a.turns + p));
+  }
+}
+
+// Head number `i` of a block's tokens: queries of all tokens first, then keys.
+template <typename T, typename P>
+struct Place {
+  int which, t;
+  int64_t x, y;
+  __device__ __forceinline__ Place(const QkArgs<T, P>& a, int64_t t0, int tokens, int i) {
+    const int q = tokens * a.heads[0];
+    which = i >= q;
+    if (which) i -= q;
+    const unsigned n = a.heads[which];
+    t = static_cast<unsigned>(i) / n;
+    const int64_t h = int64_t(i - t * static_cast<int>(n)) * a.d;
+    x = (t0 + t) * a.ld_x[which] + h;
+    y = (t0 + t) * a.ld_y[which] + h;
+  }
+};
+
+template <typename T, typename P, bool kPairs>
+__global__ void __launch_bounds__(QK_THREADS) qk_forward_whole_kernel(const __grid_constant__ QkArgs<T, P> a, const QkShape s) {
+  extern __shared__ float4 shared[];
+  float4 *table = shared, *weights = shared + s.tokens * 4 * s.turned;
   pdl_wait();
   pdl_trigger();
-  const int lane = threadIdx.x & 31, i = blockIdx.x * QK_WARPS + (threadIdx.x >> 5);
-  if (i >= 2 * d) return;
+  const int64_t t0 = int64_t(blockIdx.x) * s.tokens;
+  const int tokens = a.tokens - t0 < s.tokens ? static_cast<int>(a.tokens - t0) : s.tokens;
+  const int u = threadIdx.x % s.lanes, slots = QK_THREADS / s.lanes, items = tokens * (a.heads[0] + a.heads[1]);
+  const Unit<kPairs> unit(u, s.units, a.d, a.rot);
+  int i = threadIdx.x / s.lanes;
+  Raw<T> next;
+  if (i < items) {
+    const Place<T, P> p(a, t0, tokens, i);
+    next.load(a.x[p.which] + p.x, unit.i0, unit.i1);
+  }
+  qk_weights_to_smem<T, P, kPairs>(a, s, reinterpret_cast<float*>(weights));
+  qk_angles_to_smem(a, s, t0, tokens, reinterpret_cast<float2*>(table));
+  __syncthreads();
+  const int rounds = (items + slots - 1) / slots;  // whole warps stay together for the sums
+  for (int r = 0; r < rounds; ++r, i += slots) {
+    const bool on = i < items;
+    float v[16];
+    if (on) next.floats(v);
+    else
+#pragma unroll
+      for (int q = 0; q < 16; ++q) v[q] = 0.0f;
+    if (i + slots < items) {
+      const Place<T, P> p(a, t0, tokens, i + slots);
+      next.load(a.x[p.which] + p.x, unit.i0, unit.i1);
+    }
+    float sum = 0.0f;
+#pragma unroll
+    for (int q = 0; q < 16; ++q) sum = __fmaf_rn(v[q], v[q], sum);
+    const float rs = rsqrtf(__fmaf_rn(lanes_sum(sum, s.lanes), a.inv_d, a.eps));
+    if (!on || unit.i0 < 0) continue;
+    const Place<T, P> p(a, t0, tokens, i);
+    if (!GRS_CHECK(p.t < tokens, qk_flags, SITE_QK_HEAD)) continue;
+    const float4* w = weights + p.which * 4 * s.units + u;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const float4 k = w[q * s.units];
+      v[4 * q] *= rs * k.x;
+      v[4 * q + 1] *= rs * k.y;
+      v[4 * q + 2] *= rs * k.z;
+      v[4 * q + 3] *= rs * k.w;
+    }
+    unit.turn(v, table + p.t * 4 * s.turned + u, s.turned, false);
+    store_unit(a.o[p.which] + p.y, unit.i0, unit.i1, v);
+  }
+}
+
+template <typename T, typename P, bool kPairs>
+__global__ void __launch_bounds__(QK_THREADS) qk_backward_whole_kernel(const __grid_constant__ QkArgs<T, P> a, const QkShape s) {
+  extern __shared__ float4 shared[];
+  float4 *table = shared, *weights = shared + s.tokens * 4 * s.turned;
+  pdl_wait();
+  pdl_trigger();
+  const int u = threadIdx.x % s.lanes, slots = QK_THREADS / s.lanes;
+  const Unit<kPairs> unit(u, s.units, a.d, a.rot);
+  float dw[2][16] = {};
+  qk_weights_to_smem<T, P, kPairs>(a, s, reinterpret_cast<float*>(weights));
+  for (int64_t t0 = int64_t(blockIdx.x) * s.tokens; t0 < a.tokens; t0 += int64_t(gridDim.x) * s.tokens) {
+    const int tokens = a.tokens - t0 < s.tokens ? static_cast<int>(a.tokens - t0) : s.tokens;
+    const int items = tokens * (a.heads[0] + a.heads[1]);
+    int i = threadIdx.x / s.lanes;
+    Raw<T> nx, ny;
+    if (i < items) {
+      const Place<T, P> p(a, t0, tokens, i);
+      nx.load(a.x[p.which] + p.x, unit.i0, unit.i1);
+      ny.load(a.dy[p.which] + p.y, unit.i0, unit.i1);
+    }
+    __syncthreads();  // the table may still be read
+    qk_angles_to_smem(a, s, t0, tokens, reinterpret_cast<float2*>(table));
+    __syncthreads();
+    const int rounds = (items + slots - 1) / slots;
+    for (int r = 0; r < rounds; ++r, i += slots) {
+      const bool on = i < items;
+      float x[16], g[16];
+#pragma unroll
+      for (int q = 0; q < 16; ++q) x[q] = g[q] = 0.0f;
+      int which = 0, t = 0;
+      int64_t at = 0;
+      if (on) {
+        const Place<T, P> p(a, t0, tokens, i);
+        which = p.which;
+        t = p.t;
+        at = p.x;
+        nx.floats(x);
+        ny.floats(g);
+        if (!GRS_CHECK(t < tokens, qk_flags, SITE_QK_HEAD)) t = 0;
+      }
+      if (i + slots < items) {
+        const Place<T, P> p(a, t0, tokens, i + slots);
+        nx.load(a.x[p.which] + p.x, unit.i0, unit.i1);
+        ny.load(a.dy[p.which] + p.y, unit.i0, unit.i1);
+      }
+      float sum = 0.0f;
+#pragma unroll
+      for (int q = 0; q < 16; ++q) sum = __fmaf_rn(x[q], x[q], sum);
+      const float rs = rsqrtf(__fmaf_rn(lanes_sum(sum, s.lanes), a.inv_d, a.eps));
+      if (on) unit.turn(g, table + t * 4 * s.turned + u, s.turned, true);
+#pragma unroll
+      for (int q = 0; q < 16; ++q) {
+        x[q] *= rs;
+        const float h = g[q] * x[q];
+        if (which == 0) dw[0][q] += h;
+        else dw[1][q] += h;
+      }
+      float dot = 0.0f;
+      if (unit.i0 >= 0) {
+        const float4* w = weights + which * 4 * s.units + u;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const float4 k = w[q * s.units];
+          g[4 * q] *= k.x;
+          g[4 * q + 1] *= k.y;
+          g[4 * q + 2] *= k.z;
+          g[4 * q + 3] *= k.w;
+        }
+#pragma unroll
+        for (int q = 0; q < 16; ++q) dot = __fmaf_rn(g[q], x[q], dot);
+      }
+      const float m = lanes_sum(dot, s.lanes) * a.inv_d;
+      if (!on || a.o[which] == nullptr || unit.i0 < 0) continue;
+#pragma unroll
+      for (int q = 0; q < 16; ++q) x[q] = rs * __fmaf_rn(-x[q], m, g[q]);
+      store_unit(a.o[which] + at, unit.i0, unit.i1, x);
+    }
+  }
+  if (a.parts == nullptr) return;
+  // The block's dwq and dwk: the lane groups' sums, in order.
+  float* red = reinterpret_cast<float*>(shared);  // [slots][lanes][16]
+  for (int which = 0; which < 2; ++which) {
+    __syncthreads();
+#pragma unroll
+    for (int q = 0; q < 16; ++q) red[q * QK_THREADS + threadIdx.x] = which == 0 ? dw[0][q] : dw[1][q];
+    __syncthreads();
+    for (int i = threadIdx.x; i < 16 * s.units; i += QK_THREADS) {
+      const int v = i / 16, j = i % 16;
+      const Unit<kPairs> x(v, s.units, a.d, a.rot);
+      if (j >= 8 && x.i1 < 0) continue;
+      float sum = 0.0f;
+      for (int k = 0; k < slots; ++k) sum += red[j * QK_THREADS + k * s.lanes + v];
+      a.parts[(int64_t(blockIdx.x) * 2 + which) * a.d + (j < 8 ? x.i0 + j : x.i1 + j - 8)] = sum;
+    }
+  }
+}
+
+// dwq and dwk: 32 elements a block, the blocks' parts in a fixed order.
+template <typename G>
+__global__ void __launch_bounds__(1024) qk_weights_kernel(const float* __restrict__ parts, int n, int d, G* dwq, G* dwk) {
+  __shared__ float red[32][33];
+  pdl_wait();
+  pdl_trigger();
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, i = blockIdx.x * 32 + lane;
   float s = 0.0f;
-  for (int k = lane; k < n; k += 32) s += parts[int64_t(k) * 2 * d + i];
-  s = warp_sum(s);
-  G* o = i < d ? dwq : dwk;
-  if (lane == 0 && o != nullptr) o[i < d ? i : i - d] = from_float<G>(s);
+  if (i < 2 * d)
+    for (int k = w; k < n; k += 32) s += parts[int64_t(k) * 2 * d + i];
+  red[lane][w] = s;
+  __syncthreads();
+  s = warp_sum(red[w][lane]);
+  const int o = blockIdx.x * 32 + w;
+  if (lane != 0 || o >= 2 * d) return;
+  G* to = o < d ? dwq : dwk;
+  if (to != nullptr) to[o < d ? o : o - d] = from_float<G>(s);
 }
 
 // ------------------------------------------------------------------- host
@@ -215,10 +509,40 @@ grs_status check_qk(const grs_qk_norm* s, const char* who, int64_t (&ld)[4]) {
   return GRS_OK;
 }
 
+// Blocks of the backward pass and so parts of dwq and dwk: what any of its kernels has at most.
 int qk_blocks(const grs_qk_norm* s) {
   const int64_t b = (s->tokens * (s->q_heads + s->k_heads) + QK_WARPS - 1) / QK_WARPS;
   return static_cast<int>(b < QK_BLOCKS ? b : QK_BLOCKS);
 }
+
+// Whether heads are whole 16-byte chunks whose turned parts are whole chunks too.
+bool qk_whole(const grs_qk_norm* s, const int64_t (&ld)[4], const void* a, const void* b, const void* c, const void* d, const void* e,
+              const void* f) {
+  const int64_t chunk = 16 / dtype_size(s->dtype);
+  if (s->head_dim % 8 != 0 || s->rotary_dim % (s->interleaved ? 8 : 16) != 0 || (s->head_dim + 15) / 16 > QK_MAX_UNITS) return false;
+  for (int i = 0; i < 4; ++i)
+    if (ld[i] % chunk != 0) return false;
+  return api_aligned(a, 16) && api_aligned(b, 16) && api_aligned(c, 16) && api_aligned(d, 16) && api_aligned(e, 16) && api_aligned(f, 16);
+}
+
+QkShape qk_shape(const grs_qk_norm* s, int rounds) {
+  QkShape q;
+  const int d = s->head_dim, r = s->rotary_dim;
+  q.units = s->interleaved ? (d + 15) / 16 : r / 16 + (d - r + 15) / 16;
+  q.turned = (r + 15) / 16;
+  q.lanes = 1;
+  while (q.lanes < q.units) q.lanes *= 2;
+  // Tokens of a block: enough for `rounds` heads a lane group, as far as the table goes and every SM has blocks.
+  const int64_t heads = s->q_heads + s->k_heads, slots = QK_THREADS / q.lanes;
+  int64_t t = (rounds * slots + heads - 1) / heads;
+  if (q.turned > 0 && t > QK_TABLE / (64 * q.turned)) t = QK_TABLE / (64 * q.turned);
+  if (t > 128) t = 128;
+  if (t > s->tokens / (152 * 4)) t = s->tokens / (152 * 4);
+  q.tokens = static_cast<int>(t < 1 ? 1 : t);
+  return q;
+}
+
+int qk_smem(const QkShape& q) { return q.tokens * 64 * q.turned + 2 * 64 * q.units; }
 
 template <typename T, typename P>
 QkArgs<T, P> qk_args(const grs_qk_norm* s, const int64_t (&ld)[4], const void* dqo, const void* dko, const void* q, const void* k,
@@ -251,20 +575,39 @@ QkArgs<T, P> qk_args(const grs_qk_norm* s, const int64_t (&ld)[4], const void* d
 }
 
 template <typename T, typename P>
-cudaError_t qk_forward(const grs_qk_norm* s, const QkArgs<T, P>& a, void* stream) {
+cudaError_t qk_forward(const grs_qk_norm* s, const int64_t (&ld)[4], const QkArgs<T, P>& a, void* stream) {
+  if (qk_whole(s, ld, a.x[0], a.x[1], a.o[0], a.o[1], nullptr, nullptr)) {
+    const QkShape q = qk_shape(s, 4);
+    const int64_t blocks = (s->tokens + q.tokens - 1) / q.tokens;
+    if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
+    const dim3 grid(static_cast<unsigned>(blocks)), block(QK_THREADS);
+    return s->interleaved ? launch_pdl(qk_forward_whole_kernel<T, P, true>, grid, block, qk_smem(q), stream, a, q)
+                          : launch_pdl(qk_forward_whole_kernel<T, P, false>, grid, block, qk_smem(q), stream, a, q);
+  }
   const int64_t blocks = (s->tokens * (s->q_heads + s->k_heads) + QK_WARPS - 1) / QK_WARPS;
   if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
   return launch_pdl(qk_forward_kernel<T, P>, dim3(static_cast<unsigned>(blocks)), dim3(QK_THREADS), 0, stream, a);
 }
 
 template <typename T, typename P>
-cudaError_t qk_backward(const grs_qk_norm* s, const QkArgs<T, P>& a, void* dwq, void* dwk, void* stream) {
-  const int blocks = qk_blocks(s);
-  cudaError_t e = allow_smem<qk_backward_kernel<T, P>>(QK_WARPS * 2 * GRS_QK_MAX_DIM * 4);
-  if (e == cudaSuccess)
-    e = launch_pdl(qk_backward_kernel<T, P>, dim3(blocks), dim3(QK_THREADS), size_t(QK_WARPS) * 2 * s->head_dim * 4, stream, a);
+cudaError_t qk_backward(const grs_qk_norm* s, const int64_t (&ld)[4], const QkArgs<T, P>& a, void* dwq, void* dwk, void* stream) {
+  int blocks = qk_blocks(s);
+  cudaError_t e;
+  if (qk_whole(s, ld, a.x[0], a.x[1], a.dy[0], a.dy[1], a.o[0], a.o[1])) {
+    const QkShape q = qk_shape(s, 4);
+    const int64_t tiles = (s->tokens + q.tokens - 1) / q.tokens;
+    if (blocks > 2 * 152) blocks = 2 * 152;
+    if (blocks > tiles) blocks = static_cast<int>(tiles);
+    const int smem = qk_smem(q) > 16 * QK_THREADS * 4 ? qk_smem(q) : 16 * QK_THREADS * 4;
+    e = s->interleaved ? launch_pdl(qk_backward_whole_kernel<T, P, true>, dim3(blocks), dim3(QK_THREADS), smem, stream, a, q)
+                       : launch_pdl(qk_backward_whole_kernel<T, P, false>, dim3(blocks), dim3(QK_THREADS), smem, stream, a, q);
+  } else {
+    e = allow_smem<qk_backward_kernel<T, P>>(QK_WARPS * 2 * GRS_QK_MAX_DIM * 4);
+    if (e == cudaSuccess)
+      e = launch_pdl(qk_backward_kernel<T, P>, dim3(blocks), dim3(QK_THREADS), size_t(QK_WARPS) * 2 * s->head_dim * 4, stream, a);
+  }
   if (e != cudaSuccess || a.parts == nullptr) return e;
-  const dim3 grid((2 * s->head_dim + QK_WARPS - 1) / QK_WARPS), block(QK_THREADS);
+  const dim3 grid((2 * s->head_dim + 31) / 32), block(1024);
   return s->grad_dtype == GRS_DTYPE_FP32
              ? launch_pdl(qk_weights_kernel<float>, grid, block, 0, stream, static_cast<const float*>(a.parts), blocks, s->head_dim,
                           static_cast<float*>(dwq), static_cast<float*>(dwk))
@@ -318,7 +661,7 @@ grs_status grs_qk_norm_forward(const grs_qk_norm* s, const void* q, const void* 
       !api_aligned(wk, pa) || !api_aligned(positions, 4) || !api_aligned(turns, 8))
     return api_fail(GRS_ERR_ALIGNMENT, who, "a pointer is not aligned to its element");
   const bool f = s->dtype == GRS_DTYPE_FP32, pf = s->param_dtype == GRS_DTYPE_FP32;
-#define GRS_QK_CALL(T, P) qk_forward<T, P>(s, qk_args<T, P>(s, ld, nullptr, nullptr, q, k, wq, wk, positions, turns, qo, ko, nullptr), stream)
+#define GRS_QK_CALL(T, P) qk_forward<T, P>(s, ld, qk_args<T, P>(s, ld, nullptr, nullptr, q, k, wq, wk, positions, turns, qo, ko, nullptr), stream)
   const cudaError_t e = f ? (pf ? GRS_QK_CALL(float, float) : GRS_QK_CALL(float, uint16_t))
                           : (pf ? GRS_QK_CALL(uint16_t, float) : GRS_QK_CALL(uint16_t, uint16_t));
 #undef GRS_QK_CALL
@@ -353,7 +696,7 @@ grs_status grs_qk_norm_backward(const grs_qk_norm* s, const void* dqo, const voi
   void* parts = params ? workspace : nullptr;
   const bool f = s->dtype == GRS_DTYPE_FP32, pf = s->param_dtype == GRS_DTYPE_FP32;
 #define GRS_QK_CALL(T, P) \
-  qk_backward<T, P>(s, qk_args<T, P>(s, ld, dqo, dko, q, k, wq, wk, positions, turns, dq, dk, parts), dwq, dwk, stream)
+  qk_backward<T, P>(s, ld, qk_args<T, P>(s, ld, dqo, dko, q, k, wq, wk, positions, turns, dq, dk, parts), dwq, dwk, stream)
   e = f ? (pf ? GRS_QK_CALL(float, float) : GRS_QK_CALL(float, uint16_t))
         : (pf ? GRS_QK_CALL(uint16_t, float) : GRS_QK_CALL(uint16_t, uint16_t));
 #undef GRS_QK_CALL

@@ -25,6 +25,7 @@ namespace {
 
 constexpr int EMB_THREADS = 256;
 constexpr int EMB_SORT_THREADS = 1024;
+constexpr int EMB_ROWS = 8;                           // rows of the table that a group of threads takes
 constexpr int EMB_WARPS = EMB_SORT_THREADS / 32;
 constexpr int EMB_DIGIT = 9;                          // bits of a sorting pass at most
 constexpr int64_t EMB_TABLE = 256 * 1024;             // counts that every sorting block may add up by itself
@@ -194,6 +195,7 @@ struct EmbArgs {
   const int32_t *keys, *tokens, *starts;
   float* parts;  // [windows][2][d]
   int32_t n, rows, d, units, window;
+  int32_t group;  // threads of a row, a power of 2
   float scale;
 };
 
@@ -243,29 +245,38 @@ __global__ void __launch_bounds__(EMB_THREADS) emb_parts_kernel(const __grid_con
   }
 }
 
-// dtable[row] = scale * the sum of its tokens' vectors, a thread E elements.
+// dtable[row] = scale * the sum of its tokens' vectors.  A group of threads
+// takes a row, a thread E elements at a time; most rows of a large vocabulary
+// have no token and are zeros to store.
 template <typename T, typename G, int E>
 __global__ void __launch_bounds__(EMB_THREADS) emb_sum_kernel(const __grid_constant__ EmbArgs<T, G> a) {
   pdl_wait();
   pdl_trigger();
-  const int64_t i = int64_t(blockIdx.x) * EMB_THREADS + threadIdx.x, row = i / a.units;
-  if (row >= a.rows) return;
-  const int64_t c = (i - row * a.units) * E;
-  const int32_t s = __ldg(a.starts + row), e = __ldg(a.starts + row + 1);
-  float sum[E] = {};
-  if (e - s <= a.window) {
-    emb_add<E>(a, s, e, c, sum);
-  } else {
-    for (int32_t w = s / a.window; w <= (e - 1) / a.window; ++w) {
-      const int slot = w * int64_t(a.window) >= s ? 0 : 1;
-      const float* p = a.parts + (int64_t(w) * 2 + slot) * a.d + c;
+  const int group = a.group, g = threadIdx.x / group, u0 = threadIdx.x - g * group, groups = EMB_THREADS / group;
+  const int64_t first = int64_t(blockIdx.x) * (EMB_ROWS * groups) + g;
+#pragma unroll 1
+  for (int k = 0; k < EMB_ROWS; ++k) {
+    const int64_t row = first + k * groups;
+    if (row >= a.rows) return;
+    const int32_t s = __ldg(a.starts + row), e = __ldg(a.starts + row + 1);
+    for (int u = u0; u < a.units; u += group) {
+      const int64_t c = int64_t(u) * E;
+      float sum[E] = {};
+      if (e - s <= a.window) {
+        emb_add<E>(a, s, e, c, sum);
+      } else {
+        for (int32_t w = s / a.window; w <= (e - 1) / a.window; ++w) {
+          const int slot = w * int64_t(a.window) >= s ? 0 : 1;
+          const float* p = a.parts + (int64_t(w) * 2 + slot) * a.d + c;
 #pragma unroll
-      for (int q = 0; q < E; ++q) sum[q] += p[q];
+          for (int q = 0; q < E; ++q) sum[q] += p[q];
+        }
+      }
+#pragma unroll
+      for (int q = 0; q < E; ++q) sum[q] *= a.scale;
+      if (GRS_CHECK(c + E <= a.d, emb_flags, SITE_EMB_ROW)) store_floats<E>(a.dtable + row * a.d + c, sum);
     }
   }
-#pragma unroll
-  for (int q = 0; q < E; ++q) sum[q] *= a.scale;
-  if (GRS_CHECK(c + E <= a.d, emb_flags, SITE_EMB_ROW)) store_floats<E>(a.dtable + row * a.d + c, sum);
 }
 
 // y[t] = scale * table[row], a thread E elements of a token.
@@ -389,8 +400,9 @@ cudaError_t emb_backward(const grs_embedding* s, const int32_t* ids, const void*
   a.units = s->hidden / E;
   a.window = p.window;
   a.scale = s->scale;
-  const int64_t blocks = (int64_t(p.rows) * a.units + EMB_THREADS - 1) / EMB_THREADS;
-  if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
+  a.group = 1;
+  while (a.group < a.units && a.group < EMB_THREADS) a.group *= 2;
+  const int64_t each = EMB_ROWS * (EMB_THREADS / a.group), blocks = (p.rows + each - 1) / each;
   const dim3 block(EMB_THREADS);
   if (e == cudaSuccess)
     e = launch_pdl(emb_starts_kernel, dim3(static_cast<unsigned>(p.rows / EMB_THREADS + 1)), block, 0, stream, a.keys, a.n, p.rows, starts);

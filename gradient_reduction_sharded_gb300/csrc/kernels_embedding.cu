@@ -1,16 +1,16 @@
 // Vectors of a table by token id, and the table's gradient.
 //
-// Forward is a gather.  Backward sorts the tokens by their row of the table
-// (a stable counting sort, digit by digit, so that equal rows keep the order
-// of their tokens), finds where each row's tokens begin, and writes every row
-// of the gradient once: the sum of its tokens' vectors in order, or zeros.
-// Nothing is added by atomics, so two runs give the same bits.
+// Forward is a gather.  Backward sorts the tokens by their row of the table (a
+// stable counting sort, digit by digit, so that equal rows keep the order of
+// their tokens) and then writes every row of the gradient once: the sum of its
+// tokens' vectors in order, or zeros.  Nothing is added by atomics, so two runs
+// give the same bits.
 //
-// Token frequencies are steep (a few ids, or a padding id that counts, can be
-// a large part of a batch), so a row with more than a window of tokens is
-// added up in parts first: the sorted tokens are cut into windows, and as such
-// a row is longer than a window, a window holds parts of at most two of them,
-// the one that its first token belongs to and the one of its last.
+// Token frequencies are steep (a few ids, or a padding id that counts, can be a
+// large part of a batch), so the sorted tokens are cut into windows, and a row
+// whose tokens cross from one window into the next is added up by windows
+// first.  A window has parts of at most two such rows: the one that comes in
+// from the left (slot 0) and the one that goes on to the right (slot 1).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -24,11 +24,13 @@ namespace grs {
 namespace {
 
 constexpr int EMB_THREADS = 256;
-constexpr int EMB_SORT_THREADS = 1024;
-constexpr int EMB_ROWS = 8;                           // rows of the table that a group of threads takes
-constexpr int EMB_WARPS = EMB_SORT_THREADS / 32;
-constexpr int EMB_DIGIT = 9;                          // bits of a sorting pass at most
-constexpr int64_t EMB_TABLE = 256 * 1024;             // counts that every sorting block may add up by itself
+constexpr int EMB_WARPS = EMB_THREADS / 32;
+constexpr int EMB_DIGIT = 9;               // bits of a sorting pass at most
+constexpr int EMB_EACH = (1 << EMB_DIGIT) / EMB_THREADS;  // bins of a thread
+constexpr int EMB_MAX_CHUNKS = 128;        // chunks whose counts every sorting block may add up by itself
+constexpr int EMB_MAX_ROWS = 32;           // rows of the table that a block takes
+constexpr int EMB_TOKENS = 512;            // of a block's tokens in shared memory
+constexpr int EMB_JOIN = 32;               // units of a row that a joining block takes
 enum : int { SITE_EMB_TOKEN = 1, SITE_EMB_ROW = 2 };
 
 __device__ int emb_flags[FLAG_COUNT];
@@ -42,35 +44,44 @@ __device__ __forceinline__ int32_t emb_row(int32_t id, int32_t begin, int32_t ro
 // ------------------------------------------------------------------- sort
 // One pass orders (row, token) pairs by a digit of the row, the order of
 // equal digits kept.  The first pass takes the ids themselves (keys NULL).
+// A block has a chunk of 256 J pairs; counts[chunk][bin] says how many of each
+// digit.  The first pass's counts come from a kernel of their own, which
+// clears the later ones'; these are counted where a pass puts its pairs (by
+// integer atomics, whose order changes nothing).
 struct SortArgs {
   const int32_t *ids, *keys, *tokens;
   int32_t *keys_out, *tokens_out;
-  int32_t *counts, *totals;  // counts[chunk][bin]; totals[bin] when a scan has run, else NULL
-  int32_t n, begin, rows, shift, bins, chunks;
+  int32_t *counts, *next;    // of this pass and the next one (NULL: the last)
+  int32_t *totals;           // [bin] when a scan has run, else NULL
+  int32_t n, begin, rows, shift, bins, chunks, clear;  // clear: tables behind `counts` to clear
 };
 
-__device__ __forceinline__ int32_t sort_key(const SortArgs& a, int32_t i) {
-  return a.keys != nullptr ? a.keys[i] : emb_row(a.ids[i], a.begin, a.rows);
+__device__ __forceinline__ int32_t sort_key(const SortArgs& a, int64_t i) {
+  return a.keys != nullptr ? __ldg(a.keys + i) : emb_row(__ldg(a.ids + i), a.begin, a.rows);
 }
 
 template <int J>
-__global__ void __launch_bounds__(EMB_SORT_THREADS) emb_count_kernel(const __grid_constant__ SortArgs a) {
-  extern __shared__ int32_t hist[];
+__global__ void __launch_bounds__(EMB_THREADS) emb_count_kernel(const __grid_constant__ SortArgs a) {
+  __shared__ int32_t hist[1 << EMB_DIGIT];
   pdl_wait();
   pdl_trigger();
-  for (int b = threadIdx.x; b < a.bins; b += EMB_SORT_THREADS) hist[b] = 0;
+  for (int b = threadIdx.x; b < a.bins; b += EMB_THREADS) hist[b] = 0;
   __syncthreads();
-  const int64_t s0 = int64_t(blockIdx.x) * (EMB_SORT_THREADS * J);
+  const int64_t s0 = int64_t(blockIdx.x) * (EMB_THREADS * J);
 #pragma unroll
   for (int j = 0; j < J; ++j) {
-    const int64_t i = s0 + j * EMB_SORT_THREADS + threadIdx.x;
-    if (i < a.n) atomicAdd(&hist[(sort_key(a, i) >> a.shift) & (a.bins - 1)], 1);  // whole numbers: any order gives the same
+    const int64_t i = s0 + j * EMB_THREADS + threadIdx.x;
+    if (i < a.n) atomicAdd(&hist[(sort_key(a, i) >> a.shift) & (a.bins - 1)], 1);
   }
   __syncthreads();
-  for (int b = threadIdx.x; b < a.bins; b += EMB_SORT_THREADS) a.counts[int64_t(blockIdx.x) * a.bins + b] = hist[b];
+  for (int b = threadIdx.x; b < a.bins; b += EMB_THREADS) {
+    int32_t* c = a.counts + int64_t(blockIdx.x) * a.bins + b;
+    *c = hist[b];
+    for (int t = 1; t <= a.clear; ++t) c[int64_t(t) * a.chunks * a.bins] = 0;
+  }
 }
 
-// Exclusive prefix of a block's values, one a thread; *total = their sum.
+// Exclusive prefix over a block's threads; *total = the sum.
 __device__ __forceinline__ int32_t emb_prefix(int32_t x, int32_t* warp_total, int32_t* total) {
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   int32_t s = x;
@@ -81,20 +92,20 @@ __device__ __forceinline__ int32_t emb_prefix(int32_t x, int32_t* warp_total, in
   }
   if (lane == 31) warp_total[w] = s;
   __syncthreads();
-  int32_t t = lane < w ? warp_total[lane] : 0, all = warp_total[lane];
-  t = __reduce_add_sync(0xffffffffu, t);
-  *total = __reduce_add_sync(0xffffffffu, all);
+  const int32_t v = lane < EMB_WARPS ? warp_total[lane] : 0;
+  const int32_t t = __reduce_add_sync(0xffffffffu, lane < w ? v : 0);
+  *total = __reduce_add_sync(0xffffffffu, v);
   __syncthreads();
   return t + s - x;
 }
 
 // For very many chunks: each bin's counts to what lies before each chunk.
-__global__ void __launch_bounds__(EMB_SORT_THREADS) emb_scan_kernel(const __grid_constant__ SortArgs a) {
+__global__ void __launch_bounds__(EMB_THREADS) emb_scan_kernel(const __grid_constant__ SortArgs a) {
   __shared__ int32_t warp_total[EMB_WARPS];
   pdl_wait();
   pdl_trigger();
   int32_t carry = 0;
-  for (int64_t c0 = 0; c0 < a.chunks; c0 += EMB_SORT_THREADS) {
+  for (int64_t c0 = 0; c0 < a.chunks; c0 += EMB_THREADS) {
     const int64_t c = c0 + threadIdx.x;
     const int32_t x = c < a.chunks ? a.counts[c * a.bins + blockIdx.x] : 0;
     int32_t all;
@@ -109,82 +120,99 @@ __global__ void __launch_bounds__(EMB_SORT_THREADS) emb_scan_kernel(const __grid
 // counts them by digit in shared memory; a prefix over the warps turns the
 // counts into the warp's starts in the chunk.
 template <int J>
-__global__ void __launch_bounds__(EMB_SORT_THREADS) emb_scatter_kernel(const __grid_constant__ SortArgs a) {
-  extern __shared__ int32_t at[];  // [EMB_WARPS][bins], the bins' totals, what lies before the chunk
+__global__ void __launch_bounds__(EMB_THREADS) emb_scatter_kernel(const __grid_constant__ SortArgs a) {
+  __shared__ int32_t at[EMB_WARPS][1 << EMB_DIGIT], start[1 << EMB_DIGIT];
   __shared__ int32_t warp_total[EMB_WARPS];
   pdl_wait();
   pdl_trigger();
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, bins = a.bins;
-  const int64_t s0 = int64_t(blockIdx.x) * (EMB_SORT_THREADS * J) + w * (32 * J);
-  int32_t *mine = at + w * bins, *total = at + EMB_WARPS * bins, *before = total + bins;
+  const int64_t s0 = int64_t(blockIdx.x) * (EMB_THREADS * J) + w * (32 * J);
   int32_t key[J], token[J], rank[J];
 #pragma unroll
   for (int j = 0; j < J; ++j) {
     const int64_t i = s0 + j * 32 + lane;
     key[j] = i < a.n ? sort_key(a, i) : -1;
-    token[j] = i < a.n && a.tokens != nullptr ? a.tokens[i] : static_cast<int32_t>(i);
+    token[j] = i < a.n && a.tokens != nullptr ? __ldg(a.tokens + i) : static_cast<int32_t>(i);
   }
-  for (int i = threadIdx.x; i < (EMB_WARPS + 2) * bins; i += EMB_SORT_THREADS) at[i] = 0;
-  __syncthreads();
+  // The thread's bins: how many there are in all, and before this chunk.
+  const int b0 = threadIdx.x * EMB_EACH;
+  int32_t total[EMB_EACH] = {}, before[EMB_EACH] = {};
+  if (a.totals != nullptr) {
+#pragma unroll
+    for (int q = 0; q < EMB_EACH; ++q)
+      if (b0 + q < bins) {
+        total[q] = __ldg(a.totals + b0 + q);
+        before[q] = __ldg(a.counts + int64_t(blockIdx.x) * bins + b0 + q);
+      }
+  } else if (a.chunks > 1) {
+#pragma unroll 8
+    for (int c = 0; c < a.chunks; ++c)
+#pragma unroll
+      for (int q = 0; q < EMB_EACH; ++q)
+        if (b0 + q < bins) {
+          const int32_t v = __ldg(a.counts + int64_t(c) * bins + b0 + q);
+          total[q] += v;
+          if (c < static_cast<int>(blockIdx.x)) before[q] += v;
+        }
+  }
+  for (int b = lane; b < bins; b += 32) at[w][b] = 0;
+  __syncwarp();
 #pragma unroll
   for (int j = 0; j < J; ++j) {
     const int d = key[j] < 0 ? -1 : (key[j] >> a.shift) & (bins - 1);
     const unsigned same = __match_any_sync(0xffffffffu, d);
-    rank[j] = d >= 0 ? mine[d] + __popc(same & ((1u << lane) - 1u)) : 0;
+    rank[j] = d >= 0 ? at[w][d] + __popc(same & ((1u << lane) - 1u)) : 0;
     __syncwarp();
-    if (d >= 0 && lane == __ffs(same) - 1) mine[d] += __popc(same);
+    if (d >= 0 && lane == __ffs(same) - 1) at[w][d] += __popc(same);
     __syncwarp();
-  }
-  if (a.chunks > 1 && a.totals == nullptr) {
-    for (int c = w; c < a.chunks; c += EMB_WARPS)
-      for (int x = lane; x < bins; x += 32) {
-        const int32_t v = a.counts[int64_t(c) * bins + x];
-        if (v != 0) {
-          atomicAdd(&total[x], v);
-          if (c < static_cast<int>(blockIdx.x)) atomicAdd(&before[x], v);
-        }
-      }
   }
   __syncthreads();
-  const int x = threadIdx.x;
-  int32_t sum = 0;
-  if (x < bins) {
-    for (int k = 0; k < EMB_WARPS; ++k) {
-      const int32_t c = at[k * bins + x];
-      at[k * bins + x] = sum;
-      sum += c;
+  int32_t all = 0;
+#pragma unroll
+  for (int q = 0; q < EMB_EACH; ++q)
+    if (b0 + q < bins) {
+      int32_t sum = 0;
+#pragma unroll
+      for (int k = 0; k < EMB_WARPS; ++k) {
+        const int32_t c = at[k][b0 + q];
+        at[k][b0 + q] = sum;
+        sum += c;
+      }
+      if (a.chunks == 1) total[q] = sum;
+      all += total[q];
     }
-    if (a.chunks > 1) sum = a.totals != nullptr ? a.totals[x] : total[x];
-  }
-  int32_t all;
-  const int32_t start = emb_prefix(x < bins ? sum : 0, warp_total, &all);
-  if (x < bins) before[x] = start + (a.totals != nullptr ? a.counts[int64_t(blockIdx.x) * bins + x] : before[x]);
+  int32_t whole, s = emb_prefix(all, warp_total, &whole);
+#pragma unroll
+  for (int q = 0; q < EMB_EACH; ++q)
+    if (b0 + q < bins) {
+      start[b0 + q] = s + before[q];
+      s += total[q];
+    }
   __syncthreads();
 #pragma unroll
   for (int j = 0; j < J; ++j) {
     if (key[j] < 0) continue;
     const int d = (key[j] >> a.shift) & (bins - 1);
-    const int32_t to = before[d] + mine[d] + rank[j];
+    const int32_t to = start[d] + at[w][d] + rank[j];
     if (!GRS_CHECK(to >= 0 && to < a.n, emb_flags, SITE_EMB_TOKEN)) continue;
     a.keys_out[to] = key[j];
     a.tokens_out[to] = token[j];
+    if (a.next != nullptr)
+      atomicAdd(a.next + int64_t(to / (EMB_THREADS * J)) * bins + ((static_cast<uint32_t>(key[j]) >> a.shift) / bins & (bins - 1)), 1);
   }
 }
 
-// starts[r] = how many of the sorted rows are below r, r in [0, rows].
-__global__ void __launch_bounds__(EMB_THREADS) emb_starts_kernel(const int32_t* __restrict__ keys, int32_t n, int32_t rows,
-                                                                 int32_t* __restrict__ starts) {
-  pdl_wait();
-  pdl_trigger();
-  const int64_t r = int64_t(blockIdx.x) * EMB_THREADS + threadIdx.x;
-  if (r > rows) return;
-  int32_t lo = 0, hi = n;
+// How many of keys[lo, hi) are below `key`, plus lo: a warp, 32 places a step.
+__device__ __forceinline__ int32_t warp_lower_bound(const int32_t* keys, int64_t lo, int64_t hi, int64_t key) {
+  const int lane = threadIdx.x & 31;
   while (lo < hi) {
-    const int32_t mid = lo + (hi - lo) / 2;
-    if (__ldg(keys + mid) < r) lo = mid + 1;
-    else hi = mid;
+    const int64_t step = (hi - lo + 31) / 32, i = lo + lane * step;
+    const int below = __popc(__ballot_sync(0xffffffffu, i < hi && __ldg(keys + i) < key));
+    if (below == 0) break;
+    hi = lo + below * step < hi ? lo + below * step : hi;
+    lo += (below - 1) * step + 1;
   }
-  starts[r] = lo;
+  return static_cast<int32_t>(lo);
 }
 
 // ------------------------------------------------------------------- sums
@@ -192,90 +220,192 @@ template <typename T, typename G>
 struct EmbArgs {
   const T* dy;
   G* dtable;
-  const int32_t *keys, *tokens, *starts;
-  float* parts;  // [windows][2][d]
-  int32_t n, rows, d, units, window;
-  int32_t group;  // threads of a row, a power of 2
+  const int32_t *keys, *tokens;
+  float* parts;       // [windows][2][d]
+  int32_t n, rows, d, units, window, windows;
+  int32_t group;      // threads of a row, a power of 2
+  int32_t each;       // rows of a block
   float scale;
 };
 
-// Adds the vectors of the sorted tokens [from, to), elements [c, c + E), in order.
+// E elements of a vector on their way, as they are in memory.
+template <typename T, int E>
+struct Bits {
+  static constexpr int N = E == 1 ? 1 : static_cast<int>(sizeof(T)) / 2;
+  uint4 w[N];
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int i = 0; i < N; ++i) w[i] = make_uint4(0, 0, 0, 0);
+  }
+  __device__ __forceinline__ void load(const T* p) {
+    if constexpr (E == 1) {
+      if constexpr (sizeof(T) == 2) w[0].x = uint32_t(__ldg(p)) << 16;
+      else w[0].x = __float_as_uint(__ldg(p));
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i) w[i] = __ldcs(reinterpret_cast<const uint4*>(p) + i);
+    }
+  }
+  __device__ __forceinline__ void add_to(float (&s)[E]) const {
+    if constexpr (E == 1) {
+      s[0] += __uint_as_float(w[0].x);
+    } else if constexpr (sizeof(T) == 2) {
+      add_bf16x8(s, w[0]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        s[4 * i] += __uint_as_float(w[i].x);
+        s[4 * i + 1] += __uint_as_float(w[i].y);
+        s[4 * i + 2] += __uint_as_float(w[i].z);
+        s[4 * i + 3] += __uint_as_float(w[i].w);
+      }
+    }
+  }
+};
+
+// Adds the vectors of tokens[from, to), elements [c, c + E), in order.  The
+// loads of a batch are all on their way before the first is used.
 template <int E, typename T, typename G>
-__device__ __forceinline__ void emb_add(const EmbArgs<T, G>& a, int32_t from, int32_t to, int64_t c, float (&s)[E]) {
-  constexpr int B = 8;  // loads in flight
+__device__ __forceinline__ void emb_add(const EmbArgs<T, G>& a, const int32_t* tokens, int32_t from, int32_t to, int64_t c, float (&s)[E]) {
+  constexpr int B = E == 8 && sizeof(T) == 4 ? 4 : 8;
+#pragma unroll 1
   for (int32_t p0 = from; p0 < to; p0 += B) {
-    float v[B][E];
+    Bits<T, E> v[B];
 #pragma unroll
     for (int b = 0; b < B; ++b) {
-#pragma unroll
-      for (int q = 0; q < E; ++q) v[b][q] = 0.0f;
+      v[b].clear();
       if (p0 + b < to) {
-        const int32_t t = __ldg(a.tokens + p0 + b);
-        if (GRS_CHECK(t >= 0 && t < a.n, emb_flags, SITE_EMB_TOKEN)) load_floats<E>(a.dy + int64_t(t) * a.d + c, v[b]);
+        const int32_t t = tokens[p0 + b];
+        if (GRS_CHECK(t >= 0 && t < a.n, emb_flags, SITE_EMB_TOKEN)) v[b].load(a.dy + int64_t(t) * a.d + c);
       }
     }
 #pragma unroll
     for (int b = 0; b < B; ++b)
-      if (p0 + b < to)
-#pragma unroll
-        for (int q = 0; q < E; ++q) s[q] += v[b][q];
+      if (p0 + b < to) v[b].add_to(s);
   }
 }
 
-// Parts of the rows of more than a window of tokens: a block a window.
-template <typename T, typename G, int E>
-__global__ void __launch_bounds__(EMB_THREADS) emb_parts_kernel(const __grid_constant__ EmbArgs<T, G> a) {
-  pdl_wait();
-  pdl_trigger();
-  const int64_t p0 = int64_t(blockIdx.x) * a.window, p1 = p0 + a.window < a.n ? p0 + a.window : a.n;
-  int32_t done = -1;
-  for (int slot = 0; slot < 2; ++slot) {
-    const int32_t row = __ldg(a.keys + (slot == 0 ? p0 : p1 - 1));
-    if (row == done || row >= a.rows) break;  // (one row all the window long; from here on tokens without a row)
-    done = row;
-    const int32_t s = __ldg(a.starts + row), e = __ldg(a.starts + row + 1);
-    if (e - s <= a.window) continue;
-    for (int64_t u = threadIdx.x; u < a.units; u += EMB_THREADS) {
-      float sum[E] = {};
-      emb_add<E>(a, s > p0 ? s : static_cast<int32_t>(p0), e < p1 ? e : static_cast<int32_t>(p1), u * E, sum);
-      float* o = a.parts + (int64_t(blockIdx.x) * 2 + slot) * a.d + u * E;
+template <int E, typename T, typename G>
+__device__ __forceinline__ void emb_store(const EmbArgs<T, G>& a, int64_t row, int64_t c, float (&s)[E]) {
 #pragma unroll
-      for (int q = 0; q < E; ++q) o[q] = sum[q];
-    }
-  }
+  for (int q = 0; q < E; ++q) s[q] *= a.scale;
+  if (GRS_CHECK(row < a.rows && c + E <= a.d, emb_flags, SITE_EMB_ROW)) store_floats<E>(a.dtable + row * a.d + c, s);
 }
 
-// dtable[row] = scale * the sum of its tokens' vectors.  A group of threads
-// takes a row, a thread E elements at a time; most rows of a large vocabulary
-// have no token and are zeros to store.
+// Window w of the sorted tokens: whether its first row comes in from the left
+// and its last one goes on to the right.
+struct Window {
+  int64_t p0, p1;
+  int32_t first, last;
+  bool in, on;
+  template <typename T, typename G>
+  __device__ __forceinline__ Window(const EmbArgs<T, G>& a, int64_t w) {
+    p0 = w * a.window;
+    p1 = p0 + a.window < a.n ? p0 + a.window : a.n;
+    first = __ldg(a.keys + p0);
+    last = __ldg(a.keys + p1 - 1);
+    in = first < a.rows && p0 > 0 && __ldg(a.keys + p0 - 1) == first;
+    on = last < a.rows && p1 < a.n && __ldg(a.keys + p1) == last;
+  }
+};
+
+// Rows without tokens are most of a large vocabulary: zeros to store.  The
+// first blocks add up the windows' parts, so that these are long done when the
+// last rows are stored.
 template <typename T, typename G, int E>
 __global__ void __launch_bounds__(EMB_THREADS) emb_sum_kernel(const __grid_constant__ EmbArgs<T, G> a) {
+  __shared__ int32_t starts[EMB_MAX_ROWS + 1], tokens[EMB_TOKENS];
   pdl_wait();
   pdl_trigger();
-  const int group = a.group, g = threadIdx.x / group, u0 = threadIdx.x - g * group, groups = EMB_THREADS / group;
-  const int64_t first = int64_t(blockIdx.x) * (EMB_ROWS * groups) + g;
-#pragma unroll 1
-  for (int k = 0; k < EMB_ROWS; ++k) {
-    const int64_t row = first + k * groups;
-    if (row >= a.rows) return;
-    const int32_t s = __ldg(a.starts + row), e = __ldg(a.starts + row + 1);
-    for (int u = u0; u < a.units; u += group) {
-      const int64_t c = int64_t(u) * E;
-      float sum[E] = {};
-      if (e - s <= a.window) {
-        emb_add<E>(a, s, e, c, sum);
-      } else {
-        for (int32_t w = s / a.window; w <= (e - 1) / a.window; ++w) {
-          const int slot = w * int64_t(a.window) >= s ? 0 : 1;
-          const float* p = a.parts + (int64_t(w) * 2 + slot) * a.d + c;
+  const int w = threadIdx.x >> 5;
+  if (static_cast<int64_t>(blockIdx.x) < a.windows) {
+    const Window x(a, blockIdx.x);
+    for (int slot = 0; slot < 2; ++slot) {
+      if (slot == 0 ? !x.in : !x.on || (x.in && x.last == x.first)) continue;
+      const int32_t from = slot == 0 ? static_cast<int32_t>(x.p0) : warp_lower_bound(a.keys, x.p0, x.p1, x.last);
+      const int32_t to = slot == 0 ? warp_lower_bound(a.keys, x.p0, x.p1, int64_t(x.first) + 1) : static_cast<int32_t>(x.p1);
+      for (int64_t u = threadIdx.x; u < a.units; u += EMB_THREADS) {
+        float sum[E] = {};
+        emb_add<E>(a, a.tokens, from, to, u * E, sum);
+        float* o = a.parts + (int64_t(blockIdx.x) * 2 + slot) * a.d + u * E;
 #pragma unroll
-          for (int q = 0; q < E; ++q) sum[q] += p[q];
-        }
+        for (int q = 0; q < E; ++q) o[q] = sum[q];
       }
-#pragma unroll
-      for (int q = 0; q < E; ++q) sum[q] *= a.scale;
-      if (GRS_CHECK(c + E <= a.d, emb_flags, SITE_EMB_ROW)) store_floats<E>(a.dtable + row * a.d + c, sum);
     }
+    return;
+  }
+  const int64_t row0 = (int64_t(blockIdx.x) - a.windows) * a.each;
+  const int rows = a.rows - row0 < a.each ? static_cast<int>(a.rows - row0) : a.each;
+  if (w < 2) {
+    const int32_t at = warp_lower_bound(a.keys, 0, a.n, row0 + (w == 0 ? 0 : rows));
+    starts[w == 0 ? 0 : rows] = at;
+  }
+  __syncthreads();
+  const int32_t lo = starts[0], hi = starts[rows];
+  for (int r = threadIdx.x; r > 0 && r < rows; r += EMB_THREADS) {
+    int32_t b = lo, e = hi;
+    while (b < e) {
+      const int32_t mid = b + (e - b) / 2;
+      if (__ldg(a.keys + mid) < row0 + r) b = mid + 1;
+      else e = mid;
+    }
+    starts[r] = b;
+  }
+  const bool near = hi - lo <= EMB_TOKENS;
+  if (near)
+    for (int i = threadIdx.x; i < hi - lo; i += EMB_THREADS) tokens[i] = __ldg(a.tokens + lo + i);
+  __syncthreads();
+  const int g = threadIdx.x / a.group, u0 = threadIdx.x - g * a.group, groups = EMB_THREADS / a.group;
+#pragma unroll 1
+  for (int r = g; r < rows; r += groups) {
+    const int32_t s = starts[r], e = starts[r + 1];
+    if (s < e && s / a.window != (e - 1) / a.window) continue;  // joined from its parts
+    for (int u = u0; u < a.units; u += a.group) {
+      float sum[E] = {};
+      if (s < e) {
+        if (near) emb_add<E>(a, tokens, s - lo, e - lo, int64_t(u) * E, sum);
+        else emb_add<E>(a, a.tokens, s, e, int64_t(u) * E, sum);
+      }
+      emb_store<E>(a, row0 + r, int64_t(u) * E, sum);
+    }
+  }
+}
+
+// The row that begins in window w and goes on from it: its parts in order.
+// A block takes some units of the row, its groups of threads a run of the
+// windows each.
+template <typename T, typename G, int E>
+__global__ void __launch_bounds__(EMB_THREADS) emb_join_kernel(const __grid_constant__ EmbArgs<T, G> a) {
+  __shared__ float red[EMB_THREADS / EMB_JOIN][EMB_JOIN][E + 1];
+  pdl_wait();
+  pdl_trigger();
+  const Window x(a, blockIdx.x);
+  if (!x.on || (x.in && x.first == x.last)) return;
+  const int32_t end = warp_lower_bound(a.keys, x.p1, a.n, int64_t(x.last) + 1);
+  const int64_t n = (end - 1) / a.window - int64_t(blockIdx.x) + 1;  // windows
+  constexpr int GROUPS = EMB_THREADS / EMB_JOIN;
+  const int g = threadIdx.x / EMB_JOIN, i = threadIdx.x % EMB_JOIN;
+  const int64_t per = (n + GROUPS - 1) / GROUPS;
+  for (int64_t u0 = int64_t(blockIdx.y) * EMB_JOIN; u0 < a.units; u0 += int64_t(gridDim.y) * EMB_JOIN) {
+    const int64_t u = u0 + i;
+    float sum[E] = {};
+    if (u < a.units) {
+#pragma unroll 4
+      for (int64_t k = g * per; k < n && k < (g + 1) * per; ++k) {
+        const float* p = a.parts + ((blockIdx.x + k) * 2 + (k == 0 ? 1 : 0)) * a.d + u * E;
+#pragma unroll
+        for (int q = 0; q < E; ++q) sum[q] += p[q];
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int q = 0; q < E; ++q) red[g][i][q] = sum[q];
+    __syncthreads();
+    if (g != 0 || u >= a.units) continue;
+    for (int k = 1; k < GROUPS; ++k)
+#pragma unroll
+      for (int q = 0; q < E; ++q) sum[q] += red[k][i][q];
+    emb_store<E>(a, x.last, u * E, sum);
   }
 }
 
@@ -301,10 +431,8 @@ __global__ void __launch_bounds__(EMB_THREADS) emb_forward_kernel(const int32_t*
 struct EmbPlan {
   int32_t rows, bits, passes, digit, window;
   int64_t chunk, chunks, windows;
-  int64_t at_keys, at_tokens, at_counts, at_starts, at_parts, bytes;  // of the workspace
+  int64_t at_keys, at_tokens, at_counts, at_totals, at_parts, bytes;  // of the workspace
 };
-
-int64_t round16(int64_t b) { return (b + 15) & ~int64_t(15); }
 
 EmbPlan emb_plan(const grs_embedding* s) {
   EmbPlan p;
@@ -316,20 +444,20 @@ EmbPlan emb_plan(const grs_embedding* s) {
   // Windows of about sqrt(n) / 4 tokens: a row with all of them is added up in two steps of like length.
   p.window = 32;
   while (int64_t(p.window) * p.window * 16 < s->tokens) p.window *= 2;
-  p.chunk = s->tokens <= 152 * 1024 ? 1024 : 4096;
+  p.chunk = EMB_THREADS * (s->tokens <= 64 * 512 ? 2 : 8);  // small chunks as long as there are few
   p.chunks = (s->tokens + p.chunk - 1) / p.chunk;
   p.windows = (s->tokens + p.window - 1) / p.window;
   int64_t at = 0;
   auto take = [&at](int64_t bytes) {
     const int64_t here = at;
-    at += round16(bytes);
+    at += (bytes + 15) & ~int64_t(15);
     return here;
   };
   p.at_keys = take(2 * s->tokens * 4);
   p.at_tokens = take(2 * s->tokens * 4);
-  p.at_counts = take((p.chunks + 1) * (int64_t(1) << p.digit) * 4);
-  p.at_starts = take((int64_t(p.rows) + 1) * 4);
-  p.at_parts = take(p.windows * 2 * s->hidden * 4);
+  p.at_counts = take(p.passes * p.chunks * (int64_t(1) << p.digit) * 4);
+  p.at_totals = take((int64_t(1) << p.digit) * 4);
+  p.at_parts = take(p.windows > 1 ? p.windows * 2 * s->hidden * 4 : 0);
   p.bytes = at;
   return p;
 }
@@ -351,8 +479,9 @@ cudaError_t emb_sort(const grs_embedding* s, const EmbPlan& p, const int32_t* id
   int32_t* k[2] = {reinterpret_cast<int32_t*>(ws + p.at_keys), reinterpret_cast<int32_t*>(ws + p.at_keys) + n};
   int32_t* t[2] = {reinterpret_cast<int32_t*>(ws + p.at_tokens), reinterpret_cast<int32_t*>(ws + p.at_tokens) + n};
   const int bins = 1 << p.digit;
-  const dim3 grid(static_cast<unsigned>(p.chunks)), block(EMB_SORT_THREADS);
-  cudaError_t e = allow_smem<emb_scatter_kernel<J>>((EMB_WARPS + 2) * (1 << EMB_DIGIT) * 4);
+  const int64_t table = p.chunks * bins;
+  const dim3 grid(static_cast<unsigned>(p.chunks)), block(EMB_THREADS);
+  cudaError_t e = cudaSuccess;
   for (int i = 0; i < p.passes && e == cudaSuccess; ++i) {
     SortArgs a{};
     a.ids = ids;
@@ -360,19 +489,21 @@ cudaError_t emb_sort(const grs_embedding* s, const EmbPlan& p, const int32_t* id
     a.tokens = i == 0 ? nullptr : t[(i - 1) & 1];
     a.keys_out = k[i & 1];
     a.tokens_out = t[i & 1];
-    a.counts = reinterpret_cast<int32_t*>(ws + p.at_counts);
+    a.counts = reinterpret_cast<int32_t*>(ws + p.at_counts) + i * table;
+    a.next = p.chunks > 1 && i + 1 < p.passes ? a.counts + table : nullptr;
     a.n = static_cast<int32_t>(n);
     a.begin = s->row_begin;
     a.rows = p.rows;
     a.shift = i * p.digit;
     a.bins = bins;
     a.chunks = static_cast<int32_t>(p.chunks);
-    if (p.chunks > 1) e = launch_pdl(emb_count_kernel<J>, grid, block, size_t(bins) * 4, stream, a);
-    if (e == cudaSuccess && p.chunks * bins > EMB_TABLE) {
-      a.totals = a.counts + p.chunks * bins;
+    a.clear = p.passes - 1;
+    if (p.chunks > 1 && i == 0) e = launch_pdl(emb_count_kernel<J>, grid, block, 0, stream, a);
+    if (e == cudaSuccess && p.chunks > EMB_MAX_CHUNKS) {
+      a.totals = reinterpret_cast<int32_t*>(ws + p.at_totals);
       e = launch_pdl(emb_scan_kernel, dim3(bins), block, 0, stream, a);
     }
-    if (e == cudaSuccess) e = launch_pdl(emb_scatter_kernel<J>, grid, block, size_t(EMB_WARPS + 2) * bins * 4, stream, a);
+    if (e == cudaSuccess) e = launch_pdl(emb_scatter_kernel<J>, grid, block, 0, stream, a);
     *keys = a.keys_out;
     *tokens = a.tokens_out;
   }
@@ -387,28 +518,34 @@ template <typename T, typename G, int E>
 cudaError_t emb_backward(const grs_embedding* s, const int32_t* ids, const void* dy, void* dtable, uint8_t* ws, void* stream) {
   const EmbPlan p = emb_plan(s);
   EmbArgs<T, G> a{};
-  cudaError_t e = p.chunk == 1024 ? emb_sort<1>(s, p, ids, ws, &a.keys, &a.tokens, stream)
-                                  : emb_sort<4>(s, p, ids, ws, &a.keys, &a.tokens, stream);
-  int32_t* starts = reinterpret_cast<int32_t*>(ws + p.at_starts);
+  cudaError_t e = p.chunk == 2 * EMB_THREADS ? emb_sort<2>(s, p, ids, ws, &a.keys, &a.tokens, stream)
+                                             : emb_sort<8>(s, p, ids, ws, &a.keys, &a.tokens, stream);
   a.dy = static_cast<const T*>(dy);
   a.dtable = static_cast<G*>(dtable);
-  a.starts = starts;
   a.parts = reinterpret_cast<float*>(ws + p.at_parts);
   a.n = static_cast<int32_t>(s->tokens);
   a.rows = p.rows;
   a.d = s->hidden;
   a.units = s->hidden / E;
   a.window = p.window;
+  a.windows = p.windows > 1 ? static_cast<int32_t>(p.windows) : 0;
   a.scale = s->scale;
   a.group = 1;
   while (a.group < a.units && a.group < EMB_THREADS) a.group *= 2;
-  const int64_t each = EMB_ROWS * (EMB_THREADS / a.group), blocks = (p.rows + each - 1) / each;
+  // Rows of a block: as many as leave eight blocks an SM.
+  const int64_t groups = EMB_THREADS / a.group;
+  int64_t each = p.rows / (152 * 8) / groups * groups;
+  if (each < groups) each = groups;
+  if (each > EMB_MAX_ROWS) each = EMB_MAX_ROWS;
+  a.each = static_cast<int32_t>(each);
+  const int64_t blocks = a.windows + (p.rows + each - 1) / each, slices = (int64_t(a.units) + EMB_JOIN - 1) / EMB_JOIN;
+  if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
   const dim3 block(EMB_THREADS);
   if (e == cudaSuccess)
-    e = launch_pdl(emb_starts_kernel, dim3(static_cast<unsigned>(p.rows / EMB_THREADS + 1)), block, 0, stream, a.keys, a.n, p.rows, starts);
-  if (e == cudaSuccess && s->tokens > p.window)
-    e = launch_pdl(emb_parts_kernel<T, G, E>, dim3(static_cast<unsigned>(p.windows)), block, 0, stream, a);
-  if (e == cudaSuccess) e = launch_pdl(emb_sum_kernel<T, G, E>, dim3(static_cast<unsigned>(blocks)), block, 0, stream, a);
+    e = launch_pdl(emb_sum_kernel<T, G, E>, dim3(static_cast<unsigned>(blocks)), block, 0, stream, a);
+  if (e == cudaSuccess && a.windows > 0)
+    e = launch_pdl(emb_join_kernel<T, G, E>, dim3(static_cast<unsigned>(a.windows), static_cast<unsigned>(slices < 65535 ? slices : 65535)), block,
+                   0, stream, a);
   return e;
 }
 

@@ -187,13 +187,20 @@ __global__ void __launch_bounds__(QK_THREADS) qk_backward_kernel(const __grid_co
 // for all heads, and its lane groups take the heads in turn, the next head's
 // loads on their way while one is computed.
 constexpr int QK_MAX_UNITS = 32;       // 16-element units of a head
+constexpr int QK_FWD_ROUNDS = 6;       // heads of a lane group in a block, backward in a tile
+constexpr int QK_BWD_ROUNDS = 4;
+constexpr int QK_BWD_BLOCKS = 2;       // an SM
 constexpr int QK_TABLE = 32 * 1024;    // bytes of sines and cosines at most
+constexpr int QK_MAX_TOKENS = 128;     // of a block
+constexpr int64_t QK_MAX_LD = 1 << 22; // elements between tokens: those of a block, and one step further, lie within 2^31
+constexpr int QK_BWD_SMEM = 2 * QK_TABLE + 2 * 64 * QK_MAX_UNITS + 2 * 64 * QK_THREADS;
 
 struct QkShape {
   int units, turned, lanes;  // units of a head, of them with a rotated part; lanes that share a head (a power of 2)
   int tokens;                // of a block
 };
 
+// 16 elements on their way: eight from i0, eight from i1 (zeros for -1).
 template <typename T>
 struct Raw {
   static constexpr int N = sizeof(T) == 2 ? 1 : 2;  // 16-byte loads of 8 elements
@@ -205,26 +212,34 @@ struct Raw {
       c[1][k] = i1 >= 0 ? __ldcs(reinterpret_cast<const uint4*>(p + i1) + k) : make_uint4(0, 0, 0, 0);
     }
   }
-  __device__ __forceinline__ void floats(float (&o)[16]) const {
+  __device__ __forceinline__ void pairs(float2 (&o)[8]) const {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       if constexpr (sizeof(T) == 2) {
-        float v[8];
-        set_bf16x8(v, c[h][0]);
-#pragma unroll
-        for (int q = 0; q < 8; ++q) o[8 * h + q] = v[q];
+        o[4 * h] = bf16_pair(c[h][0].x);
+        o[4 * h + 1] = bf16_pair(c[h][0].y);
+        o[4 * h + 2] = bf16_pair(c[h][0].z);
+        o[4 * h + 3] = bf16_pair(c[h][0].w);
       } else {
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          o[8 * h + 4 * k] = __uint_as_float(c[h][k].x);
-          o[8 * h + 4 * k + 1] = __uint_as_float(c[h][k].y);
-          o[8 * h + 4 * k + 2] = __uint_as_float(c[h][k].z);
-          o[8 * h + 4 * k + 3] = __uint_as_float(c[h][k].w);
+          o[4 * h + 2 * k] = make_float2(__uint_as_float(c[h][k].x), __uint_as_float(c[h][k].y));
+          o[4 * h + 2 * k + 1] = make_float2(__uint_as_float(c[h][k].z), __uint_as_float(c[h][k].w));
         }
       }
     }
   }
 };
+
+template <typename T>
+__device__ __forceinline__ void store_chunk(T* p, const float2* v) {
+  if constexpr (sizeof(T) == 2) {
+    __stcs(reinterpret_cast<uint4*>(p), make_uint4(to_bf16_pair(v[0]), to_bf16_pair(v[1]), to_bf16_pair(v[2]), to_bf16_pair(v[3])));
+  } else {
+    __stcs(reinterpret_cast<float4*>(p), make_float4(v[0].x, v[0].y, v[1].x, v[1].y));
+    __stcs(reinterpret_cast<float4*>(p) + 1, make_float4(v[2].x, v[2].y, v[3].x, v[3].y));
+  }
+}
 
 // The lane's 16 elements: eight from i0, eight from i1 (-1: none), and whether these are turned.
 template <bool kPairs>
@@ -246,225 +261,318 @@ struct Unit {
       r0 = r1 = true;
     }
   }
-  // v turned by the unit's eight angles (back: by their negatives).
-  __device__ __forceinline__ void turn(float (&v)[16], const float4* table, int turned, bool back) const {
+  // v turned by the unit's eight angles, or back: entry q has (cos, cos, sin, sin) of its angles 2 q and 2 q + 1.
+  template <bool kBack>
+  __device__ __forceinline__ void turn(float2 (&v)[8], const float4* table, int turned) const {
     if (!r0) return;
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       if (kPairs && q >= 2 && !r1) break;
       const float4 t = table[q * turned];
+      if constexpr (kPairs) {
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const int j = 2 * q + k, a = kPairs ? 2 * j : j, b = kPairs ? 2 * j + 1 : j + 8;
-        const float c = k == 0 ? t.x : t.z, s = back ? -(k == 0 ? t.y : t.w) : (k == 0 ? t.y : t.w), x = v[a], y = v[b];
-        v[a] = __fmaf_rn(x, c, -(y * s));
-        v[b] = __fmaf_rn(x, s, y * c);
+        for (int k = 0; k < 2; ++k) {
+          const float c = k == 0 ? t.x : t.y, s = kBack ? -(k == 0 ? t.z : t.w) : (k == 0 ? t.z : t.w);
+          const float2 a = v[2 * q + k];
+          v[2 * q + k] = make_float2(__fmaf_rn(a.x, c, -(a.y * s)), __fmaf_rn(a.x, s, a.y * c));
+        }
+      } else {
+        const float2 c = make_float2(t.x, t.y), s = make_float2(t.z, t.w), m = make_float2(-t.z, -t.w), a = v[q], b = v[q + 4];
+        v[q] = fma2(b, kBack ? s : m, mul2(a, c));
+        v[q + 4] = fma2(a, kBack ? m : s, mul2(b, c));
       }
     }
   }
 };
 
-template <typename T>
-__device__ __forceinline__ void store_unit(T* p, int i0, int i1, const float (&v)[16]) {
-  float a[8], b[8];
-#pragma unroll
-  for (int q = 0; q < 8; ++q) {
-    a[q] = v[q];
-    b[q] = v[8 + q];
-  }
-  if (i0 >= 0) store_floats<8>(p + i0, a);
-  if (i1 >= 0) store_floats<8>(p + i1, b);
-}
-
 __device__ __forceinline__ float lanes_sum(float x, int lanes) {
-  for (int o = lanes / 2; o > 0; o >>= 1) x = __fadd_rn(x, __shfl_xor_sync(0xffffffffu, x, o));
+#pragma unroll
+  for (int o = 1; o < 32; o *= 2)
+    if (o < lanes) x = __fadd_rn(x, __shfl_xor_sync(0xffffffffu, x, o));
   return x;
 }
 
 // Shared memory of a block: the angles of its tokens, [token][4][turned] of
-// two (cos, sin), and the weights, [2][4][units] of four.
+// (cos, cos, sin, sin), and the weights, [2][4][units] of four.
 template <typename T, typename P, bool kPairs>
 __device__ __forceinline__ void qk_weights_to_smem(const QkArgs<T, P>& a, const QkShape& s, float* w) {
   for (int i = threadIdx.x; i < 2 * 16 * s.units; i += QK_THREADS) {
-    const int which = i / (16 * s.units), u = i % (16 * s.units) / 16, j = i % 16;
+    const int which = i >= 16 * s.units, k = i - which * 16 * s.units, u = k / 16, j = k % 16;
     const Unit<kPairs> x(u, s.units, a.d, a.rot);
     const int at = j < 8 ? x.i0 + j : x.i1 + j - 8;
     const bool on = (j < 8 || x.i1 >= 0) && a.heads[which] > 0;
     w[((which * 4 + j / 4) * s.units + u) * 4 + j % 4] = on ? weight(a, which, at) : 0.0f;
   }
 }
+// A thread's angles, the i-th with i = its number plus a multiple of the
+// block's threads: the first one's position can be asked for ahead.
 template <typename T, typename P>
-__device__ __forceinline__ void qk_angles_to_smem(const QkArgs<T, P>& a, const QkShape& s, int64_t t0, int tokens, float2* table) {
-  const int half = a.rot / 2, all = s.turned * 8;
-  for (int i = threadIdx.x; i < tokens * all; i += QK_THREADS) {
-    const int t = i / all, p = i - t * all, u = p / 8, j = p % 8;
-    if (p < half) table[((t * 4 + j / 2) * s.turned + u) * 2 + j % 2] = turn_of(__ldg(a.positions + t0 + t), __ldg(a.turns + p));
+struct Angles {
+  const QkArgs<T, P>& a;
+  const QkShape& s;
+  int t, p;
+  int32_t ahead = 0;
+  __device__ __forceinline__ Angles(const QkArgs<T, P>& a_, const QkShape& s_) : a(a_), s(s_) {
+    const int all = s.turned * 8;
+    t = all > 0 ? threadIdx.x / all : 0;
+    p = threadIdx.x - t * all;
   }
-}
-
-// Head number `i` of a block's tokens: queries of all tokens first, then keys.
-template <typename T, typename P>
-struct Place {
-  int which, t;
-  int64_t x, y;
-  __device__ __forceinline__ Place(const QkArgs<T, P>& a, int64_t t0, int tokens, int i) {
-    const int q = tokens * a.heads[0];
-    which = i >= q;
-    if (which) i -= q;
-    const unsigned n = a.heads[which];
-    t = static_cast<unsigned>(i) / n;
-    const int64_t h = int64_t(i - t * static_cast<int>(n)) * a.d;
-    x = (t0 + t) * a.ld_x[which] + h;
-    y = (t0 + t) * a.ld_y[which] + h;
+  __device__ __forceinline__ bool first(int tokens) const { return s.turned > 0 && t < tokens && p < a.rot / 2; }
+  __device__ __forceinline__ void ask(int64_t t0, int tokens) {
+    if (first(tokens)) ahead = __ldg(a.positions + t0 + t);
+  }
+  __device__ __forceinline__ void put(float* table, int ti, int pi, int32_t position) const {
+    const float2 cs = turn_of(position, __ldg(a.turns + pi));
+    float* o = table + ((ti * 4 + pi % 8 / 2) * s.turned + pi / 8) * 4 + pi % 2;
+    o[0] = cs.x;
+    o[2] = cs.y;
+  }
+  __device__ __forceinline__ void store(int64_t t0, int tokens, float* table) const {
+    if (first(tokens)) put(table, t, p, ahead);
+    const int all = s.turned * 8, n = tokens * all;
+    for (int i = threadIdx.x + QK_THREADS; i < n; i += QK_THREADS) {
+      const int ti = i / all, pi = i - ti * all;
+      if (pi < a.rot / 2) put(table, ti, pi, __ldg(a.positions + t0 + ti));
+    }
   }
 };
 
+// A lane group's way through the heads of a block's tokens, queries or keys:
+// every slots-th, and where they lie in the inputs and in the outputs.
+struct Way {
+  int t, h, dt, dh, n;
+  int32_t x, y, dx, dy, wrap_x, wrap_y;  // of a block's first token; QK_MAX_LD keeps them in 32 bits
+  template <typename T, typename P>
+  __device__ __forceinline__ Way(const QkArgs<T, P>& a, int w, int slot, int slots) : n(a.heads[w]) {
+    const int32_t ld_x = static_cast<int32_t>(a.ld_x[w]), ld_y = static_cast<int32_t>(a.ld_y[w]);
+    t = n > 0 ? slot / n : 0;
+    h = slot - t * n;
+    dt = n > 0 ? slots / n : 0;
+    dh = slots - dt * n;
+    x = t * ld_x + h * a.d;
+    y = t * ld_y + h * a.d;
+    dx = dt * ld_x + dh * a.d;
+    dy = dt * ld_y + dh * a.d;
+    wrap_x = ld_x - n * a.d;
+    wrap_y = ld_y - n * a.d;
+  }
+  __device__ __forceinline__ void step() {
+    t += dt;
+    h += dh;
+    x += dx;
+    y += dy;
+    if (h >= n) {
+      h -= n;
+      ++t;
+      x += wrap_x;
+      y += wrap_y;
+    }
+  }
+};
+
+__device__ __forceinline__ float squares_sum(const float2 (&v)[8]) {
+  float2 s = mul2(v[0], v[0]);
+#pragma unroll
+  for (int q = 1; q < 8; ++q) s = fma2(v[q], v[q], s);
+  return s.x + s.y;
+}
+
+// The heads of one kind; `raw` holds the first one's elements, and at the end
+// those of the first of the keys (W = 0), whose way is `after`.
+template <int W, typename T, typename P, bool kPairs>
+__device__ __forceinline__ void qk_forward_heads(const QkArgs<T, P>& a, const QkShape& s, int64_t t0, int tokens, int slots, Way way,
+                                                 const Way& after, const Unit<kPairs>& unit, int u, const float4* table, const float4* weights,
+                                                 Raw<T>& raw) {
+  const int rounds = (tokens * a.heads[W] + slots - 1) / slots;  // whole warps stay together for the sums
+  const T* const x = a.x[W] + t0 * a.ld_x[W];
+  T* const o = a.o[W] + t0 * a.ld_y[W];
+#pragma unroll 1
+  for (int r = 0; r < rounds; ++r) {
+    float2 v[8];
+    raw.pairs(v);
+    const int t = way.t;
+    const int32_t y = way.y;
+    way.step();
+    if (r + 1 < rounds) {
+      if (way.t < tokens) raw.load(x + way.x, unit.i0, unit.i1);
+    } else if (W == 0 && after.n > 0 && after.t < tokens) {
+      raw.load(a.x[1] + t0 * a.ld_x[1] + after.x, unit.i0, unit.i1);
+    }
+    const float rs = rsqrtf(__fmaf_rn(lanes_sum(squares_sum(v), s.lanes), a.inv_d, a.eps));
+    if (t < tokens && unit.i0 >= 0 && GRS_CHECK(t >= 0 && y >= 0, qk_flags, SITE_QK_HEAD)) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const float4 k = weights[(W * 4 + q) * s.units + u];
+        v[2 * q] = mul2(mul2(v[2 * q], both(rs)), make_float2(k.x, k.y));
+        v[2 * q + 1] = mul2(mul2(v[2 * q + 1], both(rs)), make_float2(k.z, k.w));
+      }
+      unit.template turn<false>(v, table + t * 4 * s.turned + u, s.turned);
+      store_chunk(o + y + unit.i0, v);
+      if (unit.i1 >= 0) store_chunk(o + y + unit.i1, v + 4);
+    }
+  }
+}
+
 template <typename T, typename P, bool kPairs>
-__global__ void __launch_bounds__(QK_THREADS) qk_forward_whole_kernel(const __grid_constant__ QkArgs<T, P> a, const QkShape s) {
+__global__ void __launch_bounds__(QK_THREADS) qk_forward_whole_kernel(const __grid_constant__ QkArgs<T, P> a, const __grid_constant__ QkShape s) {
   extern __shared__ float4 shared[];
   float4 *table = shared, *weights = shared + s.tokens * 4 * s.turned;
   pdl_wait();
   pdl_trigger();
   const int64_t t0 = int64_t(blockIdx.x) * s.tokens;
   const int tokens = a.tokens - t0 < s.tokens ? static_cast<int>(a.tokens - t0) : s.tokens;
-  const int u = threadIdx.x % s.lanes, slots = QK_THREADS / s.lanes, items = tokens * (a.heads[0] + a.heads[1]);
+  const int slot = threadIdx.x / s.lanes, u = threadIdx.x - slot * s.lanes, slots = QK_THREADS / s.lanes;
   const Unit<kPairs> unit(u, s.units, a.d, a.rot);
-  int i = threadIdx.x / s.lanes;
-  Raw<T> next;
-  if (i < items) {
-    const Place<T, P> p(a, t0, tokens, i);
-    next.load(a.x[p.which] + p.x, unit.i0, unit.i1);
+  Angles<T, P> angles(a, s);
+  angles.ask(t0, tokens);
+  const Way q(a, 0, slot, slots), k(a, 1, slot, slots);
+  Raw<T> raw;
+  raw.load(nullptr, -1, -1);
+  if (q.n > 0) {
+    if (q.t < tokens) raw.load(a.x[0] + t0 * a.ld_x[0] + q.x, unit.i0, unit.i1);
+  } else if (k.t < tokens) {
+    raw.load(a.x[1] + t0 * a.ld_x[1] + k.x, unit.i0, unit.i1);
   }
   qk_weights_to_smem<T, P, kPairs>(a, s, reinterpret_cast<float*>(weights));
-  qk_angles_to_smem(a, s, t0, tokens, reinterpret_cast<float2*>(table));
+  angles.store(t0, tokens, reinterpret_cast<float*>(table));
   __syncthreads();
-  const int rounds = (items + slots - 1) / slots;  // whole warps stay together for the sums
-  for (int r = 0; r < rounds; ++r, i += slots) {
-    const bool on = i < items;
-    float v[16];
-    if (on) next.floats(v);
-    else
-#pragma unroll
-      for (int q = 0; q < 16; ++q) v[q] = 0.0f;
-    if (i + slots < items) {
-      const Place<T, P> p(a, t0, tokens, i + slots);
-      next.load(a.x[p.which] + p.x, unit.i0, unit.i1);
+  qk_forward_heads<0>(a, s, t0, tokens, slots, q, k, unit, u, table, weights, raw);
+  qk_forward_heads<1>(a, s, t0, tokens, slots, k, k, unit, u, table, weights, raw);
+}
+
+// Backward, likewise; dw: the lane's share of the weight's gradient.
+template <int W, typename T, typename P, bool kPairs>
+__device__ __forceinline__ void qk_backward_heads(const QkArgs<T, P>& a, const QkShape& s, int64_t t0, int tokens, int slots, Way way,
+                                                  const Way& after, const Unit<kPairs>& unit, int u, const float4* table,
+                                                  const float4* weights, Raw<T>& rx, Raw<T>& rg, float2 (&dw)[8]) {
+  const int rounds = (tokens * a.heads[W] + slots - 1) / slots;
+  const T *const px = a.x[W] + t0 * a.ld_x[W], *const pg = a.dy[W] + t0 * a.ld_y[W];
+  T* const o = a.o[W] != nullptr ? a.o[W] + t0 * a.ld_x[W] : nullptr;
+#pragma unroll 1
+  for (int r = 0; r < rounds; ++r) {
+    const int t = way.t;
+    const int32_t at = way.x;
+    const bool on = t < tokens && unit.i0 >= 0;
+    float2 x[8], g[8];
+    rx.pairs(x);
+    rg.pairs(g);
+    way.step();
+    if (r + 1 < rounds) {
+      if (way.t < tokens) {
+        rx.load(px + way.x, unit.i0, unit.i1);
+        rg.load(pg + way.y, unit.i0, unit.i1);
+      }
+    } else if (W == 0 && after.n > 0 && after.t < tokens) {
+      rx.load(a.x[1] + t0 * a.ld_x[1] + after.x, unit.i0, unit.i1);
+      rg.load(a.dy[1] + t0 * a.ld_y[1] + after.y, unit.i0, unit.i1);
     }
-    float sum = 0.0f;
+    const float rs = rsqrtf(__fmaf_rn(lanes_sum(squares_sum(x), s.lanes), a.inv_d, a.eps));
+    float2 dot = both(0.0f);
+    if (on && GRS_CHECK(t >= 0 && at >= 0, qk_flags, SITE_QK_HEAD)) {
+      unit.template turn<true>(g, table + t * 4 * s.turned + u, s.turned);
 #pragma unroll
-    for (int q = 0; q < 16; ++q) sum = __fmaf_rn(v[q], v[q], sum);
-    const float rs = rsqrtf(__fmaf_rn(lanes_sum(sum, s.lanes), a.inv_d, a.eps));
-    if (!on || unit.i0 < 0) continue;
-    const Place<T, P> p(a, t0, tokens, i);
-    if (!GRS_CHECK(p.t < tokens, qk_flags, SITE_QK_HEAD)) continue;
-    const float4* w = weights + p.which * 4 * s.units + u;
+      for (int q = 0; q < 8; ++q) {
+        x[q] = mul2(x[q], both(rs));
+        dw[q] = fma2(g[q], x[q], dw[q]);
+      }
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const float4 k = w[q * s.units];
-      v[4 * q] *= rs * k.x;
-      v[4 * q + 1] *= rs * k.y;
-      v[4 * q + 2] *= rs * k.z;
-      v[4 * q + 3] *= rs * k.w;
+      for (int q = 0; q < 4; ++q) {
+        const float4 k = weights[(W * 4 + q) * s.units + u];
+        g[2 * q] = mul2(g[2 * q], make_float2(k.x, k.y));
+        g[2 * q + 1] = mul2(g[2 * q + 1], make_float2(k.z, k.w));
+        dot = fma2(g[2 * q], x[2 * q], dot);
+        dot = fma2(g[2 * q + 1], x[2 * q + 1], dot);
+      }
     }
-    unit.turn(v, table + p.t * 4 * s.turned + u, s.turned, false);
-    store_unit(a.o[p.which] + p.y, unit.i0, unit.i1, v);
+    const float m = -lanes_sum(dot.x + dot.y, s.lanes) * a.inv_d;
+    if (on && o != nullptr) {
+#pragma unroll
+      for (int q = 0; q < 8; ++q) x[q] = mul2(fma2(x[q], both(m), g[q]), both(rs));
+      store_chunk(o + at + unit.i0, x);
+      if (unit.i1 >= 0) store_chunk(o + at + unit.i1, x + 4);
+    }
   }
 }
 
+// Eight pairs of a thread in shared memory, [4][threads].
+__device__ __forceinline__ void park(float4* at, const float2 (&v)[8]) {
+#pragma unroll
+  for (int q = 0; q < 4; ++q) at[q * QK_THREADS + threadIdx.x] = make_float4(v[2 * q].x, v[2 * q].y, v[2 * q + 1].x, v[2 * q + 1].y);
+}
+__device__ __forceinline__ void unpark(const float4* at, float2 (&v)[8]) {
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const float4 k = at[q * QK_THREADS + threadIdx.x];
+    v[2 * q] = make_float2(k.x, k.y);
+    v[2 * q + 1] = make_float2(k.z, k.w);
+  }
+}
+
+// Blocks stay and take tiles of tokens in turn.  The shares of dwq and dwk are
+// in registers while their heads are computed and in shared memory (each
+// thread its own) while the others' are.
 template <typename T, typename P, bool kPairs>
-__global__ void __launch_bounds__(QK_THREADS) qk_backward_whole_kernel(const __grid_constant__ QkArgs<T, P> a, const QkShape s) {
+__global__ void __launch_bounds__(QK_THREADS, QK_BWD_BLOCKS)
+    qk_backward_whole_kernel(const __grid_constant__ QkArgs<T, P> a, const __grid_constant__ QkShape s) {
   extern __shared__ float4 shared[];
-  float4 *table = shared, *weights = shared + s.tokens * 4 * s.turned;
+  const int entries = s.tokens * 4 * s.turned;  // of a table of angles; there are two
+  float4 *weights = shared + 2 * entries, *parked = weights + 8 * s.units;
   pdl_wait();
   pdl_trigger();
-  const int u = threadIdx.x % s.lanes, slots = QK_THREADS / s.lanes;
+  const int slot = threadIdx.x / s.lanes, u = threadIdx.x - slot * s.lanes, slots = QK_THREADS / s.lanes;
   const Unit<kPairs> unit(u, s.units, a.d, a.rot);
-  float dw[2][16] = {};
+  Angles<T, P> angles(a, s);
+  const Way q(a, 0, slot, slots), k(a, 1, slot, slots);
+  float2 dw[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) dw[i] = both(0.0f);
+  park(parked, dw);
+  park(parked + 4 * QK_THREADS, dw);
   qk_weights_to_smem<T, P, kPairs>(a, s, reinterpret_cast<float*>(weights));
-  for (int64_t t0 = int64_t(blockIdx.x) * s.tokens; t0 < a.tokens; t0 += int64_t(gridDim.x) * s.tokens) {
-    const int tokens = a.tokens - t0 < s.tokens ? static_cast<int>(a.tokens - t0) : s.tokens;
-    const int items = tokens * (a.heads[0] + a.heads[1]);
-    int i = threadIdx.x / s.lanes;
-    Raw<T> nx, ny;
-    if (i < items) {
-      const Place<T, P> p(a, t0, tokens, i);
-      nx.load(a.x[p.which] + p.x, unit.i0, unit.i1);
-      ny.load(a.dy[p.which] + p.y, unit.i0, unit.i1);
+  const int64_t dt = int64_t(gridDim.x) * s.tokens;
+  int64_t t0 = int64_t(blockIdx.x) * s.tokens;
+  auto tokens_at = [&](int64_t t) { return t >= a.tokens ? 0 : a.tokens - t < s.tokens ? static_cast<int>(a.tokens - t) : s.tokens; };
+  angles.ask(t0, tokens_at(t0));
+  for (int flip = 0; t0 < a.tokens; t0 += dt, flip ^= 1) {
+    const int tokens = tokens_at(t0);
+    float4* table = shared + flip * entries;
+    Raw<T> rx, rg;
+    rx.load(nullptr, -1, -1);
+    rg.load(nullptr, -1, -1);
+    if (q.n > 0) {
+      if (q.t < tokens) {
+        rx.load(a.x[0] + t0 * a.ld_x[0] + q.x, unit.i0, unit.i1);
+        rg.load(a.dy[0] + t0 * a.ld_y[0] + q.y, unit.i0, unit.i1);
+      }
+    } else if (k.t < tokens) {
+      rx.load(a.x[1] + t0 * a.ld_x[1] + k.x, unit.i0, unit.i1);
+      rg.load(a.dy[1] + t0 * a.ld_y[1] + k.y, unit.i0, unit.i1);
     }
-    __syncthreads();  // the table may still be read
-    qk_angles_to_smem(a, s, t0, tokens, reinterpret_cast<float2*>(table));
-    __syncthreads();
-    const int rounds = (items + slots - 1) / slots;
-    for (int r = 0; r < rounds; ++r, i += slots) {
-      const bool on = i < items;
-      float x[16], g[16];
-#pragma unroll
-      for (int q = 0; q < 16; ++q) x[q] = g[q] = 0.0f;
-      int which = 0, t = 0;
-      int64_t at = 0;
-      if (on) {
-        const Place<T, P> p(a, t0, tokens, i);
-        which = p.which;
-        t = p.t;
-        at = p.x;
-        nx.floats(x);
-        ny.floats(g);
-        if (!GRS_CHECK(t < tokens, qk_flags, SITE_QK_HEAD)) t = 0;
-      }
-      if (i + slots < items) {
-        const Place<T, P> p(a, t0, tokens, i + slots);
-        nx.load(a.x[p.which] + p.x, unit.i0, unit.i1);
-        ny.load(a.dy[p.which] + p.y, unit.i0, unit.i1);
-      }
-      float sum = 0.0f;
-#pragma unroll
-      for (int q = 0; q < 16; ++q) sum = __fmaf_rn(x[q], x[q], sum);
-      const float rs = rsqrtf(__fmaf_rn(lanes_sum(sum, s.lanes), a.inv_d, a.eps));
-      if (on) unit.turn(g, table + t * 4 * s.turned + u, s.turned, true);
-#pragma unroll
-      for (int q = 0; q < 16; ++q) {
-        x[q] *= rs;
-        const float h = g[q] * x[q];
-        if (which == 0) dw[0][q] += h;
-        else dw[1][q] += h;
-      }
-      float dot = 0.0f;
-      if (unit.i0 >= 0) {
-        const float4* w = weights + which * 4 * s.units + u;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const float4 k = w[q * s.units];
-          g[4 * q] *= k.x;
-          g[4 * q + 1] *= k.y;
-          g[4 * q + 2] *= k.z;
-          g[4 * q + 3] *= k.w;
-        }
-#pragma unroll
-        for (int q = 0; q < 16; ++q) dot = __fmaf_rn(g[q], x[q], dot);
-      }
-      const float m = lanes_sum(dot, s.lanes) * a.inv_d;
-      if (!on || a.o[which] == nullptr || unit.i0 < 0) continue;
-#pragma unroll
-      for (int q = 0; q < 16; ++q) x[q] = rs * __fmaf_rn(-x[q], m, g[q]);
-      store_unit(a.o[which] + at, unit.i0, unit.i1, x);
+    angles.store(t0, tokens, reinterpret_cast<float*>(table));
+    angles.ask(t0 + dt, tokens_at(t0 + dt));
+    __syncthreads();  // (the other table is free: all are done with the tile before)
+    if (q.n > 0) {
+      unpark(parked, dw);
+      qk_backward_heads<0>(a, s, t0, tokens, slots, q, k, unit, u, table, weights, rx, rg, dw);
+      park(parked, dw);
+    }
+    if (k.n > 0) {
+      unpark(parked + 4 * QK_THREADS, dw);
+      qk_backward_heads<1>(a, s, t0, tokens, slots, k, k, unit, u, table, weights, rx, rg, dw);
+      park(parked + 4 * QK_THREADS, dw);
     }
   }
   if (a.parts == nullptr) return;
   // The block's dwq and dwk: the lane groups' sums, in order.
-  float* red = reinterpret_cast<float*>(shared);  // [slots][lanes][16]
-  for (int which = 0; which < 2; ++which) {
-    __syncthreads();
-#pragma unroll
-    for (int q = 0; q < 16; ++q) red[q * QK_THREADS + threadIdx.x] = which == 0 ? dw[0][q] : dw[1][q];
-    __syncthreads();
-    for (int i = threadIdx.x; i < 16 * s.units; i += QK_THREADS) {
-      const int v = i / 16, j = i % 16;
-      const Unit<kPairs> x(v, s.units, a.d, a.rot);
-      if (j >= 8 && x.i1 < 0) continue;
-      float sum = 0.0f;
-      for (int k = 0; k < slots; ++k) sum += red[j * QK_THREADS + k * s.lanes + v];
-      a.parts[(int64_t(blockIdx.x) * 2 + which) * a.d + (j < 8 ? x.i0 + j : x.i1 + j - 8)] = sum;
-    }
+  __syncthreads();
+  const float* red = reinterpret_cast<const float*>(parked);
+  for (int i = threadIdx.x; i < 2 * 16 * s.units; i += QK_THREADS) {
+    const int which = i >= 16 * s.units, n = i - which * 16 * s.units, v = n / 16, j = n % 16;
+    const Unit<kPairs> x(v, s.units, a.d, a.rot);
+    if (j >= 8 && x.i1 < 0) continue;
+    float sum = 0.0f;
+    for (int g = 0; g < slots; ++g) sum += red[((which * 4 + j / 4) * QK_THREADS + g * s.lanes + v) * 4 + j % 4];
+    a.parts[(int64_t(blockIdx.x) * 2 + which) * a.d + (j < 8 ? x.i0 + j : x.i1 + j - 8)] = sum;
   }
 }
 
@@ -521,7 +629,7 @@ bool qk_whole(const grs_qk_norm* s, const int64_t (&ld)[4], const void* a, const
   const int64_t chunk = 16 / dtype_size(s->dtype);
   if (s->head_dim % 8 != 0 || s->rotary_dim % (s->interleaved ? 8 : 16) != 0 || (s->head_dim + 15) / 16 > QK_MAX_UNITS) return false;
   for (int i = 0; i < 4; ++i)
-    if (ld[i] % chunk != 0) return false;
+    if (ld[i] % chunk != 0 || ld[i] > QK_MAX_LD) return false;
   return api_aligned(a, 16) && api_aligned(b, 16) && api_aligned(c, 16) && api_aligned(d, 16) && api_aligned(e, 16) && api_aligned(f, 16);
 }
 
@@ -536,7 +644,7 @@ QkShape qk_shape(const grs_qk_norm* s, int rounds) {
   const int64_t heads = s->q_heads + s->k_heads, slots = QK_THREADS / q.lanes;
   int64_t t = (rounds * slots + heads - 1) / heads;
   if (q.turned > 0 && t > QK_TABLE / (64 * q.turned)) t = QK_TABLE / (64 * q.turned);
-  if (t > 128) t = 128;
+  if (t > QK_MAX_TOKENS) t = QK_MAX_TOKENS;
   if (t > s->tokens / (152 * 4)) t = s->tokens / (152 * 4);
   q.tokens = static_cast<int>(t < 1 ? 1 : t);
   return q;
@@ -577,7 +685,7 @@ QkArgs<T, P> qk_args(const grs_qk_norm* s, const int64_t (&ld)[4], const void* d
 template <typename T, typename P>
 cudaError_t qk_forward(const grs_qk_norm* s, const int64_t (&ld)[4], const QkArgs<T, P>& a, void* stream) {
   if (qk_whole(s, ld, a.x[0], a.x[1], a.o[0], a.o[1], nullptr, nullptr)) {
-    const QkShape q = qk_shape(s, 4);
+    const QkShape q = qk_shape(s, QK_FWD_ROUNDS);
     const int64_t blocks = (s->tokens + q.tokens - 1) / q.tokens;
     if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
     const dim3 grid(static_cast<unsigned>(blocks)), block(QK_THREADS);
@@ -594,11 +702,13 @@ cudaError_t qk_backward(const grs_qk_norm* s, const int64_t (&ld)[4], const QkAr
   int blocks = qk_blocks(s);
   cudaError_t e;
   if (qk_whole(s, ld, a.x[0], a.x[1], a.dy[0], a.dy[1], a.o[0], a.o[1])) {
-    const QkShape q = qk_shape(s, 4);
+    const QkShape q = qk_shape(s, QK_BWD_ROUNDS);
     const int64_t tiles = (s->tokens + q.tokens - 1) / q.tokens;
-    if (blocks > 2 * 152) blocks = 2 * 152;
+    if (blocks > QK_BWD_BLOCKS * 152) blocks = QK_BWD_BLOCKS * 152;
     if (blocks > tiles) blocks = static_cast<int>(tiles);
-    const int smem = qk_smem(q) > 16 * QK_THREADS * 4 ? qk_smem(q) : 16 * QK_THREADS * 4;
+    const int smem = qk_smem(q) + q.tokens * 64 * q.turned + 2 * 64 * QK_THREADS;  // a second table, the parked shares
+    e = s->interleaved ? allow_smem<qk_backward_whole_kernel<T, P, true>>(QK_BWD_SMEM) : allow_smem<qk_backward_whole_kernel<T, P, false>>(QK_BWD_SMEM);
+    if (e != cudaSuccess) return e;
     e = s->interleaved ? launch_pdl(qk_backward_whole_kernel<T, P, true>, dim3(blocks), dim3(QK_THREADS), smem, stream, a, q)
                        : launch_pdl(qk_backward_whole_kernel<T, P, false>, dim3(blocks), dim3(QK_THREADS), smem, stream, a, q);
   } else {

@@ -50,7 +50,10 @@ struct Shape {
   static constexpr int A = MMA_F * MMA_K * 2, B = TC / kCtas * MMA_K * 2, STAGE = A + B;
   static constexpr int FIXED = 1024 + (GRS_MOE_MAX_EXPERTS + 1) * 4 + 512;  // alignment, tiles before each expert, barriers
   static constexpr int FIT = (MMA_SMEM - FIXED) / STAGE;
-  static constexpr int STAGES = FIT < 10 ? FIT : 10;
+#ifndef MAX_STAGES
+#define MAX_STAGES 10
+#endif
+  static constexpr int STAGES = FIT < MAX_STAGES ? FIT : MAX_STAGES;
   static constexpr int BYTES = STAGES * STAGE + FIXED;
 };
 
@@ -208,23 +211,24 @@ __global__ void __launch_bounds__(MMA_THREADS, 1)
   if (w == 0) {
     // ------------------------------------------------------------- loads
     uint32_t s = 0, parity = 1, tail_parity = 0;
+    const uint32_t stages_at = smem_addr(stages);
+    // Both blocks' loads are counted by the first one's barriers.
+    const uint32_t full_at = kCtas == 1 || rank == 0 ? smem_addr(full) : peer_addr(smem_addr(full), 0);
     bool ok = true;
     for (int64_t t = t0; t < tiles.total && ok; t += dt) {
       const Tile x = tiles.at(t);
-      const int64_t blocks = (x.k1 - x.k0 + MMA_K - 1) / MMA_K;
+      const int32_t k_end = static_cast<int32_t>(x.k1);
       const int32_t f0 = static_cast<int32_t>(x.f0) + static_cast<int32_t>(rank) * MMA_F;
       // Columns of this block: half of the instruction's.
       const int32_t half = kWeights ? TC / kCtas : (static_cast<int32_t>(x.c1 - x.c0) + 15) / 16 * 16 / kCtas;
       const int32_t c0 = static_cast<int32_t>(x.c0) + static_cast<int32_t>(rank) * half;
-      for (int64_t kb = 0; kb < blocks && ok; ++kb) {
-        const int32_t k = static_cast<int32_t>(x.k0 + kb * MMA_K);
-        const int32_t valid = x.k1 - k < MMA_K ? static_cast<int32_t>(x.k1 - k) : MMA_K;
+      for (int32_t k = static_cast<int32_t>(x.k0); k < k_end; k += MMA_K) {
+        const int32_t valid = k_end - k < MMA_K ? k_end - k : MMA_K;
         const bool last = kWeights && valid % 16 != 0;
-        ok = __all_sync(0xffffffffu, wait_for(empty + s, parity, abort));
+        if (lane == 0) ok = wait_for(empty + s, parity, abort);
+        if (kWeights) ok = __shfl_sync(0xffffffffu, ok, 0);
         if (!ok) break;
-        uint8_t* stage = stages + s * S::STAGE;
-        const uint32_t to = smem_addr(stage);
-        const uint32_t here = smem_addr(full + s), bar = kCtas == 1 || rank == 0 ? here : peer_addr(here, 0);
+        const uint32_t to = stages_at + s * S::STAGE, bar = full_at + s * 8;
         if (lane == 0) {
           const uint32_t on = last ? smem_addr(tail) : bar;
           if (last) mbar_arrive_expect_tx(tail, S::STAGE);
@@ -251,6 +255,7 @@ __global__ void __launch_bounds__(MMA_THREADS, 1)
           if (!ok) break;
           tail_parity ^= 1;
           const int32_t bad = (16 - valid % 16) * 8;  // 16-byte chunks of the rows to clear, in each 64 of f or c
+          uint8_t* stage = stages + s * S::STAGE;
           for (int32_t i = lane; i < bad * (S::STAGE / 8192); i += 32)
             *reinterpret_cast<uint4*>(stage + i / bad * 8192 + valid * 128 + i % bad * 16) = make_uint4(0, 0, 0, 0);
           fence_async_shared();
@@ -265,36 +270,35 @@ __global__ void __launch_bounds__(MMA_THREADS, 1)
           parity ^= 1;
         }
       }
+      if (!kWeights) ok = __shfl_sync(0xffffffffu, ok, 0);
     }
   } else if (w == 1) {
     // ---------------------------------------------------------- products
     if (lane == 0 && rank == 0) {
       uint32_t s = 0, parity = 0, acc = 0, acc_parity = 1;
+      const uint32_t a_at = operand<kASK>(smem_addr(stages), 8192), b_at = operand<kBSK>(smem_addr(stages) + S::A, 8192);
       bool ok = true;
       for (int64_t t = t0; t < tiles.total && ok; t += dt) {
         const Tile x = tiles.at(t);
-        const int64_t blocks = (x.k1 - x.k0 + MMA_K - 1) / MMA_K;
         const uint32_t n = kWeights ? TC : (static_cast<uint32_t>(x.c1 - x.c0) + 15) / 16 * 16;
         const uint32_t desc = product_desc(kASK, kBSK, MMA_F * kCtas, n);
-        int64_t kb = 0;
-        while (kb < blocks && ok) {
-          const int64_t end = kSections && blocks - kb > MMA_SECTION ? kb + MMA_SECTION : blocks;
+        int32_t rest = static_cast<int32_t>(x.k1 - x.k0);
+        while (rest > 0 && ok) {
           ok = wait_for(taken + acc, acc_parity, abort);
           tmem_after_sync();
           const uint32_t d = tmem + acc * TC;
+          int32_t section = kSections ? MMA_SECTION : INT32_MAX;
           bool add = false;
-          for (; kb < end && ok; ++kb) {
+          for (; rest > 0 && section > 0 && ok; rest -= MMA_K, --section) {
             ok = wait_for(full + s, parity, abort);
             if (!ok) break;
             tmem_after_sync();
-            const uint32_t from = smem_addr(stages + s * S::STAGE);
-            const uint64_t da = operand<kASK>(from, 8192), db = operand<kBSK>(from + S::A, 8192);
-            const int64_t rest = x.k1 - x.k0 - kb * MMA_K;
-            const int steps = rest >= MMA_K ? MMA_K / 16 : static_cast<int>(rest + 15) / 16;
-            for (int i = 0; i < steps; ++i) {
-              mma<kCtas>(d, da + i * operand_step<kASK>, db + i * operand_step<kBSK>, desc, add);
-              add = true;
-            }
+            const uint32_t da = a_at + s * (S::STAGE >> 4), db = b_at + s * (S::STAGE >> 4);
+            mma<kCtas>(d, da, db, desc, add);
+#pragma unroll
+            for (int i = 1; i < MMA_K / 16; ++i)
+              if (rest > 16 * i) mma<kCtas>(d, da + i * operand_step<kASK>, db + i * operand_step<kBSK>, desc, true);
+            add = true;
             mma_commit<kCtas>(empty + s);
             if (++s == S::STAGES) {
               s = 0;

@@ -133,11 +133,12 @@ __device__ __forceinline__ void tmem_wait_store() { asm volatile("tcgen05.wait::
 // rows of 64 bf16 numbers, eight rows (1024 bytes) a swizzled group.  Along a
 // row lies either k (kAlongK: rows are the other index) or the other index
 // (rows are k; the next 64 of it lie `next64` bytes on).
+// The descriptor's lower word has the address, which moves; its upper word stays.
 template <bool kAlongK>
-__device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t next64) {
-  const uint64_t lead = kAlongK ? 1 : next64 >> 4;
-  return uint64_t((addr & 0x3FFFF) >> 4) | lead << 16 | uint64_t(1024 >> 4) << 32 | uint64_t(1) << 46 | uint64_t(2) << 61;
+__device__ __forceinline__ uint32_t operand(uint32_t addr, uint32_t next64) {
+  return (addr & 0x3FFFF) >> 4 | (kAlongK ? 1u : next64 >> 4) << 16;
 }
+constexpr uint32_t OPERAND_UPPER = 1024 >> 4 | 1u << 14 | 2u << 29;
 // Bytes from one step of 16 along k to the next, in units of the descriptor's address.
 template <bool kAlongK>
 constexpr uint32_t operand_step = (kAlongK ? 32 : 16 * 128) >> 4;
@@ -147,19 +148,20 @@ __device__ __forceinline__ constexpr uint32_t product_desc(bool a_along_k, bool 
   return 1u << 4 | 1u << 7 | 1u << 10 | (a_along_k ? 0u : 1u << 15) | (b_along_k ? 0u : 1u << 16) | (n >> 3) << 17 | (m >> 4) << 24;
 }
 
+// d = a b, or d + a b; a and b: lower words of operands.
 template <int kCtas>
-__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t desc, bool add) {
+__device__ __forceinline__ void mma(uint32_t d, uint32_t a, uint32_t b, uint32_t desc, bool add) {
   if constexpr (kCtas == 1)
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(desc), "r"(uint32_t(add))
+        "{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\tsetp.ne.u32 p, %4, 0;\n\tmov.b64 x, {%1, %5};\n\tmov.b64 y, {%2, %5};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(desc), "r"(uint32_t(add)), "r"(OPERAND_UPPER)
         : "memory");
   else
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(desc), "r"(uint32_t(add))
+        "{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\tsetp.ne.u32 p, %4, 0;\n\tmov.b64 x, {%1, %5};\n\tmov.b64 y, {%2, %5};\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], x, y, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(desc), "r"(uint32_t(add)), "r"(OPERAND_UPPER)
         : "memory");
 }
 

@@ -6,9 +6,16 @@
 // once, straight from registers, and an expert's last rows cost only as many
 // columns as there are (in 16s).
 //
-// Blocks stay and take tiles in turn.  One warp loads (TMA, 64 of k a stage),
-// one thread issues the matrix instructions, four warps store; two
-// accumulators, so that a tile is stored while the next is multiplied.
+// Blocks stay and take tiles in turn.  One warp says which (into a ring in
+// shared memory), one loads (TMA, 64 of k a stage), one thread issues the
+// matrix instructions, four warps store; two accumulators, so that a tile is
+// stored while the next is multiplied.
+//
+// Forward and rows' gradients have tiles of one size, taken in a fixed turn.  A
+// tile of the weights' gradient is as long as its expert has rows: there the
+// largest experts come first and blocks take the next tile when they are done
+// (a fixed turn was 1.5 to 2 times as long with experts of a router without
+// balance).  Which block computes a tile changes nothing in it.
 // Operands lie along k or along the other index, as they are in memory: both
 // are layouts that the instruction takes, nothing is transposed.
 //
@@ -40,6 +47,7 @@ constexpr int MMA_THREADS = 256;
 constexpr int MMA_K = 64;            // of k a stage: a swizzled row of bf16
 constexpr int MMA_F = 128;           // features of a block
 constexpr int MMA_SECTION = 8;       // stages that fp32 gradients add up in the tensor cores
+constexpr int RING = 4;              // tiles told ahead
 constexpr int MMA_SMEM = 227 * 1024;
 enum : int { SITE_MMA_ROW = 2 };
 
@@ -48,7 +56,7 @@ __device__ int mma_flags[FLAG_COUNT];
 template <int TC, int kCtas>
 struct Shape {
   static constexpr int A = MMA_F * MMA_K * 2, B = TC / kCtas * MMA_K * 2, STAGE = A + B;
-  static constexpr int FIXED = 1024 + (GRS_MOE_MAX_EXPERTS + 1) * 4 + 512;  // alignment, tiles before each expert, barriers
+  static constexpr int FIXED = 1024 + (GRS_MOE_MAX_EXPERTS + 2) * 4 + 640;  // alignment, tiles before each expert, barriers
   static constexpr int FIT = (MMA_SMEM - FIXED) / STAGE;
 #ifndef MAX_STAGES
 #define MAX_STAGES 10
@@ -67,56 +75,70 @@ struct MmaArgs {
 };
 
 struct Tile {
-  int e;
-  int64_t f0, c0, c1, k0, k1;
+  int32_t e, f0, c0, c1, k0, k1;  // e < 0: no more
 };
 
 template <Product kP, int TC, int kCtas>
 struct Tiles {
   const int32_t* offsets;
-  const int32_t* first;  // c tiles before each expert's (not kWeights)
+  const int32_t* list;  // c tiles before each expert's; kWeights: the experts by size (NULL: as they come)
   int64_t f, c, k, ft, ct, total;
   int32_t rows;
-  int e = 0;
+  int at_e = 0;
 
   template <typename O>
-  __device__ __forceinline__ Tiles(const MmaArgs<O>& a, const int32_t* first_)
-      : offsets(a.offsets), first(first_), f(a.f), c(a.c), k(a.k), rows(a.rows) {
+  __device__ __forceinline__ Tiles(const MmaArgs<O>& a, const int32_t* list_)
+      : offsets(a.offsets), list(list_), f(a.f), c(a.c), k(a.k), rows(a.rows) {
     ft = (f + MMA_F * kCtas - 1) / (MMA_F * kCtas);
     ct = (c + TC - 1) / TC;
-    total = kP == Product::kWeights ? ft * ct * a.experts : ft * first[a.experts];
+    total = kP == Product::kWeights ? ft * ct * a.experts : ft * list[a.experts];
   }
 
-  __device__ __forceinline__ Tile at(int64_t t) {
+  __device__ __forceinline__ Tile at(int64_t t) {  // ascending, unless kWeights
     Tile x;
-    int64_t ci = t / ft;
-    x.f0 = (t - ci * ft) * (MMA_F * kCtas);
-    int32_t from, to;
+    int64_t ci = t / ft, c0, c1;
+    x.f0 = static_cast<int32_t>((t - ci * ft) * (MMA_F * kCtas));
     if constexpr (kP == Product::kWeights) {
-      e = static_cast<int>(ci / ct);
+      const int64_t e = ci / ct;
       ci -= e * ct;
-      x.c0 = ci * TC;
-      x.c1 = c < x.c0 + TC ? c : x.c0 + TC;
+      x.e = list != nullptr ? list[e] : static_cast<int32_t>(e);
+      c0 = ci * TC;
+      c1 = c;
     } else {
-      while (first[e + 1] <= ci) ++e;
+      while (list[at_e + 1] <= ci) ++at_e;
+      x.e = at_e;
     }
-    from = __ldg(offsets + e);
-    to = __ldg(offsets + e + 1);
+    int32_t from = __ldg(offsets + x.e), to = __ldg(offsets + x.e + 1);
     from = from < 0 ? 0 : from > rows ? rows : from;
     to = to < from ? from : to > rows ? rows : to;
     if constexpr (kP == Product::kWeights) {
       x.k0 = from;
       x.k1 = to;
     } else {
-      x.c0 = from + (ci - first[e]) * TC;
-      x.c1 = to < x.c0 + TC ? to : x.c0 + TC;
+      c0 = from + (ci - list[x.e]) * TC;
+      c1 = to;
       x.k0 = 0;
-      x.k1 = k;
+      x.k1 = static_cast<int32_t>(k);
     }
-    x.e = e;
+    x.c0 = static_cast<int32_t>(c0);
+    x.c1 = static_cast<int32_t>(c1 < c0 + TC ? c1 : c0 + TC);
     return x;
   }
 };
+
+// The experts from the one with the most rows on, by a block of at least as many threads.
+__device__ __forceinline__ void by_size(const int32_t* offsets, int32_t experts, int32_t* order) {
+  int32_t* size = order + experts;
+  const int e = threadIdx.x;
+  if (e < experts) size[e] = __ldg(offsets + e + 1) - __ldg(offsets + e);
+  __syncthreads();
+  if (e < experts) {
+    const int32_t n = size[e];
+    int rank = 0;
+    for (int i = 0; i < experts; ++i) rank += size[i] > n || (size[i] == n && i < e);
+    order[rank] = e;
+  }
+}
 
 // Tiles of c before each expert's, by a block of 256.
 template <int TC>
@@ -175,7 +197,10 @@ __global__ void __launch_bounds__(MMA_THREADS, 1)
   int32_t* first = reinterpret_cast<int32_t*>(stages + S::STAGES * S::STAGE);
   uint64_t* full = reinterpret_cast<uint64_t*>(first + ((GRS_MOE_MAX_EXPERTS + 1 + 1) & ~1));
   uint64_t *empty = full + S::STAGES, *done = empty + S::STAGES, *taken = done + 2, *tail = taken + 2;
-  uint32_t* tmem_at = reinterpret_cast<uint32_t*>(tail + 1);
+  uint64_t *told = tail + 1, *heard = told + RING, *answered = heard + RING, *asked = answered + 2;
+  uint4* answers = reinterpret_cast<uint4*>((reinterpret_cast<uintptr_t>(asked + 2) + 15) & ~uintptr_t(15));
+  Tile* ring = reinterpret_cast<Tile*>(answers + 2);
+  uint32_t* tmem_at = reinterpret_cast<uint32_t*>(ring + RING);
   volatile int* abort = reinterpret_cast<int*>(tmem_at + 1);
 
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
@@ -192,21 +217,47 @@ __global__ void __launch_bounds__(MMA_THREADS, 1)
       mbar_init(taken + i, 4 * kCtas);
     }
     mbar_init(tail, 1);
+    for (int i = 0; i < RING; ++i) {
+      mbar_init(told + i, 1);
+      mbar_init(heard + i, rank == 0 ? 6 : 5);  // the loading warp, four storing ones, the issuing thread
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(answered + i, 1);
+      mbar_init(asked + i, kCtas);
+    }
     *abort = 0;
     fence_mbar_init();
   }
   if (w == 1) tmem_alloc<kCtas>(tmem_at, TMEM);
   pdl_wait();
-  pdl_trigger();
-  if constexpr (!kWeights) tile_prefix<TC>(a.offsets, a.experts, a.rows, first);
+  if constexpr (kWeights) {
+    if (a.experts <= MMA_THREADS) by_size(a.offsets, a.experts, first);
+  } else {
+    pdl_trigger();  // (kWeights has blocks that never begin)
+    tile_prefix<TC>(a.offsets, a.experts, a.rows, first);
+  }
   tmem_before_sync();
   if constexpr (kCtas == 2) cluster_sync();
   else __syncthreads();
   tmem_after_sync();
   const uint32_t tmem = *tmem_at;
 
-  Tiles<kP, TC, kCtas> tiles(a, first);
-  const int64_t t0 = blockIdx.x / kCtas, dt = gridDim.x / kCtas;
+  // The next tile of the ring, for a whole warp or one thread of a role.
+  uint32_t slot = 0, slot_parity = 0;
+  auto next_tile = [&](Tile& x) {
+    if (!wait_for(told + slot, slot_parity, abort)) return false;
+    x = ring[slot];
+    return true;
+  };
+  auto heard_tile = [&] {  // by one thread of the role
+    mbar_arrive(heard + slot);
+  };
+  auto step_ring = [&] {
+    if (++slot == RING) {
+      slot = 0;
+      slot_parity ^= 1;
+    }
+  };
 
   if (w == 0) {
     // ------------------------------------------------------------- loads
@@ -215,14 +266,19 @@ __global__ void __launch_bounds__(MMA_THREADS, 1)
     // Both blocks' loads are counted by the first one's barriers.
     const uint32_t full_at = kCtas == 1 || rank == 0 ? smem_addr(full) : peer_addr(smem_addr(full), 0);
     bool ok = true;
-    for (int64_t t = t0; t < tiles.total && ok; t += dt) {
-      const Tile x = tiles.at(t);
-      const int32_t k_end = static_cast<int32_t>(x.k1);
-      const int32_t f0 = static_cast<int32_t>(x.f0) + static_cast<int32_t>(rank) * MMA_F;
+    while (ok) {
+      Tile x;
+      ok = __all_sync(0xffffffffu, next_tile(x));
+      if (!ok) break;
+      if (lane == 0) heard_tile();
+      step_ring();
+      if (x.e < 0) break;
+      const int32_t k_end = x.k1;
+      const int32_t f0 = x.f0 + static_cast<int32_t>(rank) * MMA_F;
       // Columns of this block: half of the instruction's.
-      const int32_t half = kWeights ? TC / kCtas : (static_cast<int32_t>(x.c1 - x.c0) + 15) / 16 * 16 / kCtas;
-      const int32_t c0 = static_cast<int32_t>(x.c0) + static_cast<int32_t>(rank) * half;
-      for (int32_t k = static_cast<int32_t>(x.k0); k < k_end; k += MMA_K) {
+      const int32_t half = kWeights ? TC / kCtas : (x.c1 - x.c0 + 15) / 16 * 16 / kCtas;
+      const int32_t c0 = x.c0 + static_cast<int32_t>(rank) * half;
+      for (int32_t k = x.k0; k < k_end; k += MMA_K) {
         const int32_t valid = k_end - k < MMA_K ? k_end - k : MMA_K;
         const bool last = kWeights && valid % 16 != 0;
         if (lane == 0) ok = wait_for(empty + s, parity, abort);
@@ -278,11 +334,16 @@ __global__ void __launch_bounds__(MMA_THREADS, 1)
       uint32_t s = 0, parity = 0, acc = 0, acc_parity = 1;
       const uint32_t a_at = operand<kASK>(smem_addr(stages), 8192), b_at = operand<kBSK>(smem_addr(stages) + S::A, 8192);
       bool ok = true;
-      for (int64_t t = t0; t < tiles.total && ok; t += dt) {
-        const Tile x = tiles.at(t);
+      while (ok) {
+        Tile x;
+        ok = next_tile(x);
+        if (!ok) break;
+        heard_tile();
+        step_ring();
+        if (x.e < 0) break;
         const uint32_t n = kWeights ? TC : (static_cast<uint32_t>(x.c1 - x.c0) + 15) / 16 * 16;
         const uint32_t desc = product_desc(kASK, kBSK, MMA_F * kCtas, n);
-        int32_t rest = static_cast<int32_t>(x.k1 - x.k0);
+        int32_t rest = x.k1 - x.k0;
         while (rest > 0 && ok) {
           ok = wait_for(taken + acc, acc_parity, abort);
           tmem_after_sync();
@@ -312,16 +373,64 @@ __global__ void __launch_bounds__(MMA_THREADS, 1)
         }
       }
     }
+  } else if (w == 2) {
+    // ------------------------------------------------------------- tiles
+    if (lane == 0) {
+      Tiles<kP, TC, kCtas> tiles(a, kWeights && a.experts > MMA_THREADS ? nullptr : first);
+      int64_t t = blockIdx.x / kCtas;
+      uint32_t empty_parity = 1, q = 0, q_parity = 0;
+      bool ok = true;
+      while (ok) {
+        // Ask for the tile after this one while this one is told.
+        bool more = t >= 0 && t < tiles.total;
+        if (kWeights && more) {
+          mbar_arrive_expect_tx(answered + q, 16);
+          if (rank == 0) {
+            ok = wait_for(asked + q, q_parity ^ 1, abort);  // both blocks have read what was there
+            if (!ok) break;
+            ask_cluster<kCtas>(answers + q, answered + q);
+          }
+        }
+        ok = wait_for(heard + slot, empty_parity, abort);
+        if (!ok) break;
+        Tile x;
+        x.e = -1;
+        if (more) x = tiles.at(t);
+        ring[slot] = x;
+        mbar_arrive(told + slot);
+        step_ring();
+        if (slot == 0) empty_parity ^= 1;
+        if (!more) break;
+        if constexpr (kWeights) {
+          ok = wait_for(answered + q, q_parity, abort);
+          if (!ok) break;
+          t = cluster_given(answers + q);
+          if (t >= 0) t /= kCtas;
+          fence_async_shared();
+          if (kCtas == 1) mbar_arrive(asked + q);
+          else remote_release(rank == 0 ? smem_addr(asked + q) : peer_addr(smem_addr(asked + q), 0));
+          q ^= 1;
+          if (q == 0) q_parity ^= 1;
+        } else {
+          t += gridDim.x / kCtas;
+        }
+      }
+    }
   } else if (w >= 4) {
     // ------------------------------------------------------------ results
     uint32_t acc = 0, parity = 0;
     bool ok = true;
     const uint32_t lanes = uint32_t(w - 4) << 21;  // (32 (w - 4)) << 16: this warp's lanes
-    for (int64_t t = t0; t < tiles.total && ok; t += dt) {
-      const Tile x = tiles.at(t);
-      const int64_t blocks = (x.k1 - x.k0 + MMA_K - 1) / MMA_K;
+    while (ok) {
+      Tile x;
+      ok = __all_sync(0xffffffffu, next_tile(x));
+      if (!ok) break;
+      if (lane == 0) heard_tile();
+      step_ring();
+      if (x.e < 0) break;
+      const int32_t blocks = (x.k1 - x.k0 + MMA_K - 1) / MMA_K;
       const int64_t f = x.f0 + int64_t(rank) * MMA_F + (w - 4) * 32 + lane;
-      const int n = static_cast<int>(x.c1 - x.c0);
+      const int n = x.c1 - x.c0;
       O* o = a.o + x.e * a.o_e + x.c0 * a.o_c + f;
       const bool on = f < a.f && GRS_CHECK(kWeights || (x.c0 >= 0 && x.c1 <= a.rows), mma_flags, SITE_MMA_ROW);
       if (blocks == 0) {  // a weights' gradient without rows
@@ -329,8 +438,8 @@ __global__ void __launch_bounds__(MMA_THREADS, 1)
           for (int j = 0; j < n; ++j) o[j * a.o_c] = from_float<O>(0.0f);
         continue;
       }
-      const int64_t sections = kSections ? (blocks + MMA_SECTION - 1) / MMA_SECTION : 1;
-      for (int64_t i = 0; i < sections && ok; ++i) {
+      const int32_t sections = kSections ? (blocks + MMA_SECTION - 1) / MMA_SECTION : 1;
+      for (int32_t i = 0; i < sections && ok; ++i) {
         ok = __all_sync(0xffffffffu, wait_for(done + acc, parity, abort));
         if (!ok) break;
         tmem_after_sync();
@@ -439,7 +548,9 @@ cudaError_t mma_launch(const grs_experts* s, const ExpLd& ld, const void* xs, co
   }
   if (!fine) return cudaErrorInvalidValue;
   tiles *= (a.f + MMA_F * kCtas - 1) / (MMA_F * kCtas);
-  const int64_t at_once = 152 / kCtas;
+  // Weights: a cluster for each tile, of which those that run take over the others' (ask_cluster).
+  const int64_t at_once = kP == Product::kWeights ? INT32_MAX / kCtas : 152 / kCtas;
+  if (kP == Product::kWeights && tiles > at_once) return cudaErrorInvalidConfiguration;
   const unsigned grid = static_cast<unsigned>((tiles < at_once ? tiles : at_once) * kCtas);
   const cudaError_t e = allow_smem<exp_mma_kernel<kP, TC, kCtas, O>>(S::BYTES);
   if (e != cudaSuccess) return e;

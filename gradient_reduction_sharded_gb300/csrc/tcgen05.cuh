@@ -50,6 +50,37 @@ __device__ __forceinline__ void remote_arrive_expect_tx(uint32_t bar, uint32_t b
 // Writes of this thread to shared memory, visible to TMA and matrix instructions.
 __device__ __forceinline__ void fence_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
+// ------------------------------------------------- blocks not yet launched
+// Asks for the place of a cluster of this grid that has not begun, which then
+// never will; the answer (16 bytes, aligned) comes to every block of the
+// cluster and is counted by its barrier.  Not to be asked again after a no.
+template <int kCtas>
+__device__ __forceinline__ void ask_cluster(void* answer, uint64_t* bar) {
+  if constexpr (kCtas == 1)
+    asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(smem_addr(answer)),
+                 "r"(smem_addr(bar))
+                 : "memory");
+  else
+    asm volatile(
+        "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.multicast::cluster::all.b128 [%0], [%1];" ::"r"(
+            smem_addr(answer)),
+        "r"(smem_addr(bar))
+        : "memory");
+}
+// The first block of the cluster that the answer gives, -1 for none.
+__device__ __forceinline__ int64_t cluster_given(const void* answer) {
+  uint32_t yes, x;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b128 r;\n\tld.shared.b128 r, [%2];\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\tmov.u32 %1, 0;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%1, _, _, _}, r;\n\t}"
+      : "=r"(yes), "=r"(x)
+      : "r"(smem_addr(answer))
+      : "memory");
+  return yes ? int64_t(x) : -1;
+}
+
 // ------------------------------------------------------------- tiled TMA
 __device__ __forceinline__ void prefetch_map(const CUtensorMap* m) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(m) : "memory");

@@ -27,7 +27,7 @@
 //
 // fp32 gradients: the tensor cores add with rounding towards zero (a library
 // product of 4096 rows is 4e-6 off, with a bias), so sections of 512 rows are
-// added up by ordinary fp32 additions, in tensor memory.
+// added up by ordinary fp32 additions, in the storing warps' registers.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -43,7 +43,8 @@
 namespace grs {
 namespace {
 
-constexpr int MMA_THREADS = 256;
+constexpr int MMA_STORING = 8;       // storing warps, two for each quarter of the lanes
+constexpr int MMA_THREADS = 128 + 32 * MMA_STORING;
 constexpr int MMA_K = 64;            // of k a stage: a swizzled row of bf16
 constexpr int MMA_F = 128;           // features of a block
 constexpr int MMA_SECTION = 8;       // stages that fp32 gradients add up in the tensor cores
@@ -72,6 +73,7 @@ struct MmaArgs {
   int64_t o_c, o_e;        // elements from one c, one expert to the next
   int64_t f, c, k;         // extents; an expert's rows in the place of c or k
   int32_t rows, experts;
+  int32_t words;           // two features' bf16 lie in an aligned word
 };
 
 struct Tile {
@@ -140,11 +142,11 @@ __device__ __forceinline__ void by_size(const int32_t* offsets, int32_t experts,
   }
 }
 
-// Tiles of c before each expert's, by a block of 256.
+// Tiles of c before each expert's, by a block.
 template <int TC>
 __device__ __forceinline__ void tile_prefix(const int32_t* offsets, int32_t experts, int32_t rows, int32_t* first) {
   __shared__ int32_t sums[MMA_THREADS / 32];
-  constexpr int EACH = GRS_MOE_MAX_EXPERTS / MMA_THREADS;
+  constexpr int EACH = (GRS_MOE_MAX_EXPERTS + MMA_THREADS - 1) / MMA_THREADS;
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   int32_t n[EACH], all = 0;
 #pragma unroll
@@ -182,13 +184,43 @@ __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, volatil
   return mbar_wait_bounded(bar, parity, mma_flags, abort);
 }
 
+// 32 columns, a lane a feature, to rows `ld` elements apart, the first n of
+// them; `rest`: features from this lane's on (<= 0: none).  Where words are
+// aligned two lanes store their two bf16 as one, for every second row each.
+template <typename O>
+__device__ __forceinline__ void store_columns(O* o, int64_t ld, const uint32_t (&v)[32], int n, int64_t rest, bool words) {
+  if constexpr (sizeof(O) == 2) {
+    if (words) {
+      const int odd = threadIdx.x & 1;
+      const int64_t have = rest + odd;  // from the even lane's on
+      O* p = o - odd + odd * ld;
+#pragma unroll
+      for (int j = 0; j < 32; j += 2) {
+        const uint32_t mine = to_bf16_pair(make_float2(__uint_as_float(v[j]), __uint_as_float(v[j + 1])));
+        const uint32_t other = __shfl_xor_sync(0xffffffffu, mine, 1), both = __byte_perm(mine, other, odd ? 0x3276 : 0x5410);
+        if (j + odd < n) {
+          if (have >= 2) *reinterpret_cast<uint32_t*>(p) = both;
+          else if (have == 1) *p = static_cast<O>(both);
+        }
+        p += 2 * ld;
+      }
+      return;
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < 32; ++j) {
+    if (rest > 0 && j < n) *o = from_float<O>(__uint_as_float(v[j]));
+    o += ld;
+  }
+}
+
 template <Product kP, int TC, int kCtas, typename O>
 __global__ void __launch_bounds__(MMA_THREADS, 1)
     exp_mma_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b, const __grid_constant__ MmaArgs<O> a) {
   using S = Shape<TC, kCtas>;
   constexpr bool kWeights = kP == Product::kWeights, kASK = kP == Product::kForward, kBSK = !kWeights;  // operands along k
   constexpr bool kSections = kWeights && sizeof(O) == 4;
-  constexpr uint32_t COLUMNS = kSections ? 3 * TC : 2 * TC;  // accumulators, the sections' sum
+  constexpr uint32_t COLUMNS = 2 * TC;  // two accumulators
   constexpr uint32_t TMEM = COLUMNS <= 32 ? 32 : COLUMNS <= 64 ? 64 : COLUMNS <= 128 ? 128 : COLUMNS <= 256 ? 256 : 512;
   static_assert(COLUMNS <= 512, "tensor memory has 512 columns");
   static_assert(!kWeights || TC / kCtas % 64 == 0, "operands across k come in 64s");
@@ -214,12 +246,12 @@ __global__ void __launch_bounds__(MMA_THREADS, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(done + i, 1);
-      mbar_init(taken + i, 4 * kCtas);
+      mbar_init(taken + i, MMA_STORING * kCtas);
     }
     mbar_init(tail, 1);
     for (int i = 0; i < RING; ++i) {
       mbar_init(told + i, 1);
-      mbar_init(heard + i, rank == 0 ? 6 : 5);  // the loading warp, four storing ones, the issuing thread
+      mbar_init(heard + i, MMA_STORING + (rank == 0 ? 2 : 1));  // the storing warps, the loading one, the issuing thread
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(answered + i, 1);
@@ -420,7 +452,9 @@ __global__ void __launch_bounds__(MMA_THREADS, 1)
     // ------------------------------------------------------------ results
     uint32_t acc = 0, parity = 0;
     bool ok = true;
-    const uint32_t lanes = uint32_t(w - 4) << 21;  // (32 (w - 4)) << 16: this warp's lanes
+    const int quarter = w & 3, half = (w - 4) >> 2;  // 32 lanes; every second 32 columns
+    const uint32_t from = tmem + (uint32_t(quarter) << 21) + 32 * half;
+    const bool words = sizeof(O) == 4 || a.words != 0;
     while (ok) {
       Tile x;
       ok = __all_sync(0xffffffffu, next_tile(x));
@@ -429,44 +463,42 @@ __global__ void __launch_bounds__(MMA_THREADS, 1)
       step_ring();
       if (x.e < 0) break;
       const int32_t blocks = (x.k1 - x.k0 + MMA_K - 1) / MMA_K;
-      const int64_t f = x.f0 + int64_t(rank) * MMA_F + (w - 4) * 32 + lane;
+      const int64_t f = x.f0 + int64_t(rank) * MMA_F + quarter * 32 + lane;
       const int n = x.c1 - x.c0;
-      O* o = a.o + x.e * a.o_e + x.c0 * a.o_c + f;
-      const bool on = f < a.f && GRS_CHECK(kWeights || (x.c0 >= 0 && x.c1 <= a.rows), mma_flags, SITE_MMA_ROW);
-      if (blocks == 0) {  // a weights' gradient without rows
-        if (on)
-          for (int j = 0; j < n; ++j) o[j * a.o_c] = from_float<O>(0.0f);
-        continue;
-      }
+      O* o = a.o + x.e * a.o_e + int64_t(x.c0) * a.o_c + f;
+      // (an even number of features less when a check fails: none, and the same parity)
+      const int64_t rest = GRS_CHECK(kWeights || (x.c0 >= 0 && x.c1 <= a.rows), mma_flags, SITE_MMA_ROW) ? a.f - f : -2;
+      const bool on = rest > 0;
       const int32_t sections = kSections ? (blocks + MMA_SECTION - 1) / MMA_SECTION : 1;
-      for (int32_t i = 0; i < sections && ok; ++i) {
+      // fp32: the thread's columns are added up in its registers, section by section.
+      constexpr int PARTS = kSections ? TC / 64 : 1;
+      float sum[PARTS][32];
+      if constexpr (kSections) {
+#pragma unroll
+        for (int p = 0; p < PARTS; ++p)
+#pragma unroll
+          for (int j = 0; j < 32; ++j) sum[p][j] = 0.0f;
+      }
+      for (int32_t i = 0; i < sections && blocks > 0; ++i) {
         ok = __all_sync(0xffffffffu, wait_for(done + acc, parity, abort));
         if (!ok) break;
         tmem_after_sync();
-        for (int j0 = 0; j0 < n; j0 += 32) {
-          uint32_t v[32];
-          tmem_load32(tmem + lanes + acc * TC + j0, v);
-          if (kSections && i > 0) {
-            uint32_t sum[32];
-            tmem_load32(tmem + lanes + 2 * TC + j0, sum);
+        if constexpr (kSections) {
+#pragma unroll
+          for (int p = 0; p < 2 * PARTS; ++p) {
+            uint32_t v[16];
+            tmem_load16(from + acc * TC + p / 2 * 64 + p % 2 * 16, v);
             tmem_wait_load();
 #pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(__fadd_rn(__uint_as_float(v[j]), __uint_as_float(sum[j])));
-          } else {
+            for (int j = 0; j < 16; ++j) sum[p / 2][p % 2 * 16 + j] = __fadd_rn(sum[p / 2][p % 2 * 16 + j], __uint_as_float(v[j]));
+          }
+        } else {
+          for (int j0 = 32 * half; j0 < n; j0 += 64) {
+            uint32_t v[32];
+            tmem_load32(from + acc * TC + j0 - 32 * half, v);
             tmem_wait_load();
+            store_columns(o + j0 * a.o_c, a.o_c, v, n - j0, rest, words);
           }
-          if (kSections && i < sections - 1) {
-            tmem_store32(tmem + lanes + 2 * TC + j0, v);
-            tmem_wait_store();
-          } else if (on) {
-            O* p = o + j0 * a.o_c;
-#pragma unroll
-            for (int j = 0; j < 32; ++j) {
-              if (j0 + j < n) *p = from_float<O>(__uint_as_float(v[j]));
-              p += a.o_c;
-            }
-          }
-          __syncwarp();
         }
         tmem_before_sync();
         __syncwarp();
@@ -476,6 +508,23 @@ __global__ void __launch_bounds__(MMA_THREADS, 1)
         }
         acc ^= 1;
         if (acc == 0) parity ^= 1;
+      }
+      if (!ok) break;
+      if constexpr (kSections) {
+#pragma unroll
+        for (int p = 0; p < PARTS; ++p) {
+          const int j0 = 64 * p + 32 * half;
+          O* q = o + j0 * a.o_c;
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            if (on && j0 + j < n) *q = from_float<O>(sum[p][j]);
+            q += a.o_c;
+          }
+        }
+      } else if (kWeights && blocks == 0) {  // an expert without rows
+        if (on)
+          for (int j = half; j < n; j += 2) o[j * a.o_c] = from_float<O>(0.0f);
+        __syncwarp();
       }
     }
   }
@@ -547,6 +596,7 @@ cudaError_t mma_launch(const grs_experts* s, const ExpLd& ld, const void* xs, co
     tiles = s->rows / TC + (s->rows < s->experts ? s->rows : s->experts);
   }
   if (!fine) return cudaErrorInvalidValue;
+  a.words = api_aligned(o, 4) && o_ld % 2 == 0 && a.o_e % 2 == 0;
   tiles *= (a.f + MMA_F * kCtas - 1) / (MMA_F * kCtas);
   // Weights: a cluster for each tile, of which those that run take over the others' (ask_cluster).
   const int64_t at_once = kP == Product::kWeights ? INT32_MAX / kCtas : 152 / kCtas;
@@ -574,7 +624,7 @@ cudaError_t experts_mma(Product p, const grs_experts* s, const ExpLd& ld, const 
                         const int32_t* offsets, void* o, int64_t o_ld, void* stream) {
   if (p == Product::kForward) return mma_rows<Product::kForward>(s, ld, xs, w, dys, offsets, o, o_ld, stream);
   if (p == Product::kRows) return mma_rows<Product::kRows>(s, ld, xs, w, dys, offsets, o, o_ld, stream);
-  if (s->grad_dtype == GRS_DTYPE_FP32) return mma_launch<Product::kWeights, 128, 2, float>(s, ld, xs, w, dys, offsets, o, o_ld, stream);
+  if (s->grad_dtype == GRS_DTYPE_FP32) return mma_launch<Product::kWeights, 256, 2, float>(s, ld, xs, w, dys, offsets, o, o_ld, stream);
   return mma_launch<Product::kWeights, 256, 2, uint16_t>(s, ld, xs, w, dys, offsets, o, o_ld, stream);
 }
 

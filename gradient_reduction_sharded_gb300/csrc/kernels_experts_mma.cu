@@ -22,8 +22,8 @@
 // Ragged ends: rows of forward and rows' gradients are columns of their own, so
 // what is loaded of another expert's rows is not stored, and k is cut off by the
 // tensor map, which fills with zeros.  In the weights' gradient k runs over the
-// expert's rows: there the loading warp sets to zero what the last 16 rows hold
-// beyond the expert's end, in both operands (NaN times zero is NaN).
+// expert's rows: there a warp sets to zero what the last 16 rows hold beyond the
+// expert's end, in both operands (NaN times zero is NaN).
 //
 // fp32 gradients: the tensor cores add with rounding towards zero (a library
 // product of 4096 rows is 4e-6 off, with a bias), so sections of 512 rows are
@@ -57,7 +57,7 @@ __device__ int mma_flags[FLAG_COUNT];
 template <int TC, int kCtas>
 struct Shape {
   static constexpr int A = MMA_F * MMA_K * 2, B = TC / kCtas * MMA_K * 2, STAGE = A + B;
-  static constexpr int FIXED = 1024 + (GRS_MOE_MAX_EXPERTS + 2) * 4 + 640;  // alignment, tiles before each expert, barriers
+  static constexpr int FIXED = 1024 + (GRS_MOE_MAX_EXPERTS + 2) * 4 + 768;  // alignment, tiles before each expert, barriers
   static constexpr int FIT = (MMA_SMEM - FIXED) / STAGE;
 #ifndef MAX_STAGES
 #define MAX_STAGES 10
@@ -228,8 +228,8 @@ __global__ void __launch_bounds__(MMA_THREADS, 1)
   uint8_t* stages = smem + (1024 - (smem_addr(smem) & 1023)) % 1024;
   int32_t* first = reinterpret_cast<int32_t*>(stages + S::STAGES * S::STAGE);
   uint64_t* full = reinterpret_cast<uint64_t*>(first + ((GRS_MOE_MAX_EXPERTS + 1 + 1) & ~1));
-  uint64_t *empty = full + S::STAGES, *done = empty + S::STAGES, *taken = done + 2, *tail = taken + 2;
-  uint64_t *told = tail + 1, *heard = told + RING, *answered = heard + RING, *asked = answered + 2;
+  uint64_t *empty = full + S::STAGES, *tail = empty + S::STAGES, *done = tail + S::STAGES, *taken = done + 2;
+  uint64_t *told = taken + 2, *heard = told + RING, *answered = heard + RING, *asked = answered + 2;
   uint4* answers = reinterpret_cast<uint4*>((reinterpret_cast<uintptr_t>(asked + 2) + 15) & ~uintptr_t(15));
   Tile* ring = reinterpret_cast<Tile*>(answers + 2);
   uint32_t* tmem_at = reinterpret_cast<uint32_t*>(ring + RING);
@@ -243,15 +243,15 @@ __global__ void __launch_bounds__(MMA_THREADS, 1)
     for (int s = 0; s < S::STAGES; ++s) {
       mbar_init(full + s, kCtas);
       mbar_init(empty + s, 1);
+      mbar_init(tail + s, 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(done + i, 1);
       mbar_init(taken + i, MMA_STORING * kCtas);
     }
-    mbar_init(tail, 1);
     for (int i = 0; i < RING; ++i) {
       mbar_init(told + i, 1);
-      mbar_init(heard + i, MMA_STORING + (rank == 0 ? 2 : 1));  // the storing warps, the loading one, the issuing thread
+      mbar_init(heard + i, MMA_STORING + 1 + (rank == 0) + kWeights);  // storing warps, the loading one, the issuing thread, the clearing warp
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(answered + i, 1);
@@ -293,7 +293,7 @@ __global__ void __launch_bounds__(MMA_THREADS, 1)
 
   if (w == 0) {
     // ------------------------------------------------------------- loads
-    uint32_t s = 0, parity = 1, tail_parity = 0;
+    uint32_t s = 0, parity = 1;
     const uint32_t stages_at = smem_addr(stages);
     // Both blocks' loads are counted by the first one's barriers.
     const uint32_t full_at = kCtas == 1 || rank == 0 ? smem_addr(full) : peer_addr(smem_addr(full), 0);
@@ -313,13 +313,12 @@ __global__ void __launch_bounds__(MMA_THREADS, 1)
       for (int32_t k = x.k0; k < k_end; k += MMA_K) {
         const int32_t valid = k_end - k < MMA_K ? k_end - k : MMA_K;
         const bool last = kWeights && valid % 16 != 0;
-        if (lane == 0) ok = wait_for(empty + s, parity, abort);
-        if (kWeights) ok = __shfl_sync(0xffffffffu, ok, 0);
-        if (!ok) break;
-        const uint32_t to = stages_at + s * S::STAGE, bar = full_at + s * 8;
         if (lane == 0) {
-          const uint32_t on = last ? smem_addr(tail) : bar;
-          if (last) mbar_arrive_expect_tx(tail, S::STAGE);
+          ok = wait_for(empty + s, parity, abort);
+          if (!ok) break;
+          const uint32_t to = stages_at + s * S::STAGE, bar = full_at + s * 8;
+          const uint32_t on = last ? smem_addr(tail + s) : bar;
+          if (last) mbar_arrive_expect_tx(tail + s, S::STAGE);
           else if (kCtas == 1) mbar_arrive_expect_tx(full + s, S::STAGE);
           else remote_arrive_expect_tx(bar, S::STAGE);
           if constexpr (kP == Product::kForward) {
@@ -338,27 +337,12 @@ __global__ void __launch_bounds__(MMA_THREADS, 1)
             for (int i = 0; i < TC / kCtas / 64; ++i) tma_load<kCtas>(to + S::A + i * 8192, &map_b, c0 + i * 64, k, on);
           }
         }
-        if (last) {
-          ok = __all_sync(0xffffffffu, wait_for(tail, tail_parity, abort));
-          if (!ok) break;
-          tail_parity ^= 1;
-          const int32_t bad = (16 - valid % 16) * 8;  // 16-byte chunks of the rows to clear, in each 64 of f or c
-          uint8_t* stage = stages + s * S::STAGE;
-          for (int32_t i = lane; i < bad * (S::STAGE / 8192); i += 32)
-            *reinterpret_cast<uint4*>(stage + i / bad * 8192 + valid * 128 + i % bad * 16) = make_uint4(0, 0, 0, 0);
-          fence_async_shared();
-          __syncwarp();
-          if (lane == 0) {
-            if (kCtas == 1) mbar_arrive(full + s);
-            else remote_release(bar);
-          }
-        }
         if (++s == S::STAGES) {
           s = 0;
           parity ^= 1;
         }
       }
-      if (!kWeights) ok = __shfl_sync(0xffffffffu, ok, 0);
+      ok = __shfl_sync(0xffffffffu, ok, 0);
     }
   } else if (w == 1) {
     // ---------------------------------------------------------- products
@@ -446,6 +430,37 @@ __global__ void __launch_bounds__(MMA_THREADS, 1)
         } else {
           t += gridDim.x / kCtas;
         }
+      }
+    }
+  } else if (w == 3 && kWeights) {
+    // ------------------------------------------------------- ragged ends
+    // What the last 16 rows of an expert hold of others', once it is there: cleared, then counted as loaded.
+    const uint32_t full_at = kCtas == 1 || rank == 0 ? smem_addr(full) : peer_addr(smem_addr(full), 0);
+    uint32_t s = 0, parities = 0;  // the stage of the tile's first block; a bit for each stage's `tail`
+    bool ok = true;
+    while (ok) {
+      Tile x;
+      ok = __all_sync(0xffffffffu, next_tile(x));
+      if (!ok) break;
+      if (lane == 0) heard_tile();
+      step_ring();
+      if (x.e < 0) break;
+      const int32_t n = x.k1 - x.k0, blocks = (n + MMA_K - 1) / MMA_K, valid = n % MMA_K;
+      const uint32_t last = (s + blocks + S::STAGES - 1) % S::STAGES;
+      s = (s + blocks) % S::STAGES;
+      if (valid % 16 == 0) continue;
+      ok = __all_sync(0xffffffffu, wait_for(tail + last, parities >> last & 1, abort));
+      if (!ok) break;
+      parities ^= 1u << last;
+      const int32_t bad = (16 - valid % 16) * 8;  // 16-byte chunks to clear, in each 64 of f or c
+      uint8_t* stage = stages + last * S::STAGE;
+      for (int32_t i = lane; i < bad * (S::STAGE / 8192); i += 32)
+        *reinterpret_cast<uint4*>(stage + i / bad * 8192 + valid * 128 + i % bad * 16) = make_uint4(0, 0, 0, 0);
+      fence_async_shared();
+      __syncwarp();
+      if (lane == 0) {
+        if (kCtas == 1) mbar_arrive(full + last);
+        else remote_release(full_at + last * 8);
       }
     }
   } else if (w >= 4) {

@@ -9,7 +9,7 @@
 
 #include "api_util.h"
 #include "device.cuh"
-#include "experts.h"
+#include "experts.cuh"
 #include "internal.h"
 #include "launch.cuh"
 #include "operators.cuh"
@@ -22,114 +22,224 @@ enum : int { SITE_EXP_ROW = 1 };
 
 __device__ int exp_flags[FLAG_COUNT];
 
-// An expert's rows, as the caller's offsets say within [0, rows].
-struct Span2 {
-  int32_t from, to;
-};
-__device__ __forceinline__ Span2 expert_rows(const int32_t* offsets, int e, int32_t rows) {
-  int32_t a = __ldg(offsets + e), b = __ldg(offsets + e + 1);
-  a = a < 0 ? 0 : a > rows ? rows : a;
-  b = b < a ? a : b > rows ? rows : b;
-  return {a, b};
-}
+// --------------------------------------------------------- fp32, any size
+// A block has 128 features of 64 c, a thread eight by four, as pairs of
+// neighbouring features; the next 16 of k are on their way while these are
+// multiplied.
+constexpr int GF = 128, GC = 64, GK = 16;
 
-// ------------------------------------------------------- any size and type
-constexpr int GT = 64, GK = 16;  // tile of the result, elements of a step
-
-template <typename T, typename O>
+template <typename O>
 struct GeneralArgs {
-  const T *a, *b;
+  const float *a, *b;
   O* o;
   const int32_t* offsets;
   int64_t a_f, a_k, a_e;  // distances in A of features, of k, of experts
-  int64_t b_c, b_k, b_e;
+  int64_t b_c, b_k;
   int64_t o_c, o_e;
   int64_t f, c, k;        // extents; c or k of an expert's own are its rows
   int32_t rows, experts;
 };
 
+// One operand's next GK x N elements: where a thread's lie, on their way, and
+// into shared memory as [k][N].  Neighbouring threads along what lies next to
+// one another.
+template <int N>
+struct Panel {
+  static constexpr int EACH = N * GK / EXP_THREADS;
+  const float* p;      // the thread's first element of the next step
+  int64_t next;        // elements to its next one
+  int64_t step;        // to the next step's
+  int32_t k, dk;       // of its first element, of its next ones
+  uint32_t on;         // which of its elements exist along N
+  int32_t at, dat;     // in shared memory
+  float v[EACH];
+  __device__ __forceinline__ Panel(const float* base, int64_t n0, int64_t n1, int64_t k0, int64_t ld_n, int64_t ld_k) {
+    const bool along_k = ld_k == 1;
+    constexpr int PER_K = EXP_THREADS / GK, PER_N = EXP_THREADS / N;  // between a thread's elements: in N, in k
+    const int tk = along_k ? threadIdx.x % GK : threadIdx.x / N, tn = along_k ? threadIdx.x / GK : threadIdx.x % N;
+    const int dn = along_k ? PER_K : 0;
+    p = base + (n0 + tn) * ld_n + (k0 + tk) * ld_k;
+    k = tk;
+    dk = along_k ? 0 : PER_N;
+    next = along_k ? PER_K * ld_n : PER_N * ld_k;
+    step = GK * ld_k;
+    at = tk * (N + 4) + tn;
+    dat = along_k ? PER_K : PER_N * (N + 4);
+    on = 0;
+#pragma unroll
+    for (int j = 0; j < EACH; ++j) on |= uint32_t(n0 + tn + j * dn < n1) << j;
+  }
+  // The step whose first k has `rest` left.
+  __device__ __forceinline__ void load(int64_t rest) {
+    const float* q = p;
+#pragma unroll
+    for (int j = 0; j < EACH; ++j) {
+      v[j] = (on >> j & 1) != 0 && k + j * dk < rest ? __ldg(q) : 0.0f;
+      q += next;
+    }
+    p += step;
+  }
+  __device__ __forceinline__ void store(float* s) const {
+#pragma unroll
+    for (int j = 0; j < EACH; ++j) s[at + j * dat] = v[j];
+  }
+};
+
 // Sums of 64 products are added up to the result's: shorter chains, errors
 // that grow with 64 + k / 64 additions instead of k.
-template <Product kP, typename T, typename O>
-__global__ void __launch_bounds__(EXP_THREADS) exp_general_kernel(const __grid_constant__ GeneralArgs<T, O> p) {
-  __shared__ float as[GK][GT + 4], bs[GK][GT + 4];
-  __shared__ int32_t first[GRS_MOE_MAX_EXPERTS + 1];  // tiles of c before each expert's
+template <Product kP, typename O>
+__global__ void __launch_bounds__(EXP_THREADS, 2) exp_general_kernel(const __grid_constant__ GeneralArgs<O> p) {
+  constexpr bool kWeights = kP == Product::kWeights;
+  __shared__ __align__(16) float as[2][GK][GF + 4], bs[2][GK][GC + 4];
+  __shared__ int32_t first[GRS_MOE_MAX_EXPERTS + 1];
   pdl_wait();
   pdl_trigger();
-  if (threadIdx.x == 0) {
-    int32_t n = 0;
-    for (int e = 0; e < p.experts; ++e) {
-      first[e] = n;
-      const Span2 r = expert_rows(p.offsets, e, p.rows);
-      n += kP == Product::kWeights ? static_cast<int32_t>((p.c + GT - 1) / GT) : (r.to - r.from + GT - 1) / GT;
-    }
-    first[p.experts] = n;
+  if constexpr (!kWeights) {
+    group_prefix<GC, EXP_THREADS>(p.offsets, p.experts, p.rows, first);
+    __syncthreads();
   }
-  __syncthreads();
-  const int64_t ft = (p.f + GT - 1) / GT, tiles = ft * first[p.experts];
-  const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;  // 4 features and 4 c of a thread
+  const int64_t ft = (p.f + GF - 1) / GF, ct = (p.c + GC - 1) / GC;
+  const int64_t tiles = ft * (kWeights ? ct * p.experts : first[p.experts]);
+  const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;  // features 4 tx.. and 64 + 4 tx.., c 4 ty..
   for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
-    const int32_t ct = static_cast<int32_t>(tile / ft);
-    const int64_t f0 = (tile - ct * ft) * GT;
-    int lo = 0, hi = p.experts;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) / 2;
-      if (first[mid] <= ct) lo = mid;
-      else hi = mid;
-    }
-    while (first[lo + 1] <= ct) ++lo;
-    const Span2 r = expert_rows(p.offsets, lo, p.rows);
-    int64_t c0 = int64_t(ct - first[lo]) * GT, c1 = p.c, k0 = 0, k1 = p.k;
-    if (kP == Product::kWeights) {
-      k0 = r.from;
-      k1 = r.to;
-    } else {
-      c0 += r.from;
-      c1 = r.to;
-    }
-    const T *a = p.a + lo * p.a_e, *b = p.b + lo * p.b_e;
-    float total[4][4] = {}, part[4][4] = {};
-    int steps = 0;
-    for (int64_t k = k0; k < k1; k += GK) {
-      for (int i = threadIdx.x; i < GT * GK; i += EXP_THREADS) {
-        // Neighbouring threads along what lies next to one another.
-        const int fa = p.a_k == 1 ? i / GK : i % GT, ka = p.a_k == 1 ? i % GK : i / GT;
-        as[ka][fa] = f0 + fa < p.f && k + ka < k1 ? to_float(a[(f0 + fa) * p.a_f + (k + ka) * p.a_k]) : 0.0f;
-        const int cb = p.b_k == 1 ? i / GK : i % GT, kb = p.b_k == 1 ? i % GK : i / GT;
-        bs[kb][cb] = c0 + cb < c1 && k + kb < k1 ? to_float(b[(c0 + cb) * p.b_c + (k + kb) * p.b_k]) : 0.0f;
+    const int64_t ci = tile / ft, f0 = (tile - ci * ft) * GF;
+    const int e = kWeights ? static_cast<int>(ci / ct) : expert_of(first, p.experts, ci);
+    const ExpertRows r(p.offsets, e, p.rows);
+    const int64_t c0 = kWeights ? (ci - e * ct) * GC : r.from + (ci - first[e]) * GC, c1 = kWeights ? p.c : r.to;
+    const int64_t k0 = kWeights ? r.from : 0, k1 = kWeights ? r.to : p.k;
+    const float *a = p.a + e * p.a_e, *b = p.b;
+    float2 total[4][4], part[4][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) total[i][j] = part[i][j] = both(0.0f);
+    Panel<GF> pa(a, f0, p.f, k0, p.a_f, p.a_k);
+    Panel<GC> pb(b, c0, c1, k0, p.b_c, p.b_k);
+    pa.load(k1 - k0);
+    pb.load(k1 - k0);
+    int step = 0;
+    for (int64_t k = k0; k < k1; k += GK, ++step) {
+      float(&sa)[GK][GF + 4] = as[step & 1];
+      float(&sb)[GK][GC + 4] = bs[step & 1];
+      pa.store(&sa[0][0]);
+      pb.store(&sb[0][0]);
+      __syncthreads();  // (the other half: all are done with it before they come here again)
+      if (k + GK < k1) {
+        pa.load(k1 - k - GK);
+        pb.load(k1 - k - GK);
       }
-      __syncthreads();
 #pragma unroll
       for (int q = 0; q < GK; ++q) {
-        float u[4], v[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          u[i] = as[q][tx * 4 + i];
-          v[i] = bs[q][ty * 4 + i];
-        }
+        const float4 u = *reinterpret_cast<const float4*>(&sa[q][4 * tx]), v = *reinterpret_cast<const float4*>(&sa[q][64 + 4 * tx]);
+        const float4 c = *reinterpret_cast<const float4*>(&sb[q][4 * ty]);
+        const float2 x[4] = {make_float2(u.x, u.y), make_float2(u.z, u.w), make_float2(v.x, v.y), make_float2(v.z, v.w)};
+        const float y[4] = {c.x, c.y, c.z, c.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) part[i][j] = __fmaf_rn(v[i], u[j], part[i][j]);
+          for (int j = 0; j < 4; ++j) part[i][j] = fma2(x[j], both(y[i]), part[i][j]);
       }
-      if (++steps % 4 == 0)
+      if (step % 4 == 3)
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            total[i][j] += part[i][j];
-            part[i][j] = 0.0f;
+            total[i][j] = add2(total[i][j], part[i][j]);
+            part[i][j] = both(0.0f);
           }
-      __syncthreads();
     }
+    __syncthreads();  // the panels may still be read
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < 4; ++i) {
+      const int64_t c = c0 + ty * 4 + i;
+      if (c >= c1 || !GRS_CHECK(kWeights || c < p.rows, exp_flags, SITE_EXP_ROW)) continue;
+      O* o = p.o + e * p.o_e + c * p.o_c;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const int64_t c = c0 + ty * 4 + i, f = f0 + tx * 4 + j;
-        if (c < c1 && f < p.f && GRS_CHECK(kP == Product::kWeights || c < p.rows, exp_flags, SITE_EXP_ROW))
-          p.o[lo * p.o_e + c * p.o_c + f] = from_float<O>(total[i][j] + part[i][j]);
+        const float2 v = add2(total[i][j], part[i][j]);
+        const int64_t f = f0 + (j < 2 ? 4 * tx + 2 * j : 64 + 4 * tx + 2 * (j - 2));
+        if (f < p.f) o[f] = from_float<O>(v.x);
+        if (f + 1 < p.f) o[f + 1] = from_float<O>(v.y);
       }
+    }
+  }
+}
+
+// ------------------------------------------------------------ bf16, few rows
+// Forward of a token or two is a matter of reading the weights, and the tensor
+// cores' tiles of 128 features are too few for the SMs.  A warp has two
+// features and a group of up to four rows, its lanes the same 8 of k of all,
+// products in fp32.
+constexpr int FEW = 4;        // rows of a group
+constexpr int FEW_AHEAD = 4;  // loads of each feature on their way
+constexpr int FEW_ROWS = 8;   // 2048 -> 768, 32 experts: 4 rows 6.2 us and 11.7 on the tensor cores, 8 rows 7.8 and 11.5, 20 rows 14.4 and 11.8
+
+struct FewArgs {
+  const uint16_t *x, *w;
+  uint16_t* y;
+  const int32_t* offsets;
+  int64_t ld_x, ld_y;
+  int32_t rows, experts, in, out;
+};
+
+__global__ void __launch_bounds__(EXP_THREADS) exp_few_kernel(const __grid_constant__ FewArgs a) {
+  __shared__ int32_t first[GRS_MOE_MAX_EXPERTS + 1];
+  pdl_wait();
+  pdl_trigger();
+  group_prefix<FEW, EXP_THREADS>(a.offsets, a.experts, a.rows, first);
+  __syncthreads();
+  const int lane = threadIdx.x & 31;
+  const int64_t pairs = (int64_t(a.out) + 1) / 2, items = pairs * first[a.experts], warps = int64_t(gridDim.x) * (EXP_THREADS / 32);
+  for (int64_t it = int64_t(threadIdx.x >> 5) * gridDim.x + blockIdx.x; it < items; it += warps) {
+    const int64_t g = it / pairs;
+    const int32_t f = static_cast<int32_t>(it - g * pairs) * 2;
+    const int e = expert_of(first, a.experts, g);
+    const ExpertRows r(a.offsets, e, a.rows);
+    const int32_t row = r.from + static_cast<int32_t>(g - first[e]) * FEW, n = r.to - row < FEW ? r.to - row : FEW;
+    const uint16_t *w0 = a.w + (int64_t(e) * a.out + f) * a.in, *w1 = f + 1 < a.out ? w0 + a.in : w0, *x = a.x + row * a.ld_x;
+    float2 sum[FEW][2];
+#pragma unroll
+    for (int i = 0; i < FEW; ++i) sum[i][0] = sum[i][1] = both(0.0f);
+    for (int32_t k0 = lane * 8; k0 < a.in; k0 += 256 * FEW_AHEAD) {
+      uint4 u[FEW_AHEAD], v[FEW_AHEAD];
+#pragma unroll
+      for (int j = 0; j < FEW_AHEAD; ++j) {
+        const int32_t k = k0 + 256 * j;
+        u[j] = v[j] = make_uint4(0, 0, 0, 0);
+        if (k < a.in) {
+          u[j] = __ldcs(reinterpret_cast<const uint4*>(w0 + k));
+          v[j] = __ldcs(reinterpret_cast<const uint4*>(w1 + k));
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < FEW_AHEAD; ++j) {
+        const int32_t k = k0 + 256 * j;
+        if (k >= a.in) break;
+        const float2 p[4] = {bf16_pair(u[j].x), bf16_pair(u[j].y), bf16_pair(u[j].z), bf16_pair(u[j].w)};
+        const float2 q[4] = {bf16_pair(v[j].x), bf16_pair(v[j].y), bf16_pair(v[j].z), bf16_pair(v[j].w)};
+#pragma unroll
+        for (int i = 0; i < FEW; ++i) {
+          if (i >= n) break;
+          const uint4 d = __ldg(reinterpret_cast<const uint4*>(x + i * a.ld_x + k));
+          const float2 y[4] = {bf16_pair(d.x), bf16_pair(d.y), bf16_pair(d.z), bf16_pair(d.w)};
+#pragma unroll
+          for (int h = 0; h < 4; ++h) {
+            sum[i][0] = fma2(p[h], y[h], sum[i][0]);
+            sum[i][1] = fma2(q[h], y[h], sum[i][1]);
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < FEW; ++i) {
+      if (i >= n) break;
+      const float s = warp_sum(sum[i][0].x + sum[i][0].y), t = warp_sum(sum[i][1].x + sum[i][1].y);
+      uint16_t* y = a.y + (row + i) * a.ld_y + f;
+      if (lane == 0 && GRS_CHECK(row + i < a.rows, exp_flags, SITE_EXP_ROW)) {
+        y[0] = from_float<uint16_t>(s);
+        if (f + 1 < a.out) y[1] = from_float<uint16_t>(t);
+      }
+    }
   }
 }
 
@@ -149,12 +259,12 @@ grs_status check_experts(const grs_experts* s, const char* who, ExpLd* ld) {
   return GRS_OK;
 }
 
-template <Product kP, typename T, typename O>
+template <Product kP, typename O>
 cudaError_t exp_general(const grs_experts* s, const ExpLd& ld, const void* a, const void* b, const int32_t* offsets, void* o, void* stream) {
   const int64_t in = s->in_features, out = s->out_features;
-  GeneralArgs<T, O> p{};
-  p.a = static_cast<const T*>(a);
-  p.b = static_cast<const T*>(b);
+  GeneralArgs<O> p{};
+  p.a = static_cast<const float*>(a);
+  p.b = static_cast<const float*>(b);
   p.o = static_cast<O*>(o);
   p.offsets = offsets;
   p.rows = static_cast<int32_t>(s->rows);
@@ -166,22 +276,48 @@ cudaError_t exp_general(const grs_experts* s, const ExpLd& ld, const void* a, co
   } else {  // A = xs, B = dys
     p.a_f = 1, p.a_k = ld.x, p.b_c = 1, p.b_k = ld.y, p.o_c = in, p.o_e = in * out, p.f = in, p.c = out;
   }
-  return launch_pdl(exp_general_kernel<kP, T, O>, dim3(152 * 8), dim3(EXP_THREADS), 0, stream, p);
+  return launch_pdl(exp_general_kernel<kP, O>, dim3(152 * 2), dim3(EXP_THREADS), 0, stream, p);
 }
 
 template <Product kP>
 cudaError_t exp_general(const grs_experts* s, const ExpLd& ld, const void* a, const void* b, const int32_t* offsets, void* o, void* stream) {
-  if (kP == Product::kWeights && s->grad_dtype == GRS_DTYPE_BF16) return exp_general<kP, float, uint16_t>(s, ld, a, b, offsets, o, stream);
-  return exp_general<kP, float, float>(s, ld, a, b, offsets, o, stream);
+  if (kP == Product::kWeights && s->grad_dtype == GRS_DTYPE_BF16) return exp_general<kP, uint16_t>(s, ld, a, b, offsets, o, stream);
+  return exp_general<kP, float>(s, ld, a, b, offsets, o, stream);
+}
+
+// Whether forward is left to exp_few_kernel.
+bool exp_few(const grs_experts* s, const ExpLd& ld) { return s->rows <= FEW_ROWS && s->in_features % 8 == 0 && ld.x % 8 == 0; }
+
+cudaError_t exp_few_forward(const grs_experts* s, const ExpLd& ld, const void* xs, const void* w, const int32_t* offsets, void* ys, void* stream) {
+  const FewArgs a{static_cast<const uint16_t*>(xs), static_cast<const uint16_t*>(w), static_cast<uint16_t*>(ys), offsets, ld.x, ld.y,
+                  static_cast<int32_t>(s->rows), s->experts, s->in_features, s->out_features};
+  return launch_pdl(exp_few_kernel, dim3(152 * 2), dim3(EXP_THREADS), 0, stream, a);
 }
 
 // --------------------------------------------------- bf16, rows laid out anew
-__global__ void __launch_bounds__(EXP_THREADS) exp_pad_kernel(const uint16_t* __restrict__ from, int64_t ld, uint16_t* __restrict__ to,
-                                                              int64_t ld_to, int64_t rows, int32_t width) {
+// Up to three matrices to rows that are whole 16-byte chunks apart, a thread
+// eight elements; what lies behind a row's last element is never read.
+struct PadArgs {
+  const uint16_t* from[3];
+  uint16_t* to[3];
+  int64_t ld[3], rows[3], chunks[4];  // chunks[i]: of the matrices before
+  int32_t width[3], per[3];           // elements and chunks of a row
+};
+
+__global__ void __launch_bounds__(EXP_THREADS) exp_pad_kernel(const __grid_constant__ PadArgs a) {
   pdl_wait();
   pdl_trigger();
-  for (int64_t r = blockIdx.x; r < rows; r += gridDim.x)
-    for (int32_t i = threadIdx.x; i < width; i += EXP_THREADS) to[r * ld_to + i] = from[r * ld + i];
+  const int64_t i = int64_t(blockIdx.x) * EXP_THREADS + threadIdx.x;
+  if (i >= a.chunks[3]) return;
+  const int m = i >= a.chunks[2] ? 2 : i >= a.chunks[1] ? 1 : 0;
+  const int64_t c = i - a.chunks[m], r = c / a.per[m];
+  const int32_t k = static_cast<int32_t>(c - r * a.per[m]) * 8, n = a.width[m] - k;
+  const uint16_t* p = a.from[m] + r * a.ld[m] + k;
+  uint32_t v[8];
+#pragma unroll
+  for (int q = 0; q < 8; ++q) v[q] = q < n ? __ldg(p + q) : 0;
+  if (GRS_CHECK(r < a.rows[m], exp_flags, SITE_EXP_ROW))
+    *reinterpret_cast<uint4*>(a.to[m] + c * 8) = make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
 }
 
 int64_t round8(int64_t n) { return (n + 7) & ~int64_t(7); }
@@ -189,23 +325,41 @@ int64_t round8(int64_t n) { return (n + 7) & ~int64_t(7); }
 // Bytes of an operand's copy: none where its rows are whole 16-byte chunks apart.
 int64_t pad_bytes(int64_t rows, int64_t ld, int64_t width) { return ld % 8 == 0 ? 0 : rows * round8(width) * 2; }
 
-// `p` itself, or its copy at *ws; *ld becomes the copy's.
-const void* pad_rows(const void* p, int64_t rows, int64_t* ld, int64_t width, uint8_t** ws, void* stream, cudaError_t* e) {
-  const int64_t bytes = pad_bytes(rows, *ld, width);
-  if (bytes == 0 || *e != cudaSuccess) return p;
-  uint16_t* to = reinterpret_cast<uint16_t*>(*ws);
-  *e = launch_pdl(exp_pad_kernel, dim3(static_cast<unsigned>(rows < 152 * 8 ? rows : 152 * 8)), dim3(EXP_THREADS), 0, stream,
-                  static_cast<const uint16_t*>(p), *ld, to, round8(width), rows, static_cast<int32_t>(width));
-  *ws += (bytes + 15) & ~int64_t(15);
-  *ld = round8(width);
-  return to;
-}
+// Copies to be made, at *ws one after another.
+struct Pads {
+  PadArgs a{};
+  int n = 0;
+  uint8_t* ws;
+  explicit Pads(void* ws_) : ws(static_cast<uint8_t*>(ws_)) {}
+  // `p` itself, or where its copy will be; *ld becomes the copy's.
+  const void* add(const void* p, int64_t rows, int64_t* ld, int64_t width) {
+    const int64_t bytes = pad_bytes(rows, *ld, width);
+    if (bytes == 0) return p;
+    a.from[n] = static_cast<const uint16_t*>(p);
+    a.to[n] = reinterpret_cast<uint16_t*>(ws);
+    a.ld[n] = *ld;
+    a.rows[n] = rows;
+    a.width[n] = static_cast<int32_t>(width);
+    a.per[n] = static_cast<int32_t>(round8(width) / 8);
+    const int64_t all = a.chunks[n] + rows * a.per[n];
+    for (int i = ++n; i < 4; ++i) a.chunks[i] = all;
+    *ld = round8(width);
+    void* here = ws;
+    ws += bytes;  // (whole 16-byte chunks)
+    return here;
+  }
+  cudaError_t run(void* stream) const {
+    if (n == 0) return cudaSuccess;
+    const int64_t blocks = (a.chunks[3] + EXP_THREADS - 1) / EXP_THREADS;
+    if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
+    return launch_pdl(exp_pad_kernel, dim3(static_cast<unsigned>(blocks)), dim3(EXP_THREADS), 0, stream, a);
+  }
+};
 
 int64_t exp_workspace(const grs_experts* s, const ExpLd& ld) {
   if (s->dtype == GRS_DTYPE_FP32) return 0;
-  auto up = [](int64_t b) { return (b + 15) & ~int64_t(15); };
-  return up(pad_bytes(s->rows, ld.x, s->in_features)) + up(pad_bytes(s->rows, ld.y, s->out_features)) +
-         up(pad_bytes(int64_t(s->experts) * s->out_features, ld.w, s->in_features));
+  return pad_bytes(s->rows, ld.x, s->in_features) + pad_bytes(s->rows, ld.y, s->out_features) +
+         pad_bytes(int64_t(s->experts) * s->out_features, ld.w, s->in_features);
 }
 
 }  // namespace
@@ -253,11 +407,14 @@ grs_status grs_experts_forward(const grs_experts* s, const void* xs, const void*
   cudaError_t e = cudaSuccess;
   if (s->dtype == GRS_DTYPE_FP32) {
     e = exp_general<Product::kForward>(s, ld, w, xs, offsets, ys, stream);
+  } else if (exp_few(s, ld)) {
+    e = exp_few_forward(s, ld, xs, w, offsets, ys, stream);
   } else {
-    uint8_t* ws = static_cast<uint8_t*>(workspace);
     const int64_t ld_y = ld.y;
-    xs = pad_rows(xs, s->rows, &ld.x, s->in_features, &ws, stream, &e);
-    w = pad_rows(w, int64_t(s->experts) * s->out_features, &ld.w, s->in_features, &ws, stream, &e);
+    Pads pads(workspace);
+    xs = pads.add(xs, s->rows, &ld.x, s->in_features);
+    w = pads.add(w, int64_t(s->experts) * s->out_features, &ld.w, s->in_features);
+    e = pads.run(stream);
     if (e == cudaSuccess) e = experts_mma(Product::kForward, s, ld, xs, w, nullptr, offsets, ys, ld_y, stream);
   }
   return e == cudaSuccess ? GRS_OK : api_cuda_fail(e, who);
@@ -287,17 +444,15 @@ grs_status grs_experts_backward(const grs_experts* s, const void* dys, const voi
     if (dxs != nullptr) e = exp_general<Product::kRows>(s, ld, w, dys, offsets, dxs, stream);
     if (e == cudaSuccess && dw != nullptr) e = exp_general<Product::kWeights>(s, ld, xs, dys, offsets, dw, stream);
   } else if (dxs != nullptr || dw != nullptr) {
-    uint8_t* ws = static_cast<uint8_t*>(workspace);
     const int64_t ld_x = ld.x;
-    dys = pad_rows(dys, s->rows, &ld.y, s->out_features, &ws, stream, &e);
-    if (dxs != nullptr) {
-      w = pad_rows(w, int64_t(s->experts) * s->out_features, &ld.w, s->in_features, &ws, stream, &e);
-      if (e == cudaSuccess) e = experts_mma(Product::kRows, s, ld, nullptr, w, dys, offsets, dxs, ld_x, stream);
-    }
-    if (dw != nullptr) {
-      xs = pad_rows(xs, s->rows, &ld.x, s->in_features, &ws, stream, &e);
-      if (e == cudaSuccess) e = experts_mma(Product::kWeights, s, ld, xs, nullptr, dys, offsets, dw, s->in_features, stream);
-    }
+    Pads pads(workspace);
+    dys = pads.add(dys, s->rows, &ld.y, s->out_features);
+    if (dxs != nullptr) w = pads.add(w, int64_t(s->experts) * s->out_features, &ld.w, s->in_features);
+    if (dw != nullptr) xs = pads.add(xs, s->rows, &ld.x, s->in_features);
+    e = pads.run(stream);
+    if (e == cudaSuccess && dxs != nullptr) e = experts_mma(Product::kRows, s, ld, nullptr, w, dys, offsets, dxs, ld_x, stream);
+    if (e == cudaSuccess && dw != nullptr)
+      e = experts_mma(Product::kWeights, s, ld, xs, nullptr, dys, offsets, dw, s->in_features, stream);
   }
   return e == cudaSuccess ? GRS_OK : api_cuda_fail(e, who);
 }

@@ -34,7 +34,7 @@
 
 #include "api_util.h"
 #include "device.cuh"
-#include "experts.h"
+#include "experts.cuh"
 #include "internal.h"
 #include "launch.cuh"
 #include "operators.cuh"
@@ -57,7 +57,7 @@ __device__ int mma_flags[FLAG_COUNT];
 template <int TC, int kCtas>
 struct Shape {
   static constexpr int A = MMA_F * MMA_K * 2, B = TC / kCtas * MMA_K * 2, STAGE = A + B;
-  static constexpr int FIXED = 1024 + (GRS_MOE_MAX_EXPERTS + 2) * 4 + 768;  // alignment, tiles before each expert, barriers
+  static constexpr int FIXED = 1024 + (GRS_MOE_MAX_EXPERTS + 2) * 4 + 832;  // alignment, tiles before each expert, barriers
   static constexpr int FIT = (MMA_SMEM - FIXED) / STAGE;
 #ifndef MAX_STAGES
 #define MAX_STAGES 10
@@ -77,7 +77,7 @@ struct MmaArgs {
 };
 
 struct Tile {
-  int32_t e, f0, c0, c1, k0, k1;  // e < 0: no more
+  int32_t e, f0, fn, c0, c1, k0, k1;  // e < 0: no more; fn: features
 };
 
 template <Product kP, int TC, int kCtas>
@@ -85,13 +85,14 @@ struct Tiles {
   const int32_t* offsets;
   const int32_t* list;  // c tiles before each expert's; kWeights: the experts by size (NULL: as they come)
   int64_t f, c, k, ft, ct, total;
-  int32_t rows;
+  int32_t rows, step;   // step: features from one tile to the next
   int at_e = 0;
 
   template <typename O>
   __device__ __forceinline__ Tiles(const MmaArgs<O>& a, const int32_t* list_)
       : offsets(a.offsets), list(list_), f(a.f), c(a.c), k(a.k), rows(a.rows) {
-    ft = (f + MMA_F * kCtas - 1) / (MMA_F * kCtas);
+    step = MMA_F * kCtas;
+    ft = (f + step - 1) / step;
     ct = (c + TC - 1) / TC;
     total = kP == Product::kWeights ? ft * ct * a.experts : ft * list[a.experts];
   }
@@ -99,7 +100,7 @@ struct Tiles {
   __device__ __forceinline__ Tile at(int64_t t) {  // ascending, unless kWeights
     Tile x;
     int64_t ci = t / ft, c0, c1;
-    x.f0 = static_cast<int32_t>((t - ci * ft) * (MMA_F * kCtas));
+    x.f0 = static_cast<int32_t>((t - ci * ft) * step);
     if constexpr (kP == Product::kWeights) {
       const int64_t e = ci / ct;
       ci -= e * ct;
@@ -110,15 +111,14 @@ struct Tiles {
       while (list[at_e + 1] <= ci) ++at_e;
       x.e = at_e;
     }
-    int32_t from = __ldg(offsets + x.e), to = __ldg(offsets + x.e + 1);
-    from = from < 0 ? 0 : from > rows ? rows : from;
-    to = to < from ? from : to > rows ? rows : to;
+    x.fn = step;
+    const ExpertRows r(offsets, x.e, rows);
     if constexpr (kP == Product::kWeights) {
-      x.k0 = from;
-      x.k1 = to;
+      x.k0 = r.from;
+      x.k1 = r.to;
     } else {
-      c0 = from + (ci - list[x.e]) * TC;
-      c1 = to;
+      c0 = r.from + (ci - list[x.e]) * TC;
+      c1 = r.to;
       x.k0 = 0;
       x.k1 = static_cast<int32_t>(k);
     }
@@ -139,44 +139,6 @@ __device__ __forceinline__ void by_size(const int32_t* offsets, int32_t experts,
     int rank = 0;
     for (int i = 0; i < experts; ++i) rank += size[i] > n || (size[i] == n && i < e);
     order[rank] = e;
-  }
-}
-
-// Tiles of c before each expert's, by a block.
-template <int TC>
-__device__ __forceinline__ void tile_prefix(const int32_t* offsets, int32_t experts, int32_t rows, int32_t* first) {
-  __shared__ int32_t sums[MMA_THREADS / 32];
-  constexpr int EACH = (GRS_MOE_MAX_EXPERTS + MMA_THREADS - 1) / MMA_THREADS;
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  int32_t n[EACH], all = 0;
-#pragma unroll
-  for (int i = 0; i < EACH; ++i) {
-    const int e = threadIdx.x * EACH + i;
-    n[i] = 0;
-    if (e < experts) {
-      int32_t a = __ldg(offsets + e), b = __ldg(offsets + e + 1);
-      a = a < 0 ? 0 : a > rows ? rows : a;
-      b = b < a ? a : b > rows ? rows : b;
-      n[i] = (b - a) / TC + ((b - a) % TC != 0);
-    }
-    all += n[i];
-  }
-  int32_t s = all;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int32_t y = __shfl_up_sync(0xffffffffu, s, o);
-    if (lane >= o) s += y;
-  }
-  if (lane == 31) sums[w] = s;
-  __syncthreads();
-  for (int i = 0; i < w; ++i) s += sums[i];
-  s -= all;
-#pragma unroll
-  for (int i = 0; i < EACH; ++i) {
-    const int e = threadIdx.x * EACH + i;
-    if (e < experts) first[e] = s;
-    s += n[i];
-    if (e == experts - 1) first[experts] = s;
   }
 }
 
@@ -221,7 +183,7 @@ __global__ void __launch_bounds__(MMA_THREADS, 1)
   constexpr bool kWeights = kP == Product::kWeights, kASK = kP == Product::kForward, kBSK = !kWeights;  // operands along k
   constexpr bool kSections = kWeights && sizeof(O) == 4;
   constexpr uint32_t COLUMNS = 2 * TC;  // two accumulators
-  constexpr uint32_t TMEM = COLUMNS <= 32 ? 32 : COLUMNS <= 64 ? 64 : COLUMNS <= 128 ? 128 : COLUMNS <= 256 ? 256 : 512;
+  constexpr uint32_t TMEM = COLUMNS <= 64 ? 64 : COLUMNS <= 128 ? 128 : COLUMNS <= 256 ? 256 : 512;
   static_assert(COLUMNS <= 512, "tensor memory has 512 columns");
   static_assert(!kWeights || TC / kCtas % 64 == 0, "operands across k come in 64s");
   extern __shared__ uint8_t smem[];
@@ -235,7 +197,7 @@ __global__ void __launch_bounds__(MMA_THREADS, 1)
   uint32_t* tmem_at = reinterpret_cast<uint32_t*>(ring + RING);
   volatile int* abort = reinterpret_cast<int*>(tmem_at + 1);
 
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31, w = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
   const uint32_t rank = kCtas == 1 ? 0 : cluster_rank();
   if (threadIdx.x == 0) {
     prefetch_map(&map_a);
@@ -266,7 +228,7 @@ __global__ void __launch_bounds__(MMA_THREADS, 1)
     if (a.experts <= MMA_THREADS) by_size(a.offsets, a.experts, first);
   } else {
     pdl_trigger();  // (kWeights has blocks that never begin)
-    tile_prefix<TC>(a.offsets, a.experts, a.rows, first);
+    group_prefix<TC, MMA_THREADS>(a.offsets, a.experts, a.rows, first);
   }
   tmem_before_sync();
   if constexpr (kCtas == 2) cluster_sync();
@@ -274,21 +236,26 @@ __global__ void __launch_bounds__(MMA_THREADS, 1)
   tmem_after_sync();
   const uint32_t tmem = *tmem_at;
 
-  // The next tile of the ring, for a whole warp or one thread of a role.
+  // The next tile of the ring, for a whole warp; false: a wait gave up.
   uint32_t slot = 0, slot_parity = 0;
+  auto wait_all = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, wait_for(bar, parity, abort)) != 0; };
   auto next_tile = [&](Tile& x) {
-    if (!wait_for(told + slot, slot_parity, abort)) return false;
-    x = ring[slot];
-    return true;
-  };
-  auto heard_tile = [&] {  // by one thread of the role
-    mbar_arrive(heard + slot);
-  };
-  auto step_ring = [&] {
+    if (!wait_all(told + slot, slot_parity)) return false;
+    const int32_t* r = reinterpret_cast<const int32_t*>(ring + slot);
+    const int32_t v = lane < static_cast<int>(sizeof(Tile) / 4) ? r[lane] : 0;
+    x.e = __shfl_sync(0xffffffffu, v, 0);
+    x.f0 = __shfl_sync(0xffffffffu, v, 1);
+    x.fn = __shfl_sync(0xffffffffu, v, 2);
+    x.c0 = __shfl_sync(0xffffffffu, v, 3);
+    x.c1 = __shfl_sync(0xffffffffu, v, 4);
+    x.k0 = __shfl_sync(0xffffffffu, v, 5);
+    x.k1 = __shfl_sync(0xffffffffu, v, 6);
+    if (elected()) mbar_arrive(heard + slot);
     if (++slot == RING) {
       slot = 0;
       slot_parity ^= 1;
     }
+    return true;
   };
 
   if (w == 0) {
@@ -300,24 +267,19 @@ __global__ void __launch_bounds__(MMA_THREADS, 1)
     bool ok = true;
     while (ok) {
       Tile x;
-      ok = __all_sync(0xffffffffu, next_tile(x));
-      if (!ok) break;
-      if (lane == 0) heard_tile();
-      step_ring();
-      if (x.e < 0) break;
-      const int32_t k_end = x.k1;
+      ok = next_tile(x);
+      if (!ok || x.e < 0) break;
       const int32_t f0 = x.f0 + static_cast<int32_t>(rank) * MMA_F;
       // Columns of this block: half of the instruction's.
       const int32_t half = kWeights ? TC / kCtas : (x.c1 - x.c0 + 15) / 16 * 16 / kCtas;
       const int32_t c0 = x.c0 + static_cast<int32_t>(rank) * half;
-      for (int32_t k = x.k0; k < k_end; k += MMA_K) {
-        const int32_t valid = k_end - k < MMA_K ? k_end - k : MMA_K;
-        const bool last = kWeights && valid % 16 != 0;
-        if (lane == 0) {
-          ok = wait_for(empty + s, parity, abort);
-          if (!ok) break;
-          const uint32_t to = stages_at + s * S::STAGE, bar = full_at + s * 8;
-          const uint32_t on = last ? smem_addr(tail + s) : bar;
+      for (int32_t k = x.k0; k < x.k1; k += MMA_K) {
+        const bool last = kWeights && x.k1 - k < MMA_K && (x.k1 - k) % 16 != 0;
+        ok = wait_all(empty + s, parity);
+        if (!ok) break;
+        const uint32_t to = stages_at + s * S::STAGE, bar = full_at + s * 8;
+        const uint32_t on = last ? smem_addr(tail + s) : bar;
+        if (elected()) {
           if (last) mbar_arrive_expect_tx(tail + s, S::STAGE);
           else if (kCtas == 1) mbar_arrive_expect_tx(full + s, S::STAGE);
           else remote_arrive_expect_tx(bar, S::STAGE);
@@ -337,53 +299,55 @@ __global__ void __launch_bounds__(MMA_THREADS, 1)
             for (int i = 0; i < TC / kCtas / 64; ++i) tma_load<kCtas>(to + S::A + i * 8192, &map_b, c0 + i * 64, k, on);
           }
         }
+        __syncwarp();
         if (++s == S::STAGES) {
           s = 0;
           parity ^= 1;
         }
       }
-      ok = __shfl_sync(0xffffffffu, ok, 0);
     }
   } else if (w == 1) {
     // ---------------------------------------------------------- products
-    if (lane == 0 && rank == 0) {
+    if (rank == 0) {
       uint32_t s = 0, parity = 0, acc = 0, acc_parity = 1;
       const uint32_t a_at = operand<kASK>(smem_addr(stages), 8192), b_at = operand<kBSK>(smem_addr(stages) + S::A, 8192);
       bool ok = true;
       while (ok) {
         Tile x;
         ok = next_tile(x);
-        if (!ok) break;
-        heard_tile();
-        step_ring();
-        if (x.e < 0) break;
+        if (!ok || x.e < 0) break;
         const uint32_t n = kWeights ? TC : (static_cast<uint32_t>(x.c1 - x.c0) + 15) / 16 * 16;
         const uint32_t desc = product_desc(kASK, kBSK, MMA_F * kCtas, n);
         int32_t rest = x.k1 - x.k0;
         while (rest > 0 && ok) {
-          ok = wait_for(taken + acc, acc_parity, abort);
+          ok = wait_all(taken + acc, acc_parity);
+          if (!ok) break;
           tmem_after_sync();
           const uint32_t d = tmem + acc * TC;
           int32_t section = kSections ? MMA_SECTION : INT32_MAX;
           bool add = false;
-          for (; rest > 0 && section > 0 && ok; rest -= MMA_K, --section) {
-            ok = wait_for(full + s, parity, abort);
+          for (; rest > 0 && section > 0; rest -= MMA_K, --section) {
+            ok = wait_all(full + s, parity);
             if (!ok) break;
             tmem_after_sync();
             const uint32_t da = a_at + s * (S::STAGE >> 4), db = b_at + s * (S::STAGE >> 4);
-            mma<kCtas>(d, da, db, desc, add);
+            if (elected()) {
+              mma<kCtas>(d, da, db, desc, add);
 #pragma unroll
-            for (int i = 1; i < MMA_K / 16; ++i)
-              if (rest > 16 * i) mma<kCtas>(d, da + i * operand_step<kASK>, db + i * operand_step<kBSK>, desc, true);
+              for (int i = 1; i < MMA_K / 16; ++i)
+                if (rest > 16 * i) mma<kCtas>(d, da + i * operand_step<kASK>, db + i * operand_step<kBSK>, desc, true);
+              mma_commit<kCtas>(empty + s);
+            }
+            __syncwarp();
             add = true;
-            mma_commit<kCtas>(empty + s);
             if (++s == S::STAGES) {
               s = 0;
               parity ^= 1;
             }
           }
           if (!ok) break;
-          mma_commit<kCtas>(done + acc);
+          if (elected()) mma_commit<kCtas>(done + acc);
+          __syncwarp();
           acc ^= 1;
           if (acc == 0) acc_parity ^= 1;
         }
@@ -414,8 +378,10 @@ __global__ void __launch_bounds__(MMA_THREADS, 1)
         if (more) x = tiles.at(t);
         ring[slot] = x;
         mbar_arrive(told + slot);
-        step_ring();
-        if (slot == 0) empty_parity ^= 1;
+        if (++slot == RING) {
+          slot = 0;
+          empty_parity ^= 1;
+        }
         if (!more) break;
         if constexpr (kWeights) {
           ok = wait_for(answered + q, q_parity, abort);
@@ -440,16 +406,13 @@ __global__ void __launch_bounds__(MMA_THREADS, 1)
     bool ok = true;
     while (ok) {
       Tile x;
-      ok = __all_sync(0xffffffffu, next_tile(x));
-      if (!ok) break;
-      if (lane == 0) heard_tile();
-      step_ring();
-      if (x.e < 0) break;
+      ok = next_tile(x);
+      if (!ok || x.e < 0) break;
       const int32_t n = x.k1 - x.k0, blocks = (n + MMA_K - 1) / MMA_K, valid = n % MMA_K;
       const uint32_t last = (s + blocks + S::STAGES - 1) % S::STAGES;
       s = (s + blocks) % S::STAGES;
       if (valid % 16 == 0) continue;
-      ok = __all_sync(0xffffffffu, wait_for(tail + last, parities >> last & 1, abort));
+      ok = wait_all(tail + last, parities >> last & 1);
       if (!ok) break;
       parities ^= 1u << last;
       const int32_t bad = (16 - valid % 16) * 8;  // 16-byte chunks to clear, in each 64 of f or c
@@ -472,11 +435,8 @@ __global__ void __launch_bounds__(MMA_THREADS, 1)
     const bool words = sizeof(O) == 4 || a.words != 0;
     while (ok) {
       Tile x;
-      ok = __all_sync(0xffffffffu, next_tile(x));
-      if (!ok) break;
-      if (lane == 0) heard_tile();
-      step_ring();
-      if (x.e < 0) break;
+      ok = next_tile(x);
+      if (!ok || x.e < 0) break;
       const int32_t blocks = (x.k1 - x.k0 + MMA_K - 1) / MMA_K;
       const int64_t f = x.f0 + int64_t(rank) * MMA_F + quarter * 32 + lane;
       const int n = x.c1 - x.c0;
@@ -495,7 +455,7 @@ __global__ void __launch_bounds__(MMA_THREADS, 1)
           for (int j = 0; j < 32; ++j) sum[p][j] = 0.0f;
       }
       for (int32_t i = 0; i < sections && blocks > 0; ++i) {
-        ok = __all_sync(0xffffffffu, wait_for(done + acc, parity, abort));
+        ok = wait_all(done + acc, parity);
         if (!ok) break;
         tmem_after_sync();
         if constexpr (kSections) {
@@ -612,7 +572,8 @@ cudaError_t mma_launch(const grs_experts* s, const ExpLd& ld, const void* xs, co
   }
   if (!fine) return cudaErrorInvalidValue;
   a.words = api_aligned(o, 4) && o_ld % 2 == 0 && a.o_e % 2 == 0;
-  tiles *= (a.f + MMA_F * kCtas - 1) / (MMA_F * kCtas);
+  const int64_t step = MMA_F * kCtas;
+  tiles *= (a.f + step - 1) / step;
   // Weights: a cluster for each tile, of which those that run take over the others' (ask_cluster).
   const int64_t at_once = kP == Product::kWeights ? INT32_MAX / kCtas : 152 / kCtas;
   if (kP == Product::kWeights && tiles > at_once) return cudaErrorInvalidConfiguration;
@@ -627,8 +588,15 @@ cudaError_t mma_rows(const grs_experts* s, const ExpLd& ld, const void* xs, cons
                      int64_t o_ld, void* stream) {
   const int64_t mean = s->rows / s->experts;
   if (mean >= 128) return mma_launch<kP, 256, 2, uint16_t>(s, ld, xs, w, dys, offsets, o, o_ld, stream);
-  if (mean >= 32) return mma_launch<kP, 128, 1, uint16_t>(s, ld, xs, w, dys, offsets, o, o_ld, stream);
-  return mma_launch<kP, 32, 1, uint16_t>(s, ld, xs, w, dys, offsets, o, o_ld, stream);
+#ifndef MEAN_64
+#define MEAN_64 64
+#endif
+#ifndef MEAN_16
+#define MEAN_16 16
+#endif
+  if (mean >= MEAN_64) return mma_launch<kP, 128, 1, uint16_t>(s, ld, xs, w, dys, offsets, o, o_ld, stream);
+  if (mean >= MEAN_16) return mma_launch<kP, 64, 1, uint16_t>(s, ld, xs, w, dys, offsets, o, o_ld, stream);
+  return mma_launch<kP, 16, 1, uint16_t>(s, ld, xs, w, dys, offsets, o, o_ld, stream);
 }
 
 }  // namespace

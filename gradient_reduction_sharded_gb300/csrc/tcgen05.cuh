@@ -15,6 +15,15 @@
 
 namespace grs {
 
+// One thread of a whole warp, always the same.  What it runs stays in code of
+// the whole warp, whose addresses and counters the compiler then keeps in the
+// registers that matrix and TMA instructions take them from.
+__device__ __forceinline__ bool elected() {
+  uint32_t is;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(is));
+  return is != 0;
+}
+
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));

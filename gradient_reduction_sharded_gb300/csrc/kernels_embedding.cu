@@ -202,6 +202,92 @@ __global__ void __launch_bounds__(EMB_THREADS) emb_scatter_kernel(const __grid_c
   }
 }
 
+// All passes by one block, for few tokens: pairs go from pass to pass through
+// shared memory.
+constexpr int EMB_SMALL = 16;  // pairs of a thread: up to 4096
+struct SmallSortArgs {
+  const int32_t* ids;
+  int32_t *keys_out, *tokens_out;
+  int32_t n, begin, rows, digit, passes;
+};
+
+__global__ void __launch_bounds__(EMB_THREADS) emb_small_sort_kernel(const __grid_constant__ SmallSortArgs a) {
+  __shared__ int32_t at[EMB_WARPS][1 << EMB_DIGIT], warp_total[EMB_WARPS];
+  __shared__ int2 pairs[EMB_SMALL * EMB_THREADS];
+  pdl_wait();
+  pdl_trigger();
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, bins = 1 << a.digit;
+  const int each = (a.n + EMB_THREADS - 1) / EMB_THREADS;  // of a thread; a warp has 32 each neighbours
+  int32_t key[EMB_SMALL], token[EMB_SMALL], rank[EMB_SMALL];
+#pragma unroll
+  for (int j = 0; j < EMB_SMALL; ++j) {
+    const int i = w * 32 * each + j * 32 + lane;
+    key[j] = j < each && i < a.n ? emb_row(__ldg(a.ids + i), a.begin, a.rows) : -1;
+    token[j] = i;
+  }
+  for (int pass = 0; pass < a.passes; ++pass) {
+    const int shift = pass * a.digit;
+    for (int b = lane; b < bins; b += 32) at[w][b] = 0;
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < EMB_SMALL; ++j) {
+      if (j >= each) break;
+      const int d = key[j] < 0 ? -1 : (key[j] >> shift) & (bins - 1);
+      const unsigned same = __match_any_sync(0xffffffffu, d);
+      rank[j] = d >= 0 ? at[w][d] + __popc(same & ((1u << lane) - 1u)) : 0;
+      __syncwarp();
+      if (d >= 0 && lane == __ffs(same) - 1) at[w][d] += __popc(same);
+      __syncwarp();
+    }
+    __syncthreads();
+    const int b0 = threadIdx.x * EMB_EACH;
+    int32_t total[EMB_EACH] = {}, all = 0, whole;
+#pragma unroll
+    for (int q = 0; q < EMB_EACH; ++q) {
+      if (b0 + q < bins)
+#pragma unroll
+        for (int k = 0; k < EMB_WARPS; ++k) {
+          const int32_t c = at[k][b0 + q];
+          at[k][b0 + q] = total[q];
+          total[q] += c;
+        }
+      all += total[q];
+    }
+    int32_t s = emb_prefix(all, warp_total, &whole);
+#pragma unroll
+    for (int q = 0; q < EMB_EACH; ++q) {
+      if (b0 + q < bins)
+#pragma unroll
+        for (int k = 0; k < EMB_WARPS; ++k) at[k][b0 + q] += s;
+      s += total[q];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < EMB_SMALL; ++j)
+      if (key[j] >= 0) {
+        const int to = at[w][(key[j] >> shift) & (bins - 1)] + rank[j];
+        if (GRS_CHECK(to >= 0 && to < a.n, emb_flags, SITE_EMB_TOKEN)) pairs[to] = make_int2(key[j], token[j]);
+      }
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < EMB_SMALL; ++j) {
+      const int i = w * 32 * each + j * 32 + lane;
+      if (j < each && i < a.n) {
+        key[j] = pairs[i].x;
+        token[j] = pairs[i].y;
+      }
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < EMB_SMALL; ++j) {
+    const int i = w * 32 * each + j * 32 + lane;
+    if (j < each && i < a.n) {
+      a.keys_out[i] = key[j];
+      a.tokens_out[i] = token[j];
+    }
+  }
+}
+
 // How many of keys[lo, hi) are below `key`, plus lo: a warp, 32 places a step.
 __device__ __forceinline__ int32_t warp_lower_bound(const int32_t* keys, int64_t lo, int64_t hi, int64_t key) {
   const int lane = threadIdx.x & 31;
@@ -482,6 +568,12 @@ cudaError_t emb_sort(const grs_embedding* s, const EmbPlan& p, const int32_t* id
   const int64_t table = p.chunks * bins;
   const dim3 grid(static_cast<unsigned>(p.chunks)), block(EMB_THREADS);
   cudaError_t e = cudaSuccess;
+  if (n <= EMB_SMALL * EMB_THREADS) {
+    *keys = k[0];
+    *tokens = t[0];
+    const SmallSortArgs a{ids, k[0], t[0], static_cast<int32_t>(n), s->row_begin, p.rows, p.digit, p.passes};
+    return launch_pdl(emb_small_sort_kernel, dim3(1), block, 0, stream, a);
+  }
   for (int i = 0; i < p.passes && e == cudaSuccess; ++i) {
     SortArgs a{};
     a.ids = ids;

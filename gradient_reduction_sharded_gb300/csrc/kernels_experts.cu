@@ -296,12 +296,14 @@ cudaError_t exp_few_forward(const grs_experts* s, const ExpLd& ld, const void* x
 
 // --------------------------------------------------- bf16, rows laid out anew
 // Up to three matrices to rows that are whole 16-byte chunks apart, a thread
-// eight elements; what lies behind a row's last element is never read.
+// eight elements: from the two aligned chunks that they lie in, or one by one
+// where these reach behind the matrix.  What comes after a row's last element
+// in the copy is never read.
 struct PadArgs {
   const uint16_t* from[3];
   uint16_t* to[3];
-  int64_t ld[3], rows[3], chunks[4];  // chunks[i]: of the matrices before
-  int32_t width[3], per[3];           // elements and chunks of a row
+  int64_t ld[3], end[3], chunks[4];  // end: elements up to the matrix's last; chunks[i]: of the matrices before
+  int32_t per[3];                    // chunks of a row
 };
 
 __global__ void __launch_bounds__(EXP_THREADS) exp_pad_kernel(const __grid_constant__ PadArgs a) {
@@ -310,14 +312,27 @@ __global__ void __launch_bounds__(EXP_THREADS) exp_pad_kernel(const __grid_const
   const int64_t i = int64_t(blockIdx.x) * EXP_THREADS + threadIdx.x;
   if (i >= a.chunks[3]) return;
   const int m = i >= a.chunks[2] ? 2 : i >= a.chunks[1] ? 1 : 0;
-  const int64_t c = i - a.chunks[m], r = c / a.per[m];
-  const int32_t k = static_cast<int32_t>(c - r * a.per[m]) * 8, n = a.width[m] - k;
-  const uint16_t* p = a.from[m] + r * a.ld[m] + k;
-  uint32_t v[8];
+  const int64_t c = i - a.chunks[m], r = c <= UINT32_MAX ? static_cast<uint32_t>(c) / static_cast<uint32_t>(a.per[m]) : c / a.per[m];
+  const int64_t at = r * a.ld[m] + (c - r * a.per[m]) * 8, low = at & ~int64_t(7);
+  const uint16_t* p = a.from[m];
+  uint32_t w[8];
+  if (low + 16 <= a.end[m]) {
+    const uint4 x = __ldg(reinterpret_cast<const uint4*>(p + low)), y = __ldg(reinterpret_cast<const uint4*>(p + low) + 1);
+    w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
+    w[4] = y.x; w[5] = y.y; w[6] = y.z; w[7] = y.w;
+    const int shift = static_cast<int>(at - low);  // elements
 #pragma unroll
-  for (int q = 0; q < 8; ++q) v[q] = q < n ? __ldg(p + q) : 0;
-  if (GRS_CHECK(r < a.rows[m], exp_flags, SITE_EXP_ROW))
-    *reinterpret_cast<uint4*>(a.to[m] + c * 8) = make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
+    for (int q = 0; q < 6; ++q) w[q] = (shift & 4) != 0 ? w[q + 2] : w[q];
+#pragma unroll
+    for (int q = 0; q < 5; ++q) w[q] = (shift & 2) != 0 ? w[q + 1] : w[q];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) w[q] = (shift & 1) != 0 ? __funnelshift_r(w[q], w[q + 1], 16) : w[q];
+  } else {
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      w[q] = (at + 2 * q < a.end[m] ? uint32_t(__ldg(p + at + 2 * q)) : 0u) | (at + 2 * q + 1 < a.end[m] ? uint32_t(__ldg(p + at + 2 * q + 1)) << 16 : 0u);
+  }
+  if (GRS_CHECK(at < a.end[m], exp_flags, SITE_EXP_ROW)) *reinterpret_cast<uint4*>(a.to[m] + c * 8) = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 int64_t round8(int64_t n) { return (n + 7) & ~int64_t(7); }
@@ -338,8 +353,7 @@ struct Pads {
     a.from[n] = static_cast<const uint16_t*>(p);
     a.to[n] = reinterpret_cast<uint16_t*>(ws);
     a.ld[n] = *ld;
-    a.rows[n] = rows;
-    a.width[n] = static_cast<int32_t>(width);
+    a.end[n] = (rows - 1) * *ld + width;
     a.per[n] = static_cast<int32_t>(round8(width) / 8);
     const int64_t all = a.chunks[n] + rows * a.per[n];
     for (int i = ++n; i < 4; ++i) a.chunks[i] = all;

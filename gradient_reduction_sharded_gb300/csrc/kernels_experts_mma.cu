@@ -58,11 +58,9 @@ template <int TC, int kCtas>
 struct Shape {
   static constexpr int A = MMA_F * MMA_K * 2, B = TC / kCtas * MMA_K * 2, STAGE = A + B;
   static constexpr int FIXED = 1024 + (GRS_MOE_MAX_EXPERTS + 2) * 4 + 832;  // alignment, tiles before each expert, barriers
-  static constexpr int FIT = (MMA_SMEM - FIXED) / STAGE;
-#ifndef MAX_STAGES
-#define MAX_STAGES 10
-#endif
-  static constexpr int STAGES = FIT < MAX_STAGES ? FIT : MAX_STAGES;
+  static constexpr int PER_SM = kCtas == 1 && TC <= 64 ? 2 : 1;  // blocks
+  static constexpr int FIT = ((PER_SM == 2 ? 113 * 1024 : MMA_SMEM) - FIXED) / STAGE;
+  static constexpr int STAGES = FIT < 10 ? FIT : 10;
   static constexpr int BYTES = STAGES * STAGE + FIXED;
 };
 
@@ -177,7 +175,7 @@ __device__ __forceinline__ void store_columns(O* o, int64_t ld, const uint32_t (
 }
 
 template <Product kP, int TC, int kCtas, typename O>
-__global__ void __launch_bounds__(MMA_THREADS, 1)
+__global__ void __launch_bounds__(MMA_THREADS, (Shape<TC, kCtas>::PER_SM))
     exp_mma_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b, const __grid_constant__ MmaArgs<O> a) {
   using S = Shape<TC, kCtas>;
   constexpr bool kWeights = kP == Product::kWeights, kASK = kP == Product::kForward, kBSK = !kWeights;  // operands along k
@@ -271,7 +269,7 @@ __global__ void __launch_bounds__(MMA_THREADS, 1)
       if (!ok || x.e < 0) break;
       const int32_t f0 = x.f0 + static_cast<int32_t>(rank) * MMA_F;
       // Columns of this block: half of the instruction's.
-      const int32_t half = kWeights ? TC / kCtas : (x.c1 - x.c0 + 15) / 16 * 16 / kCtas;
+      const int32_t half = (x.c1 - x.c0 + 15) / 16 * 16 / kCtas;
       const int32_t c0 = x.c0 + static_cast<int32_t>(rank) * half;
       for (int32_t k = x.k0; k < x.k1; k += MMA_K) {
         const bool last = kWeights && x.k1 - k < MMA_K && (x.k1 - k) % 16 != 0;
@@ -316,7 +314,7 @@ __global__ void __launch_bounds__(MMA_THREADS, 1)
         Tile x;
         ok = next_tile(x);
         if (!ok || x.e < 0) break;
-        const uint32_t n = kWeights ? TC : (static_cast<uint32_t>(x.c1 - x.c0) + 15) / 16 * 16;
+        const uint32_t n = (static_cast<uint32_t>(x.c1 - x.c0) + 15) / 16 * 16;
         const uint32_t desc = product_desc(kASK, kBSK, MMA_F * kCtas, n);
         int32_t rest = x.k1 - x.k0;
         while (rest > 0 && ok) {
@@ -461,6 +459,7 @@ __global__ void __launch_bounds__(MMA_THREADS, 1)
         if constexpr (kSections) {
 #pragma unroll
           for (int p = 0; p < 2 * PARTS; ++p) {
+            if (64 * (p / 2) + 32 * half + p % 2 * 16 >= n) break;
             uint32_t v[16];
             tmem_load16(from + acc * TC + p / 2 * 64 + p % 2 * 16, v);
             tmem_wait_load();
@@ -489,6 +488,7 @@ __global__ void __launch_bounds__(MMA_THREADS, 1)
 #pragma unroll
         for (int p = 0; p < PARTS; ++p) {
           const int j0 = 64 * p + 32 * half;
+          if (j0 >= n) break;
           O* q = o + j0 * a.o_c;
 #pragma unroll
           for (int j = 0; j < 32; ++j) {
@@ -575,7 +575,7 @@ cudaError_t mma_launch(const grs_experts* s, const ExpLd& ld, const void* xs, co
   const int64_t step = MMA_F * kCtas;
   tiles *= (a.f + step - 1) / step;
   // Weights: a cluster for each tile, of which those that run take over the others' (ask_cluster).
-  const int64_t at_once = kP == Product::kWeights ? INT32_MAX / kCtas : 152 / kCtas;
+  const int64_t at_once = kP == Product::kWeights ? INT32_MAX / kCtas : S::PER_SM * 152 / kCtas;
   if (kP == Product::kWeights && tiles > at_once) return cudaErrorInvalidConfiguration;
   const unsigned grid = static_cast<unsigned>((tiles < at_once ? tiles : at_once) * kCtas);
   const cudaError_t e = allow_smem<exp_mma_kernel<kP, TC, kCtas, O>>(S::BYTES);
@@ -586,16 +586,13 @@ cudaError_t mma_launch(const grs_experts* s, const ExpLd& ld, const void* xs, co
 template <Product kP>
 cudaError_t mma_rows(const grs_experts* s, const ExpLd& ld, const void* xs, const void* w, const void* dys, const int32_t* offsets, void* o,
                      int64_t o_ld, void* stream) {
+  // Columns by the rows that an expert has in the mean.  2048 -> 768, 32 experts, us with 16, 64, 128 and 256 (two
+  // blocks): 20 rows 11.8, 13.7, -, -; 512 rows 19.8, 17.1, 21.3, -; 2048 rows 45, 24.0, 25.4, 29.1; 3000 rows -, 29.9,
+  // 25.8, 31.1; 4096 rows -, 30.6, 31.5, 30.7; 131072 rows, 256: 228.
   const int64_t mean = s->rows / s->experts;
   if (mean >= 128) return mma_launch<kP, 256, 2, uint16_t>(s, ld, xs, w, dys, offsets, o, o_ld, stream);
-#ifndef MEAN_64
-#define MEAN_64 64
-#endif
-#ifndef MEAN_16
-#define MEAN_16 16
-#endif
-  if (mean >= MEAN_64) return mma_launch<kP, 128, 1, uint16_t>(s, ld, xs, w, dys, offsets, o, o_ld, stream);
-  if (mean >= MEAN_16) return mma_launch<kP, 64, 1, uint16_t>(s, ld, xs, w, dys, offsets, o, o_ld, stream);
+  if (mean >= 64) return mma_launch<kP, 128, 1, uint16_t>(s, ld, xs, w, dys, offsets, o, o_ld, stream);
+  if (mean >= 16) return mma_launch<kP, 64, 1, uint16_t>(s, ld, xs, w, dys, offsets, o, o_ld, stream);
   return mma_launch<kP, 16, 1, uint16_t>(s, ld, xs, w, dys, offsets, o, o_ld, stream);
 }
 

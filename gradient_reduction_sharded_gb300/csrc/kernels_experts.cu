@@ -306,33 +306,50 @@ struct PadArgs {
   int32_t per[3];                    // chunks of a row
 };
 
+constexpr int PAD_EACH = 4;  // chunks of a thread, their loads on their way together
+
 __global__ void __launch_bounds__(EXP_THREADS) exp_pad_kernel(const __grid_constant__ PadArgs a) {
   pdl_wait();
   pdl_trigger();
-  const int64_t i = int64_t(blockIdx.x) * EXP_THREADS + threadIdx.x;
-  if (i >= a.chunks[3]) return;
-  const int m = i >= a.chunks[2] ? 2 : i >= a.chunks[1] ? 1 : 0;
-  const int64_t c = i - a.chunks[m], r = c <= UINT32_MAX ? static_cast<uint32_t>(c) / static_cast<uint32_t>(a.per[m]) : c / a.per[m];
-  const int64_t at = r * a.ld[m] + (c - r * a.per[m]) * 8, low = at & ~int64_t(7);
-  const uint16_t* p = a.from[m];
-  uint32_t w[8];
-  if (low + 16 <= a.end[m]) {
-    const uint4 x = __ldg(reinterpret_cast<const uint4*>(p + low)), y = __ldg(reinterpret_cast<const uint4*>(p + low) + 1);
-    w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
-    w[4] = y.x; w[5] = y.y; w[6] = y.z; w[7] = y.w;
-    const int shift = static_cast<int>(at - low);  // elements
+  const int64_t i0 = int64_t(blockIdx.x) * (EXP_THREADS * PAD_EACH) + threadIdx.x;
+  uint4 x[PAD_EACH], y[PAD_EACH];
+  int shift[PAD_EACH];  // elements
 #pragma unroll
-    for (int q = 0; q < 6; ++q) w[q] = (shift & 4) != 0 ? w[q + 2] : w[q];
+  for (int u = 0; u < PAD_EACH; ++u) {
+    const int64_t i = i0 + u * EXP_THREADS;
+    shift[u] = -1;
+    if (i >= a.chunks[3]) continue;
+    const int m = i >= a.chunks[2] ? 2 : i >= a.chunks[1] ? 1 : 0;
+    const int64_t c = i - a.chunks[m], r = c <= UINT32_MAX ? static_cast<uint32_t>(c) / static_cast<uint32_t>(a.per[m]) : c / a.per[m];
+    const int64_t at = r * a.ld[m] + (c - r * a.per[m]) * 8, low = at & ~int64_t(7);
+    const uint16_t* p = a.from[m];
+    if (low + 16 <= a.end[m]) {
+      shift[u] = static_cast<int>(at - low);
+      x[u] = __ldg(reinterpret_cast<const uint4*>(p + low));
+      y[u] = __ldg(reinterpret_cast<const uint4*>(p + low) + 1);
+    } else if (GRS_CHECK(at < a.end[m], exp_flags, SITE_EXP_ROW)) {
+      uint32_t w[4];
 #pragma unroll
-    for (int q = 0; q < 5; ++q) w[q] = (shift & 2) != 0 ? w[q + 1] : w[q];
-#pragma unroll
-    for (int q = 0; q < 4; ++q) w[q] = (shift & 1) != 0 ? __funnelshift_r(w[q], w[q + 1], 16) : w[q];
-  } else {
-#pragma unroll
-    for (int q = 0; q < 4; ++q)
-      w[q] = (at + 2 * q < a.end[m] ? uint32_t(__ldg(p + at + 2 * q)) : 0u) | (at + 2 * q + 1 < a.end[m] ? uint32_t(__ldg(p + at + 2 * q + 1)) << 16 : 0u);
+      for (int q = 0; q < 4; ++q)
+        w[q] = (at + 2 * q < a.end[m] ? uint32_t(__ldg(p + at + 2 * q)) : 0u) |
+               (at + 2 * q + 1 < a.end[m] ? uint32_t(__ldg(p + at + 2 * q + 1)) << 16 : 0u);
+      *reinterpret_cast<uint4*>(a.to[m] + c * 8) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
   }
-  if (GRS_CHECK(at < a.end[m], exp_flags, SITE_EXP_ROW)) *reinterpret_cast<uint4*>(a.to[m] + c * 8) = make_uint4(w[0], w[1], w[2], w[3]);
+#pragma unroll
+  for (int u = 0; u < PAD_EACH; ++u) {
+    if (shift[u] < 0) continue;
+    const int64_t i = i0 + u * EXP_THREADS;
+    const int m = i >= a.chunks[2] ? 2 : i >= a.chunks[1] ? 1 : 0;
+    uint32_t w[8] = {x[u].x, x[u].y, x[u].z, x[u].w, y[u].x, y[u].y, y[u].z, y[u].w};
+#pragma unroll
+    for (int q = 0; q < 6; ++q) w[q] = (shift[u] & 4) != 0 ? w[q + 2] : w[q];
+#pragma unroll
+    for (int q = 0; q < 5; ++q) w[q] = (shift[u] & 2) != 0 ? w[q + 1] : w[q];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) w[q] = (shift[u] & 1) != 0 ? __funnelshift_r(w[q], w[q + 1], 16) : w[q];
+    *reinterpret_cast<uint4*>(a.to[m] + (i - a.chunks[m]) * 8) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
 }
 
 int64_t round8(int64_t n) { return (n + 7) & ~int64_t(7); }
@@ -364,7 +381,7 @@ struct Pads {
   }
   cudaError_t run(void* stream) const {
     if (n == 0) return cudaSuccess;
-    const int64_t blocks = (a.chunks[3] + EXP_THREADS - 1) / EXP_THREADS;
+    const int64_t per = EXP_THREADS * PAD_EACH, blocks = (a.chunks[3] + per - 1) / per;
     if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
     return launch_pdl(exp_pad_kernel, dim3(static_cast<unsigned>(blocks)), dim3(EXP_THREADS), 0, stream, a);
   }

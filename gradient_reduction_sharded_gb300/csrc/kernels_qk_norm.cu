@@ -46,10 +46,15 @@ struct QkArgs {
   float eps, inv_d;
 };
 
+// kExact: to two units; otherwise, for results that are rounded to bf16, to
+// 2^-21 (a half step of bf16 is 2^-9).
+template <bool kExact>
 __device__ __forceinline__ float2 turn_of(int32_t position, uint64_t turns) {
   const uint64_t a = static_cast<uint64_t>(int64_t(position)) * turns + 0x80000000u;
+  const float half_turns = static_cast<float>(static_cast<int32_t>(a >> 32)) * 0x1p-31f;
   float2 cs;
-  sincospif(static_cast<float>(static_cast<int32_t>(a >> 32)) * 0x1p-31f, &cs.y, &cs.x);
+  if constexpr (kExact) sincospif(half_turns, &cs.y, &cs.x);
+  else __sincosf(half_turns * 3.14159265358979f, &cs.y, &cs.x);
   return cs;
 }
 
@@ -78,7 +83,7 @@ __device__ __forceinline__ void each(const QkArgs<T, P>& a, int64_t t, int lane,
   const int half = a.rot / 2;
   const int32_t pos = half > 0 && angles ? __ldg(a.positions + t) : 0;
   for (int p = lane; p < half; p += 32) {
-    const float2 cs = angles ? turn_of(pos, __ldg(a.turns + p)) : make_float2(1.0f, 0.0f);
+    const float2 cs = angles ? turn_of<true>(pos, __ldg(a.turns + p)) : make_float2(1.0f, 0.0f);
     const int i = a.pairs ? 2 * p : p, j = a.pairs ? 2 * p + 1 : p + half;
     f(i, j, cs.x, cs.y);
   }
@@ -187,49 +192,40 @@ __global__ void __launch_bounds__(QK_THREADS) qk_backward_kernel(const __grid_co
 // for all heads, and its lane groups take the heads in turn, the next head's
 // loads on their way while one is computed.
 constexpr int QK_MAX_UNITS = 32;       // 16-element units of a head
-constexpr int QK_FWD_ROUNDS = 6;       // heads of a lane group in a block, backward in a tile
-constexpr int QK_BWD_ROUNDS = 4;
-constexpr int QK_BWD_BLOCKS = 2;       // an SM
+// Measured, us (forward of 16384 tokens, 16 + 16 heads of 128; backward of 32 + 4 heads of 64): forward with 4, 6 and 12
+// heads of a group in a tile 49, 47.8, 48.8; backward with 4, 8 and 12 48.7, 44.6, 43.2, with three blocks an SM
+// (80 registers) and 8 48.5.
+constexpr int QK_FWD_ROUNDS = 6;       // heads of a lane group in a tile of tokens
+constexpr int QK_BWD_ROUNDS = 12;
+constexpr int QK_FWD_BLOCKS = 4;       // an SM
+constexpr int QK_BWD_BLOCKS = 2;
+constexpr int QK_FWD_DEPTH = 4;        // heads of a thread on their way
+template <typename T>
+constexpr int qk_bwd_depth = sizeof(T) == 2 ? 4 : 2;
 constexpr int QK_TABLE = 32 * 1024;    // bytes of sines and cosines at most
 constexpr int QK_MAX_TOKENS = 128;     // of a block
 constexpr int64_t QK_MAX_LD = 1 << 22; // elements between tokens: those of a block, and one step further, lie within 2^31
-constexpr int QK_BWD_SMEM = 2 * QK_TABLE + 2 * 64 * QK_MAX_UNITS + 2 * 64 * QK_THREADS;
 
 struct QkShape {
   int units, turned, lanes;  // units of a head, of them with a rotated part; lanes that share a head (a power of 2)
   int tokens;                // of a block
+  int slots;                 // lane groups of a block
+  int dt[2], dh[2];          // tokens and heads from one of a group's queries, keys, to its next
 };
 
-// 16 elements on their way: eight from i0, eight from i1 (zeros for -1).
-template <typename T>
-struct Raw {
-  static constexpr int N = sizeof(T) == 2 ? 1 : 2;  // 16-byte loads of 8 elements
-  uint4 c[2][N];
-  __device__ __forceinline__ void load(const T* p, int i0, int i1) {
-#pragma unroll
-    for (int k = 0; k < N; ++k) {
-      c[0][k] = i0 >= 0 ? __ldcs(reinterpret_cast<const uint4*>(p + i0) + k) : make_uint4(0, 0, 0, 0);
-      c[1][k] = i1 >= 0 ? __ldcs(reinterpret_cast<const uint4*>(p + i1) + k) : make_uint4(0, 0, 0, 0);
-    }
-  }
-  __device__ __forceinline__ void pairs(float2 (&o)[8]) const {
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      if constexpr (sizeof(T) == 2) {
-        o[4 * h] = bf16_pair(c[h][0].x);
-        o[4 * h + 1] = bf16_pair(c[h][0].y);
-        o[4 * h + 2] = bf16_pair(c[h][0].z);
-        o[4 * h + 3] = bf16_pair(c[h][0].w);
-      } else {
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          o[4 * h + 2 * k] = make_float2(__uint_as_float(c[h][k].x), __uint_as_float(c[h][k].y));
-          o[4 * h + 2 * k + 1] = make_float2(__uint_as_float(c[h][k].z), __uint_as_float(c[h][k].w));
-        }
-      }
-    }
-  }
-};
+__device__ __forceinline__ void copy16(uint32_t to, const void* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ uint4 shared16(uint32_t from) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(from) : "memory");
+  return v;
+}
 
 template <typename T>
 __device__ __forceinline__ void store_chunk(T* p, const float2* v) {
@@ -241,18 +237,21 @@ __device__ __forceinline__ void store_chunk(T* p, const float2* v) {
   }
 }
 
-// The lane's 16 elements: eight from i0, eight from i1 (-1: none), and whether these are turned.
+// The lane's 16 elements: eight from i0, eight from i1 (-1: none), and whether
+// these are turned.  Neighbouring lanes have neighbouring chunks in either half.
 template <bool kPairs>
 struct Unit {
   int i0, i1;
   bool r0, r1;
   __device__ __forceinline__ Unit(int u, int units, int d, int rot) {
+    const int halves = kPairs ? 0 : rot / 16, from = kPairs ? 0 : rot;  // units of two turned halves, and what comes behind them
     if (u >= units) {
       i0 = i1 = -1;
       r0 = r1 = false;
-    } else if (kPairs || u >= rot / 16) {
-      i0 = kPairs ? 16 * u : rot + 16 * (u - rot / 16);
-      i1 = i0 + 8 < d ? i0 + 8 : -1;
+    } else if (u >= halves) {
+      i0 = from + 8 * (u - halves);
+      i1 = i0 + 8 * (units - halves);
+      if (i1 >= d) i1 = -1;
       r0 = kPairs && i0 < rot;
       r1 = kPairs && i1 >= 0 && i1 < rot;
     } else {
@@ -261,10 +260,18 @@ struct Unit {
       r0 = r1 = true;
     }
   }
+  // Where angle p of a token is in the table: entry [q][u], its place there.
+  static __device__ __forceinline__ int angle_at(int p, int turned) {
+    if constexpr (kPairs) {
+      const int c = p / 4, h = c >= turned;
+      return ((2 * h + p % 4 / 2) * turned + c - h * turned) * 4 + p % 2;
+    }
+    return (p % 8 / 2 * turned + p / 8) * 4 + p % 2;
+  }
   // v turned by the unit's eight angles, or back: entry q has (cos, cos, sin, sin) of its angles 2 q and 2 q + 1.
   template <bool kBack>
   __device__ __forceinline__ void turn(float2 (&v)[8], const float4* table, int turned) const {
-    if (!r0) return;
+    if (!r0) return;  // (r1 without r0 there is not)
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       if (kPairs && q >= 2 && !r1) break;
@@ -306,33 +313,33 @@ __device__ __forceinline__ void qk_weights_to_smem(const QkArgs<T, P>& a, const 
 }
 // A thread's angles, the i-th with i = its number plus a multiple of the
 // block's threads: the first one's position can be asked for ahead.
-template <typename T, typename P>
+template <typename T, typename P, bool kPairs>
 struct Angles {
   const QkArgs<T, P>& a;
   const QkShape& s;
   int t, p;
   int32_t ahead = 0;
   __device__ __forceinline__ Angles(const QkArgs<T, P>& a_, const QkShape& s_) : a(a_), s(s_) {
-    const int all = s.turned * 8;
-    t = all > 0 ? threadIdx.x / all : 0;
-    p = threadIdx.x - t * all;
+    const int half = a.rot / 2;
+    t = half > 0 ? threadIdx.x / half : 0;
+    p = threadIdx.x - t * half;
   }
-  __device__ __forceinline__ bool first(int tokens) const { return s.turned > 0 && t < tokens && p < a.rot / 2; }
   __device__ __forceinline__ void ask(int64_t t0, int tokens) {
-    if (first(tokens)) ahead = __ldg(a.positions + t0 + t);
+    if (a.rot > 0 && t < tokens) ahead = __ldg(a.positions + t0 + t);
   }
   __device__ __forceinline__ void put(float* table, int ti, int pi, int32_t position) const {
-    const float2 cs = turn_of(position, __ldg(a.turns + pi));
-    float* o = table + ((ti * 4 + pi % 8 / 2) * s.turned + pi / 8) * 4 + pi % 2;
+    const float2 cs = turn_of<sizeof(T) == 4>(position, __ldg(a.turns + pi));
+    float* o = table + ti * 16 * s.turned + Unit<kPairs>::angle_at(pi, s.turned);
     o[0] = cs.x;
     o[2] = cs.y;
   }
   __device__ __forceinline__ void store(int64_t t0, int tokens, float* table) const {
-    if (first(tokens)) put(table, t, p, ahead);
-    const int all = s.turned * 8, n = tokens * all;
-    for (int i = threadIdx.x + QK_THREADS; i < n; i += QK_THREADS) {
-      const int ti = i / all, pi = i - ti * all;
-      if (pi < a.rot / 2) put(table, ti, pi, __ldg(a.positions + t0 + ti));
+    const int half = a.rot / 2;
+    if (half == 0) return;
+    if (t < tokens) put(table, t, p, ahead);
+    for (int i = threadIdx.x + QK_THREADS; i < tokens * half; i += QK_THREADS) {
+      const int ti = i / half, pi = i - ti * half;
+      put(table, ti, pi, __ldg(a.positions + t0 + ti));
     }
   }
 };
@@ -340,35 +347,145 @@ struct Angles {
 // A lane group's way through the heads of a block's tokens, queries or keys:
 // every slots-th, and where they lie in the inputs and in the outputs.
 struct Way {
-  int t, h, dt, dh, n;
-  int32_t x, y, dx, dy, wrap_x, wrap_y;  // of a block's first token; QK_MAX_LD keeps them in 32 bits
+  int t, h;
+  int32_t x, y;  // from the block's first token on; QK_MAX_LD keeps them in 32 bits
   template <typename T, typename P>
-  __device__ __forceinline__ Way(const QkArgs<T, P>& a, int w, int slot, int slots) : n(a.heads[w]) {
-    const int32_t ld_x = static_cast<int32_t>(a.ld_x[w]), ld_y = static_cast<int32_t>(a.ld_y[w]);
+  __device__ __forceinline__ Way(const QkArgs<T, P>& a, int w, int slot) {
+    const int n = a.heads[w];
     t = n > 0 ? slot / n : 0;
     h = slot - t * n;
-    dt = n > 0 ? slots / n : 0;
-    dh = slots - dt * n;
-    x = t * ld_x + h * a.d;
-    y = t * ld_y + h * a.d;
-    dx = dt * ld_x + dh * a.d;
-    dy = dt * ld_y + dh * a.d;
-    wrap_x = ld_x - n * a.d;
-    wrap_y = ld_y - n * a.d;
+    x = t * static_cast<int32_t>(a.ld_x[w]) + h * a.d;
+    y = t * static_cast<int32_t>(a.ld_y[w]) + h * a.d;
   }
-  __device__ __forceinline__ void step() {
-    t += dt;
-    h += dh;
-    x += dx;
-    y += dy;
+  template <typename T, typename P>
+  __device__ __forceinline__ void step(const QkArgs<T, P>& a, const QkShape& s, int w) {
+    const int n = a.heads[w], ld_x = static_cast<int32_t>(a.ld_x[w]), ld_y = static_cast<int32_t>(a.ld_y[w]);
+    t += s.dt[w];
+    h += s.dh[w];
+    x += s.dt[w] * ld_x + s.dh[w] * a.d;
+    y += s.dt[w] * ld_y + s.dh[w] * a.d;
     if (h >= n) {
       h -= n;
       ++t;
-      x += wrap_x;
-      y += wrap_y;
+      x += ld_x - n * a.d;
+      y += ld_y - n * a.d;
     }
   }
 };
+
+// The heads that a thread's copies are under way for: ahead of those that it
+// computes, in the same order (queries of a tile of tokens, keys, the next
+// tile), so that the memory is busy across all of these ends.  A thread copies
+// what it reads itself; what has no place in memory stays zeros.
+template <typename T, typename P, int kInputs, int kDepth>
+struct Stream {
+  static_assert((kDepth & (kDepth - 1)) == 0, "a power of two");
+  static constexpr int N = static_cast<int>(sizeof(T)) / 2;  // 16-byte pieces of 8 elements
+  static constexpr int PIECE = 16 * QK_THREADS, SLOT = kInputs * 2 * N * PIECE, BYTES = kDepth * SLOT;
+  const QkArgs<T, P>& a;
+  const QkShape& s;
+  uint32_t ring;    // [kDepth][input][half][piece][threads] of 16 bytes, this thread's
+  int64_t t0, end;  // of the tile, of the block's tokens
+  int slot, i0, i1, tokens, which, left, at;  // at: bytes into the ring
+  Way way;
+  const T *x, *dy;                     // of the tile's queries or keys
+  int n, dt, dh, dx, dy_, wrap_x, wrap_y;  // and the steps of their way
+
+  __device__ __forceinline__ Stream(const QkArgs<T, P>& a_, const QkShape& s_, uint4* ring_, int64_t first, int64_t end_, int slot_, int i0_, int i1_)
+      : a(a_), s(s_), ring(smem_addr(ring_ + threadIdx.x)), t0(first), end(end_), slot(slot_), i0(i0_), i1(i1_), which(-1), at(0), way(a_, 0, slot_) {
+#pragma unroll
+    for (int i = 0; i < BYTES / PIECE; ++i) ring_[i * QK_THREADS + threadIdx.x] = make_uint4(0, 0, 0, 0);
+    tokens = count(t0);
+    next_part();
+#pragma unroll
+    for (int i = 0; i < kDepth - 1; ++i) ask();
+  }
+  __device__ __forceinline__ int count(int64_t t) const { return t >= end ? 0 : end - t < s.tokens ? static_cast<int>(end - t) : s.tokens; }
+  __device__ __forceinline__ int rounds(int w, int of) const { return (of * a.heads[w] + s.slots - 1) / s.slots; }
+  __device__ __forceinline__ void next_part() {
+    if (tokens == 0) return;
+    do {
+      if (++which == 2) {
+        which = 0;
+        t0 += s.tokens;
+        tokens = count(t0);
+        if (tokens == 0) return;
+      }
+      left = rounds(which, tokens);
+    } while (left == 0);
+    const int32_t ld_x = static_cast<int32_t>(a.ld_x[which]), ld_y = static_cast<int32_t>(a.ld_y[which]);
+    way = Way(a, which, slot);
+    n = a.heads[which];
+    dt = s.dt[which];
+    dh = s.dh[which];
+    dx = dt * ld_x + dh * a.d;
+    dy_ = dt * ld_y + dh * a.d;
+    wrap_x = ld_x - n * a.d;
+    wrap_y = ld_y - n * a.d;
+    x = a.x[which] + t0 * a.ld_x[which];
+    if constexpr (kInputs == 2) dy = a.dy[which] + t0 * a.ld_y[which];
+  }
+  __device__ __forceinline__ void ask() {
+    if (tokens > 0) {
+      if (way.t < tokens) {
+        copy(ring + at, x + way.x);
+        if constexpr (kInputs == 2) copy(ring + at + 2 * N * PIECE, dy + way.y);
+      }
+      way.t += dt;
+      way.h += dh;
+      way.x += dx;
+      if constexpr (kInputs == 2) way.y += dy_;
+      if (way.h >= n) {
+        way.h -= n;
+        ++way.t;
+        way.x += wrap_x;
+        if constexpr (kInputs == 2) way.y += wrap_y;
+      }
+      if (--left == 0) next_part();
+    }
+    copies_commit();
+    at = (at + SLOT) & (BYTES - 1);
+  }
+  __device__ __forceinline__ void copy(uint32_t to, const T* from) const {
+    if (i0 >= 0)
+#pragma unroll
+      for (int k = 0; k < N; ++k) copy16(to + k * PIECE, reinterpret_cast<const uint4*>(from + i0) + k);
+    if (i1 >= 0)
+#pragma unroll
+      for (int k = 0; k < N; ++k) copy16(to + (N + k) * PIECE, reinterpret_cast<const uint4*>(from + i1) + k);
+  }
+  // The next head: asks for a later one, waits for this one's copies.
+  __device__ __forceinline__ uint32_t next() {
+    const uint32_t from = ring + ((at + SLOT) & (BYTES - 1));
+    ask();
+    copies_wait<kDepth - 1>();
+    return from;
+  }
+  template <int kInput>
+  static __device__ __forceinline__ void get(uint32_t from, float2 (&v)[8]) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int k = 0; k < N; ++k) {
+        const uint4 c = shared16(from + ((kInput * 2 + h) * N + k) * PIECE);
+        if constexpr (sizeof(T) == 2) {
+          v[4 * h] = bf16_pair(c.x);
+          v[4 * h + 1] = bf16_pair(c.y);
+          v[4 * h + 2] = bf16_pair(c.z);
+          v[4 * h + 3] = bf16_pair(c.w);
+        } else {
+          v[4 * h + 2 * k] = make_float2(__uint_as_float(c.x), __uint_as_float(c.y));
+          v[4 * h + 2 * k + 1] = make_float2(__uint_as_float(c.z), __uint_as_float(c.w));
+        }
+      }
+  }
+};
+
+// A block's tokens follow one another: [block_token(b), block_token(b + 1)).
+__device__ __forceinline__ int64_t block_token(int64_t tokens, unsigned b) {
+  const int64_t each = tokens / gridDim.x, more = tokens % gridDim.x;
+  return each * b + (more < b ? more : b);
+}
 
 __device__ __forceinline__ float squares_sum(const float2 (&v)[8]) {
   float2 s = mul2(v[0], v[0]);
@@ -377,99 +494,77 @@ __device__ __forceinline__ float squares_sum(const float2 (&v)[8]) {
   return s.x + s.y;
 }
 
-// The heads of one kind; `raw` holds the first one's elements, and at the end
-// those of the first of the keys (W = 0), whose way is `after`.
-template <int W, typename T, typename P, bool kPairs>
-__device__ __forceinline__ void qk_forward_heads(const QkArgs<T, P>& a, const QkShape& s, int64_t t0, int tokens, int slots, Way way,
-                                                 const Way& after, const Unit<kPairs>& unit, int u, const float4* table, const float4* weights,
-                                                 Raw<T>& raw) {
-  const int rounds = (tokens * a.heads[W] + slots - 1) / slots;  // whole warps stay together for the sums
-  const T* const x = a.x[W] + t0 * a.ld_x[W];
+// The heads of one kind of a block's tokens.
+template <int W, typename T, typename P, bool kPairs, typename S>
+__device__ __forceinline__ void qk_forward_heads(const QkArgs<T, P>& a, const QkShape& s, int64_t t0, int tokens, const Unit<kPairs>& unit, int u,
+                                                 const float4* table, const float4* weights, S& stream) {
+  const int rounds = stream.rounds(W, tokens);  // whole warps stay together for the sums
   T* const o = a.o[W] + t0 * a.ld_y[W];
+  Way way(a, W, stream.slot);
 #pragma unroll 1
   for (int r = 0; r < rounds; ++r) {
     float2 v[8];
-    raw.pairs(v);
-    const int t = way.t;
-    const int32_t y = way.y;
-    way.step();
-    if (r + 1 < rounds) {
-      if (way.t < tokens) raw.load(x + way.x, unit.i0, unit.i1);
-    } else if (W == 0 && after.n > 0 && after.t < tokens) {
-      raw.load(a.x[1] + t0 * a.ld_x[1] + after.x, unit.i0, unit.i1);
-    }
+    S::template get<0>(stream.next(), v);
     const float rs = rsqrtf(__fmaf_rn(lanes_sum(squares_sum(v), s.lanes), a.inv_d, a.eps));
-    if (t < tokens && unit.i0 >= 0 && GRS_CHECK(t >= 0 && y >= 0, qk_flags, SITE_QK_HEAD)) {
+    if (way.t < tokens && unit.i0 >= 0 && GRS_CHECK(way.h < a.heads[W], qk_flags, SITE_QK_HEAD)) {
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         const float4 k = weights[(W * 4 + q) * s.units + u];
         v[2 * q] = mul2(mul2(v[2 * q], both(rs)), make_float2(k.x, k.y));
         v[2 * q + 1] = mul2(mul2(v[2 * q + 1], both(rs)), make_float2(k.z, k.w));
       }
-      unit.template turn<false>(v, table + t * 4 * s.turned + u, s.turned);
-      store_chunk(o + y + unit.i0, v);
-      if (unit.i1 >= 0) store_chunk(o + y + unit.i1, v + 4);
+      unit.template turn<false>(v, table + way.t * 4 * s.turned + u, s.turned);
+      store_chunk(o + way.y + unit.i0, v);
+      if (unit.i1 >= 0) store_chunk(o + way.y + unit.i1, v + 4);
     }
+    way.step(a, s, W);
   }
 }
 
 template <typename T, typename P, bool kPairs>
-__global__ void __launch_bounds__(QK_THREADS) qk_forward_whole_kernel(const __grid_constant__ QkArgs<T, P> a, const __grid_constant__ QkShape s) {
+__global__ void __launch_bounds__(QK_THREADS, QK_FWD_BLOCKS) qk_forward_whole_kernel(const __grid_constant__ QkArgs<T, P> a, const __grid_constant__ QkShape s) {
   extern __shared__ float4 shared[];
-  float4 *table = shared, *weights = shared + s.tokens * 4 * s.turned;
+  const int entries = s.tokens * 4 * s.turned;  // of a table of angles; there are two
+  float4* weights = shared + 2 * entries;
   pdl_wait();
   pdl_trigger();
-  const int64_t t0 = int64_t(blockIdx.x) * s.tokens;
-  const int tokens = a.tokens - t0 < s.tokens ? static_cast<int>(a.tokens - t0) : s.tokens;
-  const int slot = threadIdx.x / s.lanes, u = threadIdx.x - slot * s.lanes, slots = QK_THREADS / s.lanes;
+  const int slot = threadIdx.x / s.lanes, u = threadIdx.x - slot * s.lanes;
   const Unit<kPairs> unit(u, s.units, a.d, a.rot);
-  Angles<T, P> angles(a, s);
-  angles.ask(t0, tokens);
-  const Way q(a, 0, slot, slots), k(a, 1, slot, slots);
-  Raw<T> raw;
-  raw.load(nullptr, -1, -1);
-  if (q.n > 0) {
-    if (q.t < tokens) raw.load(a.x[0] + t0 * a.ld_x[0] + q.x, unit.i0, unit.i1);
-  } else if (k.t < tokens) {
-    raw.load(a.x[1] + t0 * a.ld_x[1] + k.x, unit.i0, unit.i1);
-  }
+  const int64_t end = block_token(a.tokens, blockIdx.x + 1);
+  int64_t t0 = block_token(a.tokens, blockIdx.x);
+  Angles<T, P, kPairs> angles(a, s);
+  Stream<T, P, 1, QK_FWD_DEPTH> stream(a, s, reinterpret_cast<uint4*>(weights + 8 * s.units), t0, end, slot, unit.i0, unit.i1);
   qk_weights_to_smem<T, P, kPairs>(a, s, reinterpret_cast<float*>(weights));
-  angles.store(t0, tokens, reinterpret_cast<float*>(table));
-  __syncthreads();
-  qk_forward_heads<0>(a, s, t0, tokens, slots, q, k, unit, u, table, weights, raw);
-  qk_forward_heads<1>(a, s, t0, tokens, slots, k, k, unit, u, table, weights, raw);
+  angles.ask(t0, stream.count(t0));
+  for (int flip = 0; t0 < end; t0 += s.tokens, flip ^= 1) {
+    const int tokens = stream.count(t0);
+    float4* table = shared + flip * entries;
+    angles.store(t0, tokens, reinterpret_cast<float*>(table));
+    angles.ask(t0 + s.tokens, stream.count(t0 + s.tokens));
+    __syncthreads();  // (the other table is free: all are done with the tile before)
+    if (a.heads[0] > 0) qk_forward_heads<0>(a, s, t0, tokens, unit, u, table, weights, stream);
+    if (a.heads[1] > 0) qk_forward_heads<1>(a, s, t0, tokens, unit, u, table, weights, stream);
+  }
 }
 
 // Backward, likewise; dw: the lane's share of the weight's gradient.
-template <int W, typename T, typename P, bool kPairs>
-__device__ __forceinline__ void qk_backward_heads(const QkArgs<T, P>& a, const QkShape& s, int64_t t0, int tokens, int slots, Way way,
-                                                  const Way& after, const Unit<kPairs>& unit, int u, const float4* table,
-                                                  const float4* weights, Raw<T>& rx, Raw<T>& rg, float2 (&dw)[8]) {
-  const int rounds = (tokens * a.heads[W] + slots - 1) / slots;
-  const T *const px = a.x[W] + t0 * a.ld_x[W], *const pg = a.dy[W] + t0 * a.ld_y[W];
+template <int W, typename T, typename P, bool kPairs, typename S>
+__device__ __forceinline__ void qk_backward_heads(const QkArgs<T, P>& a, const QkShape& s, int64_t t0, int tokens, const Unit<kPairs>& unit, int u,
+                                                  const float4* table, const float4* weights, S& stream, float2 (&dw)[8]) {
+  const int rounds = stream.rounds(W, tokens);
   T* const o = a.o[W] != nullptr ? a.o[W] + t0 * a.ld_x[W] : nullptr;
+  Way way(a, W, stream.slot);
 #pragma unroll 1
   for (int r = 0; r < rounds; ++r) {
-    const int t = way.t;
-    const int32_t at = way.x;
-    const bool on = t < tokens && unit.i0 >= 0;
+    const bool on = way.t < tokens && unit.i0 >= 0;
     float2 x[8], g[8];
-    rx.pairs(x);
-    rg.pairs(g);
-    way.step();
-    if (r + 1 < rounds) {
-      if (way.t < tokens) {
-        rx.load(px + way.x, unit.i0, unit.i1);
-        rg.load(pg + way.y, unit.i0, unit.i1);
-      }
-    } else if (W == 0 && after.n > 0 && after.t < tokens) {
-      rx.load(a.x[1] + t0 * a.ld_x[1] + after.x, unit.i0, unit.i1);
-      rg.load(a.dy[1] + t0 * a.ld_y[1] + after.y, unit.i0, unit.i1);
-    }
+    const uint32_t from = stream.next();
+    S::template get<0>(from, x);
+    S::template get<1>(from, g);
     const float rs = rsqrtf(__fmaf_rn(lanes_sum(squares_sum(x), s.lanes), a.inv_d, a.eps));
     float2 dot = both(0.0f);
-    if (on && GRS_CHECK(t >= 0 && at >= 0, qk_flags, SITE_QK_HEAD)) {
-      unit.template turn<true>(g, table + t * 4 * s.turned + u, s.turned);
+    if (on && GRS_CHECK(way.h < a.heads[W], qk_flags, SITE_QK_HEAD)) {
+      unit.template turn<true>(g, table + way.t * 4 * s.turned + u, s.turned);
 #pragma unroll
       for (int q = 0; q < 8; ++q) {
         x[q] = mul2(x[q], both(rs));
@@ -488,9 +583,10 @@ __device__ __forceinline__ void qk_backward_heads(const QkArgs<T, P>& a, const Q
     if (on && o != nullptr) {
 #pragma unroll
       for (int q = 0; q < 8; ++q) x[q] = mul2(fma2(x[q], both(m), g[q]), both(rs));
-      store_chunk(o + at + unit.i0, x);
-      if (unit.i1 >= 0) store_chunk(o + at + unit.i1, x + 4);
+      store_chunk(o + way.x + unit.i0, x);
+      if (unit.i1 >= 0) store_chunk(o + way.x + unit.i1, x + 4);
     }
+    way.step(a, s, W);
   }
 }
 
@@ -519,46 +615,33 @@ __global__ void __launch_bounds__(QK_THREADS, QK_BWD_BLOCKS)
   float4 *weights = shared + 2 * entries, *parked = weights + 8 * s.units;
   pdl_wait();
   pdl_trigger();
-  const int slot = threadIdx.x / s.lanes, u = threadIdx.x - slot * s.lanes, slots = QK_THREADS / s.lanes;
+  const int slot = threadIdx.x / s.lanes, u = threadIdx.x - slot * s.lanes, slots = s.slots;
   const Unit<kPairs> unit(u, s.units, a.d, a.rot);
-  Angles<T, P> angles(a, s);
-  const Way q(a, 0, slot, slots), k(a, 1, slot, slots);
+  Angles<T, P, kPairs> angles(a, s);
+  const int64_t end = block_token(a.tokens, blockIdx.x + 1);
+  int64_t t0 = block_token(a.tokens, blockIdx.x);
+  Stream<T, P, 2, qk_bwd_depth<T>> stream(a, s, reinterpret_cast<uint4*>(parked + 8 * QK_THREADS), t0, end, slot, unit.i0, unit.i1);
   float2 dw[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) dw[i] = both(0.0f);
   park(parked, dw);
   park(parked + 4 * QK_THREADS, dw);
   qk_weights_to_smem<T, P, kPairs>(a, s, reinterpret_cast<float*>(weights));
-  const int64_t dt = int64_t(gridDim.x) * s.tokens;
-  int64_t t0 = int64_t(blockIdx.x) * s.tokens;
-  auto tokens_at = [&](int64_t t) { return t >= a.tokens ? 0 : a.tokens - t < s.tokens ? static_cast<int>(a.tokens - t) : s.tokens; };
-  angles.ask(t0, tokens_at(t0));
-  for (int flip = 0; t0 < a.tokens; t0 += dt, flip ^= 1) {
-    const int tokens = tokens_at(t0);
+  angles.ask(t0, stream.count(t0));
+  for (int flip = 0; t0 < end; t0 += s.tokens, flip ^= 1) {
+    const int tokens = stream.count(t0);
     float4* table = shared + flip * entries;
-    Raw<T> rx, rg;
-    rx.load(nullptr, -1, -1);
-    rg.load(nullptr, -1, -1);
-    if (q.n > 0) {
-      if (q.t < tokens) {
-        rx.load(a.x[0] + t0 * a.ld_x[0] + q.x, unit.i0, unit.i1);
-        rg.load(a.dy[0] + t0 * a.ld_y[0] + q.y, unit.i0, unit.i1);
-      }
-    } else if (k.t < tokens) {
-      rx.load(a.x[1] + t0 * a.ld_x[1] + k.x, unit.i0, unit.i1);
-      rg.load(a.dy[1] + t0 * a.ld_y[1] + k.y, unit.i0, unit.i1);
-    }
     angles.store(t0, tokens, reinterpret_cast<float*>(table));
-    angles.ask(t0 + dt, tokens_at(t0 + dt));
+    angles.ask(t0 + s.tokens, stream.count(t0 + s.tokens));
     __syncthreads();  // (the other table is free: all are done with the tile before)
-    if (q.n > 0) {
+    if (a.heads[0] > 0) {
       unpark(parked, dw);
-      qk_backward_heads<0>(a, s, t0, tokens, slots, q, k, unit, u, table, weights, rx, rg, dw);
+      qk_backward_heads<0>(a, s, t0, tokens, unit, u, table, weights, stream, dw);
       park(parked, dw);
     }
-    if (k.n > 0) {
+    if (a.heads[1] > 0) {
       unpark(parked + 4 * QK_THREADS, dw);
-      qk_backward_heads<1>(a, s, t0, tokens, slots, k, k, unit, u, table, weights, rx, rg, dw);
+      qk_backward_heads<1>(a, s, t0, tokens, unit, u, table, weights, stream, dw);
       park(parked + 4 * QK_THREADS, dw);
     }
   }
@@ -637,7 +720,7 @@ QkShape qk_shape(const grs_qk_norm* s, int rounds) {
   QkShape q;
   const int d = s->head_dim, r = s->rotary_dim;
   q.units = s->interleaved ? (d + 15) / 16 : r / 16 + (d - r + 15) / 16;
-  q.turned = (r + 15) / 16;
+  q.turned = s->interleaved ? (r > 0 ? q.units : 0) : r / 16;
   q.lanes = 1;
   while (q.lanes < q.units) q.lanes *= 2;
   // Tokens of a block: enough for `rounds` heads a lane group, as far as the table goes and every SM has blocks.
@@ -645,12 +728,48 @@ QkShape qk_shape(const grs_qk_norm* s, int rounds) {
   int64_t t = (rounds * slots + heads - 1) / heads;
   if (q.turned > 0 && t > QK_TABLE / (64 * q.turned)) t = QK_TABLE / (64 * q.turned);
   if (t > QK_MAX_TOKENS) t = QK_MAX_TOKENS;
-  if (t > s->tokens / (152 * 4)) t = s->tokens / (152 * 4);
   q.tokens = static_cast<int>(t < 1 ? 1 : t);
+  q.slots = static_cast<int>(slots);
+  for (int w = 0; w < 2; ++w) {
+    const int n = w == 0 ? s->q_heads : s->k_heads;
+    q.dt[w] = n > 0 ? q.slots / n : 0;
+    q.dh[w] = n > 0 ? q.slots - q.dt[w] * n : 0;
+  }
   return q;
 }
 
-int qk_smem(const QkShape& q) { return q.tokens * 64 * q.turned + 2 * 64 * q.units; }
+// Shared memory: tables of angles, weights, backward the parked shares, and the heads under way.
+template <typename T, typename P>
+int qk_forward_smem(const QkShape& q) {
+  return 2 * q.tokens * 64 * q.turned + 2 * 64 * q.units + Stream<T, P, 1, QK_FWD_DEPTH>::BYTES;
+}
+template <typename T, typename P>
+int qk_backward_smem(const QkShape& q) {
+  return 2 * q.tokens * 64 * q.turned + 2 * 64 * q.units + 2 * 64 * QK_THREADS + Stream<T, P, 2, qk_bwd_depth<T>>::BYTES;
+}
+
+template <typename T, typename P, bool kPairs>
+cudaError_t qk_forward_whole(const grs_qk_norm* s, const QkArgs<T, P>& a, void* stream) {
+  const QkShape q = qk_shape(s, QK_FWD_ROUNDS);
+  const int64_t blocks = s->tokens < QK_FWD_BLOCKS * 152 ? s->tokens : QK_FWD_BLOCKS * 152;
+  const QkShape most{QK_MAX_UNITS, 0, 0, 0, 0, {}, {}};
+  const cudaError_t e = allow_smem<qk_forward_whole_kernel<T, P, kPairs>>(2 * QK_TABLE + qk_forward_smem<T, P>(most));
+  if (e != cudaSuccess) return e;
+  return launch_pdl(qk_forward_whole_kernel<T, P, kPairs>, dim3(static_cast<unsigned>(blocks)), dim3(QK_THREADS), qk_forward_smem<T, P>(q),
+                    stream, a, q);
+}
+
+// *blocks: at most, and then how many it has.
+template <typename T, typename P, bool kPairs>
+cudaError_t qk_backward_whole(const grs_qk_norm* s, const QkArgs<T, P>& a, int* blocks, void* stream) {
+  const QkShape q = qk_shape(s, QK_BWD_ROUNDS);
+  if (*blocks > QK_BWD_BLOCKS * 152) *blocks = QK_BWD_BLOCKS * 152;
+  if (*blocks > s->tokens) *blocks = static_cast<int>(s->tokens);
+  const QkShape most{QK_MAX_UNITS, 0, 0, 0, 0, {}, {}};
+  const cudaError_t e = allow_smem<qk_backward_whole_kernel<T, P, kPairs>>(2 * QK_TABLE + qk_backward_smem<T, P>(most));
+  if (e != cudaSuccess) return e;
+  return launch_pdl(qk_backward_whole_kernel<T, P, kPairs>, dim3(*blocks), dim3(QK_THREADS), qk_backward_smem<T, P>(q), stream, a, q);
+}
 
 template <typename T, typename P>
 QkArgs<T, P> qk_args(const grs_qk_norm* s, const int64_t (&ld)[4], const void* dqo, const void* dko, const void* q, const void* k,
@@ -685,12 +804,7 @@ QkArgs<T, P> qk_args(const grs_qk_norm* s, const int64_t (&ld)[4], const void* d
 template <typename T, typename P>
 cudaError_t qk_forward(const grs_qk_norm* s, const int64_t (&ld)[4], const QkArgs<T, P>& a, void* stream) {
   if (qk_whole(s, ld, a.x[0], a.x[1], a.o[0], a.o[1], nullptr, nullptr)) {
-    const QkShape q = qk_shape(s, QK_FWD_ROUNDS);
-    const int64_t blocks = (s->tokens + q.tokens - 1) / q.tokens;
-    if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
-    const dim3 grid(static_cast<unsigned>(blocks)), block(QK_THREADS);
-    return s->interleaved ? launch_pdl(qk_forward_whole_kernel<T, P, true>, grid, block, qk_smem(q), stream, a, q)
-                          : launch_pdl(qk_forward_whole_kernel<T, P, false>, grid, block, qk_smem(q), stream, a, q);
+    return s->interleaved ? qk_forward_whole<T, P, true>(s, a, stream) : qk_forward_whole<T, P, false>(s, a, stream);
   }
   const int64_t blocks = (s->tokens * (s->q_heads + s->k_heads) + QK_WARPS - 1) / QK_WARPS;
   if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
@@ -702,15 +816,7 @@ cudaError_t qk_backward(const grs_qk_norm* s, const int64_t (&ld)[4], const QkAr
   int blocks = qk_blocks(s);
   cudaError_t e;
   if (qk_whole(s, ld, a.x[0], a.x[1], a.dy[0], a.dy[1], a.o[0], a.o[1])) {
-    const QkShape q = qk_shape(s, QK_BWD_ROUNDS);
-    const int64_t tiles = (s->tokens + q.tokens - 1) / q.tokens;
-    if (blocks > QK_BWD_BLOCKS * 152) blocks = QK_BWD_BLOCKS * 152;
-    if (blocks > tiles) blocks = static_cast<int>(tiles);
-    const int smem = qk_smem(q) + q.tokens * 64 * q.turned + 2 * 64 * QK_THREADS;  // a second table, the parked shares
-    e = s->interleaved ? allow_smem<qk_backward_whole_kernel<T, P, true>>(QK_BWD_SMEM) : allow_smem<qk_backward_whole_kernel<T, P, false>>(QK_BWD_SMEM);
-    if (e != cudaSuccess) return e;
-    e = s->interleaved ? launch_pdl(qk_backward_whole_kernel<T, P, true>, dim3(blocks), dim3(QK_THREADS), smem, stream, a, q)
-                       : launch_pdl(qk_backward_whole_kernel<T, P, false>, dim3(blocks), dim3(QK_THREADS), smem, stream, a, q);
+    e = s->interleaved ? qk_backward_whole<T, P, true>(s, a, &blocks, stream) : qk_backward_whole<T, P, false>(s, a, &blocks, stream);
   } else {
     e = allow_smem<qk_backward_kernel<T, P>>(QK_WARPS * 2 * GRS_QK_MAX_DIM * 4);
     if (e == cudaSuccess)

@@ -22,9 +22,30 @@ struct ExpLd {
   int64_t x, y, w;  // elements from one row to the next of xs and dxs, of ys and dys, of w
 };
 
+// Where a product has few tiles with a long k, k is cut into slices whose
+// results (fp32) are added up afterwards.
+struct ExpSlices {
+  int n = 1;
+  float* parts = nullptr;       // [n][rows of the result][ld]
+  int64_t ld = 0, distance = 0;  // of its rows, of the slices
+};
+
+// k of a slice: in 512s, so that the sections of an fp32 sum are whole ones.
+__host__ __device__ inline int32_t slice_length(int32_t k, int32_t slices) {
+  return static_cast<int32_t>(((int64_t(k) + slices - 1) / slices + 511) / 512 * 512 > INT32_MAX / 2 ? INT32_MAX / 2
+                                                                                              : ((int64_t(k) + slices - 1) / slices + 511) / 512 * 512);
+}
+
+// Tiles that a product in bf16 has at most, how many columns they have, and how long k is (in the mean).
+struct ExpTiles {
+  int columns;
+  int64_t n, k;
+};
+ExpTiles experts_mma_tiles(Product p, const grs_experts* s);
+
 // One product in bf16; xs, w and dys 16-byte aligned, the row distances of
 // those that it reads multiples of 8.  o_ld: of the result's rows.
 cudaError_t experts_mma(Product p, const grs_experts* s, const ExpLd& ld, const void* xs, const void* w, const void* dys,
-                        const int32_t* offsets, void* o, int64_t o_ld, void* stream);
+                        const int32_t* offsets, void* o, int64_t o_ld, const ExpSlices& slices, void* stream);
 
 }  // namespace grs

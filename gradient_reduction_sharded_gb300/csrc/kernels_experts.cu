@@ -35,9 +35,9 @@ struct GeneralArgs {
   const int32_t* offsets;
   int64_t a_f, a_k, a_e;  // distances in A of features, of k, of experts
   int64_t b_c, b_k;
-  int64_t o_c, o_e;
+  int64_t o_c, o_e, o_s;  // distances of c, of experts, of slices
   int64_t f, c, k;        // extents; c or k of an expert's own are its rows
-  int32_t rows, experts;
+  int32_t rows, experts, slices;
 };
 
 // One operand's next GK x N elements: where a thread's lie, on their way, and
@@ -101,12 +101,17 @@ __global__ void __launch_bounds__(EXP_THREADS, 2) exp_general_kernel(const __gri
   const int64_t ft = (p.f + GF - 1) / GF, ct = (p.c + GC - 1) / GC;
   const int64_t tiles = ft * (kWeights ? ct * p.experts : first[p.experts]);
   const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;  // features 4 tx.. and 64 + 4 tx.., c 4 ty..
-  for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
-    const int64_t ci = tile / ft, f0 = (tile - ci * ft) * GF;
+  for (int64_t i = blockIdx.x; i < tiles * p.slices; i += gridDim.x) {
+    const int64_t slice = i / tiles, tile = i - slice * tiles, ci = tile / ft, f0 = (tile - ci * ft) * GF;
     const int e = kWeights ? static_cast<int>(ci / ct) : expert_of(first, p.experts, ci);
     const ExpertRows r(p.offsets, e, p.rows);
     const int64_t c0 = kWeights ? (ci - e * ct) * GC : r.from + (ci - first[e]) * GC, c1 = kWeights ? p.c : r.to;
-    const int64_t k0 = kWeights ? r.from : 0, k1 = kWeights ? r.to : p.k;
+    int64_t k0 = kWeights ? r.from : 0, k1 = kWeights ? r.to : p.k;
+    if (p.slices > 1) {
+      const int64_t n = slice_length(static_cast<int32_t>(k1 - k0), p.slices);
+      k0 = k0 + slice * n < k1 ? k0 + slice * n : k1;
+      k1 = k1 - k0 < n ? k1 : k0 + n;
+    }
     const float *a = p.a + e * p.a_e, *b = p.b;
     float2 total[4][4], part[4][4];
 #pragma unroll
@@ -153,7 +158,7 @@ __global__ void __launch_bounds__(EXP_THREADS, 2) exp_general_kernel(const __gri
     for (int i = 0; i < 4; ++i) {
       const int64_t c = c0 + ty * 4 + i;
       if (c >= c1 || !GRS_CHECK(kWeights || c < p.rows, exp_flags, SITE_EXP_ROW)) continue;
-      O* o = p.o + e * p.o_e + c * p.o_c;
+      O* o = p.o + e * p.o_e + slice * p.o_s + c * p.o_c;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const float2 v = add2(total[i][j], part[i][j]);
@@ -260,15 +265,18 @@ grs_status check_experts(const grs_experts* s, const char* who, ExpLd* ld) {
 }
 
 template <Product kP, typename O>
-cudaError_t exp_general(const grs_experts* s, const ExpLd& ld, const void* a, const void* b, const int32_t* offsets, void* o, void* stream) {
+cudaError_t exp_general(const grs_experts* s, const ExpLd& ld, const void* a, const void* b, const int32_t* offsets, void* o,
+                        const ExpSlices& sl, void* stream) {
   const int64_t in = s->in_features, out = s->out_features;
   GeneralArgs<O> p{};
   p.a = static_cast<const float*>(a);
   p.b = static_cast<const float*>(b);
-  p.o = static_cast<O*>(o);
+  p.o = static_cast<O*>(sl.n > 1 ? static_cast<void*>(sl.parts) : o);
   p.offsets = offsets;
   p.rows = static_cast<int32_t>(s->rows);
   p.experts = s->experts;
+  p.slices = sl.n;
+  p.o_s = sl.distance;
   if (kP == Product::kForward) {  // A = w, B = xs
     p.a_f = in, p.a_k = 1, p.a_e = in * out, p.b_c = ld.x, p.b_k = 1, p.o_c = ld.y, p.f = out, p.k = in;
   } else if (kP == Product::kRows) {  // A = w, B = dys
@@ -276,13 +284,82 @@ cudaError_t exp_general(const grs_experts* s, const ExpLd& ld, const void* a, co
   } else {  // A = xs, B = dys
     p.a_f = 1, p.a_k = ld.x, p.b_c = 1, p.b_k = ld.y, p.o_c = in, p.o_e = in * out, p.f = in, p.c = out;
   }
+  if (sl.n > 1) p.o_c = sl.ld;
   return launch_pdl(exp_general_kernel<kP, O>, dim3(152 * 2), dim3(EXP_THREADS), 0, stream, p);
 }
 
+ExpTiles exp_general_tiles(Product p, const grs_experts* s) {
+  const int64_t in = s->in_features, out = s->out_features, least = s->rows < s->experts ? s->rows : s->experts;
+  auto up = [](int64_t n, int64_t to) { return (n + to - 1) / to; };
+  if (p == Product::kWeights) return {GC, s->experts * up(in, GF) * up(out, GC), s->rows / s->experts};
+  return {GC, (s->rows / GC + least) * up(p == Product::kForward ? out : in, GF), p == Product::kForward ? in : out};
+}
+
+// ------------------------------------------------------------------ slices
+// The sum of the slices' results, in their order.  With offsets only the
+// experts' rows; an expert without rows has no product, its slices are zeros.
+template <typename O>
+__global__ void __launch_bounds__(EXP_THREADS) exp_join_kernel(const float* __restrict__ parts, int32_t slices, int64_t distance, int64_t rows,
+                                                               int32_t width, O* o, int64_t ld, const int32_t* offsets, int32_t experts) {
+  pdl_wait();
+  pdl_trigger();
+  int64_t from = 0, to = rows;
+  if (offsets != nullptr) {
+    from = ExpertRows(offsets, 0, static_cast<int32_t>(rows)).from;
+    to = ExpertRows(offsets, experts - 1, static_cast<int32_t>(rows)).to;
+  }
+  for (int64_t i = from * width + int64_t(blockIdx.x) * EXP_THREADS + threadIdx.x; i < to * width; i += int64_t(gridDim.x) * EXP_THREADS) {
+    float s = 0.0f;
+#pragma unroll 4
+    for (int32_t k = 0; k < slices; ++k) s = __fadd_rn(s, __ldcs(parts + k * distance + i));
+    const int64_t r = i / width;
+    if (GRS_CHECK(r < rows, exp_flags, SITE_EXP_ROW)) o[r * ld + (i - r * width)] = from_float<O>(s);
+  }
+}
+
+// How a product is cut: as far as its tiles leave SMs without any, in slices
+// of 512 at least (1024 on the tensor cores).
+ExpSlices exp_slices(Product p, const grs_experts* s) {
+  const bool f = s->dtype == GRS_DTYPE_FP32;
+  const ExpTiles t = f ? exp_general_tiles(p, s) : experts_mma_tiles(p, s);
+  ExpSlices sl;
+  const int64_t slots = f ? 2 * 152 : t.columns == 256 ? 0 : t.columns <= 64 && p != Product::kWeights ? 2 * 152 : 152;
+  int64_t n = t.n > 0 ? slots / t.n : 0, most = t.k / (f ? 512 : 1024);
+  if (n > most) n = most;
+  if (n < 2) return sl;
+  sl.n = static_cast<int>(n);
+  sl.ld = p == Product::kForward ? s->out_features : s->in_features;
+  sl.distance = (p == Product::kWeights ? int64_t(s->experts) * s->out_features : s->rows) * sl.ld;
+  return sl;
+}
+
+int64_t slices_bytes(const ExpSlices& sl) { return sl.n > 1 ? sl.n * sl.distance * 4 : 0; }
+
+template <typename O>
+cudaError_t exp_join(Product p, const grs_experts* s, const ExpSlices& sl, const int32_t* offsets, void* o, int64_t ld, void* stream) {
+  const int64_t blocks = (sl.distance + EXP_THREADS - 1) / EXP_THREADS;
+  return launch_pdl(exp_join_kernel<O>, dim3(static_cast<unsigned>(blocks < 8 * 152 ? blocks : 8 * 152)), dim3(EXP_THREADS), 0, stream,
+                    static_cast<const float*>(sl.parts), sl.n, sl.distance, sl.distance / sl.ld, static_cast<int32_t>(sl.ld), static_cast<O*>(o), ld,
+                    p == Product::kWeights ? nullptr : offsets, s->experts);
+}
+
+// One product to `o`, rows o_ld apart; parts: room for its slices.
 template <Product kP>
-cudaError_t exp_general(const grs_experts* s, const ExpLd& ld, const void* a, const void* b, const int32_t* offsets, void* o, void* stream) {
-  if (kP == Product::kWeights && s->grad_dtype == GRS_DTYPE_BF16) return exp_general<kP, uint16_t>(s, ld, a, b, offsets, o, stream);
-  return exp_general<kP, float>(s, ld, a, b, offsets, o, stream);
+cudaError_t exp_product(const grs_experts* s, const ExpLd& ld, const void* xs, const void* w, const void* dys, const int32_t* offsets, void* o,
+                        int64_t o_ld, void* parts, void* stream) {
+  ExpSlices sl = exp_slices(kP, s);
+  sl.parts = static_cast<float*>(parts);
+  const bool fp32 = (kP == Product::kWeights ? s->grad_dtype : s->dtype) == GRS_DTYPE_FP32;
+  cudaError_t e;
+  if (s->dtype == GRS_DTYPE_BF16) {
+    e = experts_mma(kP, s, ld, xs, w, dys, offsets, o, o_ld, sl, stream);
+  } else {
+    const void *a = kP == Product::kWeights ? xs : w, *b = kP == Product::kForward ? xs : dys;
+    if (fp32 || sl.n > 1) e = exp_general<kP, float>(s, ld, a, b, offsets, o, sl, stream);
+    else e = exp_general<kP, uint16_t>(s, ld, a, b, offsets, o, sl, stream);
+  }
+  if (e != cudaSuccess || sl.n == 1) return e;
+  return fp32 ? exp_join<float>(kP, s, sl, offsets, o, o_ld, stream) : exp_join<uint16_t>(kP, s, sl, offsets, o, o_ld, stream);
 }
 
 // Whether forward is left to exp_few_kernel.
@@ -387,10 +464,17 @@ struct Pads {
   }
 };
 
-int64_t exp_workspace(const grs_experts* s, const ExpLd& ld) {
-  if (s->dtype == GRS_DTYPE_FP32) return 0;
-  return pad_bytes(s->rows, ld.x, s->in_features) + pad_bytes(s->rows, ld.y, s->out_features) +
-         pad_bytes(int64_t(s->experts) * s->out_features, ld.w, s->in_features);
+// The copies of operands, then the slices of one product after another.
+int64_t exp_workspace(const grs_experts* s, const ExpLd& ld, int64_t* pads) {
+  *pads = s->dtype == GRS_DTYPE_FP32 ? 0
+                                     : pad_bytes(s->rows, ld.x, s->in_features) + pad_bytes(s->rows, ld.y, s->out_features) +
+                                           pad_bytes(int64_t(s->experts) * s->out_features, ld.w, s->in_features);
+  int64_t most = 0;
+  for (Product p : {Product::kForward, Product::kRows, Product::kWeights}) {
+    const int64_t b = slices_bytes(exp_slices(p, s));
+    if (b > most) most = b;
+  }
+  return *pads + ((most + 15) & ~int64_t(15));
 }
 
 }  // namespace
@@ -420,7 +504,8 @@ grs_status grs_operators_check_device_errors(void* stream) {
 int64_t grs_experts_workspace_bytes(const grs_experts* s) {
   ExpLd ld;
   if (check_experts(s, "grs_experts_workspace_bytes", &ld) != GRS_OK) return -1;
-  return exp_workspace(s, ld);
+  int64_t pads;
+  return exp_workspace(s, ld, &pads);
 }
 
 grs_status grs_experts_forward(const grs_experts* s, const void* xs, const void* w, const int32_t* offsets, void* ys, void* workspace,
@@ -434,19 +519,21 @@ grs_status grs_experts_forward(const grs_experts* s, const void* xs, const void*
   if (!api_aligned(xs, 16) || !api_aligned(w, 16) || !api_aligned(offsets, 4) || !api_aligned(ys, dtype_size(s->dtype)) ||
       !api_aligned(workspace, 16))
     return api_fail(GRS_ERR_ALIGNMENT, who, "a misaligned pointer");
-  if (workspace == nullptr && exp_workspace(s, ld) > 0) return api_fail(GRS_ERR_INVALID_ARG, who, "these row distances need a workspace");
+  int64_t pad = 0;
+  if (workspace == nullptr && exp_workspace(s, ld, &pad) > 0) return api_fail(GRS_ERR_INVALID_ARG, who, "this shape needs a workspace");
   cudaError_t e = cudaSuccess;
-  if (s->dtype == GRS_DTYPE_FP32) {
-    e = exp_general<Product::kForward>(s, ld, w, xs, offsets, ys, stream);
-  } else if (exp_few(s, ld)) {
+  if (s->dtype == GRS_DTYPE_BF16 && exp_few(s, ld)) {
     e = exp_few_forward(s, ld, xs, w, offsets, ys, stream);
   } else {
+    exp_workspace(s, ld, &pad);
     const int64_t ld_y = ld.y;
-    Pads pads(workspace);
-    xs = pads.add(xs, s->rows, &ld.x, s->in_features);
-    w = pads.add(w, int64_t(s->experts) * s->out_features, &ld.w, s->in_features);
-    e = pads.run(stream);
-    if (e == cudaSuccess) e = experts_mma(Product::kForward, s, ld, xs, w, nullptr, offsets, ys, ld_y, stream);
+    if (s->dtype == GRS_DTYPE_BF16) {
+      Pads pads(workspace);
+      xs = pads.add(xs, s->rows, &ld.x, s->in_features);
+      w = pads.add(w, int64_t(s->experts) * s->out_features, &ld.w, s->in_features);
+      e = pads.run(stream);
+    }
+    if (e == cudaSuccess) e = exp_product<Product::kForward>(s, ld, xs, w, nullptr, offsets, ys, ld_y, static_cast<uint8_t*>(workspace) + pad, stream);
   }
   return e == cudaSuccess ? GRS_OK : api_cuda_fail(e, who);
 }
@@ -469,21 +556,21 @@ grs_status grs_experts_backward(const grs_experts* s, const void* dys, const voi
   if (offsets == nullptr || (dys == nullptr && (dxs != nullptr || dw != nullptr)) || (w == nullptr && dxs != nullptr) ||
       (xs == nullptr && dw != nullptr))
     return api_fail(GRS_ERR_INVALID_ARG, who, "NULL argument");
-  if (workspace == nullptr && exp_workspace(s, ld) > 0) return api_fail(GRS_ERR_INVALID_ARG, who, "these row distances need a workspace");
+  int64_t pad = 0;
+  if (exp_workspace(s, ld, &pad) > 0 && workspace == nullptr) return api_fail(GRS_ERR_INVALID_ARG, who, "this shape needs a workspace");
   cudaError_t e = cudaSuccess;
-  if (s->dtype == GRS_DTYPE_FP32) {
-    if (dxs != nullptr) e = exp_general<Product::kRows>(s, ld, w, dys, offsets, dxs, stream);
-    if (e == cudaSuccess && dw != nullptr) e = exp_general<Product::kWeights>(s, ld, xs, dys, offsets, dw, stream);
-  } else if (dxs != nullptr || dw != nullptr) {
+  if (dxs != nullptr || dw != nullptr) {
     const int64_t ld_x = ld.x;
-    Pads pads(workspace);
-    dys = pads.add(dys, s->rows, &ld.y, s->out_features);
-    if (dxs != nullptr) w = pads.add(w, int64_t(s->experts) * s->out_features, &ld.w, s->in_features);
-    if (dw != nullptr) xs = pads.add(xs, s->rows, &ld.x, s->in_features);
-    e = pads.run(stream);
-    if (e == cudaSuccess && dxs != nullptr) e = experts_mma(Product::kRows, s, ld, nullptr, w, dys, offsets, dxs, ld_x, stream);
-    if (e == cudaSuccess && dw != nullptr)
-      e = experts_mma(Product::kWeights, s, ld, xs, nullptr, dys, offsets, dw, s->in_features, stream);
+    uint8_t* parts = static_cast<uint8_t*>(workspace) + pad;
+    if (s->dtype == GRS_DTYPE_BF16) {
+      Pads pads(workspace);
+      dys = pads.add(dys, s->rows, &ld.y, s->out_features);
+      if (dxs != nullptr) w = pads.add(w, int64_t(s->experts) * s->out_features, &ld.w, s->in_features);
+      if (dw != nullptr) xs = pads.add(xs, s->rows, &ld.x, s->in_features);
+      e = pads.run(stream);
+    }
+    if (e == cudaSuccess && dxs != nullptr) e = exp_product<Product::kRows>(s, ld, nullptr, w, dys, offsets, dxs, ld_x, parts, stream);
+    if (e == cudaSuccess && dw != nullptr) e = exp_product<Product::kWeights>(s, ld, xs, nullptr, dys, offsets, dw, s->in_features, parts, stream);
   }
   return e == cudaSuccess ? GRS_OK : api_cuda_fail(e, who);
 }

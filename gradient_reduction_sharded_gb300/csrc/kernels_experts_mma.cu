@@ -68,14 +68,14 @@ template <typename O>
 struct MmaArgs {
   const int32_t* offsets;
   O* o;
-  int64_t o_c, o_e;        // elements from one c, one expert to the next
+  int64_t o_c, o_e, o_s;   // elements from one c, one expert, one slice to the next
   int64_t f, c, k;         // extents; an expert's rows in the place of c or k
-  int32_t rows, experts;
+  int32_t rows, experts, slices;
   int32_t words;           // two features' bf16 lie in an aligned word
 };
 
 struct Tile {
-  int32_t e, f0, fn, c0, c1, k0, k1;  // e < 0: no more; fn: features
+  int32_t e, f0, slice, c0, c1, k0, k1;  // e < 0: no more
 };
 
 template <Product kP, int TC, int kCtas>
@@ -83,33 +83,35 @@ struct Tiles {
   const int32_t* offsets;
   const int32_t* list;  // c tiles before each expert's; kWeights: the experts by size (NULL: as they come)
   int64_t f, c, k, ft, ct, total;
-  int32_t rows, step;   // step: features from one tile to the next
+  int32_t rows, slices;
   int at_e = 0;
 
   template <typename O>
   __device__ __forceinline__ Tiles(const MmaArgs<O>& a, const int32_t* list_)
-      : offsets(a.offsets), list(list_), f(a.f), c(a.c), k(a.k), rows(a.rows) {
-    step = MMA_F * kCtas;
-    ft = (f + step - 1) / step;
-    ct = (c + TC - 1) / TC;
-    total = kP == Product::kWeights ? ft * ct * a.experts : ft * list[a.experts];
+      : offsets(a.offsets), list(list_), f(a.f), c(a.c), k(a.k), rows(a.rows), slices(a.slices) {
+    ft = (f + MMA_F * kCtas - 1) / (MMA_F * kCtas);
+    ct = kP == Product::kWeights ? (c + TC - 1) / TC : list[a.experts];
+    total = kP == Product::kWeights ? ft * ct * slices * a.experts : ft * ct * slices;
   }
 
-  __device__ __forceinline__ Tile at(int64_t t) {  // ascending, unless kWeights
+  __device__ __forceinline__ Tile at(int64_t t) {
     Tile x;
     int64_t ci = t / ft, c0, c1;
-    x.f0 = static_cast<int32_t>((t - ci * ft) * step);
+    x.f0 = static_cast<int32_t>((t - ci * ft) * (MMA_F * kCtas));
+    const int64_t si = ci / ct;  // kWeights: the slices of an expert, c of each; otherwise c of all experts, slice by slice
+    ci -= si * ct;
     if constexpr (kP == Product::kWeights) {
-      const int64_t e = ci / ct;
-      ci -= e * ct;
-      x.e = list != nullptr ? list[e] : static_cast<int32_t>(e);
+      const int32_t e = static_cast<int32_t>(si / slices);
+      x.slice = static_cast<int32_t>(si - int64_t(e) * slices);
+      x.e = list != nullptr ? list[e] : e;
       c0 = ci * TC;
       c1 = c;
     } else {
+      x.slice = static_cast<int32_t>(si);
+      if (list[at_e] > ci) at_e = 0;
       while (list[at_e + 1] <= ci) ++at_e;
       x.e = at_e;
     }
-    x.fn = step;
     const ExpertRows r(offsets, x.e, rows);
     if constexpr (kP == Product::kWeights) {
       x.k0 = r.from;
@@ -119,6 +121,11 @@ struct Tiles {
       c1 = r.to;
       x.k0 = 0;
       x.k1 = static_cast<int32_t>(k);
+    }
+    if (slices > 1) {
+      const int32_t n = slice_length(x.k1 - x.k0, slices), from = x.k0;
+      x.k0 = x.k1 - from < int64_t(x.slice) * n ? x.k1 : from + x.slice * n;
+      if (x.k1 - x.k0 > n) x.k1 = x.k0 + n;
     }
     x.c0 = static_cast<int32_t>(c0);
     x.c1 = static_cast<int32_t>(c1 < c0 + TC ? c1 : c0 + TC);
@@ -243,7 +250,7 @@ __global__ void __launch_bounds__(MMA_THREADS, (Shape<TC, kCtas>::PER_SM))
     const int32_t v = lane < static_cast<int>(sizeof(Tile) / 4) ? r[lane] : 0;
     x.e = __shfl_sync(0xffffffffu, v, 0);
     x.f0 = __shfl_sync(0xffffffffu, v, 1);
-    x.fn = __shfl_sync(0xffffffffu, v, 2);
+    x.slice = __shfl_sync(0xffffffffu, v, 2);
     x.c0 = __shfl_sync(0xffffffffu, v, 3);
     x.c1 = __shfl_sync(0xffffffffu, v, 4);
     x.k0 = __shfl_sync(0xffffffffu, v, 5);
@@ -438,7 +445,7 @@ __global__ void __launch_bounds__(MMA_THREADS, (Shape<TC, kCtas>::PER_SM))
       const int32_t blocks = (x.k1 - x.k0 + MMA_K - 1) / MMA_K;
       const int64_t f = x.f0 + int64_t(rank) * MMA_F + quarter * 32 + lane;
       const int n = x.c1 - x.c0;
-      O* o = a.o + x.e * a.o_e + int64_t(x.c0) * a.o_c + f;
+      O* o = a.o + x.e * a.o_e + x.slice * a.o_s + int64_t(x.c0) * a.o_c + f;
       // (an even number of features less when a check fails: none, and the same parity)
       const int64_t rest = GRS_CHECK(kWeights || (x.c0 >= 0 && x.c1 <= a.rows), mma_flags, SITE_MMA_ROW) ? a.f - f : -2;
       const bool on = rest > 0;
@@ -496,7 +503,7 @@ __global__ void __launch_bounds__(MMA_THREADS, (Shape<TC, kCtas>::PER_SM))
             q += a.o_c;
           }
         }
-      } else if (kWeights && blocks == 0) {  // an expert without rows
+      } else if (blocks == 0) {  // an expert without rows, a slice without k
         if (on)
           for (int j = half; j < n; j += 2) o[j * a.o_c] = from_float<O>(0.0f);
         __syncwarp();
@@ -547,21 +554,23 @@ bool make_map(CUtensorMap* m, const void* p, int n, const int64_t (&dims)[3], co
 
 template <Product kP, int TC, int kCtas, typename O>
 cudaError_t mma_launch(const grs_experts* s, const ExpLd& ld, const void* xs, const void* w, const void* dys, const int32_t* offsets,
-                       void* o, int64_t o_ld, void* stream) {
+                       void* o, int64_t o_ld, const ExpSlices& sl, void* stream) {
   using S = Shape<TC, kCtas>;
   const int64_t in = s->in_features, out = s->out_features;
   CUtensorMap ma, mb;
   MmaArgs<O> a{};
   a.offsets = offsets;
-  a.o = static_cast<O*>(o);
-  a.o_c = o_ld;
+  a.slices = sl.n;
+  a.o = static_cast<O*>(sl.n > 1 ? static_cast<void*>(sl.parts) : o);
+  a.o_c = sl.n > 1 ? sl.ld : o_ld;
+  a.o_s = sl.distance;
   a.rows = static_cast<int32_t>(s->rows);
   a.experts = s->experts;
   bool fine;
   int64_t tiles;  // at most
   if constexpr (kP == Product::kWeights) {
     fine = make_map(&ma, xs, 2, {in, s->rows, 1}, {ld.x, 0}, 64) && make_map(&mb, dys, 2, {out, s->rows, 1}, {ld.y, 0}, 64);
-    a.f = in, a.c = out, a.o_e = out * o_ld;
+    a.f = in, a.c = out, a.o_e = out * a.o_c;
     tiles = s->experts * ((out + TC - 1) / TC);
   } else {
     constexpr bool fwd = kP == Product::kForward;
@@ -571,9 +580,9 @@ cudaError_t mma_launch(const grs_experts* s, const ExpLd& ld, const void* xs, co
     tiles = s->rows / TC + (s->rows < s->experts ? s->rows : s->experts);
   }
   if (!fine) return cudaErrorInvalidValue;
-  a.words = api_aligned(o, 4) && o_ld % 2 == 0 && a.o_e % 2 == 0;
+  a.words = api_aligned(o, 4) && a.o_c % 2 == 0 && a.o_e % 2 == 0;
   const int64_t step = MMA_F * kCtas;
-  tiles *= (a.f + step - 1) / step;
+  tiles *= (a.f + step - 1) / step * sl.n;
   // Weights: a cluster for each tile, of which those that run take over the others' (ask_cluster).
   const int64_t at_once = kP == Product::kWeights ? INT32_MAX / kCtas : S::PER_SM * 152 / kCtas;
   if (kP == Product::kWeights && tiles > at_once) return cudaErrorInvalidConfiguration;
@@ -583,36 +592,64 @@ cudaError_t mma_launch(const grs_experts* s, const ExpLd& ld, const void* xs, co
   return launch_pdl_cluster(exp_mma_kernel<kP, TC, kCtas, O>, kCtas, dim3(grid), dim3(MMA_THREADS), S::BYTES, stream, ma, mb, a);
 }
 
+template <Product kP, int TC>
+cudaError_t mma_narrow(const grs_experts* s, const ExpLd& ld, const void* xs, const void* w, const void* dys, const int32_t* offsets, void* o,
+                       int64_t o_ld, const ExpSlices& sl, void* stream) {
+  if (sl.n > 1) return mma_launch<kP, TC, 1, float>(s, ld, xs, w, dys, offsets, o, o_ld, sl, stream);
+  return mma_launch<kP, TC, 1, uint16_t>(s, ld, xs, w, dys, offsets, o, o_ld, sl, stream);
+}
+
 template <Product kP>
-cudaError_t mma_rows(const grs_experts* s, const ExpLd& ld, const void* xs, const void* w, const void* dys, const int32_t* offsets, void* o,
-                     int64_t o_ld, void* stream) {
-  // Columns by the rows that an expert has in the mean.  2048 -> 768, 32 experts, us with 16, 64, 128 and 256 (two
-  // blocks): 20 rows 11.8, 13.7, -, -; 512 rows 19.8, 17.1, 21.3, -; 2048 rows 45, 24.0, 25.4, 29.1; 3000 rows -, 29.9,
-  // 25.8, 31.1; 4096 rows -, 30.6, 31.5, 30.7; 131072 rows, 256: 228.
-  const int64_t mean = s->rows / s->experts;
-  if (mean >= 128) return mma_launch<kP, 256, 2, uint16_t>(s, ld, xs, w, dys, offsets, o, o_ld, stream);
-  if (mean >= 64) return mma_launch<kP, 128, 1, uint16_t>(s, ld, xs, w, dys, offsets, o, o_ld, stream);
-  if (mean >= 16) return mma_launch<kP, 64, 1, uint16_t>(s, ld, xs, w, dys, offsets, o, o_ld, stream);
-  return mma_launch<kP, 16, 1, uint16_t>(s, ld, xs, w, dys, offsets, o, o_ld, stream);
+cudaError_t mma_rows(int columns, const grs_experts* s, const ExpLd& ld, const void* xs, const void* w, const void* dys, const int32_t* offsets,
+                     void* o, int64_t o_ld, const ExpSlices& sl, void* stream) {
+  switch (columns) {
+    case 16: return mma_narrow<kP, 16>(s, ld, xs, w, dys, offsets, o, o_ld, sl, stream);
+    case 64: return mma_narrow<kP, 64>(s, ld, xs, w, dys, offsets, o, o_ld, sl, stream);
+    case 128: return mma_narrow<kP, 128>(s, ld, xs, w, dys, offsets, o, o_ld, sl, stream);
+    default: return mma_launch<kP, 256, 2, uint16_t>(s, ld, xs, w, dys, offsets, o, o_ld, sl, stream);
+  }
 }
 
 }  // namespace
 
 cudaError_t take_experts_mma_flags(int (&total)[FLAG_COUNT], cudaStream_t st) { return take_flags(mma_flags, total, st); }
 
-cudaError_t experts_mma(Product p, const grs_experts* s, const ExpLd& ld, const void* xs, const void* w, const void* dys,
-                        const int32_t* offsets, void* o, int64_t o_ld, void* stream) {
-  if (p == Product::kForward) return mma_rows<Product::kForward>(s, ld, xs, w, dys, offsets, o, o_ld, stream);
-  if (p == Product::kRows) return mma_rows<Product::kRows>(s, ld, xs, w, dys, offsets, o, o_ld, stream);
-  // Few large tiles are shared badly: 3000 rows, 12 experts, 1024 -> 520 (144 of them) 19.1 us, 16.1 in tiles a quarter as
-  // large; 16000 rows, 32 experts, 2048 -> 768 (768 of them) 58.5 and 65.4.
-  const int64_t large = int64_t(s->experts) * ((int64_t(s->in_features) + 255) / 256) * ((int64_t(s->out_features) + 255) / 256);
-  if (large < 4 * 76) {
-    if (s->grad_dtype == GRS_DTYPE_FP32) return mma_launch<Product::kWeights, 128, 1, float>(s, ld, xs, w, dys, offsets, o, o_ld, stream);
-    return mma_launch<Product::kWeights, 128, 1, uint16_t>(s, ld, xs, w, dys, offsets, o, o_ld, stream);
+ExpTiles experts_mma_tiles(Product p, const grs_experts* s) {
+  const int64_t in = s->in_features, out = s->out_features, least = s->rows < s->experts ? s->rows : s->experts;
+  auto up = [](int64_t n, int64_t to) { return (n + to - 1) / to; };
+  ExpTiles t;
+  if (p == Product::kWeights) {
+    // Few large tiles are shared badly: 3000 rows, 12 experts, 1024 -> 520 (144 of them) 19.1 us, 16.1 in tiles a quarter
+    // as large; 16000 rows, 32 experts, 2048 -> 768 (768 of them) 58.5 and 65.4.
+    const int64_t large = s->experts * up(in, 256) * up(out, 256);
+    t.columns = large < 4 * 76 ? 128 : 256;
+    t.n = t.columns == 256 ? large : s->experts * up(in, 128) * up(out, 128);
+    t.k = s->rows / s->experts;
+  } else {
+    // Columns by the rows that an expert has in the mean.  2048 -> 768, 32 experts, us with 16, 64, 128 and 256 (two
+    // blocks): 20 rows 11.8, 13.7, -, -; 512 rows 19.8, 17.1, 21.3, -; 2048 rows 45, 24.0, 25.4, 29.1; 3000 rows -, 29.9,
+    // 25.8, 31.1; 4096 rows -, 30.6, 31.5, 30.7; 131072 rows, 256: 228.
+    const int64_t f = p == Product::kForward ? out : in, mean = s->rows / s->experts;
+    const int64_t large = (s->rows / 256 + least) * up(f, 256);
+    t.columns = mean >= 128 && large >= 76 ? 256 : mean >= 64 ? 128 : mean >= 16 ? 64 : 16;
+    t.n = t.columns == 256 ? large : (s->rows / t.columns + least) * up(f, 128);
+    t.k = p == Product::kForward ? in : out;
   }
-  if (s->grad_dtype == GRS_DTYPE_FP32) return mma_launch<Product::kWeights, 256, 2, float>(s, ld, xs, w, dys, offsets, o, o_ld, stream);
-  return mma_launch<Product::kWeights, 256, 2, uint16_t>(s, ld, xs, w, dys, offsets, o, o_ld, stream);
+  return t;
+}
+
+cudaError_t experts_mma(Product p, const grs_experts* s, const ExpLd& ld, const void* xs, const void* w, const void* dys,
+                        const int32_t* offsets, void* o, int64_t o_ld, const ExpSlices& sl, void* stream) {
+  const int columns = experts_mma_tiles(p, s).columns;
+  if (p == Product::kForward) return mma_rows<Product::kForward>(columns, s, ld, xs, w, dys, offsets, o, o_ld, sl, stream);
+  if (p == Product::kRows) return mma_rows<Product::kRows>(columns, s, ld, xs, w, dys, offsets, o, o_ld, sl, stream);
+  const bool fp32 = s->grad_dtype == GRS_DTYPE_FP32 || sl.n > 1;
+  if (columns == 128) {
+    if (fp32) return mma_launch<Product::kWeights, 128, 1, float>(s, ld, xs, w, dys, offsets, o, o_ld, sl, stream);
+    return mma_launch<Product::kWeights, 128, 1, uint16_t>(s, ld, xs, w, dys, offsets, o, o_ld, sl, stream);
+  }
+  if (fp32) return mma_launch<Product::kWeights, 256, 2, float>(s, ld, xs, w, dys, offsets, o, o_ld, sl, stream);
+  return mma_launch<Product::kWeights, 256, 2, uint16_t>(s, ld, xs, w, dys, offsets, o, o_ld, sl, stream);
 }
 
 }  // namespace grs

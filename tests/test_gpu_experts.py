@@ -112,6 +112,13 @@ def test_a_large_expert_beside_small_ones():
     Case([5, 4097, 11, 0, 700], 776, 1032, "bf16", "fp32", tail=77).check()
 
 
+@pytest.mark.parametrize("counts, k, n", [([3], 8200, 64), ([20, 0, 1], 4100, 136), ([200], 16384, 8), ([5000, 3], 64, 40), ([20003], 8, 16),
+                                          ([0, 9000, 0], 72, 24), ([100, 300], 33, 9000), ([1500, 4], 2056, 2056)])
+@pytest.mark.parametrize("act, grad", [("bf16", "bf16"), ("bf16", "fp32"), ("fp32", "fp32"), ("fp32", "bf16")])
+def test_a_long_k_with_few_tiles(counts, k, n, act, grad):
+    Case(counts, k, n, act, grad, first=1, tail=3).check()
+
+
 def test_offsets_outside_the_rows_are_taken_as_the_nearest():
     c = Case([40, 20, 30], 64, 64)
     want = c.forward()

@@ -24,9 +24,14 @@ __device__ int exp_flags[FLAG_COUNT];
 
 // --------------------------------------------------------- fp32, any size
 // A block has 128 features of 64 c, a thread eight by four, as pairs of
-// neighbouring features; the next 16 of k are on their way while these are
-// multiplied.
-constexpr int GF = 128, GC = 64, GK = 16;
+// neighbouring features.  Operands come by copies of single numbers, which
+// turns either layout into [k][feature or c]; three steps of 16 of k are on
+// their way while one is multiplied (with one ahead a step took as long as the
+// memory's answer).  3000 rows, 8 experts, 1024 -> 1024: forward 224 us, rows'
+// gradients 215, weights' gradients 181 (28 to 35 TFLOP/s), bound by shared
+// memory and instruction issue together.
+constexpr int GF = 128, GC = 64, GK = 16, G_AHEAD = 4;
+constexpr int G_SMEM = G_AHEAD * GK * (GC + 4) * 4;  // the c operand's stages
 
 template <typename O>
 struct GeneralArgs {
@@ -40,20 +45,22 @@ struct GeneralArgs {
   int32_t rows, experts, slices;
 };
 
-// One operand's next GK x N elements: where a thread's lie, on their way, and
-// into shared memory as [k][N].  Neighbouring threads along what lies next to
-// one another.
+__device__ __forceinline__ void copy_number(uint32_t to, const float* from, bool there) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to), "l"(from), "r"(there ? 4 : 0) : "memory");
+}
+
+// One operand's next GK x N elements: where a thread's lie and go.
+// Neighbouring threads along what lies next to one another.
 template <int N>
 struct Panel {
-  static constexpr int EACH = N * GK / EXP_THREADS;
-  const float* p;      // the thread's first element of the next step
-  int64_t next;        // elements to its next one
-  int64_t step;        // to the next step's
-  int32_t k, dk;       // of its first element, of its next ones
-  uint32_t on;         // which of its elements exist along N
-  int32_t at, dat;     // in shared memory
-  float v[EACH];
-  __device__ __forceinline__ Panel(const float* base, int64_t n0, int64_t n1, int64_t k0, int64_t ld_n, int64_t ld_k) {
+  static constexpr int EACH = N * GK / EXP_THREADS, STAGE = GK * (N + 4) * 4;
+  const float *p, *none;  // the thread's first element of the next step; an address for what is not there
+  int64_t next;           // elements to its next one
+  int64_t step;           // to the next step's
+  int32_t k, dk;          // of its first element, of its next ones
+  uint32_t on;            // which of its elements exist along N
+  uint32_t at, dat;       // in shared memory
+  __device__ __forceinline__ Panel(const float* base, int64_t n0, int64_t n1, int64_t k0, int64_t ld_n, int64_t ld_k, uint32_t shared) : none(base) {
     const bool along_k = ld_k == 1;
     constexpr int PER_K = EXP_THREADS / GK, PER_N = EXP_THREADS / N;  // between a thread's elements: in N, in k
     const int tk = along_k ? threadIdx.x % GK : threadIdx.x / N, tn = along_k ? threadIdx.x / GK : threadIdx.x % N;
@@ -63,25 +70,22 @@ struct Panel {
     dk = along_k ? 0 : PER_N;
     next = along_k ? PER_K * ld_n : PER_N * ld_k;
     step = GK * ld_k;
-    at = tk * (N + 4) + tn;
-    dat = along_k ? PER_K : PER_N * (N + 4);
+    at = shared + (tk * (N + 4) + tn) * 4;
+    dat = (along_k ? PER_K : PER_N * (N + 4)) * 4;
     on = 0;
 #pragma unroll
     for (int j = 0; j < EACH; ++j) on |= uint32_t(n0 + tn + j * dn < n1) << j;
   }
-  // The step whose first k has `rest` left.
-  __device__ __forceinline__ void load(int64_t rest) {
+  // The step whose first k has `rest` left, to a stage; what is not there becomes zeros.
+  __device__ __forceinline__ void load(int64_t rest, int stage) {
     const float* q = p;
 #pragma unroll
     for (int j = 0; j < EACH; ++j) {
-      v[j] = (on >> j & 1) != 0 && k + j * dk < rest ? __ldg(q) : 0.0f;
+      const bool there = (on >> j & 1) != 0 && k + j * dk < rest;
+      copy_number(at + stage * STAGE + j * dat, there ? q : none, there);
       q += next;
     }
     p += step;
-  }
-  __device__ __forceinline__ void store(float* s) const {
-#pragma unroll
-    for (int j = 0; j < EACH; ++j) s[at + j * dat] = v[j];
   }
 };
 
@@ -90,7 +94,9 @@ struct Panel {
 template <Product kP, typename O>
 __global__ void __launch_bounds__(EXP_THREADS, 2) exp_general_kernel(const __grid_constant__ GeneralArgs<O> p) {
   constexpr bool kWeights = kP == Product::kWeights;
-  __shared__ __align__(16) float as[2][GK][GF + 4], bs[2][GK][GC + 4];
+  __shared__ __align__(16) float as[G_AHEAD][GK][GF + 4];
+  extern __shared__ __align__(16) float bs_[];
+  float(*bs)[GK][GC + 4] = reinterpret_cast<float(*)[GK][GC + 4]>(bs_);
   __shared__ int32_t first[GRS_MOE_MAX_EXPERTS + 1];
   pdl_wait();
   pdl_trigger();
@@ -113,36 +119,37 @@ __global__ void __launch_bounds__(EXP_THREADS, 2) exp_general_kernel(const __gri
       k1 = k1 - k0 < n ? k1 : k0 + n;
     }
     const float *a = p.a + e * p.a_e, *b = p.b;
-    float2 total[4][4], part[4][4];
+    uint64_t total[4][4] = {}, part[4][4] = {};
+    Panel<GF> pa(a, f0, p.f, k0, p.a_f, p.a_k, smem_addr(as));
+    Panel<GC> pb(b, c0, c1, k0, p.b_c, p.b_k, smem_addr(bs_));
+    int64_t rest = k1 - k0;  // of k, from the next step to be asked for
+    auto ask = [&](int stage) {
+      if (rest > 0) {
+        pa.load(rest, stage);
+        pb.load(rest, stage);
+      }
+      rest -= GK;
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) total[i][j] = part[i][j] = both(0.0f);
-    Panel<GF> pa(a, f0, p.f, k0, p.a_f, p.a_k);
-    Panel<GC> pb(b, c0, c1, k0, p.b_c, p.b_k);
-    pa.load(k1 - k0);
-    pb.load(k1 - k0);
+    for (int i = 0; i < G_AHEAD - 1; ++i) ask(i);
     int step = 0;
     for (int64_t k = k0; k < k1; k += GK, ++step) {
-      float(&sa)[GK][GF + 4] = as[step & 1];
-      float(&sb)[GK][GC + 4] = bs[step & 1];
-      pa.store(&sa[0][0]);
-      pb.store(&sb[0][0]);
-      __syncthreads();  // (the other half: all are done with it before they come here again)
-      if (k + GK < k1) {
-        pa.load(k1 - k - GK);
-        pb.load(k1 - k - GK);
-      }
+      asm volatile("cp.async.wait_group %0;" ::"n"(G_AHEAD - 2) : "memory");
+      __syncthreads();  // all have this step's copies, and are done with the stage that is asked for next
+      ask((step + G_AHEAD - 1) % G_AHEAD);
+      float(&sa)[GK][GF + 4] = as[step % G_AHEAD];
+      float(&sb)[GK][GC + 4] = bs[step % G_AHEAD];
 #pragma unroll
       for (int q = 0; q < GK; ++q) {
-        const float4 u = *reinterpret_cast<const float4*>(&sa[q][4 * tx]), v = *reinterpret_cast<const float4*>(&sa[q][64 + 4 * tx]);
+        const ulonglong2 u = *reinterpret_cast<const ulonglong2*>(&sa[q][4 * tx]), v = *reinterpret_cast<const ulonglong2*>(&sa[q][64 + 4 * tx]);
         const float4 c = *reinterpret_cast<const float4*>(&sb[q][4 * ty]);
-        const float2 x[4] = {make_float2(u.x, u.y), make_float2(u.z, u.w), make_float2(v.x, v.y), make_float2(v.z, v.w)};
-        const float y[4] = {c.x, c.y, c.z, c.w};
+        const uint64_t x[4] = {u.x, u.y, v.x, v.y};
+        const uint64_t y[4] = {pair_bits(both(c.x)), pair_bits(both(c.y)), pair_bits(both(c.z)), pair_bits(both(c.w))};
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) part[i][j] = fma2(x[j], both(y[i]), part[i][j]);
+          for (int j = 0; j < 4; ++j) part[i][j] = fma2(x[j], y[i], part[i][j]);
       }
       if (step % 4 == 3)
 #pragma unroll
@@ -150,10 +157,10 @@ __global__ void __launch_bounds__(EXP_THREADS, 2) exp_general_kernel(const __gri
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             total[i][j] = add2(total[i][j], part[i][j]);
-            part[i][j] = both(0.0f);
+            part[i][j] = 0;
           }
     }
-    __syncthreads();  // the panels may still be read
+    __syncthreads();  // the stages may still be read
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int64_t c = c0 + ty * 4 + i;
@@ -161,7 +168,7 @@ __global__ void __launch_bounds__(EXP_THREADS, 2) exp_general_kernel(const __gri
       O* o = p.o + e * p.o_e + slice * p.o_s + c * p.o_c;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const float2 v = add2(total[i][j], part[i][j]);
+        const float2 v = pair_floats(add2(total[i][j], part[i][j]));
         const int64_t f = f0 + (j < 2 ? 4 * tx + 2 * j : 64 + 4 * tx + 2 * (j - 2));
         if (f < p.f) o[f] = from_float<O>(v.x);
         if (f + 1 < p.f) o[f + 1] = from_float<O>(v.y);
@@ -285,7 +292,9 @@ cudaError_t exp_general(const grs_experts* s, const ExpLd& ld, const void* a, co
     p.a_f = 1, p.a_k = ld.x, p.b_c = 1, p.b_k = ld.y, p.o_c = in, p.o_e = in * out, p.f = in, p.c = out;
   }
   if (sl.n > 1) p.o_c = sl.ld;
-  return launch_pdl(exp_general_kernel<kP, O>, dim3(152 * 2), dim3(EXP_THREADS), 0, stream, p);
+  const cudaError_t e = allow_smem<exp_general_kernel<kP, O>>(G_SMEM);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(exp_general_kernel<kP, O>, dim3(152 * 2), dim3(EXP_THREADS), G_SMEM, stream, p);
 }
 
 ExpTiles exp_general_tiles(Product p, const grs_experts* s) {

@@ -37,6 +37,24 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
   return pair_floats(r);
 }
 
+// The same on pairs that stay in their register pair: what is kept from one
+// instruction to the next as two floats may cost moves in between.
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
 __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 
 // The product rounded by itself, whatever is added to it.  The assembler

@@ -12,8 +12,8 @@ of y - target.  Its parameters show three owners:
   up, down        LOCAL_SHARD   a tp rank holds half of the experts and sorts
                                 the tokens that go to them
 
-A step: grs_layernorm_forward, grs_moe_sort / dispatch, the experts' products
-(torch), grs_moe_combine; the same back; grs_reduce_all by owner and
+A step: grs_layernorm_forward, grs_moe_sort / dispatch, grs_experts_forward,
+grs_moe_combine; the same back; grs_reduce_all by owner and
 grs_grad_norm_sq on the plan; grs_tensors_adamw8_step (or adamw_step) over the
 plan's arrays; grs_gather_params.
 
@@ -118,27 +118,31 @@ class Job:
         grs.grs_plan_destroy(self.plan)
 
 
-def experts_forward(p, t, offsets, xs):
-    """The products of tp rank t's experts on their rows (offsets: host list)."""
-    mid = torch.zeros(xs.shape[0], FFN, dtype=torch.bfloat16, device="cuda")
-    ys = torch.zeros_like(xs)
-    for e in range(LOCAL):
-        rows = slice(offsets[e], offsets[e + 1])
-        mid[rows] = torch.relu(xs[rows] @ p["up"][t * LOCAL + e].T)
-        ys[rows] = mid[rows] @ p["down"][t * LOCAL + e].T
-    return mid, ys
+class Experts:
+    """The products of tp rank t's experts on their rows; nothing waits for the offsets on the host."""
 
+    def __init__(self, p, t, rows, stream):
+        bf16 = grs.GRS_DTYPE_BF16
+        self.up, self.down = (grs.make_experts(rows, LOCAL, a, b, bf16, bf16) for a, b in ((HIDDEN, FFN), (FFN, HIDDEN)))
+        size = max(grs.grs_experts_workspace_bytes(self.up), grs.grs_experts_workspace_bytes(self.down), 16)
+        self.ws = torch.empty(size, dtype=torch.uint8, device="cuda")
+        self.w_up, self.w_down = (p[k][t * LOCAL:(t + 1) * LOCAL] for k in ("up", "down"))
+        self.stream = stream
 
-def experts_backward(p, t, offsets, xs, mid, dys, d_up, d_down):
-    """Gradients of the experts' weights (into the rank's buffer) and of their rows."""
-    dxs = torch.zeros_like(xs)
-    for e in range(LOCAL):
-        rows = slice(offsets[e], offsets[e + 1])
-        d_down[e] = dys[rows].T @ mid[rows]
-        d_mid = (dys[rows] @ p["down"][t * LOCAL + e]) * (mid[rows] > 0)
-        d_up[e] = d_mid.T @ xs[rows]
-        dxs[rows] = d_mid @ p["up"][t * LOCAL + e]
-    return dxs
+    def forward(self, offsets, xs):
+        mid, ys = torch.zeros(xs.shape[0], FFN, dtype=torch.bfloat16, device="cuda"), torch.zeros_like(xs)
+        grs.grs_experts_forward(self.up, ptr(xs), ptr(self.w_up), ptr(offsets), ptr(mid), ptr(self.ws), self.stream)
+        mid.relu_()
+        grs.grs_experts_forward(self.down, ptr(mid), ptr(self.w_down), ptr(offsets), ptr(ys), ptr(self.ws), self.stream)
+        return mid, ys
+
+    def backward(self, offsets, xs, mid, dys, d_up, d_down):
+        """Gradients of the weights (into the rank's buffer) and of the rows."""
+        d_mid, dxs = torch.zeros_like(mid), torch.zeros_like(xs)
+        grs.grs_experts_backward(self.down, ptr(dys), ptr(mid), ptr(self.w_down), ptr(offsets), ptr(d_mid), ptr(d_down), ptr(self.ws), self.stream)
+        d_mid *= mid > 0
+        grs.grs_experts_backward(self.up, ptr(d_mid), ptr(xs), ptr(self.w_up), ptr(offsets), ptr(dxs), ptr(d_up), ptr(self.ws), self.stream)
+        return dxs
 
 
 def forward_backward(job: Job, dp: int, x: torch.Tensor, target: torch.Tensor) -> torch.Tensor:
@@ -171,23 +175,23 @@ def forward_backward(job: Job, dp: int, x: torch.Tensor, target: torch.Tensor) -
         grs.grs_moe_sort(moe, ptr(ids), ptr(offsets), ptr(row_slot), ptr(slot_row), ptr(ws), st)
         xs = torch.zeros(n, HIDDEN, dtype=torch.bfloat16, device=dev)
         grs.grs_moe_dispatch(moe, ptr(h), ptr(slot_row), ptr(xs), st)
-        off = offsets.tolist()
-        mid, ys = experts_forward(p, t, off, xs)
+        experts = Experts(p, t, n, st)
+        mid, ys = experts.forward(offsets, xs)
         out = torch.empty(TOKENS, HIDDEN, dtype=torch.bfloat16, device=dev)
         grs.grs_moe_combine(moe, ptr(ys), ptr(slot_row), ptr(weights), ptr(out), st)
         y += out.float()
-        kept.append((moe, off, slot_row, xs, mid, ys))
+        kept.append((moe, experts, offsets, slot_row, xs, mid, ys))
     diff = y - target.float()
     loss = diff.square().mean()
     dy = (diff * (2.0 / diff.numel())).to(torch.bfloat16)
     # Back.
     dh = torch.zeros(TOKENS, HIDDEN, device=dev)
     dweights = torch.zeros(TOKENS, TOP_K, device=dev)
-    for t, (moe, off, slot_row, xs, mid, ys) in enumerate(kept):
+    for t, (moe, experts, offsets, slot_row, xs, mid, ys) in enumerate(kept):
         rank = dp * TP + t
         dys, dw = torch.zeros_like(ys), torch.empty(TOKENS, TOP_K, device=dev)
         grs.grs_moe_combine_backward(moe, ptr(dy), ptr(ys), ptr(slot_row), ptr(weights), ptr(dys), ptr(dw), st)
-        dxs = experts_backward(p, t, off, xs, mid, dys, job.grad(rank, "up").view(LOCAL, FFN, HIDDEN), job.grad(rank, "down").view(LOCAL, HIDDEN, FFN))
+        dxs = experts.backward(offsets, xs, mid, dys, job.grad(rank, "up"), job.grad(rank, "down"))
         part = torch.empty(TOKENS, HIDDEN, dtype=torch.bfloat16, device=dev)
         grs.grs_moe_dispatch_backward(moe, ptr(dxs), ptr(slot_row), ptr(part), st)
         dh += part.float()

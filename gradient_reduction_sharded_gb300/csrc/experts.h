@@ -31,10 +31,7 @@ struct ExpSlices {
 };
 
 // k of a slice: in 512s, so that the sections of an fp32 sum are whole ones.
-__host__ __device__ inline int32_t slice_length(int32_t k, int32_t slices) {
-  return static_cast<int32_t>(((int64_t(k) + slices - 1) / slices + 511) / 512 * 512 > INT32_MAX / 2 ? INT32_MAX / 2
-                                                                                              : ((int64_t(k) + slices - 1) / slices + 511) / 512 * 512);
-}
+__host__ __device__ inline int64_t slice_length(int64_t k, int32_t slices) { return ((k + slices - 1) / slices + 511) / 512 * 512; }
 
 // Tiles that a product in bf16 has at most, how many columns they have, and how long k is (in the mean).
 struct ExpTiles {

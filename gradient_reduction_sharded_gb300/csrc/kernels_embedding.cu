@@ -550,8 +550,8 @@ EmbPlan emb_plan(const grs_embedding* s) {
 
 grs_status check_embedding(const grs_embedding* s, const char* who) {
   if (s == nullptr) return api_fail(GRS_ERR_INVALID_ARG, who, "shape is NULL");
-  if (s->tokens < 0 || s->tokens > INT32_MAX || s->hidden < 1 || s->hidden > GRS_MAX_WIDTH)
-    return api_fail(GRS_ERR_SHAPE, who, "tokens must be in [0, 2^31) and hidden in [1, GRS_MAX_WIDTH]");
+  if (s->tokens < 0 || s->tokens > GRS_MAX_ROWS || s->hidden < 1 || s->hidden > GRS_MAX_WIDTH)
+    return api_fail(GRS_ERR_SHAPE, who, "tokens must be in [0, GRS_MAX_ROWS] and hidden in [1, GRS_MAX_WIDTH]");
   if (s->row_begin < 0 || s->row_end <= s->row_begin)
     return api_fail(GRS_ERR_INVALID_ARG, who, "the row range must be 0 <= begin < end");
   if (!dtype_ok(s->dtype) || !dtype_ok(s->grad_dtype)) return api_fail(GRS_ERR_INVALID_ARG, who, "unknown element type");

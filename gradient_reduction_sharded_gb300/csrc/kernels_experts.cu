@@ -114,7 +114,7 @@ __global__ void __launch_bounds__(EXP_THREADS, 2) exp_general_kernel(const __gri
     const int64_t c0 = kWeights ? (ci - e * ct) * GC : r.from + (ci - first[e]) * GC, c1 = kWeights ? p.c : r.to;
     int64_t k0 = kWeights ? r.from : 0, k1 = kWeights ? r.to : p.k;
     if (p.slices > 1) {
-      const int64_t n = slice_length(static_cast<int32_t>(k1 - k0), p.slices);
+      const int64_t n = slice_length(k1 - k0, p.slices);
       k0 = k0 + slice * n < k1 ? k0 + slice * n : k1;
       k1 = k1 - k0 < n ? k1 : k0 + n;
     }
@@ -258,7 +258,7 @@ __global__ void __launch_bounds__(EXP_THREADS) exp_few_kernel(const __grid_const
 // ------------------------------------------------------------------- host
 grs_status check_experts(const grs_experts* s, const char* who, ExpLd* ld) {
   if (s == nullptr) return api_fail(GRS_ERR_INVALID_ARG, who, "shape is NULL");
-  if (s->rows < 0 || s->rows > INT32_MAX) return api_fail(GRS_ERR_SHAPE, who, "rows must be in [0, 2^31)");
+  if (s->rows < 0 || s->rows > GRS_MAX_ROWS) return api_fail(GRS_ERR_SHAPE, who, "rows must be in [0, GRS_MAX_ROWS]");
   if (s->experts < 1 || s->experts > GRS_MOE_MAX_EXPERTS) return api_fail(GRS_ERR_SHAPE, who, "experts must be in [1, GRS_MOE_MAX_EXPERTS]");
   if (s->in_features < 1 || s->out_features < 1 || s->in_features > GRS_MAX_WIDTH || s->out_features > GRS_MAX_WIDTH)
     return api_fail(GRS_ERR_SHAPE, who, "in_features and out_features must be in [1, GRS_MAX_WIDTH]");

@@ -123,9 +123,9 @@ struct Tiles {
       x.k1 = static_cast<int32_t>(k);
     }
     if (slices > 1) {
-      const int32_t n = slice_length(x.k1 - x.k0, slices), from = x.k0;
-      x.k0 = x.k1 - from < int64_t(x.slice) * n ? x.k1 : from + x.slice * n;
-      if (x.k1 - x.k0 > n) x.k1 = x.k0 + n;
+      const int64_t n = slice_length(x.k1 - x.k0, slices), from = x.k0 + x.slice * n, to = from + n;
+      x.k0 = from < x.k1 ? static_cast<int32_t>(from) : x.k1;
+      x.k1 = to < x.k1 ? static_cast<int32_t>(to) : x.k1;
     }
     x.c0 = static_cast<int32_t>(c0);
     x.c1 = static_cast<int32_t>(c1 < c0 + TC ? c1 : c0 + TC);

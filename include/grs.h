@@ -838,6 +838,8 @@ grs_status grs_moe_combine_backward(const grs_moe* shape, const void* dy, const 
 
 /* -------------------- operators of a decoder's other parameters */
 
+#define GRS_MAX_ROWS 2147418112 /* rows of the experts, tokens of an embedding: 2^31 - 2^16 */
+
 /* Synchronise `stream`, read and clear the current device's flags of
  * grs_experts_*, grs_embedding_* and grs_qk_norm_*, which the calls of all its
  * streams share: BOUNDS if a checked build found an index out of place, TIMEOUT
@@ -853,7 +855,7 @@ grs_status grs_operators_check_device_errors(void* stream);
  * [ISSUE] "Why this needs separate work"; their gradient is written in
  * grad_dtype, so that it can go straight into a rank's gradient buffer. */
 typedef struct grs_experts {
-  int64_t rows;          /* rows that xs and ys have, 0..2^31 - 1 */
+  int64_t rows;          /* rows that xs and ys have, 0..GRS_MAX_ROWS */
   int64_t ld_x;          /* elements from one row of xs and dxs to the next, 0 = in_features */
   int64_t ld_y;          /* of ys and dys, 0 = out_features */
   int32_t experts;       /* 1..GRS_MOE_MAX_EXPERTS */
@@ -871,6 +873,7 @@ typedef struct grs_experts {
  *             (values outside are taken as the nearest of them).
  *   workspace : device, 16-byte aligned, grs_experts_workspace_bytes (not
  *             initialised); NULL where that is 0.  Calls that share one must not overlap.
+ * bf16 runs on the tensor cores.  Which sums are cut into parts goes by the shape.
  * Rows outside [offsets[0], offsets[experts]) are neither read for a result nor
  * written; NaN in them changes nothing.  xs, w and dys start at multiples of 16
  * bytes, outputs at multiples of their element.  In bf16, widths and row
@@ -896,7 +899,7 @@ int64_t grs_experts_workspace_bytes(const grs_experts* shape);
  * too: padding) has no row here: its vector is zeros, so that the ranks'
  * results add up, and its gradient goes nowhere. */
 typedef struct grs_embedding {
-  int64_t tokens;        /* 0..2^31 - 1 */
+  int64_t tokens;        /* 0..GRS_MAX_ROWS */
   int32_t row_begin;     /* >= 0 */
   int32_t row_end;       /* > row_begin */
   int32_t hidden;        /* elements of a vector, 1..GRS_MAX_WIDTH */

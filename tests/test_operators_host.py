@@ -56,7 +56,7 @@ A = 1 << 20
 
 
 @pytest.mark.parametrize("status, change", [
-    ("SHAPE", {"rows": -1}), ("SHAPE", {"rows": 1 << 31}), ("SHAPE", {"experts": 0}), ("SHAPE", {"experts": 1025}),
+    ("SHAPE", {"rows": -1}), ("SHAPE", {"rows": (1 << 31) - (1 << 16) + 1}), ("SHAPE", {"experts": 0}), ("SHAPE", {"experts": 1025}),
     ("SHAPE", {"in_features": 0}), ("SHAPE", {"out_features": 0}), ("SHAPE", {"in_features": (1 << 30) + 1}),
     ("SHAPE", {"ld_x": 15}), ("SHAPE", {"ld_y": 7}), ("SHAPE", {"ld_x": -16}), ("SHAPE", {"ld_y": (1 << 30) + 1}),
     ("INVALID_ARG", {"dtype": 2}), ("INVALID_ARG", {"grad_dtype": -1})])
@@ -93,7 +93,7 @@ def test_experts_refuse_pointers(grs):
 
 
 @pytest.mark.parametrize("status, change", [
-    ("SHAPE", {"tokens": -1}), ("SHAPE", {"tokens": 1 << 31}), ("SHAPE", {"hidden": 0}), ("SHAPE", {"hidden": (1 << 30) + 1}),
+    ("SHAPE", {"tokens": -1}), ("SHAPE", {"tokens": (1 << 31) - (1 << 16) + 1}), ("SHAPE", {"hidden": 0}), ("SHAPE", {"hidden": (1 << 30) + 1}),
     ("INVALID_ARG", {"row_begin": -1}), ("INVALID_ARG", {"row_end": 4}), ("INVALID_ARG", {"dtype": 3}), ("INVALID_ARG", {"grad_dtype": 2})])
 def test_embedding_refuses_shapes(grs, status, change):
     s = grs.make_embedding(5, 4, 20, 16, 1.0, grs.GRS_DTYPE_FP32, grs.GRS_DTYPE_BF16)

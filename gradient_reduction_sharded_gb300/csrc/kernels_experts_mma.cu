@@ -619,10 +619,11 @@ ExpTiles experts_mma_tiles(Product p, const grs_experts* s) {
   auto up = [](int64_t n, int64_t to) { return (n + to - 1) / to; };
   ExpTiles t;
   if (p == Product::kWeights) {
-    // Few large tiles are shared badly: 3000 rows, 12 experts, 1024 -> 520 (144 of them) 19.1 us, 16.1 in tiles a quarter
-    // as large; 16000 rows, 32 experts, 2048 -> 768 (768 of them) 58.5 and 65.4.
-    const int64_t large = s->experts * up(in, 256) * up(out, 256);
-    t.columns = large < 4 * 76 ? 128 : 256;
+    // Few large tiles are shared badly, small ones read more for each product: 12 experts, 1024 -> 520 (144 large tiles),
+    // 3000 rows 19.1 us with large and 16.1 with small ones, 8000 rows 31.8 and 28.5; 8 experts, 2048 -> 768 (192), 32768
+    // rows 82 and 93; 32 experts (768), 16000 rows 58.5 and 65.4.
+    const int64_t large = s->experts * up(in, 256) * up(out, 256), mean = s->rows / s->experts;
+    t.columns = large < 76 || (large < 4 * 76 && mean < 1024) ? 128 : 256;
     t.n = t.columns == 256 ? large : s->experts * up(in, 128) * up(out, 128);
     t.k = s->rows / s->experts;
   } else {

@@ -327,7 +327,9 @@ __global__ void __launch_bounds__(EXP_THREADS) exp_join_kernel(const float* __re
 }
 
 // How a product is cut: as far as its tiles leave SMs without any, in slices
-// of 512 at least (1024 on the tensor cores).
+// of 512 at least (1024 on the tensor cores).  20 rows, 32 experts, 2048 -> 768:
+// 12.7 us whole, 11.7 in two slices; 16 rows, 8 experts, 8192 -> 1024 32 and 16.5.
+// Twice as many slices: 512 rows 17.2 -> 21.1.
 ExpSlices exp_slices(Product p, const grs_experts* s) {
   const bool f = s->dtype == GRS_DTYPE_FP32;
   const ExpTiles t = f ? exp_general_tiles(p, s) : experts_mma_tiles(p, s);

@@ -457,7 +457,7 @@ __global__ void __launch_bounds__(MMA_THREADS, (Shape<TC, kCtas>::PER_SM))
       const int64_t f = x.f0 + int64_t(rank) * MMA_F + quarter * 32 + lane;
       const int n = x.c1 - x.c0;
       O* o = a.o + x.e * a.o_e + x.slice * a.o_s + int64_t(x.c0) * a.o_c + f;
-      // (an even number of features less when a check fails: none, and the same parity)
+      // Features from this lane's on; where a check fails none, of the same parity.
       const int64_t rest = GRS_CHECK(kWeights || (x.c0 >= 0 && x.c1 <= a.rows), mma_flags, SITE_MMA_ROW) ? a.f - f : -2;
       const bool on = rest > 0;
       const int32_t sections = kSections ? (blocks + MMA_SECTION - 1) / MMA_SECTION : 1;

@@ -60,6 +60,7 @@ constexpr int MMA_K = 64;            // of k a stage: a swizzled row of bf16
 constexpr int MMA_F = 128;           // features of a block
 constexpr int MMA_SECTION = 8;       // stages that fp32 gradients add up in the tensor cores
 constexpr int RING = 4;              // tiles told ahead
+constexpr int TURN_ROW = 80;         // bytes of a row on its way out: 32 features and a gap, so that rows lie in other banks
 constexpr int MMA_SMEM = 227 * 1024;
 enum : int { SITE_MMA_ROW = 2 };
 
@@ -68,7 +69,9 @@ __device__ int mma_flags[FLAG_COUNT];
 template <int TC, int kCtas>
 struct Shape {
   static constexpr int A = MMA_F * MMA_K * 2, B = TC / kCtas * MMA_K * 2, STAGE = A + B;
-  static constexpr int FIXED = 1024 + (GRS_MOE_MAX_EXPERTS + 2) * 4 + 832;  // alignment, tiles before each expert, barriers
+  static constexpr bool TURNED = TC >= 128;  // results go out by store_turned (narrow tiles would lose a stage to it)
+  static constexpr int OUT = TURNED ? MMA_STORING * 32 * TURN_ROW : 0;
+  static constexpr int FIXED = 1024 + (GRS_MOE_MAX_EXPERTS + 2) * 4 + 832 + OUT;  // alignment, tiles before each expert, barriers, results
   static constexpr int PER_SM = kCtas == 1 && TC <= 64 ? 2 : 1;  // blocks
   static constexpr int FIT = ((PER_SM == 2 ? 113 * 1024 : MMA_SMEM) - FIXED) / STAGE;
   static constexpr int STAGES = FIT < 10 ? FIT : 10;
@@ -82,7 +85,7 @@ struct MmaArgs {
   int64_t o_c, o_e, o_s;   // elements from one c, one expert, one slice to the next
   int64_t f, c, k;         // extents; an expert's rows in the place of c or k
   int32_t rows, experts, slices;
-  int32_t words;           // two features' bf16 lie in an aligned word
+  int32_t pieces;          // rows of the result are whole 16-byte pieces
 };
 
 struct Tile {
@@ -158,37 +161,56 @@ __device__ __forceinline__ void by_size(const int32_t* offsets, int32_t experts,
   }
 }
 
+__device__ __forceinline__ uint4 shared_piece(uint32_t at) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+  return v;
+}
+
 __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, volatile int* abort) {
   return mbar_wait_bounded(bar, parity, mma_flags, abort);
 }
 
 // 32 columns, a lane a feature, to rows `ld` elements apart, the first n of
-// them; `rest`: features from this lane's on (<= 0: none).  Where words are
-// aligned two lanes store their two bf16 as one, for every second row each.
+// them; `on`: there is such a feature.
 template <typename O>
-__device__ __forceinline__ void store_columns(O* o, int64_t ld, const uint32_t (&v)[32], int n, int64_t rest, bool words) {
-  if constexpr (sizeof(O) == 2) {
-    if (words) {
-      const int odd = threadIdx.x & 1;
-      const int64_t have = rest + odd;  // from the even lane's on
-      O* p = o - odd + odd * ld;
-#pragma unroll
-      for (int j = 0; j < 32; j += 2) {
-        const uint32_t mine = to_bf16_pair(make_float2(__uint_as_float(v[j]), __uint_as_float(v[j + 1])));
-        const uint32_t other = __shfl_xor_sync(0xffffffffu, mine, 1), both = __byte_perm(mine, other, odd ? 0x3276 : 0x5410);
-        if (j + odd < n) {
-          if (have >= 2) *reinterpret_cast<uint32_t*>(p) = both;
-          else if (have == 1) *p = static_cast<O>(both);
-        }
-        p += 2 * ld;
-      }
-      return;
-    }
-  }
+__device__ __forceinline__ void store_columns(O* o, int64_t ld, const uint32_t (&v)[32], int n, bool on) {
 #pragma unroll
   for (int j = 0; j < 32; ++j) {
-    if (rest > 0 && j < n) *o = from_float<O>(__uint_as_float(v[j]));
+    if (on && j < n) *o = from_float<O>(__uint_as_float(v[j]));
     o += ld;
+  }
+}
+
+// The same 32 x 32 results in bf16 by 16-byte stores: rounded as fragments,
+// transposed on the way to the warp's place in shared memory, and read as four
+// pieces of each row.  `o`: this thread's piece of row t / 4; `on`: there are
+// its eight features.  (One 16-bit store a feature and column took 2.5 us a
+// tile, pairs by shuffles 4.1.)
+__device__ __forceinline__ void store_turned(uint32_t from, uint32_t place, uint16_t* o, int64_t ld, int n, bool on) {
+  const int t = threadIdx.x & 31;
+  uint32_t v[2][16];
+  tmem_load_fragments(from, v[0]);
+  tmem_load_fragments(from + (16u << 16), v[1]);
+  tmem_wait_load();
+  __syncwarp();  // the place has been read
+  const uint32_t to = place + ((t >> 4) * 8 + (t & 7)) * TURN_ROW + (t >> 3 & 1) * 16;
+#pragma unroll
+  for (int l = 0; l < 2; ++l)
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      uint32_t m[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        m[q] = to_bf16_pair(make_float2(__uint_as_float(v[l][8 * k + 2 * q]), __uint_as_float(v[l][8 * k + 2 * q + 1])));
+      store_transposed(to + k * 16 * TURN_ROW + l * 32, m[0], m[1], m[2], m[3]);
+    }
+  __syncwarp();
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const int row = (t >> 2) + 8 * q;
+    const uint4 w = shared_piece(place + row * TURN_ROW + (t & 3) * 16);
+    if (on && row < n) *reinterpret_cast<uint4*>(o + 8 * q * ld) = w;
   }
 }
 
@@ -204,7 +226,8 @@ __global__ void __launch_bounds__(MMA_THREADS, (Shape<TC, kCtas>::PER_SM))
   static_assert(!kWeights || TC / kCtas % 64 == 0, "operands across k come in 64s");
   extern __shared__ uint8_t smem[];
   uint8_t* stages = smem + (1024 - (smem_addr(smem) & 1023)) % 1024;
-  int32_t* first = reinterpret_cast<int32_t*>(stages + S::STAGES * S::STAGE);
+  uint8_t* out = stages + S::STAGES * S::STAGE;
+  int32_t* first = reinterpret_cast<int32_t*>(out + S::OUT);
   uint64_t* full = reinterpret_cast<uint64_t*>(first + ((GRS_MOE_MAX_EXPERTS + 1 + 1) & ~1));
   uint64_t *empty = full + S::STAGES, *tail = empty + S::STAGES, *done = tail + S::STAGES, *taken = done + 2;
   uint64_t *told = taken + 2, *heard = told + RING, *answered = heard + RING, *asked = answered + 2;
@@ -448,7 +471,8 @@ __global__ void __launch_bounds__(MMA_THREADS, (Shape<TC, kCtas>::PER_SM))
     bool ok = true;
     const int quarter = w & 3, half = (w - 4) >> 2;  // 32 lanes; every second 32 columns
     const uint32_t from = tmem + (uint32_t(quarter) << 21) + 32 * half;
-    const bool words = sizeof(O) == 4 || a.words != 0;
+    const bool turned = S::TURNED && sizeof(O) == 2 && a.pieces != 0;
+    const uint32_t place = smem_addr(out) + (w - 4) * 32 * TURN_ROW;
     while (ok) {
       Tile x;
       ok = next_tile(x);
@@ -457,9 +481,7 @@ __global__ void __launch_bounds__(MMA_THREADS, (Shape<TC, kCtas>::PER_SM))
       const int64_t f = x.f0 + int64_t(rank) * MMA_F + quarter * 32 + lane;
       const int n = x.c1 - x.c0;
       O* o = a.o + x.e * a.o_e + x.slice * a.o_s + int64_t(x.c0) * a.o_c + f;
-      // Features from this lane's on; where a check fails none, of the same parity.
-      const int64_t rest = GRS_CHECK(kWeights || (x.c0 >= 0 && x.c1 <= a.rows), mma_flags, SITE_MMA_ROW) ? a.f - f : -2;
-      const bool on = rest > 0;
+      const bool rows_on = GRS_CHECK(kWeights || (x.c0 >= 0 && x.c1 <= a.rows), mma_flags, SITE_MMA_ROW), on = rows_on && f < a.f;
       const int32_t sections = kSections ? (blocks + MMA_SECTION - 1) / MMA_SECTION : 1;
       // fp32: the thread's columns are added up in its registers, section by section.
       constexpr int PARTS = kSections ? TC / 64 : 1;
@@ -486,10 +508,19 @@ __global__ void __launch_bounds__(MMA_THREADS, (Shape<TC, kCtas>::PER_SM))
           }
         } else {
           for (int j0 = 32 * half; j0 < n; j0 += 64) {
+            if constexpr (S::TURNED && sizeof(O) == 2) {
+              if (turned) {
+                const int piece = (lane & 3) * 8 - lane;  // from this lane's feature to its piece's
+                store_turned(from + acc * TC + j0 - 32 * half, place, o + piece + (j0 + (lane >> 2)) * a.o_c, a.o_c, n - j0,
+                             rows_on && f + piece < a.f);
+                continue;
+              }
+            }
             uint32_t v[32];
             tmem_load32(from + acc * TC + j0 - 32 * half, v);
             tmem_wait_load();
-            store_columns(o + j0 * a.o_c, a.o_c, v, n - j0, rest, words);
+            store_columns(o + j0 * a.o_c, a.o_c, v, n - j0, on);
+            __syncwarp();
           }
         }
         tmem_before_sync();
@@ -591,7 +622,7 @@ cudaError_t mma_launch(const grs_experts* s, const ExpLd& ld, const void* xs, co
     tiles = s->rows / TC + (s->rows < s->experts ? s->rows : s->experts);
   }
   if (!fine) return cudaErrorInvalidValue;
-  a.words = api_aligned(o, 4) && a.o_c % 2 == 0 && a.o_e % 2 == 0;
+  a.pieces = api_aligned(o, 16) && a.o_c % 8 == 0 && a.o_e % 8 == 0 && a.f % 8 == 0;
   const int64_t step = MMA_F * kCtas;
   tiles *= (a.f + step - 1) / step * sl.n;
   // Weights: a cluster for each tile, of which those that run take over the others' (ask_cluster).

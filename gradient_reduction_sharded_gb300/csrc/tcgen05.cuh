@@ -163,6 +163,22 @@ __device__ __forceinline__ void tmem_load16(uint32_t address, uint32_t (&v)[16])
         "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
       : "r"(address));
 }
+// 32 columns of 16 lanes: as a matrix instruction's result, v[4 i ..] the eight
+// columns from 8 i on: of lane t / 4 those from 2 (t % 4) on, two, and the same of
+// lane t / 4 + 8, for thread t.
+__device__ __forceinline__ void tmem_load_fragments(uint32_t address, uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]),
+        "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+      : "r"(address));
+}
+// Four 8 x 8 matrices of 16-bit numbers to shared memory, transposed: thread t
+// has two neighbours of row t / 4 of each, and the address of row t % 8 of
+// matrix t / 8 as it is stored.
+__device__ __forceinline__ void store_transposed(uint32_t address, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(address), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
 __device__ __forceinline__ void tmem_wait_load() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 
 // -------------------------------------------------------- matrix product

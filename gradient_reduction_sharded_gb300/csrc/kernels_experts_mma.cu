@@ -60,7 +60,7 @@ constexpr int MMA_K = 64;            // of k a stage: a swizzled row of bf16
 constexpr int MMA_F = 128;           // features of a block
 constexpr int MMA_SECTION = 8;       // stages that fp32 gradients add up in the tensor cores
 constexpr int RING = 4;              // tiles told ahead
-constexpr int TURN_ROW = 80;         // bytes of a row on its way out: 32 features and a gap, so that rows lie in other banks
+constexpr int TURN_ROW = 64;         // bytes of a row on its way out: 32 features, with the 64-byte swizzle
 constexpr int MMA_SMEM = 227 * 1024;
 enum : int { SITE_MMA_ROW = 2 };
 
@@ -182,19 +182,25 @@ __device__ __forceinline__ void store_columns(O* o, int64_t ld, const uint32_t (
   }
 }
 
-// The same 32 x 32 results in bf16 by 16-byte stores: rounded as fragments,
-// transposed on the way to the warp's place in shared memory, and read as four
-// pieces of each row.  `o`: this thread's piece of row t / 4; `on`: there are
-// its eight features.  (One 16-bit store a feature and column took 2.5 us a
-// tile, pairs by shuffles 4.1.)
-__device__ __forceinline__ void store_turned(uint32_t from, uint32_t place, uint16_t* o, int64_t ld, int n, bool on) {
+// The same 32 x 32 results in bf16, where rows of the result are whole 16-byte
+// pieces: rounded as fragments and transposed on the way to the warp's own
+// swizzled box in shared memory, which leaves as one copy.  With `all` false (a
+// row behind the first n is another expert's) its rows go as 16-byte pieces,
+// `o` this thread's piece of row t / 4, `on`: there are its eight features.
+// us with 32768 rows, 8 experts, 256 -> 2432 in bf16 (26 of memory, 22 of matrix
+// instructions): a 16-bit store a feature and row 69; pairs by shuffles longer
+// still; pieces only 43; boxes 40.  Boxes of 16 rows of all 128 features, filled
+// by four warps together, 57; copies of single rows 114.
+__device__ __forceinline__ void store_turned(uint32_t from, uint32_t place, const CUtensorMap* map, int32_t f, int32_t c, int32_t e, bool all,
+                                             uint16_t* o, int64_t ld, int n, bool on) {
   const int t = threadIdx.x & 31;
   uint32_t v[2][16];
   tmem_load_fragments(from, v[0]);
   tmem_load_fragments(from + (16u << 16), v[1]);
   tmem_wait_load();
+  bulk_wait_read();
   __syncwarp();  // the place has been read
-  const uint32_t to = place + ((t >> 4) * 8 + (t & 7)) * TURN_ROW + (t >> 3 & 1) * 16;
+  const uint32_t to = place + ((t >> 4) * 8 + (t & 7)) * TURN_ROW + ((t >> 3 ^ t >> 1) & 1) * 16, flip = (t >> 2 & 1) * 32;
 #pragma unroll
   for (int l = 0; l < 2; ++l)
 #pragma unroll
@@ -203,20 +209,30 @@ __device__ __forceinline__ void store_turned(uint32_t from, uint32_t place, uint
 #pragma unroll
       for (int q = 0; q < 4; ++q)
         m[q] = to_bf16_pair(make_float2(__uint_as_float(v[l][8 * k + 2 * q]), __uint_as_float(v[l][8 * k + 2 * q + 1])));
-      store_transposed(to + k * 16 * TURN_ROW + l * 32, m[0], m[1], m[2], m[3]);
+      store_transposed(to + k * 16 * TURN_ROW + (l * 32 ^ flip), m[0], m[1], m[2], m[3]);
     }
+  if (all) {
+    fence_async_shared();
+    __syncwarp();
+    if (t == 0) {
+      tma_store(map, place, f, c, e);
+      bulk_commit();
+    }
+    return;
+  }
   __syncwarp();
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
     const int row = (t >> 2) + 8 * q;
-    const uint4 w = shared_piece(place + row * TURN_ROW + (t & 3) * 16);
+    const uint4 w = shared_piece(place + row * TURN_ROW + ((t ^ t >> 3) & 3) * 16);
     if (on && row < n) *reinterpret_cast<uint4*>(o + 8 * q * ld) = w;
   }
 }
 
 template <Product kP, int TC, int kCtas, typename O>
 __global__ void __launch_bounds__(MMA_THREADS, (Shape<TC, kCtas>::PER_SM))
-    exp_mma_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b, const __grid_constant__ MmaArgs<O> a) {
+    exp_mma_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
+                   const __grid_constant__ CUtensorMap map_o, const __grid_constant__ MmaArgs<O> a) {
   using S = Shape<TC, kCtas>;
   constexpr bool kWeights = kP == Product::kWeights, kASK = kP == Product::kForward, kBSK = !kWeights;  // operands along k
   constexpr bool kSections = kWeights && sizeof(O) == 4;
@@ -241,6 +257,7 @@ __global__ void __launch_bounds__(MMA_THREADS, (Shape<TC, kCtas>::PER_SM))
   if (threadIdx.x == 0) {
     prefetch_map(&map_a);
     prefetch_map(&map_b);
+    if (a.pieces) prefetch_map(&map_o);
     for (int s = 0; s < S::STAGES; ++s) {
       mbar_init(full + s, kCtas);
       mbar_init(empty + s, 1);
@@ -511,7 +528,10 @@ __global__ void __launch_bounds__(MMA_THREADS, (Shape<TC, kCtas>::PER_SM))
             if constexpr (S::TURNED && sizeof(O) == 2) {
               if (turned) {
                 const int piece = (lane & 3) * 8 - lane;  // from this lane's feature to its piece's
-                store_turned(from + acc * TC + j0 - 32 * half, place, o + piece + (j0 + (lane >> 2)) * a.o_c, a.o_c, n - j0,
+                const int64_t f0 = f - lane;
+                // Rows behind the result's and features behind its width are cut off by the map.
+                store_turned(from + acc * TC + j0 - 32 * half, place, &map_o, static_cast<int32_t>(f0), x.c0 + j0, kWeights ? x.e : 0,
+                             rows_on && f0 < a.f && (kWeights || n - j0 >= 32), o + piece + (j0 + (lane >> 2)) * a.o_c, a.o_c, n - j0,
                              rows_on && f + piece < a.f);
                 continue;
               }
@@ -551,6 +571,7 @@ __global__ void __launch_bounds__(MMA_THREADS, (Shape<TC, kCtas>::PER_SM))
         __syncwarp();
       }
     }
+    bulk_wait();
   }
   // A wait that gave up leaves copies and products under way: they end by themselves.
   if (*abort) {
@@ -581,16 +602,16 @@ EncodeTiled encode_tiled() {
   return f;
 }
 
-// A bf16 tensor of `n` dimensions, its boxes 64 wide with the 128-byte swizzle.
-bool make_map(CUtensorMap* m, const void* p, int n, const int64_t (&dims)[3], const int64_t (&ld)[2], int box_rows) {
+// A bf16 tensor of `n` dimensions, its boxes `width` wide: 64 or 32, a row of the 128 or 64-byte swizzle.
+bool make_map(CUtensorMap* m, const void* p, int n, const int64_t (&dims)[3], const int64_t (&ld)[2], int box_rows, int width = 64) {
   const EncodeTiled f = encode_tiled();
   if (f == nullptr) return false;
   cuuint64_t d[3], stride[2];
-  cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_rows), 1}, one[3] = {1, 1, 1};
+  cuuint32_t box[3] = {static_cast<cuuint32_t>(width), static_cast<cuuint32_t>(box_rows), 1}, one[3] = {1, 1, 1};
   for (int i = 0; i < 3; ++i) d[i] = static_cast<cuuint64_t>(dims[i]);
   for (int i = 0; i < 2; ++i) stride[i] = static_cast<cuuint64_t>(ld[i]) * 2;
   return f(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, static_cast<cuuint32_t>(n), const_cast<void*>(p), d, stride, box, one,
-           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+           CU_TENSOR_MAP_INTERLEAVE_NONE, width == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -599,7 +620,7 @@ cudaError_t mma_launch(const grs_experts* s, const ExpLd& ld, const void* xs, co
                        void* o, int64_t o_ld, const ExpSlices& sl, void* stream) {
   using S = Shape<TC, kCtas>;
   const int64_t in = s->in_features, out = s->out_features;
-  CUtensorMap ma, mb;
+  CUtensorMap ma, mb, mo{};
   MmaArgs<O> a{};
   a.offsets = offsets;
   a.slices = sl.n;
@@ -622,7 +643,9 @@ cudaError_t mma_launch(const grs_experts* s, const ExpLd& ld, const void* xs, co
     tiles = s->rows / TC + (s->rows < s->experts ? s->rows : s->experts);
   }
   if (!fine) return cudaErrorInvalidValue;
-  a.pieces = api_aligned(o, 16) && a.o_c % 8 == 0 && a.o_e % 8 == 0 && a.f % 8 == 0;
+  if (S::TURNED && sizeof(O) == 2 && api_aligned(o, 16) && a.o_c % 8 == 0 && a.f % 8 == 0)
+    a.pieces = make_map(&mo, o, 3, {a.f, kP == Product::kWeights ? a.c : s->rows, kP == Product::kWeights ? s->experts : 1},
+                        {a.o_c, kP == Product::kWeights ? a.o_e : a.o_c}, 32, 32);
   const int64_t step = MMA_F * kCtas;
   tiles *= (a.f + step - 1) / step * sl.n;
   // Weights: a cluster for each tile, of which those that run take over the others' (ask_cluster).
@@ -631,7 +654,7 @@ cudaError_t mma_launch(const grs_experts* s, const ExpLd& ld, const void* xs, co
   const unsigned grid = static_cast<unsigned>((tiles < at_once ? tiles : at_once) * kCtas);
   const cudaError_t e = allow_smem<exp_mma_kernel<kP, TC, kCtas, O>>(S::BYTES);
   if (e != cudaSuccess) return e;
-  return launch_pdl_cluster(exp_mma_kernel<kP, TC, kCtas, O>, kCtas, dim3(grid), dim3(MMA_THREADS), S::BYTES, stream, ma, mb, a);
+  return launch_pdl_cluster(exp_mma_kernel<kP, TC, kCtas, O>, kCtas, dim3(grid), dim3(MMA_THREADS), S::BYTES, stream, ma, mb, mo, a);
 }
 
 template <Product kP, int TC>

@@ -122,6 +122,16 @@ __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, i
         : "memory");
 }
 
+// A box of shared memory to (x, y, z) of a tensor, cut off at its extents; the
+// thread that sends it waits: until what it sent has been read, or written.
+__device__ __forceinline__ void tma_store(const CUtensorMap* map, uint32_t from, int32_t x, int32_t y, int32_t z) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(map), "r"(x), "r"(y), "r"(z), "r"(from)
+               : "memory");
+}
+__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+
 // ---------------------------------------------------------- tensor memory
 // Columns [address, + n) of 128 lanes of 32 bits; one warp of each block.
 template <int kCtas>

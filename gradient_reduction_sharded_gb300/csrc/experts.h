@@ -30,8 +30,11 @@ struct ExpSlices {
   int64_t ld = 0, distance = 0;  // of its rows, of the slices
 };
 
-// k of a slice: in 512s, so that the sections of an fp32 sum are whole ones.
-__host__ __device__ inline int64_t slice_length(int64_t k, int32_t slices) { return ((k + slices - 1) / slices + 511) / 512 * 512; }
+// k of a slice: in 512s on the tensor cores and 64s elsewhere, so that the sections of an fp32 sum are whole ones.
+template <int kSection>
+__host__ __device__ inline int64_t slice_length(int64_t k, int32_t slices) {
+  return ((k + slices - 1) / slices + kSection - 1) / kSection * kSection;
+}
 
 // Tiles that a product in bf16 has at most, how many columns they have, and how long k is (in the mean).
 struct ExpTiles {

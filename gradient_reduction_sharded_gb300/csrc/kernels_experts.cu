@@ -23,15 +23,16 @@ enum : int { SITE_EXP_ROW = 1 };
 __device__ int exp_flags[FLAG_COUNT];
 
 // --------------------------------------------------------- fp32, any size
-// A block has 128 features of 64 c, a thread eight by four, as pairs of
-// neighbouring features.  Operands come by copies of single numbers, which
-// turns either layout into [k][feature or c]; three steps of 16 of k are on
-// their way while one is multiplied (with one ahead a step took as long as the
-// memory's answer).  3000 rows, 8 experts, 1024 -> 1024: forward 224 us, rows'
-// gradients 215, weights' gradients 181 (28 to 35 TFLOP/s), bound by shared
-// memory and instruction issue together.
-constexpr int GF = 128, GC = 64, GK = 16, G_AHEAD = 4;
-constexpr int G_SMEM = G_AHEAD * GK * (GC + 4) * 4;  // the c operand's stages
+// A block has 128 features of 64 c, a thread eight by eight, as pairs of
+// neighbouring features.  Operands are read as single numbers, which turns
+// either layout into [k][feature or c] in shared memory; the next 16 of k are in
+// registers, the ones after on their way, while 16 are multiplied.  3000 rows, 8
+// experts, 1024 -> 1024: forward 166 us, rows' gradients 160, weights' gradients
+// 136 (38 to 46 TFLOP/s); 16384 rows 45 to 50.  Bound by reads of shared memory:
+// four a thread and k for 32 additions of pairs; eight by four (three for 16)
+// took 224, 215 and 182, copies of single numbers past the registers the same,
+// every c twice in shared memory instead of moves 17 % more.
+constexpr int GF = 128, GC = 64, GK = 16, G_THREADS = 128, G_PER_SM = 2;
 
 template <typename O>
 struct GeneralArgs {
@@ -45,68 +46,66 @@ struct GeneralArgs {
   int32_t rows, experts, slices;
 };
 
-__device__ __forceinline__ void copy_number(uint32_t to, const float* from, bool there) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to), "l"(from), "r"(there ? 4 : 0) : "memory");
-}
-
 // One operand's next GK x N elements: where a thread's lie and go.
-// Neighbouring threads along what lies next to one another.
-template <int N>
+// Neighbouring threads along what lies next to one another, k with kAlongK.
+template <int N, bool kAlongK>
 struct Panel {
-  static constexpr int EACH = N * GK / EXP_THREADS, STAGE = GK * (N + 4) * 4;
-  const float *p, *none;  // the thread's first element of the next step; an address for what is not there
-  int64_t next;           // elements to its next one
-  int64_t step;           // to the next step's
-  int32_t k, dk;          // of its first element, of its next ones
-  uint32_t on;            // which of its elements exist along N
-  uint32_t at, dat;       // in shared memory
-  __device__ __forceinline__ Panel(const float* base, int64_t n0, int64_t n1, int64_t k0, int64_t ld_n, int64_t ld_k, uint32_t shared) : none(base) {
-    const bool along_k = ld_k == 1;
-    constexpr int PER_K = EXP_THREADS / GK, PER_N = EXP_THREADS / N;  // between a thread's elements: in N, in k
-    const int tk = along_k ? threadIdx.x % GK : threadIdx.x / N, tn = along_k ? threadIdx.x / GK : threadIdx.x % N;
-    const int dn = along_k ? PER_K : 0;
+  static constexpr int EACH = N * GK / G_THREADS;
+  static constexpr int PER_K = G_THREADS / GK, PER_N = G_THREADS / N;  // between a thread's elements: in N, in k
+  static constexpr int DAT = kAlongK ? PER_K : PER_N * (N + 4);        // in shared memory
+  const float* p;      // the thread's first element of the next step
+  int64_t next, step;  // elements to its next one, to the next step's
+  int32_t k;           // of its first element
+  uint32_t on;         // which of its elements exist along N
+  uint32_t at;         // in shared memory
+  bool whole;          // all of the panel's N exist
+  float v[EACH];
+  __device__ __forceinline__ Panel(const float* base, int64_t n0, int64_t n1, int64_t k0, int64_t ld_n, int64_t ld_k)
+      : whole(n0 + N <= n1) {
+    const int tk = kAlongK ? threadIdx.x % GK : threadIdx.x / N, tn = kAlongK ? threadIdx.x / GK : threadIdx.x % N;
     p = base + (n0 + tn) * ld_n + (k0 + tk) * ld_k;
     k = tk;
-    dk = along_k ? 0 : PER_N;
-    next = along_k ? PER_K * ld_n : PER_N * ld_k;
+    next = kAlongK ? PER_K * ld_n : PER_N * ld_k;
     step = GK * ld_k;
-    at = shared + (tk * (N + 4) + tn) * 4;
-    dat = (along_k ? PER_K : PER_N * (N + 4)) * 4;
+    at = tk * (N + 4) + tn;
     on = 0;
 #pragma unroll
-    for (int j = 0; j < EACH; ++j) on |= uint32_t(n0 + tn + j * dn < n1) << j;
+    for (int j = 0; j < EACH; ++j) on |= uint32_t(n0 + tn + (kAlongK ? j * PER_K : 0) < n1) << j;
   }
-  // The step whose first k has `rest` left, to a stage; what is not there becomes zeros.
-  __device__ __forceinline__ void load(int64_t rest, int stage) {
+  // The step whose first k has `rest` left; what is not there is zero.
+  __device__ __forceinline__ void load(int64_t rest) {
     const float* q = p;
+    if (whole && rest >= GK) {
 #pragma unroll
-    for (int j = 0; j < EACH; ++j) {
-      const bool there = (on >> j & 1) != 0 && k + j * dk < rest;
-      copy_number(at + stage * STAGE + j * dat, there ? q : none, there);
-      q += next;
+      for (int j = 0; j < EACH; ++j, q += next) v[j] = __ldg(q);
+    } else {
+#pragma unroll
+      for (int j = 0; j < EACH; ++j, q += next) v[j] = (on >> j & 1) != 0 && k + (kAlongK ? 0 : j * PER_N) < rest ? __ldg(q) : 0.0f;
     }
     p += step;
+  }
+  __device__ __forceinline__ void put(float* stage) const {
+#pragma unroll
+    for (int j = 0; j < EACH; ++j) stage[at + j * DAT] = v[j];
   }
 };
 
 // Sums of 64 products are added up to the result's: shorter chains, errors
 // that grow with 64 + k / 64 additions instead of k.
 template <Product kP, typename O>
-__global__ void __launch_bounds__(EXP_THREADS, 2) exp_general_kernel(const __grid_constant__ GeneralArgs<O> p) {
+__global__ void __launch_bounds__(G_THREADS, G_PER_SM) exp_general_kernel(const __grid_constant__ GeneralArgs<O> p) {
   constexpr bool kWeights = kP == Product::kWeights;
-  __shared__ __align__(16) float as[G_AHEAD][GK][GF + 4];
-  extern __shared__ __align__(16) float bs_[];
-  float(*bs)[GK][GC + 4] = reinterpret_cast<float(*)[GK][GC + 4]>(bs_);
+  __shared__ __align__(16) float as[2][GK * (GF + 4)], bs[2][GK * (GC + 4)];
   __shared__ int32_t first[GRS_MOE_MAX_EXPERTS + 1];
   pdl_wait();
   pdl_trigger();
   if constexpr (!kWeights) {
-    group_prefix<GC, EXP_THREADS>(p.offsets, p.experts, p.rows, first);
+    group_prefix<GC, G_THREADS>(p.offsets, p.experts, p.rows, first);
     __syncthreads();
   }
   const int64_t ft = (p.f + GF - 1) / GF, ct = (p.c + GC - 1) / GC;
   const int64_t tiles = ft * (kWeights ? ct * p.experts : first[p.experts]);
-  const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;  // features 4 tx.. and 64 + 4 tx.., c 4 ty..
+  const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;  // features 4 tx.. and 64 + 4 tx.., c 4 ty.. and 32 + 4 ty..
   for (int64_t i = blockIdx.x; i < tiles * p.slices; i += gridDim.x) {
     const int64_t slice = i / tiles, tile = i - slice * tiles, ci = tile / ft, f0 = (tile - ci * ft) * GF;
     const int e = kWeights ? static_cast<int>(ci / ct) : expert_of(first, p.experts, ci);
@@ -114,56 +113,58 @@ __global__ void __launch_bounds__(EXP_THREADS, 2) exp_general_kernel(const __gri
     const int64_t c0 = kWeights ? (ci - e * ct) * GC : r.from + (ci - first[e]) * GC, c1 = kWeights ? p.c : r.to;
     int64_t k0 = kWeights ? r.from : 0, k1 = kWeights ? r.to : p.k;
     if (p.slices > 1) {
-      const int64_t n = slice_length(k1 - k0, p.slices);
+      const int64_t n = slice_length<64>(k1 - k0, p.slices);
       k0 = k0 + slice * n < k1 ? k0 + slice * n : k1;
       k1 = k1 - k0 < n ? k1 : k0 + n;
     }
     const float *a = p.a + e * p.a_e, *b = p.b;
-    uint64_t total[4][4] = {}, part[4][4] = {};
-    Panel<GF> pa(a, f0, p.f, k0, p.a_f, p.a_k, smem_addr(as));
-    Panel<GC> pb(b, c0, c1, k0, p.b_c, p.b_k, smem_addr(bs_));
-    int64_t rest = k1 - k0;  // of k, from the next step to be asked for
-    auto ask = [&](int stage) {
-      if (rest > 0) {
-        pa.load(rest, stage);
-        pb.load(rest, stage);
-      }
-      rest -= GK;
-      asm volatile("cp.async.commit_group;" ::: "memory");
-    };
-#pragma unroll
-    for (int i = 0; i < G_AHEAD - 1; ++i) ask(i);
+    uint64_t total[8][4] = {}, part[8][4] = {};
+    Panel<GF, kP == Product::kForward> pa(a, f0, p.f, k0, p.a_f, p.a_k);
+    Panel<GC, !kWeights> pb(b, c0, c1, k0, p.b_c, p.b_k);
+    pa.load(k1 - k0);
+    pb.load(k1 - k0);
+    __syncthreads();  // the tile before has been read
+    pa.put(as[0]);
+    pb.put(bs[0]);
+    if (k1 - k0 > GK) {
+      pa.load(k1 - k0 - GK);
+      pb.load(k1 - k0 - GK);
+    }
     int step = 0;
     for (int64_t k = k0; k < k1; k += GK, ++step) {
-      asm volatile("cp.async.wait_group %0;" ::"n"(G_AHEAD - 2) : "memory");
-      __syncthreads();  // all have this step's copies, and are done with the stage that is asked for next
-      ask((step + G_AHEAD - 1) % G_AHEAD);
-      float(&sa)[GK][GF + 4] = as[step % G_AHEAD];
-      float(&sb)[GK][GC + 4] = bs[step % G_AHEAD];
+      __syncthreads();  // all have put this step's numbers, and are done with those of the step before
+      if (k + GK < k1) {
+        pa.put(as[(step + 1) & 1]);
+        pb.put(bs[(step + 1) & 1]);
+        if (k + 2 * GK < k1) {
+          pa.load(k1 - k - 2 * GK);
+          pb.load(k1 - k - 2 * GK);
+        }
+      }
+      const float *sa = as[step & 1], *sb = bs[step & 1];
 #pragma unroll
       for (int q = 0; q < GK; ++q) {
-        const ulonglong2 u = *reinterpret_cast<const ulonglong2*>(&sa[q][4 * tx]), v = *reinterpret_cast<const ulonglong2*>(&sa[q][64 + 4 * tx]);
-        const float4 c = *reinterpret_cast<const float4*>(&sb[q][4 * ty]);
+        const ulonglong2 u = *reinterpret_cast<const ulonglong2*>(sa + q * (GF + 4) + 4 * tx), v = *reinterpret_cast<const ulonglong2*>(sa + q * (GF + 4) + 64 + 4 * tx);
+        const float4 c = *reinterpret_cast<const float4*>(sb + q * (GC + 4) + 4 * ty), d = *reinterpret_cast<const float4*>(sb + q * (GC + 4) + 32 + 4 * ty);
         const uint64_t x[4] = {u.x, u.y, v.x, v.y};
-        const uint64_t y[4] = {pair_bits(both(c.x)), pair_bits(both(c.y)), pair_bits(both(c.z)), pair_bits(both(c.w))};
+        const float y[8] = {c.x, c.y, c.z, c.w, d.x, d.y, d.z, d.w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < 8; ++i)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) part[i][j] = fma2(x[j], y[i], part[i][j]);
+          for (int j = 0; j < 4; ++j) part[i][j] = fma2(x[j], pair_bits(both(y[i])), part[i][j]);
       }
       if (step % 4 == 3)
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < 8; ++i)
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             total[i][j] = add2(total[i][j], part[i][j]);
             part[i][j] = 0;
           }
     }
-    __syncthreads();  // the stages may still be read
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int64_t c = c0 + ty * 4 + i;
+    for (int i = 0; i < 8; ++i) {
+      const int64_t c = c0 + (i < 4 ? 4 * ty + i : 28 + 4 * ty + i);
       if (c >= c1 || !GRS_CHECK(kWeights || c < p.rows, exp_flags, SITE_EXP_ROW)) continue;
       O* o = p.o + e * p.o_e + slice * p.o_s + c * p.o_c;
 #pragma unroll
@@ -271,6 +272,40 @@ grs_status check_experts(const grs_experts* s, const char* who, ExpLd* ld) {
   return GRS_OK;
 }
 
+// Tiles of a product, n of them where experts have equal numbers of rows, `most` at most.
+struct GeneralTiles {
+  int64_t n, most, k;
+};
+GeneralTiles exp_general_tiles(Product p, const grs_experts* s) {
+  const int64_t in = s->in_features, out = s->out_features, some = s->rows < s->experts ? s->rows : s->experts;
+  auto up = [](int64_t n, int64_t to) { return (n + to - 1) / to; };
+  if (p == Product::kWeights) {
+    const int64_t n = s->experts * up(in, GF) * up(out, GC);
+    return {n, n, s->rows / s->experts};
+  }
+  const int64_t ft = up(p == Product::kForward ? out : in, GF);
+  return {some * up(s->rows / some, GC) * ft, (s->rows / GC + some) * ft, p == Product::kForward ? in : out};
+}
+
+// Slices of such a product, of 64 at least: those that end first, by the measured
+// 1.8 us of a step with two blocks an SM and 4 us and 5 TB/s of the joining
+// kernel.  749 rows, 9 experts, 1251 -> 1208: forward 134 us whole, 93 so; 138
+// rows, 2 experts, 507 -> 120 35 and 15; 2048 rows, one expert, 64 x 64, weights'
+// gradient 39 (in slices of 512) and 12.
+int exp_general_slices(const GeneralTiles& t, int64_t outputs) {
+  const int64_t slots = G_PER_SM * 152;
+  double best = 1e30;
+  int n = 1;
+  for (int i = 1; i <= 64 && (i == 1 || i * 64 <= t.k); ++i) {
+    const double us = double((t.n * i + slots - 1) / slots) * ((t.k + i - 1) / i) * (1.8 / GK) + (i > 1 ? 4.0 + 8e-6 / 5 * outputs * i : 0.0);
+    if (us < 0.95 * best) {
+      best = us;
+      n = i;
+    }
+  }
+  return n;
+}
+
 template <Product kP, typename O>
 cudaError_t exp_general(const grs_experts* s, const ExpLd& ld, const void* a, const void* b, const int32_t* offsets, void* o,
                         const ExpSlices& sl, void* stream) {
@@ -292,16 +327,8 @@ cudaError_t exp_general(const grs_experts* s, const ExpLd& ld, const void* a, co
     p.a_f = 1, p.a_k = ld.x, p.b_c = 1, p.b_k = ld.y, p.o_c = in, p.o_e = in * out, p.f = in, p.c = out;
   }
   if (sl.n > 1) p.o_c = sl.ld;
-  const cudaError_t e = allow_smem<exp_general_kernel<kP, O>>(G_SMEM);
-  if (e != cudaSuccess) return e;
-  return launch_pdl(exp_general_kernel<kP, O>, dim3(152 * 2), dim3(EXP_THREADS), G_SMEM, stream, p);
-}
-
-ExpTiles exp_general_tiles(Product p, const grs_experts* s) {
-  const int64_t in = s->in_features, out = s->out_features, least = s->rows < s->experts ? s->rows : s->experts;
-  auto up = [](int64_t n, int64_t to) { return (n + to - 1) / to; };
-  if (p == Product::kWeights) return {GC, s->experts * up(in, GF) * up(out, GC), s->rows / s->experts};
-  return {GC, (s->rows / GC + least) * up(p == Product::kForward ? out : in, GF), p == Product::kForward ? in : out};
+  const int64_t tiles = exp_general_tiles(kP, s).most * sl.n;
+  return launch_pdl(exp_general_kernel<kP, O>, dim3(static_cast<unsigned>(tiles < 152 * G_PER_SM ? tiles : 152 * G_PER_SM)), dim3(G_THREADS), 0, stream, p);
 }
 
 // ------------------------------------------------------------------ slices
@@ -326,21 +353,24 @@ __global__ void __launch_bounds__(EXP_THREADS) exp_join_kernel(const float* __re
   }
 }
 
-// How a product is cut: as far as its tiles leave SMs without any, in slices
-// of 512 at least (1024 on the tensor cores).  20 rows, 32 experts, 2048 -> 768:
+// How a product on the tensor cores is cut: as far as its tiles leave SMs
+// without any, in slices of 1024 at least.  20 rows, 32 experts, 2048 -> 768:
 // 12.7 us whole, 11.7 in two slices; 16 rows, 8 experts, 8192 -> 1024 32 and 16.5.
 // Twice as many slices: 512 rows 17.2 -> 21.1.
 ExpSlices exp_slices(Product p, const grs_experts* s) {
-  const bool f = s->dtype == GRS_DTYPE_FP32;
-  const ExpTiles t = f ? exp_general_tiles(p, s) : experts_mma_tiles(p, s);
   ExpSlices sl;
-  const int64_t slots = f ? 2 * 152 : t.columns == 256 ? 0 : t.columns <= 64 && p != Product::kWeights ? 2 * 152 : 152;
-  int64_t n = t.n > 0 ? slots / t.n : 0, most = t.k / (f ? 512 : 1024);
-  if (n > most) n = most;
-  if (n < 2) return sl;
-  sl.n = static_cast<int>(n);
   sl.ld = p == Product::kForward ? s->out_features : s->in_features;
   sl.distance = (p == Product::kWeights ? int64_t(s->experts) * s->out_features : s->rows) * sl.ld;
+  if (s->rows == 0) return sl;
+  if (s->dtype == GRS_DTYPE_FP32) {
+    sl.n = exp_general_slices(exp_general_tiles(p, s), sl.distance);
+    return sl;
+  }
+  const ExpTiles t = experts_mma_tiles(p, s);
+  const int64_t slots = t.columns == 256 ? 0 : t.columns <= 64 && p != Product::kWeights ? 2 * 152 : 152;
+  int64_t n = t.n > 0 ? slots / t.n : 0, most = t.k / 1024;
+  if (n > most) n = most;
+  if (n >= 2) sl.n = static_cast<int>(n);
   return sl;
 }
 

@@ -137,7 +137,7 @@ struct Tiles {
       x.k1 = static_cast<int32_t>(k);
     }
     if (slices > 1) {
-      const int64_t n = slice_length(x.k1 - x.k0, slices), from = x.k0 + x.slice * n, to = from + n;
+      const int64_t n = slice_length<MMA_SECTION * MMA_K>(x.k1 - x.k0, slices), from = x.k0 + x.slice * n, to = from + n;
       x.k0 = from < x.k1 ? static_cast<int32_t>(from) : x.k1;
       x.k1 = to < x.k1 ? static_cast<int32_t>(to) : x.k1;
     }

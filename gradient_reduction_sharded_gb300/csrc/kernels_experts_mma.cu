@@ -161,6 +161,9 @@ __device__ __forceinline__ void by_size(const int32_t* offsets, int32_t experts,
   }
 }
 
+__device__ __forceinline__ void store_piece(uint32_t at, uint4 v) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
 __device__ __forceinline__ uint4 shared_piece(uint32_t at) {
   uint4 v;
   asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
@@ -566,8 +569,20 @@ __global__ void __launch_bounds__(MMA_THREADS, (Shape<TC, kCtas>::PER_SM))
           }
         }
       } else if (blocks == 0) {  // an expert without rows, a slice without k
-        if (on)
+        if (kWeights && turned) {
+          const int64_t f0 = f - lane;
+          bulk_wait_read();
+          __syncwarp();
+          for (int i = lane; i < 32 * TURN_ROW / 16; i += 32) store_piece(place + i * 16, make_uint4(0, 0, 0, 0));
+          fence_async_shared();
+          __syncwarp();
+          if (lane == 0 && f0 < a.f) {
+            for (int j0 = 32 * half; j0 < n; j0 += 64) tma_store(&map_o, place, static_cast<int32_t>(f0), x.c0 + j0, x.e);
+            bulk_commit();
+          }
+        } else if (on) {
           for (int j = half; j < n; j += 2) o[j * a.o_c] = from_float<O>(0.0f);
+        }
         __syncwarp();
       }
     }
@@ -686,18 +701,20 @@ ExpTiles experts_mma_tiles(Product p, const grs_experts* s) {
   if (p == Product::kWeights) {
     // Few large tiles are shared badly, small ones read more for each product: 12 experts, 1024 -> 520 (144 large tiles),
     // 3000 rows 19.1 us with large and 16.1 with small ones, 8000 rows 31.8 and 28.5; 8 experts, 2048 -> 768 (192), 32768
-    // rows 82 and 93; 32 experts (768), 16000 rows 58.5 and 65.4.
+    // rows 82 and 93; 32 experts (768), 16000 rows 58.5 and 65.4.  Nor are 256 features taken where a quarter of what they
+    // multiply is not there: 32 experts, 36000 rows, 384 -> 768 42 and 35.5, 128 -> 2048 50 and 42.
     const int64_t large = s->experts * up(in, 256) * up(out, 256), mean = s->rows / s->experts;
-    t.columns = large < 76 || (large < 4 * 76 && mean < 1024) ? 128 : 256;
+    t.columns = large < 76 || (large < 4 * 76 && mean < 1024) || 2 * up(in, 256) * 3 >= up(in, 128) * 4 ? 128 : 256;
     t.n = t.columns == 256 ? large : s->experts * up(in, 128) * up(out, 128);
     t.k = s->rows / s->experts;
   } else {
     // Columns by the rows that an expert has in the mean.  2048 -> 768, 32 experts, us with 16, 64, 128 and 256 (two
     // blocks): 20 rows 11.8, 13.7, -, -; 512 rows 19.8, 17.1, 21.3, -; 2048 rows 45, 24.0, 25.4, 29.1; 3000 rows -, 29.9,
-    // 25.8, 31.1; 4096 rows -, 30.6, 31.5, 30.7; 131072 rows, 256: 228.
+    // 25.8, 31.1; 4096 rows -, 30.6, 31.5, 30.7; 131072 rows, 256: 228.  256 features where there are half of them: 32
+    // experts, 36000 rows, 2048 -> 128 41, 128 columns 32.
     const int64_t f = p == Product::kForward ? out : in, mean = s->rows / s->experts;
     const int64_t large = (s->rows / 256 + least) * up(f, 256);
-    t.columns = mean >= 128 && large >= 76 ? 256 : mean >= 64 ? 128 : mean >= 16 ? 64 : 16;
+    t.columns = mean >= 128 && large >= 76 && f > 128 ? 256 : mean >= 64 ? 128 : mean >= 16 ? 64 : 16;
     t.n = t.columns == 256 ? large : (s->rows / t.columns + least) * up(f, 128);
     t.k = p == Product::kForward ? in : out;
   }

@@ -2,13 +2,15 @@
 //
 // A tile is 128 features f (256 of a cluster of two blocks) times up to TC of
 // c, in tensor memory with a lane a feature and a column a c: features lie next
-// to one another in the result, so a warp stores 32 neighbours of a row at
-// once, straight from registers, and an expert's last rows cost only as many
-// columns as there are (in 16s).
+// to one another in the result, and an expert's last rows cost only as many
+// columns as there are (in 16s).  A warp sends 32 features of 32 rows away as one
+// box, turned on the way through shared memory; fp32, narrow tiles and results
+// whose rows are not whole 16-byte pieces go from registers, 32 neighbours of a
+// row at once.
 //
 // Blocks stay and take tiles in turn.  One warp says which (into a ring in
 // shared memory), one loads (TMA, 64 of k a stage), one thread issues the
-// matrix instructions, four warps store; two accumulators, so that a tile is
+// matrix instructions, eight warps store; two accumulators, so that a tile is
 // stored while the next is multiplied.
 //
 // Forward and rows' gradients have tiles of one size, taken in a fixed turn.  A
@@ -26,14 +28,15 @@
 // expert's end, in both operands (NaN times zero is NaN).
 //
 // What bounds it: the tensor cores, and with them the power limit.  131072 rows,
-// 2048 -> 768, 32 even experts, 20 calls: forward 228 us (1808 TFLOP/s; a
+// 2048 -> 768, 32 even experts, 20 calls: forward 230 us (1796 TFLOP/s; a
 // library product of the same size in one matrix 219 to 224), rows' gradients
-// 241 (229 to 240), weights' gradients 234 (263 to 304), in fp32 252; in seconds
-// of it the clock falls and forward takes 268 (the library 246).  The tensor
-// pipe is 76 to 82 % active at 32768 rows, DRAM moves the operands once.  What
+// 241 (229 to 242), weights' gradients 234 (263 to 310), in fp32 257; in seconds
+// of it the clock falls and forward takes 261 (the library 246).  The tensor
+// pipe is 76 to 83 % active at 32768 rows, DRAM moves the operands once.  What
 // carried it there: arrivals between the two blocks without cluster-wide
 // ordering (547 -> 295 us), an issuing loop in 32 bits (-> 247), eight storing
-// warps and words (-> 240), loops of whole warps with one thread elected (-> 228).
+// warps (-> 240), loops of whole warps with one thread elected (-> 228), and
+// where k is short the boxes (32768 rows, 8 experts, 256 -> 2432: 69 -> 40).
 // Few rows are bound by reading the weights: 20 rows of 13 experts 11 us for 41 MB.
 //
 // fp32 gradients: the tensor cores add with rounding towards zero (a library

@@ -119,6 +119,26 @@ def test_a_long_k_with_few_tiles(counts, k, n, act, grad):
     Case(counts, k, n, act, grad, first=1, tail=3).check()
 
 
+@pytest.mark.parametrize("counts, k, n", [([138, 6], 507, 120), ([1, 0, 0], 1300, 123), ([749], 251, 1208), ([64, 65, 63], 640, 129), ([90, 0, 7], 65, 64)])
+@pytest.mark.parametrize("act, grad", [("fp32", "fp32"), ("fp32", "bf16")])
+def test_fp32_in_slices(counts, k, n, act, grad):
+    Case(counts, k, n, act, grad, first=2, tail=1).check()
+
+
+@pytest.mark.parametrize("counts, k, n", [([33, 160, 31, 0, 257, 300, 1, 480] * 2, 1048, 2056), ([95, 97, 0, 64, 130], 136, 264), ([700, 650], 2040, 72)])
+@pytest.mark.parametrize("pad", [0, 8, 4])
+def test_ends_of_experts_and_of_rows_inside_a_box_of_results(counts, k, n, pad):
+    Case(counts, k, n, "bf16", "bf16", first=5, tail=40, pad_x=pad, pad_y=2 * pad).check()
+
+
+@pytest.mark.parametrize("experts, k, n", [(81, 152, 340), (400, 264, 296), (400, 260, 33), (90, 131, 300)])
+@pytest.mark.parametrize("grad", ["bf16", "fp32"])
+def test_weights_of_experts_without_rows_have_no_gradient(experts, k, n, grad):
+    counts = [0] * experts
+    counts[3], counts[experts // 2], counts[-2] = 5, 1, 17
+    Case(counts, k, n, "bf16", grad, tail=2).check()
+
+
 def test_offsets_outside_the_rows_are_taken_as_the_nearest():
     c = Case([40, 20, 30], 64, 64)
     want = c.forward()

@@ -291,12 +291,12 @@ GeneralTiles exp_general_tiles(Product p, const grs_experts* s) {
 // 1.8 us of a step with two blocks an SM and 4 us and 5 TB/s of the joining
 // kernel.  749 rows, 9 experts, 1251 -> 1208: forward 134 us whole, 93 so; 138
 // rows, 2 experts, 507 -> 120 35 and 15; 2048 rows, one expert, 64 x 64, weights'
-// gradient 39 (in slices of 512) and 12.
+// gradient 39 (in slices of 512) and 16.
 int exp_general_slices(const GeneralTiles& t, int64_t outputs) {
   const int64_t slots = G_PER_SM * 152;
   double best = 1e30;
   int n = 1;
-  for (int i = 1; i <= 64 && (i == 1 || i * 64 <= t.k); ++i) {
+  for (int i = 1; i <= 64 && (i == 1 || i * 64 <= t.k); i += i < 8 ? 1 : i / 4) {
     const double us = double((t.n * i + slots - 1) / slots) * ((t.k + i - 1) / i) * (1.8 / GK) + (i > 1 ? 4.0 + 8e-6 / 5 * outputs * i : 0.0);
     if (us < 0.95 * best) {
       best = us;

@@ -702,19 +702,21 @@ ExpTiles experts_mma_tiles(Product p, const grs_experts* s) {
   auto up = [](int64_t n, int64_t to) { return (n + to - 1) / to; };
   ExpTiles t;
   if (p == Product::kWeights) {
-    // Few large tiles are shared badly, small ones read more for each product: 12 experts, 1024 -> 520 (144 large tiles),
-    // 3000 rows 19.1 us with large and 16.1 with small ones, 8000 rows 31.8 and 28.5; 8 experts, 2048 -> 768 (192), 32768
-    // rows 82 and 93; 32 experts (768), 16000 rows 58.5 and 65.4.  Nor are 256 features taken where a quarter of what they
-    // multiply is not there: 32 experts, 36000 rows, 384 -> 768 42 and 35.5, 128 -> 2048 50 and 42.
+    // Few large tiles are shared badly, small ones read more for each product.  Even experts, us with small and large ones:
+    // 12 experts, 1024 -> 520 (144 large tiles), 1500 rows 9.0 and 10.0, 3000 11.1 and 10.9, 8000 18.3 and 15.5; 8 experts,
+    // 2048 -> 768 (192), 4000 rows 18.1 and 16.6; 32 experts, 768 -> 512 (192), 4000 rows 10.8 and 12.0, 12000 15.5 and
+    // 14.6.  A skewed router's 8000 rows of the first 26.8 and 29.1, of the second 27.9 and 23.6.  Nor are 256 features
+    // taken where a quarter of what they multiply is not there: 32 experts, 36000 rows, 384 -> 768 42 and 35.5, 128 -> 2048
+    // 50 and 42.
     const int64_t large = s->experts * up(in, 256) * up(out, 256), mean = s->rows / s->experts;
-    t.columns = large < 76 || (large < 4 * 76 && mean < 1024) || 2 * up(in, 256) * 3 >= up(in, 128) * 4 ? 128 : 256;
+    t.columns = large < 76 || (large < 4 * 76 && mean < 448) || 2 * up(in, 256) * 3 >= up(in, 128) * 4 ? 128 : 256;
     t.n = t.columns == 256 ? large : s->experts * up(in, 128) * up(out, 128);
     t.k = s->rows / s->experts;
   } else {
     // Columns by the rows that an expert has in the mean.  2048 -> 768, 32 experts, us with 16, 64, 128 and 256 (two
-    // blocks): 20 rows 11.8, 13.7, -, -; 512 rows 19.8, 17.1, 21.3, -; 2048 rows 45, 24.0, 25.4, 29.1; 3000 rows -, 29.9,
-    // 25.8, 31.1; 4096 rows -, 30.6, 31.5, 30.7; 131072 rows, 256: 228.  256 features where there are half of them: 32
-    // experts, 36000 rows, 2048 -> 128 41, 128 columns 32.
+    // blocks): 20 rows 11.8, 13.7, -, -; 512 rows 19.1, 18.3, 21.6, 22.1; 2048 rows 30.6, 22.0, 24.8, 25.3; 3000 rows 36.4,
+    // 28.3, 26.4, 26.8; 4096 rows 49.4, 29.4, 27.2, 27.7; 131072 rows -, 407, 312, 227.  256 features where there are half
+    // of them: 32 experts, 36000 rows, 2048 -> 128 41, 128 columns 32.
     const int64_t f = p == Product::kForward ? out : in, mean = s->rows / s->experts;
     const int64_t large = (s->rows / 256 + least) * up(f, 256);
     t.columns = mean >= 128 && large >= 76 && f > 128 ? 256 : mean >= 64 ? 128 : mean >= 16 ? 64 : 16;

@@ -39,9 +39,11 @@
 // where k is short the boxes (32768 rows, 8 experts, 256 -> 2432: 69 -> 40).
 // Few rows are bound by reading the weights: 20 rows of 13 experts 11 us for 41 MB.
 //
-// fp32 gradients: the tensor cores add with rounding towards zero (a library
-// product of 4096 rows is 4e-6 off, with a bias), so sections of 512 rows are
-// added up by ordinary fp32 additions, in the storing warps' registers.
+// Long sums: the tensor cores add with rounding towards zero, so sums of values
+// of one sign are too small by a part that grows with k: 2.5e-5 at 4096, 7.9e-4
+// at 131072 (a half step of bf16 is 3.9e-3).  Sections of k are therefore added
+// up by ordinary fp32 additions, in the storing warps' registers: of 512 for
+// gradients in fp32, of 4096 for every other result.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -61,7 +63,8 @@ constexpr int MMA_STORING = 8;       // storing warps, two for each quarter of t
 constexpr int MMA_THREADS = 128 + 32 * MMA_STORING;
 constexpr int MMA_K = 64;            // of k a stage: a swizzled row of bf16
 constexpr int MMA_F = 128;           // features of a block
-constexpr int MMA_SECTION = 8;       // stages that fp32 gradients add up in the tensor cores
+// Stages that the tensor cores add up: of gradients in fp32, and of all else, whose result is rounded to bf16 in the end.
+constexpr int MMA_SECTION = 8, MMA_LONG_SECTION = 64;
 constexpr int RING = 4;              // tiles told ahead
 constexpr int TURN_ROW = 64;         // bytes of a row on its way out: 32 features, with the 64-byte swizzle
 constexpr int MMA_SMEM = 227 * 1024;
@@ -241,7 +244,8 @@ __global__ void __launch_bounds__(MMA_THREADS, (Shape<TC, kCtas>::PER_SM))
                    const __grid_constant__ CUtensorMap map_o, const __grid_constant__ MmaArgs<O> a) {
   using S = Shape<TC, kCtas>;
   constexpr bool kWeights = kP == Product::kWeights, kASK = kP == Product::kForward, kBSK = !kWeights;  // operands along k
-  constexpr bool kSections = kWeights && sizeof(O) == 4;
+  constexpr bool kShort = kWeights && sizeof(O) == 4;
+  constexpr int32_t SECTION = kShort ? MMA_SECTION : MMA_LONG_SECTION;
   constexpr uint32_t COLUMNS = 2 * TC;  // two accumulators
   constexpr uint32_t TMEM = COLUMNS <= 64 ? 64 : COLUMNS <= 128 ? 128 : COLUMNS <= 256 ? 256 : 512;
   static_assert(COLUMNS <= 512, "tensor memory has 512 columns");
@@ -386,7 +390,7 @@ __global__ void __launch_bounds__(MMA_THREADS, (Shape<TC, kCtas>::PER_SM))
           if (!ok) break;
           tmem_after_sync();
           const uint32_t d = tmem + acc * TC;
-          int32_t section = kSections ? MMA_SECTION : INT32_MAX;
+          int32_t section = SECTION;
           bool add = false;
           for (; rest > 0 && section > 0; rest -= MMA_K, --section) {
             ok = wait_all(full + s, parity);
@@ -505,50 +509,13 @@ __global__ void __launch_bounds__(MMA_THREADS, (Shape<TC, kCtas>::PER_SM))
       const int n = x.c1 - x.c0;
       O* o = a.o + x.e * a.o_e + x.slice * a.o_s + int64_t(x.c0) * a.o_c + f;
       const bool rows_on = GRS_CHECK(kWeights || (x.c0 >= 0 && x.c1 <= a.rows), mma_flags, SITE_MMA_ROW), on = rows_on && f < a.f;
-      const int32_t sections = kSections ? (blocks + MMA_SECTION - 1) / MMA_SECTION : 1;
-      // fp32: the thread's columns are added up in its registers, section by section.
-      constexpr int PARTS = kSections ? TC / 64 : 1;
-      float sum[PARTS][32];
-      if constexpr (kSections) {
-#pragma unroll
-        for (int p = 0; p < PARTS; ++p)
-#pragma unroll
-          for (int j = 0; j < 32; ++j) sum[p][j] = 0.0f;
-      }
-      for (int32_t i = 0; i < sections && blocks > 0; ++i) {
+      const int32_t sections = (blocks + SECTION - 1) / SECTION;
+      auto begin = [&] {
         ok = wait_all(done + acc, parity);
-        if (!ok) break;
         tmem_after_sync();
-        if constexpr (kSections) {
-#pragma unroll
-          for (int p = 0; p < 2 * PARTS; ++p) {
-            if (64 * (p / 2) + 32 * half + p % 2 * 16 >= n) break;
-            uint32_t v[16];
-            tmem_load16(from + acc * TC + p / 2 * 64 + p % 2 * 16, v);
-            tmem_wait_load();
-#pragma unroll
-            for (int j = 0; j < 16; ++j) sum[p / 2][p % 2 * 16 + j] = __fadd_rn(sum[p / 2][p % 2 * 16 + j], __uint_as_float(v[j]));
-          }
-        } else {
-          for (int j0 = 32 * half; j0 < n; j0 += 64) {
-            if constexpr (S::TURNED && sizeof(O) == 2) {
-              if (turned) {
-                const int piece = (lane & 3) * 8 - lane;  // from this lane's feature to its piece's
-                const int64_t f0 = f - lane;
-                // Rows behind the result's and features behind its width are cut off by the map.
-                store_turned(from + acc * TC + j0 - 32 * half, place, &map_o, static_cast<int32_t>(f0), x.c0 + j0, kWeights ? x.e : 0,
-                             rows_on && f0 < a.f && (kWeights || n - j0 >= 32), o + piece + (j0 + (lane >> 2)) * a.o_c, a.o_c, n - j0,
-                             rows_on && f + piece < a.f);
-                continue;
-              }
-            }
-            uint32_t v[32];
-            tmem_load32(from + acc * TC + j0 - 32 * half, v);
-            tmem_wait_load();
-            store_columns(o + j0 * a.o_c, a.o_c, v, n - j0, on);
-            __syncwarp();
-          }
-        }
+        return ok;
+      };
+      auto end = [&] {
         tmem_before_sync();
         __syncwarp();
         if (lane == 0) {
@@ -557,21 +524,64 @@ __global__ void __launch_bounds__(MMA_THREADS, (Shape<TC, kCtas>::PER_SM))
         }
         acc ^= 1;
         if (acc == 0) parity ^= 1;
-      }
-      if (!ok) break;
-      if constexpr (kSections) {
+      };
+      if (kShort || sections > 1) {
+        // The thread's columns are added up in its registers, section by section.
+        constexpr int PARTS = TC >= 64 ? TC / 64 : 1, EACH = TC < 32 ? TC : 32;
+        float sum[PARTS][EACH];
+#pragma unroll
+        for (int p = 0; p < PARTS; ++p)
+#pragma unroll
+          for (int j = 0; j < EACH; ++j) sum[p][j] = 0.0f;
+        for (int32_t i = 0; i < sections; ++i) {
+          if (!begin()) break;
+#pragma unroll
+          for (int p = 0; p < PARTS * EACH / 16; ++p) {
+            const int part = p * 16 / EACH, q = p * 16 % EACH;
+            if (64 * part + 32 * half + q >= n) break;
+            uint32_t v[16];
+            tmem_load16(from + acc * TC + 64 * part + q, v);
+            tmem_wait_load();
+#pragma unroll
+            for (int j = 0; j < 16; ++j) sum[part][q + j] = __fadd_rn(sum[part][q + j], __uint_as_float(v[j]));
+          }
+          end();
+        }
+        if (!ok) break;
 #pragma unroll
         for (int p = 0; p < PARTS; ++p) {
           const int j0 = 64 * p + 32 * half;
           if (j0 >= n) break;
           O* q = o + j0 * a.o_c;
 #pragma unroll
-          for (int j = 0; j < 32; ++j) {
+          for (int j = 0; j < EACH; ++j) {
             if (on && j0 + j < n) *q = from_float<O>(sum[p][j]);
             q += a.o_c;
           }
         }
-      } else if (blocks == 0) {  // an expert without rows, a slice without k
+        __syncwarp();
+      } else if (sections == 1) {
+        if (!begin()) break;
+        for (int j0 = 32 * half; j0 < n; j0 += 64) {
+          if constexpr (S::TURNED && sizeof(O) == 2) {
+            if (turned) {
+              const int piece = (lane & 3) * 8 - lane;  // from this lane's feature to its piece's
+              const int64_t f0 = f - lane;
+              // Rows behind the result's and features behind its width are cut off by the map.
+              store_turned(from + acc * TC + j0 - 32 * half, place, &map_o, static_cast<int32_t>(f0), x.c0 + j0, kWeights ? x.e : 0,
+                           rows_on && f0 < a.f && (kWeights || n - j0 >= 32), o + piece + (j0 + (lane >> 2)) * a.o_c, a.o_c, n - j0,
+                           rows_on && f + piece < a.f);
+              continue;
+            }
+          }
+          uint32_t v[32];
+          tmem_load32(from + acc * TC + j0 - 32 * half, v);
+          tmem_wait_load();
+          store_columns(o + j0 * a.o_c, a.o_c, v, n - j0, on);
+          __syncwarp();
+        }
+        end();
+      } else {  // an expert without rows, a slice without k
         if (kWeights && turned) {
           const int64_t f0 = f - lane;
           bulk_wait_read();

@@ -873,7 +873,10 @@ typedef struct grs_experts {
  *             (values outside are taken as the nearest of them).
  *   workspace : device, 16-byte aligned, grs_experts_workspace_bytes (not
  *             initialised); NULL where that is 0.  Calls that share one must not overlap.
- * bf16 runs on the tensor cores.  Which sums are cut into parts goes by the shape.
+ * bf16 runs on the tensor cores, which add up to 4096 of a sum (512 of a
+ * gradient in fp32) with rounding towards zero, up to 2^-15 (2^-18) of its
+ * magnitudes, and fp32 additions join these.  Which sums are cut into parts goes
+ * by the shape.
  * Rows outside [offsets[0], offsets[experts]) are neither read for a result nor
  * written; NaN in them changes nothing.  xs, w and dys start at multiples of 16
  * bytes, outputs at multiples of their element.  In bf16, widths and row

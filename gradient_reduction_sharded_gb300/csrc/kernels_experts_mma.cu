@@ -238,14 +238,16 @@ __device__ __forceinline__ void store_turned(uint32_t from, uint32_t place, cons
   }
 }
 
-template <Product kP, int TC, int kCtas, typename O>
+// kLong: k may be more than MMA_LONG_SECTION stages.  Short k, which stores bound, does without the registers of its sums
+// (32768 rows, 8 experts, 256 -> 2432: 39.0 us, with them 39.4).
+template <Product kP, int TC, int kCtas, typename O, bool kLong>
 __global__ void __launch_bounds__(MMA_THREADS, (Shape<TC, kCtas>::PER_SM))
     exp_mma_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
                    const __grid_constant__ CUtensorMap map_o, const __grid_constant__ MmaArgs<O> a) {
   using S = Shape<TC, kCtas>;
   constexpr bool kWeights = kP == Product::kWeights, kASK = kP == Product::kForward, kBSK = !kWeights;  // operands along k
   constexpr bool kShort = kWeights && sizeof(O) == 4;
-  constexpr int32_t SECTION = kShort ? MMA_SECTION : MMA_LONG_SECTION;
+  constexpr int32_t SECTION = kShort ? MMA_SECTION : kLong ? MMA_LONG_SECTION : INT32_MAX;
   constexpr uint32_t COLUMNS = 2 * TC;  // two accumulators
   constexpr uint32_t TMEM = COLUMNS <= 64 ? 64 : COLUMNS <= 128 ? 128 : COLUMNS <= 256 ? 256 : 512;
   static_assert(COLUMNS <= 512, "tensor memory has 512 columns");
@@ -494,7 +496,7 @@ __global__ void __launch_bounds__(MMA_THREADS, (Shape<TC, kCtas>::PER_SM))
     }
   } else if (w >= 4) {
     // ------------------------------------------------------------ results
-    uint32_t acc = 0, parity = 0;
+    uint32_t taken_so_far = 0;  // accumulators: their turn and their barriers' parity
     bool ok = true;
     const int quarter = w & 3, half = (w - 4) >> 2;  // 32 lanes; every second 32 columns
     const uint32_t from = tmem + (uint32_t(quarter) << 21) + 32 * half;
@@ -504,14 +506,16 @@ __global__ void __launch_bounds__(MMA_THREADS, (Shape<TC, kCtas>::PER_SM))
       Tile x;
       ok = next_tile(x);
       if (!ok || x.e < 0) break;
-      const int32_t blocks = (x.k1 - x.k0 + MMA_K - 1) / MMA_K;
-      const int64_t f = x.f0 + int64_t(rank) * MMA_F + quarter * 32 + lane;
+      const int32_t blocks = (x.k1 - x.k0 + MMA_K - 1) / MMA_K, width = static_cast<int32_t>(a.f);
+      const int32_t f = x.f0 + static_cast<int32_t>(rank) * MMA_F + quarter * 32 + lane;
       const int n = x.c1 - x.c0;
       O* o = a.o + x.e * a.o_e + x.slice * a.o_s + int64_t(x.c0) * a.o_c + f;
-      const bool rows_on = GRS_CHECK(kWeights || (x.c0 >= 0 && x.c1 <= a.rows), mma_flags, SITE_MMA_ROW), on = rows_on && f < a.f;
-      const int32_t sections = (blocks + SECTION - 1) / SECTION;
+      const bool rows_on = GRS_CHECK(kWeights || (x.c0 >= 0 && x.c1 <= a.rows), mma_flags, SITE_MMA_ROW), on = rows_on && f < width;
+      const int32_t sections = blocks / SECTION + (blocks % SECTION != 0);
+      uint32_t acc;
       auto begin = [&] {
-        ok = wait_all(done + acc, parity);
+        acc = taken_so_far & 1;
+        ok = wait_all(done + acc, taken_so_far >> 1 & 1);
         tmem_after_sync();
         return ok;
       };
@@ -520,13 +524,13 @@ __global__ void __launch_bounds__(MMA_THREADS, (Shape<TC, kCtas>::PER_SM))
         __syncwarp();
         if (lane == 0) {
           if (kCtas == 1) mbar_arrive(taken + acc);
-          else remote_arrive(rank == 0 ? smem_addr(taken + acc) : peer_addr(smem_addr(taken + acc), 0));
+          else remote_arrive(peer_addr(smem_addr(taken + acc), 0));
         }
-        acc ^= 1;
-        if (acc == 0) parity ^= 1;
+        ++taken_so_far;
       };
-      if (kShort || sections > 1) {
-        // The thread's columns are added up in its registers, section by section.
+      if (kShort || (kLong && sections > 1)) {
+        // The thread's columns are added up in its registers, section by section, eight at a time: with 16 the registers
+        // run over, and a kernel with a stack took 0.5 to 1 us more (5000 rows, 32 experts, 1024 -> 1024, 21.9 to 22.9).
         constexpr int PARTS = TC >= 64 ? TC / 64 : 1, EACH = TC < 32 ? TC : 32;
         float sum[PARTS][EACH];
 #pragma unroll
@@ -536,14 +540,14 @@ __global__ void __launch_bounds__(MMA_THREADS, (Shape<TC, kCtas>::PER_SM))
         for (int32_t i = 0; i < sections; ++i) {
           if (!begin()) break;
 #pragma unroll
-          for (int p = 0; p < PARTS * EACH / 16; ++p) {
-            const int part = p * 16 / EACH, q = p * 16 % EACH;
+          for (int p = 0; p < PARTS * EACH / 8; ++p) {
+            const int part = p * 8 / EACH, q = p * 8 % EACH;
             if (64 * part + 32 * half + q >= n) break;
-            uint32_t v[16];
-            tmem_load16(from + acc * TC + 64 * part + q, v);
+            uint32_t v[8];
+            tmem_load8(from + acc * TC + 64 * part + q, v);
             tmem_wait_load();
 #pragma unroll
-            for (int j = 0; j < 16; ++j) sum[part][q + j] = __fadd_rn(sum[part][q + j], __uint_as_float(v[j]));
+            for (int j = 0; j < 8; ++j) sum[part][q + j] = __fadd_rn(sum[part][q + j], __uint_as_float(v[j]));
           }
           end();
         }
@@ -566,9 +570,9 @@ __global__ void __launch_bounds__(MMA_THREADS, (Shape<TC, kCtas>::PER_SM))
           if constexpr (S::TURNED && sizeof(O) == 2) {
             if (turned) {
               const int piece = (lane & 3) * 8 - lane;  // from this lane's feature to its piece's
-              const int64_t f0 = f - lane;
+              const int32_t f0 = f - lane;
               // Rows behind the result's and features behind its width are cut off by the map.
-              store_turned(from + acc * TC + j0 - 32 * half, place, &map_o, static_cast<int32_t>(f0), x.c0 + j0, kWeights ? x.e : 0,
+              store_turned(from + acc * TC + j0 - 32 * half, place, &map_o, f0, x.c0 + j0, kWeights ? x.e : 0,
                            rows_on && f0 < a.f && (kWeights || n - j0 >= 32), o + piece + (j0 + (lane >> 2)) * a.o_c, a.o_c, n - j0,
                            rows_on && f + piece < a.f);
               continue;
@@ -583,14 +587,14 @@ __global__ void __launch_bounds__(MMA_THREADS, (Shape<TC, kCtas>::PER_SM))
         end();
       } else {  // an expert without rows, a slice without k
         if (kWeights && turned) {
-          const int64_t f0 = f - lane;
+          const int32_t f0 = f - lane;
           bulk_wait_read();
           __syncwarp();
           for (int i = lane; i < 32 * TURN_ROW / 16; i += 32) store_piece(place + i * 16, make_uint4(0, 0, 0, 0));
           fence_async_shared();
           __syncwarp();
           if (lane == 0 && f0 < a.f) {
-            for (int j0 = 32 * half; j0 < n; j0 += 64) tma_store(&map_o, place, static_cast<int32_t>(f0), x.c0 + j0, x.e);
+            for (int j0 = 32 * half; j0 < n; j0 += 64) tma_store(&map_o, place, f0, x.c0 + j0, x.e);
             bulk_commit();
           }
         } else if (on) {
@@ -643,9 +647,9 @@ bool make_map(CUtensorMap* m, const void* p, int n, const int64_t (&dims)[3], co
            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <Product kP, int TC, int kCtas, typename O>
-cudaError_t mma_launch(const grs_experts* s, const ExpLd& ld, const void* xs, const void* w, const void* dys, const int32_t* offsets,
-                       void* o, int64_t o_ld, const ExpSlices& sl, void* stream) {
+template <Product kP, int TC, int kCtas, typename O, bool kLong>
+cudaError_t mma_launch_as(const grs_experts* s, const ExpLd& ld, const void* xs, const void* w, const void* dys, const int32_t* offsets,
+                          void* o, int64_t o_ld, const ExpSlices& sl, void* stream) {
   using S = Shape<TC, kCtas>;
   const int64_t in = s->in_features, out = s->out_features;
   CUtensorMap ma, mb, mo{};
@@ -680,9 +684,20 @@ cudaError_t mma_launch(const grs_experts* s, const ExpLd& ld, const void* xs, co
   const int64_t at_once = kP == Product::kWeights ? INT32_MAX / kCtas : S::PER_SM * 152 / kCtas;
   if (kP == Product::kWeights && tiles > at_once) return cudaErrorInvalidConfiguration;
   const unsigned grid = static_cast<unsigned>((tiles < at_once ? tiles : at_once) * kCtas);
-  const cudaError_t e = allow_smem<exp_mma_kernel<kP, TC, kCtas, O>>(S::BYTES);
+  const cudaError_t e = allow_smem<exp_mma_kernel<kP, TC, kCtas, O, kLong>>(S::BYTES);
   if (e != cudaSuccess) return e;
-  return launch_pdl_cluster(exp_mma_kernel<kP, TC, kCtas, O>, kCtas, dim3(grid), dim3(MMA_THREADS), S::BYTES, stream, ma, mb, mo, a);
+  return launch_pdl_cluster(exp_mma_kernel<kP, TC, kCtas, O, kLong>, kCtas, dim3(grid), dim3(MMA_THREADS), S::BYTES, stream, ma, mb, mo, a);
+}
+
+template <Product kP, int TC, int kCtas, typename O>
+cudaError_t mma_launch(const grs_experts* s, const ExpLd& ld, const void* xs, const void* w, const void* dys, const int32_t* offsets,
+                       void* o, int64_t o_ld, const ExpSlices& sl, void* stream) {
+  constexpr bool kShort = kP == Product::kWeights && sizeof(O) == 4;  // has sections of its own
+  // An expert may have all of the rows.
+  const int64_t k = kP == Product::kWeights ? s->rows : kP == Product::kForward ? s->in_features : s->out_features;
+  if (!kShort && slice_length<MMA_SECTION * MMA_K>(k, sl.n) > MMA_LONG_SECTION * MMA_K)
+    return mma_launch_as<kP, TC, kCtas, O, !kShort>(s, ld, xs, w, dys, offsets, o, o_ld, sl, stream);
+  return mma_launch_as<kP, TC, kCtas, O, false>(s, ld, xs, w, dys, offsets, o, o_ld, sl, stream);
 }
 
 template <Product kP, int TC>

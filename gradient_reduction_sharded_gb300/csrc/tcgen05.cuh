@@ -166,12 +166,10 @@ __device__ __forceinline__ void tmem_load32(uint32_t address, uint32_t (&v)[32])
         "=r"(v[31])
       : "r"(address));
 }
-__device__ __forceinline__ void tmem_load16(uint32_t address, uint32_t (&v)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
-      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]),
-        "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
-      : "r"(address));
+__device__ __forceinline__ void tmem_load8(uint32_t address, uint32_t (&v)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+               : "r"(address));
 }
 // 32 columns of 16 lanes: as a matrix instruction's result, v[4 i ..] the eight
 // columns from 8 i on: of lane t / 4 those from 2 (t % 4) on, two, and the same of

@@ -967,7 +967,9 @@ grs_status grs_rope_turns(const double* inv_freq, int32_t n, uint64_t* turns);
 
 /* For each head x of D elements: u = x / sqrt(sum x^2 / D + eps) * w; then pair
  * i of the first rotary_dim elements, (a, b), becomes (a cos - b sin, a sin + b
- * cos) of positions[t] * inv_freq[i].  In fp32, rounded once.
+ * cos) of positions[t] * inv_freq[i].  In fp32, rounded once; sines and cosines
+ * to two fp32 units of their angle's fraction of a turn in 32 bits, for outputs
+ * in bf16 to 2^-21.
  *   q, k, qo, ko : device, aligned to the element; 16-byte aligned heads (row
  *             distances and head_dim multiples of 8 elements) are fastest.
  *   wq, wk  : device [D], or NULL (1).
@@ -982,8 +984,8 @@ grs_status grs_qk_norm_forward(const grs_qk_norm* shape, const void* q, const vo
  * x^2 / D + eps) and dh = du * w:
  *   dx = r * (dh - h * sum(dh * h) / D),  dw = sum over tokens and heads of du * h
  * (overwritten; zeros without tokens or heads), each of the four NULL if not wanted.
- * Sums in fp32 in an order that the shape, the types and whether heads are
- * whole 16-byte chunks fix.  workspace: device, 16-byte aligned,
+ * Sines and cosines as for outputs in fp32.  Sums in fp32 in an order that the
+ * shape, the types and whether heads are whole 16-byte chunks fix.  workspace: device, 16-byte aligned,
  * grs_qk_norm_workspace_bytes (not initialised), needed for dwq or dwk; calls
  * that share one must not overlap.  dq may be dqo itself where ld_q = ld_qo, dk
  * dko likewise; otherwise no output may overlap an input. */

@@ -103,6 +103,24 @@ def test_ends_of_experts(cuda, counts, k, n, act, grad, pad):
     Exact(counts, k, n, act, grad, first=5, tail=40, pad_x=pad, pad_y=2 * pad).check()
 
 
+# Up to eight rows in all, which forward leaves to the ordinary cores, and nine and widths that it does not: several and
+# empty experts, a second group of four rows, odd numbers of results, k below a warp's 256 and beyond, rows inside wider ones.
+@on_gpu
+@pytest.mark.parametrize("counts", [[1], [8], [5, 0, 3], [0, 4, 0, 1, 2], [0, 0, 7, 1, 0], [1] * 8, [9], [3, 0, 6]])
+@pytest.mark.parametrize("n", [1, 7, 64, 129])
+@pytest.mark.parametrize("k", [8, 136, 1032, 2056, 35])
+def test_a_few_rows(cuda, counts, n, k):
+    Exact(counts, k, n).check()
+    Exact(counts, k, n, pad_x=8, pad_y=3).check()
+
+
+@on_gpu
+@pytest.mark.parametrize("counts, first, tail", [([1], 3, 4), ([4, 2], 1, 1), ([0, 5, 0], 0, 3), ([2, 0, 1, 3], 2, 0), ([0, 0], 4, 4)])
+@pytest.mark.parametrize("n, k, pad", [(7, 136, 0), (130, 1032, 8), (1, 8, 16)])
+def test_a_few_rows_of_which_some_are_no_expert_s(cuda, counts, first, tail, n, k, pad):
+    Exact(counts, k, n, first=first, tail=tail, pad_x=pad, pad_y=1).check()
+
+
 @pytest.mark.parametrize("counts, k, n", [([20003], 8, 16), ([0, 9000, 0], 72, 24), ([5000, 3], 64, 40)])
 @pytest.mark.parametrize("grad", ["bf16", "fp32"])
 def test_one_row_left_out_would_show(counts, k, n, grad):

@@ -13,9 +13,10 @@
 // MB).  Others go a warp a head, element by element (forward 203, backward 331
 // for the same).  Pairs kept in 64-bit registers changed nothing (50 and 45).
 //
-// Angles: a frequency is a fraction of a turn in 64 bits, and a position times
-// it modulo 2^64 the fraction of its angle, without rounding at any position;
-// its upper 32 bits go to sincospi.
+// Angles: a frequency is a fraction of a turn, rounded to 64 bits, and a position
+// times it modulo 2^64 the fraction of its angle: the product adds no rounding,
+// and the frequency's grows to 2^-33 of a turn at position 2^31.  Its upper 32
+// bits go to sincospi.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -706,6 +707,13 @@ grs_status check_qk(const grs_qk_norm* s, const char* who, int64_t (&ld)[4]) {
   return GRS_OK;
 }
 
+// x modulo 1 in units of 2^-64, rounded to the nearest.
+uint64_t fraction64(double x) {
+  const double a = std::fabs(x), f = a - std::floor(a), hi = std::floor(f * 0x1p32);  // (all exact; two halves: 2^64 does not fit)
+  const uint64_t t = (static_cast<uint64_t>(hi) << 32) + static_cast<uint64_t>(std::floor((f * 0x1p32 - hi) * 0x1p32 + 0.5));
+  return x < 0 ? 0 - t : t;
+}
+
 // Blocks of the backward pass and so parts of dwq and dwk: what any of its kernels has at most.
 int qk_blocks(const grs_qk_norm* s) {
   const int64_t b = (s->tokens * (s->q_heads + s->k_heads) + QK_WARPS - 1) / QK_WARPS;
@@ -852,10 +860,10 @@ grs_status grs_rope_turns(const double* inv_freq, int32_t n, uint64_t* turns) {
   if (n < 0 || (n > 0 && (inv_freq == nullptr || turns == nullptr))) return api_fail(GRS_ERR_INVALID_ARG, who, "NULL argument or n < 0");
   for (int32_t i = 0; i < n; ++i) {
     if (!std::isfinite(inv_freq[i])) return api_fail(GRS_ERR_INVALID_ARG, who, "a frequency that is not finite");
-    double f = inv_freq[i] / 6.283185307179586476925;
-    f -= std::floor(f);                          // exact for f >= 0; [0, 1], 1 by rounding of a tiny negative f
-    const double hi = std::floor(f * 0x1p32);    // two halves: 2^64 itself does not fit
-    turns[i] = (static_cast<uint64_t>(hi) << 32) + static_cast<uint64_t>(std::floor((f * 0x1p32 - hi) * 0x1p32 + 0.5));
+    // 1 / (2 pi) in two doubles, so that the product in two doubles is good to 2^-107 of the frequency.
+    const double f = inv_freq[i], inv_hi = 0.15915494309189535, inv_lo = -9.839338337591243e-18;
+    const double p = f * inv_hi, rest = std::fma(f, inv_lo, std::fma(f, inv_hi, -p));
+    turns[i] = fraction64(p) + fraction64(rest);
   }
   return GRS_OK;
 }

@@ -960,8 +960,8 @@ typedef struct grs_qk_norm {
 
 /* Frequencies of the rotation for the calls below: turns[i] = inv_freq[i] / (2
  * pi) as a fraction of 2^64 (host arrays; copy `turns` to the device).  A
- * position's angle is position * turns[i] modulo 2^64, exact to |position| *
- * 2^-53 of a turn.  Any finite inv_freq
+ * position's angle is position * turns[i] modulo 2^64: off by |position| *
+ * (2^-64 + |inv_freq[i]| * 2^-107) of a turn at most.  Any finite inv_freq
  * (base^(-2 i / rotary_dim), or one stretched for longer contexts).  Errors: INVALID_ARG. */
 grs_status grs_rope_turns(const double* inv_freq, int32_t n, uint64_t* turns);
 

@@ -22,6 +22,11 @@ struct ExpLd {
   int64_t x, y, w;  // elements from one row to the next of xs and dxs, of ys and dys, of w
 };
 
+// The self-test has the loads of block `quitter` give up at its `tile`th tile.
+struct ExpQuit {
+  int32_t quitter = -1, tile = 0;
+};
+
 // Where a product has few tiles with a long k, k is cut into slices whose
 // results (fp32) are added up afterwards.
 struct ExpSlices {
@@ -46,6 +51,6 @@ ExpTiles experts_mma_tiles(Product p, const grs_experts* s);
 // One product in bf16; xs, w and dys 16-byte aligned, the row distances of
 // those that it reads multiples of 8.  o_ld: of the result's rows.
 cudaError_t experts_mma(Product p, const grs_experts* s, const ExpLd& ld, const void* xs, const void* w, const void* dys,
-                        const int32_t* offsets, void* o, int64_t o_ld, const ExpSlices& slices, void* stream);
+                        const int32_t* offsets, void* o, int64_t o_ld, const ExpSlices& slices, const ExpQuit& quit, void* stream);
 
 }  // namespace grs

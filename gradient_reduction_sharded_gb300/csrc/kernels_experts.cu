@@ -387,13 +387,13 @@ cudaError_t exp_join(Product p, const grs_experts* s, const ExpSlices& sl, const
 // One product to `o`, rows o_ld apart; parts: room for its slices.
 template <Product kP>
 cudaError_t exp_product(const grs_experts* s, const ExpLd& ld, const void* xs, const void* w, const void* dys, const int32_t* offsets, void* o,
-                        int64_t o_ld, void* parts, void* stream) {
+                        int64_t o_ld, void* parts, const ExpQuit& quit, void* stream) {
   ExpSlices sl = exp_slices(kP, s);
   sl.parts = static_cast<float*>(parts);
   const bool fp32 = (kP == Product::kWeights ? s->grad_dtype : s->dtype) == GRS_DTYPE_FP32;
   cudaError_t e;
   if (s->dtype == GRS_DTYPE_BF16) {
-    e = experts_mma(kP, s, ld, xs, w, dys, offsets, o, o_ld, sl, stream);
+    e = experts_mma(kP, s, ld, xs, w, dys, offsets, o, o_ld, sl, quit, stream);
   } else {
     const void *a = kP == Product::kWeights ? xs : w, *b = kP == Product::kForward ? xs : dys;
     if (fp32 || sl.n > 1) e = exp_general<kP, float>(s, ld, a, b, offsets, o, sl, stream);
@@ -518,6 +518,42 @@ int64_t exp_workspace(const grs_experts* s, const ExpLd& ld, int64_t* pads) {
   return *pads + ((most + 15) & ~int64_t(15));
 }
 
+grs_status experts_backward(const grs_experts* s, const void* dys, const void* xs, const void* w, const int32_t* offsets, void* dxs, void* dw,
+                            void* workspace, const ExpQuit& quit, void* stream, const char* who) {
+  ExpLd ld;
+  const grs_status st = check_experts(s, who, &ld);
+  if (st != GRS_OK) return st;
+  if (!api_aligned(dys, 16) || !api_aligned(xs, 16) || !api_aligned(w, 16) || !api_aligned(offsets, 4) ||
+      !api_aligned(dxs, dtype_size(s->dtype)) || !api_aligned(dw, dtype_size(s->grad_dtype)) || !api_aligned(workspace, 16))
+    return api_fail(GRS_ERR_ALIGNMENT, who, "a misaligned pointer");
+  if (s->rows == 0) {
+    if (dw == nullptr) return GRS_OK;
+    const size_t bytes = size_t(s->experts) * s->in_features * s->out_features * dtype_size(s->grad_dtype);
+    const cudaError_t e = cudaMemsetAsync(dw, 0, bytes, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? GRS_OK : api_cuda_fail(e, who);
+  }
+  if (offsets == nullptr || (dys == nullptr && (dxs != nullptr || dw != nullptr)) || (w == nullptr && dxs != nullptr) ||
+      (xs == nullptr && dw != nullptr))
+    return api_fail(GRS_ERR_INVALID_ARG, who, "NULL argument");
+  int64_t pad = 0;
+  if (exp_workspace(s, ld, &pad) > 0 && workspace == nullptr) return api_fail(GRS_ERR_INVALID_ARG, who, "this shape needs a workspace");
+  cudaError_t e = cudaSuccess;
+  if (dxs != nullptr || dw != nullptr) {
+    const int64_t ld_x = ld.x;
+    uint8_t* parts = static_cast<uint8_t*>(workspace) + pad;
+    if (s->dtype == GRS_DTYPE_BF16) {
+      Pads pads(workspace);
+      dys = pads.add(dys, s->rows, &ld.y, s->out_features);
+      if (dxs != nullptr) w = pads.add(w, int64_t(s->experts) * s->out_features, &ld.w, s->in_features);
+      if (dw != nullptr) xs = pads.add(xs, s->rows, &ld.x, s->in_features);
+      e = pads.run(stream);
+    }
+    if (e == cudaSuccess && dxs != nullptr) e = exp_product<Product::kRows>(s, ld, nullptr, w, dys, offsets, dxs, ld_x, parts, quit, stream);
+    if (e == cudaSuccess && dw != nullptr) e = exp_product<Product::kWeights>(s, ld, xs, nullptr, dys, offsets, dw, s->in_features, parts, quit, stream);
+  }
+  return e == cudaSuccess ? GRS_OK : api_cuda_fail(e, who);
+}
+
 }  // namespace
 
 cudaError_t take_experts_flags(int (&total)[FLAG_COUNT], cudaStream_t st) { return take_flags(exp_flags, total, st); }
@@ -574,46 +610,22 @@ grs_status grs_experts_forward(const grs_experts* s, const void* xs, const void*
       w = pads.add(w, int64_t(s->experts) * s->out_features, &ld.w, s->in_features);
       e = pads.run(stream);
     }
-    if (e == cudaSuccess) e = exp_product<Product::kForward>(s, ld, xs, w, nullptr, offsets, ys, ld_y, static_cast<uint8_t*>(workspace) + pad, stream);
+    if (e == cudaSuccess) e = exp_product<Product::kForward>(s, ld, xs, w, nullptr, offsets, ys, ld_y, static_cast<uint8_t*>(workspace) + pad, ExpQuit{}, stream);
   }
   return e == cudaSuccess ? GRS_OK : api_cuda_fail(e, who);
 }
 
 grs_status grs_experts_backward(const grs_experts* s, const void* dys, const void* xs, const void* w, const int32_t* offsets, void* dxs,
                                 void* dw, void* workspace, void* stream) {
-  static const char who[] = "grs_experts_backward";
-  ExpLd ld;
-  const grs_status st = check_experts(s, who, &ld);
-  if (st != GRS_OK) return st;
-  if (!api_aligned(dys, 16) || !api_aligned(xs, 16) || !api_aligned(w, 16) || !api_aligned(offsets, 4) ||
-      !api_aligned(dxs, dtype_size(s->dtype)) || !api_aligned(dw, dtype_size(s->grad_dtype)) || !api_aligned(workspace, 16))
-    return api_fail(GRS_ERR_ALIGNMENT, who, "a misaligned pointer");
-  if (s->rows == 0) {
-    if (dw == nullptr) return GRS_OK;
-    const size_t bytes = size_t(s->experts) * s->in_features * s->out_features * dtype_size(s->grad_dtype);
-    const cudaError_t e = cudaMemsetAsync(dw, 0, bytes, static_cast<cudaStream_t>(stream));
-    return e == cudaSuccess ? GRS_OK : api_cuda_fail(e, who);
-  }
-  if (offsets == nullptr || (dys == nullptr && (dxs != nullptr || dw != nullptr)) || (w == nullptr && dxs != nullptr) ||
-      (xs == nullptr && dw != nullptr))
-    return api_fail(GRS_ERR_INVALID_ARG, who, "NULL argument");
-  int64_t pad = 0;
-  if (exp_workspace(s, ld, &pad) > 0 && workspace == nullptr) return api_fail(GRS_ERR_INVALID_ARG, who, "this shape needs a workspace");
-  cudaError_t e = cudaSuccess;
-  if (dxs != nullptr || dw != nullptr) {
-    const int64_t ld_x = ld.x;
-    uint8_t* parts = static_cast<uint8_t*>(workspace) + pad;
-    if (s->dtype == GRS_DTYPE_BF16) {
-      Pads pads(workspace);
-      dys = pads.add(dys, s->rows, &ld.y, s->out_features);
-      if (dxs != nullptr) w = pads.add(w, int64_t(s->experts) * s->out_features, &ld.w, s->in_features);
-      if (dw != nullptr) xs = pads.add(xs, s->rows, &ld.x, s->in_features);
-      e = pads.run(stream);
-    }
-    if (e == cudaSuccess && dxs != nullptr) e = exp_product<Product::kRows>(s, ld, nullptr, w, dys, offsets, dxs, ld_x, parts, stream);
-    if (e == cudaSuccess && dw != nullptr) e = exp_product<Product::kWeights>(s, ld, xs, nullptr, dys, offsets, dw, s->in_features, parts, stream);
-  }
-  return e == cudaSuccess ? GRS_OK : api_cuda_fail(e, who);
+  return experts_backward(s, dys, xs, w, offsets, dxs, dw, workspace, ExpQuit{}, stream, "grs_experts_backward");
+}
+
+grs_status grs_selftest_experts_wait(const grs_experts* s, const void* dys, const void* xs, const void* w, const int32_t* offsets, void* dxs,
+                                     void* dw, void* workspace, int32_t quitter, int32_t quit_tile, void* stream) {
+  static const char who[] = "grs_selftest_experts_wait";
+  if (quitter < 0 || quit_tile < 0) return api_fail(GRS_ERR_INVALID_ARG, who, "quitter and quit_tile must be >= 0");
+  if (s != nullptr && s->dtype != GRS_DTYPE_BF16) return api_fail(GRS_ERR_INVALID_ARG, who, "only products in bf16 have such waits");
+  return experts_backward(s, dys, xs, w, offsets, dxs, dw, workspace, ExpQuit{quitter, quit_tile}, stream, who);
 }
 
 }  // extern "C"

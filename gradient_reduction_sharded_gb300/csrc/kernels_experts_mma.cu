@@ -92,6 +92,7 @@ struct MmaArgs {
   int64_t f, c, k;         // extents; an expert's rows in the place of c or k
   int32_t rows, experts, slices;
   int32_t pieces;          // rows of the result are whole 16-byte pieces
+  ExpQuit quit;
 };
 
 struct Tile {
@@ -174,10 +175,6 @@ __device__ __forceinline__ uint4 shared_piece(uint32_t at) {
   uint4 v;
   asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
   return v;
-}
-
-__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, volatile int* abort) {
-  return mbar_wait_bounded(bar, parity, mma_flags, abort);
 }
 
 // 32 columns, a lane a feature, to rows `ld` elements apart, the first n of
@@ -306,7 +303,8 @@ __global__ void __launch_bounds__(MMA_THREADS, (Shape<TC, kCtas>::PER_SM))
 
   // The next tile of the ring, for a whole warp; false: a wait gave up.
   uint32_t slot = 0, slot_parity = 0;
-  auto wait_all = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, wait_for(bar, parity, abort)) != 0; };
+  auto wait_for = [&](uint64_t* bar, uint32_t parity) { return mbar_wait_bounded(bar, parity, mma_flags, abort); };
+  auto wait_all = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, wait_for(bar, parity)) != 0; };
   auto next_tile = [&](Tile& x) {
     if (!wait_all(told + slot, slot_parity)) return false;
     const int32_t* r = reinterpret_cast<const int32_t*>(ring + slot);
@@ -333,10 +331,19 @@ __global__ void __launch_bounds__(MMA_THREADS, (Shape<TC, kCtas>::PER_SM))
     // Both blocks' loads are counted by the first one's barriers.
     const uint32_t full_at = kCtas == 1 || rank == 0 ? smem_addr(full) : peer_addr(smem_addr(full), 0);
     bool ok = true;
+    int32_t left = static_cast<int32_t>(blockIdx.x) == a.quit.quitter ? a.quit.tile : -1;
     while (ok) {
       Tile x;
       ok = next_tile(x);
       if (!ok || x.e < 0) break;
+      if (left-- == 0) {  // the self-test: as if a wait had given up
+        if (elected()) {
+          atomicOr(mma_flags + FLAG_TIMEOUT, 1);
+          *abort = 1;
+        }
+        __syncwarp();
+        break;
+      }
       const int32_t f0 = x.f0 + static_cast<int32_t>(rank) * MMA_F;
       // Columns of this block: half of the instruction's.
       const int32_t half = (x.c1 - x.c0 + 15) / 16 * 16 / kCtas;
@@ -434,12 +441,12 @@ __global__ void __launch_bounds__(MMA_THREADS, (Shape<TC, kCtas>::PER_SM))
         if (kWeights && more) {
           mbar_arrive_expect_tx(answered + q, 16);
           if (rank == 0) {
-            ok = wait_for(asked + q, q_parity ^ 1, abort);  // both blocks have read what was there
+            ok = wait_for(asked + q, q_parity ^ 1);  // both blocks have read what was there
             if (!ok) break;
             ask_cluster<kCtas>(answers + q, answered + q);
           }
         }
-        ok = wait_for(heard + slot, empty_parity, abort);
+        ok = wait_for(heard + slot, empty_parity);
         if (!ok) break;
         Tile x;
         x.e = -1;
@@ -452,7 +459,7 @@ __global__ void __launch_bounds__(MMA_THREADS, (Shape<TC, kCtas>::PER_SM))
         }
         if (!more) break;
         if constexpr (kWeights) {
-          ok = wait_for(answered + q, q_parity, abort);
+          ok = wait_for(answered + q, q_parity);
           if (!ok) break;
           t = cluster_given(answers + q);
           if (t >= 0) t /= kCtas;
@@ -605,7 +612,8 @@ __global__ void __launch_bounds__(MMA_THREADS, (Shape<TC, kCtas>::PER_SM))
     }
     bulk_wait();
   }
-  // A wait that gave up leaves copies and products under way: they end by themselves.
+  // A wait that gave up leaves copies and products under way: they end by themselves.  The cluster's other block, which
+  // misses this one's loads, arrivals or answers, gives up too, at the limit.
   if (*abort) {
     const uint64_t since = global_ns();
     while (global_ns() - since < 200000) {
@@ -649,7 +657,7 @@ bool make_map(CUtensorMap* m, const void* p, int n, const int64_t (&dims)[3], co
 
 template <Product kP, int TC, int kCtas, typename O, bool kLong>
 cudaError_t mma_launch_as(const grs_experts* s, const ExpLd& ld, const void* xs, const void* w, const void* dys, const int32_t* offsets,
-                          void* o, int64_t o_ld, const ExpSlices& sl, void* stream) {
+                          void* o, int64_t o_ld, const ExpSlices& sl, const ExpQuit& quit, void* stream) {
   using S = Shape<TC, kCtas>;
   const int64_t in = s->in_features, out = s->out_features;
   CUtensorMap ma, mb, mo{};
@@ -661,6 +669,7 @@ cudaError_t mma_launch_as(const grs_experts* s, const ExpLd& ld, const void* xs,
   a.o_s = sl.distance;
   a.rows = static_cast<int32_t>(s->rows);
   a.experts = s->experts;
+  a.quit = quit;
   bool fine;
   int64_t tiles;  // at most
   if constexpr (kP == Product::kWeights) {
@@ -691,30 +700,30 @@ cudaError_t mma_launch_as(const grs_experts* s, const ExpLd& ld, const void* xs,
 
 template <Product kP, int TC, int kCtas, typename O>
 cudaError_t mma_launch(const grs_experts* s, const ExpLd& ld, const void* xs, const void* w, const void* dys, const int32_t* offsets,
-                       void* o, int64_t o_ld, const ExpSlices& sl, void* stream) {
+                       void* o, int64_t o_ld, const ExpSlices& sl, const ExpQuit& quit, void* stream) {
   constexpr bool kShort = kP == Product::kWeights && sizeof(O) == 4;  // has sections of its own
   // An expert may have all of the rows.
   const int64_t k = kP == Product::kWeights ? s->rows : kP == Product::kForward ? s->in_features : s->out_features;
   if (!kShort && slice_length<MMA_SECTION * MMA_K>(k, sl.n) > MMA_LONG_SECTION * MMA_K)
-    return mma_launch_as<kP, TC, kCtas, O, !kShort>(s, ld, xs, w, dys, offsets, o, o_ld, sl, stream);
-  return mma_launch_as<kP, TC, kCtas, O, false>(s, ld, xs, w, dys, offsets, o, o_ld, sl, stream);
+    return mma_launch_as<kP, TC, kCtas, O, !kShort>(s, ld, xs, w, dys, offsets, o, o_ld, sl, quit, stream);
+  return mma_launch_as<kP, TC, kCtas, O, false>(s, ld, xs, w, dys, offsets, o, o_ld, sl, quit, stream);
 }
 
 template <Product kP, int TC>
 cudaError_t mma_narrow(const grs_experts* s, const ExpLd& ld, const void* xs, const void* w, const void* dys, const int32_t* offsets, void* o,
-                       int64_t o_ld, const ExpSlices& sl, void* stream) {
-  if (sl.n > 1) return mma_launch<kP, TC, 1, float>(s, ld, xs, w, dys, offsets, o, o_ld, sl, stream);
-  return mma_launch<kP, TC, 1, uint16_t>(s, ld, xs, w, dys, offsets, o, o_ld, sl, stream);
+                       int64_t o_ld, const ExpSlices& sl, const ExpQuit& quit, void* stream) {
+  if (sl.n > 1) return mma_launch<kP, TC, 1, float>(s, ld, xs, w, dys, offsets, o, o_ld, sl, quit, stream);
+  return mma_launch<kP, TC, 1, uint16_t>(s, ld, xs, w, dys, offsets, o, o_ld, sl, quit, stream);
 }
 
 template <Product kP>
 cudaError_t mma_rows(int columns, const grs_experts* s, const ExpLd& ld, const void* xs, const void* w, const void* dys, const int32_t* offsets,
-                     void* o, int64_t o_ld, const ExpSlices& sl, void* stream) {
+                     void* o, int64_t o_ld, const ExpSlices& sl, const ExpQuit& quit, void* stream) {
   switch (columns) {
-    case 16: return mma_narrow<kP, 16>(s, ld, xs, w, dys, offsets, o, o_ld, sl, stream);
-    case 64: return mma_narrow<kP, 64>(s, ld, xs, w, dys, offsets, o, o_ld, sl, stream);
-    case 128: return mma_narrow<kP, 128>(s, ld, xs, w, dys, offsets, o, o_ld, sl, stream);
-    default: return mma_launch<kP, 256, 2, uint16_t>(s, ld, xs, w, dys, offsets, o, o_ld, sl, stream);
+    case 16: return mma_narrow<kP, 16>(s, ld, xs, w, dys, offsets, o, o_ld, sl, quit, stream);
+    case 64: return mma_narrow<kP, 64>(s, ld, xs, w, dys, offsets, o, o_ld, sl, quit, stream);
+    case 128: return mma_narrow<kP, 128>(s, ld, xs, w, dys, offsets, o, o_ld, sl, quit, stream);
+    default: return mma_launch<kP, 256, 2, uint16_t>(s, ld, xs, w, dys, offsets, o, o_ld, sl, quit, stream);
   }
 }
 
@@ -752,17 +761,17 @@ ExpTiles experts_mma_tiles(Product p, const grs_experts* s) {
 }
 
 cudaError_t experts_mma(Product p, const grs_experts* s, const ExpLd& ld, const void* xs, const void* w, const void* dys,
-                        const int32_t* offsets, void* o, int64_t o_ld, const ExpSlices& sl, void* stream) {
+                        const int32_t* offsets, void* o, int64_t o_ld, const ExpSlices& sl, const ExpQuit& quit, void* stream) {
   const int columns = experts_mma_tiles(p, s).columns;
-  if (p == Product::kForward) return mma_rows<Product::kForward>(columns, s, ld, xs, w, dys, offsets, o, o_ld, sl, stream);
-  if (p == Product::kRows) return mma_rows<Product::kRows>(columns, s, ld, xs, w, dys, offsets, o, o_ld, sl, stream);
+  if (p == Product::kForward) return mma_rows<Product::kForward>(columns, s, ld, xs, w, dys, offsets, o, o_ld, sl, quit, stream);
+  if (p == Product::kRows) return mma_rows<Product::kRows>(columns, s, ld, xs, w, dys, offsets, o, o_ld, sl, quit, stream);
   const bool fp32 = s->grad_dtype == GRS_DTYPE_FP32 || sl.n > 1;
   if (columns == 128) {
-    if (fp32) return mma_launch<Product::kWeights, 128, 1, float>(s, ld, xs, w, dys, offsets, o, o_ld, sl, stream);
-    return mma_launch<Product::kWeights, 128, 1, uint16_t>(s, ld, xs, w, dys, offsets, o, o_ld, sl, stream);
+    if (fp32) return mma_launch<Product::kWeights, 128, 1, float>(s, ld, xs, w, dys, offsets, o, o_ld, sl, quit, stream);
+    return mma_launch<Product::kWeights, 128, 1, uint16_t>(s, ld, xs, w, dys, offsets, o, o_ld, sl, quit, stream);
   }
-  if (fp32) return mma_launch<Product::kWeights, 256, 2, float>(s, ld, xs, w, dys, offsets, o, o_ld, sl, stream);
-  return mma_launch<Product::kWeights, 256, 2, uint16_t>(s, ld, xs, w, dys, offsets, o, o_ld, sl, stream);
+  if (fp32) return mma_launch<Product::kWeights, 256, 2, float>(s, ld, xs, w, dys, offsets, o, o_ld, sl, quit, stream);
+  return mma_launch<Product::kWeights, 256, 2, uint16_t>(s, ld, xs, w, dys, offsets, o, o_ld, sl, quit, stream);
 }
 
 }  // namespace grs

@@ -199,6 +199,7 @@ _sig = {
     "grs_experts_forward": ([_P(grs_experts)] + [_vp] * 6, ctypes.c_int),
     "grs_experts_backward": ([_P(grs_experts)] + [_vp] * 8, ctypes.c_int),
     "grs_experts_workspace_bytes": ([_P(grs_experts)], ctypes.c_int64),
+    "grs_selftest_experts_wait": ([_P(grs_experts)] + [_vp] * 7 + [ctypes.c_int32, ctypes.c_int32, _vp], ctypes.c_int),
     "grs_embedding_forward": ([_P(grs_embedding)] + [_vp] * 4, ctypes.c_int),
     "grs_embedding_backward": ([_P(grs_embedding)] + [_vp] * 5, ctypes.c_int),
     "grs_embedding_workspace_bytes": ([_P(grs_embedding)], ctypes.c_int64),
@@ -601,6 +602,12 @@ def grs_experts_backward(shape: grs_experts, dys: int, xs: Optional[int], w: Opt
                          dw: Optional[int], workspace: Optional[int], stream: int) -> None:
     _check(_lib.grs_experts_backward(ctypes.byref(shape), dys, xs, w, offsets, dxs, dw, workspace, stream),
            "grs_experts_backward")
+
+
+def grs_selftest_experts_wait(shape: grs_experts, dys: int, xs: Optional[int], w: Optional[int], offsets: int, dxs: Optional[int],
+                              dw: Optional[int], workspace: Optional[int], quitter: int, quit_tile: int, stream: int) -> None:
+    _check(_lib.grs_selftest_experts_wait(ctypes.byref(shape), dys, xs, w, offsets, dxs, dw, workspace, quitter, quit_tile, stream),
+           "grs_selftest_experts_wait")
 
 
 def make_embedding(tokens: int, row_begin: int, row_end: int, hidden: int, scale: float, dtype: int,

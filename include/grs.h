@@ -893,6 +893,16 @@ grs_status grs_experts_backward(const grs_experts* shape, const void* dys, const
                                 const int32_t* offsets, void* dxs, void* dw, void* workspace, void* stream);
 /* Bytes (of either call), or -1 for a shape that the calls refuse. */
 int64_t grs_experts_workspace_bytes(const grs_experts* shape);
+/* Failure-detection self-test: grs_experts_backward in bf16 (other types are
+ * refused with INVALID_ARG), in which the loads of block `quitter` of each of
+ * its products give up at the block's quit_tile-th tile (from 0), as if a wait
+ * had lasted its 2 s; where two blocks share a tile the other one's waits do.
+ * The call ends, its outputs are not to be used,
+ * grs_operators_check_device_errors reports it where there is such a tile, and
+ * the CUDA context stays usable. */
+grs_status grs_selftest_experts_wait(const grs_experts* shape, const void* dys, const void* xs, const void* w,
+                                     const int32_t* offsets, void* dxs, void* dw, void* workspace, int32_t quitter,
+                                     int32_t quit_tile, void* stream);
 
 /* ------------------------------------------------------------- embedding */
 

@@ -666,7 +666,7 @@ cudaError_t emb_forward(const grs_embedding* s, const int32_t* ids, const void* 
 
 }  // namespace
 
-cudaError_t take_embedding_flags(int (&total)[FLAG_COUNT], cudaStream_t st) { return take_flags(emb_flags, total, st); }
+cudaError_t embedding_flags(int** at) { return cudaGetSymbolAddress(reinterpret_cast<void**>(at), emb_flags); }
 
 }  // namespace grs
 

@@ -7,6 +7,8 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <mutex>
+
 #include "api_util.h"
 #include "device.cuh"
 #include "experts.cuh"
@@ -554,9 +556,44 @@ grs_status experts_backward(const grs_experts* s, const void* dys, const void* x
   return e == cudaSuccess ? GRS_OK : api_cuda_fail(e, who);
 }
 
+// ------------------------------------------------------------------ flags
+// Kernels of other streams may raise a flag at any time, so each is read and
+// cleared in one step: what is raised afterwards stays for the next look.
+constexpr int FLAG_FILES = 4;
+struct FlagFiles {
+  int* at[FLAG_FILES];
+};
+
+__device__ int flags_taken[FLAG_COUNT];
+
+__global__ void take_flags_kernel(const __grid_constant__ FlagFiles files) {
+  if (threadIdx.x >= FLAG_COUNT) return;
+  int x = 0;
+  for (int f = 0; f < FLAG_FILES; ++f) {
+    const int y = atomicExch(files.at[f] + threadIdx.x, 0);
+    if (x == 0) x = y;
+  }
+  flags_taken[threadIdx.x] = x;
+}
+
+cudaError_t take_flags(const FlagFiles& files, int (&flags)[FLAG_COUNT], cudaStream_t st) try {
+  static std::mutex one;  // flags_taken holds one look's
+  const std::lock_guard<std::mutex> lock(one);
+  void* at = nullptr;
+  cudaError_t e = cudaGetSymbolAddress(&at, flags_taken);
+  if (e != cudaSuccess) return e;
+  take_flags_kernel<<<1, 32, 0, st>>>(files);
+  e = cudaGetLastError();
+  if (e == cudaSuccess) e = cudaMemcpyAsync(flags, at, sizeof(flags), cudaMemcpyDeviceToHost, st);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(st);
+  return e;
+} catch (...) {  // the lock's
+  return cudaErrorUnknown;
+}
+
 }  // namespace
 
-cudaError_t take_experts_flags(int (&total)[FLAG_COUNT], cudaStream_t st) { return take_flags(exp_flags, total, st); }
+cudaError_t experts_flags(int** at) { return cudaGetSymbolAddress(reinterpret_cast<void**>(at), exp_flags); }
 
 }  // namespace grs
 
@@ -568,11 +605,13 @@ grs_status grs_operators_check_device_errors(void* stream) {
   static const char who[] = "grs_operators_check_device_errors";
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   int flags[FLAG_COUNT] = {};
+  FlagFiles files{};
   cudaError_t e = cudaStreamSynchronize(st);
-  if (e == cudaSuccess) e = take_experts_flags(flags, st);
-  if (e == cudaSuccess) e = take_experts_mma_flags(flags, st);
-  if (e == cudaSuccess) e = take_embedding_flags(flags, st);
-  if (e == cudaSuccess) e = take_qk_norm_flags(flags, st);
+  if (e == cudaSuccess) e = experts_flags(&files.at[0]);
+  if (e == cudaSuccess) e = experts_mma_flags(&files.at[1]);
+  if (e == cudaSuccess) e = embedding_flags(&files.at[2]);
+  if (e == cudaSuccess) e = qk_norm_flags(&files.at[3]);
+  if (e == cudaSuccess) e = take_flags(files, flags, st);
   if (e != cudaSuccess) return api_cuda_fail(e, who);
   if (flags[FLAG_BOUNDS] != 0) return api_fail(GRS_ERR_BOUNDS, who, "an index out of place");
   return flags[FLAG_TIMEOUT] != 0 ? api_fail(GRS_ERR_TIMEOUT, who, "a bounded device wait timed out") : GRS_OK;

@@ -729,7 +729,7 @@ cudaError_t mma_rows(int columns, const grs_experts* s, const ExpLd& ld, const v
 
 }  // namespace
 
-cudaError_t take_experts_mma_flags(int (&total)[FLAG_COUNT], cudaStream_t st) { return take_flags(mma_flags, total, st); }
+cudaError_t experts_mma_flags(int** at) { return cudaGetSymbolAddress(reinterpret_cast<void**>(at), mma_flags); }
 
 ExpTiles experts_mma_tiles(Product p, const grs_experts* s) {
   const int64_t in = s->in_features, out = s->out_features, least = s->rows < s->experts ? s->rows : s->experts;

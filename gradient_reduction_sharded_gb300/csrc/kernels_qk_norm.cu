@@ -847,7 +847,7 @@ cudaError_t qk_backward(const grs_qk_norm* s, const int64_t (&ld)[4], const QkAr
 
 }  // namespace
 
-cudaError_t take_qk_norm_flags(int (&total)[FLAG_COUNT], cudaStream_t st) { return take_flags(qk_flags, total, st); }
+cudaError_t qk_norm_flags(int** at) { return cudaGetSymbolAddress(reinterpret_cast<void**>(at), qk_flags); }
 
 }  // namespace grs
 

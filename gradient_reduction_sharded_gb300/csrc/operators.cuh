@@ -48,24 +48,10 @@ __device__ __forceinline__ void store_floats(T* p, const float (&v)[N]) {
   }
 }
 
-// Adds a file's device flags (a __device__ array of FLAG_COUNT ints) to
-// `total` and clears them.
-template <typename Flags>
-cudaError_t take_flags(const Flags& symbol, int (&total)[FLAG_COUNT], cudaStream_t st) {
-  void* at = nullptr;
-  int have[FLAG_COUNT] = {};
-  cudaError_t e = cudaGetSymbolAddress(&at, symbol);
-  if (e == cudaSuccess) e = cudaMemcpyAsync(have, at, sizeof(have), cudaMemcpyDeviceToHost, st);
-  if (e == cudaSuccess) e = cudaMemsetAsync(at, 0, sizeof(have), st);
-  if (e == cudaSuccess) e = cudaStreamSynchronize(st);
-  for (int i = 0; i < FLAG_COUNT; ++i)
-    if (have[i] != 0) total[i] = have[i];
-  return e;
-}
-
-cudaError_t take_experts_flags(int (&total)[FLAG_COUNT], cudaStream_t st);
-cudaError_t take_experts_mma_flags(int (&total)[FLAG_COUNT], cudaStream_t st);
-cudaError_t take_embedding_flags(int (&total)[FLAG_COUNT], cudaStream_t st);
-cudaError_t take_qk_norm_flags(int (&total)[FLAG_COUNT], cudaStream_t st);
+// The device flags (FLAG_COUNT ints) of each file on the current device.
+cudaError_t experts_flags(int** at);
+cudaError_t experts_mma_flags(int** at);
+cudaError_t embedding_flags(int** at);
+cudaError_t qk_norm_flags(int** at);
 
 }  // namespace grs

@@ -151,7 +151,7 @@ __global__ void __launch_bounds__(EMB_THREADS) emb_scatter_kernel(const __grid_c
         total[q] = __ldg(a.totals + b0 + q);
         before[q] = __ldg(a.counts + int64_t(blockIdx.x) * bins + b0 + q);
       }
-  } else if (a.chunks > 1) {
+  } else {
 #pragma unroll 8
     for (int c = 0; c < a.chunks; ++c)
 #pragma unroll
@@ -185,7 +185,6 @@ __global__ void __launch_bounds__(EMB_THREADS) emb_scatter_kernel(const __grid_c
         at[k][b0 + q] = sum;
         sum += c;
       }
-      if (a.chunks == 1) total[q] = sum;
       all += total[q];
     }
   int32_t whole, s = emb_prefix(all, warp_total, &whole);
@@ -581,7 +580,7 @@ cudaError_t emb_sort(const grs_embedding* s, const EmbPlan& p, const int32_t* id
     const SmallSortArgs a{ids, k[0], t[0], static_cast<int32_t>(n), s->row_begin, p.rows, p.digit, p.passes};
     return launch_pdl(emb_small_sort_kernel, dim3(1), block, 0, stream, a);
   }
-  for (int i = 0; i < p.passes && e == cudaSuccess; ++i) {
+  for (int i = 0; i < p.passes && e == cudaSuccess; ++i) {  // more tokens than that are several chunks
     SortArgs a{};
     a.ids = ids;
     a.keys = i == 0 ? nullptr : k[(i - 1) & 1];
@@ -589,7 +588,7 @@ cudaError_t emb_sort(const grs_embedding* s, const EmbPlan& p, const int32_t* id
     a.keys_out = k[i & 1];
     a.tokens_out = t[i & 1];
     a.counts = reinterpret_cast<int32_t*>(ws + p.at_counts) + i * table;
-    a.next = p.chunks > 1 && i + 1 < p.passes ? a.counts + table : nullptr;
+    a.next = i + 1 < p.passes ? a.counts + table : nullptr;
     a.n = static_cast<int32_t>(n);
     a.begin = s->row_begin;
     a.rows = p.rows;
@@ -597,7 +596,7 @@ cudaError_t emb_sort(const grs_embedding* s, const EmbPlan& p, const int32_t* id
     a.bins = bins;
     a.chunks = static_cast<int32_t>(p.chunks);
     a.clear = p.passes - 1;
-    if (p.chunks > 1 && i == 0) e = launch_pdl(emb_count_kernel<J>, grid, block, 0, stream, a);
+    if (i == 0) e = launch_pdl(emb_count_kernel<J>, grid, block, 0, stream, a);
     if (e == cudaSuccess && p.chunks > EMB_MAX_CHUNKS) {
       a.totals = reinterpret_cast<int32_t*>(ws + p.at_totals);
       e = launch_pdl(emb_scan_kernel, dim3(bins), block, 0, stream, a);

@@ -398,8 +398,12 @@ cudaError_t exp_product(const grs_experts* s, const ExpLd& ld, const void* xs, c
     e = experts_mma(kP, s, ld, xs, w, dys, offsets, o, o_ld, sl, quit, stream);
   } else {
     const void *a = kP == Product::kWeights ? xs : w, *b = kP == Product::kForward ? xs : dys;
-    if (fp32 || sl.n > 1) e = exp_general<kP, float>(s, ld, a, b, offsets, o, sl, stream);
-    else e = exp_general<kP, uint16_t>(s, ld, a, b, offsets, o, sl, stream);
+    if constexpr (kP == Product::kWeights) {  // only gradients may be of another type
+      e = fp32 || sl.n > 1 ? exp_general<kP, float>(s, ld, a, b, offsets, o, sl, stream)
+                           : exp_general<kP, uint16_t>(s, ld, a, b, offsets, o, sl, stream);
+    } else {
+      e = exp_general<kP, float>(s, ld, a, b, offsets, o, sl, stream);
+    }
   }
   if (e != cudaSuccess || sl.n == 1) return e;
   return fp32 ? exp_join<float>(kP, s, sl, offsets, o, o_ld, stream) : exp_join<uint16_t>(kP, s, sl, offsets, o, o_ld, stream);

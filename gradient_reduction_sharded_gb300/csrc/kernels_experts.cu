@@ -271,6 +271,10 @@ grs_status check_experts(const grs_experts* s, const char* who, ExpLd* ld) {
   if (ld->x < s->in_features || ld->y < s->out_features || ld->x > GRS_MAX_WIDTH || ld->y > GRS_MAX_WIDTH)
     return api_fail(GRS_ERR_SHAPE, who, "a distance of rows below their width or above GRS_MAX_WIDTH");
   ld->w = s->in_features;
+  // (so that bytes of anything here fit 64 bits)
+  const int64_t wide = ld->x > ld->y ? ld->x : ld->y;
+  if (int64_t(s->in_features) * s->out_features > GRS_MAX_ELEMENTS / s->experts || s->rows > GRS_MAX_ELEMENTS / wide)
+    return api_fail(GRS_ERR_SHAPE, who, "more than GRS_MAX_ELEMENTS elements of a matrix or of all weights");
   return GRS_OK;
 }
 

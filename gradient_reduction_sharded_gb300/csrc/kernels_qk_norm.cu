@@ -690,8 +690,9 @@ grs_status check_qk(const grs_qk_norm* s, const char* who, int64_t (&ld)[4]) {
   if (s == nullptr) return api_fail(GRS_ERR_INVALID_ARG, who, "shape is NULL");
   if (s->tokens < 0 || s->q_heads < 0 || s->k_heads < 0 || s->head_dim < 1 || s->head_dim > GRS_QK_MAX_DIM)
     return api_fail(GRS_ERR_SHAPE, who, "tokens and heads must be >= 0 and head_dim in [1, GRS_QK_MAX_DIM]");
-  if ((int64_t(s->q_heads) + s->k_heads) * s->head_dim > GRS_MAX_WIDTH || s->tokens > (int64_t(1) << 40))
-    return api_fail(GRS_ERR_SHAPE, who, "more than GRS_MAX_WIDTH elements a token, or 2^40 tokens");
+  const int64_t all = (int64_t(s->q_heads) + s->k_heads) * s->head_dim;
+  if (all > GRS_MAX_WIDTH || s->tokens > GRS_MAX_ELEMENTS / (all > 0 ? all : 1))
+    return api_fail(GRS_ERR_SHAPE, who, "more than GRS_MAX_WIDTH elements a token, or GRS_MAX_ELEMENTS in all");
   if (s->rotary_dim < 0 || s->rotary_dim > s->head_dim || s->rotary_dim % 2 != 0)
     return api_fail(GRS_ERR_SHAPE, who, "rotary_dim must be even and in [0, head_dim]");
   if (s->interleaved != 0 && s->interleaved != 1) return api_fail(GRS_ERR_INVALID_ARG, who, "interleaved must be 0 or 1");
@@ -702,7 +703,8 @@ grs_status check_qk(const grs_qk_norm* s, const char* who, int64_t (&ld)[4]) {
   for (int i = 0; i < 4; ++i) {
     const int64_t row = int64_t(i % 2 == 0 ? s->q_heads : s->k_heads) * s->head_dim;
     ld[i] = given[i] == 0 ? row : given[i];
-    if (ld[i] < row || ld[i] > (int64_t(1) << 40)) return api_fail(GRS_ERR_SHAPE, who, "a distance of tokens below their heads' elements");
+    if (ld[i] < row || ld[i] > GRS_MAX_ELEMENTS / (s->tokens > 1 ? s->tokens - 1 : 1))
+      return api_fail(GRS_ERR_SHAPE, who, "a distance of tokens below their heads' elements, or GRS_MAX_ELEMENTS from the first to the last");
   }
   return GRS_OK;
 }

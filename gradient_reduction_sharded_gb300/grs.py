@@ -41,6 +41,7 @@ GRS_MOE_MAX_EXPERTS = 1024
 GRS_MAX_WIDTH = 1 << 30
 GRS_QK_MAX_DIM = 1024
 GRS_MAX_ROWS = (1 << 31) - (1 << 16)
+GRS_MAX_ELEMENTS = 1 << 40
 
 STATUS_NAMES = {0: "OK", 1: "INVALID_ARG", 2: "UNSUPPORTED_COMPOSITION", 3: "SHAPE",
                 4: "ALIGNMENT", 5: "CUDA", 6: "TIMEOUT", 7: "NONFINITE", 8: "NO_DEVICE",

@@ -839,6 +839,7 @@ grs_status grs_moe_combine_backward(const grs_moe* shape, const void* dy, const 
 /* -------------------- operators of a decoder's other parameters */
 
 #define GRS_MAX_ROWS 2147418112 /* rows of the experts, tokens of an embedding: 2^31 - 2^16 */
+#define GRS_MAX_ELEMENTS ((int64_t)1 << 40) /* of rows with their distance, of all experts' weights, of all heads */
 
 /* Synchronise `stream`, read and clear the current device's flags of
  * grs_experts_*, grs_embedding_* and grs_qk_norm_*, which the calls of all its
@@ -855,7 +856,8 @@ grs_status grs_operators_check_device_errors(void* stream);
  * [ISSUE] "Why this needs separate work"; their gradient is written in
  * grad_dtype, so that it can go straight into a rank's gradient buffer. */
 typedef struct grs_experts {
-  int64_t rows;          /* rows that xs and ys have, 0..GRS_MAX_ROWS */
+  int64_t rows;          /* rows that xs and ys have, 0..GRS_MAX_ROWS; they, and all weights, are at most
+                            GRS_MAX_ELEMENTS elements */
   int64_t ld_x;          /* elements from one row of xs and dxs to the next, 0 = in_features */
   int64_t ld_y;          /* of ys and dys, 0 = out_features */
   int32_t experts;       /* 1..GRS_MOE_MAX_EXPERTS */
@@ -950,7 +952,7 @@ int64_t grs_embedding_workspace_bytes(const grs_embedding* shape);
  * work"); their gradients are written in grad_dtype, so that they can go
  * straight into a rank's gradient buffer. */
 typedef struct grs_qk_norm {
-  int64_t tokens;        /* >= 0 */
+  int64_t tokens;        /* >= 0; with any of the distances below at most GRS_MAX_ELEMENTS elements */
   int64_t ld_q;          /* elements from a token's queries to the next token's, 0 = q_heads * head_dim;
                             q and dq: they may lie in the rows of a joint projection */
   int64_t ld_k;          /* the same of k and dk */

@@ -21,6 +21,8 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <cmath>
+
 #include "api_util.h"
 #include "device.cuh"
 #include "internal.h"
@@ -560,6 +562,7 @@ grs_status check_embedding(const grs_embedding* s, const char* who) {
     return api_fail(GRS_ERR_SHAPE, who, "tokens must be in [0, GRS_MAX_ROWS] and hidden in [1, GRS_MAX_WIDTH]");
   if (s->row_begin < 0 || s->row_end <= s->row_begin)
     return api_fail(GRS_ERR_INVALID_ARG, who, "the row range must be 0 <= begin < end");
+  if (!std::isfinite(s->scale)) return api_fail(GRS_ERR_INVALID_ARG, who, "scale must be finite");
   if (!dtype_ok(s->dtype) || !dtype_ok(s->grad_dtype)) return api_fail(GRS_ERR_INVALID_ARG, who, "unknown element type");
   return GRS_OK;
 }

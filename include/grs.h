@@ -918,7 +918,7 @@ typedef struct grs_embedding {
   int32_t row_begin;     /* >= 0 */
   int32_t row_end;       /* > row_begin */
   int32_t hidden;        /* elements of a vector, 1..GRS_MAX_WIDTH */
-  float scale;           /* of every vector, e.g. sqrt(hidden) or 1 */
+  float scale;           /* of every vector, e.g. sqrt(hidden) or 1; finite */
   int32_t dtype;         /* grs_dtype of table, y and dy */
   int32_t grad_dtype;    /* of dtable */
   int32_t reserved[2];

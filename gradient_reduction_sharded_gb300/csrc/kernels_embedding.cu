@@ -12,9 +12,13 @@
 // first.  A window has parts of at most two such rows: the one that comes in
 // from the left (slot 0) and the one that goes on to the right (slot 1).
 //
-// Both are bound by memory.  Forward of 32768 vectors of 2048 bf16 takes 42 us
-// (6.4 TB/s).  Backward of 16384 tokens into 151936 rows of 2048 takes 135: the
-// sums and zeros 114 (631 MB of DRAM traffic, 5.5 TB/s; issue 72 %), the sort
+// Forward of 32768 vectors of 2048 bf16 takes 42 us; where ids fall as 1 / rank
+// some 12200 of the vectors are distinct, and their 50 MB and the result's 134
+// need 27: it is bound by latency, a thread waits for its id and then for its
+// one load (DRAM 3 TB/s, L2 32 %).
+//
+// Backward is bound by memory.  16384 tokens into 151936 rows of 2048 take 135:
+// the sums and zeros 114 (631 MB of DRAM traffic, 5.5 TB/s; issue 72 %), the sort
 // about 17 in three launches bound by latency, the joining of split rows 5.  One
 // block sorting all 16384 took 41, rows cleared beside the sort made it 143.
 // Vectors that are not whole 16-byte chunks go by elements.

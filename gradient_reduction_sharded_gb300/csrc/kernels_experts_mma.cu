@@ -37,7 +37,9 @@
 // ordering (547 -> 295 us), an issuing loop in 32 bits (-> 247), eight storing
 // warps (-> 240), loops of whole warps with one thread elected (-> 228), and
 // where k is short the boxes (32768 rows, 8 experts, 256 -> 2432: 69 -> 40).
-// Few rows are bound by reading the weights: 20 rows of 13 experts 11 us for 41 MB.
+// Few rows are bound by what comes one after the other: 20 rows of 13 experts
+// take 11 us, of which reading their 41 MB needs 6, launch, offsets and first
+// loads 4, the sum of two slices of k 2.
 //
 // Long sums: the tensor cores add with rounding towards zero, so sums of values
 // of one sign are too small by a part that grows with k: 2.5e-5 at 4096, 7.9e-4
@@ -736,21 +738,27 @@ ExpTiles experts_mma_tiles(Product p, const grs_experts* s) {
   auto up = [](int64_t n, int64_t to) { return (n + to - 1) / to; };
   ExpTiles t;
   if (p == Product::kWeights) {
-    // Few large tiles are shared badly, small ones read more for each product.  Even experts, us with small and large ones:
-    // 12 experts, 1024 -> 520 (144 large tiles), 1500 rows 9.0 and 10.0, 3000 11.1 and 10.9, 8000 18.3 and 15.5; 8 experts,
-    // 2048 -> 768 (192), 4000 rows 18.1 and 16.6; 32 experts, 768 -> 512 (192), 4000 rows 10.8 and 12.0, 12000 15.5 and
-    // 14.6.  A skewed router's 8000 rows of the first 26.8 and 29.1, of the second 27.9 and 23.6.  Nor are 256 features
-    // taken where a quarter of what they multiply is not there: 32 experts, 36000 rows, 384 -> 768 42 and 35.5, 128 -> 2048
-    // 50 and 42.
+    // Few large tiles are shared badly, small ones read more for each product.  us with small and large ones, even experts
+    // and (in brackets) a skewed router's: 12 experts, 1024 -> 520 (144 large tiles), 1500 rows 8.3 and 9.6 (9.6, 10.7),
+    // 3000 10.3 and 10.5 (12.8, 14.0), 8000 17.7 and 15.2 (17.8, 16.9); 8 experts, 2048 -> 768 (192), 4000 rows 17.4 and
+    // 16.0 (17.7, 17.2); 32 experts, 768 -> 512 (192), 4000 rows 10.2 and 11.6 (12.3, 13.9), 12000 15.3 and 14.2 (18.2,
+    // 19.2), 16000 18.0 and 16.7 (20.4, 21.7).  Even experts would have large ones from a mean of 250 to 400 rows on, skewed
+    // ones later: 448 lies between.  Nor are 256 features taken where a quarter of what they multiply is not there: 32
+    // experts, 36000 rows, 384 -> 768 24.7 and 26.8, 128 -> 2048 32.1 and 38.1.
     const int64_t large = s->experts * up(in, 256) * up(out, 256), mean = s->rows / s->experts;
     t.columns = large < 76 || (large < 4 * 76 && mean < 448) || 2 * up(in, 256) * 3 >= up(in, 128) * 4 ? 128 : 256;
     t.n = t.columns == 256 ? large : s->experts * up(in, 128) * up(out, 128);
     t.k = s->rows / s->experts;
   } else {
-    // Columns by the rows that an expert has in the mean.  2048 -> 768, 32 experts, us with 16, 64, 128 and 256 (two
-    // blocks): 20 rows 11.8, 13.7, -, -; 512 rows 19.1, 18.3, 21.6, 22.1; 2048 rows 30.6, 22.0, 24.8, 25.3; 3000 rows 36.4,
-    // 28.3, 26.4, 26.8; 4096 rows 49.4, 29.4, 27.2, 27.7; 131072 rows -, 407, 312, 227.  256 features where there are half
-    // of them: 32 experts, 36000 rows, 2048 -> 128 41, 128 columns 32.
+    // Columns by the rows that an expert has in the mean, those outside all experts' counted too (the host does not know
+    // them).  Forward, 2048 -> 768, 32 even experts, us with 16, 64, 128 and 256 (two blocks), in brackets those of a skewed
+    // router: 20 rows 12.4, 17.8, 20.1, 21.4; 512 rows 19.9, 19.7, 21.7, 21.8 (20.2, 17.2, 22.6, 21.6); 2048 rows 30.3,
+    // 21.9, 24.8, 25.5 (29.6, 22.2, 24.2, 27.5); 2560 rows 35.9, 27.8, 25.5, 26.0 (36.0, 28.7, 24.7, 26.6); 4096 rows 49.1,
+    // 28.9, 26.9, 27.4 (49.5, 28.4, 24.9, 28.9); 6000 rows 64.1, 29.9, 31.3, 30.0 (63.9, 35.3, 30.8, 29.0); 12000 rows
+    // (120.4, 51.4, 45.0, 37.8); 131072 rows 1228, 421, 329, 237.  So 128 take over from 64 between means of 64 and 80, and
+    // 256 from 128 between 128 and 190; the rule takes the lower ends, where forward of exactly 64 rows an expert is 13 %
+    // and of 128 2 to 16 % longer than it could be (rows' gradients 5 and 3 %, skewed not at all).  256 features where there
+    // are half of them: 32 experts, 36000 rows, 2048 -> 128 40.8, 128 columns 31.1.
     const int64_t f = p == Product::kForward ? out : in, mean = s->rows / s->experts;
     const int64_t large = (s->rows / 256 + least) * up(f, 256);
     t.columns = mean >= 128 && large >= 76 && f > 128 ? 256 : mean >= 64 ? 128 : mean >= 16 ? 64 : 16;

@@ -889,8 +889,10 @@ grs_status grs_experts_forward(const grs_experts* shape, const void* xs, const v
                                void* workspace, void* stream);
 /* dxs[r] = w[e]^T dys[r]; dw[e] = sum over the expert's rows of dys[r] xs[r]^T
  * (overwritten, zeros for an expert without rows), in fp32, rounded once; each
- * of the two NULL if not wanted (w is needed for dxs, xs for dw).  Sums have an
- * order that the shape and the offsets fix: no float atomics. */
+ * of the two NULL if not wanted (w is needed for dxs, xs for dw).  Two maps of
+ * the same rows (a gate's and an up projection's) write two dxs, which the
+ * caller adds.  Sums have an order that the shape and the offsets fix: no float
+ * atomics. */
 grs_status grs_experts_backward(const grs_experts* shape, const void* dys, const void* xs, const void* w,
                                 const int32_t* offsets, void* dxs, void* dw, void* workspace, void* stream);
 /* Bytes (of either call), or -1 for a shape that the calls refuse. */
@@ -932,7 +934,8 @@ typedef struct grs_embedding {
 grs_status grs_embedding_forward(const grs_embedding* shape, const int32_t* ids, const void* table, void* y,
                                  void* stream);
 /* dtable[v] = scale * sum of dy[t] over the tokens t with ids[t] = row_begin + v
- * (overwritten, zeros for a row without tokens), in fp32, rounded once.  Tokens
+ * (overwritten, zeros for a row without tokens: where the table is the output
+ * head's too, the caller adds that gradient), in fp32, rounded once.  Tokens
  * are sorted by id first and added up in an order that the shape and the ids
  * fix: no float atomics.  dtable: device [row_end - row_begin, hidden], aligned
  * to the element.  workspace: device, 16-byte aligned,

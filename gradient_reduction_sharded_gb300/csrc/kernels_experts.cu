@@ -575,6 +575,7 @@ struct FlagFiles {
 __device__ int flags_taken[FLAG_COUNT];
 
 __global__ void take_flags_kernel(const __grid_constant__ FlagFiles files) {
+  pdl_wait();
   if (threadIdx.x >= FLAG_COUNT) return;
   int x = 0;
   for (int f = 0; f < FLAG_FILES; ++f) {
@@ -590,8 +591,7 @@ cudaError_t take_flags(const FlagFiles& files, int (&flags)[FLAG_COUNT], cudaStr
   void* at = nullptr;
   cudaError_t e = cudaGetSymbolAddress(&at, flags_taken);
   if (e != cudaSuccess) return e;
-  take_flags_kernel<<<1, 32, 0, st>>>(files);
-  e = cudaGetLastError();
+  e = launch_pdl(take_flags_kernel, dim3(1), dim3(32), 0, st, files);
   if (e == cudaSuccess) e = cudaMemcpyAsync(flags, at, sizeof(flags), cudaMemcpyDeviceToHost, st);
   if (e == cudaSuccess) e = cudaStreamSynchronize(st);
   return e;
